@@ -297,6 +297,140 @@ FATTN_API int fattn_fwd_unfused_static(const void* q, const void* k, const void*
                              float scale, int causal, int dtype, fattn_stream_t stream);
 
 /*
+ * ---- Serving: packed prompts and a paged key/value cache -------------------
+ *
+ * The entry points below take rows of 16-bit elements (FATTN_BF16 / FATTN_F16;
+ * FATTN_F32 -> FATTN_ERR_UNSUPPORTED) addressed by strides, so that q, k and v
+ * can be slices of one projection's output.  Strides count elements, are
+ * multiples of 8 and not negative; the D elements of a row are contiguous, and
+ * every row starts on a 16-byte boundary.  Tables in device memory
+ * (cu_seqlens, slots, pos, block_table, seq_lens) are read by the kernels, so
+ * an entry out of range cannot be refused before the launch: the kernels skip
+ * what it names, touch no memory outside the buffers, and
+ * fattn_get_device_status then returns FATTN_ERR_INVALID_ARG.
+ *
+ * A paged cache is a pool of num_pages pages of page_size tokens (a multiple
+ * of 16, at most 65536).  16 bits: k_pages and v_pages, each [num_pages]
+ * [Hkv][page_size][D] of `dtype` with page_stride elements from page to page
+ * (Hkv*page_size*D when dense; larger when K and V pages share a tensor).
+ * 4 bits: for K and V each, codes [num_pages][Hkv][page_size][D/2] bytes and
+ * scales fp16 [num_pages][Hkv][page_size][D/32][2], dense.  Element d of a row
+ * stands for code * scale + zero with (scale, zero) = scales[..][d/32].  A
+ * row's codes are nibbles, nibble n in byte n/2, low half first; the order is
+ * the one in which the attention kernel's matrix instructions take them:
+ *   K: element d = 32 i + 8 t + e at nibble 8 (t D/32 + i) + e/2 + 4 (e mod 2)
+ *   V: element d = 16 j + 8 u + g at nibble (D/8) g + (D/16) u + j
+ * A slot is page * page_size + place in the page.
+ */
+
+/*
+ * fattn_cache_append -- rows k and v of T new tokens into a 16-bit paged
+ * cache, rotating k (and q) by position on the way.
+ *
+ *   q        : [T, H, D] or NULL (then q_out must be NULL and H is ignored).
+ *   k, v     : [T, Hkv, D].
+ *   q_out    : [T, H, D], the rotated q; NULL only when q is NULL.
+ *   k_out    : [T, Hkv, D], k as the cache holds it; may be NULL.
+ *   strides  : host array of 10: token stride and head stride of q, k, v,
+ *              q_out, k_out (entries of NULL tensors are ignored).
+ *   k_pages, v_pages, page_stride, num_pages, page_size : the cache (above).
+ *   slots    : device int64 [T].  Token t goes to slots[t]; a negative slot
+ *              skips the token: nothing of it is read or written (padding of a
+ *              batch).  A slot past the cache is an index out of range.  Slots
+ *              of one call must differ; where two tokens share one, that slot
+ *              holds a mixture of their rows.
+ *   pos      : device int32 [T], rows of the rotation tables, 0 <= pos < max_pos.
+ *   cos, sin : device fp32 [max_pos][rot/2].
+ *   rot      : elements of each row that turn, a multiple of 16, 0..D; 0 = no
+ *              rotation (pos, cos and sin are ignored).
+ *   interleaved : 0 = element i turns with element i + rot/2, otherwise 2i with 2i+1:
+ *              (a, b) -> (a cos - b sin, b cos + a sin) in fp32, each product
+ *              and sum rounded, the result rounded once to `dtype`.
+ *
+ * An output may be its own input (same pointer and strides); any other overlap
+ * among inputs, outputs and cache -> FATTN_ERR_INVALID_ARG.  One launch.
+ */
+FATTN_API int fattn_cache_append(const void* q, const void* k, const void* v, void* q_out, void* k_out,
+                       const int64_t* strides, void* k_pages, void* v_pages, int64_t page_stride,
+                       int64_t num_pages, int64_t page_size, const int64_t* slots,
+                       const int32_t* pos, const float* cos, const float* sin, int64_t max_pos,
+                       int64_t rot, int interleaved, int64_t T, int64_t H, int64_t Hkv, int64_t D,
+                       int dtype, fattn_stream_t stream);
+
+/*
+ * fattn_cache_append_kv4 -- fattn_cache_append into a 4-bit cache.  The
+ * rotated k (fp32, not rounded to `dtype` first) and v are quantised in groups
+ * of 32 elements: zero = fp16(min), scale = fp16((max - min) / 15), code =
+ * clamp(round((x - zero) / scale), 0, 15), 0 where scale is 0, all in fp32.
+ * Elements past +-65504 are held as +-65504; a NaN takes no part in its
+ * group's scale and is held as the group's zero.
+ *
+ *   held     : 0 = k_out receives the rotated k rounded to `dtype`, and v_out
+ *              v itself; otherwise both receive the values that the cache now
+ *              stands for, rounded to `dtype` (a prompt's own attention then
+ *              sees what later steps will read).  Either may be NULL.
+ *   strides  : host array of 12: q, k, v, q_out, k_out, v_out.
+ * Everything else as fattn_cache_append.
+ */
+FATTN_API int fattn_cache_append_kv4(const void* q, const void* k, const void* v, void* q_out, void* k_out,
+                           void* v_out, const int64_t* strides, void* k_codes, void* k_scales,
+                           void* v_codes, void* v_scales, int64_t num_pages, int64_t page_size,
+                           const int64_t* slots, const int32_t* pos, const float* cos,
+                           const float* sin, int64_t max_pos, int64_t rot, int interleaved,
+                           int held, int64_t T, int64_t H, int64_t Hkv, int64_t D, int dtype,
+                           fattn_stream_t stream);
+
+/*
+ * fattn_decode_workspace_bytes -- bytes of device workspace fattn_decode and
+ * fattn_decode_kv4 need; it does not depend on the sequences' lengths.  0 for
+ * an empty or invalid size.
+ */
+FATTN_API int64_t fattn_decode_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t D);
+
+/*
+ * fattn_decode -- attention of the last Nq tokens of each of B sequences over
+ * a 16-bit paged cache that already holds those tokens:
+ *
+ *     O[b,h,i] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q[b,h,i] . k_j),
+ *     j = 0 .. seq_lens[b] - Nq + i,   LSE = ln sum_j p_j
+ *
+ * with k_j, v_j the rows of K/V head h / (H/Hkv) in page block_table[b][j /
+ * page_size], place j mod page_size.  A row that sees no key gets O = 0 and
+ * LSE = -inf.  Nothing but visible rows is read from the cache as numbers:
+ * what a page holds behind the last token never reaches O.
+ *
+ *   q, o        : [B, H, Nq, D]; `strides` is a host array of 6: batch, head
+ *                 and token stride of q, then of o.  o overlaps nothing else.
+ *   lse         : fp32 [B, H, Nq] contiguous, or NULL.
+ *   block_table : device int32 [B][table_width].
+ *   seq_lens    : device int32 [B], 0 <= seq_lens[b] <= table_width*page_size
+ *                 (and table_width*page_size < 2^31).
+ *   workspace   : caller-owned, fattn_decode_workspace_bytes, 16-byte aligned;
+ *                 contents ignored on entry.  Calls that run at the same time
+ *                 (two streams, two graphs) need workspaces of their own.
+ * The result does not depend on how the work is split beyond fp32 rounding,
+ * and is the same for every run of the same call.
+ */
+FATTN_API int fattn_decode(const void* q, void* o, float* lse, const int64_t* strides,
+                 const void* k_pages, const void* v_pages, int64_t page_stride, int64_t num_pages,
+                 int64_t page_size, const int32_t* block_table, int64_t table_width,
+                 const int32_t* seq_lens, void* workspace, int64_t workspace_bytes, int64_t B,
+                 int64_t H, int64_t Hkv, int64_t Nq, int64_t D, float scale, int dtype,
+                 fattn_stream_t stream);
+
+/*
+ * fattn_decode_kv4 -- fattn_decode over a 4-bit cache (above).  q and o are
+ * `dtype`; K's codes enter the products exactly and its scales in fp32, V is
+ * taken as fp16(code * scale + zero).
+ */
+FATTN_API int fattn_decode_kv4(const void* q, void* o, float* lse, const int64_t* strides,
+                     const void* k_codes, const void* k_scales, const void* v_codes,
+                     const void* v_scales, int64_t num_pages, int64_t page_size,
+                     const int32_t* block_table, int64_t table_width, const int32_t* seq_lens,
+                     void* workspace, int64_t workspace_bytes, int64_t B, int64_t H, int64_t Hkv,
+                     int64_t Nq, int64_t D, float scale, int dtype, fattn_stream_t stream);
+
+/*
  * fattn_plan -- host-only description of the launch fattn_fwd would make for
  * these arguments (no CUDA call when num_sms > 0).  Fills `out` with:
  *   out[0] path       : 0 = none (empty problem), 1 = FFMA fp32, 2 = tcgen05 bf16/fp16
@@ -333,8 +467,9 @@ FATTN_API int fattn_plan_head_group(int64_t B, int64_t H, int64_t Hkv, int64_t N
  * current device's error word.  Returns FATTN_OK, FATTN_ERR_TIMEOUT if a
  * kernel gave up a bounded wait since the last call, FATTN_ERR_INTERNAL if a
  * kernel found a broken launch invariant (e.g. shared-memory alignment) and
- * returned without computing, or FATTN_ERR_CUDA if the synchronisation itself
- * failed.
+ * returned without computing, FATTN_ERR_INVALID_ARG if a kernel found an entry
+ * of a device table out of range (and skipped what it names), or
+ * FATTN_ERR_CUDA if the synchronisation itself failed.
  */
 FATTN_API int fattn_get_device_status(fattn_stream_t stream);
 

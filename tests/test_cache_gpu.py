@@ -1,0 +1,442 @@
+"""Appending to a paged cache and attention over it, 16 and 4 bits, against
+plain 64-bit forms (tests/serving_ref.py)."""
+import math
+
+import pytest
+import torch
+
+import tiled_attention_forward_gb300 as fattn
+from tests import serving_ref as R
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
+INVALID = 1
+
+
+def ok():
+    torch.cuda.synchronize()
+    assert fattn.get_device_status() == 0
+
+
+def new_cache(kv4, P, Hkv, ps, D, dt, fill):
+    """Cache tensors on the GPU, every element set (fill: 16-bit value)."""
+    if not kv4:
+        return [torch.full((P, Hkv, ps, D), fill, dtype=dt, device="cuda") for _ in range(2)]
+    out = []
+    for _ in range(2):
+        out += [torch.full((P, Hkv, ps, D // 2), 0xA7, dtype=torch.uint8, device="cuda"),
+                torch.full((P, Hkv, ps, D // 32, 2), fill, dtype=torch.float16, device="cuda")]
+    return out
+
+
+def append(kv4, k, v, cache, slots, **kw):
+    if kv4:
+        return fattn.cache_append_kv4(k, v, *cache, slots, **kw)
+    kw.pop("v_out", None)
+    kw.pop("held", None)
+    return fattn.cache_append(k, v, *cache, slots, **kw)
+
+
+def qkv_slices(T, H, Hkv, D, dt, seed, std=1.0):
+    """q, k, v as slices of one projection's output, on the GPU."""
+    g = torch.Generator().manual_seed(seed)
+    x = (torch.randn(T, H + 2 * Hkv, D, generator=g) * std).to(dt).cuda()
+    return x[:, :H], x[:, H:H + Hkv], x[:, H + Hkv:]
+
+
+def check_quantised(x, mag, codes, scales, which, what):
+    """codes, scales [.., Hkv, D/2], [.., Hkv, D/32, 2] on the CPU hold x (float64)."""
+    ex = 3 * 2.0 ** -24 * mag  # error of the fp32 values that were quantised
+    xg, eg = x.unflatten(-1, (-1, 32)), ex.unflatten(-1, (-1, 32)).amax(-1)
+    lo, hi = xg.amin(-1), xg.amax(-1)
+    s, z = scales[..., 0].double(), scales[..., 1].double()
+    u16, t16 = 2.0 ** -11, R.tiny(torch.float16)
+    assert ((z - lo).abs() <= u16 * (lo.abs() + eg) + eg + t16).all(), what
+    step = (hi - lo) / 15
+    es = 2 * eg / 15 + 2.0 ** -22 * step
+    assert ((s - step).abs() <= u16 * (step + es) + es + t16).all(), what
+    c = R.unpack(codes, which).double().unflatten(-1, (-1, 32))
+    sd = torch.where(s > 0, s, 1.0)[..., None]
+    want = torch.where(s[..., None] > 0, (xg - z[..., None]) / sd, 0.0).clamp(0, 15)
+    # code = rint of an fp32 quotient: half a step, the input's error in steps, fp32 roundings of values up to ~16
+    slack = 0.5 + (eg[..., None] / sd) + 2.0 ** -18
+    assert ((c - want).abs() <= slack).all(), what
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("kv4", [False, True])
+@pytest.mark.parametrize("dtype,D,H,Hkv,T,ps,rot", [
+    ("bf16", 128, 4, 2, 67, 16, 128), ("fp16", 64, 8, 1, 33, 48, 32), ("bf16", 64, 5, 5, 1, 16, 64),
+    ("fp16", 128, 3, 1, 3, 32, 16), ("bf16", 128, 40, 8, 9, 64, 64), ("fp16", 64, 1, 1, 130, 16, 0)])
+def test_append(dtype, D, H, Hkv, T, ps, rot, kv4, interleaved):
+    dt = DT[dtype]
+    P = -(-T // ps) + 2
+    q, k, v = qkv_slices(T, H, Hkv, D, dt, T + D)
+    g = torch.Generator().manual_seed(5)
+    slots = torch.randperm(P * ps, generator=g)[:T]
+    if T > 2:
+        slots[1] = -1          # a padded token
+        slots[T - 1] = -7
+    pos = torch.randint(0, 5000, (T,), generator=g, dtype=torch.int32)
+    cos, sin = R.tables(5000, rot)
+    cache = new_cache(kv4, P, Hkv, ps, D, dt, 3.5)
+    before = [t.cpu().clone() for t in cache]
+    k_out, v_out = (torch.full((T, Hkv, D), 7.0, dtype=dt, device="cuda") for _ in range(2))
+    q_out = torch.full((T, H, D), 7.0, dtype=dt, device="cuda")
+    rotation = dict(pos=pos.cuda(), cos=cos.cuda(), sin=sin.cuda(), interleaved=interleaved) if rot else {}
+    append(kv4, k, v, cache, slots.cuda(), q=q, q_out=q_out, k_out=k_out, v_out=v_out, **rotation)
+    ok()
+    live = slots >= 0
+    qr, qm = R.rotate(q.cpu(), pos, cos, sin, interleaved)
+    kr, km = R.rotate(k.cpu(), pos, cos, sin, interleaved)
+    R.check(q_out[live.cuda()], qr[live], R.rotated_bound(qr, qm, dt)[live], "q_out")
+    R.check(k_out[live.cuda()], kr[live], R.rotated_bound(kr, km, dt)[live], "k_out")
+    for t in (q_out, k_out) + ((v_out,) if kv4 else ()):
+        assert (t.cpu()[~live] == 7.0).all()  # a padded token's rows are left as they were
+    pg, at = slots[live] // ps, slots[live] % ps
+    after = [t.cpu() for t in cache]
+    if not kv4:
+        assert torch.equal(after[0][pg, :, at], k_out.cpu()[live])
+        assert torch.equal(after[1][pg, :, at], v.cpu()[live])
+    else:
+        assert torch.equal(v_out.cpu()[live], v.cpu()[live])
+        check_quantised(kr[live], km[live], after[0][pg, :, at], after[1][pg, :, at], "k", "K")
+        check_quantised(v.cpu().double()[live], torch.zeros_like(v.cpu().double()[live]), after[2][pg, :, at],
+                        after[3][pg, :, at], "v", "V")
+        # the values that the cache stands for
+        append(kv4, k, v, cache, slots.cuda(), q=q, q_out=q_out, k_out=k_out, v_out=v_out, held=True, **rotation)
+        ok()
+        for n, out, c, sc in (("k", k_out, after[0], after[1]), ("v", v_out, after[2], after[3])):
+            val = R.held(c[pg, :, at], sc[pg, :, at], n)
+            size = val.abs() + 16 * sc[pg, :, at][..., 0].double().repeat_interleave(32, -1)
+            R.check(out[live.cuda()], val, R.u_of(dt) * (1 + 2.0 ** -10) * val.abs() + 2.0 ** -23 * size + R.tiny(dt), n)
+    for b, a in zip(before, after):  # every other slot is left as it was
+        a = a.clone()
+        a[pg, :, at] = b[pg, :, at]
+        assert torch.equal(a, b)
+
+
+def test_append_in_place_without_q_and_head_major():
+    T, H, Hkv, D, ps = 21, 6, 3, 128, 16
+    dt = torch.bfloat16
+    q, k, v = qkv_slices(T, H, Hkv, D, dt, 3)
+    cos, sin = (t.cuda() for t in R.tables(64, D))
+    pos, slots = torch.arange(T, dtype=torch.int32).cuda(), torch.arange(T).cuda()
+    c1, c2, c3 = (new_cache(False, 2, Hkv, ps, D, dt, 0.0) for _ in range(3))
+    q_ref, k_ref = fattn.cache_append(k, v, *c1, slots, pos=pos, cos=cos, sin=sin, q=q,
+                                      k_out=torch.empty(T, Hkv, D, dtype=dt, device="cuda"))
+    # without q
+    assert fattn.cache_append(k, v, *c2, slots, pos=pos, cos=cos, sin=sin) == (None, None)
+    # head-major inputs, and q and k turned in place
+    qh, kh, vh = (t.transpose(0, 1).contiguous().transpose(0, 1) for t in (q, k, v))
+    out = fattn.cache_append(kh, vh, *c3, slots, pos=pos, cos=cos, sin=sin, q=qh, q_out=qh, k_out=kh)
+    ok()
+    assert out[0] is qh and torch.equal(qh, q_ref) and torch.equal(kh, k_ref)
+    for a, b, c in zip(c1, c2, c3):
+        assert torch.equal(a, b) and torch.equal(a, c)
+
+
+@pytest.mark.parametrize("kv4", [False, True])
+def test_append_index_out_of_range_is_skipped_and_reported(kv4):
+    T, Hkv, D, ps, P = 6, 2, 64, 16, 2
+    dt = torch.float16
+    _, k, v = qkv_slices(T, 1, Hkv, D, dt, 4)
+    cos, sin = (t.cuda() for t in R.tables(8, D))
+    for slots, pos in (([0, 1, P * ps, 3, 1 << 40, 5], [0, 1, 2, 3, 4, 5]),
+                       ([0, 1, 2, 3, 4, 5], [0, 1, 8, 3, -1, 5])):
+        cache = new_cache(kv4, P, Hkv, ps, D, dt, 2.0)
+        before = [t.clone() for t in cache]
+        append(kv4, k, v, cache, torch.tensor(slots).cuda(), cos=cos, sin=sin,
+               pos=torch.tensor(pos, dtype=torch.int32).cuda())
+        torch.cuda.synchronize()
+        assert fattn.get_device_status() == INVALID
+        assert fattn.get_device_status() == 0
+        for a, b in zip(cache, before):
+            written = (a != b).flatten(3).any(-1).any(1)  # [P, ps]
+            assert written.flatten().nonzero().flatten().tolist() == [0, 1, 3, 5]
+
+
+def test_append_kv4_special_values():
+    D, ps = 64, 16
+    x = torch.randn(5, 1, D, generator=torch.Generator().manual_seed(6))
+    x[0] = 0.0                       # a constant row: scale 0
+    x[1, 0, :32] = -3.25
+    x[2, 0, 3] = math.nan
+    x[3, 0, 5] = math.inf
+    x[4, 0, :32] = math.nan
+    x = x.to(torch.bfloat16).cuda()
+    cache = new_cache(True, 1, 1, ps, D, torch.bfloat16, 0.0)
+    slots = torch.arange(5).cuda()
+    k_out, v_out = torch.empty_like(x), torch.empty_like(x)
+    fattn.cache_append_kv4(x, x, *cache, slots, k_out=k_out, v_out=v_out, held=True)
+    ok()
+    for out in (k_out, v_out):
+        assert torch.isfinite(out).all()
+        assert (out[0] == 0).all() and (out[1, 0, :32] == -3.25).all()
+        row = x[2, 0].double().cpu()
+        fine = torch.cat([row[:3], row[4:32]])
+        assert abs(out[2, 0, 3].item() - fine.min().item()) <= 2.0 ** -8 * abs(fine.min().item())
+        step = (fine.max() - fine.min()).item() / 15
+        assert (torch.cat([out[2, 0, :3], out[2, 0, 4:32]]).double().cpu() - fine).abs().max() <= 0.6 * step
+        assert out[3, 0, 5].item() == 65536.0  # 65504 rounded to bf16
+        assert (out[4, 0, :32] == 0).all()
+    for t in (cache[1], cache[3]):
+        assert torch.isfinite(t).all()
+
+
+# ---------------------------------------------------------------------------
+# Attention over the cache
+# ---------------------------------------------------------------------------
+def make_decode(kv4, lens, H, Hkv, Nq, D, ps, dtype, seed, q_std=2.0, spare=2):
+    """Inputs on the GPU.  Slots behind each sequence's last token hold NaN, and
+    table entries behind its last page are out of range: none may be used."""
+    dt = DT[dtype]
+    g = torch.Generator().manual_seed(seed)
+    B = len(lens)
+    need = [-(-n // ps) for n in lens]
+    P = sum(need) + spare
+    W = max(max(need), 1)
+    perm = torch.randperm(P, generator=g)
+    table = torch.full((B, W), 1 << 30, dtype=torch.int32)
+    table[:, ::2] = -1
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = perm[at:at + n]
+        at += n
+    q = (torch.randn(B, H, Nq, D, generator=g) * q_std).to(dt)
+    used = torch.zeros(P, ps, dtype=torch.bool)
+    for b, n in enumerate(lens):
+        j = torch.arange(n)
+        used[table[b].long()[j // ps], j % ps] = True
+    hidden = ~used[:, None, :, None]
+    if kv4:
+        cache = []
+        for which in "kv":
+            cache.append(R.pack(torch.randint(0, 16, (P, Hkv, ps, D), generator=g), which))
+            s = 0.05 + 0.4 * torch.rand(P, Hkv, ps, D // 32, generator=g)
+            z = -7.5 * s + 0.3 * torch.randn(s.shape, generator=g)
+            cache.append(torch.stack([s, z], -1).half().masked_fill(hidden[..., None], math.nan))
+    else:
+        cache = [torch.randn(P, Hkv, ps, D, generator=g).to(dt).masked_fill(hidden, math.nan) for _ in range(2)]
+    return q.cuda(), [t.cuda() for t in cache], table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+
+
+def run_decode(kv4, q, cache, table, lens, **kw):
+    return (fattn.decode_kv4 if kv4 else fattn.decode)(q, *cache, table, lens, **kw)
+
+
+def check_decode(kv4, q, cache, table, lens, scale, o, lse, what=""):
+    B, H, Nq, D = q.shape
+    dt = q.dtype
+    cache, table = [t.cpu() for t in cache], table.cpu()
+    for b, n in enumerate(lens.tolist()):
+        ends = [max(0, n - Nq + 1 + i) for i in range(Nq)]
+        v_err = 0.0
+        if kv4:
+            rows = [R.gather(t, table[b], n) for t in cache]
+            k, v = R.held(rows[0], rows[1], "k"), R.held(rows[2], rows[3], "v")
+            # V enters as an fp16 number: off by 2^-11 of the value, and its
+            # offset within the conversion (|zero| + 16 scale) by 2^-11 of that
+            off = (rows[3][..., 1].double().abs() + 16 * rows[3][..., 0].double()).repeat_interleave(32, -1)
+            verr = 2.0 ** -11 * (v.abs() + off)
+        else:
+            k, v = (R.gather(t, table[b], n).double() for t in cache)
+            verr = None
+        ro, rl, av, worst = R.attend(q[b].cpu().double(), k, v, scale, ends)
+        if kv4:
+            _, _, v_err, _ = R.attend(q[b].cpu().double(), k, verr, scale, ends)
+        u_p = 2.0 ** -11 if kv4 else R.u_of(dt)
+        bo, bl = R.attend_bounds(ro, rl, av, worst, D, dt, u_p, v_err)
+        empty = torch.tensor([e == 0 for e in ends])
+        got_l = lse[b].cpu().double()
+        assert (o[b].cpu()[:, empty] == 0).all() and (got_l[:, empty] == -math.inf).all(), what
+        if (~empty).any():
+            R.check(o[b][:, (~empty).cuda()], ro[:, ~empty], bo[:, ~empty], "%s O, sequence %d of %d" % (what, b, n))
+            R.check(got_l[:, ~empty], rl[:, ~empty], bl[:, ~empty], "%s LSE, sequence %d of %d" % (what, b, n))
+
+
+LENS = [0, 1, 15, 16, 17, 63, 64, 65, 127, 129, 300, 1000]
+
+
+@pytest.mark.parametrize("kv4", [False, True])
+@pytest.mark.parametrize("dtype,D,H,Hkv,Nq,ps", [
+    ("bf16", 128, 8, 2, 1, 16), ("fp16", 64, 4, 4, 1, 32), ("bf16", 64, 6, 2, 2, 48), ("fp16", 128, 16, 1, 1, 64),
+    ("bf16", 128, 32, 1, 1, 16), ("fp16", 64, 8, 1, 4, 128), ("bf16", 64, 10, 1, 7, 16), ("fp16", 128, 5, 1, 1, 80)])
+def test_decode(dtype, D, H, Hkv, Nq, ps, kv4):
+    q, cache, table, lens = make_decode(kv4, LENS, H, Hkv, Nq, D, ps, dtype, D + H + Nq)
+    scale = fattn._default_scale(D)
+    o, lse = run_decode(kv4, q, cache, table, lens)
+    ok()
+    check_decode(kv4, q, cache, table, lens, scale, o, lse)
+
+
+@pytest.mark.parametrize("kv4", [False, True])
+@pytest.mark.parametrize("B,H,Hkv,n", [(1, 8, 1, 20011), (1, 32, 8, 4097), (200, 4, 2, 70), (2, 64, 1, 3000)])
+def test_decode_work_splits(B, H, Hkv, n, kv4):
+    """Few long sequences (the keys are split over the GPU) and many short ones."""
+    lens = [max(1, n - 13 * b) for b in range(B)]
+    q, cache, table, lens = make_decode(kv4, lens, H, Hkv, 1, 128, 64, "bf16", B + n, q_std=1.0)
+    o, lse = run_decode(kv4, q, cache, table, lens, scale=0.25)
+    ok()
+    check_decode(kv4, q, cache, table, lens, 0.25, o, lse)
+    o2, lse2 = run_decode(kv4, q, cache, table, lens, scale=0.25)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)  # the same call, the same bits
+
+
+@pytest.mark.parametrize("kv4", [False, True])
+def test_decode_scores_of_any_size(kv4):
+    """Scores far from zero, rising along the keys (every key moves the running
+    max), equal scores, and scale 0."""
+    D, ps, n = 64, 16, 700
+    q, cache, table, lens = make_decode(kv4, [n], 4, 2, 1, D, ps, "fp16", 9)
+    if kv4:
+        cache[0].fill_(0)
+        ramp = torch.arange(n, device="cuda").half() * 0.25 - 90
+        for j in range(-(-n // ps)):
+            part = ramp[j * ps:(j + 1) * ps]
+            cache[1][table[0, j], :, :len(part), :, 1] = part[None, :, None]
+            cache[1][table[0, j], :, :len(part), :, 0] = 0
+    else:
+        for j in range(n):
+            cache[0][table[0, j // ps], :, j % ps] = 0.25 * j - 90
+    for scale in (0.125, 1.0, 0.0):
+        for sign in (1.0, -1.0):
+            qq = (q.abs() * sign).contiguous()
+            o, lse = run_decode(kv4, qq, cache, table, lens, scale=scale)
+            ok()
+            check_decode(kv4, qq, cache, table, lens, scale, o, lse, "scale %g" % (scale * sign))
+
+
+@pytest.mark.parametrize("kv4", [False, True])
+def test_decode_tables_out_of_range(kv4):
+    """A page out of range among those a sequence uses: its keys take no part;
+    a length outside the table: cut to it.  Both are reported."""
+    D, ps = 128, 16
+    q, cache, table, lens = make_decode(kv4, [64, 48], 4, 2, 1, D, ps, "bf16", 10)
+    good, _ = run_decode(kv4, q, cache, table, lens)
+    ok()
+    for bad_page in (-1, cache[0].shape[0], 1 << 30):
+        t = table.clone()
+        t[0, 1] = bad_page
+        o, lse = run_decode(kv4, q, cache, t, lens)
+        torch.cuda.synchronize()
+        assert fattn.get_device_status() == INVALID and fattn.get_device_status() == 0
+        assert torch.equal(o[1], good[1])
+        # the keys of the other three pages, in an order of its own
+        t4 = torch.stack([table[0, 0], table[0, 2], table[0, 3]])[None].contiguous()
+        one = torch.tensor([48], dtype=torch.int32).cuda()
+        check_decode(kv4, q[:1], cache, t4, one, fattn._default_scale(D), o[:1], lse[:1], "page %d" % bad_page)
+    for bad_len in (-5, 4 * ps + 1, 2 ** 31 - 1):
+        l = lens.clone()
+        l[0] = bad_len
+        o, lse = run_decode(kv4, q, cache, table, l)
+        torch.cuda.synchronize()
+        assert fattn.get_device_status() == INVALID and fattn.get_device_status() == 0
+        assert torch.equal(o[1], good[1])
+        if bad_len < 0:
+            assert (o[0] == 0).all() and (lse[0] == -math.inf).all()
+        else:
+            assert torch.equal(o[0], good[0])
+
+
+def test_decode_strides_and_page_stride():
+    """q as a slice of a projection, o token-major, K and V pages in one tensor."""
+    B, H, Hkv, Nq, D, ps = 3, 8, 2, 2, 64, 32
+    dt = torch.float16
+    q, cache, table, lens = make_decode(False, [100, 3, 33], H, Hkv, Nq, D, ps, "fp16", 11)
+    o, lse = fattn.decode(q, *cache, table, lens)
+    both = torch.stack(cache, 1).contiguous()  # [P, 2, Hkv, ps, D]
+    proj = torch.zeros(B, Nq, H + 2 * Hkv, D, dtype=dt, device="cuda")
+    proj[:, :, :H] = q.transpose(1, 2)
+    out = torch.zeros(B, Nq, H, D, dtype=dt, device="cuda")
+    o2, lse2 = fattn.decode(proj[:, :, :H].transpose(1, 2), both[:, 0], both[:, 1], table, lens,
+                            out=out.transpose(1, 2))
+    ok()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2) and torch.equal(out.transpose(1, 2), o)
+    o3, none = fattn.decode(q, *cache, table, lens, return_lse=False)
+    assert none is None and torch.equal(o3, o)
+    # an append into the shared tensor, through its page stride
+    _, k, v = qkv_slices(2, 1, Hkv, D, dt, 12)
+    slots = torch.tensor([5, ps * (both.shape[0] - 1) + 1]).cuda()
+    before = both.clone()
+    fattn.cache_append(k, v, both[:, 0], both[:, 1], slots)
+    ok()
+    for t in range(2):
+        p, at = slots[t].item() // ps, slots[t].item() % ps
+        assert torch.equal(both[p, 0, :, at], k[t]) and torch.equal(both[p, 1, :, at], v[t])
+        both[p, :, :, at] = before[p, :, :, at]
+    assert torch.equal(both.nan_to_num(9.0), before.nan_to_num(9.0))
+
+
+def test_offsets_past_32_bits():
+    """A 16-bit pool of more than 2^32 bytes and 2^31 elements per tensor: the
+    last pages are written and read where they are."""
+    Hkv, ps, D = 8, 64, 128
+    P = (1 << 31) // (Hkv * ps * D) + 40
+    cache = [torch.empty(P, Hkv, ps, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    n = 150
+    pages = torch.tensor([P - 1, 3, P - 7], dtype=torch.int32)
+    q, k, v = qkv_slices(n, 16, Hkv, D, torch.bfloat16, 13)
+    j = torch.arange(n)
+    slots = pages.long()[j // ps] * ps + j % ps
+    fattn.cache_append(k, v, *cache, slots.cuda())
+    qd = q[-1:].unsqueeze(2).contiguous()
+    o, lse = fattn.decode(qd, *cache, pages[None].cuda(), torch.tensor([n], dtype=torch.int32).cuda(), scale=0.1)
+    ok()
+    small = [torch.zeros(3, Hkv, ps, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    fattn.cache_append(k, v, *small, j.cuda())
+    table = torch.arange(3, dtype=torch.int32)[None].cuda()
+    lens = torch.tensor([n], dtype=torch.int32).cuda()
+    o2, lse2 = fattn.decode(qd, *small, table, lens, scale=0.1)
+    ok()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    check_decode(False, qd, small, table, lens, 0.1, o, lse)
+
+
+@pytest.mark.parametrize("kv4", [False, True])
+def test_streams_and_graphs(kv4):
+    """A step on another stream, captured and replayed with lengths and tables
+    that change between replays; two graphs with a workspace each."""
+    H, Hkv, D, ps, B = 8, 2, 128, 16, 3
+    q, cache, table, lens = make_decode(kv4, [200, 7, 90], H, Hkv, 1, D, ps, "bf16", 14)
+    _, k, v = qkv_slices(B, 1, Hkv, D, torch.bfloat16, 15)
+    slots = torch.tensor([-1] * B).cuda()
+    o = torch.zeros_like(q)
+    lse = torch.zeros(B, H, 1, device="cuda")
+    wss = [torch.empty(fattn.decode_workspace_bytes(B, H, 1, D, Hkv), dtype=torch.uint8, device="cuda") for _ in range(2)]
+
+    def step(stream=None, ws=None, out=o, l=lse):
+        append(kv4, k, v, cache, slots, stream=stream)
+        return run_decode(kv4, q, cache, table, lens, out=out, lse=l, workspace=ws, stream=stream)
+
+    step(ws=wss[0])
+    ok()
+    first = o.clone()
+    outs = [(torch.zeros_like(o), torch.zeros_like(lse)) for _ in range(2)]
+    graphs = []
+    for ws, (oo, ll) in zip(wss, outs):
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(s):
+            with torch.cuda.graph(g, stream=s):
+                step(stream=s, ws=ws, out=oo, l=ll)
+        torch.cuda.current_stream().wait_stream(s)
+        graphs.append((g, s))
+    for lengths in ([200, 7, 90], [1, 7, 33], [0, 3, 80]):
+        lens.copy_(torch.tensor(lengths, dtype=torch.int32))
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for g, s in graphs:   # both at once, on their own streams
+                with torch.cuda.stream(s):
+                    g.replay()
+        ok()
+        want, want_l = step()
+        ok()
+        for oo, ll in outs:
+            assert torch.equal(oo, want) and torch.equal(ll, want_l)
+        check_decode(kv4, q, cache, table, lens, fattn._default_scale(D), *outs[0])
+    lens.copy_(torch.tensor([200, 7, 90], dtype=torch.int32))
+    step()
+    assert torch.equal(o, first)

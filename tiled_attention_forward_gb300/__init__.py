@@ -21,7 +21,8 @@ import torch
 __all__ = ["fwd", "fwd_host", "bwd", "bwd_host", "bwd_workspace_bytes", "fwd_unfused", "fwd_unfused_static", "unfused_workspace_bytes",
            "UNFUSED_STATIC_BYTES", "plan", "get_device_status", "selftest_wait_timeout",
            "status_string", "library_path", "load", "FattnError", "FattnLibraryMissing",
-           "DTYPE_CODES", "STATUS"]
+           "DTYPE_CODES", "STATUS", "cache_append", "cache_append_kv4", "decode", "decode_kv4",
+           "decode_workspace_bytes", "KV4_GROUP"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libfattn.so")
@@ -31,6 +32,7 @@ STATUS = {0: "FATTN_OK", 1: "FATTN_ERR_INVALID_ARG", 2: "FATTN_ERR_UNSUPPORTED",
           3: "FATTN_ERR_MISALIGNED", 4: "FATTN_ERR_CUDA", 5: "FATTN_ERR_TIMEOUT",
           6: "FATTN_ERR_NO_DEVICE", 7: "FATTN_ERR_INTERNAL"}
 UNFUSED_STATIC_BYTES = 64 << 20  # FATTN_UNFUSED_STATIC_BYTES
+KV4_GROUP = 32  # elements of a 4-bit cache row that share one (scale, zero)
 PLAN_FIELDS = ("path", "grid_x", "grid_y", "threads", "smem_bytes", "tasks", "kv_tiles",
                "rows_per_task", "keys_per_kv_tile")
 
@@ -82,6 +84,13 @@ def load():
     lib.fattn_unfused_workspace_bytes.restype = i64
     lib.fattn_plan.argtypes = [i64, i64, i64, i64, ci, ci, ci, ctypes.POINTER(i64)]
     lib.fattn_plan_head_group.argtypes = [i64, i64, i64, i64, i64, ctypes.POINTER(i64)]
+    lib.fattn_cache_append.argtypes = [vp] * 8 + [i64] * 3 + [vp] * 4 + [i64] * 2 + [ci] + [i64] * 4 + [ci, vp]
+    lib.fattn_cache_append_kv4.argtypes = ([vp] * 11 + [i64] * 2 + [vp] * 4 + [i64] * 2 + [ci] * 2 + [i64] * 4 +
+                                           [ci, vp])
+    lib.fattn_decode_workspace_bytes.argtypes = [i64] * 5
+    lib.fattn_decode_workspace_bytes.restype = i64
+    lib.fattn_decode.argtypes = ([vp] * 6 + [i64] * 3 + [vp, i64, vp, vp] + [i64] * 6 + [f32, ci, vp])
+    lib.fattn_decode_kv4.argtypes = ([vp] * 8 + [i64] * 2 + [vp, i64, vp, vp] + [i64] * 6 + [f32, ci, vp])
     lib.fattn_get_device_status.argtypes = [vp]
     lib.fattn_selftest_wait_timeout.argtypes = [ctypes.c_uint64, vp]
     lib.fattn_status_string.argtypes = [ci]
@@ -89,6 +98,7 @@ def load():
     lib.fattn_version.argtypes = []
     for f in ("fattn_fwd", "fattn_fwd_gqa", "fattn_fwd_host", "fattn_fwd_unfused", "fattn_bwd", "fattn_bwd_gqa", "fattn_bwd_host",
               "fattn_fwd_unfused_static", "fattn_plan", "fattn_plan_head_group",
+              "fattn_cache_append", "fattn_cache_append_kv4", "fattn_decode", "fattn_decode_kv4",
               "fattn_get_device_status",
               "fattn_selftest_wait_timeout", "fattn_version"):
         getattr(lib, f).restype = ci
@@ -348,6 +358,240 @@ def fwd_unfused_static(q, k, v, causal=False, scale=None, out=None, lse=None, re
                                           DTYPE_CODES[q.dtype], _stream_handle(stream))
     _check(rc, "fattn_fwd_unfused_static")
     return out, (lse if return_lse else None)
+
+
+# ---------------------------------------------------------------------------
+# Serving: rows by strides, paged caches
+# ---------------------------------------------------------------------------
+_STRIDES = {n: ctypes.c_int64 * n for n in (6, 8, 10, 12)}
+
+
+def _on(device, *tensors):
+    """Every tensor (None skipped) on one CUDA device."""
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError("all tensors must be on %s" % device)
+
+
+def _rows(name, t, shape, dtype):
+    """Strides of a 16-bit tensor whose last dimension is contiguous; 0 stands
+    for a dimension of one element (its stride is never used)."""
+    if tuple(t.shape) != shape or t.dtype != dtype:
+        raise ValueError("%s must be %s %s" % (name, list(shape), dtype))
+    st = t.stride()
+    if st[-1] != 1:
+        raise ValueError("%s must be contiguous along its last dimension" % name)
+    return [0 if n == 1 else x for n, x in zip(shape[:-1], st)]
+
+
+def _table(name, t, shape, dtype):
+    if tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError("%s must be contiguous %s %s" % (name, list(shape), dtype))
+
+
+def _call(device, stream, where, fn, *args):
+    """fn(*args, stream) with `device` current; the stream defaults to torch's
+    current one on that device."""
+    handle = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
+    if torch._C._cuda_getDevice() == device.index:
+        _check(fn(*args, handle), where)
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, handle), where)
+
+
+def _pages(k_pages, v_pages, Hkv, D, dtype):
+    """(page stride, pages, page size) of a 16-bit cache."""
+    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.shape[1] != Hkv or k_pages.shape[3] != D:
+        raise ValueError("k_pages and v_pages must be [pages, Hkv, page_size, D]")
+    if k_pages.dtype != dtype or v_pages.dtype != dtype:
+        raise ValueError("the cache must have the rows' dtype")
+    P, _, ps, _ = k_pages.shape
+    inner = Hkv * ps * D
+    stride = inner
+    for n, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if P > 0 and not t[0].is_contiguous():
+            raise ValueError("each page of %s must be contiguous" % n)
+    if P > 1:
+        stride = k_pages.stride(0)
+        if v_pages.stride(0) != stride:
+            raise ValueError("k_pages and v_pages must have one page stride")
+    return stride, P, ps
+
+
+def _pages_kv4(k_codes, k_scales, v_codes, v_scales, Hkv, D):
+    """(pages, page size) of a 4-bit cache."""
+    if k_codes.dim() != 4:
+        raise ValueError("codes must be [pages, Hkv, page_size, D/2]")
+    P, _, ps, _ = k_codes.shape
+    for n, c, sc in (("k", k_codes, k_scales), ("v", v_codes, v_scales)):
+        _table(n + "_codes", c, (P, Hkv, ps, D // 2), torch.uint8)
+        _table(n + "_scales", sc, (P, Hkv, ps, D // KV4_GROUP, 2), torch.float16)
+    return P, ps
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _append_rows(k, v, q, q_out, k_out, v_out, slots, pos, cos, sin):
+    """Checks what both appends share; returns (T, H, Hkv, D, strides, rot, max_pos, q_out)."""
+    if not k.is_cuda or k.dim() != 3:
+        raise ValueError("k must be a CUDA tensor [T, Hkv, D]")
+    T, Hkv, D = k.shape
+    dt = k.dtype
+    if dt not in DTYPE_CODES:
+        raise ValueError("dtype must be float16 or bfloat16")
+    H = 0
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError("q must be [T, H, D]")
+        H = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty((T, H, D), dtype=dt, device=k.device)
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    st = []
+    for n, t, h in (("q", q, H), ("k", k, Hkv), ("v", v, Hkv), ("q_out", q_out, H), ("k_out", k_out, Hkv),
+                    ("v_out", v_out, Hkv)):
+        st += [0, 0] if t is None else _rows(n, t, (T, h, D), dt)
+    _table("slots", slots, (T,), torch.int64)
+    rot = max_pos = 0
+    if cos is not None:
+        if sin is None or pos is None or cos.dim() != 2:
+            raise ValueError("a rotation needs pos, and cos and sin [max_pos, rot/2]")
+        max_pos, rot = cos.shape[0], 2 * cos.shape[1]
+        for n, t in (("cos", cos), ("sin", sin)):
+            _table(n, t, tuple(cos.shape), torch.float32)
+        _table("pos", pos, (T,), torch.int32)
+    elif sin is not None:
+        raise ValueError("a rotation needs cos and sin")
+    _on(k.device, q, v, q_out, k_out, v_out, slots, pos, cos, sin)
+    return T, H, Hkv, D, st, rot, max_pos, q_out
+
+
+def cache_append(k, v, k_pages, v_pages, slots, pos=None, cos=None, sin=None, interleaved=False, q=None,
+                 q_out=None, k_out=None, stream=None):
+    """Appends T new tokens to a 16-bit paged cache, rotating k and q by position.
+
+    k, v: [T, Hkv, D] CUDA tensors (float16 or bfloat16, D in {64, 128}), q
+    (optional): [T, H, D]; any token and head strides (slices of one
+    projection), last dimension contiguous.  k_pages, v_pages: [pages, Hkv,
+    page_size, D], page_size a multiple of 16, one stride between pages.
+    slots: int64 [T] = page * page_size + place, all different; a negative
+    slot skips its token.  pos: int32 [T], rows of cos and sin, float32
+    [max_pos, rot/2] (rot a multiple of 16, the first rot elements of a row
+    turn: element i with i + rot/2, or 2i with 2i+1 when ``interleaved``);
+    without cos and sin nothing turns.  Returns (q_out, k_out): q rotated (None
+    without q; allocated here when None) and, where ``k_out`` is given, k as
+    the cache holds it.  ``q_out`` may be q itself.  An index out of range is
+    skipped and reported by ``get_device_status``."""
+    T, H, Hkv, D, st, rot, max_pos, q_out = _append_rows(k, v, q, q_out, k_out, None, slots, pos, cos, sin)
+    stride, P, ps = _pages(k_pages, v_pages, Hkv, D, k.dtype)
+    _on(k.device, k_pages, v_pages)
+    _call(k.device, stream, "fattn_cache_append", load().fattn_cache_append,
+          _ptr(q), k.data_ptr(), v.data_ptr(), _ptr(q_out), _ptr(k_out), _STRIDES[10](*st[:10]),
+          k_pages.data_ptr(), v_pages.data_ptr(), stride, P, ps, slots.data_ptr(), _ptr(pos), _ptr(cos),
+          _ptr(sin), max_pos, rot, int(bool(interleaved)), T, H, Hkv, D, DTYPE_CODES[k.dtype])
+    return q_out, k_out
+
+
+def cache_append_kv4(k, v, k_codes, k_scales, v_codes, v_scales, slots, pos=None, cos=None, sin=None,
+                     interleaved=False, q=None, q_out=None, k_out=None, v_out=None, held=False, stream=None):
+    """``cache_append`` into a 4-bit cache: k_codes, v_codes uint8 [pages, Hkv,
+    page_size, D/2]; k_scales, v_scales float16 [pages, Hkv, page_size, D/32,
+    2] = (scale, zero) of each group of 32 elements (the nibble order is in
+    include/fattn.h).  Returns (q_out, k_out, v_out); where given, k_out and
+    v_out receive the rotated k and v, or with ``held`` the values that the
+    cache now stands for."""
+    T, H, Hkv, D, st, rot, max_pos, q_out = _append_rows(k, v, q, q_out, k_out, v_out, slots, pos, cos, sin)
+    P, ps = _pages_kv4(k_codes, k_scales, v_codes, v_scales, Hkv, D)
+    _on(k.device, k_codes, k_scales, v_codes, v_scales)
+    _call(k.device, stream, "fattn_cache_append_kv4", load().fattn_cache_append_kv4,
+          _ptr(q), k.data_ptr(), v.data_ptr(), _ptr(q_out), _ptr(k_out), _ptr(v_out), _STRIDES[12](*st),
+          k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), P, ps,
+          slots.data_ptr(), _ptr(pos), _ptr(cos), _ptr(sin), max_pos, rot, int(bool(interleaved)),
+          int(bool(held)), T, H, Hkv, D, DTYPE_CODES[k.dtype])
+    return q_out, k_out, v_out
+
+
+def decode_workspace_bytes(B, H, Nq, D, Hkv=None):
+    """Bytes of workspace ``decode`` and ``decode_kv4`` need (whatever the sequences' lengths)."""
+    return int(load().fattn_decode_workspace_bytes(int(B), int(H), int(H if Hkv is None else Hkv), int(Nq), int(D)))
+
+
+def _decode_args(q, Hkv, block_table, seq_lens, scale, out, lse, workspace, return_lse):
+    B, H, Nq, D = q.shape
+    dt = q.dtype
+    if dt not in DTYPE_CODES:
+        raise ValueError("dtype must be float16 or bfloat16")
+    if scale is None:
+        scale = _default_scale(D)
+    if out is None:
+        out = torch.empty((B, H, Nq, D), dtype=dt, device=q.device)
+    if not return_lse:
+        lse = None
+    elif lse is None:
+        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+    else:
+        _table("lse", lse, (B, H, Nq), torch.float32)
+    st = _rows("q", q, (B, H, Nq, D), dt) + _rows("out", out, (B, H, Nq, D), dt)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, pages per sequence]")
+    _table("block_table", block_table, (B, block_table.shape[1]), torch.int32)
+    _table("seq_lens", seq_lens, (B,), torch.int32)
+    if workspace is None:
+        workspace = torch.empty(max(decode_workspace_bytes(B, H, Nq, D, Hkv), 16), dtype=torch.uint8,
+                                device=q.device)
+    _on(q.device, out, lse, block_table, seq_lens, workspace)
+    return out, lse, workspace, float(scale), _STRIDES[6](*st)
+
+
+def decode(q, k_pages, v_pages, block_table, seq_lens, scale=None, out=None, lse=None, workspace=None,
+           return_lse=True, stream=None):
+    """Attention of the last Nq tokens of each sequence over a 16-bit paged
+    cache that already holds them (``cache_append``).
+
+    q: [B, H, Nq, D] (any strides, last dimension contiguous); k_pages,
+    v_pages: [pages, Hkv, page_size, D] with H a multiple of Hkv; block_table:
+    int32 [B, pages per sequence]; seq_lens: int32 [B], cached tokens of each
+    sequence.  Token i of the Nq sees keys 0 .. seq_lens[b] - Nq + i.  Returns
+    (o, lse) like ``fwd``: o [B, H, Nq, D], lse float32 [B, H, Nq]; a row
+    without keys gives o = 0, lse = -inf.  ``workspace``: a CUDA uint8 tensor
+    of at least ``decode_workspace_bytes`` bytes (allocated here when None);
+    calls running at the same time need one each."""
+    if not q.is_cuda or q.dim() != 4:
+        raise ValueError("q must be a CUDA tensor [B, H, Nq, D]")
+    B, H, Nq, D = q.shape
+    Hkv = k_pages.shape[1] if k_pages.dim() == 4 else 0
+    stride, P, ps = _pages(k_pages, v_pages, Hkv, D, q.dtype)
+    out, lse, workspace, scale, st = _decode_args(q, Hkv, block_table, seq_lens, scale, out, lse, workspace,
+                                                  return_lse)
+    _on(q.device, k_pages, v_pages)
+    _call(q.device, stream, "fattn_decode", load().fattn_decode,
+          q.data_ptr(), out.data_ptr(), _ptr(lse), st, k_pages.data_ptr(), v_pages.data_ptr(), stride, P, ps,
+          block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size(), B, H, Hkv, Nq, D, scale, DTYPE_CODES[q.dtype])
+    return out, lse
+
+
+def decode_kv4(q, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens, scale=None, out=None, lse=None,
+               workspace=None, return_lse=True, stream=None):
+    """``decode`` over a 4-bit cache (``cache_append_kv4``)."""
+    if not q.is_cuda or q.dim() != 4:
+        raise ValueError("q must be a CUDA tensor [B, H, Nq, D]")
+    B, H, Nq, D = q.shape
+    Hkv = k_codes.shape[1] if k_codes.dim() == 4 else 0
+    P, ps = _pages_kv4(k_codes, k_scales, v_codes, v_scales, Hkv, D)
+    out, lse, workspace, scale, st = _decode_args(q, Hkv, block_table, seq_lens, scale, out, lse, workspace,
+                                                  return_lse)
+    _on(q.device, k_codes, k_scales, v_codes, v_scales)
+    _call(q.device, stream, "fattn_decode_kv4", load().fattn_decode_kv4,
+          q.data_ptr(), out.data_ptr(), _ptr(lse), st, k_codes.data_ptr(), k_scales.data_ptr(),
+          v_codes.data_ptr(), v_scales.data_ptr(), P, ps, block_table.data_ptr(), block_table.shape[1],
+          seq_lens.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), B, H, Hkv,
+          Nq, D, scale, DTYPE_CODES[q.dtype])
+    return out, lse
 
 
 def plan(B, H, N, D, causal=False, dtype=torch.bfloat16, num_sms=0):

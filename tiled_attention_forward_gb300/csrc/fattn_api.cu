@@ -5,6 +5,7 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <utility>
 #include <cudaTypedefs.h>
 
 #include "fattn.h"
@@ -86,6 +87,65 @@ int current_sm_count(int* sms) {
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// A set of equal intervals of bytes, `outer` apart: the rows of a strided
+// tensor, or the pages of a pool.  `inner` is the extent of one interval.
+struct View {
+    uintptr_t p = 0;
+    uintptr_t total = 0;  // first byte to past the last one; 0: empty
+    uintptr_t outer = 0;
+    uintptr_t inner = 0;
+};
+
+// 16-bit rows of D elements at strides (s0, s1), n0 x n1 of them.
+View rows_view(const void* p, int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t D) {
+    View v;
+    if (!p || n0 <= 0 || n1 <= 0) return v;
+    v.p = reinterpret_cast<uintptr_t>(p);
+    const bool first_outer = s0 >= s1;
+    const int64_t no = first_outer ? n0 : n1, so = first_outer ? s0 : s1;
+    const int64_t ni = first_outer ? n1 : n0, si = first_outer ? s1 : s0;
+    v.inner = static_cast<uintptr_t>(2 * ((ni - 1) * si + D));
+    v.outer = static_cast<uintptr_t>(2 * so);
+    v.total = static_cast<uintptr_t>(2 * (no - 1) * so) + v.inner;
+    return v;
+}
+
+View dense_view(const void* p, int64_t bytes) {
+    View v;
+    if (!p || bytes <= 0) return v;
+    v.p = reinterpret_cast<uintptr_t>(p);
+    v.total = v.inner = v.outer = static_cast<uintptr_t>(bytes);
+    return v;
+}
+
+// Whether two views share a byte.  Views with one outer stride whose intervals
+// fit into it (slices of one tensor) are compared modulo that stride; all
+// others by their whole ranges.
+bool views_overlap(const View& a, const View& b) {
+    if (a.total == 0 || b.total == 0) return false;
+    if (!(a.p < b.p + b.total && b.p < a.p + a.total)) return false;
+    if (a.outer == b.outer && a.inner <= a.outer && b.inner <= b.outer) {
+        const uintptr_t m = a.outer;
+        const uintptr_t d = (b.p >= a.p) ? (b.p - a.p) % m : (m - (a.p - b.p) % m) % m;  // b's place in a's period
+        return d < a.inner || d + b.inner > m;
+    }
+    return true;
+}
+
+bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0 && s <= kMaxElements; }
+
+// Sizes of a paged cache and of its rows.
+int validate_cache(int64_t num_pages, int64_t page_size, int64_t Hkv, int64_t D, int dtype) {
+    if (dtype != FATTN_F32 && dtype != FATTN_F16 && dtype != FATTN_BF16) return FATTN_ERR_INVALID_ARG;
+    if (Hkv <= 0 || num_pages < 0 || page_size <= 0 || D < 0) return FATTN_ERR_INVALID_ARG;
+    if (dtype == FATTN_F32 || (D != 64 && D != 128)) return FATTN_ERR_UNSUPPORTED;
+    if (page_size % 16 != 0 || page_size > 65536) return FATTN_ERR_UNSUPPORTED;
+    if (num_pages > 0x7fffffffll || Hkv > (int64_t(1) << 16) ||
+        num_pages * page_size > kMaxElements / (Hkv * D))
+        return FATTN_ERR_UNSUPPORTED;
+    return FATTN_OK;
+}
 
 // K/V tiles one task visits: Q rows [r0, r0+rows) against keys, Bc-key tiles.
 int64_t kv_tiles_for(int64_t r0, int64_t rows, int64_t N, int64_t bc, bool causal) {
@@ -650,17 +710,295 @@ int fattn_bwd_host(const void* q_host, const void* k_host, const void* v_host, c
     return FATTN_OK;
 }
 
+namespace {
+
+// fattn_cache_append and fattn_cache_append_kv4: `a` comes filled but for what
+// is derived here.
+int run_append(AppendArgs& a, const int64_t* strides, int64_t num_pages, int64_t page_size, int64_t rot,
+               int64_t T, int64_t H, int64_t Hkv, int64_t D, int dtype, bool kv4, fattn_stream_t stream_h) {
+    int st = validate_cache(num_pages, page_size, Hkv, D, dtype);
+    if (st != FATTN_OK) return st;
+    if (T < 0 || rot < 0 || rot > D || !strides) return FATTN_ERR_INVALID_ARG;
+    if (rot % 16 != 0) return FATTN_ERR_UNSUPPORTED;
+    if (T == 0) return FATTN_OK;
+    if (T > (int64_t(1) << 30)) return FATTN_ERR_UNSUPPORTED;
+    if ((a.q == nullptr) != (a.q_out == nullptr)) return FATTN_ERR_INVALID_ARG;
+    if (!a.q) H = 0;
+    if (H < 0 || (a.q && H == 0)) return FATTN_ERR_INVALID_ARG;
+    if (H > (int64_t(1) << 16)) return FATTN_ERR_UNSUPPORTED;
+    if (!a.k || !a.v || !a.k_pages || !a.v_pages || !a.slots || (kv4 && (!a.k_scales || !a.v_scales)))
+        return FATTN_ERR_INVALID_ARG;
+    if (rot > 0 && (!a.pos || !a.cos || !a.sin || a.max_pos < 0)) return FATTN_ERR_INVALID_ARG;
+    const void* rows[6] = {a.q, a.k, a.v, a.q_out, a.k_out, a.v_out};
+    const int64_t heads[6] = {H, Hkv, Hkv, H, Hkv, Hkv};
+    int64_t* dst[6][2] = {{&a.q_ts, &a.q_hs},   {&a.k_ts, &a.k_hs},   {&a.v_ts, &a.v_hs},
+                          {&a.qo_ts, &a.qo_hs}, {&a.ko_ts, &a.ko_hs}, {&a.vo_ts, &a.vo_hs}};
+    View views[6];
+    for (int i = 0; i < 6; ++i) {
+        if (!rows[i]) continue;
+        const int64_t ts = strides[2 * i], hs = strides[2 * i + 1];
+        if (!stride_ok(ts) || !stride_ok(hs)) return FATTN_ERR_INVALID_ARG;
+        if (T * ts > kMaxElements || heads[i] * hs > kMaxElements) return FATTN_ERR_UNSUPPORTED;
+        if (!aligned16(rows[i])) return FATTN_ERR_MISALIGNED;
+        if (i >= 3 && ((T > 1 && ts < D) || (heads[i] > 1 && hs < D))) return FATTN_ERR_INVALID_ARG;
+        *dst[i][0] = ts;
+        *dst[i][1] = hs;
+        views[i] = rows_view(rows[i], T, ts, heads[i], hs, D);
+    }
+    const int64_t page_rows = num_pages * page_size * Hkv;
+    if (!aligned16(a.k_pages) || !aligned16(a.v_pages) || (kv4 && (!aligned16(a.k_scales) || !aligned16(a.v_scales))) ||
+        (reinterpret_cast<uintptr_t>(a.slots) & 7u) || (rot > 0 && ((reinterpret_cast<uintptr_t>(a.pos) & 3u) ||
+        !aligned16(a.cos) || !aligned16(a.sin))))
+        return FATTN_ERR_MISALIGNED;
+    View cache[4];
+    if (kv4) {
+        cache[0] = dense_view(a.k_pages, page_rows * (D / 2));
+        cache[1] = dense_view(a.v_pages, page_rows * (D / 2));
+        cache[2] = dense_view(a.k_scales, page_rows * (D / kKv4Group) * 4);
+        cache[3] = dense_view(a.v_scales, page_rows * (D / kKv4Group) * 4);
+    } else {
+        const int64_t inner = Hkv * page_size * D;
+        if (!stride_ok(a.page_stride) || a.page_stride < inner) return FATTN_ERR_INVALID_ARG;
+        if (num_pages * a.page_stride > kMaxElements) return FATTN_ERR_UNSUPPORTED;
+        cache[0] = rows_view(a.k_pages, num_pages, a.page_stride, 1, 0, inner);
+        cache[1] = rows_view(a.v_pages, num_pages, a.page_stride, 1, 0, inner);
+    }
+    const View tables[4] = {dense_view(a.slots, T * 8), dense_view(rot > 0 ? a.pos : nullptr, T * 4),
+                            dense_view(rot > 0 ? a.cos : nullptr, a.max_pos * (rot / 2) * 4),
+                            dense_view(rot > 0 ? a.sin : nullptr, a.max_pos * (rot / 2) * 4)};
+    for (int i = 0; i < 4; ++i) {
+        for (int j = 0; j < 6; ++j)
+            if (views_overlap(cache[i], views[j])) return FATTN_ERR_INVALID_ARG;
+        for (int j = i + 1; j < 4; ++j)
+            if (views_overlap(cache[i], cache[j])) return FATTN_ERR_INVALID_ARG;
+        for (int j = 0; j < 4; ++j)
+            if (views_overlap(cache[i], tables[j])) return FATTN_ERR_INVALID_ARG;
+    }
+    for (int i = 3; i < 6; ++i) {
+        if (!rows[i]) continue;
+        // An output's own rows must not run into one another.
+        if (T > 1 && heads[i] > 1 && views[i].inner > views[i].outer) return FATTN_ERR_INVALID_ARG;
+        for (int j = 0; j < 6; ++j) {
+            if (j == i) continue;
+            const bool itself = j == i - 3 && rows[j] == rows[i] && *dst[j][0] == *dst[i][0] && *dst[j][1] == *dst[i][1];
+            if (!itself && views_overlap(views[i], views[j])) return FATTN_ERR_INVALID_ARG;
+        }
+        for (int j = 0; j < 4; ++j)
+            if (views_overlap(views[i], tables[j])) return FATTN_ERR_INVALID_ARG;
+    }
+    int sms = 0;
+    st = current_sm_count(&sms);
+    if (st != FATTN_OK) return st;
+    a.T = T;
+    a.num_slots = num_pages * page_size;
+    a.page_size = static_cast<int>(page_size);
+    a.H = static_cast<int>(H);
+    a.Hkv = static_cast<int>(Hkv);
+    a.rot = static_cast<int>(rot);
+    const cudaError_t e = append_launch(a, static_cast<int>(D), dtype == FATTN_BF16, kv4,
+                                        reinterpret_cast<cudaStream_t>(stream_h));
+    return e == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
+}
+
+// fattn_decode and fattn_decode_kv4.
+int run_decode(DecodeArgs& a, const int64_t* strides, int64_t num_pages, int64_t page_size, int64_t table_width,
+               int64_t ws_bytes, int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t D, float scale, int dtype,
+               bool kv4, fattn_stream_t stream_h) {
+    int st = validate_cache(num_pages, page_size, Hkv, D, dtype);
+    if (st != FATTN_OK) return st;
+    if (B < 0 || H < 0 || Nq < 0 || table_width < 0 || !strides || H % Hkv != 0) return FATTN_ERR_INVALID_ARG;
+    if (!std::isfinite(scale) || scale < 0.f) return FATTN_ERR_INVALID_ARG;
+    if (B == 0 || H == 0 || Nq == 0) return FATTN_OK;
+    const int64_t need = fattn_decode_workspace_bytes(B, H, Hkv, Nq, D);
+    if (need <= 0 || table_width > 0x7fffffffll / page_size) return FATTN_ERR_UNSUPPORTED;
+    if (!a.q || !a.o || !a.k_pages || !a.v_pages || (kv4 && (!a.k_scales || !a.v_scales)) || !a.seq_lens ||
+        (table_width > 0 && !a.block_table) || !a.workspace || ws_bytes < need)
+        return FATTN_ERR_INVALID_ARG;
+    for (int i = 0; i < 6; ++i) {
+        if (!stride_ok(strides[i])) return FATTN_ERR_INVALID_ARG;
+        if (strides[i] > kMaxElements / (i % 3 == 0 ? B : (i % 3 == 1 ? H : Nq))) return FATTN_ERR_UNSUPPORTED;
+    }
+    if (!aligned16(a.q) || !aligned16(a.o) || !aligned16(a.k_pages) || !aligned16(a.v_pages) ||
+        (kv4 && (!aligned16(a.k_scales) || !aligned16(a.v_scales))) || !aligned16(a.workspace) ||
+        (reinterpret_cast<uintptr_t>(a.lse) & 3u) || (reinterpret_cast<uintptr_t>(a.block_table) & 3u) ||
+        (reinterpret_cast<uintptr_t>(a.seq_lens) & 3u))
+        return FATTN_ERR_MISALIGNED;
+    // Whole ranges; o's rows must not run into one another: some order of its
+    // strides nests.
+    auto extent = [&](const int64_t* s) { return 2 * ((B - 1) * s[0] + (H - 1) * s[1] + (Nq - 1) * s[2] + D); };
+    {
+        int64_t n[3] = {B, H, Nq}, s[3] = {strides[3], strides[4], strides[5]};
+        for (int i = 0; i < 2; ++i)
+            for (int j = 0; j < 2; ++j)
+                if (s[j] > s[j + 1]) {
+                    std::swap(s[j], s[j + 1]);
+                    std::swap(n[j], n[j + 1]);
+                }
+        int64_t inner = D;
+        for (int i = 0; i < 3; ++i) {
+            if (n[i] > 1 && s[i] < inner) return FATTN_ERR_INVALID_ARG;
+            if (n[i] > 1) inner = (n[i] - 1) * s[i] + inner;
+        }
+    }
+    const int64_t page_rows = num_pages * page_size * Hkv;
+    const int64_t inner = Hkv * page_size * D;
+    if (!kv4) {
+        if (!stride_ok(a.page_stride) || a.page_stride < inner) return FATTN_ERR_INVALID_ARG;
+        if (num_pages * a.page_stride > kMaxElements) return FATTN_ERR_UNSUPPORTED;
+    }
+    const int64_t page_bytes = kv4 ? page_rows * (D / 2)
+                                   : (num_pages > 0 ? 2 * ((num_pages - 1) * a.page_stride + inner) : 0);
+    const int64_t scale_bytes = kv4 ? page_rows * (D / kKv4Group) * 4 : 0;
+    const View in[7] = {dense_view(a.q, extent(strides)),          dense_view(a.k_pages, page_bytes),
+                        dense_view(a.v_pages, page_bytes),         dense_view(a.k_scales, scale_bytes),
+                        dense_view(a.v_scales, scale_bytes),       dense_view(a.block_table, B * table_width * 4),
+                        dense_view(a.seq_lens, B * 4)};
+    const View out[3] = {dense_view(a.o, extent(strides + 3)), dense_view(a.lse, B * H * Nq * 4),
+                         dense_view(a.workspace, need)};
+    for (int i = 0; i < 3; ++i) {
+        for (const View& v : in)
+            if (views_overlap(out[i], v)) return FATTN_ERR_INVALID_ARG;
+        for (int j = i + 1; j < 3; ++j)
+            if (views_overlap(out[i], out[j])) return FATTN_ERR_INVALID_ARG;
+    }
+    int sms = 0;
+    st = current_sm_count(&sms);
+    if (st != FATTN_OK) return st;
+    a.q_bs = strides[0];
+    a.q_hs = strides[1];
+    a.q_ns = strides[2];
+    a.o_bs = strides[3];
+    a.o_hs = strides[4];
+    a.o_ns = strides[5];
+    a.num_pages = num_pages;
+    a.table_width = table_width;
+    a.page_size = static_cast<int>(page_size);
+    a.B = static_cast<int>(B);
+    a.H = static_cast<int>(H);
+    a.Hkv = static_cast<int>(Hkv);
+    a.Nq = static_cast<int>(Nq);
+    a.scale_log2 = scale * kLog2e;
+    const cudaError_t e = decode_launch(a, static_cast<int>(D), dtype == FATTN_BF16, kv4, sms,
+                                        reinterpret_cast<cudaStream_t>(stream_h));
+    return e == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
+}
+
+}  // namespace
+
+int fattn_cache_append(const void* q, const void* k, const void* v, void* q_out, void* k_out,
+                       const int64_t* strides, void* k_pages, void* v_pages, int64_t page_stride,
+                       int64_t num_pages, int64_t page_size, const int64_t* slots, const int32_t* pos,
+                       const float* cos, const float* sin, int64_t max_pos, int64_t rot, int interleaved,
+                       int64_t T, int64_t H, int64_t Hkv, int64_t D, int dtype, fattn_stream_t stream_h) {
+    AppendArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_out = q_out;
+    a.k_out = k_out;
+    a.k_pages = k_pages;
+    a.v_pages = v_pages;
+    a.page_stride = page_stride;
+    a.slots = slots;
+    a.pos = pos;
+    a.cos = cos;
+    a.sin = sin;
+    a.max_pos = max_pos;
+    a.interleaved = interleaved != 0;
+    return run_append(a, strides, num_pages, page_size, rot, T, H, Hkv, D, dtype, false, stream_h);
+}
+
+int fattn_cache_append_kv4(const void* q, const void* k, const void* v, void* q_out, void* k_out, void* v_out,
+                           const int64_t* strides, void* k_codes, void* k_scales, void* v_codes,
+                           void* v_scales, int64_t num_pages, int64_t page_size, const int64_t* slots,
+                           const int32_t* pos, const float* cos, const float* sin, int64_t max_pos,
+                           int64_t rot, int interleaved, int held, int64_t T, int64_t H, int64_t Hkv,
+                           int64_t D, int dtype, fattn_stream_t stream_h) {
+    AppendArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_out = q_out;
+    a.k_out = k_out;
+    a.v_out = v_out;
+    a.k_pages = k_codes;
+    a.v_pages = v_codes;
+    a.k_scales = k_scales;
+    a.v_scales = v_scales;
+    a.slots = slots;
+    a.pos = pos;
+    a.cos = cos;
+    a.sin = sin;
+    a.max_pos = max_pos;
+    a.interleaved = interleaved != 0;
+    a.held = held != 0;
+    return run_append(a, strides, num_pages, page_size, rot, T, H, Hkv, D, dtype, true, stream_h);
+}
+
+int64_t fattn_decode_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t D) {
+    if (B <= 0 || H <= 0 || Hkv <= 0 || Nq <= 0 || H % Hkv != 0 || (D != 64 && D != 128)) return 0;
+    const int64_t lim = int64_t(1) << 30;
+    if (B > lim || H > lim || Nq > lim || B * H > lim || B * H * Nq > lim) return 0;
+    return decode_workspace_bytes(B, H, Hkv, Nq, D);
+}
+
+int fattn_decode(const void* q, void* o, float* lse, const int64_t* strides, const void* k_pages,
+                 const void* v_pages, int64_t page_stride, int64_t num_pages, int64_t page_size,
+                 const int32_t* block_table, int64_t table_width, const int32_t* seq_lens, void* workspace,
+                 int64_t workspace_bytes, int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t D, float scale,
+                 int dtype, fattn_stream_t stream_h) {
+    DecodeArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.q = q;
+    a.o = o;
+    a.lse = lse;
+    a.k_pages = k_pages;
+    a.v_pages = v_pages;
+    a.page_stride = page_stride;
+    a.block_table = block_table;
+    a.seq_lens = seq_lens;
+    a.workspace = workspace;
+    return run_decode(a, strides, num_pages, page_size, table_width, workspace_bytes, B, H, Hkv, Nq, D, scale,
+                      dtype, false, stream_h);
+}
+
+int fattn_decode_kv4(const void* q, void* o, float* lse, const int64_t* strides, const void* k_codes,
+                     const void* k_scales, const void* v_codes, const void* v_scales, int64_t num_pages,
+                     int64_t page_size, const int32_t* block_table, int64_t table_width, const int32_t* seq_lens,
+                     void* workspace, int64_t workspace_bytes, int64_t B, int64_t H, int64_t Hkv, int64_t Nq,
+                     int64_t D, float scale, int dtype, fattn_stream_t stream_h) {
+    DecodeArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.q = q;
+    a.o = o;
+    a.lse = lse;
+    a.k_pages = k_codes;
+    a.v_pages = v_codes;
+    a.k_scales = k_scales;
+    a.v_scales = v_scales;
+    a.block_table = block_table;
+    a.seq_lens = seq_lens;
+    a.workspace = workspace;
+    return run_decode(a, strides, num_pages, page_size, table_width, workspace_bytes, B, H, Hkv, Nq, D, scale,
+                      dtype, true, stream_h);
+}
+
 int fattn_get_device_status(fattn_stream_t stream_h) {
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_h);
     if (cudaStreamSynchronize(stream) != cudaSuccess) return FATTN_ERR_CUDA;
-    uint32_t word = 0, word_unfused = 0, word_bwd = 0;
+    uint32_t word = 0, word_unfused = 0, word_bwd = 0, word_append = 0, word_decode = 0;
     if (read_and_clear_error_word(&word) != cudaSuccess ||
         unfused_read_and_clear_error_word(&word_unfused) != cudaSuccess ||
-        bwd_read_and_clear_error_word(&word_bwd) != cudaSuccess)
+        bwd_read_and_clear_error_word(&word_bwd) != cudaSuccess ||
+        append_read_and_clear_error_word(&word_append) != cudaSuccess ||
+        decode_read_and_clear_error_word(&word_decode) != cudaSuccess)
         return FATTN_ERR_CUDA;
-    word |= word_unfused | word_bwd;
+    word |= word_unfused | word_bwd | word_append | word_decode;
     if (word & (1u << FATTN_ERR_INTERNAL)) return FATTN_ERR_INTERNAL;
     if (word & (1u << FATTN_ERR_TIMEOUT)) return FATTN_ERR_TIMEOUT;
+    if (word & (1u << FATTN_ERR_INVALID_ARG)) return FATTN_ERR_INVALID_ARG;
     return FATTN_OK;
 }
 

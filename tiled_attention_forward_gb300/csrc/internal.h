@@ -130,6 +130,68 @@ cudaError_t bwd_launch(const BwdArgs& a, const void* o, const void* dout, const 
                        bool bf16, bool causal, cudaStream_t s);
 cudaError_t bwd_read_and_clear_error_word(uint32_t* out);
 
+// ---- paged cache: append (cache_append.cu) and attention (decode.cu) --------
+constexpr uint32_t kDevErrInvalidArg = 1u;  // error-word bit: an index in device memory is out of range
+constexpr int kKv4Group = 32;               // elements of a 4-bit row that share one scale and zero
+
+struct AppendArgs {
+    const void* q;        // [T][H][D] by strides, or nullptr
+    const void* k;        // [T][Hkv][D] by strides
+    const void* v;
+    void* q_out;          // or nullptr
+    void* k_out;
+    void* v_out;
+    int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs;        // token and head strides, elements
+    int64_t qo_ts, qo_hs, ko_ts, ko_hs, vo_ts, vo_hs;
+    void* k_pages;        // 16-bit [pages][Hkv][page_size][D], or codes [pages][Hkv][page_size][D/2] bytes
+    void* v_pages;
+    void* k_scales;       // 4-bit: fp16 [pages][Hkv][page_size][D/32][2]
+    void* v_scales;
+    int64_t page_stride;  // 16-bit: elements from one page to the next
+    const int64_t* slots; // [T]
+    const int32_t* pos;   // [T]
+    const float* cos;     // [max_pos][rot/2]
+    const float* sin;
+    int64_t T;
+    int64_t num_slots;    // num_pages * page_size
+    int64_t max_pos;
+    int page_size;
+    int H;                // 0 when q is nullptr
+    int Hkv;
+    int rot;
+    int interleaved;
+    int held;             // 4-bit: k_out / v_out receive the values that the cache stands for
+    int lanes_per_token;  // set by append_launch
+};
+cudaError_t append_launch(AppendArgs a, int D, bool bf16, bool kv4, cudaStream_t s);
+cudaError_t append_read_and_clear_error_word(uint32_t* out);
+
+struct DecodeArgs {
+    const void* q;        // [B][H][Nq][D] by strides
+    void* o;
+    float* lse;           // [B][H][Nq] or nullptr
+    int64_t q_bs, q_hs, q_ns, o_bs, o_hs, o_ns;  // element strides
+    const void* k_pages;  // as AppendArgs
+    const void* v_pages;
+    const void* k_scales;
+    const void* v_scales;
+    int64_t page_stride;
+    const int32_t* block_table;  // [B][table_width]
+    const int32_t* seq_lens;     // [B]
+    void* workspace;
+    int64_t num_pages;
+    int64_t table_width;
+    int page_size;
+    int B;
+    int H;
+    int Hkv;
+    int Nq;
+    float scale_log2;
+};
+cudaError_t decode_launch(const DecodeArgs& a, int D, bool bf16, bool kv4, int sms, cudaStream_t s);
+int64_t decode_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t D);
+cudaError_t decode_read_and_clear_error_word(uint32_t* out);
+
 // Key/value head read by query head bh = b*H + h: b*Hkv + h / (H/Hkv).
 __host__ __device__ __forceinline__ int kv_head_of(int bh, int H, int Hkv) {
     return (bh / H) * Hkv + (bh % H) / (H / Hkv);
