@@ -78,7 +78,7 @@ BWD_FLOP_FACTOR = 2.5
 # profiles/), tagged with the hash of that kernel's device sources when it
 # was taken.  Reported only while those sources still hash the same; null
 # once the kernel has changed.
-KERNEL_SOURCES = {"tc": ["fwd_tc.cu", "sm103_ptx.cuh"], "ffma": ["fwd_ffma.cu"],
+KERNEL_SOURCES = {"tc": ["fwd_tc.cu", "fwd_tc_kernel.cuh", "sm103_ptx.cuh"], "ffma": ["fwd_ffma.cu"],
                   "unfused": ["fwd_unfused.cu", "sm103_ptx.cuh"],
                   "bwd": ["bwd_tc.cu", "sm103_ptx.cuh"]}
 NCU_TRAFFIC = {

@@ -324,6 +324,40 @@ FATTN_API int fattn_fwd_unfused_static(const void* q, const void* k, const void*
  */
 
 /*
+ * fattn_packed_workspace_bytes -- bytes of device workspace fattn_fwd_packed
+ * needs for B sequences of T tokens in all (the list of Q blocks): 16 * (1 +
+ * T/256 + B).  0 for an empty or invalid size.
+ */
+FATTN_API int64_t fattn_packed_workspace_bytes(int64_t B, int64_t T);
+
+/*
+ * fattn_fwd_packed -- fattn_fwd_gqa on B sequences of different lengths packed
+ * one after the other: sequence b is tokens cu_seqlens[b] .. cu_seqlens[b+1]-1
+ * of q, o [T, H, D] and k, v [T, Hkv, D]; each attends to itself alone, causal
+ * (key j visible to row i of the same sequence iff j <= i) or in full.
+ *
+ *   q, k, v, o : `strides` is a host array of 8: token and head stride of q, k,
+ *                v, o.  A stride of a dimension of more than one is positive.
+ *                o overlaps nothing else.
+ *   lse        : fp32 [H, T], or NULL.
+ *   cu_seqlens : device int32 [B + 1], not decreasing, 0 <= cu_seqlens[0],
+ *                cu_seqlens[B] <= T; sequences may be empty.  Rows that belong
+ *                to no sequence are left as they were, and what q, k and v hold
+ *                there is never used.  A table that breaks these rules makes
+ *                the call do nothing but report it (fattn_get_device_status).
+ *   workspace  : caller-owned, fattn_packed_workspace_bytes, 16-byte aligned;
+ *                contents ignored on entry.  Calls that run at the same time
+ *                need workspaces of their own.
+ * Within a sequence, a NaN or infinity in a V row also reaches earlier rows of
+ * the same 256-row block (their weight 0 times it), as in fattn_fwd; it never
+ * reaches another sequence.  Two launches (the list of Q blocks, the forward).
+ */
+FATTN_API int fattn_fwd_packed(const void* q, const void* k, const void* v, void* o, float* lse,
+                     const int64_t* strides, const int32_t* cu_seqlens, void* workspace,
+                     int64_t workspace_bytes, int64_t B, int64_t T, int64_t H, int64_t Hkv,
+                     int64_t D, float scale, int causal, int dtype, fattn_stream_t stream);
+
+/*
  * fattn_cache_append -- rows k and v of T new tokens into a 16-bit paged
  * cache, rotating k (and q) by position on the way.
  *

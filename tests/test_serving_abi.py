@@ -185,3 +185,59 @@ def test_header_documents_the_entry_points():
         assert "FATTN_API" in text and name in text
     assert "32 i + 8 t + e at nibble 8 (t D/32 + i) + e/2 + 4 (e mod 2)" in text
     assert "16 j + 8 u + g at nibble (D/8) g + (D/16) u + j" in text
+
+
+def call_packed(q=A, k=2 * A, v=3 * A, o=4 * A, lse=5 * A, strides=None, cu=6 * A, ws=7 * A, wsb=None, B=3, T=100, H=4,
+                Hkv=2, D=64, scale=0.125, causal=1, dtype=2):
+    lib = fattn.load()
+    st = i64s(*(strides or [H * D, D, Hkv * D, D, Hkv * D, D, H * D, D]))
+    wsb = lib.fattn_packed_workspace_bytes(B, T) if wsb is None else wsb
+    return lib.fattn_fwd_packed(q, k, v, o, lse, st, cu, ws, wsb, B, T, H, Hkv, D, scale, causal, dtype, None)
+
+
+def test_packed_refusals():
+    call = call_packed
+    assert call(dtype=0) == UNSUPPORTED and call(dtype=3) == INVALID and call(D=32) == UNSUPPORTED
+    assert call(B=-1) == INVALID and call(T=-1) == INVALID and call(Hkv=3) == INVALID and call(Hkv=0) == INVALID
+    assert call(scale=float("inf")) == INVALID and call(scale=-0.5) == INVALID
+    assert call(B=0) == OK and call(T=0) == OK and call(H=0) == OK
+    for name in ("q", "k", "v", "o", "cu", "ws"):
+        assert call(**{name: None}) == INVALID, name
+    assert call(wsb=fattn.packed_workspace_bytes(3, 100) - 1) == INVALID
+    for name, at in (("q", A), ("k", 2 * A), ("v", 3 * A), ("o", 4 * A), ("ws", 7 * A)):
+        assert call(**{name: at + 8}) == MISALIGNED, name
+    assert call(lse=5 * A + 2) == MISALIGNED and call(cu=6 * A + 1) == MISALIGNED
+    base = [256, 64, 128, 64, 128, 64, 256, 64]
+    for i in range(8):
+        for bad in (-64, 4, 0):
+            assert call(strides=base[:i] + [bad] + base[i + 1:]) == INVALID, i
+    assert call(strides=base[:6] + [128, 64]) == INVALID   # o's rows run into one another
+    assert call(strides=[1 << 39] + base[1:]) == UNSUPPORTED
+    assert call(o=A) == INVALID and call(o=3 * A + 128) == INVALID and call(lse=4 * A) == INVALID
+    assert call(ws=6 * A) == INVALID and call(ws=2 * A) == INVALID and call(lse=7 * A) == INVALID
+    far = dict(q=1 << 45, k=1 << 46, v=1 << 47, o=1 << 48, lse=1 << 49, cu=1 << 50, ws=1 << 51)
+    assert call(T=1 << 30, H=1 << 9, **far) == UNSUPPORTED  # more than 2^30 tasks
+    assert call(T=(1 << 30) + 1, **far) == UNSUPPORTED
+
+
+def test_packed_workspace_bytes():
+    ws = fattn.load().fattn_packed_workspace_bytes
+    for B, T in ((1, 1), (3, 255), (64, 16384), (1, 256)):
+        assert ws(B, T) == 16 * (1 + T // 256 + B)
+        # one list entry per Q block, however the tokens are dealt out
+        assert T // 256 + B >= sum(-(-n // 256) for n in [T - (B - 1)] + [1] * (B - 1) if n > 0)
+    for bad in ((0, 1), (1, 0), (-1, 5), (1 << 31, 1), (1, 1 << 31)):
+        assert ws(*bad) == 0
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-GPU path")
+def test_packed_accepts():
+    call = call_packed
+    assert call() == NO_DEVICE and call(lse=None) == NO_DEVICE
+    # slices of one projection; head-major; a single token or head with any stride
+    assert call(k=A + 512, v=A + 768, strides=[512, 64] * 3 + [256, 64]) == NO_DEVICE
+    assert call(strides=[64, 6400] * 4) == NO_DEVICE
+    assert call(T=1, H=1, Hkv=1, strides=[0] * 8) == NO_DEVICE
+    # o in a slice of the tensor that q, k and v are slices of, beside them
+    assert call(k=A + 512, v=A + 768, o=A + 1024, strides=[768, 64] * 4) == NO_DEVICE
+    assert call(k=A + 512, v=A + 768, o=A + 1008, strides=[768, 64] * 4) == INVALID

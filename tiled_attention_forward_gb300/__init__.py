@@ -22,7 +22,7 @@ __all__ = ["fwd", "fwd_host", "bwd", "bwd_host", "bwd_workspace_bytes", "fwd_unf
            "UNFUSED_STATIC_BYTES", "plan", "get_device_status", "selftest_wait_timeout",
            "status_string", "library_path", "load", "FattnError", "FattnLibraryMissing",
            "DTYPE_CODES", "STATUS", "cache_append", "cache_append_kv4", "decode", "decode_kv4",
-           "decode_workspace_bytes", "KV4_GROUP"]
+           "decode_workspace_bytes", "KV4_GROUP", "fwd_packed", "packed_workspace_bytes"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libfattn.so")
@@ -84,6 +84,9 @@ def load():
     lib.fattn_unfused_workspace_bytes.restype = i64
     lib.fattn_plan.argtypes = [i64, i64, i64, i64, ci, ci, ci, ctypes.POINTER(i64)]
     lib.fattn_plan_head_group.argtypes = [i64, i64, i64, i64, i64, ctypes.POINTER(i64)]
+    lib.fattn_packed_workspace_bytes.argtypes = [i64, i64]
+    lib.fattn_packed_workspace_bytes.restype = i64
+    lib.fattn_fwd_packed.argtypes = [vp] * 8 + [i64] * 6 + [f32, ci, ci, vp]
     lib.fattn_cache_append.argtypes = [vp] * 8 + [i64] * 3 + [vp] * 4 + [i64] * 2 + [ci] + [i64] * 4 + [ci, vp]
     lib.fattn_cache_append_kv4.argtypes = ([vp] * 11 + [i64] * 2 + [vp] * 4 + [i64] * 2 + [ci] * 2 + [i64] * 4 +
                                            [ci, vp])
@@ -98,7 +101,7 @@ def load():
     lib.fattn_version.argtypes = []
     for f in ("fattn_fwd", "fattn_fwd_gqa", "fattn_fwd_host", "fattn_fwd_unfused", "fattn_bwd", "fattn_bwd_gqa", "fattn_bwd_host",
               "fattn_fwd_unfused_static", "fattn_plan", "fattn_plan_head_group",
-              "fattn_cache_append", "fattn_cache_append_kv4", "fattn_decode", "fattn_decode_kv4",
+              "fattn_fwd_packed", "fattn_cache_append", "fattn_cache_append_kv4", "fattn_decode", "fattn_decode_kv4",
               "fattn_get_device_status",
               "fattn_selftest_wait_timeout", "fattn_version"):
         getattr(lib, f).restype = ci
@@ -398,6 +401,57 @@ def _call(device, stream, where, fn, *args):
     else:
         with torch.cuda.device(device):
             _check(fn(*args, handle), where)
+
+
+def packed_workspace_bytes(B, T):
+    """Bytes of workspace ``fwd_packed`` needs for B sequences of T tokens in all."""
+    return int(load().fattn_packed_workspace_bytes(int(B), int(T)))
+
+
+def fwd_packed(q, k, v, cu_seqlens, causal=True, scale=None, out=None, lse=None, workspace=None, return_lse=True,
+               stream=None):
+    """Attention of sequences of different lengths packed one after the other.
+
+    q: [T, H, D]; k, v: [T, Hkv, D] with H a multiple of Hkv; float16 or
+    bfloat16 CUDA tensors, D in {64, 128}, any token and head strides (slices
+    of one projection), last dimension contiguous.  cu_seqlens: int32 [B + 1]
+    on the GPU; sequence b is tokens cu_seqlens[b] .. cu_seqlens[b+1] - 1 and
+    attends to itself alone.  Returns (o, lse): o [T, H, D], lse float32
+    [H, T] or None; rows of no sequence are left as they were in ``out`` and
+    ``lse`` (zero where those are allocated here).  ``workspace``: a CUDA uint8
+    tensor of at least ``packed_workspace_bytes(B, T)`` bytes (allocated here
+    when None); calls running at the same time need one each."""
+    if not q.is_cuda or q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q, k, v must be CUDA tensors [T, H, D] and [T, Hkv, D]")
+    T, H, D = q.shape
+    Hkv = k.shape[1]
+    dt = q.dtype
+    if dt not in DTYPE_CODES:
+        raise ValueError("dtype must be float16 or bfloat16")
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise ValueError("cu_seqlens must be [B + 1]")
+    B = cu_seqlens.shape[0] - 1
+    _table("cu_seqlens", cu_seqlens, (B + 1,), torch.int32)
+    if scale is None:
+        scale = _default_scale(D)
+    if out is None:
+        out = torch.zeros((T, H, D), dtype=dt, device=q.device)
+    if not return_lse:
+        lse = None
+    elif lse is None:
+        lse = torch.zeros((H, T), dtype=torch.float32, device=q.device)
+    else:
+        _table("lse", lse, (H, T), torch.float32)
+    st = (_rows("q", q, (T, H, D), dt) + _rows("k", k, (T, Hkv, D), dt) + _rows("v", v, (T, Hkv, D), dt) +
+          _rows("out", out, (T, H, D), dt))
+    if workspace is None:
+        workspace = torch.empty(max(packed_workspace_bytes(B, T), 16), dtype=torch.uint8, device=q.device)
+    _on(q.device, k, v, out, lse, cu_seqlens, workspace)
+    _call(q.device, stream, "fattn_fwd_packed", load().fattn_fwd_packed,
+          q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(lse), _STRIDES[8](*st),
+          cu_seqlens.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), B, T, H, Hkv, D,
+          float(scale), int(bool(causal)), DTYPE_CODES[dt])
+    return out, lse
 
 
 def _pages(k_pages, v_pages, Hkv, D, dtype):

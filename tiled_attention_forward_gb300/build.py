@@ -22,8 +22,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfattn.so")
 SOURCES = ["fattn_api.cu", "fwd_tc.cu", "fwd_ffma.cu", "fwd_unfused.cu", "bwd_tc.cu",
-           "cache_append.cu", "decode.cu"]
-HEADERS = ["internal.h", "sm103_ptx.cuh"]
+           "fwd_packed.cu", "cache_append.cu", "decode.cu"]
+HEADERS = ["internal.h", "sm103_ptx.cuh", "fwd_tc_kernel.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",

@@ -227,6 +227,23 @@ int causal_head_group(int64_t BH, int64_t H, int64_t Hkv, int64_t N, int64_t D) 
     return static_cast<int>(std::min<int64_t>(hg, BH));
 }
 
+// One 16-bit tensor of T x heads rows at strides (ts, hs), as the map of
+// tc_encode_maps with tokens in the place of rows.
+cudaError_t packed_encode_map(CUtensorMap* map, const void* p, int64_t T, int64_t ts, int64_t heads, int64_t hs,
+                              int64_t D, bool bf16) {
+    auto encode = get_encode_fn();
+    if (!encode) return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(T), static_cast<cuuint64_t>(heads)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ts * 2), static_cast<cuuint64_t>(hs * 2)};
+    const cuuint32_t box[3] = {64, 128, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                              const_cast<void*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 }  // namespace
 
 cudaError_t tc_encode_maps(TcArgs& a, const void* q, const void* k, const void* v, int64_t BH,
@@ -937,6 +954,87 @@ int fattn_cache_append_kv4(const void* q, const void* k, const void* v, void* q_
     return run_append(a, strides, num_pages, page_size, rot, T, H, Hkv, D, dtype, true, stream_h);
 }
 
+int64_t fattn_packed_workspace_bytes(int64_t B, int64_t T) {
+    if (B <= 0 || T <= 0 || B > (int64_t(1) << 30) || T > (int64_t(1) << 30)) return 0;
+    return 16 * (1 + T / (kTcBM * kTcQTiles) + B);
+}
+
+int fattn_fwd_packed(const void* q, const void* k, const void* v, void* o, float* lse, const int64_t* strides,
+                     const int32_t* cu_seqlens, void* workspace, int64_t workspace_bytes, int64_t B, int64_t T,
+                     int64_t H, int64_t Hkv, int64_t D, float scale, int causal, int dtype,
+                     fattn_stream_t stream_h) {
+    if (dtype != FATTN_F32 && dtype != FATTN_F16 && dtype != FATTN_BF16) return FATTN_ERR_INVALID_ARG;
+    if (B < 0 || T < 0 || H < 0 || D < 0 || !strides) return FATTN_ERR_INVALID_ARG;
+    if (H > 0 && (Hkv <= 0 || H % Hkv != 0)) return FATTN_ERR_INVALID_ARG;
+    if (!std::isfinite(scale) || scale < 0.f) return FATTN_ERR_INVALID_ARG;
+    if (dtype == FATTN_F32 || (D != 64 && D != 128)) return FATTN_ERR_UNSUPPORTED;
+    if (B == 0 || T == 0 || H == 0) return FATTN_OK;
+    const int64_t need = fattn_packed_workspace_bytes(B, T);
+    if (need <= 0 || H > (int64_t(1) << 16)) return FATTN_ERR_UNSUPPORTED;
+    // Task indices (Q blocks x heads) are ints in the kernel.
+    const int64_t capacity = T / (kTcBM * kTcQTiles) + B;
+    if (capacity * H > (int64_t(1) << 30)) return FATTN_ERR_UNSUPPORTED;
+    if (!q || !k || !v || !o || !cu_seqlens || !workspace || workspace_bytes < need) return FATTN_ERR_INVALID_ARG;
+    const void* ptrs[4] = {q, k, v, o};
+    const int64_t heads[4] = {H, Hkv, Hkv, H};
+    int64_t ts[4], hs[4];
+    View views[4];
+    for (int i = 0; i < 4; ++i) {
+        ts[i] = strides[2 * i];
+        hs[i] = strides[2 * i + 1];
+        if (!stride_ok(ts[i]) || !stride_ok(hs[i])) return FATTN_ERR_INVALID_ARG;
+        if ((T > 1 && ts[i] == 0) || (heads[i] > 1 && hs[i] == 0)) return FATTN_ERR_INVALID_ARG;
+        // A tensor map's strides are below 2^40 bytes.
+        if (ts[i] >= (int64_t(1) << 39) || hs[i] >= (int64_t(1) << 39) || ts[i] > kMaxElements / T ||
+            hs[i] > kMaxElements / heads[i])
+            return FATTN_ERR_UNSUPPORTED;
+        if (!aligned16(ptrs[i])) return FATTN_ERR_MISALIGNED;
+        if (T == 1) ts[i] = D;  // strides that are never stepped by
+        if (heads[i] == 1) hs[i] = D;
+        views[i] = rows_view(ptrs[i], T, ts[i], heads[i], hs[i], D);
+    }
+    if (!aligned16(workspace) || (reinterpret_cast<uintptr_t>(lse) & 3u) ||
+        (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u))
+        return FATTN_ERR_MISALIGNED;
+    // o's rows must not run into one another.
+    if ((T > 1 && ts[3] < D) || (H > 1 && hs[3] < D) || (T > 1 && H > 1 && views[3].inner > views[3].outer))
+        return FATTN_ERR_INVALID_ARG;
+    const View ins[4] = {views[0], views[1], views[2], dense_view(cu_seqlens, (B + 1) * 4)};
+    const View outs[3] = {views[3], dense_view(lse, H * T * 4), dense_view(workspace, need)};
+    for (int i = 0; i < 3; ++i) {
+        for (const View& x : ins)
+            if (views_overlap(outs[i], x)) return FATTN_ERR_INVALID_ARG;
+        for (int j = i + 1; j < 3; ++j)
+            if (views_overlap(outs[i], outs[j])) return FATTN_ERR_INVALID_ARG;
+    }
+    int sms = 0;
+    int st = current_sm_count(&sms);
+    if (st != FATTN_OK) return st;
+    PackedArgs a;
+    std::memset(static_cast<void*>(&a), 0, sizeof(a));
+    CUtensorMap* maps[3] = {&a.tmap_q, &a.tmap_k, &a.tmap_v};
+    for (int i = 0; i < 3; ++i)
+        if (packed_encode_map(maps[i], ptrs[i], T, ts[i], heads[i], hs[i], D, dtype == FATTN_BF16) != cudaSuccess)
+            return FATTN_ERR_CUDA;
+    a.o = o;
+    a.lse = lse;
+    a.H = static_cast<int>(H);
+    a.Hkv = static_cast<int>(Hkv);
+    a.BH = a.H;
+    a.head_group = causal_head_group(H, H, Hkv, T, D);  // as one sequence of all tokens
+    a.scale_log2 = scale * kLog2e;
+    a.timeout_ns = kDefaultTimeoutNs;
+    a.plan = static_cast<PackedPlan*>(workspace);
+    a.T = T;
+    a.o_ts = ts[3];
+    a.o_hs = hs[3];
+    const int grid = static_cast<int>(std::min<int64_t>(capacity * H, sms));
+    const cudaError_t e = packed_launch(a, cu_seqlens, static_cast<int>(B), static_cast<int>(D), dtype == FATTN_BF16,
+                                        causal != 0, static_cast<int>(capacity), grid,
+                                        reinterpret_cast<cudaStream_t>(stream_h));
+    return e == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
+}
+
 int64_t fattn_decode_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t D) {
     if (B <= 0 || H <= 0 || Hkv <= 0 || Nq <= 0 || H % Hkv != 0 || (D != 64 && D != 128)) return 0;
     const int64_t lim = int64_t(1) << 30;
@@ -988,14 +1086,15 @@ int fattn_decode_kv4(const void* q, void* o, float* lse, const int64_t* strides,
 int fattn_get_device_status(fattn_stream_t stream_h) {
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_h);
     if (cudaStreamSynchronize(stream) != cudaSuccess) return FATTN_ERR_CUDA;
-    uint32_t word = 0, word_unfused = 0, word_bwd = 0, word_append = 0, word_decode = 0;
+    uint32_t word = 0, word_unfused = 0, word_bwd = 0, word_append = 0, word_decode = 0, word_packed = 0;
     if (read_and_clear_error_word(&word) != cudaSuccess ||
         unfused_read_and_clear_error_word(&word_unfused) != cudaSuccess ||
         bwd_read_and_clear_error_word(&word_bwd) != cudaSuccess ||
         append_read_and_clear_error_word(&word_append) != cudaSuccess ||
-        decode_read_and_clear_error_word(&word_decode) != cudaSuccess)
+        decode_read_and_clear_error_word(&word_decode) != cudaSuccess ||
+        packed_read_and_clear_error_word(&word_packed) != cudaSuccess)
         return FATTN_ERR_CUDA;
-    word |= word_unfused | word_bwd | word_append | word_decode;
+    word |= word_unfused | word_bwd | word_append | word_decode | word_packed;
     if (word & (1u << FATTN_ERR_INTERNAL)) return FATTN_ERR_INTERNAL;
     if (word & (1u << FATTN_ERR_TIMEOUT)) return FATTN_ERR_TIMEOUT;
     if (word & (1u << FATTN_ERR_INVALID_ARG)) return FATTN_ERR_INVALID_ARG;

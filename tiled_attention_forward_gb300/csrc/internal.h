@@ -59,6 +59,22 @@ cudaError_t tc_encode_maps(TcArgs& a, const void* q, const void* k, const void* 
 cudaError_t tc_launch(const TcArgs& a, int D, bool bf16, bool causal, int grid,
                       cudaStream_t stream);
 
+// ---- packed sequences on the tensor-core path, fwd_packed.cu -------------------
+struct PackedPlan {  // in the caller's workspace
+    int blocks;
+    int pad[3];
+    int4 list[1];    // [blocks]: first token and length of the sequence, Q block within it
+};
+struct PackedArgs : TcArgs {  // tmaps {D, T, heads}; N, BH, num_qblk and num_tasks are unused
+    PackedPlan* plan;
+    int64_t T;
+    int64_t o_ts;        // token and head stride of o, elements
+    int64_t o_hs;
+};
+cudaError_t packed_launch(const PackedArgs& a, const int32_t* cu, int B, int D, bool bf16, bool causal, int capacity,
+                          int grid, cudaStream_t s);
+cudaError_t packed_read_and_clear_error_word(uint32_t* out);
+
 // ---- CUDA-core path (fp32), fwd_ffma.cu --------------------------------------
 constexpr int kFfmaBr = 128;      // Q rows per CTA
 int ffma_bc(int D);               // keys per K/V tile
