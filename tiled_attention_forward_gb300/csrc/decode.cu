@@ -1,9 +1,33 @@
 // decode.cu -- attention of the newest tokens of each sequence over a paged
 // cache held in 16 or in 4 bits.
 //
-// Simple form: a block per (sequence, query row), whose four warps take the
-// visible keys in turn, a lane per D/32 dims, each warp with its own running
-// max and sum (online softmax), joined in shared memory at the end.
+// One row of K and V is read per key, for all query rows that share the K/V
+// head (G = H/Hkv heads times Nq tokens): the call is bound by the cache's
+// bytes, so the kernel is built to keep them streaming.
+//
+// Products.  Both run transposed on mma.sync m16n8k16 (M = 16 keys or dims, N =
+// 8 query rows): S^T = K Q^T and O^T += V^T P^T.  Eight query rows fill N, so a
+// group of up to 8 wastes no tensor work and O needs only D/4 registers; NT =
+// 1, 2 or 4 tiles of 8 rows share one pass over the keys, and more rows than 32
+// take further passes.  (tcgen05 needs M >= 64 rows of S, 8 to 16 times what a
+// decode step has, and its operands in shared memory; the rate needed here,
+// two m16n8k16 per 16 keys and 16 dims, is a small part of mma.sync's.)
+//
+// Keys.  A unit of work is 128 keys of one (sequence, K/V head, row block):
+// the units of the whole call are numbered in that order, and CTA c of a fixed
+// grid takes an equal share [c U / G, (c+1) U / G), whatever the lengths: only
+// device memory knows them, each CTA forms the prefix sums itself.  Within a
+// unit a warp takes 16 keys, with a ring of stages of its own in shared memory
+// filled by cp.async (zero-filled behind the last key), so that warps never
+// wait for one another until their share of a sequence is done; then the CTA
+// joins its eight warps' (max, sum, O).  A sequence that lies in one CTA is
+// written out there; of the others each CTA writes its part to the workspace
+// and a second kernel joins them in a fixed order.  At most two parts per CTA
+// (its first and its last sequence) are ever cut.
+//
+// Softmax.  A lane keeps the reference max of its query rows; O and the sums
+// are rescaled only when a score passes it by more than 8 (log2), by a vote
+// that costs one instruction otherwise.  Sums stay in the lanes until the end.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -16,68 +40,723 @@ __device__ uint32_t g_decode_error_word;
 namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kKeys = 16;                 // keys of a warp's stage
+constexpr int kUnit = kWarps * kKeys;     // keys of a unit
+constexpr int kMaxCtas = 320;             // parts in the workspace: two per CTA
+constexpr float kRescaleThreshold = 8.0f; // log2 units: P <= 2^8 while the max is stale
 
+// ---- instructions ----------------------------------------------------------
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+// 16 bytes, of which the first `bytes` come from src and the rest are zero.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
 template <bool BF16>
-__device__ __forceinline__ float load16(const void* p, int64_t i) {
-    const uint16_t u = static_cast<const uint16_t*>(p)[i];
-    if (BF16) return __uint_as_float(static_cast<uint32_t>(u) << 16);
-    return __half2float(__ushort_as_half(u));
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if (BF16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+    if (BF16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
+__device__ __forceinline__ uint32_t as_u32(__half2 x) { return *reinterpret_cast<const uint32_t*>(&x); }
+
+// ---- a warp's stage in shared memory ----------------------------------------
+// 16 bits: K rows, then V rows, 16-byte chunk c of key r at chunk c ^ (r mod 8)
+// (ldmatrix reads 8 rows of one chunk without bank conflicts).
+// 4 bits: K codes (D/2 a key), K scales (D/8 a key), then V rows of codes and
+// scales, 16 bytes wider than the codes: lanes that take keys 2t of 8 bytes (4
+// at D = 64) then meet 32 different banks.
+template <int D, bool KV4>
+struct Stage {
+    static constexpr int kCode = D / 2, kMeta = D / kKv4Group * 4;
+    static constexpr int kVRow = KV4 ? kCode + 16 : 2 * D;
+    static constexpr int kKMetaOff = kKeys * kCode;
+    static constexpr int kVOff = KV4 ? kKMetaOff + kKeys * kMeta : kKeys * 2 * D;
+    static constexpr int kBytes = kVOff + kKeys * kVRow;
+};
+
+template <int D, bool KV4, int NT>
+struct Config {
+    static constexpr int kStages = KV4 ? 4 : 3;
+    static constexpr int kCtasPerSm = NT == 4 || (!KV4 && D == 128) ? 1 : 2;
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kRing = kWarps * kStages * Stage<D, KV4>::kBytes;
+    // The warps' O is joined in the same memory.
+    static constexpr int kJoin = kWarps * kRows * D * 4;
+    static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
+    static_assert(kSmem * kCtasPerSm <= 224 * 1024, "shared memory budget");
+};
+
+// A part of a cut sequence: per row the max (log2 units), the sum, then O.
+template <int D>
+__device__ __forceinline__ float* part_of(void* ws, int slot, int rows) {
+    return static_cast<float*>(ws) + 4 * kMaxCtas + static_cast<int64_t>(slot) * rows * (D + 2);
+}
+// Per CTA, what the joining kernel needs to know: {sequence, head and row
+// block, parts, first part's slot} of the cut sequence that starts in it.
+__device__ __forceinline__ int4* cuts_of(void* ws) { return static_cast<int4*>(ws); }
+
+// The share of CTA c.
+__device__ __forceinline__ int64_t share_begin(int64_t units, int c, int ctas) { return units * c / ctas; }
+
+__device__ __forceinline__ int visible_len(const DecodeArgs& a, int b, bool report) {
+    const int64_t most = a.table_width * a.page_size;
+    const int len = a.seq_lens[b];
+    if (len < 0 || len > most) {
+        if (report) atomicOr(&g_decode_error_word, 1u << kDevErrInvalidArg);
+        return len < 0 ? 0 : static_cast<int>(most);
+    }
+    return len;
+}
+__device__ __forceinline__ int units_of(int len) { return max(1, (len + kUnit - 1) / kUnit); }
+
+template <int D, bool BF16>
+__device__ __forceinline__ void store_row4(const DecodeArgs& a, int b, int h, int i, int d, const float (&x)[4]) {
+    uint16_t* o = static_cast<uint16_t*>(a.o) + b * a.o_bs + h * a.o_hs + i * a.o_ns + d;
+    *reinterpret_cast<uint2*>(o) = make_uint2(pack16<BF16>(x[0], x[1]), pack16<BF16>(x[2], x[3]));
 }
 
-template <int D, bool BF16, bool KV4>
-__global__ void __launch_bounds__(128) decode_kernel(const __grid_constant__ DecodeArgs a) {
-    constexpr int E = D / 32;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int h = blockIdx.x / a.Nq, i = blockIdx.x % a.Nq, b = blockIdx.y;
-    const int kvh = h / (a.H / a.Hkv);
-    int64_t len = a.seq_lens[b];
-    if (len < 0 || len > a.table_width * a.page_size) {
-        if (threadIdx.x == 0) atomicOr(&g_decode_error_word, 1u << kDevErrInvalidArg);
-        len = len < 0 ? 0 : a.table_width * a.page_size;
-    }
-    const int64_t end = len - a.Nq + i + 1;
-    float q[E], o[E], m = -INFINITY, l = 0.f;
+// ---- one warp's keys ----------------------------------------------------------
+template <int D, bool BF16, bool KV4, int NT>
+struct Warp {
+    using S = Stage<D, KV4>;
+    static constexpr int kQ = D / 16;   // k-steps of S^T, m-tiles of O^T
+    uint32_t q[NT][kQ][2];              // B fragments of Q^T
+    uint32_t qsum[NT];                  // 4 bits: (high, low) part of the sum of q over group t
+    float f[NT][2];                     // log2-score of one unit of S, rows 2t and 2t+1
+    float m[NT][2], l[NT][2];
+    float o[NT][kQ][4];
+
+    // Query rows of K/V head kvh, row block rb.  Lane (g, t) = (lane/4, lane%4).
+    __device__ __forceinline__ void load_q(const DecodeArgs& a, int b, int kvh, int rb) {
+        const int lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+        const int rows = (a.H / a.Hkv) * a.Nq;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        q[e] = load16<BF16>(a.q, b * a.q_bs + h * a.q_hs + i * a.q_ns + lane * E + e) * a.scale_log2;
-        o[e] = 0.f;
-    }
-    for (int64_t j = warp; j < end; j += 4) {
-        const int64_t page = a.block_table[b * a.table_width + j / a.page_size];
-        if (page < 0 || page >= a.num_pages) {
-            if (lane == 0) atomicOr(&g_decode_error_word, 1u << kDevErrInvalidArg);
-            continue;
-        }
-        const int64_t in_page = static_cast<int64_t>(kvh) * a.page_size + j % a.page_size;
-        float k[E], v[E];
+        for (int n = 0; n < NT; ++n) {
+            const int r = rb * 8 * NT + n * 8 + g;
+            const uint16_t* src = nullptr;
+            if (r < rows)
+                src = static_cast<const uint16_t*>(a.q) + b * a.q_bs +
+                      static_cast<int64_t>(kvh * (a.H / a.Hkv) + r / a.Nq) * a.q_hs + (r % a.Nq) * a.q_ns;
+            if constexpr (!KV4) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int d = lane * E + e;
-            if (KV4) {
-                const int64_t row = page * a.Hkv * a.page_size + in_page;
-                const int nk = 8 * ((d % 32) / 8 * (D / 32) + d / 32) + (d % 8) / 2 + 4 * (d % 2);
-                const int nv = (d % 8) * (D / 8) + (d % 16) / 8 * (D / 16) + d / 16;
-                const int ck = (static_cast<const uint8_t*>(a.k_pages)[row * (D / 2) + nk / 2] >> (4 * (nk % 2))) & 15;
-                const int cv = (static_cast<const uint8_t*>(a.v_pages)[row * (D / 2) + nv / 2] >> (4 * (nv % 2))) & 15;
-                const float2 sk = __half22float2(static_cast<const __half2*>(a.k_scales)[row * (D / 32) + d / 32]);
-                const float2 sv = __half22float2(static_cast<const __half2*>(a.v_scales)[row * (D / 32) + d / 32]);
-                k[e] = fmaf(static_cast<float>(ck), sk.x, sk.y);
-                v[e] = fmaf(static_cast<float>(cv), sv.x, sv.y);
+                for (int kk = 0; kk < kQ; ++kk) {
+                    q[n][kk][0] = src ? *reinterpret_cast<const uint32_t*>(src + 16 * kk + 2 * t) : 0u;
+                    q[n][kk][1] = src ? *reinterpret_cast<const uint32_t*>(src + 16 * kk + 8 + 2 * t) : 0u;
+                }
+                f[n][0] = f[n][1] = a.scale_log2;
+                qsum[n] = 0u;
             } else {
-                k[e] = load16<BF16>(a.k_pages, page * a.page_stride + in_page * D + d);
-                v[e] = load16<BF16>(a.v_pages, page * a.page_stride + in_page * D + d);
+                // q as fp16 whatever its type: scaled by a power of two so that
+                // the row's largest element lies in [2^9, 2^10), which keeps
+                // every element within 2^-20 of it exact, and sums of 32 below
+                // fp16's largest.
+                float x[D / 32][8];
+                float big = 0.f;
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+                    if (src) raw = *reinterpret_cast<const uint4*>(src + 32 * i + 8 * t);
+                    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        if (BF16) {
+                            x[i][2 * p] = __uint_as_float(w[p] << 16);
+                            x[i][2 * p + 1] = __uint_as_float(w[p] & 0xffff0000u);
+                        } else {
+                            const float2 v = __half22float2(as_half2(w[p]));
+                            x[i][2 * p] = v.x;
+                            x[i][2 * p + 1] = v.y;
+                        }
+                        big = fmaxf(big, fmaxf(fabsf(x[i][2 * p]), fabsf(x[i][2 * p + 1])));
+                    }
+                }
+                big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+                big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+                const int e = max(static_cast<int>((__float_as_uint(big) >> 23) & 255u) - 127, -100);
+                const float up = __uint_as_float(static_cast<uint32_t>(127 + 9 - e) << 23);
+                float mine = 0.f;
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    float sum = 0.f;
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        // pairs 1 and 3 meet codes that sit 4 bits higher
+                        const float k = (p & 1) ? up * 0.0625f : up;
+                        q[n][2 * i + p / 2][p & 1] = pack16<false>(x[i][2 * p] * k, x[i][2 * p + 1] * k);
+                        sum += x[i][2 * p] * up + x[i][2 * p + 1] * up;
+                    }
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                    if (i == t) mine = sum;
+                }
+                const float hi = __half2float(__float2half_rn(mine));
+                qsum[n] = pack16<false>(hi, mine - hi);
+                const float down = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - 9 + e) << 23);
+                f[n][0] = __shfl_sync(0xffffffffu, down, 8 * t);
+                f[n][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
+            }
+            m[n][0] = m[n][1] = -INFINITY;
+            l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+            for (int j = 0; j < kQ; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.f;
+        }
+    }
+
+    // Starts the copies of 16 keys from place `off` of `page` (`valid` of them
+    // are keys of the sequence; the rest of the stage becomes zero).
+    __device__ __forceinline__ void fetch(const DecodeArgs& a, uint32_t stage, int64_t page, int kvh, int off, int valid) {
+        const int lane = threadIdx.x % 32;
+        if constexpr (!KV4) {
+            constexpr int kChunks = D / 8, kRowsAtOnce = 32 / kChunks;
+            const int64_t at = page * a.page_stride + (static_cast<int64_t>(kvh) * a.page_size + off) * D;
+            const int c = lane % kChunks;
+            const uint16_t* k = static_cast<const uint16_t*>(a.k_pages) + at + 8 * lane;
+            const uint16_t* v = static_cast<const uint16_t*>(a.v_pages) + at + 8 * lane;
+#pragma unroll
+            for (int i = 0; i < kKeys / kRowsAtOnce; ++i) {
+                const int r = i * kRowsAtOnce + lane / kChunks;
+                const uint32_t dst = stage + r * 2 * D + ((c ^ (r & 7)) << 4);
+                const int bytes = r < valid ? 16 : 0;
+                cp_async16(dst, k + i * 256, bytes);
+                cp_async16(dst + S::kVOff, v + i * 256, bytes);
+            }
+        } else {
+            constexpr int kChunks = D / 32;  // 16-byte chunks of a row of codes
+            const int64_t row = (page * a.Hkv + kvh) * a.page_size + off;
+            const uint8_t* k = static_cast<const uint8_t*>(a.k_pages) + row * S::kCode;
+            const uint8_t* v = static_cast<const uint8_t*>(a.v_pages) + row * S::kCode;
+#pragma unroll
+            for (int i = 0; i < kKeys * kChunks / 32; ++i) {
+                const int x = i * 32 + lane, r = x / kChunks, c = x % kChunks;
+                const int bytes = r < valid ? 16 : 0;
+                cp_async16(stage + x * 16, k + x * 16, bytes);
+                cp_async16(stage + S::kVOff + r * S::kVRow + c * 16, v + x * 16, bytes);
+            }
+            const int r = lane % 16;
+            const bool is_k = lane < 16;
+            const uint8_t* sc = static_cast<const uint8_t*>(is_k ? a.k_scales : a.v_scales) + (row + r) * S::kMeta;
+            const uint32_t dst = is_k ? stage + S::kKMetaOff + r * S::kMeta : stage + S::kVOff + r * S::kVRow + S::kCode;
+            cp_async_small<S::kMeta>(dst, sc, r < valid ? S::kMeta : 0);
+        }
+    }
+
+    // S^T of the stage's 16 keys, in log2 units: s[n][0..1] key g, s[n][2..3] key
+    // g + 8, rows 2t and 2t+1.
+    __device__ __forceinline__ void scores(uint32_t stage, float (&s)[NT][4]) const {
+        const int lane = threadIdx.x % 32;
+        if constexpr (!KV4) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+            const int r = (lane & 7) + (lane & 8);
+#pragma unroll
+            for (int kk = 0; kk < kQ; ++kk) {
+                uint32_t k[4];
+                ldmatrix4(k, stage + r * 2 * D + (((2 * kk + lane / 16) ^ (r & 7)) << 4));
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma16816<BF16>(s[n], k, q[n][kk][0], q[n][kk][1]);
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                s[n][0] *= f[n][0];
+                s[n][1] *= f[n][1];
+                s[n][2] *= f[n][0];
+                s[n][3] *= f[n][1];
+            }
+        } else {
+            // sum_d q_d (c_d scale + zero) = sum over groups of scale (sum q c) +
+            // zero (sum q): the codes enter as fp16 subnormals, c 2^-24 (or 16
+            // times that), which the tensor cores multiply exactly, the scales
+            // in fp32, and the zeros as one more product, (zero, zero) with
+            // (high, low) part of the sum of q, group t in lane t.
+            const int g = lane / 4, t = lane % 4;
+            uint32_t w[2][D / 32], meta[2][D / 32];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const uint32_t at = stage + (g + 8 * u) * S::kCode + t * (D / 8);
+                const uint32_t mt = stage + S::kKMetaOff + (g + 8 * u) * S::kMeta;
+                lds_words(w[u], at);
+                lds_words(meta[u], mt);
+            }
+            uint32_t z[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                uint32_t mine = 0u;
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i)
+                    if (i == t) mine = meta[u][i];
+                z[u] = __byte_perm(mine, 0u, 0x3232);
+            }
+            float zs[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                zs[n][0] = zs[n][1] = zs[n][2] = zs[n][3] = 0.f;
+                mma16816<false>(zs[n], z, qsum[n], 0u);
+                s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                uint32_t a0[4], a1[4];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const uint32_t hi = w[u][i] >> 8;
+                    a0[u] = w[u][i] & 0x000f000fu;
+                    a0[u + 2] = w[u][i] & 0x00f000f0u;
+                    a1[u] = hi & 0x000f000fu;
+                    a1[u + 2] = hi & 0x00f000f0u;
+                }
+                const float sc0 = __low2float(as_half2(meta[0][i])), sc1 = __low2float(as_half2(meta[1][i]));
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float c[4] = {0.f, 0.f, 0.f, 0.f};
+                    mma16816<false>(c, a0, q[n][2 * i][0], q[n][2 * i][1]);
+                    mma16816<false>(c, a1, q[n][2 * i + 1][0], q[n][2 * i + 1][1]);
+                    s[n][0] = fmaf(c[0], sc0, s[n][0]);
+                    s[n][1] = fmaf(c[1], sc0, s[n][1]);
+                    s[n][2] = fmaf(c[2], sc1, s[n][2]);
+                    s[n][3] = fmaf(c[3], sc1, s[n][3]);
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) s[n][x] = fmaf(s[n][x], 16777216.f, zs[n][x]) * f[n][x & 1];
+        }
+    }
+
+    template <int N>
+    static __device__ __forceinline__ void lds_words(uint32_t (&w)[N], uint32_t addr) {
+        if constexpr (N == 4)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(addr)
+                         : "memory");
+        else
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
+    }
+    static __device__ __forceinline__ uint32_t lds_word(uint32_t addr) {
+        uint32_t w;
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(addr) : "memory");
+        return w;
+    }
+
+    // O^T += V^T P^T; p[n][u]: B fragments (keys 2t, 2t+1 and 8 further, row g).
+    __device__ __forceinline__ void accumulate(uint32_t stage, const uint32_t (&p)[NT][2]) {
+        const int lane = threadIdx.x % 32;
+        const uint32_t base = stage + S::kVOff;
+        if constexpr (!KV4) {
+            const int r = (lane & 7) + ((lane & 16) >> 1);
+#pragma unroll
+            for (int j = 0; j < kQ; ++j) {
+                uint32_t v[4];
+                ldmatrix4_trans(v, base + r * 2 * D + (((2 * j + ((lane >> 3) & 1)) ^ (r & 7)) << 4));
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma16816<BF16>(o[n][j], v, p[n][0], p[n][1]);
+            }
+        } else {
+            // Lane (g, t) takes keys 2t, 2t+1, 2t+8, 2t+9, dims 16 j + 8 u + g.  Two
+            // keys' 16-bit halves side by side are 4 pairs of codes, each made
+            // fp16 by setting exponent bits (1024 + c, or 64 + c where the code
+            // sits 4 bits higher), taking that off again (exact), and one fused
+            // c scale + zero.
+            const int g = lane / 4, t = lane % 4;
+            constexpr int kHalves = D / 32;                      // 16-bit pieces of a key that this lane takes
+            uint32_t x[2][kHalves];                              // [key pair][piece]
+            uint32_t sc[2][D / 32], ze[2][D / 32];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const uint32_t k0 = base + (2 * t + 8 * u) * S::kVRow, k1 = k0 + S::kVRow;
+                if constexpr (D == 128) {
+                    uint32_t w0[2], w1[2];
+                    lds_words(w0, k0 + 8 * g);
+                    lds_words(w1, k1 + 8 * g);
+                    x[u][0] = __byte_perm(w0[0], w1[0], 0x5410);  // u-half 0: j = 0..3
+                    x[u][1] = __byte_perm(w0[0], w1[0], 0x7632);  //           j = 4..7
+                    x[u][2] = __byte_perm(w0[1], w1[1], 0x5410);  // u-half 1: j = 0..3
+                    x[u][3] = __byte_perm(w0[1], w1[1], 0x7632);  //           j = 4..7
+                } else {
+                    const uint32_t w0 = lds_word(k0 + 4 * g), w1 = lds_word(k1 + 4 * g);
+                    x[u][0] = __byte_perm(w0, w1, 0x5410);        // half 0, j = 0..3
+                    x[u][1] = __byte_perm(w0, w1, 0x7632);        // half 1, j = 0..3
+                }
+                uint32_t m0[D / 32], m1[D / 32];
+                lds_words(m0, k0 + S::kCode);
+                lds_words(m1, k1 + S::kCode);
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    sc[u][i] = __byte_perm(m0[i], m1[i], 0x5410);
+                    ze[u][i] = __byte_perm(m0[i], m1[i], 0x7632);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kQ; ++j) {
+                uint32_t v[4];
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t piece = x[u][D == 128 ? 2 * h + j / 4 : h];
+                        const uint32_t part = (j & 2) ? piece >> 8 : piece;
+                        const uint32_t up = (j & 1) ? ((part & 0x00f000f0u) | 0x54005400u)
+                                                    : ((part & 0x000f000fu) | 0x64006400u);
+                        const __half2 c = __hsub2(as_half2(up), as_half2((j & 1) ? 0x54005400u : 0x64006400u));
+                        v[2 * u + h] = as_u32(__hfma2(c, as_half2(sc[u][j / 2]), as_half2(ze[u][j / 2])));
+                    }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma16816<false>(o[n][j], v, p[n][0], p[n][1]);
             }
         }
-        float s = 0.f;
+    }
+
+    // The stage's keys: `key` is the first one's index, ends[n][x] the number of
+    // keys that row 2t + x sees (tested when `masked`).
+    __device__ __forceinline__ void keys(uint32_t stage, int key, bool masked, const int (&ends)[NT][2]) {
+        const int lane = threadIdx.x % 32, g = lane / 4;
+        float s[NT][4];
+        scores(stage, s);
+        if (masked) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) s = fmaf(q[e], k[e], s);
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int x = 16; x > 0; x /= 2) s += __shfl_xor_sync(0xffffffffu, s, x);
-        const float mn = fmaxf(m, s);
-        const float alpha = m == -INFINITY ? 0.f : exp2f(m - mn), p = exp2f(s - mn);
-        l = l * alpha + p;
+                for (int x = 0; x < 4; ++x)
+                    if (key + g + (x & 2) * 4 >= ends[n][x & 1]) s[n][x] = -INFINITY;
+        }
+        bool grow = false;
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = o[e] * alpha + p * v[e];
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) grow |= fmaxf(s[n][x], s[n][x + 2]) > m[n][x] + kRescaleThreshold;
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    float mx = fmaxf(s[n][x], s[n][x + 2]);
+#pragma unroll
+                    for (int d = 4; d < 32; d *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                    const float mn = fmaxf(m[n][x], mx);
+                    const float alpha = mn == -INFINITY ? 1.f : ex2(m[n][x] - mn);
+                    m[n][x] = mn;
+                    l[n][x] *= alpha;
+#pragma unroll
+                    for (int j = 0; j < kQ; ++j) {
+                        o[n][j][x] *= alpha;
+                        o[n][j][x + 2] *= alpha;
+                    }
+                }
+        }
+        uint32_t p[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const float m0 = m[n][0] == -INFINITY ? 0.f : m[n][0], m1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+            const float p0 = ex2(s[n][0] - m0), p1 = ex2(s[n][1] - m1), p2 = ex2(s[n][2] - m0), p3 = ex2(s[n][3] - m1);
+            l[n][0] += p0 + p2;
+            l[n][1] += p1 + p3;
+            // P rounded to the operands' type (fp16 beside 4-bit values), key by row
+            // to row by key.
+            p[n][0] = movmatrix_trans(pack16<BF16 && !KV4>(p0, p1));
+            p[n][1] = movmatrix_trans(pack16<BF16 && !KV4>(p2, p3));
+        }
+        accumulate(stage, p);
+    }
+};
+
+template <int D, bool BF16, bool KV4, int NT>
+__global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
+    decode_kernel(const __grid_constant__ DecodeArgs a) {
+    using C = Config<D, KV4, NT>;
+    using S = Stage<D, KV4>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int64_t s_scan[kWarps];
+    __shared__ int64_t s_begin;   // units before the first sequence of this share
+    __shared__ int s_first;       // that sequence
+    __shared__ float s_m[kWarps][C::kRows], s_l[kWarps][C::kRows];
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int rows = (a.H / a.Hkv) * a.Nq;
+    const int row_blocks = (rows + C::kRows - 1) / C::kRows;
+    const int per_key = a.Hkv * row_blocks;  // targets of one sequence
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    // All units of the call, and this CTA's share of them.
+    int64_t mine = 0;
+    for (int b = tid; b < a.B; b += kThreads) mine += units_of(visible_len(a, b, blockIdx.x == 0));
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) mine += __shfl_xor_sync(0xffffffffu, mine, d);
+    if (lane == 0) s_scan[warp] = mine;
+    __syncthreads();
+    int64_t units = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) units += s_scan[w];
+    units *= per_key;
+    // CTAs that get a share: no more than units, so that the CTAs a sequence is
+    // cut between are neighbours.
+    const int ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), units)), cta = blockIdx.x;
+    if (cta >= ctas) {
+        if (tid == 0) cuts_of(a.workspace)[cta] = make_int4(0, 0, 0, 0);
+        return;
+    }
+    const int64_t begin = share_begin(units, cta, ctas), end = share_begin(units, cta + 1, ctas);
+    // The sequence of unit `begin`: prefix sums, kThreads sequences at a time.
+    int64_t before = 0;
+    for (int b0 = 0;; b0 += kThreads) {
+        __syncthreads();  // s_scan is read by all before it is written again
+        const int b = b0 + tid;
+        const int64_t own = b < a.B ? static_cast<int64_t>(units_of(visible_len(a, b, false))) * per_key : 0;
+        int64_t x = own;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+            if (lane >= d) x += y;
+        }
+        if (lane == 31) s_scan[warp] = x;
+        __syncthreads();
+        int64_t left = before, all = before;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) left += s_scan[w];
+            all += s_scan[w];
+        }
+        x += left;
+        if (own > 0 && begin >= x - own && begin < x) {
+            s_first = b;
+            s_begin = x - own;
+        }
+        before = all;
+        if (before > begin || b0 + kThreads >= a.B) break;
+    }
+    __syncthreads();
+
+    int b = s_first;
+    int64_t seq_at = s_begin;  // first unit of sequence b
+    int4 cut = make_int4(0, 0, 0, 0);
+    uint32_t ring = smem_addr(smem) + warp * C::kStages * S::kBytes;
+    const int page_shift = (a.page_size & (a.page_size - 1)) == 0 ? __ffs(a.page_size) - 1 : -1;
+    Warp<D, BF16, KV4, NT> w;
+    int64_t at = begin;
+    while (at < end) {
+        const int len = visible_len(a, b, false);
+        const int tiles = units_of(len);
+        const int64_t in_seq = at - seq_at;
+        const int target = static_cast<int>(in_seq / tiles);  // K/V head and row block
+        const int t0 = static_cast<int>(in_seq - static_cast<int64_t>(target) * tiles);
+        const int t1 = static_cast<int>(min(static_cast<int64_t>(tiles), t0 + (end - at)));
+        const int kvh = target / row_blocks, rb = target - kvh * row_blocks;
+        const int32_t* table = a.block_table + b * a.table_width;
+
+        w.load_q(a, b, kvh, rb);
+        int ends[NT][2];
+        const int min_end = len - a.Nq + 1;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int r = rb * C::kRows + n * 8 + (lane % 4) * 2 + x;
+                ends[n][x] = r < rows ? min_end + r % a.Nq : len;  // rows that are none: anything finite
+            }
+
+        // This warp's keys: 16 at first + 128 i.
+        const int first = t0 * kUnit + warp * kKeys;
+        const int last = min(len, t1 * kUnit);
+        const int turns = first < last ? (last - first + kUnit - 1) / kUnit : 0;
+        auto page_at = [&](int i) -> int {  // the page of turn i, -1 where there is none
+            const int key = first + i * kUnit;
+            if (i >= turns) return -1;
+            return table[page_shift >= 0 ? key >> page_shift : key / a.page_size];
+        };
+        uint32_t skip = 0u;  // bit s: stage s holds nothing
+        auto start = [&](int i, int page) {
+            if (i < turns) {
+                const int stage = i % C::kStages;
+                const int key = first + i * kUnit;
+                if (page < 0 || page >= a.num_pages) {
+                    if (lane == 0) atomicOr(&g_decode_error_word, 1u << kDevErrInvalidArg);
+                    skip |= 1u << stage;
+                } else {
+                    skip &= ~(1u << stage);
+                    const int off = page_shift >= 0 ? key & (a.page_size - 1) : key % a.page_size;
+                    w.fetch(a, ring + stage * S::kBytes, page, kvh, off, len - key);
+                }
+            }
+            cp_async_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < C::kStages - 1; ++i) start(i, page_at(i));
+        int page = page_at(C::kStages - 1);
+        for (int i = 0; i < turns; ++i) {
+            start(i + C::kStages - 1, page);
+            page = page_at(i + C::kStages);  // needed one turn later
+            cp_async_wait<C::kStages - 1>();
+            __syncwarp();
+            const int stage = i % C::kStages;
+            const int key = first + i * kUnit;
+            if (!((skip >> stage) & 1u)) w.keys(ring + stage * S::kBytes, key, key + kKeys > min_end, ends);
+            __syncwarp();  // every lane is done with the stage before it is filled again
+        }
+        cp_async_wait<0>();
+
+        // Join the eight warps: their O by rows, in the ring's memory.
+        __syncthreads();
+        float* so = reinterpret_cast<float*>(smem) + warp * C::kRows * D;
+        {
+            const int g = lane / 4, t = lane % 4;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    float l = w.l[n][x];
+#pragma unroll
+                    for (int d = 4; d < 32; d *= 2) l += __shfl_xor_sync(0xffffffffu, l, d);
+                    const int r = n * 8 + 2 * t + x;
+                    if (g == 0) {
+                        s_m[warp][r] = w.m[n][x];
+                        s_l[warp][r] = l;
+                    }
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j) {
+                        so[r * D + 16 * j + g] = w.o[n][j][x];
+                        so[r * D + 16 * j + 8 + g] = w.o[n][j][x + 2];
+                    }
+                }
+        }
+        __syncthreads();
+        const bool whole = t0 == 0 && t1 == tiles;
+        const int slot = 2 * cta + (at == begin ? 0 : 1);
+        float* part = part_of<D>(a.workspace, slot, C::kRows);
+        for (int x = tid; x < C::kRows * D / 4; x += kThreads) {
+            const int r = x / (D / 4), d = 4 * (x % (D / 4));
+            float mx = s_m[0][r];
+#pragma unroll
+            for (int y = 1; y < kWarps; ++y) mx = fmaxf(mx, s_m[y][r]);
+            float sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int y = 0; y < kWarps; ++y) {
+                const float wt = s_m[y][r] == -INFINITY ? 0.f : ex2(s_m[y][r] - mx);
+                sum = fmaf(wt, s_l[y][r], sum);
+                const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem) +
+                                                                  (y * C::kRows + r) * D + d);
+                acc[0] = fmaf(wt, v.x, acc[0]);
+                acc[1] = fmaf(wt, v.y, acc[1]);
+                acc[2] = fmaf(wt, v.z, acc[2]);
+                acc[3] = fmaf(wt, v.w, acc[3]);
+            }
+            if (whole) {
+                const int row = rb * C::kRows + r;
+                if (row < rows) {
+                    const int h = kvh * (a.H / a.Hkv) + row / a.Nq, i = row % a.Nq;
+                    const float inv = mx == -INFINITY ? 0.f : 1.f / sum;
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) acc[y] *= inv;
+                    store_row4<D, BF16>(a, b, h, i, d, acc);
+                    if (d == 0 && a.lse != nullptr)
+                        a.lse[(static_cast<int64_t>(b) * a.H + h) * a.Nq + i] =
+                            mx == -INFINITY ? -INFINITY : (mx + log2f(sum)) * kLn2;
+                }
+            } else {
+                *reinterpret_cast<float4*>(part + 2 * C::kRows + r * D + d) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+                if (d == 0) {
+                    part[r] = mx;
+                    part[C::kRows + r] = sum;
+                }
+            }
+        }
+        if (!whole && t0 == 0) {
+            // Cut, and begun here: the CTAs up to that of its last unit hold the rest.
+            const int64_t last_unit = at + tiles - 1;
+            int c = cta;
+            while (share_begin(units, c + 1, ctas) <= last_unit) ++c;
+            cut = make_int4(b, target, c - cta + 1, slot);
+        }
+        __syncthreads();  // the joined memory becomes the ring again
+        at += t1 - t0;
+        if (t1 == tiles && at - seq_at == static_cast<int64_t>(tiles) * per_key) {
+            seq_at = at;
+            ++b;
+        }
+    }
+    if (tid == 0) cuts_of(a.workspace)[cta] = cut;
+}
+
+// Joins the parts of the cut sequence that starts in CTA blockIdx.x of the
+// first kernel (its parts: that CTA's, then the first parts of the CTAs after
+// it), row blockIdx.y, in a fixed order: four warps take the parts in turn.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(128) decode_join_kernel(const __grid_constant__ DecodeArgs a, int rows_per_block) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int4 cut = cuts_of(a.workspace)[blockIdx.x];
+    if (cut.z == 0) return;
+    const int rows = (a.H / a.Hkv) * a.Nq;
+    const int row_blocks = (rows + rows_per_block - 1) / rows_per_block;
+    const int kvh = cut.y / row_blocks, rb = cut.y - kvh * row_blocks;
+    const int r = blockIdx.y, row = rb * rows_per_block + r;
+    if (row >= rows) return;
+    constexpr int E = D / 32;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    float m = -INFINITY, l = 0.f, o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+    for (int p = warp; p < cut.z; p += 4) {
+        const int slot = p == 0 ? cut.w : 2 * (static_cast<int>(blockIdx.x) + p);
+        const float* part = part_of<D>(a.workspace, slot, rows_per_block);
+        const float pm = part[r], pl = part[rows_per_block + r];
+        float v[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = part[2 * rows_per_block + r * D + lane * E + e];
+        const float mn = fmaxf(m, pm);
+        const float wo = m == -INFINITY ? 0.f : ex2(m - mn), wp = pm == -INFINITY ? 0.f : ex2(pm - mn);
+        l = l * wo + pl * wp;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = o[e] * wo + v[e] * wp;
         m = mn;
     }
     __shared__ float sm[4], sl[4], so[4][D];
@@ -89,44 +768,79 @@ __global__ void __launch_bounds__(128) decode_kernel(const __grid_constant__ Dec
     }
     __syncthreads();
     const float mx = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-    float lt = 0.f, w[4];
+    float sum = 0.f, wt[4];
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-        w[x] = sm[x] == -INFINITY ? 0.f : exp2f(sm[x] - mx);
-        lt += w[x] * sl[x];
+        wt[x] = sm[x] == -INFINITY ? 0.f : ex2(sm[x] - mx);
+        sum += wt[x] * sl[x];
     }
-    const float inv = lt > 0.f ? 1.f / lt : 0.f;
-    if (threadIdx.x < D) {
-        float acc = 0.f;
+    const int h = kvh * (a.H / a.Hkv) + row / a.Nq, i = row % a.Nq;
+    if (threadIdx.x < D / 4) {
+        const int d = 4 * threadIdx.x;
+        const float inv = mx == -INFINITY ? 0.f : 1.f / sum;
+        float acc[4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) acc += w[x] * so[x][threadIdx.x];
-        const int64_t at = b * a.o_bs + h * a.o_hs + i * a.o_ns + threadIdx.x;
-        if (BF16)
-            static_cast<__nv_bfloat16*>(a.o)[at] = __float2bfloat16(acc * inv);
-        else
-            static_cast<__half*>(a.o)[at] = __float2half(acc * inv);
+        for (int y = 0; y < 4; ++y)
+            acc[y] = (wt[0] * so[0][d + y] + wt[1] * so[1][d + y] + wt[2] * so[2][d + y] + wt[3] * so[3][d + y]) * inv;
+        store_row4<D, BF16>(a, cut.x, h, i, d, acc);
     }
     if (threadIdx.x == 0 && a.lse != nullptr)
-        a.lse[(static_cast<int64_t>(b) * a.H + h) * a.Nq + i] = lt > 0.f ? (mx + log2f(lt)) * kLn2 : -INFINITY;
+        a.lse[(static_cast<int64_t>(cut.x) * a.H + h) * a.Nq + i] =
+            mx == -INFINITY ? -INFINITY : (mx + log2f(sum)) * kLn2;
+}
+
+template <int D, bool BF16, bool KV4, int NT>
+cudaError_t launch_one(const DecodeArgs& a, int sms, cudaStream_t s) {
+    using C = Config<D, KV4, NT>;
+    auto* fn = decode_kernel<D, BF16, KV4, NT>;
+    static std::atomic<bool> done[kMaxDevices] = {};
+    cudaError_t e = opt_in_smem_once(fn, C::kSmem, done);
+    if (e != cudaSuccess) return e;
+    const int grid = sms * C::kCtasPerSm < kMaxCtas ? sms * C::kCtasPerSm : kMaxCtas;
+    fn<<<grid, kThreads, C::kSmem, s>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    // No sequence can be longer than a unit: none is cut.
+    if (a.table_width * a.page_size <= kUnit) return cudaSuccess;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, C::kRows);
+    cfg.blockDim = dim3(128);
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, decode_join_kernel<D, BF16>, a, static_cast<int>(C::kRows));
+}
+
+// Tiles of 8 query rows that share one pass over the keys.
+int row_tiles(int64_t rows) { return rows <= 8 ? 1 : (rows <= 16 ? 2 : 4); }
+
+template <int D, bool BF16, bool KV4>
+cudaError_t launch_rows(const DecodeArgs& a, int sms, cudaStream_t s) {
+    switch (row_tiles(static_cast<int64_t>(a.H / a.Hkv) * a.Nq)) {
+        case 1: return launch_one<D, BF16, KV4, 1>(a, sms, s);
+        case 2: return launch_one<D, BF16, KV4, 2>(a, sms, s);
+        default: return launch_one<D, BF16, KV4, 4>(a, sms, s);
+    }
 }
 
 template <int D, bool BF16>
-cudaError_t launch_kind(const DecodeArgs& a, bool kv4, cudaStream_t s) {
-    const dim3 grid(a.H * a.Nq, a.B);
-    if (kv4)
-        decode_kernel<D, BF16, true><<<grid, 128, 0, s>>>(a);
-    else
-        decode_kernel<D, BF16, false><<<grid, 128, 0, s>>>(a);
-    return cudaGetLastError();
+cudaError_t launch_kind(const DecodeArgs& a, bool kv4, int sms, cudaStream_t s) {
+    return kv4 ? launch_rows<D, BF16, true>(a, sms, s) : launch_rows<D, BF16, false>(a, sms, s);
 }
 
 }  // namespace
 
-int64_t decode_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t) { return 16; }
+int64_t decode_workspace_bytes(int64_t, int64_t H, int64_t Hkv, int64_t Nq, int64_t D) {
+    const int64_t rows = 8 * row_tiles(H / Hkv * Nq);
+    return 16 * kMaxCtas + 2 * kMaxCtas * rows * (D + 2) * static_cast<int64_t>(sizeof(float));
+}
 
-cudaError_t decode_launch(const DecodeArgs& a, int D, bool bf16, bool kv4, int, cudaStream_t s) {
-    if (D == 128) return bf16 ? launch_kind<128, true>(a, kv4, s) : launch_kind<128, false>(a, kv4, s);
-    return bf16 ? launch_kind<64, true>(a, kv4, s) : launch_kind<64, false>(a, kv4, s);
+cudaError_t decode_launch(const DecodeArgs& a, int D, bool bf16, bool kv4, int sms, cudaStream_t s) {
+    if (D == 128) return bf16 ? launch_kind<128, true>(a, kv4, sms, s) : launch_kind<128, false>(a, kv4, sms, s);
+    return bf16 ? launch_kind<64, true>(a, kv4, sms, s) : launch_kind<64, false>(a, kv4, sms, s);
 }
 
 cudaError_t decode_read_and_clear_error_word(uint32_t* out) {
