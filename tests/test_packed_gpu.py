@@ -245,3 +245,35 @@ def test_prompts_then_steps(dtype, D, H, Hkv, kv4):
         o, lse = att(qd, *cache, table.cuda(), seq)
         ok()
         check_decode(kv4, qd, cache, table, seq, scale, o, lse, "step %d" % step)
+
+
+def test_results_allocated_on_the_call_s_stream():
+    """Without out, lse and workspace a call on another stream allocates them
+    there: nothing enqueued on the current stream touches them meanwhile."""
+    H, Hkv, D = 4, 2, 64
+    q, k, v, cu = make([300, 5], H, Hkv, D, torch.float16, 12)
+    want, want_l = fattn.fwd_packed(q, k, v, cu)
+    pages = torch.zeros(20, Hkv, 16, D, dtype=torch.float16, device="cuda")
+    vpages = torch.zeros_like(pages)
+    slots = torch.arange(305).cuda()
+    table = torch.arange(20, dtype=torch.int32, device="cuda")[None]
+    n = torch.tensor([305], dtype=torch.int32).cuda()
+    fattn.cache_append(k, v, pages, vpages, slots)
+    qd = q[-1:].unsqueeze(2)
+    dec, dec_l = fattn.decode(qd, pages, vpages, table, n)
+    ok()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    big = torch.empty(1 << 26, device="cuda")
+    for _ in range(20):
+        big.normal_()  # keeps the current stream busy, and its freed blocks in use
+        junk = torch.full_like(want, 9.0)
+        del junk
+        o, l = fattn.fwd_packed(q, k, v, cu, stream=s)
+        o2, l2 = fattn.decode(qd, pages, vpages, table, n, stream=s)
+        s.synchronize()
+        with torch.cuda.stream(s):
+            assert torch.equal(o, want) and torch.equal(l, want_l)
+            assert torch.equal(o2, dec) and torch.equal(l2, dec_l)
+    torch.cuda.synchronize()
+    assert fattn.get_device_status() == 0
