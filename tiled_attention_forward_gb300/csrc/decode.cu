@@ -21,9 +21,10 @@
 // filled by cp.async (zero-filled behind the last key), so that warps never
 // wait for one another until their share of a sequence is done; then the CTA
 // joins its eight warps' (max, sum, O).  A sequence that lies in one CTA is
-// written out there; of the others each CTA writes its part to the workspace
-// and a second kernel joins them in a fixed order.  At most two parts per CTA
-// (its first and its last sequence) are ever cut.
+// written out there; of the others each CTA writes its part to the workspace,
+// and the CTA whose part comes last joins them all, in the order of the keys
+// (so that the result does not depend on which one that is).  At most two parts
+// per CTA (its first and its last sequence) are ever cut.
 //
 // Softmax.  A lane keeps the reference max of its query rows; O and the sums
 // are rescaled only when a score passes it by more than 8 (log2), by a vote
@@ -45,6 +46,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kKeys = 16;                 // keys of a warp's stage
 constexpr int kUnit = kWarps * kKeys;     // keys of a unit
 constexpr int kMaxCtas = 320;             // parts in the workspace: two per CTA
+constexpr int kMaxParts = 64;             // CTAs a sequence is cut between: one CTA joins the parts
 constexpr float kRescaleThreshold = 8.0f; // log2 units: P <= 2^8 while the max is stale
 
 // ---- instructions ----------------------------------------------------------
@@ -143,12 +145,32 @@ template <int D>
 __device__ __forceinline__ float* part_of(void* ws, int slot, int rows) {
     return static_cast<float*>(ws) + 4 * kMaxCtas + static_cast<int64_t>(slot) * rows * (D + 2);
 }
-// Per CTA, what the joining kernel needs to know: {sequence, head and row
-// block, parts, first part's slot} of the cut sequence that starts in it.
-__device__ __forceinline__ int4* cuts_of(void* ws) { return static_cast<int4*>(ws); }
+// Per CTA, the arrivals of the parts of the cut sequence that starts in it: a
+// mark in the upper 48 bits, the count in the lower 16.  A call leaves its words
+// marked with count 0, so that in a workspace that was used before an arrival
+// is one atomicAdd; a word without the mark is whatever the caller's memory
+// held: the first arrival to replace it counts 1, and what others added to it
+// meanwhile is not counted (they find no mark either and come again).
+constexpr unsigned long long kMark = 0x5bd1e995a7c3ull << 16;
+__device__ __forceinline__ unsigned long long* arrivals_of(void* ws) { return static_cast<unsigned long long*>(ws); }
+__device__ __forceinline__ int arrive(unsigned long long* word) {  // the arrivals so far, this one among them
+    unsigned long long seen = atomicAdd(word, 1ull);
+    while ((seen >> 16) != (kMark >> 16)) {
+        const unsigned long long now = atomicCAS(word, seen, kMark | 1ull);
+        if (now == seen) return 1;
+        seen = (now >> 16) == (kMark >> 16) ? atomicAdd(word, 1ull) : now;
+    }
+    return static_cast<int>(seen & 0xffffull) + 1;
+}
 
 // The share of CTA c.
 __device__ __forceinline__ int64_t share_begin(int64_t units, int c, int ctas) { return units * c / ctas; }
+// The CTA whose share holds a unit.
+__device__ __forceinline__ int cta_of(int64_t unit, int64_t units, int ctas) {
+    int c = static_cast<int>(unit * ctas / units);
+    while (share_begin(units, c + 1, ctas) <= unit) ++c;
+    return c;
+}
 
 __device__ __forceinline__ int visible_len(const DecodeArgs& a, int b, bool report) {
     const int64_t most = a.table_width * a.page_size;
@@ -161,10 +183,19 @@ __device__ __forceinline__ int visible_len(const DecodeArgs& a, int b, bool repo
 }
 __device__ __forceinline__ int units_of(int len) { return max(1, (len + kUnit - 1) / kUnit); }
 
+// Writes 4 dims of one query row (of K/V head kvh) from its unnormalised sum.
 template <int D, bool BF16>
-__device__ __forceinline__ void store_row4(const DecodeArgs& a, int b, int h, int i, int d, const float (&x)[4]) {
+__device__ __forceinline__ void store_out(const DecodeArgs& a, int b, int kvh, int row, int d, const float (&acc)[4],
+                                          float mx, float sum) {
+    const int share = a.H / a.Hkv;
+    if (row >= share * a.Nq) return;
+    const int h = kvh * share + row / a.Nq, i = row % a.Nq;
+    const float inv = mx == -INFINITY ? 0.f : 1.f / sum;
     uint16_t* o = static_cast<uint16_t*>(a.o) + b * a.o_bs + h * a.o_hs + i * a.o_ns + d;
-    *reinterpret_cast<uint2*>(o) = make_uint2(pack16<BF16>(x[0], x[1]), pack16<BF16>(x[2], x[3]));
+    *reinterpret_cast<uint2*>(o) =
+        make_uint2(pack16<BF16>(acc[0] * inv, acc[1] * inv), pack16<BF16>(acc[2] * inv, acc[3] * inv));
+    if (d == 0 && a.lse != nullptr)
+        a.lse[(static_cast<int64_t>(b) * a.H + h) * a.Nq + i] = mx == -INFINITY ? -INFINITY : (mx + log2f(sum)) * kLn2;
 }
 
 // ---- one warp's keys ----------------------------------------------------------
@@ -519,33 +550,46 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
     using S = Stage<D, KV4>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t s_scan[kWarps];
+    __shared__ int s_most[kWarps];
     __shared__ int64_t s_begin;   // units before the first sequence of this share
     __shared__ int s_first;       // that sequence
+    __shared__ int s_last;        // this CTA's part was the last to come
     __shared__ float s_m[kWarps][C::kRows], s_l[kWarps][C::kRows];
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int rows = (a.H / a.Hkv) * a.Nq;
     const int row_blocks = (rows + C::kRows - 1) / C::kRows;
     const int per_key = a.Hkv * row_blocks;  // targets of one sequence
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // All units of the call, and this CTA's share of them.
     int64_t mine = 0;
-    for (int b = tid; b < a.B; b += kThreads) mine += units_of(visible_len(a, b, blockIdx.x == 0));
+    int most = 0;
+    for (int b = tid; b < a.B; b += kThreads) {
+        const int n = units_of(visible_len(a, b, blockIdx.x == 0));
+        mine += n;
+        most = max(most, n);
+    }
 #pragma unroll
     for (int d = 16; d > 0; d /= 2) mine += __shfl_xor_sync(0xffffffffu, mine, d);
-    if (lane == 0) s_scan[warp] = mine;
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) {
+        s_scan[warp] = mine;
+        s_most[warp] = most;
+    }
     __syncthreads();
     int64_t units = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) units += s_scan[w];
+    for (int w = 0; w < kWarps; ++w) {
+        units += s_scan[w];
+        most = max(most, s_most[w]);
+    }
     units *= per_key;
     // CTAs that get a share: no more than units, so that the CTAs a sequence is
-    // cut between are neighbours.
-    const int ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), units)), cta = blockIdx.x;
-    if (cta >= ctas) {
-        if (tid == 0) cuts_of(a.workspace)[cta] = make_int4(0, 0, 0, 0);
-        return;
-    }
+    // cut between are neighbours, and so few that the longest sequence is cut
+    // into about kMaxParts.
+    const int cta = blockIdx.x;
+    const int ctas = static_cast<int>(min(min(static_cast<int64_t>(gridDim.x), units),
+                                          max(units * kMaxParts / most, static_cast<int64_t>(1))));
+    if (cta >= ctas) return;
     const int64_t begin = share_begin(units, cta, ctas), end = share_begin(units, cta + 1, ctas);
     // The sequence of unit `begin`: prefix sums, kThreads sequences at a time.
     int64_t before = 0;
@@ -579,7 +623,6 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
 
     int b = s_first;
     int64_t seq_at = s_begin;  // first unit of sequence b
-    int4 cut = make_int4(0, 0, 0, 0);
     uint32_t ring = smem_addr(smem) + warp * C::kStages * S::kBytes;
     const int page_shift = (a.page_size & (a.page_size - 1)) == 0 ? __ffs(a.page_size) - 1 : -1;
     Warp<D, BF16, KV4, NT> w;
@@ -594,7 +637,6 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
         const int kvh = target / row_blocks, rb = target - kvh * row_blocks;
         const int32_t* table = a.block_table + b * a.table_width;
 
-        w.load_q(a, b, kvh, rb);
         int ends[NT][2];
         const int min_end = len - a.Nq + 1;
 #pragma unroll
@@ -630,9 +672,16 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
             }
             cp_async_commit();
         };
+        int page;
+        {
+            int pages[C::kStages];  // all on their way before the first is used
 #pragma unroll
-        for (int i = 0; i < C::kStages - 1; ++i) start(i, page_at(i));
-        int page = page_at(C::kStages - 1);
+            for (int i = 0; i < C::kStages; ++i) pages[i] = page_at(i);
+#pragma unroll
+            for (int i = 0; i < C::kStages - 1; ++i) start(i, pages[i]);
+            page = pages[C::kStages - 1];
+        }
+        w.load_q(a, b, kvh, rb);
         for (int i = 0; i < turns; ++i) {
             start(i + C::kStages - 1, page);
             page = page_at(i + C::kStages);  // needed one turn later
@@ -691,31 +740,61 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
                 acc[3] = fmaf(wt, v.w, acc[3]);
             }
             if (whole) {
-                const int row = rb * C::kRows + r;
-                if (row < rows) {
-                    const int h = kvh * (a.H / a.Hkv) + row / a.Nq, i = row % a.Nq;
-                    const float inv = mx == -INFINITY ? 0.f : 1.f / sum;
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) acc[y] *= inv;
-                    store_row4<D, BF16>(a, b, h, i, d, acc);
-                    if (d == 0 && a.lse != nullptr)
-                        a.lse[(static_cast<int64_t>(b) * a.H + h) * a.Nq + i] =
-                            mx == -INFINITY ? -INFINITY : (mx + log2f(sum)) * kLn2;
-                }
+                store_out<D, BF16>(a, b, kvh, rb * C::kRows + r, d, acc, mx, sum);
             } else {
-                *reinterpret_cast<float4*>(part + 2 * C::kRows + r * D + d) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+                __stcg(reinterpret_cast<float4*>(part + 2 * C::kRows + r * D + d), make_float4(acc[0], acc[1], acc[2], acc[3]));
                 if (d == 0) {
-                    part[r] = mx;
-                    part[C::kRows + r] = sum;
+                    __stcg(part + r, mx);
+                    __stcg(part + C::kRows + r, sum);
                 }
             }
         }
-        if (!whole && t0 == 0) {
-            // Cut, and begun here: the CTAs up to that of its last unit hold the rest.
-            const int64_t last_unit = at + tiles - 1;
-            int c = cta;
-            while (share_begin(units, c + 1, ctas) <= last_unit) ++c;
-            cut = make_int4(b, target, c - cta + 1, slot);
+        if (!whole) {
+            const int64_t from = at - t0;  // the target's first unit
+            const int c0 = t0 == 0 ? cta : cta_of(from, units, ctas);
+            const int parts = cta_of(from + tiles - 1, units, ctas) - c0 + 1;
+            const int slot0 = 2 * c0 + (from == share_begin(units, c0, ctas) ? 0 : 1);
+            unsigned long long* word = arrivals_of(a.workspace) + c0;
+            __threadfence();  // this thread's part, before the arrival
+            __syncthreads();
+            if (tid == 0) {
+                s_last = arrive(word) == parts;
+                if (s_last) atomicExch(word, kMark);
+            }
+            __syncthreads();
+            if (s_last) {
+                __threadfence();
+                for (int x = tid; x < C::kRows * D / 4; x += kThreads) {
+                    const int r = x / (D / 4), d = 4 * (x % (D / 4));
+                    float mx = -INFINITY, sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+                    constexpr int kAtOnce = 4;
+                    for (int y0 = 0; y0 < parts; y0 += kAtOnce) {
+                        float pm[kAtOnce], pl[kAtOnce];
+                        float4 v[kAtOnce];
+#pragma unroll
+                        for (int y = 0; y < kAtOnce; ++y) {
+                            const int z = min(y0 + y, parts - 1);
+                            const float* p = part_of<D>(a.workspace, z == 0 ? slot0 : 2 * (c0 + z), C::kRows);
+                            pm[y] = __ldcg(p + r);
+                            pl[y] = __ldcg(p + C::kRows + r);
+                            v[y] = __ldcg(reinterpret_cast<const float4*>(p + 2 * C::kRows + r * D + d));
+                        }
+#pragma unroll
+                        for (int y = 0; y < kAtOnce; ++y) {
+                            if (y0 + y >= parts || pm[y] == -INFINITY) continue;
+                            const float mn = fmaxf(mx, pm[y]);
+                            const float wo = ex2(mx - mn), wt = ex2(pm[y] - mn);
+                            mx = mn;
+                            sum = fmaf(wt, pl[y], sum * wo);
+                            acc[0] = fmaf(wt, v[y].x, acc[0] * wo);
+                            acc[1] = fmaf(wt, v[y].y, acc[1] * wo);
+                            acc[2] = fmaf(wt, v[y].z, acc[2] * wo);
+                            acc[3] = fmaf(wt, v[y].w, acc[3] * wo);
+                        }
+                    }
+                    store_out<D, BF16>(a, b, kvh, rb * C::kRows + r, d, acc, mx, sum);
+                }
+            }
         }
         __syncthreads();  // the joined memory becomes the ring again
         at += t1 - t0;
@@ -724,69 +803,6 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
             ++b;
         }
     }
-    if (tid == 0) cuts_of(a.workspace)[cta] = cut;
-}
-
-// Joins the parts of the cut sequence that starts in CTA blockIdx.x of the
-// first kernel (its parts: that CTA's, then the first parts of the CTAs after
-// it), row blockIdx.y, in a fixed order: four warps take the parts in turn.
-template <int D, bool BF16>
-__global__ void __launch_bounds__(128) decode_join_kernel(const __grid_constant__ DecodeArgs a, int rows_per_block) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int4 cut = cuts_of(a.workspace)[blockIdx.x];
-    if (cut.z == 0) return;
-    const int rows = (a.H / a.Hkv) * a.Nq;
-    const int row_blocks = (rows + rows_per_block - 1) / rows_per_block;
-    const int kvh = cut.y / row_blocks, rb = cut.y - kvh * row_blocks;
-    const int r = blockIdx.y, row = rb * rows_per_block + r;
-    if (row >= rows) return;
-    constexpr int E = D / 32;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    float m = -INFINITY, l = 0.f, o[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.f;
-    for (int p = warp; p < cut.z; p += 4) {
-        const int slot = p == 0 ? cut.w : 2 * (static_cast<int>(blockIdx.x) + p);
-        const float* part = part_of<D>(a.workspace, slot, rows_per_block);
-        const float pm = part[r], pl = part[rows_per_block + r];
-        float v[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = part[2 * rows_per_block + r * D + lane * E + e];
-        const float mn = fmaxf(m, pm);
-        const float wo = m == -INFINITY ? 0.f : ex2(m - mn), wp = pm == -INFINITY ? 0.f : ex2(pm - mn);
-        l = l * wo + pl * wp;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = o[e] * wo + v[e] * wp;
-        m = mn;
-    }
-    __shared__ float sm[4], sl[4], so[4][D];
-#pragma unroll
-    for (int e = 0; e < E; ++e) so[warp][lane * E + e] = o[e];
-    if (lane == 0) {
-        sm[warp] = m;
-        sl[warp] = l;
-    }
-    __syncthreads();
-    const float mx = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-    float sum = 0.f, wt[4];
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-        wt[x] = sm[x] == -INFINITY ? 0.f : ex2(sm[x] - mx);
-        sum += wt[x] * sl[x];
-    }
-    const int h = kvh * (a.H / a.Hkv) + row / a.Nq, i = row % a.Nq;
-    if (threadIdx.x < D / 4) {
-        const int d = 4 * threadIdx.x;
-        const float inv = mx == -INFINITY ? 0.f : 1.f / sum;
-        float acc[4];
-#pragma unroll
-        for (int y = 0; y < 4; ++y)
-            acc[y] = (wt[0] * so[0][d + y] + wt[1] * so[1][d + y] + wt[2] * so[2][d + y] + wt[3] * so[3][d + y]) * inv;
-        store_row4<D, BF16>(a, cut.x, h, i, d, acc);
-    }
-    if (threadIdx.x == 0 && a.lse != nullptr)
-        a.lse[(static_cast<int64_t>(cut.x) * a.H + h) * a.Nq + i] =
-            mx == -INFINITY ? -INFINITY : (mx + log2f(sum)) * kLn2;
 }
 
 template <int D, bool BF16, bool KV4, int NT>
@@ -798,20 +814,7 @@ cudaError_t launch_one(const DecodeArgs& a, int sms, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const int grid = sms * C::kCtasPerSm < kMaxCtas ? sms * C::kCtasPerSm : kMaxCtas;
     fn<<<grid, kThreads, C::kSmem, s>>>(a);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    // No sequence can be longer than a unit: none is cut.
-    if (a.table_width * a.page_size <= kUnit) return cudaSuccess;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, C::kRows);
-    cfg.blockDim = dim3(128);
-    cfg.stream = s;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, decode_join_kernel<D, BF16>, a, static_cast<int>(C::kRows));
+    return cudaGetLastError();
 }
 
 // Tiles of 8 query rows that share one pass over the keys.
