@@ -13,11 +13,11 @@
 // decode step has, and its operands in shared memory; the rate needed here,
 // two m16n8k16 per 16 keys and 16 dims, is a small part of mma.sync's.)
 //
-// Keys.  A unit of work is 128 keys of one (sequence, K/V head, row block):
+// Keys.  A unit of work is 8 warps' stages of keys of one (sequence, K/V head, row block):
 // the units of the whole call are numbered in that order, and CTA c of a fixed
 // grid takes an equal share [c U / G, (c+1) U / G), whatever the lengths: only
 // device memory knows them, each CTA forms the prefix sums itself.  Within a
-// unit a warp takes 16 keys, with a ring of stages of its own in shared memory
+// unit a warp takes one stage, with a ring of stages of its own in shared memory
 // filled by cp.async (zero-filled behind the last key), so that warps never
 // wait for one another until their share of a sequence is done; then the CTA
 // joins its eight warps' (max, sum, O).  A sequence that lies in one CTA is
@@ -43,8 +43,7 @@ namespace {
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kKeys = 16;                 // keys of a warp's stage
-constexpr int kUnit = kWarps * kKeys;     // keys of a unit
+constexpr int kPart = 16;                 // keys that lie in one page and take one pass of the products
 constexpr int kMaxCtas = 320;             // parts in the workspace: two per CTA
 constexpr int kMaxParts = 64;             // CTAs a sequence is cut between: one CTA joins the parts
 constexpr float kRescaleThreshold = 8.0f; // log2 units: P <= 2^8 while the max is stale
@@ -119,8 +118,14 @@ __device__ __forceinline__ uint32_t as_u32(__half2 x) { return *reinterpret_cast
 // 4 bits: K codes (D/2 a key), K scales (D/8 a key), then V rows of codes and
 // scales, 16 bytes wider than the codes: lanes that take keys 2t of 8 bytes (4
 // at D = 64) then meet 32 different banks.
-template <int D, bool KV4>
+template <int D, bool KV4, int NT>
 struct Stage {
+    // Keys of a warp's stage.  4 bits: two parts of 16, whose loop, votes and
+    // addresses are paid once, where registers allow; 16 bits: one, as a stage
+    // is 4 times as large.
+    static constexpr int kKeys = KV4 && NT == 1 ? 32 : 16;
+    static constexpr int kParts = kKeys / kPart;
+    static constexpr int kUnit = kWarps * kKeys;  // keys of a unit
     static constexpr int kCode = D / 2, kMeta = D / kKv4Group * 4;
     static constexpr int kVRow = KV4 ? kCode + 16 : 2 * D;
     static constexpr int kKMetaOff = kKeys * kCode;
@@ -130,10 +135,10 @@ struct Stage {
 
 template <int D, bool KV4, int NT>
 struct Config {
-    static constexpr int kStages = KV4 ? 4 : 3;
+    static constexpr int kStages = KV4 ? (NT == 1 ? 2 : 4) : 3;
     static constexpr int kCtasPerSm = NT == 4 || (!KV4 && D == 128) ? 1 : 2;
     static constexpr int kRows = 8 * NT;
-    static constexpr int kRing = kWarps * kStages * Stage<D, KV4>::kBytes;
+    static constexpr int kRing = kWarps * kStages * Stage<D, KV4, NT>::kBytes;
     // The warps' O is joined in the same memory.
     static constexpr int kJoin = kWarps * kRows * D * 4;
     static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
@@ -181,7 +186,10 @@ __device__ __forceinline__ int visible_len(const DecodeArgs& a, int b, bool repo
     }
     return len;
 }
-__device__ __forceinline__ int units_of(int len) { return max(1, (len + kUnit - 1) / kUnit); }
+template <int UNIT>
+__device__ __forceinline__ int units_of(int len) {
+    return max(1, static_cast<int>((static_cast<uint32_t>(len) + UNIT - 1) / UNIT));
+}
 
 // Writes 4 dims of one query row (of K/V head kvh) from its unnormalised sum.
 template <int D, bool BF16>
@@ -201,7 +209,7 @@ __device__ __forceinline__ void store_out(const DecodeArgs& a, int b, int kvh, i
 // ---- one warp's keys ----------------------------------------------------------
 template <int D, bool BF16, bool KV4, int NT>
 struct Warp {
-    using S = Stage<D, KV4>;
+    using S = Stage<D, KV4, NT>;
     static constexpr int kQ = D / 16;   // k-steps of S^T, m-tiles of O^T
     uint32_t q[NT][kQ][2];              // B fragments of Q^T
     uint32_t qsum[NT];                  // 4 bits: (high, low) part of the sum of q over group t
@@ -285,47 +293,71 @@ struct Warp {
         }
     }
 
-    // Starts the copies of 16 keys from place `off` of `page` (`valid` of them
-    // are keys of the sequence; the rest of the stage becomes zero).
-    __device__ __forceinline__ void fetch(const DecodeArgs& a, uint32_t stage, int64_t page, int kvh, int off, int valid) {
+    // What fetch() adds a page's row to: this lane's first 16 bytes (and, 4
+    // bits, its key's scales), for K/V head kvh.
+    struct Source {
+        const uint8_t* k;
+        const uint8_t* v;
+        const uint8_t* scales;
+    };
+    static __device__ __forceinline__ Source source(const DecodeArgs& a, int kvh) {
+        const int lane = threadIdx.x % 32;
+        const int64_t head = static_cast<int64_t>(kvh) * a.page_size;  // rows before this head in a page
+        Source f;
+        if constexpr (!KV4) {
+            f.k = static_cast<const uint8_t*>(a.k_pages) + head * 2 * D + 16 * lane;
+            f.v = static_cast<const uint8_t*>(a.v_pages) + head * 2 * D + 16 * lane;
+            f.scales = nullptr;
+        } else {
+            f.k = static_cast<const uint8_t*>(a.k_pages) + head * S::kCode + 16 * lane;
+            f.v = static_cast<const uint8_t*>(a.v_pages) + head * S::kCode + 16 * lane;
+            f.scales = static_cast<const uint8_t*>(lane < 16 ? a.k_scales : a.v_scales) + (head + lane % 16) * S::kMeta;
+        }
+        return f;
+    }
+
+    // Starts the copies of part `part` of a stage: 16 keys from place `off` of
+    // `page` (`valid` of them are keys of the sequence; the rest become zero).
+    // FULL: all of them are.
+    template <bool FULL>
+    static __device__ __forceinline__ void fetch(const DecodeArgs& a, const Source& f, uint32_t stage, int part,
+                                                 int page, int off, int valid) {
         const int lane = threadIdx.x % 32;
         if constexpr (!KV4) {
             constexpr int kChunks = D / 8, kRowsAtOnce = 32 / kChunks;
-            const int64_t at = page * a.page_stride + (static_cast<int64_t>(kvh) * a.page_size + off) * D;
+            const int64_t at = 2 * (page * a.page_stride + static_cast<int64_t>(off) * D);
             const int c = lane % kChunks;
-            const uint16_t* k = static_cast<const uint16_t*>(a.k_pages) + at + 8 * lane;
-            const uint16_t* v = static_cast<const uint16_t*>(a.v_pages) + at + 8 * lane;
 #pragma unroll
-            for (int i = 0; i < kKeys / kRowsAtOnce; ++i) {
+            for (int i = 0; i < kPart / kRowsAtOnce; ++i) {
                 const int r = i * kRowsAtOnce + lane / kChunks;
                 const uint32_t dst = stage + r * 2 * D + ((c ^ (r & 7)) << 4);
-                const int bytes = r < valid ? 16 : 0;
-                cp_async16(dst, k + i * 256, bytes);
-                cp_async16(dst + S::kVOff, v + i * 256, bytes);
+                const int bytes = FULL || r < valid ? 16 : 0;
+                cp_async16(dst, f.k + at + i * 512, bytes);
+                cp_async16(dst + S::kVOff, f.v + at + i * 512, bytes);
             }
         } else {
             constexpr int kChunks = D / 32;  // 16-byte chunks of a row of codes
-            const int64_t row = (page * a.Hkv + kvh) * a.page_size + off;
-            const uint8_t* k = static_cast<const uint8_t*>(a.k_pages) + row * S::kCode;
-            const uint8_t* v = static_cast<const uint8_t*>(a.v_pages) + row * S::kCode;
+            const uint64_t row = static_cast<uint64_t>(static_cast<uint32_t>(page)) *
+                                     static_cast<uint32_t>(a.Hkv * a.page_size) + static_cast<uint32_t>(off);
+            const uint8_t* k = f.k + row * S::kCode;
+            const uint8_t* v = f.v + row * S::kCode;
 #pragma unroll
-            for (int i = 0; i < kKeys * kChunks / 32; ++i) {
-                const int x = i * 32 + lane, r = x / kChunks, c = x % kChunks;
-                const int bytes = r < valid ? 16 : 0;
-                cp_async16(stage + x * 16, k + x * 16, bytes);
-                cp_async16(stage + S::kVOff + r * S::kVRow + c * 16, v + x * 16, bytes);
+            for (int i = 0; i < kPart * kChunks / 32; ++i) {
+                const int r = i * (32 / kChunks) + lane / kChunks, c = lane % kChunks;
+                const int bytes = FULL || r < valid ? 16 : 0;
+                cp_async16(stage + part * kPart * S::kCode + i * 512 + lane * 16, k + i * 512, bytes);
+                cp_async16(stage + S::kVOff + (part * kPart + r) * S::kVRow + c * 16, v + i * 512, bytes);
             }
             const int r = lane % 16;
-            const bool is_k = lane < 16;
-            const uint8_t* sc = static_cast<const uint8_t*>(is_k ? a.k_scales : a.v_scales) + (row + r) * S::kMeta;
-            const uint32_t dst = is_k ? stage + S::kKMetaOff + r * S::kMeta : stage + S::kVOff + r * S::kVRow + S::kCode;
-            cp_async_small<S::kMeta>(dst, sc, r < valid ? S::kMeta : 0);
+            const uint32_t dst = lane < 16 ? stage + S::kKMetaOff + (part * kPart + r) * S::kMeta
+                                           : stage + S::kVOff + (part * kPart + r) * S::kVRow + S::kCode;
+            cp_async_small<S::kMeta>(dst, f.scales + row * S::kMeta, FULL || r < valid ? S::kMeta : 0);
         }
     }
 
-    // S^T of the stage's 16 keys, in log2 units: s[n][0..1] key g, s[n][2..3] key
+    // S^T of 16 keys of the stage, in log2 units: s[n][0..1] key g, s[n][2..3] key
     // g + 8, rows 2t and 2t+1.
-    __device__ __forceinline__ void scores(uint32_t stage, float (&s)[NT][4]) const {
+    __device__ __forceinline__ void scores(uint32_t stage, int part, float (&s)[NT][4]) const {
         const int lane = threadIdx.x % 32;
         if constexpr (!KV4) {
 #pragma unroll
@@ -353,21 +385,17 @@ struct Warp {
             // (high, low) part of the sum of q, group t in lane t.
             const int g = lane / 4, t = lane % 4;
             uint32_t w[2][D / 32], meta[2][D / 32];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const uint32_t at = stage + (g + 8 * u) * S::kCode + t * (D / 8);
-                const uint32_t mt = stage + S::kKMetaOff + (g + 8 * u) * S::kMeta;
-                lds_words(w[u], at);
-                lds_words(meta[u], mt);
-            }
             uint32_t z[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                uint32_t mine = 0u;
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i)
-                    if (i == t) mine = meta[u][i];
-                z[u] = __byte_perm(mine, 0u, 0x3232);
+                const int key = part * kPart + g + 8 * u;
+                const uint32_t mt = stage + S::kKMetaOff + key * S::kMeta;
+                lds_words(w[u], stage + key * S::kCode + t * (D / 8));
+                lds_words(meta[u], mt);
+                // (D = 64 has two groups: lanes 2 and 3 repeat them, and meet a
+                // sum of q that is zero.)
+                z[u] = lds_word(mt + 4 * (t % (D / 32)));
+                z[u] = __byte_perm(z[u], 0u, 0x3232);
             }
             float zs[NT][4];
 #pragma unroll
@@ -423,9 +451,9 @@ struct Warp {
     }
 
     // O^T += V^T P^T; p[n][u]: B fragments (keys 2t, 2t+1 and 8 further, row g).
-    __device__ __forceinline__ void accumulate(uint32_t stage, const uint32_t (&p)[NT][2]) {
+    __device__ __forceinline__ void accumulate(uint32_t stage, int part, const uint32_t (&p)[NT][2]) {
         const int lane = threadIdx.x % 32;
-        const uint32_t base = stage + S::kVOff;
+        const uint32_t base = stage + S::kVOff + part * kPart * S::kVRow;
         if constexpr (!KV4) {
             const int r = (lane & 7) + ((lane & 16) >> 1);
 #pragma unroll
@@ -491,32 +519,44 @@ struct Warp {
     }
 
     // The stage's keys: `key` is the first one's index, ends[n][x] the number of
-    // keys that row 2t + x sees (tested when `masked`).
-    __device__ __forceinline__ void keys(uint32_t stage, int key, bool masked, const int (&ends)[NT][2]) {
+    // keys that row 2t + x sees (tested when `masked`); bit p of `skip`: part p
+    // holds nothing.
+    __device__ __forceinline__ void keys(uint32_t stage, int key, bool masked, uint32_t skip, const int (&ends)[NT][2]) {
         const int lane = threadIdx.x % 32, g = lane / 4;
-        float s[NT][4];
-        scores(stage, s);
+        constexpr int P = S::kParts;
+        float s[P][NT][4];
+#pragma unroll
+        for (int u = 0; u < P; ++u) scores(stage, u, s[u]);
         if (masked) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int u = 0; u < P; ++u)
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    if (key + g + (x & 2) * 4 >= ends[n][x & 1]) s[n][x] = -INFINITY;
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        if (key + u * kPart + g + (x & 2) * 4 >= ends[n][x & 1] || ((skip >> u) & 1u))
+                            s[u][n][x] = -INFINITY;
         }
+        float mx[NT][2];
         bool grow = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int x = 0; x < 2; ++x) grow |= fmaxf(s[n][x], s[n][x + 2]) > m[n][x] + kRescaleThreshold;
+            for (int x = 0; x < 2; ++x) {
+                mx[n][x] = fmaxf(s[0][n][x], s[0][n][x + 2]);
+#pragma unroll
+                for (int u = 1; u < P; ++u) mx[n][x] = fmaxf(mx[n][x], fmaxf(s[u][n][x], s[u][n][x + 2]));
+                grow |= mx[n][x] > m[n][x] + kRescaleThreshold;
+            }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    float mx = fmaxf(s[n][x], s[n][x + 2]);
+                    float top = mx[n][x];
 #pragma unroll
-                    for (int d = 4; d < 32; d *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                    const float mn = fmaxf(m[n][x], mx);
+                    for (int d = 4; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                    const float mn = fmaxf(m[n][x], top);
                     const float alpha = mn == -INFINITY ? 1.f : ex2(m[n][x] - mn);
                     m[n][x] = mn;
                     l[n][x] *= alpha;
@@ -527,19 +567,23 @@ struct Warp {
                     }
                 }
         }
-        uint32_t p[NT][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const float m0 = m[n][0] == -INFINITY ? 0.f : m[n][0], m1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
-            const float p0 = ex2(s[n][0] - m0), p1 = ex2(s[n][1] - m1), p2 = ex2(s[n][2] - m0), p3 = ex2(s[n][3] - m1);
-            l[n][0] += p0 + p2;
-            l[n][1] += p1 + p3;
-            // P rounded to the operands' type (fp16 beside 4-bit values), key by row
-            // to row by key.
-            p[n][0] = movmatrix_trans(pack16<BF16 && !KV4>(p0, p1));
-            p[n][1] = movmatrix_trans(pack16<BF16 && !KV4>(p2, p3));
+        for (int u = 0; u < P; ++u) {
+            uint32_t p[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const float m0 = m[n][0] == -INFINITY ? 0.f : m[n][0], m1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+                const float p0 = ex2(s[u][n][0] - m0), p1 = ex2(s[u][n][1] - m1);
+                const float p2 = ex2(s[u][n][2] - m0), p3 = ex2(s[u][n][3] - m1);
+                l[n][0] += p0 + p2;
+                l[n][1] += p1 + p3;
+                // P rounded to the operands' type (fp16 beside 4-bit values), key by
+                // row to row by key.
+                p[n][0] = movmatrix_trans(pack16<BF16 && !KV4>(p0, p1));
+                p[n][1] = movmatrix_trans(pack16<BF16 && !KV4>(p2, p3));
+            }
+            accumulate(stage, u, p);
         }
-        accumulate(stage, p);
     }
 };
 
@@ -547,7 +591,7 @@ template <int D, bool BF16, bool KV4, int NT>
 __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
     decode_kernel(const __grid_constant__ DecodeArgs a) {
     using C = Config<D, KV4, NT>;
-    using S = Stage<D, KV4>;
+    using S = Stage<D, KV4, NT>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t s_scan[kWarps];
     __shared__ int s_most[kWarps];
@@ -564,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
     int64_t mine = 0;
     int most = 0;
     for (int b = tid; b < a.B; b += kThreads) {
-        const int n = units_of(visible_len(a, b, blockIdx.x == 0));
+        const int n = units_of<S::kUnit>(visible_len(a, b, blockIdx.x == 0));
         mine += n;
         most = max(most, n);
     }
@@ -596,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
     for (int b0 = 0;; b0 += kThreads) {
         __syncthreads();  // s_scan is read by all before it is written again
         const int b = b0 + tid;
-        const int64_t own = b < a.B ? static_cast<int64_t>(units_of(visible_len(a, b, false))) * per_key : 0;
+        const int64_t own = b < a.B ? static_cast<int64_t>(units_of<S::kUnit>(visible_len(a, b, false))) * per_key : 0;
         int64_t x = own;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
@@ -625,11 +669,12 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
     int64_t seq_at = s_begin;  // first unit of sequence b
     uint32_t ring = smem_addr(smem) + warp * C::kStages * S::kBytes;
     const int page_shift = (a.page_size & (a.page_size - 1)) == 0 ? __ffs(a.page_size) - 1 : -1;
+    const bool one_page = a.page_size % S::kKeys == 0;  // a stage never crosses pages
     Warp<D, BF16, KV4, NT> w;
     int64_t at = begin;
     while (at < end) {
         const int len = visible_len(a, b, false);
-        const int tiles = units_of(len);
+        const int tiles = units_of<S::kUnit>(len);
         const int64_t in_seq = at - seq_at;
         const int target = static_cast<int>(in_seq / tiles);  // K/V head and row block
         const int t0 = static_cast<int>(in_seq - static_cast<int64_t>(target) * tiles);
@@ -647,49 +692,85 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
                 ends[n][x] = r < rows ? min_end + r % a.Nq : len;  // rows that are none: anything finite
             }
 
-        // This warp's keys: 16 at first + 128 i.
-        const int first = t0 * kUnit + warp * kKeys;
-        const int last = min(len, t1 * kUnit);
-        const int turns = first < last ? (last - first + kUnit - 1) / kUnit : 0;
-        auto page_at = [&](int i) -> int {  // the page of turn i, -1 where there is none
-            const int key = first + i * kUnit;
-            if (i >= turns) return -1;
-            return table[page_shift >= 0 ? key >> page_shift : key / a.page_size];
+        // This warp's keys: kKeys at first + kUnit i.
+        const int first = t0 * S::kUnit + warp * S::kKeys;
+        const int last = min(len, t1 * S::kUnit);
+        const int turns = first < last ? (last - first + S::kUnit - 1) / S::kUnit : 0;
+        const typename Warp<D, BF16, KV4, NT>::Source source = w.source(a, kvh);
+        struct Pages {
+            int p[S::kParts];
         };
-        uint32_t skip = 0u;  // bit s: stage s holds nothing
-        auto start = [&](int i, int page) {
+        auto pages_at = [&](int i) -> Pages {  // the pages of turn i's parts (any where there are none)
+            const int key = first + i * S::kUnit;
+            Pages r;
+#pragma unroll
+            for (int u = 0; u < S::kParts; ++u) {
+                const int k = key + u * kPart;
+                if (u > 0 && one_page)
+                    r.p[u] = r.p[0];
+                else
+                    r.p[u] = i < turns && k < last ? table[page_shift >= 0 ? k >> page_shift : k / a.page_size] : 0;
+            }
+            return r;
+        };
+        uint32_t skip = 0u;  // bit s * kParts + u: part u of stage s holds nothing
+        auto start = [&](int i, const Pages& pages) {
             if (i < turns) {
                 const int stage = i % C::kStages;
-                const int key = first + i * kUnit;
-                if (page < 0 || page >= a.num_pages) {
-                    if (lane == 0) atomicOr(&g_decode_error_word, 1u << kDevErrInvalidArg);
-                    skip |= 1u << stage;
+                const uint32_t at = ring + stage * S::kBytes;
+                const int key = first + i * S::kUnit;
+                const uint32_t bits = ((1u << S::kParts) - 1u) << (stage * S::kParts);
+                bool fine = last - key >= S::kKeys;
+#pragma unroll
+                for (int u = 0; u < S::kParts; ++u)
+                    fine = fine && static_cast<uint32_t>(pages.p[u]) < static_cast<uint32_t>(a.num_pages);
+                skip &= ~bits;
+                if (fine) {
+                    int off = page_shift >= 0 ? key & (a.page_size - 1) : key % a.page_size;
+#pragma unroll
+                    for (int u = 0; u < S::kParts; ++u) {
+                        w.template fetch<true>(a, source, at, u, pages.p[u], off, kPart);
+                        off += kPart;
+                        if (off == a.page_size) off = 0;
+                    }
                 } else {
-                    skip &= ~(1u << stage);
-                    const int off = page_shift >= 0 ? key & (a.page_size - 1) : key % a.page_size;
-                    w.fetch(a, ring + stage * S::kBytes, page, kvh, off, len - key);
+#pragma unroll 1
+                    for (int u = 0; u < S::kParts; ++u) {
+                        const int k = key + u * kPart;
+                        int page = u == 0 ? pages.p[0] : pages.p[S::kParts - 1];
+                        if (k >= last) {
+                            page = 0;  // no key: zeros, from anywhere inside the pool
+                        } else if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.num_pages)) {
+                            if (lane == 0) atomicOr(&g_decode_error_word, 1u << kDevErrInvalidArg);
+                            skip |= 1u << (stage * S::kParts + u);
+                            page = 0;
+                        }
+                        const int valid = ((skip >> (stage * S::kParts + u)) & 1u) ? 0 : last - k;
+                        w.template fetch<false>(a, source, at, u, page, k % a.page_size, valid);
+                    }
                 }
             }
             cp_async_commit();
         };
-        int page;
+        Pages pages;
         {
-            int pages[C::kStages];  // all on their way before the first is used
+            Pages early[C::kStages];  // all on their way before the first is used
 #pragma unroll
-            for (int i = 0; i < C::kStages; ++i) pages[i] = page_at(i);
+            for (int i = 0; i < C::kStages; ++i) early[i] = pages_at(i);
 #pragma unroll
-            for (int i = 0; i < C::kStages - 1; ++i) start(i, pages[i]);
-            page = pages[C::kStages - 1];
+            for (int i = 0; i < C::kStages - 1; ++i) start(i, early[i]);
+            pages = early[C::kStages - 1];
         }
         w.load_q(a, b, kvh, rb);
         for (int i = 0; i < turns; ++i) {
-            start(i + C::kStages - 1, page);
-            page = page_at(i + C::kStages);  // needed one turn later
+            start(i + C::kStages - 1, pages);
+            pages = pages_at(i + C::kStages);  // needed one turn later
             cp_async_wait<C::kStages - 1>();
             __syncwarp();
             const int stage = i % C::kStages;
-            const int key = first + i * kUnit;
-            if (!((skip >> stage) & 1u)) w.keys(ring + stage * S::kBytes, key, key + kKeys > min_end, ends);
+            const int key = first + i * S::kUnit;
+            const uint32_t none = (skip >> (stage * S::kParts)) & ((1u << S::kParts) - 1u);
+            w.keys(ring + stage * S::kBytes, key, key + S::kKeys > min_end || none != 0u, none, ends);
             __syncwarp();  // every lane is done with the stage before it is filled again
         }
         cp_async_wait<0>();

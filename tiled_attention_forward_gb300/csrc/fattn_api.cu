@@ -141,7 +141,7 @@ int validate_cache(int64_t num_pages, int64_t page_size, int64_t Hkv, int64_t D,
     if (Hkv <= 0 || num_pages < 0 || page_size <= 0 || D < 0) return FATTN_ERR_INVALID_ARG;
     if (dtype == FATTN_F32 || (D != 64 && D != 128)) return FATTN_ERR_UNSUPPORTED;
     if (page_size % 16 != 0 || page_size > 65536) return FATTN_ERR_UNSUPPORTED;
-    if (num_pages > 0x7fffffffll || Hkv > (int64_t(1) << 16) ||
+    if (num_pages > 0x7fffffffll || Hkv > (int64_t(1) << 16) || Hkv * page_size > (int64_t(1) << 30) ||
         num_pages * page_size > kMaxElements / (Hkv * D))
         return FATTN_ERR_UNSUPPORTED;
     return FATTN_OK;
