@@ -46,6 +46,8 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kPart = 16;                 // keys that lie in one page and take one pass of the products
 constexpr int kMaxCtas = 320;             // parts in the workspace: two per CTA
 constexpr int kMaxParts = 64;             // CTAs a sequence is cut between: one CTA joins the parts
+constexpr float kLow = -3.0e38f;          // the running max of a row that has seen no key
+constexpr int kTargetCost = 4;            // what starting and joining a target costs, in units
 constexpr float kRescaleThreshold = 8.0f; // log2 units: P <= 2^8 while the max is stale
 
 // ---- instructions ----------------------------------------------------------
@@ -140,7 +142,8 @@ struct Config {
     static constexpr int kRows = 8 * NT;
     static constexpr int kRing = kWarps * kStages * Stage<D, KV4, NT>::kBytes;
     // The warps' O is joined in the same memory.
-    static constexpr int kJoin = kWarps * kRows * D * 4;
+    static constexpr int kPitch = D + 4;  // of a row of O there
+    static constexpr int kJoin = kWarps * kRows * kPitch * 4;
     static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
     static_assert(kSmem * kCtasPerSm <= 224 * 1024, "shared memory budget");
 };
@@ -198,12 +201,12 @@ __device__ __forceinline__ void store_out(const DecodeArgs& a, int b, int kvh, i
     const int share = a.H / a.Hkv;
     if (row >= share * a.Nq) return;
     const int h = kvh * share + row / a.Nq, i = row % a.Nq;
-    const float inv = mx == -INFINITY ? 0.f : 1.f / sum;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // 0: the row sees no key
     uint16_t* o = static_cast<uint16_t*>(a.o) + b * a.o_bs + h * a.o_hs + i * a.o_ns + d;
     *reinterpret_cast<uint2*>(o) =
         make_uint2(pack16<BF16>(acc[0] * inv, acc[1] * inv), pack16<BF16>(acc[2] * inv, acc[3] * inv));
     if (d == 0 && a.lse != nullptr)
-        a.lse[(static_cast<int64_t>(b) * a.H + h) * a.Nq + i] = mx == -INFINITY ? -INFINITY : (mx + log2f(sum)) * kLn2;
+        a.lse[(static_cast<int64_t>(b) * a.H + h) * a.Nq + i] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
 }
 
 // ---- one warp's keys ----------------------------------------------------------
@@ -286,7 +289,7 @@ struct Warp {
                 f[n][0] = __shfl_sync(0xffffffffu, down, 8 * t);
                 f[n][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
             }
-            m[n][0] = m[n][1] = -INFINITY;
+            m[n][0] = m[n][1] = kLow;
             l[n][0] = l[n][1] = 0.f;
 #pragma unroll
             for (int j = 0; j < kQ; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.f;
@@ -464,36 +467,33 @@ struct Warp {
                 for (int n = 0; n < NT; ++n) mma16816<BF16>(o[n][j], v, p[n][0], p[n][1]);
             }
         } else {
-            // Lane (g, t) takes keys 2t, 2t+1, 2t+8, 2t+9, dims 16 j + 8 u + g.  Two
-            // keys' 16-bit halves side by side are 4 pairs of codes, each made
-            // fp16 by setting exponent bits (1024 + c, or 64 + c where the code
-            // sits 4 bits higher), taking that off again (exact), and one fused
-            // c scale + zero.
+            // ldmatrix, transposed, on the codes' 16-bit pieces (4 codes each): lane
+            // (g, t) gets piece g of a 16-byte chunk for keys 2t and 2t+1 side by
+            // side, 4 pairs of codes.  Each pair is made fp16 by setting exponent
+            // bits (1024 + c, or 64 + c where the code sits 4 bits higher), taking
+            // that off again (exact), and one fused c scale + zero.  Which dims the
+            // lane's rows of O^T are is dim_of().
             const int g = lane / 4, t = lane % 4;
-            constexpr int kHalves = D / 32;                      // 16-bit pieces of a key that this lane takes
-            uint32_t x[2][kHalves];                              // [key pair][piece]
-            uint32_t sc[2][D / 32], ze[2][D / 32];
+            uint32_t x[2][D / 32];                   // [keys 0-7, 8-15][chunk]
+            const uint32_t row = base + ((lane & 7) + (lane & 8)) * S::kVRow + (lane >> 4) * 16;
+#pragma unroll
+            for (int c = 0; c < D / 32; c += 2) {
+                uint32_t y[4];
+                ldmatrix4_trans(y, row + c * 16);
+                x[0][c] = y[0];
+                x[1][c] = y[1];
+                x[0][c + 1] = y[2];
+                x[1][c + 1] = y[3];
+            }
+            uint32_t sc[2][2], ze[2][2];             // of the two groups that this lane's dims lie in
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const uint32_t k0 = base + (2 * t + 8 * u) * S::kVRow, k1 = k0 + S::kVRow;
-                if constexpr (D == 128) {
-                    uint32_t w0[2], w1[2];
-                    lds_words(w0, k0 + 8 * g);
-                    lds_words(w1, k1 + 8 * g);
-                    x[u][0] = __byte_perm(w0[0], w1[0], 0x5410);  // u-half 0: j = 0..3
-                    x[u][1] = __byte_perm(w0[0], w1[0], 0x7632);  //           j = 4..7
-                    x[u][2] = __byte_perm(w0[1], w1[1], 0x5410);  // u-half 1: j = 0..3
-                    x[u][3] = __byte_perm(w0[1], w1[1], 0x7632);  //           j = 4..7
-                } else {
-                    const uint32_t w0 = lds_word(k0 + 4 * g), w1 = lds_word(k1 + 4 * g);
-                    x[u][0] = __byte_perm(w0, w1, 0x5410);        // half 0, j = 0..3
-                    x[u][1] = __byte_perm(w0, w1, 0x7632);        // half 1, j = 0..3
-                }
-                uint32_t m0[D / 32], m1[D / 32];
-                lds_words(m0, k0 + S::kCode);
-                lds_words(m1, k1 + S::kCode);
+                const uint32_t at = base + (2 * t + 8 * u) * S::kVRow + S::kCode + (D == 128 ? 8 * (g & 1) : 0);
+                uint32_t m0[2], m1[2];
+                lds_words(m0, at);
+                lds_words(m1, at + S::kVRow);
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
+                for (int i = 0; i < 2; ++i) {
                     sc[u][i] = __byte_perm(m0[i], m1[i], 0x5410);
                     ze[u][i] = __byte_perm(m0[i], m1[i], 0x7632);
                 }
@@ -502,20 +502,28 @@ struct Warp {
             for (int j = 0; j < kQ; ++j) {
                 uint32_t v[4];
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
+                for (int u = 0; u < 2; ++u) {
+                    const uint32_t piece = (j & 1) ? x[u][j / 2] >> 8 : x[u][j / 2];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const uint32_t piece = x[u][D == 128 ? 2 * h + j / 4 : h];
-                        const uint32_t part = (j & 2) ? piece >> 8 : piece;
-                        const uint32_t up = (j & 1) ? ((part & 0x00f000f0u) | 0x54005400u)
-                                                    : ((part & 0x000f000fu) | 0x64006400u);
-                        const __half2 c = __hsub2(as_half2(up), as_half2((j & 1) ? 0x54005400u : 0x64006400u));
-                        v[2 * u + h] = as_u32(__hfma2(c, as_half2(sc[u][j / 2]), as_half2(ze[u][j / 2])));
+                        const uint32_t magic = h ? 0x54005400u : 0x64006400u;
+                        const uint32_t up = (piece & (h ? 0x00f000f0u : 0x000f000fu)) | magic;
+                        const __half2 c = __hsub2(as_half2(up), as_half2(magic));
+                        v[2 * u + h] = as_u32(__hfma2(c, as_half2(sc[u][j & 1]), as_half2(ze[u][j & 1])));
                     }
+                }
 #pragma unroll
                 for (int n = 0; n < NT; ++n) mma16816<false>(o[n][j], v, p[n][0], p[n][1]);
             }
         }
+    }
+
+    // The dim that row g + 8 h of m-tile j of O^T is.
+    static __device__ __forceinline__ int dim_of(int j, int h, int g) {
+        if (!KV4) return 16 * j + 8 * h + g;
+        const int q = 2 * (j & 1) + h, c = j / 2;  // nibble of the piece, 16-byte chunk
+        return D == 128 ? 16 * (4 * (g & 1) + q) + 8 * ((g >> 1) & 1) + 2 * c + (g >> 2)
+                        : 16 * q + 8 * (g & 1) + 4 * c + (g >> 1);
     }
 
     // The stage's keys: `key` is the first one's index, ends[n][x] the number of
@@ -557,7 +565,7 @@ struct Warp {
 #pragma unroll
                     for (int d = 4; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
                     const float mn = fmaxf(m[n][x], top);
-                    const float alpha = mn == -INFINITY ? 1.f : ex2(m[n][x] - mn);
+                    const float alpha = ex2(m[n][x] - mn);
                     m[n][x] = mn;
                     l[n][x] *= alpha;
 #pragma unroll
@@ -572,9 +580,8 @@ struct Warp {
             uint32_t p[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const float m0 = m[n][0] == -INFINITY ? 0.f : m[n][0], m1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
-                const float p0 = ex2(s[u][n][0] - m0), p1 = ex2(s[u][n][1] - m1);
-                const float p2 = ex2(s[u][n][2] - m0), p3 = ex2(s[u][n][3] - m1);
+                const float p0 = ex2(s[u][n][0] - m[n][0]), p1 = ex2(s[u][n][1] - m[n][1]);
+                const float p2 = ex2(s[u][n][2] - m[n][0]), p3 = ex2(s[u][n][3] - m[n][1]);
                 l[n][0] += p0 + p2;
                 l[n][1] += p1 + p3;
                 // P rounded to the operands' type (fp16 beside 4-bit values), key by
@@ -604,11 +611,14 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
     const int row_blocks = (rows + C::kRows - 1) / C::kRows;
     const int per_key = a.Hkv * row_blocks;  // targets of one sequence
 
-    // All units of the call, and this CTA's share of them.
+    // All units of the call, and this CTA's share of them.  A target (K/V head
+    // and row block of a sequence) counts kTargetCost units more than it has, so
+    // that shares of many short sequences take no longer than others.
     int64_t mine = 0;
-    int most = 0;
+    int most = 0, first_cost = 0;
     for (int b = tid; b < a.B; b += kThreads) {
-        const int n = units_of<S::kUnit>(visible_len(a, b, blockIdx.x == 0));
+        const int n = units_of<S::kUnit>(visible_len(a, b, blockIdx.x == 0)) + kTargetCost;
+        if (b == tid) first_cost = n;
         mine += n;
         most = max(most, n);
     }
@@ -640,7 +650,10 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
     for (int b0 = 0;; b0 += kThreads) {
         __syncthreads();  // s_scan is read by all before it is written again
         const int b = b0 + tid;
-        const int64_t own = b < a.B ? static_cast<int64_t>(units_of<S::kUnit>(visible_len(a, b, false))) * per_key : 0;
+        int64_t own = 0;
+        if (b < a.B)
+            own = static_cast<int64_t>(b0 == 0 ? first_cost
+                                               : units_of<S::kUnit>(visible_len(a, b, false)) + kTargetCost) * per_key;
         int64_t x = own;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
@@ -672,13 +685,27 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
     const bool one_page = a.page_size % S::kKeys == 0;  // a stage never crosses pages
     Warp<D, BF16, KV4, NT> w;
     int64_t at = begin;
+    int next_b = b;
     while (at < end) {
         const int len = visible_len(a, b, false);
         const int tiles = units_of<S::kUnit>(len);
+        const int cost = tiles + kTargetCost;
         const int64_t in_seq = at - seq_at;
-        const int target = static_cast<int>(in_seq / tiles);  // K/V head and row block
-        const int t0 = static_cast<int>(in_seq - static_cast<int64_t>(target) * tiles);
-        const int t1 = static_cast<int>(min(static_cast<int64_t>(tiles), t0 + (end - at)));
+        const int target = static_cast<int>(in_seq / cost);  // K/V head and row block
+        const int place = static_cast<int>(in_seq - static_cast<int64_t>(target) * cost);
+        const int taken = static_cast<int>(min(static_cast<int64_t>(cost - place), end - at));
+        // The extra units come first; tiles [t0, t1) are this CTA's.
+        const int t0 = max(place - kTargetCost, 0), t1 = place + taken - kTargetCost;
+        const int64_t target_at = at - place;  // the target's first unit
+        at += taken;
+        if (at - seq_at == static_cast<int64_t>(cost) * per_key) {
+            seq_at = at;
+            ++next_b;
+        }
+        if (t1 <= t0) {
+            b = next_b;
+            continue;
+        }
         const int kvh = target / row_blocks, rb = target - kvh * row_blocks;
         const int32_t* table = a.block_table + b * a.table_width;
 
@@ -777,7 +804,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
 
         // Join the eight warps: their O by rows, in the ring's memory.
         __syncthreads();
-        float* so = reinterpret_cast<float*>(smem) + warp * C::kRows * D;
+        float* so = reinterpret_cast<float*>(smem) + warp * C::kRows * C::kPitch;
         {
             const int g = lane / 4, t = lane % 4;
 #pragma unroll
@@ -794,14 +821,14 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
                     }
 #pragma unroll
                     for (int j = 0; j < D / 16; ++j) {
-                        so[r * D + 16 * j + g] = w.o[n][j][x];
-                        so[r * D + 16 * j + 8 + g] = w.o[n][j][x + 2];
+                        so[r * C::kPitch + w.dim_of(j, 0, g)] = w.o[n][j][x];
+                        so[r * C::kPitch + w.dim_of(j, 1, g)] = w.o[n][j][x + 2];
                     }
                 }
         }
         __syncthreads();
         const bool whole = t0 == 0 && t1 == tiles;
-        const int slot = 2 * cta + (at == begin ? 0 : 1);
+        const int slot = 2 * cta + (target_at <= begin ? 0 : 1);
         float* part = part_of<D>(a.workspace, slot, C::kRows);
         for (int x = tid; x < C::kRows * D / 4; x += kThreads) {
             const int r = x / (D / 4), d = 4 * (x % (D / 4));
@@ -811,10 +838,10 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
             float sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int y = 0; y < kWarps; ++y) {
-                const float wt = s_m[y][r] == -INFINITY ? 0.f : ex2(s_m[y][r] - mx);
+                const float wt = ex2(s_m[y][r] - mx);
                 sum = fmaf(wt, s_l[y][r], sum);
                 const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem) +
-                                                                  (y * C::kRows + r) * D + d);
+                                                                  (y * C::kRows + r) * C::kPitch + d);
                 acc[0] = fmaf(wt, v.x, acc[0]);
                 acc[1] = fmaf(wt, v.y, acc[1]);
                 acc[2] = fmaf(wt, v.z, acc[2]);
@@ -831,10 +858,9 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
             }
         }
         if (!whole) {
-            const int64_t from = at - t0;  // the target's first unit
-            const int c0 = t0 == 0 ? cta : cta_of(from, units, ctas);
-            const int parts = cta_of(from + tiles - 1, units, ctas) - c0 + 1;
-            const int slot0 = 2 * c0 + (from == share_begin(units, c0, ctas) ? 0 : 1);
+            const int c0 = t0 == 0 ? cta : cta_of(target_at + kTargetCost, units, ctas);
+            const int parts = cta_of(target_at + cost - 1, units, ctas) - c0 + 1;
+            const int slot0 = 2 * c0 + (target_at <= share_begin(units, c0, ctas) ? 0 : 1);
             unsigned long long* word = arrivals_of(a.workspace) + c0;
             __threadfence();  // this thread's part, before the arrival
             __syncthreads();
@@ -847,7 +873,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
                 __threadfence();
                 for (int x = tid; x < C::kRows * D / 4; x += kThreads) {
                     const int r = x / (D / 4), d = 4 * (x % (D / 4));
-                    float mx = -INFINITY, sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+                    float mx = kLow, sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
                     constexpr int kAtOnce = 4;
                     for (int y0 = 0; y0 < parts; y0 += kAtOnce) {
                         float pm[kAtOnce], pl[kAtOnce];
@@ -862,7 +888,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
                         }
 #pragma unroll
                         for (int y = 0; y < kAtOnce; ++y) {
-                            if (y0 + y >= parts || pm[y] == -INFINITY) continue;
+                            if (y0 + y >= parts) continue;
                             const float mn = fmaxf(mx, pm[y]);
                             const float wo = ex2(mx - mn), wt = ex2(pm[y] - mn);
                             mx = mn;
@@ -878,11 +904,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
             }
         }
         __syncthreads();  // the joined memory becomes the ring again
-        at += t1 - t0;
-        if (t1 == tiles && at - seq_at == static_cast<int64_t>(tiles) * per_key) {
-            seq_at = at;
-            ++b;
-        }
+        b = next_b;
     }
 }
 
