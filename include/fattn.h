@@ -369,7 +369,7 @@ FATTN_API int fattn_fwd_packed(const void* q, const void* k, const void* v, void
  *              q_out, k_out (entries of NULL tensors are ignored).
  *   k_pages, v_pages, page_stride, num_pages, page_size : the cache (above).
  *   slots    : device int64 [T].  Token t goes to slots[t]; a negative slot
- *              skips the token: nothing of it is read or written (padding of a
+ *              skips the token: nothing of it is written or used (padding of a
  *              batch).  A slot past the cache is an index out of range.  Slots
  *              of one call must differ; where two tokens share one, that slot
  *              holds a mixture of their rows.

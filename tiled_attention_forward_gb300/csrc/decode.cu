@@ -47,7 +47,6 @@ constexpr int kPart = 16;                 // keys that lie in one page and take 
 constexpr int kMaxCtas = 320;             // parts in the workspace: two per CTA
 constexpr int kMaxParts = 64;             // CTAs a sequence is cut between: one CTA joins the parts
 constexpr float kLow = -3.0e38f;          // the running max of a row that has seen no key
-constexpr int kTargetCost = 4;            // what starting and joining a target costs, in units
 constexpr float kRescaleThreshold = 8.0f; // log2 units: P <= 2^8 while the max is stale
 
 // ---- instructions ----------------------------------------------------------
@@ -138,8 +137,10 @@ struct Stage {
 template <int D, bool KV4, int NT>
 struct Config {
     static constexpr int kStages = KV4 ? (NT == 1 ? 2 : 4) : 3;
-    static constexpr int kCtasPerSm = NT == 4 || (!KV4 && D == 128) ? 1 : 2;
+    static constexpr int kCtasPerSm = NT == 4 || (D == 128 && (NT == 2 || !KV4)) ? 1 : 2;
     static constexpr int kRows = 8 * NT;
+    // What starting and joining a target costs, in units of keys.
+    static constexpr int kTargetCost = KV4 ? 2 : 4;
     static constexpr int kRing = kWarps * kStages * Stage<D, KV4, NT>::kBytes;
     // The warps' O is joined in the same memory.
     static constexpr int kPitch = D + 4;  // of a row of O there
@@ -612,12 +613,12 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
     const int per_key = a.Hkv * row_blocks;  // targets of one sequence
 
     // All units of the call, and this CTA's share of them.  A target (K/V head
-    // and row block of a sequence) counts kTargetCost units more than it has, so
+    // and row block of a sequence) counts C::kTargetCost units more than it has, so
     // that shares of many short sequences take no longer than others.
     int64_t mine = 0;
     int most = 0, first_cost = 0;
     for (int b = tid; b < a.B; b += kThreads) {
-        const int n = units_of<S::kUnit>(visible_len(a, b, blockIdx.x == 0)) + kTargetCost;
+        const int n = units_of<S::kUnit>(visible_len(a, b, blockIdx.x == 0)) + C::kTargetCost;
         if (b == tid) first_cost = n;
         mine += n;
         most = max(most, n);
@@ -653,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
         int64_t own = 0;
         if (b < a.B)
             own = static_cast<int64_t>(b0 == 0 ? first_cost
-                                               : units_of<S::kUnit>(visible_len(a, b, false)) + kTargetCost) * per_key;
+                                               : units_of<S::kUnit>(visible_len(a, b, false)) + C::kTargetCost) * per_key;
         int64_t x = own;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
@@ -689,13 +690,13 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
     while (at < end) {
         const int len = visible_len(a, b, false);
         const int tiles = units_of<S::kUnit>(len);
-        const int cost = tiles + kTargetCost;
+        const int cost = tiles + C::kTargetCost;
         const int64_t in_seq = at - seq_at;
         const int target = static_cast<int>(in_seq / cost);  // K/V head and row block
         const int place = static_cast<int>(in_seq - static_cast<int64_t>(target) * cost);
         const int taken = static_cast<int>(min(static_cast<int64_t>(cost - place), end - at));
         // The extra units come first; tiles [t0, t1) are this CTA's.
-        const int t0 = max(place - kTargetCost, 0), t1 = place + taken - kTargetCost;
+        const int t0 = max(place - C::kTargetCost, 0), t1 = place + taken - C::kTargetCost;
         const int64_t target_at = at - place;  // the target's first unit
         at += taken;
         if (at - seq_at == static_cast<int64_t>(cost) * per_key) {
@@ -858,7 +859,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
             }
         }
         if (!whole) {
-            const int c0 = t0 == 0 ? cta : cta_of(target_at + kTargetCost, units, ctas);
+            const int c0 = t0 == 0 ? cta : cta_of(target_at + C::kTargetCost, units, ctas);
             const int parts = cta_of(target_at + cost - 1, units, ctas) - c0 + 1;
             const int slot0 = 2 * c0 + (target_at <= share_begin(units, c0, ctas) ? 0 : 1);
             unsigned long long* word = arrivals_of(a.workspace) + c0;
@@ -874,7 +875,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
                 for (int x = tid; x < C::kRows * D / 4; x += kThreads) {
                     const int r = x / (D / 4), d = 4 * (x % (D / 4));
                     float mx = kLow, sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-                    constexpr int kAtOnce = 4;
+                    constexpr int kAtOnce = 8;
                     for (int y0 = 0; y0 < parts; y0 += kAtOnce) {
                         float pm[kAtOnce], pl[kAtOnce];
                         float4 v[kAtOnce];

@@ -812,7 +812,7 @@ int run_append(AppendArgs& a, const int64_t* strides, int64_t num_pages, int64_t
     a.H = static_cast<int>(H);
     a.Hkv = static_cast<int>(Hkv);
     a.rot = static_cast<int>(rot);
-    const cudaError_t e = append_launch(a, static_cast<int>(D), dtype == FATTN_BF16, kv4,
+    const cudaError_t e = append_launch(a, static_cast<int>(D), dtype == FATTN_BF16, kv4, sms,
                                         reinterpret_cast<cudaStream_t>(stream_h));
     return e == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
 }
