@@ -366,7 +366,7 @@ FATTN_API int fattn_fwd_packed(const void* q, const void* k, const void* v, void
  *   q_out    : [T, H, D], the rotated q; NULL only when q is NULL.
  *   k_out    : [T, Hkv, D], k as the cache holds it; may be NULL.
  *   strides  : host array of 10: token stride and head stride of q, k, v,
- *              q_out, k_out (entries of NULL tensors are ignored).
+ *              q_out, k_out (entries of NULL tensors are ignored), below 2^31.
  *   k_pages, v_pages, page_stride, num_pages, page_size : the cache (above).
  *   slots    : device int64 [T].  Token t goes to slots[t]; a negative slot
  *              skips the token: nothing of it is written or used (padding of a
@@ -378,8 +378,8 @@ FATTN_API int fattn_fwd_packed(const void* q, const void* k, const void* v, void
  *   rot      : elements of each row that turn, a multiple of 16, 0..D; 0 = no
  *              rotation (pos, cos and sin are ignored).
  *   interleaved : 0 = element i turns with element i + rot/2, otherwise 2i with 2i+1:
- *              (a, b) -> (a cos - b sin, b cos + a sin) in fp32, each product
- *              and sum rounded, the result rounded once to `dtype`.
+ *              (a, b) -> (a cos - b sin, b cos + a sin) in fp32, the result
+ *              rounded once to `dtype`.
  *
  * An output may be its own input (same pointer and strides); any other overlap
  * among inputs, outputs and cache -> FATTN_ERR_INVALID_ARG.  One launch.

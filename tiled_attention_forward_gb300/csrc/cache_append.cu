@@ -88,103 +88,117 @@ __device__ __forceinline__ uint32_t transpose_nibbles(uint32_t x, int lane) {
     return x;
 }
 
-// Four codes (floats 0..15) as 16 bits, nibble by nibble: exact in fp32.
-__device__ __forceinline__ uint32_t pack_codes(float a, float b, float c, float d) {
-    return static_cast<uint32_t>(fmaf(d, 4096.f, fmaf(c, 256.f, fmaf(b, 16.f, a))));
+// (d0, d1) = (a0, a1) * (b0, b1) [+ (c0, c1)]: two fp32 results an instruction.
+__device__ __forceinline__ void mul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b0, float b1, float c0, float c1) {
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
 }
 
-// Quantises this thread's 8 elements (4 threads hold a group): its codes,
-// scale and zero.
-__device__ __forceinline__ void quantise(const float (&x)[8], float (&code)[8], __half& scale, __half& zero) {
-    float y[8];
-    float lo = kFp16Max, hi = -kFp16Max;
+// Quantises this thread's 8 elements (4 threads hold a group): its codes as the
+// floats 2^23 + code (whose low bits are the code), scale and zero.  A NaN takes
+// no part in the range (min and max drop it) and gets code 0 (so does .sat);
+// values past the fp16 range get the codes of its ends.
+__device__ __forceinline__ void quantise(const float (&x)[8], float (&t)[8], __half& scale, __half& zero) {
+    float lo = x[0], hi = x[0];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        y[e] = x[e] > kFp16Max ? kFp16Max : (x[e] < -kFp16Max ? -kFp16Max : x[e]);
-        lo = fminf(lo, y[e]);  // a NaN takes no part, and gets code 0 below
-        hi = fmaxf(hi, y[e]);
+    for (int e = 1; e < 8; ++e) {
+        lo = fminf(lo, x[e]);
+        hi = fmaxf(hi, x[e]);
     }
 #pragma unroll
     for (int m = 1; m <= 2; m <<= 1) {
         lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, m));
         hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, m));
     }
-    if (lo > hi) lo = hi = 0.f;  // nothing but NaN
+    if (!(lo <= hi)) lo = hi = 0.f;  // nothing but NaN
+    lo = fminf(fmaxf(lo, -kFp16Max), kFp16Max);
+    hi = fminf(fmaxf(hi, -kFp16Max), kFp16Max);
     scale = __float2half_rn((hi - lo) / 15.f);
     zero = __float2half_rn(lo);
     const float s = __half2float(scale), z = __half2float(zero);
-    const float inv = s > 0.f ? 1.f / s : 0.f;
+    const float inv = s > 0.f ? 1.f / (15.f * s) : 0.f;  // 15 s is exact
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        // Adding 2^23 rounds to the nearest whole number, ties to even.
-        const float c = fminf(fmaxf((y[e] - z) * inv, 0.f), 15.f);
-        code[e] = __fsub_rn(__fadd_rn(c, 8388608.f), 8388608.f);
-    }
+    for (int e = 0; e < 8; ++e)  // adding 2^23 rounds to the nearest whole number, ties to even
+        t[e] = fmaf(__saturatef((x[e] - z) * inv), 15.f, 8388608.f);
 }
 
-// One row's 8 elements: rotation, outputs, cache.  Whole warps call it.
+// Nibbles e = 0..7 from t[0..7] = 2^23 + code: a sum in 32-bit integers, from
+// which the exponents' share is taken off.
+__device__ __forceinline__ uint32_t pack_codes(float t0, float t1, float t2, float t3, float t4, float t5, float t6, float t7) {
+    const float t[8] = {t0, t1, t2, t3, t4, t5, t6, t7};
+    uint32_t w = __float_as_uint(t[7]);
+#pragma unroll
+    for (int e = 6; e >= 0; --e) w = w * 16u + __float_as_uint(t[e]);
+    return w - 0x4b000000u * 0x11111111u;
+}
+
+// Where an item (a row of a token) is.
+struct Item {
+    int tl;  // token within the block
+    int r;   // row: query heads, key heads, value heads
+};
+
+// One row's 8 elements: rotation, outputs, cache.  Whole warps call it, with
+// lanes that are not `on` repeating some row.  cs: the token's angles, four
+// 16-byte pieces for each of this thread's positions c, kChunks pieces apart.
 template <int D, bool BF16, bool KV4>
-__device__ __forceinline__ void append_row(const AppendArgs& a, const uint4& raw, int64_t t, int r, bool on, int64_t page, int off,
-                                           const float* cs) {
+__device__ __forceinline__ void append_row(const AppendArgs& a, const uint4& raw, uint32_t t, int r, bool on, int64_t page,
+                                           int off, const float4* cs) {
     constexpr int kChunks = D / 8;
     const int c = threadIdx.x % kChunks, lane = threadIdx.x % 32;
     const bool is_q = r < a.H;
     const bool is_k = !is_q && r < a.H + a.Hkv;
-    const bool is_v = !is_q && !is_k;
     const int h = is_q ? r : (is_k ? r - a.H : r - a.H - a.Hkv);
+    uint4 rounded = raw;
     float x[8];
     unpack8<BF16>(raw, x);
-    // Rotation (q and k rows): the pair's first half is chunk c < rot/16, its
-    // second the chunk rot/16 further; interleaved pairs lie within a chunk.
-    // Products and sums are rounded one by one.
-    const int half_chunks = a.rot / 16;
-    const bool turns = c < 2 * half_chunks && !is_v;
-    if (a.rot > 0) {
-        const float* sn = cs + a.rot / 2;
+    // Rotation (q and k rows).  Halves: chunk c < rot/16 holds the pairs' first
+    // elements, the chunk rot/16 further their second ones, and the sign of a
+    // sin - b cos comes with the angles.  Interleaved pairs lie within a chunk.
+    if (a.rot > 0 && __any_sync(0xffffffffu, is_q || is_k)) {
+        const int half_chunks = a.rot / 16;
+        const bool turns = c < 2 * half_chunks && (is_q || is_k);
+        float y[8];
         if (a.interleaved) {
-            if (turns) {
-                const float4 co = *reinterpret_cast<const float4*>(cs + 4 * c);
-                const float4 si = *reinterpret_cast<const float4*>(sn + 4 * c);
-                const float cv[4] = {co.x, co.y, co.z, co.w}, sv[4] = {si.x, si.y, si.z, si.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float p = x[2 * e], q = x[2 * e + 1];
-                    x[2 * e] = __fsub_rn(__fmul_rn(p, cv[e]), __fmul_rn(q, sv[e]));
-                    x[2 * e + 1] = __fadd_rn(__fmul_rn(q, cv[e]), __fmul_rn(p, sv[e]));
-                }
-            }
+            for (int e = 0; e < 8; ++e) y[e] = x[e ^ 1];
         } else {
-            const bool first = c < half_chunks;
-            const int partner = turns ? (first ? c + half_chunks : c - half_chunks) : c;
-            const int from = (lane & ~(kChunks - 1)) + partner;
+            const int from = lane - c + (turns ? (c < half_chunks ? c + half_chunks : c - half_chunks) : c);
             uint4 other;
             other.x = __shfl_sync(0xffffffffu, raw.x, from);
             other.y = __shfl_sync(0xffffffffu, raw.y, from);
             other.z = __shfl_sync(0xffffffffu, raw.z, from);
             other.w = __shfl_sync(0xffffffffu, raw.w, from);
-            if (turns) {
-                float y[8];
-                unpack8<BF16>(other, y);
-                const int i = 8 * (first ? c : c - half_chunks);
-                const float sg = first ? -1.f : 1.f;  // a' = a cos - b sin, b' = b cos + a sin
+            unpack8<BF16>(other, y);
+        }
+        if (turns) {
 #pragma unroll
-                for (int e = 0; e < 8; e += 4) {
-                    const float4 co = *reinterpret_cast<const float4*>(cs + i + e);
-                    const float4 si = *reinterpret_cast<const float4*>(sn + i + e);
-                    const float cv[4] = {co.x, co.y, co.z, co.w}, sv[4] = {si.x, si.y, si.z, si.w};
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        x[e + u] = __fadd_rn(__fmul_rn(x[e + u], cv[u]), __fmul_rn(y[e + u], sg * sv[u]));
-                }
+            for (int u = 0; u < 2; ++u) {
+                const float4 co = cs[(2 * u) * kChunks], si = cs[(2 * u + 1) * kChunks];
+                float z[4];
+                mul2(z[0], z[1], x[4 * u], x[4 * u + 1], co.x, co.y);
+                mul2(z[2], z[3], x[4 * u + 2], x[4 * u + 3], co.z, co.w);
+                fma2(x[4 * u], x[4 * u + 1], y[4 * u], y[4 * u + 1], si.x, si.y, z[0], z[1]);
+                fma2(x[4 * u + 2], x[4 * u + 3], y[4 * u + 2], y[4 * u + 3], si.z, si.w, z[2], z[3]);
             }
+            rounded = pack8<BF16>(x);
         }
     }
-    uint4 rounded = turns ? pack8<BF16>(x) : raw;
-    if (on && is_q) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.q_out) + t * a.qo_ts + h * a.qo_hs + 8 * c) = rounded;
+    if (on && is_q)
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.q_out) + static_cast<uint64_t>(t) * a.qo_ts +
+                                  static_cast<uint64_t>(static_cast<uint32_t>(h)) * a.qo_hs + 8 * c) = rounded;
     // What follows is for key and value rows: query rows are most of them, and
     // whole warps of them leave here.
-    if (!__any_sync(0xffffffffu, on && !is_q)) return;
     const bool kv = on && !is_q;
+    if (!__any_sync(0xffffffffu, kv)) return;
     if constexpr (KV4) {
         __half scale, zero;
         float code[8];
@@ -193,24 +207,22 @@ __device__ __forceinline__ void append_row(const AppendArgs& a, const uint4& raw
         if (__any_sync(0xffffffffu, is_k)) {
             // K: element e = 2 l + u of the chunk at nibble l + 4 u, so that a word's
             // even and odd elements unpack as 16-bit pairs.
-            const uint32_t w = pack_codes(code[0], code[2], code[4], code[6]) |
-                               (pack_codes(code[1], code[3], code[5], code[7]) << 16);
+            const uint32_t w = pack_codes(code[0], code[2], code[4], code[6], code[1], code[3], code[5], code[7]);
             if (kv && is_k) static_cast<uint32_t*>(a.k_pages)[row * (D / 8) + (c % 4) * (D / 32) + c / 4] = w;
         }
-        if (__any_sync(0xffffffffu, is_v)) {
+        if (__any_sync(0xffffffffu, !is_k)) {
             // V: dim 16 j + 8 u + g (chunk 2 j + u, element g) at nibble j of word
             // 2 g + u (D = 128), nibble 4 u + j of word g (D = 64).
-            const uint32_t w = pack_codes(code[0], code[1], code[2], code[3]) |
-                               (pack_codes(code[4], code[5], code[6], code[7]) << 16);
+            const uint32_t w = pack_codes(code[0], code[1], code[2], code[3], code[4], code[5], code[6], code[7]);
             const uint32_t wt = D == 128 ? transpose_nibbles<2, 4, 8>(w, lane) : transpose_nibbles<2, 4, 1>(w, lane);
-            if (kv && is_v) static_cast<uint32_t*>(a.v_pages)[row * (D / 8) + (D == 128 ? c : 4 * (c & 1) + c / 2)] = wt;
+            if (kv && !is_k) static_cast<uint32_t*>(a.v_pages)[row * (D / 8) + (D == 128 ? c : 4 * (c & 1) + c / 2)] = wt;
         }
         if (kv && c % 4 == 0)
             static_cast<__half2*>(is_k ? a.k_scales : a.v_scales)[row * (D / 32) + c / 4] = __halves2half2(scale, zero);
         if (a.held) {
             const float s = __half2float(scale), z = __half2float(zero);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = fmaf(code[e], s, z);
+            for (int e = 0; e < 8; ++e) x[e] = fmaf(code[e] - 8388608.f, s, z);
             rounded = pack8<BF16>(x);
         }
     } else if (kv) {
@@ -218,10 +230,11 @@ __device__ __forceinline__ void append_row(const AppendArgs& a, const uint4& raw
         *reinterpret_cast<uint4*>(pages + page * a.page_stride + (static_cast<int64_t>(h) * a.page_size + off) * D + 8 * c) =
             rounded;
     }
-    if (kv && is_k && a.k_out != nullptr)
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.k_out) + t * a.ko_ts + h * a.ko_hs + 8 * c) = rounded;
-    if (kv && is_v && a.v_out != nullptr)
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.v_out) + t * a.vo_ts + h * a.vo_hs + 8 * c) = rounded;
+    void* out = is_k ? a.k_out : a.v_out;
+    if (kv && out != nullptr)
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + static_cast<uint64_t>(t) * (is_k ? a.ko_ts : a.vo_ts) +
+                                  static_cast<uint64_t>(static_cast<uint32_t>(h)) * (is_k ? a.ko_hs : a.vo_hs) + 8 * c) =
+            rounded;
 }
 
 template <int D, bool BF16, bool KV4>
@@ -230,38 +243,50 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
     constexpr int kLanes = kThreads / kChunks;      // rows in flight per block
     __shared__ int64_t s_page[kMaxTokens];          // -1: nothing of the token is written
     __shared__ int s_off[kMaxTokens];
-    __shared__ __align__(16) float s_cs[kMaxTokens][D];  // cos, then sin, of the tokens' positions
+    __shared__ float4 s_cs[kMaxTokens][4 * kChunks];
     const int c = threadIdx.x % kChunks;
     const int rlane = threadIdx.x / kChunks;
     const int rows = a.H + 2 * a.Hkv;
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * a.tokens;
+    const uint32_t first = blockIdx.x * static_cast<uint32_t>(a.tokens);
     const int tokens = static_cast<int>(min(static_cast<int64_t>(a.tokens), a.T - first));
-    const int items = tokens * rows;
 
-    uint4 raw[kAhead];
-    auto load = [&](int u, int item) {
-        raw[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (item < items) {
-            const int tl = item / rows, r = item - tl * rows;
-            const int64_t t = first + tl;
-            const uint16_t* src;
-            if (r < a.H)
-                src = static_cast<const uint16_t*>(a.q) + t * a.q_ts + r * a.q_hs;
-            else if (r < a.H + a.Hkv)
-                src = static_cast<const uint16_t*>(a.k) + t * a.k_ts + (r - a.H) * a.k_hs;
-            else
-                src = static_cast<const uint16_t*>(a.v) + t * a.v_ts + (r - a.H - a.Hkv) * a.v_hs;
-            raw[u] = *reinterpret_cast<const uint4*>(src + 8 * c);
+    // Items are dealt to the row lanes in turn; from one to a lane's next:
+    const int step_tl = kLanes / rows, step_r = kLanes - step_tl * rows;
+    auto next = [&](Item& x) {
+        x.tl += step_tl;
+        x.r += step_r;
+        if (x.r >= rows) {
+            x.r -= rows;
+            ++x.tl;
         }
     };
+    uint4 raw[kAhead];
+    Item ahead, now;
+    now.tl = rlane / rows;
+    now.r = rlane - now.tl * rows;
+    ahead = now;
+    auto load = [&](int u) {
+        raw[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (ahead.tl < tokens) {
+            const int r = ahead.r;
+            const bool is_q = r < a.H, is_k = r < a.H + a.Hkv;
+            const uint16_t* src = static_cast<const uint16_t*>(is_q ? a.q : (is_k ? a.k : a.v));
+            const uint32_t ts = is_q ? a.q_ts : (is_k ? a.k_ts : a.v_ts);
+            const uint32_t hs = is_q ? a.q_hs : (is_k ? a.k_hs : a.v_hs);
+            const uint32_t h = is_q ? r : (is_k ? r - a.H : r - a.H - a.Hkv);
+            raw[u] = *reinterpret_cast<const uint4*>(src + static_cast<uint64_t>(first + ahead.tl) * ts +
+                                                     static_cast<uint64_t>(h) * hs + 8 * c);
+        }
+        next(ahead);
+    };
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) load(u, rlane + u * kLanes);
+    for (int u = 0; u < kAhead; ++u) load(u);
 
-    // The tokens' angles: as many threads as fit take a token each (a warp or
-    // more for one token when there are few).
-    const int quarter = a.rot / 4;  // 16-byte pieces of a token's angles (cos and sin)
-    for (int x = threadIdx.x; x < tokens * max(quarter, 1); x += kThreads) {
-        const int tl = quarter > 0 ? x / quarter : x, e = quarter > 0 ? x - tl * quarter : 0;
+    // The tokens' places and angles: threads take a token each when nothing
+    // turns, else one chunk of one token's angles.
+    const int pieces = a.rot > 0 ? a.rot / 8 : 1;
+    for (int x = threadIdx.x; x < tokens * pieces; x += kThreads) {
+        const int tl = x / pieces, e = x - tl * pieces;
         int64_t slot = a.slots[first + tl];
         const int pos = a.rot > 0 ? a.pos[first + tl] : 0;
         if (slot >= 0 && (slot >= a.num_slots || (a.rot > 0 && (pos < 0 || pos >= a.max_pos)))) {
@@ -273,26 +298,42 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
             s_page[tl] = page;
             s_off[tl] = slot < 0 ? 0 : static_cast<int>(slot - page * a.page_size);
         }
-        if (slot >= 0 && quarter > 0) {
-            const float* table = e < quarter / 2 ? a.cos : a.sin;
-            const int at = 4 * (e < quarter / 2 ? e : e - quarter / 2);
-            *reinterpret_cast<float4*>(&s_cs[tl][4 * e]) =
-                *reinterpret_cast<const float4*>(table + static_cast<int64_t>(pos) * (a.rot / 2) + at);
+        if (slot >= 0 && a.rot > 0) {
+            const int64_t at = static_cast<int64_t>(pos) * (a.rot / 2);
+            if (a.interleaved) {  // pairs 4e .. 4e + 3, each angle for both elements
+                const float4 co = *reinterpret_cast<const float4*>(a.cos + at + 4 * e);
+                const float4 si = *reinterpret_cast<const float4*>(a.sin + at + 4 * e);
+                s_cs[tl][e] = make_float4(co.x, co.x, co.y, co.y);
+                s_cs[tl][kChunks + e] = make_float4(-si.x, si.x, -si.y, si.y);
+                s_cs[tl][2 * kChunks + e] = make_float4(co.z, co.z, co.w, co.w);
+                s_cs[tl][3 * kChunks + e] = make_float4(-si.z, si.z, -si.w, si.w);
+            } else {
+                const bool second = e >= a.rot / 16;
+                const int64_t i = at + 8 * (second ? e - a.rot / 16 : e);
+                const float sg = second ? 1.f : -1.f;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const float4 si = *reinterpret_cast<const float4*>(a.sin + i + 4 * u);
+                    s_cs[tl][2 * u * kChunks + e] = *reinterpret_cast<const float4*>(a.cos + i + 4 * u);
+                    s_cs[tl][(2 * u + 1) * kChunks + e] = make_float4(sg * si.x, sg * si.y, sg * si.z, sg * si.w);
+                }
+            }
         }
     }
     __syncthreads();
 
     // Every thread of a warp makes the same number of turns (shuffles inside).
-    for (int i = 0; i < items; i += kAhead * kLanes) {
+    const int turns = (tokens * rows + kLanes - 1) / kLanes;
+    for (int i = 0; i < turns; i += kAhead) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            const int item = i + u * kLanes + rlane;
-            if (i + u * kLanes < items) {
-                const int tl = min(item / rows, tokens - 1), r = item - tl * rows;
+            if (i + u < turns) {
+                const int tl = min(now.tl, tokens - 1);
                 const int64_t page = s_page[tl];
-                append_row<D, BF16, KV4>(a, raw[u], first + tl, min(r, rows - 1), item < items && page >= 0, page,
-                                         s_off[tl], s_cs[tl]);
-                load(u, item + kAhead * kLanes);
+                append_row<D, BF16, KV4>(a, raw[u], first + tl, now.r, now.tl < tokens && page >= 0, page, s_off[tl],
+                                         &s_cs[tl][c]);
+                next(now);
+                load(u);
             }
         }
     }

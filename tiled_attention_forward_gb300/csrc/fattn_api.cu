@@ -748,18 +748,18 @@ int run_append(AppendArgs& a, const int64_t* strides, int64_t num_pages, int64_t
     if (rot > 0 && (!a.pos || !a.cos || !a.sin || a.max_pos < 0)) return FATTN_ERR_INVALID_ARG;
     const void* rows[6] = {a.q, a.k, a.v, a.q_out, a.k_out, a.v_out};
     const int64_t heads[6] = {H, Hkv, Hkv, H, Hkv, Hkv};
-    int64_t* dst[6][2] = {{&a.q_ts, &a.q_hs},   {&a.k_ts, &a.k_hs},   {&a.v_ts, &a.v_hs},
+    uint32_t* dst[6][2] = {{&a.q_ts, &a.q_hs},   {&a.k_ts, &a.k_hs},   {&a.v_ts, &a.v_hs},
                           {&a.qo_ts, &a.qo_hs}, {&a.ko_ts, &a.ko_hs}, {&a.vo_ts, &a.vo_hs}};
     View views[6];
     for (int i = 0; i < 6; ++i) {
         if (!rows[i]) continue;
         const int64_t ts = strides[2 * i], hs = strides[2 * i + 1];
         if (!stride_ok(ts) || !stride_ok(hs)) return FATTN_ERR_INVALID_ARG;
-        if (T * ts > kMaxElements || heads[i] * hs > kMaxElements) return FATTN_ERR_UNSUPPORTED;
+        if (ts >= (int64_t(1) << 31) || hs >= (int64_t(1) << 31)) return FATTN_ERR_UNSUPPORTED;
         if (!aligned16(rows[i])) return FATTN_ERR_MISALIGNED;
         if (i >= 3 && ((T > 1 && ts < D) || (heads[i] > 1 && hs < D))) return FATTN_ERR_INVALID_ARG;
-        *dst[i][0] = ts;
-        *dst[i][1] = hs;
+        *dst[i][0] = static_cast<uint32_t>(ts);
+        *dst[i][1] = static_cast<uint32_t>(hs);
         views[i] = rows_view(rows[i], T, ts, heads[i], hs, D);
     }
     const int64_t page_rows = num_pages * page_size * Hkv;

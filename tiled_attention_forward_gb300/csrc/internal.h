@@ -157,8 +157,8 @@ struct AppendArgs {
     void* q_out;          // or nullptr
     void* k_out;
     void* v_out;
-    int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs;        // token and head strides, elements
-    int64_t qo_ts, qo_hs, ko_ts, ko_hs, vo_ts, vo_hs;
+    uint32_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs;        // token and head strides, elements
+    uint32_t qo_ts, qo_hs, ko_ts, ko_hs, vo_ts, vo_hs;
     void* k_pages;        // 16-bit [pages][Hkv][page_size][D], or codes [pages][Hkv][page_size][D/2] bytes
     void* v_pages;
     void* k_scales;       // 4-bit: fp16 [pages][Hkv][page_size][D/32][2]
