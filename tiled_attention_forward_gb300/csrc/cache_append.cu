@@ -16,11 +16,11 @@
 //
 // Work split: one thread moves 16 bytes (8 elements) of a row, D/8 threads a
 // row, so partner elements of a rotation pair and the 4 threads of a group
-// meet by shuffles within a warp.  A block takes the rows (query heads, key
-// heads, value heads) of one or a few tokens; a thread starts the loads of
-// kAhead of its rows before the tokens' slots, positions and angles (which
-// depend on one another) have come, and the angles go through shared memory
-// once for all heads.
+// meet by shuffles within a warp.  A block takes the query rows, or the key and
+// value rows, of one or a few tokens; a thread starts the loads of kAhead of
+// its rows before the tokens' slots, positions and angles (which depend on one
+// another) have come, and the angles go through shared memory once for all
+// heads.
 #include <algorithm>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -36,6 +36,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kAhead = 4;       // rows that a thread has on their way
+constexpr int kTurns = 8;       // rows that a thread takes, where there are enough
 constexpr int kMaxTokens = 16;  // tokens of a block
 constexpr float kFp16Max = 65504.f;
 
@@ -143,29 +144,37 @@ __device__ __forceinline__ uint32_t pack_codes(float t0, float t1, float t2, flo
 // Where an item (a row of a token) is.
 struct Item {
     int tl;  // token within the block
-    int r;   // row: query heads, key heads, value heads
+    int r;   // row: a query head, or key heads and then value heads
+};
+
+template <int D>
+struct Shared {
+    static constexpr int kChunks = D / 8;
+    int64_t page[kMaxTokens];  // -1: nothing of the token is written
+    int off[kMaxTokens];
+    // Each token's angles, as the thread of chunk c multiplies by them: cos of
+    // its first 4 elements, signed sin of them, then of its other 4.
+    float4 cs[kMaxTokens][4][kChunks];
 };
 
 // One row's 8 elements: rotation, outputs, cache.  Whole warps call it, with
-// lanes that are not `on` repeating some row.  cs: the token's angles, four
-// 16-byte pieces for each of this thread's positions c, kChunks pieces apart.
-template <int D, bool BF16, bool KV4>
+// lanes that are not `on` repeating some row.
+template <int D, bool BF16, bool KV4, bool QUERY>
 __device__ __forceinline__ void append_row(const AppendArgs& a, const uint4& raw, uint32_t t, int r, bool on, int64_t page,
                                            int off, const float4* cs) {
     constexpr int kChunks = D / 8;
     const int c = threadIdx.x % kChunks, lane = threadIdx.x % 32;
-    const bool is_q = r < a.H;
-    const bool is_k = !is_q && r < a.H + a.Hkv;
-    const int h = is_q ? r : (is_k ? r - a.H : r - a.H - a.Hkv);
+    const bool is_v = !QUERY && r >= a.Hkv;
+    const uint32_t h = is_v ? r - a.Hkv : r;
     uint4 rounded = raw;
     float x[8];
-    unpack8<BF16>(raw, x);
+    if (!QUERY || a.rot > 0) unpack8<BF16>(raw, x);
     // Rotation (q and k rows).  Halves: chunk c < rot/16 holds the pairs' first
     // elements, the chunk rot/16 further their second ones, and the sign of a
     // sin - b cos comes with the angles.  Interleaved pairs lie within a chunk.
-    if (a.rot > 0 && __any_sync(0xffffffffu, is_q || is_k)) {
+    if (a.rot > 0 && (QUERY || __any_sync(0xffffffffu, !is_v))) {
         const int half_chunks = a.rot / 16;
-        const bool turns = c < 2 * half_chunks && (is_q || is_k);
+        const bool turns = c < 2 * half_chunks && !is_v;
         float y[8];
         if (a.interleaved) {
 #pragma unroll
@@ -192,63 +201,57 @@ __device__ __forceinline__ void append_row(const AppendArgs& a, const uint4& raw
             rounded = pack8<BF16>(x);
         }
     }
-    if (on && is_q)
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.q_out) + static_cast<uint64_t>(t) * a.qo_ts +
-                                  static_cast<uint64_t>(static_cast<uint32_t>(h)) * a.qo_hs + 8 * c) = rounded;
-    // What follows is for key and value rows: query rows are most of them, and
-    // whole warps of them leave here.
-    const bool kv = on && !is_q;
-    if (!__any_sync(0xffffffffu, kv)) return;
+    auto out_row = [&](void* p, uint32_t ts, uint32_t hs) {
+        return reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + static_cast<uint64_t>(t) * ts +
+                                        static_cast<uint64_t>(h) * hs + 8 * c);
+    };
+    if constexpr (QUERY) {
+        if (on) *out_row(a.q_out, a.qo_ts, a.qo_hs) = rounded;
+        return;
+    }
     if constexpr (KV4) {
         __half scale, zero;
         float code[8];
         quantise(x, code, scale, zero);
         const int64_t row = (page * a.Hkv + h) * a.page_size + off;
-        if (__any_sync(0xffffffffu, is_k)) {
+        if (__any_sync(0xffffffffu, !is_v)) {
             // K: element e = 2 l + u of the chunk at nibble l + 4 u, so that a word's
             // even and odd elements unpack as 16-bit pairs.
             const uint32_t w = pack_codes(code[0], code[2], code[4], code[6], code[1], code[3], code[5], code[7]);
-            if (kv && is_k) static_cast<uint32_t*>(a.k_pages)[row * (D / 8) + (c % 4) * (D / 32) + c / 4] = w;
+            if (on && !is_v) static_cast<uint32_t*>(a.k_pages)[row * (D / 8) + (c % 4) * (D / 32) + c / 4] = w;
         }
-        if (__any_sync(0xffffffffu, !is_k)) {
+        if (__any_sync(0xffffffffu, is_v)) {
             // V: dim 16 j + 8 u + g (chunk 2 j + u, element g) at nibble j of word
             // 2 g + u (D = 128), nibble 4 u + j of word g (D = 64).
             const uint32_t w = pack_codes(code[0], code[1], code[2], code[3], code[4], code[5], code[6], code[7]);
             const uint32_t wt = D == 128 ? transpose_nibbles<2, 4, 8>(w, lane) : transpose_nibbles<2, 4, 1>(w, lane);
-            if (kv && !is_k) static_cast<uint32_t*>(a.v_pages)[row * (D / 8) + (D == 128 ? c : 4 * (c & 1) + c / 2)] = wt;
+            if (on && is_v) static_cast<uint32_t*>(a.v_pages)[row * (D / 8) + (D == 128 ? c : 4 * (c & 1) + c / 2)] = wt;
         }
-        if (kv && c % 4 == 0)
-            static_cast<__half2*>(is_k ? a.k_scales : a.v_scales)[row * (D / 32) + c / 4] = __halves2half2(scale, zero);
+        if (on && c % 4 == 0)
+            static_cast<__half2*>(is_v ? a.v_scales : a.k_scales)[row * (D / 32) + c / 4] = __halves2half2(scale, zero);
         if (a.held) {
             const float s = __half2float(scale), z = __half2float(zero);
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = fmaf(code[e] - 8388608.f, s, z);
             rounded = pack8<BF16>(x);
         }
-    } else if (kv) {
-        uint16_t* pages = static_cast<uint16_t*>(is_k ? a.k_pages : a.v_pages);
+    } else if (on) {
+        uint16_t* pages = static_cast<uint16_t*>(is_v ? a.v_pages : a.k_pages);
         *reinterpret_cast<uint4*>(pages + page * a.page_stride + (static_cast<int64_t>(h) * a.page_size + off) * D + 8 * c) =
             rounded;
     }
-    void* out = is_k ? a.k_out : a.v_out;
-    if (kv && out != nullptr)
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + static_cast<uint64_t>(t) * (is_k ? a.ko_ts : a.vo_ts) +
-                                  static_cast<uint64_t>(static_cast<uint32_t>(h)) * (is_k ? a.ko_hs : a.vo_hs) + 8 * c) =
-            rounded;
+    void* out = is_v ? a.v_out : a.k_out;
+    if (on && out != nullptr) *out_row(out, is_v ? a.vo_ts : a.ko_ts, is_v ? a.vo_hs : a.ko_hs) = rounded;
 }
 
-template <int D, bool BF16, bool KV4>
-__global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_constant__ AppendArgs a) {
+// The query rows, or the key and value rows, of tokens [first, first + tokens).
+template <int D, bool BF16, bool KV4, bool QUERY>
+__device__ __forceinline__ void append_block(const AppendArgs& a, Shared<D>& sh, uint32_t first, int tokens) {
     constexpr int kChunks = D / 8;                  // threads per row
     constexpr int kLanes = kThreads / kChunks;      // rows in flight per block
-    __shared__ int64_t s_page[kMaxTokens];          // -1: nothing of the token is written
-    __shared__ int s_off[kMaxTokens];
-    __shared__ float4 s_cs[kMaxTokens][4 * kChunks];
     const int c = threadIdx.x % kChunks;
     const int rlane = threadIdx.x / kChunks;
-    const int rows = a.H + 2 * a.Hkv;
-    const uint32_t first = blockIdx.x * static_cast<uint32_t>(a.tokens);
-    const int tokens = static_cast<int>(min(static_cast<int64_t>(a.tokens), a.T - first));
+    const int rows = QUERY ? a.H : 2 * a.Hkv;
 
     // Items are dealt to the row lanes in turn; from one to a lane's next:
     const int step_tl = kLanes / rows, step_r = kLanes - step_tl * rows;
@@ -268,12 +271,11 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
     auto load = [&](int u) {
         raw[u] = make_uint4(0u, 0u, 0u, 0u);
         if (ahead.tl < tokens) {
-            const int r = ahead.r;
-            const bool is_q = r < a.H, is_k = r < a.H + a.Hkv;
-            const uint16_t* src = static_cast<const uint16_t*>(is_q ? a.q : (is_k ? a.k : a.v));
-            const uint32_t ts = is_q ? a.q_ts : (is_k ? a.k_ts : a.v_ts);
-            const uint32_t hs = is_q ? a.q_hs : (is_k ? a.k_hs : a.v_hs);
-            const uint32_t h = is_q ? r : (is_k ? r - a.H : r - a.H - a.Hkv);
+            const bool is_v = !QUERY && ahead.r >= a.Hkv;
+            const uint16_t* src = static_cast<const uint16_t*>(QUERY ? a.q : (is_v ? a.v : a.k));
+            const uint32_t ts = QUERY ? a.q_ts : (is_v ? a.v_ts : a.k_ts);
+            const uint32_t hs = QUERY ? a.q_hs : (is_v ? a.v_hs : a.k_hs);
+            const uint32_t h = is_v ? ahead.r - a.Hkv : ahead.r;
             raw[u] = *reinterpret_cast<const uint4*>(src + static_cast<uint64_t>(first + ahead.tl) * ts +
                                                      static_cast<uint64_t>(h) * hs + 8 * c);
         }
@@ -294,19 +296,26 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
             slot = -1;
         }
         if (e == 0) {
-            const int64_t page = slot < 0 ? -1 : slot / a.page_size;
-            s_page[tl] = page;
-            s_off[tl] = slot < 0 ? 0 : static_cast<int>(slot - page * a.page_size);
+            int64_t page = -1;
+            int off = 0;
+            if (slot >= 0 && !QUERY) {  // 32-bit division where it does
+                page = (slot >> 32) == 0 ? static_cast<uint32_t>(slot) / static_cast<uint32_t>(a.page_size)
+                                         : slot / a.page_size;
+                off = static_cast<int>(slot - page * a.page_size);
+            }
+            sh.page[tl] = QUERY ? (slot < 0 ? -1 : 0) : page;
+            sh.off[tl] = off;
         }
         if (slot >= 0 && a.rot > 0) {
             const int64_t at = static_cast<int64_t>(pos) * (a.rot / 2);
+            float4(&cs)[4][kChunks] = sh.cs[tl];
             if (a.interleaved) {  // pairs 4e .. 4e + 3, each angle for both elements
                 const float4 co = *reinterpret_cast<const float4*>(a.cos + at + 4 * e);
                 const float4 si = *reinterpret_cast<const float4*>(a.sin + at + 4 * e);
-                s_cs[tl][e] = make_float4(co.x, co.x, co.y, co.y);
-                s_cs[tl][kChunks + e] = make_float4(-si.x, si.x, -si.y, si.y);
-                s_cs[tl][2 * kChunks + e] = make_float4(co.z, co.z, co.w, co.w);
-                s_cs[tl][3 * kChunks + e] = make_float4(-si.z, si.z, -si.w, si.w);
+                cs[0][e] = make_float4(co.x, co.x, co.y, co.y);
+                cs[1][e] = make_float4(-si.x, si.x, -si.y, si.y);
+                cs[2][e] = make_float4(co.z, co.z, co.w, co.w);
+                cs[3][e] = make_float4(-si.z, si.z, -si.w, si.w);
             } else {
                 const bool second = e >= a.rot / 16;
                 const int64_t i = at + 8 * (second ? e - a.rot / 16 : e);
@@ -314,8 +323,8 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const float4 si = *reinterpret_cast<const float4*>(a.sin + i + 4 * u);
-                    s_cs[tl][2 * u * kChunks + e] = *reinterpret_cast<const float4*>(a.cos + i + 4 * u);
-                    s_cs[tl][(2 * u + 1) * kChunks + e] = make_float4(sg * si.x, sg * si.y, sg * si.z, sg * si.w);
+                    cs[2 * u][e] = *reinterpret_cast<const float4*>(a.cos + i + 4 * u);
+                    cs[2 * u + 1][e] = make_float4(sg * si.x, sg * si.y, sg * si.z, sg * si.w);
                 }
             }
         }
@@ -329,14 +338,28 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
         for (int u = 0; u < kAhead; ++u) {
             if (i + u < turns) {
                 const int tl = min(now.tl, tokens - 1);
-                const int64_t page = s_page[tl];
-                append_row<D, BF16, KV4>(a, raw[u], first + tl, now.r, now.tl < tokens && page >= 0, page, s_off[tl],
-                                         &s_cs[tl][c]);
+                const int64_t page = sh.page[tl];
+                append_row<D, BF16, KV4, QUERY>(a, raw[u], first + tl, now.r, now.tl < tokens && page >= 0, page,
+                                                sh.off[tl], &sh.cs[tl][0][c]);
                 next(now);
                 load(u);
             }
         }
     }
+}
+
+// The first blocks take key and value rows (more work each), the rest query rows.
+template <int D, bool BF16, bool KV4>
+__global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_constant__ AppendArgs a) {
+    __shared__ Shared<D> sh;
+    const bool query = blockIdx.x >= a.kv_blocks;
+    const uint32_t per = query ? a.q_tokens : a.kv_tokens;
+    const uint32_t first = (query ? blockIdx.x - a.kv_blocks : blockIdx.x) * per;
+    const int tokens = static_cast<int>(min(static_cast<int64_t>(per), a.T - first));
+    if (query)
+        append_block<D, BF16, KV4, true>(a, sh, first, tokens);
+    else
+        append_block<D, BF16, KV4, false>(a, sh, first, tokens);
 }
 
 template <int D, bool BF16>
@@ -352,13 +375,19 @@ cudaError_t launch_kind(const AppendArgs& a, bool kv4, unsigned grid, cudaStream
 
 cudaError_t append_launch(AppendArgs a, int D, bool bf16, bool kv4, int sms, cudaStream_t s) {
     // Tokens per block: one while that leaves SMs without a block, then as many
-    // as give a block's threads kAhead rows each.
+    // as give a block's threads kTurns rows each.
     const int lanes = kThreads / (D / 8);
-    const int rows = a.H + 2 * a.Hkv;
-    int tokens = (kAhead * lanes + rows - 1) / rows;
-    tokens = std::min(std::min(tokens, kMaxTokens), static_cast<int>((a.T + 4 * sms - 1) / (4 * sms)));
-    a.tokens = std::max(tokens, 1);
-    const unsigned grid = static_cast<unsigned>((a.T + a.tokens - 1) / a.tokens);
+    auto tokens = [&](int rows) {
+        const int64_t most = std::min<int64_t>(std::max(kTurns * lanes / rows, 1), kMaxTokens);
+        return static_cast<uint32_t>(std::max<int64_t>(std::min(most, a.T / (4 * sms)), 1));
+    };
+    a.kv_tokens = tokens(2 * a.Hkv);
+    a.kv_blocks = static_cast<uint32_t>((a.T + a.kv_tokens - 1) / a.kv_tokens);
+    unsigned grid = a.kv_blocks;
+    if (a.H > 0) {
+        a.q_tokens = tokens(a.H);
+        grid += static_cast<unsigned>((a.T + a.q_tokens - 1) / a.q_tokens);
+    }
     if (D == 128) return bf16 ? launch_kind<128, true>(a, kv4, grid, s) : launch_kind<128, false>(a, kv4, grid, s);
     return bf16 ? launch_kind<64, true>(a, kv4, grid, s) : launch_kind<64, false>(a, kv4, grid, s);
 }

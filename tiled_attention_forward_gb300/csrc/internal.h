@@ -177,7 +177,9 @@ struct AppendArgs {
     int rot;
     int interleaved;
     int held;             // 4-bit: k_out / v_out receive the values that the cache stands for
-    int tokens;           // of a block, set by append_launch
+    uint32_t kv_blocks;   // blocks of key and value rows, tokens of a block (set by append_launch)
+    uint32_t kv_tokens;
+    uint32_t q_tokens;
 };
 cudaError_t append_launch(AppendArgs a, int D, bool bf16, bool kv4, int sms, cudaStream_t s);
 cudaError_t append_read_and_clear_error_word(uint32_t* out);
