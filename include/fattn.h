@@ -325,8 +325,9 @@ FATTN_API int fattn_fwd_unfused_static(const void* q, const void* k, const void*
 
 /*
  * fattn_packed_workspace_bytes -- bytes of device workspace fattn_fwd_packed
- * needs for B sequences of T tokens in all (the list of Q blocks): 16 * (1 +
- * T/256 + B).  0 for an empty or invalid size.
+ * needs for B sequences of T tokens in all: the list of Q blocks, 16 * (1 +
+ * T/256 + B), or where T/256 + B <= 64 one of 1040 bytes for each of up to 160
+ * CTAs.  0 for an empty or invalid size.
  */
 FATTN_API int64_t fattn_packed_workspace_bytes(int64_t B, int64_t T);
 
@@ -350,7 +351,8 @@ FATTN_API int64_t fattn_packed_workspace_bytes(int64_t B, int64_t T);
  *                need workspaces of their own.
  * Within a sequence, a NaN or infinity in a V row also reaches earlier rows of
  * the same 256-row block (their weight 0 times it), as in fattn_fwd; it never
- * reaches another sequence.  Two launches (the list of Q blocks, the forward).
+ * reaches another sequence.  One launch where T/256 + B <= 64, else two (the
+ * list of Q blocks, the forward).
  */
 FATTN_API int fattn_fwd_packed(const void* q, const void* k, const void* v, void* o, float* lse,
                      const int64_t* strides, const int32_t* cu_seqlens, void* workspace,

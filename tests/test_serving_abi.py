@@ -222,8 +222,9 @@ def test_packed_refusals():
 
 def test_packed_workspace_bytes():
     ws = fattn.load().fattn_packed_workspace_bytes
-    for B, T in ((1, 1), (3, 255), (64, 16384), (1, 256)):
-        assert ws(B, T) == 16 * (1 + T // 256 + B)
+    for B, T in ((1, 1), (3, 255), (64, 16384), (1, 256), (64, 255), (65, 255), (1, 64 * 256)):
+        blocks = T // 256 + B
+        assert ws(B, T) == (16 * (1 + blocks) if blocks > 64 else 160 * 16 * 65)
         # one list entry per Q block, however the tokens are dealt out
         assert T // 256 + B >= sum(-(-n // 256) for n in [T - (B - 1)] + [1] * (B - 1) if n > 0)
     for bad in ((0, 1), (1, 0), (-1, 5), (1 << 31, 1), (1, 1 << 31)):

@@ -36,7 +36,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kAhead = 4;       // rows that a thread has on their way
-constexpr int kTurns = 8;       // rows that a thread takes, where there are enough
+constexpr int kTurns = 16;      // rows that a thread takes, where there are enough
 constexpr int kMaxTokens = 16;  // tokens of a block
 constexpr float kFp16Max = 65504.f;
 
@@ -350,7 +350,7 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, Shared<D>& sh,
 
 // The first blocks take key and value rows (more work each), the rest query rows.
 template <int D, bool BF16, bool KV4>
-__global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, 5) cache_append_kernel(const __grid_constant__ AppendArgs a) {
     __shared__ Shared<D> sh;
     const bool query = blockIdx.x >= a.kv_blocks;
     const uint32_t per = query ? a.q_tokens : a.kv_tokens;
@@ -379,7 +379,7 @@ cudaError_t append_launch(AppendArgs a, int D, bool bf16, bool kv4, int sms, cud
     const int lanes = kThreads / (D / 8);
     auto tokens = [&](int rows) {
         const int64_t most = std::min<int64_t>(std::max(kTurns * lanes / rows, 1), kMaxTokens);
-        return static_cast<uint32_t>(std::max<int64_t>(std::min(most, a.T / (4 * sms)), 1));
+        return static_cast<uint32_t>(std::max<int64_t>(std::min(most, a.T / (3 * sms)), 1));
     };
     a.kv_tokens = tokens(2 * a.Hkv);
     a.kv_blocks = static_cast<uint32_t>((a.T + a.kv_tokens - 1) / a.kv_tokens);

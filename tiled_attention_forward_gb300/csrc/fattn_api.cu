@@ -956,7 +956,8 @@ int fattn_cache_append_kv4(const void* q, const void* k, const void* v, void* q_
 
 int64_t fattn_packed_workspace_bytes(int64_t B, int64_t T) {
     if (B <= 0 || T <= 0 || B > (int64_t(1) << 30) || T > (int64_t(1) << 30)) return 0;
-    return 16 * (1 + T / (kTcBM * kTcQTiles) + B);
+    const int64_t blocks = T / (kTcBM * kTcQTiles) + B;
+    return blocks <= kSmallPlan ? int64_t(kSmallPlanCtas) * kSmallPlanBytes : 16 * (1 + blocks);
 }
 
 int fattn_fwd_packed(const void* q, const void* k, const void* v, void* o, float* lse, const int64_t* strides,
@@ -1025,13 +1026,15 @@ int fattn_fwd_packed(const void* q, const void* k, const void* v, void* o, float
     a.scale_log2 = scale * kLog2e;
     a.timeout_ns = kDefaultTimeoutNs;
     a.plan = static_cast<PackedPlan*>(workspace);
+    a.cu = cu_seqlens;
+    a.B = static_cast<int>(B);
     a.T = T;
     a.o_ts = ts[3];
     a.o_hs = hs[3];
     const int grid = static_cast<int>(std::min<int64_t>(capacity * H, sms));
-    const cudaError_t e = packed_launch(a, cu_seqlens, static_cast<int>(B), static_cast<int>(D), dtype == FATTN_BF16,
-                                        causal != 0, static_cast<int>(capacity), grid,
-                                        reinterpret_cast<cudaStream_t>(stream_h));
+    a.plan_stride = capacity <= kSmallPlan && grid <= kSmallPlanCtas ? kSmallPlanBytes : 0;
+    const cudaError_t e = packed_launch(a, static_cast<int>(D), dtype == FATTN_BF16, causal != 0,
+                                        static_cast<int>(capacity), grid, reinterpret_cast<cudaStream_t>(stream_h));
     return e == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
 }
 

@@ -117,6 +117,11 @@ struct TcLayout {
     static_assert((kRot ? 384 : 256) + 2 * D <= 512, "TMEM budget");
 };
 
+// The list of Q blocks that this CTA follows.
+__device__ __forceinline__ PackedPlan* plan_of(const PackedArgs& a) {
+    return reinterpret_cast<PackedPlan*>(reinterpret_cast<uint8_t*>(a.plan) + blockIdx.x * a.plan_stride);
+}
+
 struct Task {
     int bh;     // query head (dense: b * H + h)
     int q0;     // first row of the Q block within its sequence
@@ -143,12 +148,13 @@ __device__ __forceinline__ Task decode_task(int t, const ArgsOf<PACKED>& a) {
     k.n = a.N;
     k.start = 0;
     if constexpr (PACKED) {
-        const int blocks = a.plan->blocks;
+        const PackedPlan* plan = plan_of(a);
+        const int blocks = plan->blocks;
         const int per_group = a.head_group * blocks;
         const int g = t / per_group;
         const int r = t - g * per_group;
         const int gsize = min(a.head_group, a.H - g * a.head_group);
-        const int4 e = a.plan->list[r / gsize];
+        const int4 e = plan->list[r / gsize];
         k.bh = g * a.head_group + r % gsize;
         k.start = e.x;
         k.n = e.y;
@@ -308,7 +314,7 @@ __device__ __forceinline__ void release_task(const TaskRing& r, int kt) {
 template <bool PACKED>
 __device__ __forceinline__ int num_tasks_of(const ArgsOf<PACKED>& a) {
     if constexpr (PACKED)
-        return a.plan->blocks * a.H;
+        return plan_of(a)->blocks * a.H;
     else
         return a.num_tasks;
 }
@@ -318,6 +324,76 @@ __device__ __forceinline__ bool schedule_ended(int t, const ArgsOf<PACKED>& a) {
         return t == static_cast<int>(kEndOfSchedule);
     else
         return t >= a.num_tasks;
+}
+
+// K/V tiles that Q block `blk` of a sequence of n tokens visits: the key of the
+// list's order.
+template <bool CAUSAL>
+__device__ __forceinline__ int block_tiles(int n, int blk) {
+    const int keys = CAUSAL ? min(n, (blk + 1) * (kTcBM * kTcQTiles)) : n;
+    return (keys + kTcBN - 1) / kTcBN;
+}
+
+// Packed, few Q blocks: every CTA lists them, longest first, instead of waiting
+// for a launch that does (the whole CTA calls this; T/256 + B <= kSmallPlan, so
+// there are at most kSmallPlan sequences and blocks).  Each has a list of its
+// own in the workspace: one list that all write the same values to cost 8 us of
+// a short call (17 against 9), and one in shared memory makes every later access
+// generic, which cost the softmax warps registers and 2 % of a long call.  Warp 0
+// takes two sequences a lane, checks them, and writes their
+// blocks in order; each block's place is then the number of blocks before it.
+// The scratch lies in the tiles' memory, which no copy has reached yet.
+template <bool CAUSAL>
+__device__ __forceinline__ void list_blocks(const PackedArgs& a, int4* scratch) {
+    constexpr int kRows = kTcBM * kTcQTiles;
+    PackedPlan* plan = plan_of(a);
+    const int lane = threadIdx.x % 32;
+    if (threadIdx.x < 32) {
+        int start[2], n[2], blocks[2];
+        bool bad = false;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int b = 2 * lane + u;
+            start[u] = n[u] = 0;
+            if (b < a.B) {
+                start[u] = a.cu[b];
+                const int end = a.cu[b + 1];
+                bad |= start[u] < 0 || end < start[u] || end > a.T;
+                n[u] = end - start[u];
+            }
+            blocks[u] = (n[u] + kRows - 1) / kRows;
+        }
+        const bool any_bad = __any_sync(0xffffffffu, bad);
+        int at = blocks[0] + blocks[1];
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int y = __shfl_up_sync(0xffffffffu, at, d);
+            if (lane >= d) at += y;
+        }
+        const int total = any_bad ? 0 : min(__shfl_sync(0xffffffffu, at, 31), kSmallPlan);
+        at -= blocks[0] + blocks[1];
+        if (!any_bad) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                for (int blk = 0; blk < blocks[u]; ++blk, ++at)
+                    if (at < kSmallPlan) scratch[at] = make_int4(start[u], n[u], blk, block_tiles<CAUSAL>(n[u], blk));
+        }
+        if (lane == 0) {
+            plan->blocks = total;
+            if (any_bad && blockIdx.x == 0) atomicOr(&g_error_word, 1u << kDevErrInvalidArg);
+        }
+    }
+    __syncthreads();
+    const int total = plan->blocks;
+    if (threadIdx.x < total) {
+        const int4 e = scratch[threadIdx.x];
+        int place = 0;
+        for (int i = 0; i < total; ++i) {
+            const int w = scratch[i].w;
+            place += w > e.w || (w == e.w && i < static_cast<int>(threadIdx.x));
+        }
+        plan->list[place] = make_int4(e.x, e.y, e.z, 0);
+    }
 }
 
 // Packed: the V rows of a tile behind its sequence's last key (`rows` of the
@@ -1135,6 +1211,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_tc_kernel(const __grid
     if (warp == 8) {
         tmem_alloc(misc, L::kTmemCols);
         tmem_relinquish();
+    }
+    if constexpr (PACKED) {
+        if (a.plan_stride != 0) {
+            list_blocks<CAUSAL>(a, reinterpret_cast<int4*>(smem));
+            // The scratch becomes a copy's destination (the async proxy).
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        } else {
+            asm volatile("griddepcontrol.wait;" ::: "memory");  // the launch that writes the list
+        }
     }
     if (warp == 9 && lane == 0) {
         tma_prefetch_desc(&a.tmap_q);

@@ -66,13 +66,18 @@ struct PackedPlan {  // in the caller's workspace
     int4 list[1];    // [blocks]: first token and length of the sequence, Q block within it
 };
 struct PackedArgs : TcArgs {  // tmaps {D, T, heads}; N, BH, num_qblk and num_tasks are unused
-    PackedPlan* plan;
+    PackedPlan* plan;    // the workspace
+    int plan_stride;     // few blocks: each CTA has a list of its own, so many bytes apart (else 0)
+    const int32_t* cu;   // [B + 1]
+    int B;
     int64_t T;
     int64_t o_ts;        // token and head stride of o, elements
     int64_t o_hs;
 };
-cudaError_t packed_launch(const PackedArgs& a, const int32_t* cu, int B, int D, bool bf16, bool causal, int capacity,
-                          int grid, cudaStream_t s);
+constexpr int kSmallPlan = 64;       // Q blocks that a CTA lists for itself
+constexpr int kSmallPlanCtas = 160;  // lists of their own in the workspace
+constexpr int kSmallPlanBytes = 16 * (1 + kSmallPlan);
+cudaError_t packed_launch(const PackedArgs& a, int D, bool bf16, bool causal, int capacity, int grid, cudaStream_t s);
 cudaError_t packed_read_and_clear_error_word(uint32_t* out);
 
 // ---- CUDA-core path (fp32), fwd_ffma.cu --------------------------------------
