@@ -13,6 +13,7 @@ call raises ``FattnLibraryMissing``.
     o, lse = fattn.fwd(q, k, v, causal=True)     # q,k,v: [B,H,N,D] cuda tensors
 """
 import ctypes
+import importlib.util
 import math
 import os
 
@@ -367,76 +368,53 @@ def fwd_unfused_static(q, k, v, causal=False, scale=None, out=None, lse=None, re
 # Serving: rows by strides, paged caches
 # ---------------------------------------------------------------------------
 # These calls are short (a decode step's kernels take a few microseconds), so
-# the checks below read each tensor attribute once and build nothing they do
-# not pass on.
-_I6, _I8, _I10, _I12 = (ctypes.c_int64 * n for n in (6, 8, 10, 12))
-_16BIT = {torch.float16: 1, torch.bfloat16: 2}
+# their tensors are checked and turned into the library's arguments by
+# _fattn_binding (csrc/binding.cpp); the functions below only fill in what the
+# caller left out.
+_BINDING_PATH = os.path.join(_HERE, "_fattn_binding.so")
+_fast = None
 
 
-def _bad(name, shape, dtype, where):
-    raise ValueError("%s must be %s %s on cuda:%d, contiguous along its last dimension"
-                     % (name, list(shape), dtype, where))
+def _binding():
+    global _fast
+    if _fast is None:
+        load()
+        if not os.path.exists(_BINDING_PATH):
+            raise FattnLibraryMissing(
+                "_fattn_binding.so is not built at %s; run `python -m tiled_attention_forward_gb300.build`"
+                % _BINDING_PATH)
+        spec = importlib.util.spec_from_file_location("_fattn_binding", _BINDING_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _fast = module
+    return _fast
 
 
-def _rows3(name, t, n0, n1, D, dtype, where):
-    """Strides of a 16-bit [n0, n1, D] tensor whose last dimension is
-    contiguous; 0 stands for that of a dimension of one element, which is never
-    used."""
-    s0, s1, s2 = t.stride() if t.dim() == 3 else (0, 0, 0)
-    if t.shape != (n0, n1, D) or t.dtype is not dtype or s2 != 1 or t.get_device() != where:
-        _bad(name, (n0, n1, D), dtype, where)
-    return (0 if n0 == 1 else s0), (0 if n1 == 1 else s1)
-
-
-def _rows4(name, t, n0, n1, n2, D, dtype, where):
-    s0, s1, s2, s3 = t.stride() if t.dim() == 4 else (0, 0, 0, 0)
-    if t.shape != (n0, n1, n2, D) or t.dtype is not dtype or s3 != 1 or t.get_device() != where:
-        _bad(name, (n0, n1, n2, D), dtype, where)
-    return (0 if n0 == 1 else s0), (0 if n1 == 1 else s1), (0 if n2 == 1 else s2)
-
-
-def _dense(name, t, shape, dtype, where):
-    """The address of a contiguous tensor."""
-    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or t.get_device() != where:
-        raise ValueError("%s must be contiguous %s %s on cuda:%d" % (name, list(shape), dtype, where))
-    return t.data_ptr()
-
-
-def _call(where, stream, name, fn, *args):
-    """fn(*args, stream) with device `where` current; the stream defaults to
-    torch's current one on that device."""
+def _handle(stream, t):
+    """The stream's handle (-1: torch's current one on the tensors' device)."""
     if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(where)
-    elif stream.device_index == where:
-        handle = stream.cuda_stream
-    else:
-        raise ValueError("the stream must be one of cuda:%d" % where)
-    if torch._C._cuda_getDevice() == where:
-        rc = fn(*args, handle)
-    else:
-        with torch.cuda.device(where):
-            rc = fn(*args, handle)
-    if rc != 0:
-        raise FattnError(rc, name)
+        return -1
+    if stream.device_index != t.get_device():
+        raise ValueError("the stream must be one of %s" % t.device)
+    return stream.cuda_stream
 
 
-def _new(shape, dtype, where, stream, make=torch.empty):
-    """A tensor for a call on `stream`: allocated (and filled) in that stream's
-    order, so that what held its memory before is done with it, and so that a
-    workspace can be dropped when the call returns."""
+def _new(shape, dtype, like, stream, make=torch.empty):
+    """A tensor for a call on `stream`, beside `like`: allocated (and filled) in
+    that stream's order, so that what held its memory before is done with it,
+    and so that a workspace can be dropped when the call returns."""
+    if not like.is_cuda:
+        raise ValueError("the tensors must be CUDA tensors")
     if stream is None:
-        return make(shape, dtype=dtype, device="cuda:%d" % where)
+        return make(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return make(shape, dtype=dtype, device="cuda:%d" % where)
+        return make(shape, dtype=dtype, device=like.device)
 
 
-def _workspace(workspace, need, where, stream):
-    """(tensor, address, bytes): the caller's workspace, or a new one."""
-    if workspace is None:
-        workspace = _new(max(need(), 16), torch.uint8, where, stream)
-    elif workspace.get_device() != where or not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous on cuda:%d" % where)
-    return workspace, workspace.data_ptr(), workspace.nbytes
+def _dims(name, t, n):
+    if t.dim() != n:
+        raise ValueError("%s must have %d dimensions" % (name, n))
+    return t.shape
 
 
 def packed_workspace_bytes(B, T):
@@ -457,94 +435,22 @@ def fwd_packed(q, k, v, cu_seqlens, causal=True, scale=None, out=None, lse=None,
     ``lse`` (zero where those are allocated here).  ``workspace``: a CUDA uint8
     tensor of at least ``packed_workspace_bytes(B, T)`` bytes (allocated here
     when None); calls running at the same time need one each."""
-    if not q.is_cuda or q.dim() != 3 or k.dim() != 3 or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
-        raise ValueError("q, k, v must be CUDA tensors [T, H, D] and [T, Hkv, D], cu_seqlens [B + 1]")
-    T, H, D = q.shape
-    Hkv = k.shape[1]
-    dt = q.dtype
-    where = q.get_device()
-    if dt not in _16BIT:
-        raise ValueError("dtype must be float16 or bfloat16")
-    B = cu_seqlens.shape[0] - 1
-    cu = _dense("cu_seqlens", cu_seqlens, (B + 1,), torch.int32, where)
-    if scale is None:
-        scale = _default_scale(D)
-    if out is None:
-        out = _new((T, H, D), dt, where, stream, torch.zeros)
+    if scale is None or out is None or workspace is None or (return_lse and lse is None):
+        T, H, D = _dims("q", q, 3)
+        scale = _default_scale(D) if scale is None else scale
+        if out is None:
+            out = _new((T, H, D), q.dtype, q, stream, torch.zeros)
+        if return_lse and lse is None:
+            lse = _new((H, T), torch.float32, q, stream, torch.zeros)
+        if workspace is None:
+            need = packed_workspace_bytes(_dims("cu_seqlens", cu_seqlens, 1)[0] - 1, T)
+            workspace = _new(max(need, 16), torch.uint8, q, stream)
     if not return_lse:
         lse = None
-    elif lse is None:
-        lse = _new((H, T), torch.float32, where, stream, torch.zeros)
-    strides = _I8(*_rows3("q", q, T, H, D, dt, where), *_rows3("k", k, T, Hkv, D, dt, where),
-                  *_rows3("v", v, T, Hkv, D, dt, where), *_rows3("out", out, T, H, D, dt, where))
-    lse_ptr = None if lse is None else _dense("lse", lse, (H, T), torch.float32, where)
-    workspace, ws, ws_bytes = _workspace(workspace, lambda: packed_workspace_bytes(B, T), where, stream)
-    _call(where, stream, "fattn_fwd_packed", load().fattn_fwd_packed,
-          q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse_ptr, strides, cu, ws, ws_bytes, B, T, H, Hkv,
-          D, scale, 1 if causal else 0, _16BIT[dt])
+    rc = _binding().fwd_packed(q, k, v, cu_seqlens, out, lse, workspace, scale, 1 if causal else 0, _handle(stream, q))
+    if rc != 0:
+        raise FattnError(rc, "fattn_fwd_packed")
     return out, lse
-
-
-def _pages(k_pages, v_pages, Hkv, D, dtype, where):
-    """(page stride, pages, page size) of a 16-bit cache."""
-    if k_pages.dim() != 4:
-        raise ValueError("k_pages and v_pages must be [pages, Hkv, page_size, D]")
-    P, h, ps, d = shape = k_pages.shape
-    if h != Hkv or d != D or v_pages.shape != shape or k_pages.dtype is not dtype or v_pages.dtype is not dtype or \
-            k_pages.get_device() != where or v_pages.get_device() != where:
-        raise ValueError("k_pages and v_pages must be [pages, %d, page_size, %d] %s on cuda:%d" % (Hkv, D, dtype, where))
-    strides = []
-    for t in (k_pages, v_pages):
-        s0, s1, s2, s3 = t.stride()
-        if s3 != 1 or (ps > 1 and s2 != D) or (Hkv > 1 and s1 != ps * D):
-            raise ValueError("each page must be contiguous")
-        strides.append(s0 if P > 1 else Hkv * ps * D)
-    if strides[0] != strides[1]:
-        raise ValueError("k_pages and v_pages must have one page stride")
-    return strides[0], P, ps
-
-
-def _pages_kv4(k_codes, k_scales, v_codes, v_scales, Hkv, D, where):
-    """Addresses, pages and page size of a 4-bit cache."""
-    if k_codes.dim() != 4:
-        raise ValueError("codes must be [pages, Hkv, page_size, D/2]")
-    P, _, ps, _ = k_codes.shape
-    cs, ss = (P, Hkv, ps, D // 2), (P, Hkv, ps, D // KV4_GROUP, 2)
-    return (_dense("k_codes", k_codes, cs, torch.uint8, where), _dense("k_scales", k_scales, ss, torch.float16, where),
-            _dense("v_codes", v_codes, cs, torch.uint8, where), _dense("v_scales", v_scales, ss, torch.float16, where),
-            P, ps)
-
-
-def _append_rows(k, q, q_out, slots, pos, cos, sin, stream):
-    """What both appends share: (T, H, Hkv, D, dtype, device, q_out, and the
-    arguments slots .. rot of the library call)."""
-    if not k.is_cuda or k.dim() != 3:
-        raise ValueError("k must be a CUDA tensor [T, Hkv, D]")
-    T, Hkv, D = k.shape
-    dt = k.dtype
-    where = k.get_device()
-    if dt not in _16BIT:
-        raise ValueError("dtype must be float16 or bfloat16")
-    H = 0
-    if q is not None:
-        if q.dim() != 3:
-            raise ValueError("q must be [T, H, D]")
-        H = q.shape[1]
-        if q_out is None:
-            q_out = _new((T, H, D), dt, where, stream)
-    elif q_out is not None:
-        raise ValueError("q_out needs q")
-    at = _dense("slots", slots, (T,), torch.int64, where)
-    if cos is None:
-        if sin is not None:
-            raise ValueError("a rotation needs cos and sin")
-        return T, H, Hkv, D, dt, where, q_out, (at, None, None, None, 0, 0)
-    if sin is None or pos is None or cos.dim() != 2:
-        raise ValueError("a rotation needs pos, and cos and sin [max_pos, rot/2]")
-    shape = cos.shape
-    return T, H, Hkv, D, dt, where, q_out, (
-        at, _dense("pos", pos, (T,), torch.int32, where), _dense("cos", cos, shape, torch.float32, where),
-        _dense("sin", sin, shape, torch.float32, where), shape[0], 2 * shape[1])
 
 
 def cache_append(k, v, k_pages, v_pages, slots, pos=None, cos=None, sin=None, interleaved=False, q=None,
@@ -563,17 +469,12 @@ def cache_append(k, v, k_pages, v_pages, slots, pos=None, cos=None, sin=None, in
     without q; allocated here when None) and, where ``k_out`` is given, k as
     the cache holds it.  ``q_out`` may be q itself.  An index out of range is
     skipped and reported by ``get_device_status``."""
-    T, H, Hkv, D, dt, where, q_out, place = _append_rows(k, q, q_out, slots, pos, cos, sin, stream)
-    stride, P, ps = _pages(k_pages, v_pages, Hkv, D, dt, where)
-    none = (0, 0)
-    strides = _I10(*(none if q is None else _rows3("q", q, T, H, D, dt, where)), *_rows3("k", k, T, Hkv, D, dt, where),
-                   *_rows3("v", v, T, Hkv, D, dt, where),
-                   *(none if q is None else _rows3("q_out", q_out, T, H, D, dt, where)),
-                   *(none if k_out is None else _rows3("k_out", k_out, T, Hkv, D, dt, where)))
-    _call(where, stream, "fattn_cache_append", load().fattn_cache_append,
-          None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), None if q is None else q_out.data_ptr(),
-          None if k_out is None else k_out.data_ptr(), strides, k_pages.data_ptr(), v_pages.data_ptr(), stride, P, ps,
-          *place, 1 if interleaved else 0, T, H, Hkv, D, _16BIT[dt])
+    if q is not None and q_out is None:
+        q_out = _new(q.shape, q.dtype, q, stream)
+    rc = _binding().cache_append(k, v, k_pages, v_pages, slots, pos, cos, sin, 1 if interleaved else 0, q, q_out, k_out,
+                                 _handle(stream, k))
+    if rc != 0:
+        raise FattnError(rc, "fattn_cache_append")
     return q_out, k_out
 
 
@@ -585,18 +486,13 @@ def cache_append_kv4(k, v, k_codes, k_scales, v_codes, v_scales, slots, pos=None
     include/fattn.h).  Returns (q_out, k_out, v_out); where given, k_out and
     v_out receive the rotated k and v, or with ``held`` the values that the
     cache now stands for."""
-    T, H, Hkv, D, dt, where, q_out, place = _append_rows(k, q, q_out, slots, pos, cos, sin, stream)
-    cache = _pages_kv4(k_codes, k_scales, v_codes, v_scales, Hkv, D, where)
-    none = (0, 0)
-    strides = _I12(*(none if q is None else _rows3("q", q, T, H, D, dt, where)), *_rows3("k", k, T, Hkv, D, dt, where),
-                   *_rows3("v", v, T, Hkv, D, dt, where),
-                   *(none if q is None else _rows3("q_out", q_out, T, H, D, dt, where)),
-                   *(none if k_out is None else _rows3("k_out", k_out, T, Hkv, D, dt, where)),
-                   *(none if v_out is None else _rows3("v_out", v_out, T, Hkv, D, dt, where)))
-    _call(where, stream, "fattn_cache_append_kv4", load().fattn_cache_append_kv4,
-          None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), None if q is None else q_out.data_ptr(),
-          None if k_out is None else k_out.data_ptr(), None if v_out is None else v_out.data_ptr(), strides, *cache,
-          *place, 1 if interleaved else 0, 1 if held else 0, T, H, Hkv, D, _16BIT[dt])
+    if q is not None and q_out is None:
+        q_out = _new(q.shape, q.dtype, q, stream)
+    rc = _binding().cache_append_kv4(k, v, k_codes, k_scales, v_codes, v_scales, slots, pos, cos, sin,
+                                     1 if interleaved else 0, q, q_out, k_out, v_out, 1 if held else 0,
+                                     _handle(stream, k))
+    if rc != 0:
+        raise FattnError(rc, "fattn_cache_append_kv4")
     return q_out, k_out, v_out
 
 
@@ -605,31 +501,17 @@ def decode_workspace_bytes(B, H, Nq, D, Hkv=None):
     return int(load().fattn_decode_workspace_bytes(int(B), int(H), int(H if Hkv is None else Hkv), int(Nq), int(D)))
 
 
-def _decode_args(q, Hkv, block_table, seq_lens, scale, out, lse, workspace, return_lse, where, stream):
-    """(out, lse, workspace tensor, the arguments q .. strides, and block_table
-    .. scale of the library call)."""
-    B, H, Nq, D = q.shape
-    dt = q.dtype
-    if dt not in _16BIT:
-        raise ValueError("dtype must be float16 or bfloat16")
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, pages per sequence]")
+def _decode_defaults(q, Hkv, scale, out, lse, workspace, return_lse, stream):
+    B, H, Nq, D = _dims("q", q, 4)
     if scale is None:
         scale = _default_scale(D)
     if out is None:
-        out = _new((B, H, Nq, D), dt, where, stream)
-    if not return_lse:
-        lse = None
-    elif lse is None:
-        lse = _new((B, H, Nq), torch.float32, where, stream)
-    strides = _I6(*_rows4("q", q, B, H, Nq, D, dt, where), *_rows4("out", out, B, H, Nq, D, dt, where))
-    width = block_table.shape[1]
-    workspace, ws, ws_bytes = _workspace(workspace, lambda: decode_workspace_bytes(B, H, Nq, D, Hkv), where, stream)
-    return out, lse, workspace, (
-        q.data_ptr(), out.data_ptr(), None if lse is None else _dense("lse", lse, (B, H, Nq), torch.float32, where),
-        strides), (
-        _dense("block_table", block_table, (B, width), torch.int32, where), width,
-        _dense("seq_lens", seq_lens, (B,), torch.int32, where), ws, ws_bytes, B, H, Hkv, Nq, D, scale, _16BIT[dt])
+        out = _new((B, H, Nq, D), q.dtype, q, stream)
+    if return_lse and lse is None:
+        lse = _new((B, H, Nq), torch.float32, q, stream)
+    if workspace is None:
+        workspace = _new(max(decode_workspace_bytes(B, H, Nq, D, Hkv), 16), torch.uint8, q, stream)
+    return scale, out, lse, workspace
 
 
 def decode(q, k_pages, v_pages, block_table, seq_lens, scale=None, out=None, lse=None, workspace=None,
@@ -645,29 +527,29 @@ def decode(q, k_pages, v_pages, block_table, seq_lens, scale=None, out=None, lse
     without keys gives o = 0, lse = -inf.  ``workspace``: a CUDA uint8 tensor
     of at least ``decode_workspace_bytes`` bytes (allocated here when None);
     calls running at the same time need one each."""
-    if not q.is_cuda or q.dim() != 4:
-        raise ValueError("q must be a CUDA tensor [B, H, Nq, D]")
-    where = q.get_device()
-    Hkv = k_pages.shape[1] if k_pages.dim() == 4 else 0
-    pages = _pages(k_pages, v_pages, Hkv, q.shape[3], q.dtype, where)
-    out, lse, workspace, rows, rest = _decode_args(q, Hkv, block_table, seq_lens, scale, out, lse, workspace,
-                                                   return_lse, where, stream)
-    _call(where, stream, "fattn_decode", load().fattn_decode, *rows, k_pages.data_ptr(), v_pages.data_ptr(), *pages,
-          *rest)
+    if scale is None or out is None or workspace is None or (return_lse and lse is None):
+        scale, out, lse, workspace = _decode_defaults(q, _dims("k_pages", k_pages, 4)[1], scale, out, lse, workspace,
+                                                      return_lse, stream)
+    if not return_lse:
+        lse = None
+    rc = _binding().decode(q, k_pages, v_pages, block_table, seq_lens, scale, out, lse, workspace, _handle(stream, q))
+    if rc != 0:
+        raise FattnError(rc, "fattn_decode")
     return out, lse
 
 
 def decode_kv4(q, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens, scale=None, out=None, lse=None,
                workspace=None, return_lse=True, stream=None):
     """``decode`` over a 4-bit cache (``cache_append_kv4``)."""
-    if not q.is_cuda or q.dim() != 4:
-        raise ValueError("q must be a CUDA tensor [B, H, Nq, D]")
-    where = q.get_device()
-    Hkv = k_codes.shape[1] if k_codes.dim() == 4 else 0
-    cache = _pages_kv4(k_codes, k_scales, v_codes, v_scales, Hkv, q.shape[3], where)
-    out, lse, workspace, rows, rest = _decode_args(q, Hkv, block_table, seq_lens, scale, out, lse, workspace,
-                                                   return_lse, where, stream)
-    _call(where, stream, "fattn_decode_kv4", load().fattn_decode_kv4, *rows, *cache, *rest)
+    if scale is None or out is None or workspace is None or (return_lse and lse is None):
+        scale, out, lse, workspace = _decode_defaults(q, _dims("k_codes", k_codes, 4)[1], scale, out, lse, workspace,
+                                                      return_lse, stream)
+    if not return_lse:
+        lse = None
+    rc = _binding().decode_kv4(q, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens, scale, out, lse, workspace,
+                               _handle(stream, q))
+    if rc != 0:
+        raise FattnError(rc, "fattn_decode_kv4")
     return out, lse
 
 
