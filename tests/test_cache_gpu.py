@@ -440,3 +440,32 @@ def test_streams_and_graphs(kv4):
     lens.copy_(torch.tensor([200, 7, 90], dtype=torch.int32))
     step()
     assert torch.equal(o, first)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_append_kv4_ties_round_to_even(dtype):
+    """Values on a coarse grid, where (x - zero) / scale is often exactly k + 1/2:
+    every code is the exact quotient's rounding, ties to even."""
+    D, ps, T = 128, 16, 160
+    g = torch.Generator().manual_seed(16)
+    x = torch.randint(-1024, 1025, (T, 1, D), generator=g).float() / 256
+    # ranges of 15 * 2^k grid steps: scales that are powers of two
+    for i in range(T // 2):
+        lo = x[i, 0].view(4, 32).amin(-1, keepdim=True)
+        span = torch.randint(0, 31, (4, 32), generator=g).float() * 2.0 ** -(1 + i % 4)
+        x[i, 0] = (lo + span.clamp(max=30 * 2.0 ** -(1 + i % 4))).flatten()
+        x[i, 0, ::32] = lo.flatten()
+        x[i, 0, 1::32] = lo.flatten() + 30 * 2.0 ** -(1 + i % 4)
+    x = x.to(DT[dtype])
+    cache = new_cache(True, T // ps, 1, ps, D, DT[dtype], 0.0)
+    fattn.cache_append_kv4(x.cuda(), x.cuda(), *cache, torch.arange(T).cuda())
+    ok()
+    ties = 0
+    for which, codes, scales in (("k", cache[0], cache[1]), ("v", cache[2], cache[3])):
+        c = R.unpack(codes.cpu().transpose(1, 2).reshape(T, 1, D // 2), which).double()
+        s = scales.cpu().double().transpose(1, 2).reshape(T, 1, D // 32, 2).repeat_interleave(32, dim=2)
+        q = (x.double() - s[..., 1]) / s[..., 0]
+        q = torch.where(s[..., 0] > 0, q, 0.0).clamp(0, 15)
+        ties += ((q - q.floor()) == 0.5).sum().item()
+        assert torch.equal(c, q.round())
+    assert ties > 1000

@@ -105,8 +105,11 @@ __device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, f
 
 // Quantises this thread's 8 elements (4 threads hold a group): its codes as the
 // floats 2^23 + code (whose low bits are the code), scale and zero.  A NaN takes
-// no part in the range (min and max drop it) and gets code 0 (so does .sat);
-// values past the fp16 range get the codes of its ends.
+// no part in the range and gets code 0 (min and max drop it); values past the
+// fp16 range get the codes of its ends.  The quotient is formed to the last bit
+// (one Newton step on the residual, which fma gives exactly): 16-bit values
+// stand on a grid, where quotients of exactly k + 1/2 are common, and a quotient
+// off by one bit there would round to the other neighbour.
 __device__ __forceinline__ void quantise(const float (&x)[8], float (&t)[8], __half& scale, __half& zero) {
     float lo = x[0], hi = x[0];
 #pragma unroll
@@ -125,10 +128,14 @@ __device__ __forceinline__ void quantise(const float (&x)[8], float (&t)[8], __h
     scale = __float2half_rn((hi - lo) / 15.f);
     zero = __float2half_rn(lo);
     const float s = __half2float(scale), z = __half2float(zero);
-    const float inv = s > 0.f ? 1.f / (15.f * s) : 0.f;  // 15 s is exact
+    const float inv = s > 0.f ? 1.f / s : 0.f;
+    const float top = 15.f * s;  // exact
 #pragma unroll
-    for (int e = 0; e < 8; ++e)  // adding 2^23 rounds to the nearest whole number, ties to even
-        t[e] = fmaf(__saturatef((x[e] - z) * inv), 15.f, 8388608.f);
+    for (int e = 0; e < 8; ++e) {
+        const float d = fminf(fmaxf(x[e] - z, 0.f), top);
+        const float q = d * inv;
+        t[e] = __fadd_rn(fmaf(fmaf(-q, s, d), inv, q), 8388608.f);  // 2^23 +: to the nearest, ties to even
+    }
 }
 
 // Nibbles e = 0..7 from t[0..7] = 2^23 + code: a sum in 32-bit integers, from
@@ -352,6 +359,7 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, Shared<D>& sh,
 template <int D, bool BF16, bool KV4>
 __global__ void __launch_bounds__(kThreads, 5) cache_append_kernel(const __grid_constant__ AppendArgs a) {
     __shared__ Shared<D> sh;
+    grid_dependency();
     const bool query = blockIdx.x >= a.kv_blocks;
     const uint32_t per = query ? a.q_tokens : a.kv_tokens;
     const uint32_t first = (query ? blockIdx.x - a.kv_blocks : blockIdx.x) * per;
@@ -364,11 +372,8 @@ __global__ void __launch_bounds__(kThreads, 5) cache_append_kernel(const __grid_
 
 template <int D, bool BF16>
 cudaError_t launch_kind(const AppendArgs& a, bool kv4, unsigned grid, cudaStream_t s) {
-    if (kv4)
-        cache_append_kernel<D, BF16, true><<<grid, kThreads, 0, s>>>(a);
-    else
-        cache_append_kernel<D, BF16, false><<<grid, kThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    return kv4 ? launch_overlapped(cache_append_kernel<D, BF16, true>, grid, kThreads, 0, s, a)
+               : launch_overlapped(cache_append_kernel<D, BF16, false>, grid, kThreads, 0, s, a);
 }
 
 }  // namespace

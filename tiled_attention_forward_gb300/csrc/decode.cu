@@ -612,6 +612,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
     const int row_blocks = (rows + C::kRows - 1) / C::kRows;
     const int per_key = a.Hkv * row_blocks;  // targets of one sequence
 
+    grid_dependency();
     // All units of the call, and this CTA's share of them.  A target (K/V head
     // and row block of a sequence) counts C::kTargetCost units more than it has, so
     // that shares of many short sequences take no longer than others.
@@ -917,8 +918,7 @@ cudaError_t launch_one(const DecodeArgs& a, int sms, cudaStream_t s) {
     cudaError_t e = opt_in_smem_once(fn, C::kSmem, done);
     if (e != cudaSuccess) return e;
     const int grid = sms * C::kCtasPerSm < kMaxCtas ? sms * C::kCtasPerSm : kMaxCtas;
-    fn<<<grid, kThreads, C::kSmem, s>>>(a);
-    return cudaGetLastError();
+    return launch_overlapped(fn, grid, kThreads, C::kSmem, s, a);
 }
 
 // Tiles of 8 query rows that share one pass over the keys.

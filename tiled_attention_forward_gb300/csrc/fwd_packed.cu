@@ -16,17 +16,24 @@ namespace fattn {
 namespace {
 
 constexpr int kPlanThreads = 1024;
+struct PlanArgs {
+    const int* cu;
+    int B, T, capacity;
+    PackedPlan* plan;
+};
 
 // Warp w keeps sequences w, w + 32, .. in its lanes (1024 of them at once, read
 // once where there are no more) and takes them one after the other, lanes over
 // blocks.
 template <bool CAUSAL>
-__global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const int* __restrict__ cu, int B, int T,
-                                                                   int capacity, PackedPlan* plan) {
+__global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PlanArgs args) {
+    const int* __restrict__ cu = args.cu;
+    const int B = args.B, T = args.T, capacity = args.capacity;
+    PackedPlan* plan = args.plan;
     __shared__ int bins[kPlanThreads];
     __shared__ int warp_sums[32];
     __shared__ int most, bad;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    grid_dependency();
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     if (tid == 0) most = bad = 0;
     bins[tid] = 0;
@@ -108,24 +115,13 @@ cudaError_t launch_one(const PackedArgs& a, int capacity, int grid, cudaStream_t
     static std::atomic<bool> done[kMaxDevices] = {};
     cudaError_t e = opt_in_smem_once(fn, L::kAlloc, done);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kTcThreads);
-    cfg.dynamicSmemBytes = L::kAlloc;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr;
     if (a.plan_stride == 0) {
-        packed_plan_kernel<CAUSAL><<<1, kPlanThreads, 0, stream>>>(a.cu, a.B, static_cast<int>(a.T), capacity, a.plan);
-        e = cudaGetLastError();
+        const PlanArgs p = {a.cu, a.B, static_cast<int>(a.T), capacity, a.plan};
+        e = launch_overlapped(packed_plan_kernel<CAUSAL>, 1, kPlanThreads, 0, stream, p);
         if (e != cudaSuccess) return e;
-        // The forward's own setup runs while the list is written; it waits for
-        // that launch before it reads anything.
-        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr.val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
     }
-    return cudaLaunchKernelEx(&cfg, fn, a);
+    // The forward's own setup runs while the list is written.
+    return launch_overlapped(fn, grid, kTcThreads, L::kAlloc, stream, a);
 }
 
 template <int D, bool BF16>

@@ -1213,12 +1213,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_tc_kernel(const __grid
         tmem_relinquish();
     }
     if constexpr (PACKED) {
+        // Waits for the kernel before it on the stream (the one that writes the
+        // list, where that is a launch of its own).
+        grid_dependency();
         if (a.plan_stride != 0) {
             list_blocks<CAUSAL>(a, reinterpret_cast<int4*>(smem));
             // The scratch becomes a copy's destination (the async proxy).
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        } else {
-            asm volatile("griddepcontrol.wait;" ::: "memory");  // the launch that writes the list
         }
     }
     if (warp == 9 && lane == 0) {

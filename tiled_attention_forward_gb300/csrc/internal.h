@@ -28,6 +28,33 @@ inline cudaError_t opt_in_smem_once(K* fn, int bytes, std::atomic<bool> (&done)[
     return cudaSuccess;
 }
 
+// Launches a kernel whose start may overlap the end of the kernel before it on
+// the stream (programmatic stream serialization): it calls grid_dependency()
+// before it touches memory, which waits for that kernel to complete.
+template <typename A>
+inline cudaError_t launch_overlapped(void (*fn)(A), unsigned grid, unsigned threads, size_t smem, cudaStream_t s,
+                                     const A& a) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fn, a);
+}
+#ifdef __CUDACC__
+// Every thread of a kernel launched so calls this first.  (The next kernel may
+// be set up as soon as every CTA of this one has come here; it waits likewise.)
+__device__ __forceinline__ void grid_dependency() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+#endif
+
 // ---- tensor-core path (bf16 / fp16), fwd_tc.cu ------------------------------
 constexpr int kTcBM = 128;        // Q rows per MMA tile (tcgen05 M)
 constexpr int kTcQTiles = 2;      // Q tiles per task (rows per task = 256)
