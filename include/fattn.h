@@ -397,7 +397,9 @@ FATTN_API int fattn_cache_append(const void* q, const void* k, const void* v, vo
  * fattn_cache_append_kv4 -- fattn_cache_append into a 4-bit cache.  The
  * rotated k (fp32, not rounded to `dtype` first) and v are quantised in groups
  * of 32 elements: zero = fp16(min), scale = fp16((max - min) / 15), code =
- * clamp(round((x - zero) / scale), 0, 15), 0 where scale is 0, all in fp32.
+ * clamp(round((x - zero) / scale), 0, 15), ties to even, 0 where scale is 0; in
+ * fp32, and to twice its precision where fp32 cannot tell to which side one of
+ * them rounds.
  * Elements past +-65504 are held as +-65504; a NaN takes no part in its
  * group's scale and is held as the group's zero.
  *

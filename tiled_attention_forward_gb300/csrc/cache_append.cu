@@ -110,7 +110,14 @@ __device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, f
 // (one Newton step on the residual, which fma gives exactly): 16-bit values
 // stand on a grid, where quotients of exactly k + 1/2 are common, and a quotient
 // off by one bit there would round to the other neighbour.
-__device__ __forceinline__ void quantise(const float (&x)[8], float (&t)[8], __half& scale, __half& zero) {
+//
+// `err` bounds the error of x (0: exact).  True where some rounding -- of the
+// zero, the scale or a code -- is too close to its border for fp32 to tell the
+// side: about one group in a thousand, which requantise() then settles.  (A
+// code on the wrong side is off by a whole step, and a reader of the cache
+// could not tell that from an error.)  Exact x needs this for the scale alone:
+// its quotients are exact ties or well away from one.
+__device__ __forceinline__ bool quantise(const float (&x)[8], float err, float (&t)[8], __half& scale, __half& zero) {
     float lo = x[0], hi = x[0];
 #pragma unroll
     for (int e = 1; e < 8; ++e) {
@@ -125,16 +132,102 @@ __device__ __forceinline__ void quantise(const float (&x)[8], float (&t)[8], __h
     if (!(lo <= hi)) lo = hi = 0.f;  // nothing but NaN
     lo = fminf(fmaxf(lo, -kFp16Max), kFp16Max);
     hi = fminf(fmaxf(hi, -kFp16Max), kFp16Max);
-    scale = __float2half_rn((hi - lo) / 15.f);
+    const float step = (hi - lo) / 15.f;
+    scale = __float2half_rn(step);
     zero = __float2half_rn(lo);
+    const float es = fmaf(0.14f, err, 2.4e-7f * step);  // 2 err / 15 and three roundings
+    auto apart = [](float a, float b) { return __half_as_ushort(__float2half_rn(a)) != __half_as_ushort(__float2half_rn(b)); };
+    bool near = apart(lo - err, lo + err) || apart(step - es, step + es);
     const float s = __half2float(scale), z = __half2float(zero);
     const float inv = s > 0.f ? 1.f / s : 0.f;
     const float top = 15.f * s;  // exact
+    float worst = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const float d = fminf(fmaxf(x[e] - z, 0.f), top);
         const float q = d * inv;
-        t[e] = __fadd_rn(fmaf(fmaf(-q, s, d), inv, q), 8388608.f);  // 2^23 +: to the nearest, ties to even
+        const float r = fmaf(fmaf(-q, s, d), inv, q);
+        t[e] = __fadd_rn(r, 8388608.f);  // 2^23 +: to the nearest, ties to even
+        worst = fmaxf(worst, fabsf(r - __fsub_rn(t[e], 8388608.f)));
+    }
+    // The quotient's own error: 16 * 2 roundings, and that of x in steps.
+    if (err > 0.f) near = near || worst > 0.5f - fmaf(err, inv, 2.0e-6f);
+    return near;
+}
+
+// The same to twice fp32's precision: values are unevaluated sums h + l of two
+// floats, products by fma and sums by the two-sum of Knuth (fp64 would take 10
+// times as long on this part).  From the row's raw elements: x the thread's own,
+// y their partners, cs as in append_row; turns: whether they turn.  Whole
+// groups call it.
+struct Two {
+    float h, l;
+};
+__device__ __forceinline__ Two two_sum(float a, float b) {
+    const float s = __fadd_rn(a, b), v = __fsub_rn(s, a);
+    return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, v)), __fsub_rn(b, v))};
+}
+__device__ __forceinline__ Two normal(float h, float l) {  // |h| >= |l|
+    const float s = __fadd_rn(h, l);
+    return {s, __fsub_rn(l, __fsub_rn(s, h))};
+}
+template <bool BF16, int CHUNKS>
+__device__ __noinline__ void requantise(uint4 raw, uint4 other, bool swap, bool turns, const float4* cs, uint32_t group,
+                                        float* t, __half* scale, __half* zero) {
+    float xf[8], yf[8];
+    unpack8<BF16>(raw, xf);
+    unpack8<BF16>(other, yf);
+    Two x[8], lo = {INFINITY, 0.f}, hi = {-INFINITY, 0.f};
+    auto less = [](const Two& a, const Two& b) { return a.h < b.h || (a.h == b.h && a.l < b.l); };
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        x[e] = {xf[e], 0.f};
+        if (turns) {
+            const float co = reinterpret_cast<const float*>(cs + (e / 4) * 2 * CHUNKS)[e % 4];
+            const float si = reinterpret_cast<const float*>(cs + ((e / 4) * 2 + 1) * CHUNKS)[e % 4];
+            const float y = swap ? xf[e ^ 1] : yf[e];
+            const float p = __fmul_rn(xf[e], co), q = __fmul_rn(y, si);
+            const Two w = two_sum(p, q);
+            x[e] = normal(w.h, __fadd_rn(w.l, __fadd_rn(__fmaf_rn(xf[e], co, -p), __fmaf_rn(y, si, -q))));
+        }
+        if (less(x[e], lo)) lo = x[e];
+        if (less(hi, x[e])) hi = x[e];
+    }
+#pragma unroll
+    for (int m = 1; m <= 2; m <<= 1) {
+        const Two a = {__shfl_xor_sync(group, lo.h, m), __shfl_xor_sync(group, lo.l, m)};
+        const Two b = {__shfl_xor_sync(group, hi.h, m), __shfl_xor_sync(group, hi.l, m)};
+        if (less(a, lo)) lo = a;
+        if (less(hi, b)) hi = b;
+    }
+    if (lo.h > hi.h) lo = hi = {0.f, 0.f};
+    auto clamp = [](Two& a) {
+        if (a.h > kFp16Max) a = {kFp16Max, 0.f};
+        if (a.h < -kFp16Max) a = {-kFp16Max, 0.f};
+    };
+    clamp(lo);
+    clamp(hi);
+    const Two d = two_sum(hi.h, -lo.h);
+    const Two range = normal(d.h, __fadd_rn(d.l, __fsub_rn(hi.l, lo.l)));
+    const float q0 = range.h / 15.f;
+    *scale = __float2half_rn(__fadd_rn(q0, __fadd_rn(__fmaf_rn(-q0, 15.f, range.h), range.l) / 15.f));
+    *zero = __float2half_rn(lo.h);
+    const float s = __half2float(*scale), z = __half2float(*zero);
+    const float inv = s > 0.f ? 1.f / s : 0.f, half = 0.5f * s;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        // k: the code that fp32 finds; then which side of k +- 1/2 the value is on.
+        const Two w = two_sum(x[e].h, -z);
+        const float low = __fadd_rn(w.l, x[e].l);
+        float k = rintf(fminf(fmaxf(w.h * inv, 0.f), 15.f));
+        const float rest = __fmaf_rn(-k, s, w.h);
+        const float above = __fadd_rn(__fsub_rn(rest, half), low), below = __fadd_rn(__fadd_rn(rest, half), low);
+        const bool odd = (static_cast<int>(k) & 1) != 0;
+        if (k < 15.f && (above > 0.f || (above == 0.f && odd && s > 0.f)))
+            k += 1.f;
+        else if (k > 0.f && (below < 0.f || (below == 0.f && odd && s > 0.f)))
+            k -= 1.f;
+        t[e] = 8388608.f + (s > 0.f ? k : 0.f);
     }
 }
 
@@ -173,7 +266,9 @@ __device__ __forceinline__ void append_row(const AppendArgs& a, const uint4& raw
     const int c = threadIdx.x % kChunks, lane = threadIdx.x % 32;
     const bool is_v = !QUERY && r >= a.Hkv;
     const uint32_t h = is_v ? r - a.Hkv : r;
-    uint4 rounded = raw;
+    uint4 rounded = raw, other = raw;
+    bool turns = false;
+    float err = 0.f;  // 4 bits: bound of the rotated elements' error
     float x[8];
     if (!QUERY || a.rot > 0) unpack8<BF16>(raw, x);
     // Rotation (q and k rows).  Halves: chunk c < rot/16 holds the pairs' first
@@ -181,14 +276,13 @@ __device__ __forceinline__ void append_row(const AppendArgs& a, const uint4& raw
     // sin - b cos comes with the angles.  Interleaved pairs lie within a chunk.
     if (a.rot > 0 && (QUERY || __any_sync(0xffffffffu, !is_v))) {
         const int half_chunks = a.rot / 16;
-        const bool turns = c < 2 * half_chunks && !is_v;
+        turns = c < 2 * half_chunks && !is_v;
         float y[8];
         if (a.interleaved) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] = x[e ^ 1];
         } else {
             const int from = lane - c + (turns ? (c < half_chunks ? c + half_chunks : c - half_chunks) : c);
-            uint4 other;
             other.x = __shfl_sync(0xffffffffu, raw.x, from);
             other.y = __shfl_sync(0xffffffffu, raw.y, from);
             other.z = __shfl_sync(0xffffffffu, raw.z, from);
@@ -196,6 +290,13 @@ __device__ __forceinline__ void append_row(const AppendArgs& a, const uint4& raw
             unpack8<BF16>(other, y);
         }
         if (turns) {
+            if (KV4 && !QUERY) {
+                // Two roundings of at most |x cos| and |x cos| + |y sin|.
+                float most = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) most = fmaxf(most, fmaxf(fabsf(x[e]), fabsf(y[e])));
+                err = 1.8e-7f * most;  // 3 * 2^-24
+            }
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const float4 co = cs[(2 * u) * kChunks], si = cs[(2 * u + 1) * kChunks];
@@ -219,7 +320,22 @@ __device__ __forceinline__ void append_row(const AppendArgs& a, const uint4& raw
     if constexpr (KV4) {
         __half scale, zero;
         float code[8];
-        quantise(x, code, scale, zero);
+        err = fmaxf(err, __shfl_xor_sync(0xffffffffu, err, 1));
+        err = fmaxf(err, __shfl_xor_sync(0xffffffffu, err, 2));
+        const uint32_t unsure = __ballot_sync(0xffffffffu, quantise(x, err, code, scale, zero));
+        if (unsure != 0u) {
+            const uint32_t group = 15u << (lane & ~3);
+            if (unsure & group) {
+                float exact[8];  // (code itself stays in registers)
+                __half es, ez;
+                requantise<BF16, kChunks>(raw, other, a.interleaved, turns, cs, group, exact, &es, &ez);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) code[e] = exact[e];
+                scale = es;
+                zero = ez;
+            }
+            __syncwarp();
+        }
         const int64_t row = (page * a.Hkv + h) * a.page_size + off;
         if (__any_sync(0xffffffffu, !is_v)) {
             // K: element e = 2 l + u of the chunk at nibble l + 4 u, so that a word's
@@ -357,7 +473,7 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, Shared<D>& sh,
 
 // The first blocks take key and value rows (more work each), the rest query rows.
 template <int D, bool BF16, bool KV4>
-__global__ void __launch_bounds__(kThreads, 5) cache_append_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, KV4 ? 4 : 5) cache_append_kernel(const __grid_constant__ AppendArgs a) {
     __shared__ Shared<D> sh;
     grid_dependency();
     const bool query = blockIdx.x >= a.kv_blocks;
