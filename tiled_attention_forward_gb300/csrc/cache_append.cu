@@ -111,13 +111,16 @@ __device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, f
 // stand on a grid, where quotients of exactly k + 1/2 are common, and a quotient
 // off by one bit there would round to the other neighbour.
 //
-// `err` bounds the error of x (0: exact).  True where some rounding -- of the
+// `rotated`: x is off by up to 3 roundings of its pair's magnitude, which this
+// group's range and that of the lane `partner`'s group bound (|a|, |b| <=
+// sqrt(2) max(|a'|, |b'|)); else x is exact.  True where some rounding -- of the
 // zero, the scale or a code -- is too close to its border for fp32 to tell the
 // side: about one group in a thousand, which requantise() then settles.  (A
 // code on the wrong side is off by a whole step, and a reader of the cache
 // could not tell that from an error.)  Exact x needs this for the scale alone:
 // its quotients are exact ties or well away from one.
-__device__ __forceinline__ bool quantise(const float (&x)[8], float err, float (&t)[8], __half& scale, __half& zero) {
+__device__ __forceinline__ bool quantise(const float (&x)[8], bool rotated, int partner, float (&t)[8], __half& scale,
+                                         __half& zero) {
     float lo = x[0], hi = x[0];
 #pragma unroll
     for (int e = 1; e < 8; ++e) {
@@ -135,8 +138,15 @@ __device__ __forceinline__ bool quantise(const float (&x)[8], float err, float (
     const float step = (hi - lo) / 15.f;
     scale = __float2half_rn(step);
     zero = __float2half_rn(lo);
+    float most = fmaxf(-lo, hi);
+    most = fmaxf(most, __shfl_sync(0xffffffffu, most, partner));
+    const float err = rotated ? 2.6e-7f * most : 0.f;  // 3 sqrt(2) 2^-24
     const float es = fmaf(0.14f, err, 2.4e-7f * step);  // 2 err / 15 and three roundings
-    auto apart = [](float a, float b) { return __half_as_ushort(__float2half_rn(a)) != __half_as_ushort(__float2half_rn(b)); };
+    auto apart = [](float a, float b) {
+        const __half2 h = __floats2half2_rn(a, b);
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(&h);
+        return (w >> 16) != (w & 0xffffu);
+    };
     bool near = apart(lo - err, lo + err) || apart(step - es, step + es);
     const float s = __half2float(scale), z = __half2float(zero);
     const float inv = s > 0.f ? 1.f / s : 0.f;
@@ -151,7 +161,7 @@ __device__ __forceinline__ bool quantise(const float (&x)[8], float err, float (
         worst = fmaxf(worst, fabsf(r - __fsub_rn(t[e], 8388608.f)));
     }
     // The quotient's own error: 16 * 2 roundings, and that of x in steps.
-    if (err > 0.f) near = near || worst > 0.5f - fmaf(err, inv, 2.0e-6f);
+    if (rotated) near = near || worst > 0.5f - fmaf(err, inv, 2.0e-6f);
     return near;
 }
 
@@ -268,7 +278,7 @@ __device__ __forceinline__ void append_row(const AppendArgs& a, const uint4& raw
     const uint32_t h = is_v ? r - a.Hkv : r;
     uint4 rounded = raw, other = raw;
     bool turns = false;
-    float err = 0.f;  // 4 bits: bound of the rotated elements' error
+    int from = lane;  // the lane of this thread's partner elements
     float x[8];
     if (!QUERY || a.rot > 0) unpack8<BF16>(raw, x);
     // Rotation (q and k rows).  Halves: chunk c < rot/16 holds the pairs' first
@@ -282,7 +292,7 @@ __device__ __forceinline__ void append_row(const AppendArgs& a, const uint4& raw
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] = x[e ^ 1];
         } else {
-            const int from = lane - c + (turns ? (c < half_chunks ? c + half_chunks : c - half_chunks) : c);
+            from = lane - c + (turns ? (c < half_chunks ? c + half_chunks : c - half_chunks) : c);
             other.x = __shfl_sync(0xffffffffu, raw.x, from);
             other.y = __shfl_sync(0xffffffffu, raw.y, from);
             other.z = __shfl_sync(0xffffffffu, raw.z, from);
@@ -290,13 +300,6 @@ __device__ __forceinline__ void append_row(const AppendArgs& a, const uint4& raw
             unpack8<BF16>(other, y);
         }
         if (turns) {
-            if (KV4 && !QUERY) {
-                // Two roundings of at most |x cos| and |x cos| + |y sin|.
-                float most = 0.f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) most = fmaxf(most, fmaxf(fabsf(x[e]), fabsf(y[e])));
-                err = 1.8e-7f * most;  // 3 * 2^-24
-            }
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const float4 co = cs[(2 * u) * kChunks], si = cs[(2 * u + 1) * kChunks];
@@ -320,9 +323,7 @@ __device__ __forceinline__ void append_row(const AppendArgs& a, const uint4& raw
     if constexpr (KV4) {
         __half scale, zero;
         float code[8];
-        err = fmaxf(err, __shfl_xor_sync(0xffffffffu, err, 1));
-        err = fmaxf(err, __shfl_xor_sync(0xffffffffu, err, 2));
-        const uint32_t unsure = __ballot_sync(0xffffffffu, quantise(x, err, code, scale, zero));
+        const uint32_t unsure = __ballot_sync(0xffffffffu, quantise(x, turns, from, code, scale, zero));
         if (unsure != 0u) {
             const uint32_t group = 15u << (lane & ~3);
             if (unsure & group) {
