@@ -35,7 +35,7 @@ __device__ uint32_t g_append_error_word;
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 4;       // rows that a thread has on their way
+constexpr int kAhead = 2;       // rows that a thread has on their way
 constexpr int kTurns = 16;      // rows that a thread takes, where there are enough
 constexpr int kMaxTokens = 16;  // tokens of a block
 constexpr float kFp16Max = 65504.f;
@@ -474,7 +474,7 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, Shared<D>& sh,
 
 // The first blocks take key and value rows (more work each), the rest query rows.
 template <int D, bool BF16, bool KV4>
-__global__ void __launch_bounds__(kThreads, KV4 ? 4 : 5) cache_append_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, 5) cache_append_kernel(const __grid_constant__ AppendArgs a) {
     __shared__ Shared<D> sh;
     grid_dependency();
     const bool query = blockIdx.x >= a.kv_blocks;

@@ -46,6 +46,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kPart = 16;                 // keys that lie in one page and take one pass of the products
 constexpr int kMaxCtas = 320;             // parts in the workspace: two per CTA
 constexpr int kMaxParts = 64;             // CTAs a sequence is cut between: one CTA joins the parts
+constexpr float kLeastFactor = 1.2e-38f;  // keeps masked scores -inf at scale 0
 constexpr float kLow = -3.0e38f;          // the running max of a row that has seen no key
 constexpr float kRescaleThreshold = 8.0f; // log2 units: P <= 2^8 while the max is stale
 
@@ -217,7 +218,7 @@ struct Warp {
     static constexpr int kQ = D / 16;   // k-steps of S^T, m-tiles of O^T
     uint32_t q[NT][kQ][2];              // B fragments of Q^T
     uint32_t qsum[NT];                  // 4 bits: (high, low) part of the sum of q over group t
-    float f[NT][2];                     // log2-score of one unit of S, rows 2t and 2t+1
+    float f[NT][2];                     // log2-score of one unit of S, rows 2t and 2t+1 (> 0)
     float m[NT][2], l[NT][2];
     float o[NT][kQ][4];
 
@@ -238,7 +239,7 @@ struct Warp {
                     q[n][kk][0] = src ? *reinterpret_cast<const uint32_t*>(src + 16 * kk + 2 * t) : 0u;
                     q[n][kk][1] = src ? *reinterpret_cast<const uint32_t*>(src + 16 * kk + 8 + 2 * t) : 0u;
                 }
-                f[n][0] = f[n][1] = a.scale_log2;
+                f[n][0] = f[n][1] = fmaxf(a.scale_log2, kLeastFactor);
                 qsum[n] = 0u;
             } else {
                 // q as fp16 whatever its type: scaled by a power of two so that
@@ -287,8 +288,8 @@ struct Warp {
                 const float hi = __half2float(__float2half_rn(mine));
                 qsum[n] = pack16<false>(hi, mine - hi);
                 const float down = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - 9 + e) << 23);
-                f[n][0] = __shfl_sync(0xffffffffu, down, 8 * t);
-                f[n][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
+                f[n][0] = fmaxf(__shfl_sync(0xffffffffu, down, 8 * t), kLeastFactor);
+                f[n][1] = fmaxf(__shfl_sync(0xffffffffu, down, 8 * t + 4), kLeastFactor);
             }
             m[n][0] = m[n][1] = kLow;
             l[n][0] = l[n][1] = 0.f;
@@ -297,7 +298,7 @@ struct Warp {
         }
     }
 
-    // What fetch() adds a page's row to: this lane's first 16 bytes (and, 4
+    // What rows_of() adds a page's row to: this lane's first 16 bytes (and, 4
     // bits, its key's scales), for K/V head kvh.
     struct Source {
         const uint8_t* k;
@@ -320,46 +321,59 @@ struct Warp {
         return f;
     }
 
-    // Starts the copies of part `part` of a stage: 16 keys from place `off` of
-    // `page` (`valid` of them are keys of the sequence; the rest become zero).
-    // FULL: all of them are.
+    // The rows from place `off` of `page` on.
+    static __device__ __forceinline__ Source rows_of(const DecodeArgs& a, const Source& f, int page, int off) {
+        Source r;
+        if constexpr (!KV4) {
+            const int64_t at = 2 * (page * a.page_stride + static_cast<int64_t>(off) * D);
+            r.k = f.k + at;
+            r.v = f.v + at;
+            r.scales = nullptr;
+        } else {
+            const uint64_t row = static_cast<uint64_t>(static_cast<uint32_t>(page)) *
+                                     static_cast<uint32_t>(a.Hkv * a.page_size) + static_cast<uint32_t>(off);
+            r.k = f.k + row * S::kCode;
+            r.v = f.v + row * S::kCode;
+            r.scales = f.scales + row * S::kMeta;
+        }
+        return r;
+    }
+
+    // Starts the copies of part `part` of a stage: 16 keys, `skip` rows further
+    // (`valid` of them are keys of the sequence; the rest become zero).  FULL:
+    // all of them are.
     template <bool FULL>
-    static __device__ __forceinline__ void fetch(const DecodeArgs& a, const Source& f, uint32_t stage, int part,
-                                                 int page, int off, int valid) {
+    static __device__ __forceinline__ void copy(const Source& f, uint32_t stage, int part, int skip, int valid) {
         const int lane = threadIdx.x % 32;
         if constexpr (!KV4) {
             constexpr int kChunks = D / 8, kRowsAtOnce = 32 / kChunks;
-            const int64_t at = 2 * (page * a.page_stride + static_cast<int64_t>(off) * D);
             const int c = lane % kChunks;
 #pragma unroll
             for (int i = 0; i < kPart / kRowsAtOnce; ++i) {
                 const int r = i * kRowsAtOnce + lane / kChunks;
                 const uint32_t dst = stage + r * 2 * D + ((c ^ (r & 7)) << 4);
                 const int bytes = FULL || r < valid ? 16 : 0;
-                cp_async16(dst, f.k + at + i * 512, bytes);
-                cp_async16(dst + S::kVOff, f.v + at + i * 512, bytes);
+                cp_async16(dst, f.k + skip * 2 * D + i * 512, bytes);
+                cp_async16(dst + S::kVOff, f.v + skip * 2 * D + i * 512, bytes);
             }
         } else {
             constexpr int kChunks = D / 32;  // 16-byte chunks of a row of codes
-            const uint64_t row = static_cast<uint64_t>(static_cast<uint32_t>(page)) *
-                                     static_cast<uint32_t>(a.Hkv * a.page_size) + static_cast<uint32_t>(off);
-            const uint8_t* k = f.k + row * S::kCode;
-            const uint8_t* v = f.v + row * S::kCode;
 #pragma unroll
             for (int i = 0; i < kPart * kChunks / 32; ++i) {
                 const int r = i * (32 / kChunks) + lane / kChunks, c = lane % kChunks;
                 const int bytes = FULL || r < valid ? 16 : 0;
-                cp_async16(stage + part * kPart * S::kCode + i * 512 + lane * 16, k + i * 512, bytes);
-                cp_async16(stage + S::kVOff + (part * kPart + r) * S::kVRow + c * 16, v + i * 512, bytes);
+                cp_async16(stage + part * kPart * S::kCode + i * 512 + lane * 16, f.k + skip * S::kCode + i * 512, bytes);
+                cp_async16(stage + S::kVOff + (part * kPart + r) * S::kVRow + c * 16, f.v + skip * S::kCode + i * 512,
+                           bytes);
             }
             const int r = lane % 16;
             const uint32_t dst = lane < 16 ? stage + S::kKMetaOff + (part * kPart + r) * S::kMeta
                                            : stage + S::kVOff + (part * kPart + r) * S::kVRow + S::kCode;
-            cp_async_small<S::kMeta>(dst, f.scales + row * S::kMeta, FULL || r < valid ? S::kMeta : 0);
+            cp_async_small<S::kMeta>(dst, f.scales + skip * S::kMeta, FULL || r < valid ? S::kMeta : 0);
         }
     }
 
-    // S^T of 16 keys of the stage, in log2 units: s[n][0..1] key g, s[n][2..3] key
+    // S^T of 16 keys of the stage, in units of f: s[n][0..1] key g, s[n][2..3] key
     // g + 8, rows 2t and 2t+1.
     __device__ __forceinline__ void scores(uint32_t stage, int part, float (&s)[NT][4]) const {
         const int lane = threadIdx.x % 32;
@@ -373,13 +387,6 @@ struct Warp {
                 ldmatrix4(k, stage + r * 2 * D + (((2 * kk + lane / 16) ^ (r & 7)) << 4));
 #pragma unroll
                 for (int n = 0; n < NT; ++n) mma16816<BF16>(s[n], k, q[n][kk][0], q[n][kk][1]);
-            }
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                s[n][0] *= f[n][0];
-                s[n][1] *= f[n][1];
-                s[n][2] *= f[n][0];
-                s[n][3] *= f[n][1];
             }
         } else {
             // sum_d q_d (c_d scale + zero) = sum over groups of scale (sum q c) +
@@ -434,7 +441,7 @@ struct Warp {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int x = 0; x < 4; ++x) s[n][x] = fmaf(s[n][x], 16777216.f, zs[n][x]) * f[n][x & 1];
+                for (int x = 0; x < 4; ++x) s[n][x] = fmaf(s[n][x], 16777216.f, zs[n][x]);
         }
     }
 
@@ -555,6 +562,7 @@ struct Warp {
                 mx[n][x] = fmaxf(s[0][n][x], s[0][n][x + 2]);
 #pragma unroll
                 for (int u = 1; u < P; ++u) mx[n][x] = fmaxf(mx[n][x], fmaxf(s[u][n][x], s[u][n][x + 2]));
+                mx[n][x] *= f[n][x];
                 grow |= mx[n][x] > m[n][x] + kRescaleThreshold;
             }
         if (__any_sync(0xffffffffu, grow)) {
@@ -581,8 +589,8 @@ struct Warp {
             uint32_t p[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const float p0 = ex2(s[u][n][0] - m[n][0]), p1 = ex2(s[u][n][1] - m[n][1]);
-                const float p2 = ex2(s[u][n][2] - m[n][0]), p3 = ex2(s[u][n][3] - m[n][1]);
+                const float p0 = ex2(fmaf(s[u][n][0], f[n][0], -m[n][0])), p1 = ex2(fmaf(s[u][n][1], f[n][1], -m[n][1]));
+                const float p2 = ex2(fmaf(s[u][n][2], f[n][0], -m[n][0])), p3 = ex2(fmaf(s[u][n][3], f[n][1], -m[n][1]));
                 l[n][0] += p0 + p2;
                 l[n][1] += p1 + p3;
                 // P rounded to the operands' type (fp16 beside 4-bit values), key by
@@ -754,11 +762,16 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
                 for (int u = 0; u < S::kParts; ++u)
                     fine = fine && static_cast<uint32_t>(pages.p[u]) < static_cast<uint32_t>(a.num_pages);
                 skip &= ~bits;
-                if (fine) {
+                if (fine && one_page) {
+                    const int off = page_shift >= 0 ? key & (a.page_size - 1) : key % a.page_size;
+                    const auto rows = w.rows_of(a, source, pages.p[0], off);
+#pragma unroll
+                    for (int u = 0; u < S::kParts; ++u) w.template copy<true>(rows, at, u, u * kPart, kPart);
+                } else if (fine) {
                     int off = page_shift >= 0 ? key & (a.page_size - 1) : key % a.page_size;
 #pragma unroll
                     for (int u = 0; u < S::kParts; ++u) {
-                        w.template fetch<true>(a, source, at, u, pages.p[u], off, kPart);
+                        w.template copy<true>(w.rows_of(a, source, pages.p[u], off), at, u, 0, kPart);
                         off += kPart;
                         if (off == a.page_size) off = 0;
                     }
@@ -775,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
                             page = 0;
                         }
                         const int valid = ((skip >> (stage * S::kParts + u)) & 1u) ? 0 : last - k;
-                        w.template fetch<false>(a, source, at, u, page, k % a.page_size, valid);
+                        w.template copy<false>(w.rows_of(a, source, page, k % a.page_size), at, u, 0, valid);
                     }
                 }
             }
