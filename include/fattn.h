@@ -434,15 +434,16 @@ FATTN_API int64_t fattn_decode_workspace_bytes(int64_t B, int64_t H, int64_t Hkv
  *
  * with k_j, v_j the rows of K/V head h / (H/Hkv) in page block_table[b][j /
  * page_size], place j mod page_size.  A row that sees no key gets O = 0 and
- * LSE = -inf.  Nothing but visible rows is read from the cache as numbers:
- * what a page holds behind the last token never reaches O.
+ * LSE = -inf.  What a page holds behind the last token never reaches O.  (With
+ * Nq > 1 a NaN or infinity in V of one of the newest Nq tokens also reaches the
+ * rows before it, whose weight of it is 0.)
  *
  *   q, o        : [B, H, Nq, D]; `strides` is a host array of 6: batch, head
  *                 and token stride of q, then of o.  o overlaps nothing else.
  *   lse         : fp32 [B, H, Nq] contiguous, or NULL.
  *   block_table : device int32 [B][table_width].
  *   seq_lens    : device int32 [B], 0 <= seq_lens[b] <= table_width*page_size
- *                 (and table_width*page_size < 2^31).
+ *                 (and table_width*page_size < 2^31 - 65536).
  *   workspace   : caller-owned, fattn_decode_workspace_bytes, 16-byte aligned;
  *                 contents ignored on entry.  Calls that run at the same time
  *                 (two streams, two graphs) need workspaces of their own.
@@ -459,7 +460,7 @@ FATTN_API int fattn_decode(const void* q, void* o, float* lse, const int64_t* st
 /*
  * fattn_decode_kv4 -- fattn_decode over a 4-bit cache (above).  q and o are
  * `dtype`; K's codes enter the products exactly and its scales in fp32, V is
- * taken as fp16(code * scale + zero).
+ * taken as fp16(code * scale + zero), and the weights are rounded to fp16.
  */
 FATTN_API int fattn_decode_kv4(const void* q, void* o, float* lse, const int64_t* strides,
                      const void* k_codes, const void* k_scales, const void* v_codes,

@@ -369,29 +369,103 @@ def test_decode_strides_and_page_stride():
     assert torch.equal(both.nan_to_num(9.0), before.nan_to_num(9.0))
 
 
-def test_offsets_past_32_bits():
-    """A 16-bit pool of more than 2^32 bytes and 2^31 elements per tensor: the
-    last pages are written and read where they are."""
+@pytest.mark.parametrize("kv4", [False, True])
+def test_offsets_past_32_bits(kv4):
+    """A pool of more than 2^32 bytes per tensor (16 bits: more than 2^31
+    elements): the last pages are written and read where they are."""
     Hkv, ps, D = 8, 64, 128
-    P = (1 << 31) // (Hkv * ps * D) + 40
-    cache = [torch.empty(P, Hkv, ps, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    P = (1 << 32) // (Hkv * ps * (D // 2 if kv4 else 2 * D)) + 40
+    if kv4:
+        cache = []
+        for _ in range(2):
+            cache += [torch.empty(P, Hkv, ps, D // 2, dtype=torch.uint8, device="cuda"),
+                      torch.empty(P, Hkv, ps, D // 32, 2, dtype=torch.float16, device="cuda")]
+    else:
+        cache = [torch.empty(P, Hkv, ps, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
     n = 150
     pages = torch.tensor([P - 1, 3, P - 7], dtype=torch.int32)
     q, k, v = qkv_slices(n, 16, Hkv, D, torch.bfloat16, 13)
     j = torch.arange(n)
     slots = pages.long()[j // ps] * ps + j % ps
-    fattn.cache_append(k, v, *cache, slots.cuda())
+    append(kv4, k, v, cache, slots.cuda())
     qd = q[-1:].unsqueeze(2).contiguous()
-    o, lse = fattn.decode(qd, *cache, pages[None].cuda(), torch.tensor([n], dtype=torch.int32).cuda(), scale=0.1)
-    ok()
-    small = [torch.zeros(3, Hkv, ps, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
-    fattn.cache_append(k, v, *small, j.cuda())
-    table = torch.arange(3, dtype=torch.int32)[None].cuda()
     lens = torch.tensor([n], dtype=torch.int32).cuda()
-    o2, lse2 = fattn.decode(qd, *small, table, lens, scale=0.1)
+    o, lse = run_decode(kv4, qd, cache, pages[None].cuda(), lens, scale=0.1)
+    ok()
+    small = new_cache(kv4, 3, Hkv, ps, D, torch.bfloat16, 0.0)
+    append(kv4, k, v, small, j.cuda())
+    table = torch.arange(3, dtype=torch.int32)[None].cuda()
+    o2, lse2 = run_decode(kv4, qd, small, table, lens, scale=0.1)
     ok()
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
-    check_decode(False, qd, small, table, lens, 0.1, o, lse)
+    check_decode(kv4, qd, small, table, lens, 0.1, o, lse)
+
+
+@pytest.mark.parametrize("kv4", [False, True])
+def test_decode_more_sequences_than_threads(kv4):
+    """The prefix sums over sequences run in pieces; many are empty, one is long."""
+    g = torch.Generator().manual_seed(17)
+    lens = torch.randint(0, 40, (700,), generator=g)
+    lens[torch.randperm(700, generator=g)[:200]] = 0
+    lens[601] = 3000
+    q, cache, table, lens = make_decode(kv4, lens.tolist(), 4, 2, 1, 64, 16, "fp16", 18)
+    o, lse = run_decode(kv4, q, cache, table, lens)
+    ok()
+    check_decode(kv4, q, cache, table, lens, 0.125, o, lse)
+
+
+@pytest.mark.parametrize("kv4", [False, True])
+def test_decode_workspace_contents_are_ignored(kv4):
+    """Whatever the workspace holds on entry, also what calls of other shapes
+    left in it, the result is the same."""
+    n = [2000, 0, 300, 5000]
+    q, cache, table, lens = make_decode(kv4, n, 8, 2, 1, 128, 32, "bf16", 19)
+    want, want_l = run_decode(kv4, q, cache, table, lens)
+    ws = torch.empty(fattn.decode_workspace_bytes(4, 64, 4, 128, 2), dtype=torch.uint8, device="cuda")
+    other = make_decode(kv4, [700, 900], 64, 2, 4, 128, 16, "bf16", 20)
+    for fill in (0, 1, 0x5B, 0xFF, None, None):
+        if fill is None:  # a call of another shape, with the same workspace, right before
+            run_decode(kv4, *other, workspace=ws)
+        else:
+            ws.fill_(fill)
+        for _ in range(2):
+            o, lse = run_decode(kv4, q, cache, table, lens, workspace=ws)
+            ok()
+            assert torch.equal(o, want) and torch.equal(lse, want_l)
+    g = torch.Generator(device="cuda").manual_seed(21)
+    for _ in range(3):
+        ws.random_(0, 256, generator=g)
+        o, lse = run_decode(kv4, q, cache, table, lens, workspace=ws)
+        ok()
+        assert torch.equal(o, want) and torch.equal(lse, want_l)
+
+
+@pytest.mark.parametrize("kv4", [False, True])
+def test_decode_non_finite_query_stays_in_its_row(kv4):
+    q, cache, table, lens = make_decode(kv4, [100, 260], 8, 2, 2, 64, 16, "fp16", 22)
+    want, want_l = run_decode(kv4, q, cache, table, lens)
+    for bad in (math.nan, math.inf):
+        q2 = q.clone()
+        q2[0, 3, 1, 5] = bad
+        q2[1, 6, 0, :] = bad
+        o, lse = run_decode(kv4, q2, cache, table, lens)
+        ok()
+        keep = torch.ones(q.shape[:3], dtype=torch.bool, device="cuda")
+        keep[0, 3, 1] = keep[1, 6, 0] = False
+        assert torch.equal(o[keep], want[keep]) and torch.equal(lse[keep], want_l[keep])
+        assert torch.isnan(o[~keep]).all()
+
+
+def test_decode_padded_batch_and_shared_pages():
+    """Rows of a padded batch have length 0; sequences may share pages."""
+    H, Hkv, D, ps = 8, 4, 128, 16
+    q, cache, table, lens = make_decode(False, [120, 64, 0, 0], H, Hkv, 1, D, ps, "bf16", 23)
+    table[2:] = table[0]
+    table[1, :2] = table[0, :2]
+    table[1, 2:4] = table[0, 4:6]
+    o, lse = fattn.decode(q, *cache, table, lens)
+    ok()
+    check_decode(False, q, cache, table, lens, fattn._default_scale(D), o, lse)
 
 
 @pytest.mark.parametrize("kv4", [False, True])

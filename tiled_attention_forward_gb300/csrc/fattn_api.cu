@@ -827,7 +827,8 @@ int run_decode(DecodeArgs& a, const int64_t* strides, int64_t num_pages, int64_t
     if (!std::isfinite(scale) || scale < 0.f) return FATTN_ERR_INVALID_ARG;
     if (B == 0 || H == 0 || Nq == 0) return FATTN_OK;
     const int64_t need = fattn_decode_workspace_bytes(B, H, Hkv, Nq, D);
-    if (need <= 0 || table_width > 0x7fffffffll / page_size) return FATTN_ERR_UNSUPPORTED;
+    // Key indices are ints, and the last unit of keys ends past the last key.
+    if (need <= 0 || table_width > (0x7fffffffll - 65536) / page_size) return FATTN_ERR_UNSUPPORTED;
     if (!a.q || !a.o || !a.k_pages || !a.v_pages || (kv4 && (!a.k_scales || !a.v_scales)) || !a.seq_lens ||
         (table_width > 0 && !a.block_table) || !a.workspace || ws_bytes < need)
         return FATTN_ERR_INVALID_ARG;

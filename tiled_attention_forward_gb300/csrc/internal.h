@@ -44,7 +44,9 @@ inline cudaError_t launch_overlapped(void (*fn)(A), unsigned grid, unsigned thre
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fn, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, a);
+    if (e != cudaSuccess) (void)cudaGetLastError();  // reported here, not left for the caller's next check
+    return e;
 }
 #ifdef __CUDACC__
 // Every thread of a kernel launched so calls this first.  (The next kernel may
