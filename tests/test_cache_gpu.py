@@ -543,3 +543,27 @@ def test_append_kv4_ties_round_to_even(dtype):
         ties += ((q - q.floor()) == 0.5).sum().item()
         assert torch.equal(c, q.round())
     assert ties > 1000
+
+
+@pytest.mark.parametrize("kv4", [False, True])
+@pytest.mark.parametrize("dtype,D,H,Hkv,Nq,ps", [("bf16", 128, 8, 8, 1, 16), ("fp16", 64, 16, 1, 1, 32),
+                                                ("bf16", 64, 32, 2, 2, 48), ("fp16", 128, 40, 1, 2, 16),
+                                                ("bf16", 128, 16, 1, 1, 64), ("fp16", 64, 6, 6, 3, 16)])
+def test_decode_short_sequences(dtype, D, H, Hkv, Nq, ps, kv4):
+    """Many short sequences (where there are enough, a warp takes each), some of
+    the next longer kind among them."""
+    g = torch.Generator().manual_seed(24)
+    B = 660 // Hkv + 1
+    lens = torch.randint(0, 300, (B,), generator=g)
+    lens[::7] = torch.randint(200, 700, (len(lens[::7]),), generator=g)
+    lens[3] = lens[4] = 0
+    lens[50] = 40
+    q, cache, table, lens = make_decode(kv4, lens.tolist(), H, Hkv, Nq, D, ps, dtype, 25)
+    table[50, 0] = -1  # a page out of range: that sequence alone changes
+    o, lse = run_decode(kv4, q, cache, table, lens)
+    torch.cuda.synchronize()
+    assert fattn.get_device_status() == INVALID
+    keep = torch.arange(B) != 50
+    check_decode(kv4, q[keep.cuda()], cache, table[keep.cuda()], lens[keep.cuda()], fattn._default_scale(D),
+                 o[keep.cuda()], lse[keep.cuda()])
+    assert torch.isfinite(o[50]).all()

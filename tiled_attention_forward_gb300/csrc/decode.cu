@@ -45,6 +45,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kPart = 16;                 // keys that lie in one page and take one pass of the products
 constexpr int kMaxCtas = 320;             // parts in the workspace: two per CTA
+constexpr int kAloneUnits = 2;            // longest target that one warp takes alone
 constexpr int kMaxParts = 64;             // CTAs a sequence is cut between: one CTA joins the parts
 constexpr float kLeastFactor = 1.2e-38f;  // keeps masked scores -inf at scale 0
 constexpr float kLow = -3.0e38f;          // the running max of a row that has seen no key
@@ -148,6 +149,7 @@ struct Config {
     static constexpr int kJoin = kWarps * kRows * kPitch * 4;
     static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
     static_assert(kSmem * kCtasPerSm <= 224 * 1024, "shared memory budget");
+    static_assert(8 * kPitch * 4 <= kStages * Stage<D, KV4, NT>::kBytes, "a warp's O, eight rows at a time, in its ring");
 };
 
 // A part of a cut sequence: per row the max (log2 units), the sum, then O.
@@ -603,7 +605,7 @@ struct Warp {
     }
 };
 
-template <int D, bool BF16, bool KV4, int NT>
+template <int D, bool BF16, bool KV4, int NT, bool ALONE>
 __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
     decode_kernel(const __grid_constant__ DecodeArgs a) {
     using C = Config<D, KV4, NT>;
@@ -707,38 +709,82 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
         // The extra units come first; tiles [t0, t1) are this CTA's.
         const int t0 = max(place - C::kTargetCost, 0), t1 = place + taken - C::kTargetCost;
         const int64_t target_at = at - place;  // the target's first unit
-        at += taken;
-        if (at - seq_at == static_cast<int64_t>(cost) * per_key) {
-            seq_at = at;
-            ++next_b;
+
+        // Short targets that lie whole in this share: up to kWarps of them at
+        // once, a warp each, and nothing to join.  Worth it where there are
+        // more of them than units in the longest (a warp alone takes kWarps
+        // turns a unit, about what starting and joining a target costs).
+        int batch = 0, my_b = b, my_target = target, my_len = len;
+        if (ALONE && place <= C::kTargetCost && tiles <= kAloneUnits) {
+            int w_b = b, w_target = target, w_len = len, longest = 0;
+            int64_t w_at = target_at, w_seq = seq_at;
+            while (batch < kWarps) {
+                const int n = units_of<S::kUnit>(w_len);
+                if (n > kAloneUnits || w_at + n + C::kTargetCost > end) break;
+                if (batch == warp) {
+                    my_b = w_b;
+                    my_target = w_target;
+                    my_len = w_len;
+                }
+                longest = max(longest, n);
+                ++batch;
+                w_at += n + C::kTargetCost;
+                if (++w_target == per_key) {
+                    w_target = 0;
+                    ++w_b;
+                    w_seq = w_at;
+                    if (w_at >= end) break;
+                    w_len = visible_len(a, w_b, false);
+                }
+                if (w_at >= end) break;
+            }
+            if (batch > longest && batch > 1) {
+                at = w_at;
+                seq_at = w_seq;
+                next_b = w_b;
+            } else {
+                batch = 0;
+                my_b = b;
+                my_target = target;
+                my_len = len;
+            }
         }
-        if (t1 <= t0) {
-            b = next_b;
-            continue;
+        const bool alone = ALONE && batch > 0;
+        if (!alone) {
+            at += taken;
+            if (at - seq_at == static_cast<int64_t>(cost) * per_key) {
+                seq_at = at;
+                ++next_b;
+            }
+            if (t1 <= t0) {
+                b = next_b;
+                continue;
+            }
         }
-        const int kvh = target / row_blocks, rb = target - kvh * row_blocks;
-        const int32_t* table = a.block_table + b * a.table_width;
+        const int kvh = my_target / row_blocks, rb = my_target - kvh * row_blocks;
+        const int32_t* table = a.block_table + my_b * a.table_width;
 
         int ends[NT][2];
-        const int min_end = len - a.Nq + 1;
+        const int min_end = my_len - a.Nq + 1;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const int r = rb * C::kRows + n * 8 + (lane % 4) * 2 + x;
-                ends[n][x] = r < rows ? min_end + r % a.Nq : len;  // rows that are none: anything finite
+                ends[n][x] = r < rows ? min_end + r % a.Nq : my_len;  // rows that are none: anything finite
             }
 
-        // This warp's keys: kKeys at first + kUnit i.
-        const int first = t0 * S::kUnit + warp * S::kKeys;
-        const int last = min(len, t1 * S::kUnit);
-        const int turns = first < last ? (last - first + S::kUnit - 1) / S::kUnit : 0;
+        // This warp's keys: kKeys at first + stride i.
+        const int stride = alone ? S::kKeys : S::kUnit;
+        const int first = alone ? 0 : t0 * S::kUnit + warp * S::kKeys;
+        const int last = alone ? (warp < batch ? my_len : 0) : min(len, t1 * S::kUnit);
+        const int turns = first < last ? (last - first + stride - 1) / stride : 0;
         const typename Warp<D, BF16, KV4, NT>::Source source = w.source(a, kvh);
         struct Pages {
             int p[S::kParts];
         };
         auto pages_at = [&](int i) -> Pages {  // the pages of turn i's parts (any where there are none)
-            const int key = first + i * S::kUnit;
+            const int key = first + i * stride;
             Pages r;
 #pragma unroll
             for (int u = 0; u < S::kParts; ++u) {
@@ -755,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
             if (i < turns) {
                 const int stage = i % C::kStages;
                 const uint32_t at = ring + stage * S::kBytes;
-                const int key = first + i * S::kUnit;
+                const int key = first + i * stride;
                 const uint32_t bits = ((1u << S::kParts) - 1u) << (stage * S::kParts);
                 bool fine = last - key >= S::kKeys;
 #pragma unroll
@@ -803,19 +849,57 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
             for (int i = 0; i < C::kStages - 1; ++i) start(i, early[i]);
             pages = early[C::kStages - 1];
         }
-        w.load_q(a, b, kvh, rb);
+        w.load_q(a, my_b, kvh, rb);
         for (int i = 0; i < turns; ++i) {
             start(i + C::kStages - 1, pages);
             pages = pages_at(i + C::kStages);  // needed one turn later
             cp_async_wait<C::kStages - 1>();
             __syncwarp();
             const int stage = i % C::kStages;
-            const int key = first + i * S::kUnit;
+            const int key = first + i * stride;
             const uint32_t none = (skip >> (stage * S::kParts)) & ((1u << S::kParts) - 1u);
             w.keys(ring + stage * S::kBytes, key, key + S::kKeys > min_end || none != 0u, none, ends);
             __syncwarp();  // every lane is done with the stage before it is filled again
         }
         cp_async_wait<0>();
+
+        if (alone) {
+            // The warp's own O, eight rows at a time through its ring.
+            if (warp < batch) {
+                float* mine = reinterpret_cast<float*>(smem + warp * C::kStages * S::kBytes);
+                const int g = lane / 4, t = lane % 4;
+                __syncwarp();
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float l[2];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        l[x] = w.l[n][x];
+#pragma unroll
+                        for (int d = 4; d < 32; d *= 2) l[x] += __shfl_xor_sync(0xffffffffu, l[x], d);
+#pragma unroll
+                        for (int j = 0; j < D / 16; ++j) {
+                            mine[(2 * t + x) * C::kPitch + w.dim_of(j, 0, g)] = w.o[n][j][x];
+                            mine[(2 * t + x) * C::kPitch + w.dim_of(j, 1, g)] = w.o[n][j][x + 2];
+                        }
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) {
+                        const float sum = __shfl_sync(0xffffffffu, l[r & 1], r / 2);
+                        const float mx = __shfl_sync(0xffffffffu, w.m[n][r & 1], r / 2);
+                        if (4 * lane < D) {
+                            const float4 v = *reinterpret_cast<const float4*>(mine + r * C::kPitch + 4 * lane);
+                            const float acc[4] = {v.x, v.y, v.z, v.w};
+                            store_out<D, BF16>(a, my_b, kvh, rb * C::kRows + n * 8 + r, 4 * lane, acc, mx, sum);
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+            b = next_b;
+            continue;
+        }
 
         // Join the eight warps: their O by rows, in the ring's memory.
         __syncthreads();
@@ -923,10 +1007,10 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
     }
 }
 
-template <int D, bool BF16, bool KV4, int NT>
+template <int D, bool BF16, bool KV4, int NT, bool ALONE>
 cudaError_t launch_one(const DecodeArgs& a, int sms, cudaStream_t s) {
     using C = Config<D, KV4, NT>;
-    auto* fn = decode_kernel<D, BF16, KV4, NT>;
+    auto* fn = decode_kernel<D, BF16, KV4, NT, ALONE>;
     static std::atomic<bool> done[kMaxDevices] = {};
     cudaError_t e = opt_in_smem_once(fn, C::kSmem, done);
     if (e != cudaSuccess) return e;
@@ -937,12 +1021,26 @@ cudaError_t launch_one(const DecodeArgs& a, int sms, cudaStream_t s) {
 // Tiles of 8 query rows that share one pass over the keys.
 int row_tiles(int64_t rows) { return rows <= 8 ? 1 : (rows <= 16 ? 2 : 4); }
 
+// Whether short targets may be taken by one warp each: only where a CTA's share
+// holds two targets or more on average.  (200 sequences of up to 300 tokens, 8
+// K/V heads: 42.6 -> 33.6 us.  The kernel that can loses 2 % on long sequences
+// and 4 to 10 % on the smallest calls to the registers that this takes, and
+// with 32 query rows 6 to 10 % everywhere, so that form does not exist.)
+template <int D, bool BF16, bool KV4, int NT>
+cudaError_t launch_targets(const DecodeArgs& a, int sms, cudaStream_t s) {
+    if constexpr (NT <= 2) {
+        const int64_t targets = static_cast<int64_t>(a.B) * a.Hkv;
+        if (targets >= 2 * sms * Config<D, KV4, NT>::kCtasPerSm) return launch_one<D, BF16, KV4, NT, true>(a, sms, s);
+    }
+    return launch_one<D, BF16, KV4, NT, false>(a, sms, s);
+}
+
 template <int D, bool BF16, bool KV4>
 cudaError_t launch_rows(const DecodeArgs& a, int sms, cudaStream_t s) {
     switch (row_tiles(static_cast<int64_t>(a.H / a.Hkv) * a.Nq)) {
-        case 1: return launch_one<D, BF16, KV4, 1>(a, sms, s);
-        case 2: return launch_one<D, BF16, KV4, 2>(a, sms, s);
-        default: return launch_one<D, BF16, KV4, 4>(a, sms, s);
+        case 1: return launch_targets<D, BF16, KV4, 1>(a, sms, s);
+        case 2: return launch_targets<D, BF16, KV4, 2>(a, sms, s);
+        default: return launch_targets<D, BF16, KV4, 4>(a, sms, s);
     }
 }
 
