@@ -82,9 +82,9 @@ KERNEL_SOURCES = {"tc": ["fwd_tc.cu", "fwd_tc_kernel.cuh", "sm103_ptx.cuh"], "ff
                   "unfused": ["fwd_unfused.cu", "sm103_ptx.cuh"],
                   "bwd": ["bwd_tc.cu", "sm103_ptx.cuh"]}
 NCU_TRAFFIC = {
-    "bf16_B4_H16_N4096_D128": (201829632 + 39738624, "3a3002c616902885"),
-    "bf16_B2_H32_N8192_D128_causal_qstd4": (410912768 + 111794176, "3a3002c616902885"),
-    "fp16_B1_H16_N16000_D64_causal": (98407936 + 10369024, "3a3002c616902885"),
+    "bf16_B4_H16_N4096_D128": (202378496 + 37780992, "0629ca7bfe420bee"),
+    "bf16_B2_H32_N8192_D128_causal_qstd4": (409667584 + 107061760, "0629ca7bfe420bee"),
+    "fp16_B1_H16_N16000_D64_causal": (98405376 + 7730688, "0629ca7bfe420bee"),
     "fp32_B4_H8_N8192_D64_causal": (201639936 + 51146240, "61c5185890f7842f"),
 }
 

@@ -21,6 +21,14 @@
 // its rows before the tokens' slots, positions and angles (which depend on one
 // another) have come, and the angles go through shared memory once for all
 // heads.
+//
+// Measured (GB300): 8191 tokens of 16 + 2 * 2 heads, D = 64, 16 bits (45 MB) 13
+// us, of which about 2.5 are the launch; 16000 tokens of 32 + 2 * 8 heads, D =
+// 128, into 4 bits (422 MB with the values held) 106 us, 4.0 TB/s, bound by
+// issue slots (about 190 instructions for 16 bytes of a key or value row).  64
+// tokens take 2.6 us.  Two rows ahead and five blocks an SM: four ahead cost
+// registers (115 us at four blocks), one ahead 110.  16 rows a thread: 8 took 110
+// (blocks' starts), 32 the same 106.
 #include <algorithm>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
