@@ -108,6 +108,22 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// c = a b: no accumulator to set to zero first.
+template <bool BF16>
+__device__ __forceinline__ void mma16816_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if (BF16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%10, %10, %10, %10};"
+            : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%10, %10, %10, %10};"
+            : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -390,15 +406,17 @@ struct Warp {
     __device__ __forceinline__ void scores(uint32_t stage, int part, float (&s)[NT][4]) const {
         const int lane = threadIdx.x % 32;
         if constexpr (!KV4) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
             const int r = (lane & 7) + (lane & 8);
 #pragma unroll
             for (int kk = 0; kk < kQ; ++kk) {
                 uint32_t k[4];
                 ldmatrix4(k, stage + r * 2 * D + (((2 * kk + lane / 16) ^ (r & 7)) << 4));
 #pragma unroll
-                for (int n = 0; n < NT; ++n) mma16816<BF16>(s[n], k, q[n][kk][0], q[n][kk][1]);
+                for (int n = 0; n < NT; ++n)
+                    if (kk == 0)
+                        mma16816_first<BF16>(s[n], k, q[n][kk][0], q[n][kk][1]);
+                    else
+                        mma16816<BF16>(s[n], k, q[n][kk][0], q[n][kk][1]);
             }
         } else {
             // sum_d q_d (c_d scale + zero) = sum over groups of scale (sum q c) +
@@ -422,11 +440,7 @@ struct Warp {
             }
             float zs[NT][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                zs[n][0] = zs[n][1] = zs[n][2] = zs[n][3] = 0.f;
-                mma16816<false>(zs[n], z, qsum[n], 0u);
-                s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-            }
+            for (int n = 0; n < NT; ++n) mma16816_first<false>(zs[n], z, qsum[n], 0u);
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
                 uint32_t a0[4], a1[4];
@@ -441,13 +455,13 @@ struct Warp {
                 const float sc0 = __low2float(as_half2(meta[0][i])), sc1 = __low2float(as_half2(meta[1][i]));
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    float c[4] = {0.f, 0.f, 0.f, 0.f};
-                    mma16816<false>(c, a0, q[n][2 * i][0], q[n][2 * i][1]);
+                    float c[4];
+                    mma16816_first<false>(c, a0, q[n][2 * i][0], q[n][2 * i][1]);
                     mma16816<false>(c, a1, q[n][2 * i + 1][0], q[n][2 * i + 1][1]);
-                    s[n][0] = fmaf(c[0], sc0, s[n][0]);
-                    s[n][1] = fmaf(c[1], sc0, s[n][1]);
-                    s[n][2] = fmaf(c[2], sc1, s[n][2]);
-                    s[n][3] = fmaf(c[3], sc1, s[n][3]);
+                    s[n][0] = i == 0 ? c[0] * sc0 : fmaf(c[0], sc0, s[n][0]);
+                    s[n][1] = i == 0 ? c[1] * sc0 : fmaf(c[1], sc0, s[n][1]);
+                    s[n][2] = i == 0 ? c[2] * sc1 : fmaf(c[2], sc1, s[n][2]);
+                    s[n][3] = i == 0 ? c[3] * sc1 : fmaf(c[3], sc1, s[n][3]);
                 }
             }
 #pragma unroll
