@@ -67,7 +67,8 @@ typedef enum {
 
 typedef enum {
     FATTN_OK = 0,
-    FATTN_ERR_INVALID_ARG = 1,   /* null pointer, negative size, bad dtype, non-finite or negative scale, overlapping O */
+    FATTN_ERR_INVALID_ARG = 1,   /* null pointer, negative size, bad dtype, non-finite or negative scale, overlapping O;
+                                    from fattn_get_device_status: an entry of a device table out of range */
     FATTN_ERR_UNSUPPORTED = 2,   /* D not in {64, 128}; N or B*H above 2^30, or B*H*N*D above 2^52 */
     FATTN_ERR_MISALIGNED = 3,    /* a tensor pointer not 16-byte aligned (TMA / vector access requirement) */
     FATTN_ERR_CUDA = 4,          /* a CUDA runtime/driver call failed (launch, copy, tensor-map encode) */
@@ -308,6 +309,8 @@ FATTN_API int fattn_fwd_unfused_static(const void* q, const void* k, const void*
  * an entry out of range cannot be refused before the launch: the kernels skip
  * what it names, touch no memory outside the buffers, and
  * fattn_get_device_status then returns FATTN_ERR_INVALID_ARG.
+ * A kernel of these calls may be set up while the one before it on the stream
+ * still runs; it waits for that to complete before it touches memory.
  *
  * A paged cache is a pool of num_pages pages of page_size tokens (a multiple
  * of 16, at most 65536).  16 bits: k_pages and v_pages, each [num_pages]
