@@ -650,27 +650,40 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
     // All units of the call, and this CTA's share of them.  A target (K/V head
     // and row block of a sequence) counts C::kTargetCost units more than it has, so
     // that shares of many short sequences take no longer than others.
-    int64_t mine = 0;
-    int most = 0, first_cost = 0;
-    for (int b = tid; b < a.B; b += kThreads) {
-        const int n = units_of<S::kUnit>(visible_len(a, b, blockIdx.x == 0)) + C::kTargetCost;
-        if (b == tid) first_cost = n;
-        mine += n;
-        most = max(most, n);
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d /= 2) mine += __shfl_xor_sync(0xffffffffu, mine, d);
-    most = __reduce_max_sync(0xffffffffu, most);
-    if (lane == 0) {
-        s_scan[warp] = mine;
-        s_most[warp] = most;
-    }
-    __syncthreads();
     int64_t units = 0;
+    int most = 0, first_cost = 0, upto = 0;
+    const bool few = a.B <= 32;  // every warp does it for itself
+    if (few) {
+        first_cost = lane < a.B ? units_of<S::kUnit>(visible_len(a, lane, blockIdx.x == 0 && warp == 0)) + C::kTargetCost : 0;
+        upto = first_cost;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        units += s_scan[w];
-        most = max(most, s_most[w]);
+        for (int d = 1; d < 32; d *= 2) {
+            const int y = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += y;
+        }
+        units = __shfl_sync(0xffffffffu, upto, 31);
+        most = __reduce_max_sync(0xffffffffu, first_cost);
+    } else {
+        int64_t mine = 0;
+        for (int b = tid; b < a.B; b += kThreads) {
+            const int n = units_of<S::kUnit>(visible_len(a, b, blockIdx.x == 0)) + C::kTargetCost;
+            if (b == tid) first_cost = n;
+            mine += n;
+            most = max(most, n);
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2) mine += __shfl_xor_sync(0xffffffffu, mine, d);
+        most = __reduce_max_sync(0xffffffffu, most);
+        if (lane == 0) {
+            s_scan[warp] = mine;
+            s_most[warp] = most;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            units += s_scan[w];
+            most = max(most, s_most[w]);
+        }
     }
     units *= per_key;
     // CTAs that get a share: no more than units, so that the CTAs a sequence is
@@ -682,40 +695,48 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
     if (cta >= ctas) return;
     const int64_t begin = share_begin(units, cta, ctas), end = share_begin(units, cta + 1, ctas);
     // The sequence of unit `begin`: prefix sums, kThreads sequences at a time.
-    int64_t before = 0;
-    for (int b0 = 0;; b0 += kThreads) {
-        __syncthreads();  // s_scan is read by all before it is written again
-        const int b = b0 + tid;
-        int64_t own = 0;
-        if (b < a.B)
-            own = static_cast<int64_t>(b0 == 0 ? first_cost
-                                               : units_of<S::kUnit>(visible_len(a, b, false)) + C::kTargetCost) * per_key;
-        int64_t x = own;
+    int b;
+    int64_t seq_at;  // first unit of sequence b
+    if (few) {
+        const uint32_t past = __ballot_sync(0xffffffffu, lane < a.B && static_cast<int64_t>(upto) * per_key > begin);
+        b = __ffs(past) - 1;
+        seq_at = static_cast<int64_t>(__shfl_sync(0xffffffffu, upto - first_cost, b)) * per_key;
+    } else {
+        int64_t before = 0;
+        for (int b0 = 0;; b0 += kThreads) {
+            __syncthreads();  // s_scan is read by all before it is written again
+            const int b = b0 + tid;
+            int64_t own = 0;
+            if (b < a.B)
+                own = static_cast<int64_t>(b0 == 0 ? first_cost
+                                                   : units_of<S::kUnit>(visible_len(a, b, false)) + C::kTargetCost) * per_key;
+            int64_t x = own;
 #pragma unroll
-        for (int d = 1; d < 32; d *= 2) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
-            if (lane >= d) x += y;
+            for (int d = 1; d < 32; d *= 2) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+                if (lane >= d) x += y;
+            }
+            if (lane == 31) s_scan[warp] = x;
+            __syncthreads();
+            int64_t left = before, all = before;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                if (w < warp) left += s_scan[w];
+                all += s_scan[w];
+            }
+            x += left;
+            if (own > 0 && begin >= x - own && begin < x) {
+                s_first = b;
+                s_begin = x - own;
+            }
+            before = all;
+            if (before > begin || b0 + kThreads >= a.B) break;
         }
-        if (lane == 31) s_scan[warp] = x;
         __syncthreads();
-        int64_t left = before, all = before;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) left += s_scan[w];
-            all += s_scan[w];
-        }
-        x += left;
-        if (own > 0 && begin >= x - own && begin < x) {
-            s_first = b;
-            s_begin = x - own;
-        }
-        before = all;
-        if (before > begin || b0 + kThreads >= a.B) break;
+        b = s_first;
+        seq_at = s_begin;
     }
-    __syncthreads();
 
-    int b = s_first;
-    int64_t seq_at = s_begin;  // first unit of sequence b
     uint32_t ring = smem_addr(smem) + warp * C::kStages * S::kBytes;
     const int page_shift = (a.page_size & (a.page_size - 1)) == 0 ? __ffs(a.page_size) - 1 : -1;
     const bool one_page = a.page_size % S::kKeys == 0;  // a stage never crosses pages
