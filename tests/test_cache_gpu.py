@@ -567,3 +567,32 @@ def test_decode_short_sequences(dtype, D, H, Hkv, Nq, ps, kv4):
     check_decode(kv4, q[keep.cuda()], cache, table[keep.cuda()], lens[keep.cuda()], fattn._default_scale(D),
                  o[keep.cuda()], lse[keep.cuda()])
     assert torch.isfinite(o[50]).all()
+
+
+@pytest.mark.parametrize("D,rot,dtype,interleaved", [(128, 128, "bf16", False), (64, 32, "fp16", True),
+                                                     (64, 64, "bf16", False)])
+def test_append_kv4_rotated_codes_are_the_definitions(D, rot, dtype, interleaved):
+    """Of 50000 groups and more, some hundred lie so close to a rounding's border
+    that fp32 cannot tell its side: all their codes, scales and zeros are those
+    of the rotation in 64 bits (scale and zero as fp16 of the nearest fp32)."""
+    T, Hkv, ps = 8000, 2, 16
+    g = torch.Generator().manual_seed(27)
+    k = (torch.randn(T, Hkv, D, generator=g) * 2.0 ** torch.randint(-9, 10, (T, 1, 1), generator=g)).to(DT[dtype])
+    k[5] = 0.0
+    k[6, 1, : D // 2] = 0.0
+    k[7] = 1.0
+    pos = torch.randint(0, 4096, (T,), generator=g, dtype=torch.int32)
+    cos, sin = R.tables(4096, rot)
+    cache = new_cache(True, T // ps, Hkv, ps, D, DT[dtype], 0.0)
+    fattn.cache_append_kv4(k.cuda(), k.cuda(), *cache, torch.arange(T).cuda(), pos=pos.cuda(), cos=cos.cuda(),
+                           sin=sin.cuda(), interleaved=interleaved)
+    ok()
+    x = R.rotate(k, pos, cos, sin, interleaved)[0].unflatten(-1, (-1, 32))
+    lo, hi = x.amin(-1), x.amax(-1)
+    scale, zero = ((hi - lo) / 15).float().half().double(), lo.float().half().double()
+    got = cache[1].cpu().double().transpose(1, 2).reshape(T, Hkv, D // 32, 2)
+    assert torch.equal(got[..., 0], scale) and torch.equal(got[..., 1], zero)
+    q = (x - zero[..., None]) / torch.where(scale > 0, scale, 1.0)[..., None]
+    want = torch.where(scale[..., None] > 0, q, 0.0).clamp(0, 15).round().flatten(-2)
+    codes = R.unpack(cache[0].cpu().transpose(1, 2).reshape(T, Hkv, D // 2), "k").double()
+    assert torch.equal(codes, want)

@@ -17,18 +17,21 @@
 // Work split: one thread moves 16 bytes (8 elements) of a row, D/8 threads a
 // row, so partner elements of a rotation pair and the 4 threads of a group
 // meet by shuffles within a warp.  A block takes the query rows, or the key and
-// value rows, of one or a few tokens; a thread starts the loads of kAhead of
-// its rows before the tokens' slots, positions and angles (which depend on one
-// another) have come, and the angles go through shared memory once for all
-// heads.
+// value rows, of one or a few tokens; a thread starts the loads of two rows (of
+// q, or a head's k and v) before the tokens' slots, positions and angles (which
+// depend on one another) have come, and the angles go through shared memory once
+// for all heads.  The kind of a row is known where it is compiled: selecting
+// between k and v at run time, addresses included, took a third of all
+// instructions (4-bit prompt 104 -> 91 us).
 //
-// Measured (GB300): 8191 tokens of 16 + 2 * 2 heads, D = 64, 16 bits (45 MB) 13
-// us, of which about 2.5 are the launch; 16000 tokens of 32 + 2 * 8 heads, D =
-// 128, into 4 bits (422 MB with the values held) 106 us, 4.0 TB/s, bound by
-// issue slots (about 190 instructions for 16 bytes of a key or value row).  64
-// tokens take 2.6 us.  Two rows ahead and five blocks an SM: four ahead cost
-// registers (115 us at four blocks), one ahead 110.  16 rows a thread: 8 took 110
-// (blocks' starts), 32 the same 106.
+// Measured (GB300): 8191 tokens of 16 + 2 * 2 heads, D = 64, 16 bits (45 MB)
+// 12.3 us, of which about 2.5 are the launch; 16000 tokens of 32 + 2 * 8 heads, D
+// = 128, 73 us in 16 bits (5.9 TB/s) and 87 us into 4 bits (422 MB with the
+// values held, 4.9 TB/s), bound by issue slots (about 300 instructions for 16
+// bytes of a key or value row) and latency.  64 tokens take 2.4 us, into 4 bits
+// 3.3.  Two rows ahead and five blocks an SM: four blocks took 91 us (3 % less in
+// the small 16-bit prompt), six too.  16 rows a thread: 8 took 4 us more (blocks'
+// starts), 32 three.
 #include <algorithm>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -43,10 +46,10 @@ __device__ uint32_t g_append_error_word;
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 2;       // rows that a thread has on their way
 constexpr int kTurns = 16;      // rows that a thread takes, where there are enough
 constexpr int kMaxTokens = 16;  // tokens of a block
 constexpr float kFp16Max = 65504.f;
+constexpr float kTwo23 = 8388608.f;  // an integer added to it stands in the low bits
 
 template <bool BF16>
 __device__ __forceinline__ void unpack8(const uint4& r, float (&x)[8]) {
@@ -98,6 +101,12 @@ __device__ __forceinline__ uint32_t transpose_nibbles(uint32_t x, int lane) {
 }
 
 // (d0, d1) = (a0, a1) * (b0, b1) [+ (c0, c1)]: two fp32 results an instruction.
+__device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
 __device__ __forceinline__ void mul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
     asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
         "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
@@ -109,6 +118,17 @@ __device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, f
         "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
         : "=f"(d0), "=f"(d1)
         : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+
+__device__ __forceinline__ float min3(float a, float b, float c) {
+    float d;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 
 // Quantises this thread's 8 elements (4 threads hold a group): its codes as the
@@ -129,21 +149,18 @@ __device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, f
 // its quotients are exact ties or well away from one.
 __device__ __forceinline__ bool quantise(const float (&x)[8], bool rotated, int partner, float (&t)[8], __half& scale,
                                          __half& zero) {
-    float lo = x[0], hi = x[0];
-#pragma unroll
-    for (int e = 1; e < 8; ++e) {
-        lo = fminf(lo, x[e]);
-        hi = fmaxf(hi, x[e]);
-    }
+    float lo = min3(x[0], x[1], x[2]), hi = max3(x[0], x[1], x[2]);
+    lo = fminf(min3(lo, x[3], x[4]), min3(x[5], x[6], x[7]));
+    hi = fmaxf(max3(hi, x[3], x[4]), max3(x[5], x[6], x[7]));
 #pragma unroll
     for (int m = 1; m <= 2; m <<= 1) {
         lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, m));
         hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, m));
     }
     if (!(lo <= hi)) lo = hi = 0.f;  // nothing but NaN
-    lo = fminf(fmaxf(lo, -kFp16Max), kFp16Max);
+    lo = fminf(fmaxf(lo, -kFp16Max), kFp16Max) + 0.f;  // (+ 0: never -0, whose bits differ from 0's below)
     hi = fminf(fmaxf(hi, -kFp16Max), kFp16Max);
-    const float step = (hi - lo) / 15.f;
+    const float step = (hi - lo) * (1.f / 15.f);
     scale = __float2half_rn(step);
     zero = __float2half_rn(lo);
     float most = fmaxf(-lo, hi);
@@ -157,16 +174,22 @@ __device__ __forceinline__ bool quantise(const float (&x)[8], bool rotated, int 
     };
     bool near = apart(lo - err, lo + err) || apart(step - es, step + es);
     const float s = __half2float(scale), z = __half2float(zero);
-    const float inv = s > 0.f ? 1.f / s : 0.f;
+    const float inv = s > 0.f ? __fdividef(1.f, s) : 0.f;
     const float top = 15.f * s;  // exact
     float worst = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float d = fminf(fmaxf(x[e] - z, 0.f), top);
-        const float q = d * inv;
-        const float r = fmaf(fmaf(-q, s, d), inv, q);
-        t[e] = __fadd_rn(r, 8388608.f);  // 2^23 +: to the nearest, ties to even
-        worst = fmaxf(worst, fabsf(r - __fsub_rn(t[e], 8388608.f)));
+    for (int e = 0; e < 8; e += 2) {
+        float d0, d1, q0, q1, r0, r1;
+        add2(d0, d1, x[e], x[e + 1], -z, -z);
+        d0 = fminf(fmaxf(d0, 0.f), top);
+        d1 = fminf(fmaxf(d1, 0.f), top);
+        mul2(q0, q1, d0, d1, inv, inv);
+        fma2(r0, r1, q0, q1, -s, -s, d0, d1);
+        fma2(r0, r1, r0, r1, inv, inv, q0, q1);
+        add2(t[e], t[e + 1], r0, r1, kTwo23, kTwo23);  // to the nearest, ties to even
+        add2(q0, q1, t[e], t[e + 1], -kTwo23, -kTwo23);
+        fma2(q0, q1, q0, q1, -1.f, -1.f, r0, r1);  // how far each quotient is from its code
+        worst = max3(worst, fabsf(q0), fabsf(q1));
     }
     // The quotient's own error: 16 * 2 roundings, and that of x in steps.
     if (rotated) near = near || worst > 0.5f - fmaf(err, inv, 2.0e-6f);
@@ -175,9 +198,12 @@ __device__ __forceinline__ bool quantise(const float (&x)[8], bool rotated, int 
 
 // The same to twice fp32's precision: values are unevaluated sums h + l of two
 // floats, products by fma and sums by the two-sum of Knuth (fp64 would take 10
-// times as long on this part).  From the row's raw elements: x the thread's own,
-// y their partners, cs as in append_row; turns: whether they turn.  Whole
-// groups call it.
+// times as long on this part).  From the raw elements of a group's rows and of
+// their partners, which its four lanes (from `base` on) hold, with whether and by
+// which angles they turn.  The whole warp calls it and takes one element a lane:
+// with 8 a lane it was four times as many instructions, which a call for few
+// tokens waits for (64 tokens 5.3 -> 3.3 us, 16000 91 -> 87), and whole warps
+// never run this as often as to hide it.
 struct Two {
     float h, l;
 };
@@ -189,32 +215,43 @@ __device__ __forceinline__ Two normal(float h, float l) {  // |h| >= |l|
     const float s = __fadd_rn(h, l);
     return {s, __fsub_rn(l, __fsub_rn(s, h))};
 }
+template <bool BF16>
+__device__ __forceinline__ float element(uint32_t w, bool high) {
+    if (BF16) return __uint_as_float(high ? w & 0xffff0000u : w << 16);
+    return __half2float(__ushort_as_half(static_cast<uint16_t>(high ? w >> 16 : w)));
+}
+struct Exact {
+    float t;           // 2^23 + code
+    uint32_t params;   // zero << 16 | scale
+};
 template <bool BF16, int CHUNKS>
-__device__ __noinline__ void requantise(uint4 raw, uint4 other, bool swap, bool turns, const float4* cs, uint32_t group,
-                                        float* t, __half* scale, __half* zero) {
-    float xf[8], yf[8];
-    unpack8<BF16>(raw, xf);
-    unpack8<BF16>(other, yf);
-    Two x[8], lo = {INFINITY, 0.f}, hi = {-INFINITY, 0.f};
-    auto less = [](const Two& a, const Two& b) { return a.h < b.h || (a.h == b.h && a.l < b.l); };
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        x[e] = {xf[e], 0.f};
-        if (turns) {
-            const float co = reinterpret_cast<const float*>(cs + (e / 4) * 2 * CHUNKS)[e % 4];
-            const float si = reinterpret_cast<const float*>(cs + ((e / 4) * 2 + 1) * CHUNKS)[e % 4];
-            const float y = swap ? xf[e ^ 1] : yf[e];
-            const float p = __fmul_rn(xf[e], co), q = __fmul_rn(y, si);
-            const Two w = two_sum(p, q);
-            x[e] = normal(w.h, __fadd_rn(w.l, __fadd_rn(__fmaf_rn(xf[e], co, -p), __fmaf_rn(y, si, -q))));
-        }
-        if (less(x[e], lo)) lo = x[e];
-        if (less(hi, x[e])) hi = x[e];
+__device__ __noinline__ Exact requantise(uint4 raw, uint4 other, int base, bool swap, bool turns, const float* angles,
+                                         int at) {
+    const int lane = threadIdx.x % 32, e = lane % 8, owner = base + lane / 8;
+    auto pick = [&](const uint4& v) {
+        const uint32_t a = __shfl_sync(0xffffffffu, v.x, owner), b = __shfl_sync(0xffffffffu, v.y, owner);
+        const uint32_t c = __shfl_sync(0xffffffffu, v.z, owner), d = __shfl_sync(0xffffffffu, v.w, owner);
+        return e < 4 ? (e < 2 ? a : b) : (e < 6 ? c : d);
+    };
+    const uint32_t wx = pick(raw), wy = pick(other);
+    turns = __shfl_sync(0xffffffffu, turns, owner);
+    at = __shfl_sync(0xffffffffu, at, owner) + (e / 4) * 8 * CHUNKS + e % 4;
+    Two x = {element<BF16>(wx, e & 1), 0.f};
+    if (turns) {
+        const float co = angles[at], si = angles[at + 4 * CHUNKS];
+        const float y = element<BF16>(swap ? wx : wy, swap ? !(e & 1) : (e & 1));
+        const float p = __fmul_rn(x.h, co), q = __fmul_rn(y, si);
+        const Two w = two_sum(p, q);
+        const float l = __fadd_rn(w.l, __fadd_rn(__fmaf_rn(x.h, co, -p), __fmaf_rn(y, si, -q)));
+        x = fabsf(w.h) < INFINITY ? normal(w.h, l) : Two{w.h, 0.f};
     }
-#pragma unroll
-    for (int m = 1; m <= 2; m <<= 1) {
-        const Two a = {__shfl_xor_sync(group, lo.h, m), __shfl_xor_sync(group, lo.l, m)};
-        const Two b = {__shfl_xor_sync(group, hi.h, m), __shfl_xor_sync(group, hi.l, m)};
+    auto less = [](const Two& a, const Two& b) { return a.h < b.h || (a.h == b.h && a.l < b.l); };
+    Two lo = {INFINITY, 0.f}, hi = {-INFINITY, 0.f};
+    if (x.h == x.h) lo = hi = x;
+#pragma unroll 1
+    for (int m = 1; m < 32; m <<= 1) {
+        const Two a = {__shfl_xor_sync(0xffffffffu, lo.h, m), __shfl_xor_sync(0xffffffffu, lo.l, m)};
+        const Two b = {__shfl_xor_sync(0xffffffffu, hi.h, m), __shfl_xor_sync(0xffffffffu, hi.l, m)};
         if (less(a, lo)) lo = a;
         if (less(hi, b)) hi = b;
     }
@@ -228,25 +265,23 @@ __device__ __noinline__ void requantise(uint4 raw, uint4 other, bool swap, bool 
     const Two d = two_sum(hi.h, -lo.h);
     const Two range = normal(d.h, __fadd_rn(d.l, __fsub_rn(hi.l, lo.l)));
     const float q0 = range.h / 15.f;
-    *scale = __float2half_rn(__fadd_rn(q0, __fadd_rn(__fmaf_rn(-q0, 15.f, range.h), range.l) / 15.f));
-    *zero = __float2half_rn(lo.h);
-    const float s = __half2float(*scale), z = __half2float(*zero);
+    const __half scale = __float2half_rn(__fadd_rn(q0, __fadd_rn(__fmaf_rn(-q0, 15.f, range.h), range.l) / 15.f));
+    const __half zero = __float2half_rn(lo.h);
+    const float s = __half2float(scale), z = __half2float(zero);
     const float inv = s > 0.f ? 1.f / s : 0.f, half = 0.5f * s;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        // k: the code that fp32 finds; then which side of k +- 1/2 the value is on.
-        const Two w = two_sum(x[e].h, -z);
-        const float low = __fadd_rn(w.l, x[e].l);
-        float k = rintf(fminf(fmaxf(w.h * inv, 0.f), 15.f));
-        const float rest = __fmaf_rn(-k, s, w.h);
-        const float above = __fadd_rn(__fsub_rn(rest, half), low), below = __fadd_rn(__fadd_rn(rest, half), low);
-        const bool odd = (static_cast<int>(k) & 1) != 0;
-        if (k < 15.f && (above > 0.f || (above == 0.f && odd && s > 0.f)))
-            k += 1.f;
-        else if (k > 0.f && (below < 0.f || (below == 0.f && odd && s > 0.f)))
-            k -= 1.f;
-        t[e] = 8388608.f + (s > 0.f ? k : 0.f);
-    }
+    // k: the code that fp32 finds; then which side of k +- 1/2 the value is on.
+    const Two w = two_sum(x.h, -z);
+    const float low = __fadd_rn(w.l, x.l);
+    float k = rintf(fminf(fmaxf(w.h * inv, 0.f), 15.f));
+    const float rest = __fmaf_rn(-k, s, w.h);
+    const float above = __fadd_rn(__fsub_rn(rest, half), low), below = __fadd_rn(__fadd_rn(rest, half), low);
+    const bool odd = (static_cast<int>(k) & 1) != 0;
+    if (k < 15.f && (above > 0.f || (above == 0.f && odd && s > 0.f)))
+        k += 1.f;
+    else if (k > 0.f && (below < 0.f || (below == 0.f && odd && s > 0.f)))
+        k -= 1.f;
+    const __half2 params = __halves2half2(scale, zero);
+    return {kTwo23 + (s > 0.f ? k : 0.f), *reinterpret_cast<const uint32_t*>(&params)};
 }
 
 // Nibbles e = 0..7 from t[0..7] = 2^23 + code: a sum in 32-bit integers, from
@@ -259,42 +294,43 @@ __device__ __forceinline__ uint32_t pack_codes(float t0, float t1, float t2, flo
     return w - 0x4b000000u * 0x11111111u;
 }
 
-// Where an item (a row of a token) is.
+enum Kind { kQuery, kKey, kValue, kKeyAndValue };  // the last: of a block, not of a row
+
+// Where an item (a token's row of a head) is.
 struct Item {
     int tl;  // token within the block
-    int r;   // row: a query head, or key heads and then value heads
+    int h;
 };
 
 template <int D>
 struct Shared {
     static constexpr int kChunks = D / 8;
-    int64_t page[kMaxTokens];  // -1: nothing of the token is written
-    int off[kMaxTokens];
+    // Where the token's row of head 0 is in the cache: in rows (4 bits) or in
+    // elements (16 bits).  -1: nothing of the token is written.
+    int64_t place[kMaxTokens];
     // Each token's angles, as the thread of chunk c multiplies by them: cos of
     // its first 4 elements, signed sin of them, then of its other 4.
     float4 cs[kMaxTokens][4][kChunks];
 };
 
 // One row's 8 elements: rotation, outputs, cache.  Whole warps call it, with
-// lanes that are not `on` repeating some row.
-template <int D, bool BF16, bool KV4, bool QUERY>
-__device__ __forceinline__ void append_row(const AppendArgs& a, const uint4& raw, uint32_t t, int r, bool on, int64_t page,
-                                           int off, const float4* cs) {
+// lanes that are not `on` repeating some row.  `place`: the row's in the cache.
+template <int D, bool BF16, bool KV4, Kind KIND>
+__device__ __forceinline__ void append_row(const AppendArgs& a, const uint4& raw, uint32_t t, uint32_t h, bool on,
+                                           int64_t place, const float* angles, int at) {
     constexpr int kChunks = D / 8;
     const int c = threadIdx.x % kChunks, lane = threadIdx.x % 32;
-    const bool is_v = !QUERY && r >= a.Hkv;
-    const uint32_t h = is_v ? r - a.Hkv : r;
     uint4 rounded = raw, other = raw;
     bool turns = false;
     int from = lane;  // the lane of this thread's partner elements
     float x[8];
-    if (!QUERY || a.rot > 0) unpack8<BF16>(raw, x);
+    if ((KV4 && KIND != kQuery) || (KIND != kValue && a.rot > 0)) unpack8<BF16>(raw, x);
     // Rotation (q and k rows).  Halves: chunk c < rot/16 holds the pairs' first
     // elements, the chunk rot/16 further their second ones, and the sign of a
     // sin - b cos comes with the angles.  Interleaved pairs lie within a chunk.
-    if (a.rot > 0 && (QUERY || __any_sync(0xffffffffu, !is_v))) {
+    if (KIND != kValue && a.rot > 0) {
         const int half_chunks = a.rot / 16;
-        turns = c < 2 * half_chunks && !is_v;
+        turns = c < 2 * half_chunks;
         float y[8];
         if (a.interleaved) {
 #pragma unroll
@@ -310,7 +346,8 @@ __device__ __forceinline__ void append_row(const AppendArgs& a, const uint4& raw
         if (turns) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const float4 co = cs[(2 * u) * kChunks], si = cs[(2 * u + 1) * kChunks];
+                const float4 co = *reinterpret_cast<const float4*>(angles + at + 8 * u * kChunks);
+                const float4 si = *reinterpret_cast<const float4*>(angles + at + (8 * u + 4) * kChunks);
                 float z[4];
                 mul2(z[0], z[1], x[4 * u], x[4 * u + 1], co.x, co.y);
                 mul2(z[2], z[3], x[4 * u + 2], x[4 * u + 3], co.z, co.w);
@@ -324,101 +361,105 @@ __device__ __forceinline__ void append_row(const AppendArgs& a, const uint4& raw
         return reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + static_cast<uint64_t>(t) * ts +
                                         static_cast<uint64_t>(h) * hs + 8 * c);
     };
-    if constexpr (QUERY) {
+    if constexpr (KIND == kQuery) {
         if (on) *out_row(a.q_out, a.qo_ts, a.qo_hs) = rounded;
         return;
     }
+    constexpr bool kIsV = KIND == kValue;
     if constexpr (KV4) {
         __half scale, zero;
         float code[8];
-        const uint32_t unsure = __ballot_sync(0xffffffffu, quantise(x, turns, from, code, scale, zero));
-        if (unsure != 0u) {
-            const uint32_t group = 15u << (lane & ~3);
-            if (unsure & group) {
-                float exact[8];  // (code itself stays in registers)
-                __half es, ez;
-                requantise<BF16, kChunks>(raw, other, a.interleaved, turns, cs, group, exact, &es, &ez);
+        const bool unsure = quantise(x, turns, from, code, scale, zero);
+        for (uint32_t left = __ballot_sync(0xffffffffu, unsure && on); left != 0u;) {
+            const int base = (__ffs(left) - 1) & ~3;
+            left &= ~(15u << base);
+            const Exact exact = requantise<BF16, kChunks>(raw, other, base, a.interleaved, turns, angles, at);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) code[e] = exact[e];
-                scale = es;
-                zero = ez;
+            for (int e = 0; e < 8; ++e) {
+                const float t = __shfl_sync(0xffffffffu, exact.t, (lane % 4) * 8 + e);
+                if ((lane & ~3) == base) code[e] = t;
             }
-            __syncwarp();
+            if ((lane & ~3) == base) {
+                scale = __ushort_as_half(static_cast<uint16_t>(exact.params));
+                zero = __ushort_as_half(static_cast<uint16_t>(exact.params >> 16));
+            }
         }
-        const int64_t row = (page * a.Hkv + h) * a.page_size + off;
-        if (__any_sync(0xffffffffu, !is_v)) {
-            // K: element e = 2 l + u of the chunk at nibble l + 4 u, so that a word's
+        uint32_t* words = static_cast<uint32_t*>(kIsV ? a.v_pages : a.k_pages) + place * (D / 8);
+        if constexpr (!kIsV) {
+            // Element e = 2 l + u of the chunk at nibble l + 4 u, so that a word's
             // even and odd elements unpack as 16-bit pairs.
             const uint32_t w = pack_codes(code[0], code[2], code[4], code[6], code[1], code[3], code[5], code[7]);
-            if (on && !is_v) static_cast<uint32_t*>(a.k_pages)[row * (D / 8) + (c % 4) * (D / 32) + c / 4] = w;
-        }
-        if (__any_sync(0xffffffffu, is_v)) {
-            // V: dim 16 j + 8 u + g (chunk 2 j + u, element g) at nibble j of word
+            if (on) words[(c % 4) * (D / 32) + c / 4] = w;
+        } else {
+            // Dim 16 j + 8 u + g (chunk 2 j + u, element g) at nibble j of word
             // 2 g + u (D = 128), nibble 4 u + j of word g (D = 64).
             const uint32_t w = pack_codes(code[0], code[1], code[2], code[3], code[4], code[5], code[6], code[7]);
             const uint32_t wt = D == 128 ? transpose_nibbles<2, 4, 8>(w, lane) : transpose_nibbles<2, 4, 1>(w, lane);
-            if (on && is_v) static_cast<uint32_t*>(a.v_pages)[row * (D / 8) + (D == 128 ? c : 4 * (c & 1) + c / 2)] = wt;
+            if (on) words[D == 128 ? c : 4 * (c & 1) + c / 2] = wt;
         }
         if (on && c % 4 == 0)
-            static_cast<__half2*>(is_v ? a.v_scales : a.k_scales)[row * (D / 32) + c / 4] = __halves2half2(scale, zero);
+            static_cast<__half2*>(kIsV ? a.v_scales : a.k_scales)[place * (D / 32) + c / 4] = __halves2half2(scale, zero);
         if (a.held) {
             const float s = __half2float(scale), z = __half2float(zero);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = fmaf(code[e] - 8388608.f, s, z);
+            for (int e = 0; e < 8; e += 2) {
+                add2(x[e], x[e + 1], code[e], code[e + 1], -kTwo23, -kTwo23);
+                fma2(x[e], x[e + 1], x[e], x[e + 1], s, s, z, z);
+            }
             rounded = pack8<BF16>(x);
         }
     } else if (on) {
-        uint16_t* pages = static_cast<uint16_t*>(is_v ? a.v_pages : a.k_pages);
-        *reinterpret_cast<uint4*>(pages + page * a.page_stride + (static_cast<int64_t>(h) * a.page_size + off) * D + 8 * c) =
-            rounded;
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(kIsV ? a.v_pages : a.k_pages) + place + 8 * c) = rounded;
     }
-    void* out = is_v ? a.v_out : a.k_out;
-    if (on && out != nullptr) *out_row(out, is_v ? a.vo_ts : a.ko_ts, is_v ? a.vo_hs : a.ko_hs) = rounded;
+    void* out = kIsV ? a.v_out : a.k_out;
+    if (on && out != nullptr) *out_row(out, kIsV ? a.vo_ts : a.ko_ts, kIsV ? a.vo_hs : a.ko_hs) = rounded;
 }
 
-// The query rows, or the key and value rows, of tokens [first, first + tokens).
-template <int D, bool BF16, bool KV4, bool QUERY>
+// The rows of one kind of tokens [first, first + tokens).
+template <int D, bool BF16, bool KV4, Kind KIND>
 __device__ __forceinline__ void append_block(const AppendArgs& a, Shared<D>& sh, uint32_t first, int tokens) {
     constexpr int kChunks = D / 8;                  // threads per row
-    constexpr int kLanes = kThreads / kChunks;      // rows in flight per block
+    constexpr int kLanes = kThreads / kChunks;      // row lanes of a block
+    constexpr bool QUERY = KIND == kQuery;
     const int c = threadIdx.x % kChunks;
     const int rlane = threadIdx.x / kChunks;
-    const int rows = QUERY ? a.H : 2 * a.Hkv;
+    const int rows = QUERY ? a.H : a.Hkv;
 
     // Items are dealt to the row lanes in turn; from one to a lane's next:
-    const int step_tl = kLanes / rows, step_r = kLanes - step_tl * rows;
+    const int step_tl = kLanes / rows, step_h = kLanes - step_tl * rows;
     auto next = [&](Item& x) {
         x.tl += step_tl;
-        x.r += step_r;
-        if (x.r >= rows) {
-            x.r -= rows;
+        x.h += step_h;
+        if (x.h >= rows) {
+            x.h -= rows;
             ++x.tl;
         }
     };
-    uint4 raw[kAhead];
+    // Rows on their way: an item's k and v, or those of two items.
+    uint4 raw[2];
     Item ahead, now;
     now.tl = rlane / rows;
-    now.r = rlane - now.tl * rows;
+    now.h = rlane - now.tl * rows;
     ahead = now;
     auto load = [&](int u) {
         raw[u] = make_uint4(0u, 0u, 0u, 0u);
         if (ahead.tl < tokens) {
-            const bool is_v = !QUERY && ahead.r >= a.Hkv;
-            const uint16_t* src = static_cast<const uint16_t*>(QUERY ? a.q : (is_v ? a.v : a.k));
-            const uint32_t ts = QUERY ? a.q_ts : (is_v ? a.v_ts : a.k_ts);
-            const uint32_t hs = QUERY ? a.q_hs : (is_v ? a.v_hs : a.k_hs);
-            const uint32_t h = is_v ? ahead.r - a.Hkv : ahead.r;
+            const bool v = KIND == kValue || (KIND == kKeyAndValue && u == 1);
+            const uint16_t* src = static_cast<const uint16_t*>(QUERY ? a.q : (v ? a.v : a.k));
+            const uint32_t ts = QUERY ? a.q_ts : (v ? a.v_ts : a.k_ts);
+            const uint32_t hs = QUERY ? a.q_hs : (v ? a.v_hs : a.k_hs);
             raw[u] = *reinterpret_cast<const uint4*>(src + static_cast<uint64_t>(first + ahead.tl) * ts +
-                                                     static_cast<uint64_t>(h) * hs + 8 * c);
+                                                     static_cast<uint64_t>(ahead.h) * hs + 8 * c);
         }
-        next(ahead);
+        if (KIND != kKeyAndValue || u == 1) next(ahead);
     };
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) load(u);
+    load(0);
+    load(1);
 
     // The tokens' places and angles: threads take a token each when nothing
     // turns, else one chunk of one token's angles.
-    const int pieces = a.rot > 0 ? a.rot / 8 : 1;
+    const bool turn = KIND != kValue && a.rot > 0;
+    const int pieces = turn ? a.rot / 8 : 1;
     for (int x = threadIdx.x; x < tokens * pieces; x += kThreads) {
         const int tl = x / pieces, e = x - tl * pieces;
         int64_t slot = a.slots[first + tl];
@@ -428,17 +469,16 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, Shared<D>& sh,
             slot = -1;
         }
         if (e == 0) {
-            int64_t page = -1;
-            int off = 0;
+            int64_t place = slot < 0 ? -1 : 0;
             if (slot >= 0 && !QUERY) {  // 32-bit division where it does
-                page = (slot >> 32) == 0 ? static_cast<uint32_t>(slot) / static_cast<uint32_t>(a.page_size)
-                                         : slot / a.page_size;
-                off = static_cast<int>(slot - page * a.page_size);
+                const int64_t page = (slot >> 32) == 0 ? static_cast<uint32_t>(slot) / static_cast<uint32_t>(a.page_size)
+                                                       : slot / a.page_size;
+                const int64_t off = slot - page * a.page_size;
+                place = KV4 ? page * a.Hkv * a.page_size + off : page * a.page_stride + off * D;
             }
-            sh.page[tl] = QUERY ? (slot < 0 ? -1 : 0) : page;
-            sh.off[tl] = off;
+            sh.place[tl] = place;
         }
-        if (slot >= 0 && a.rot > 0) {
+        if (slot >= 0 && turn) {
             const int64_t at = static_cast<int64_t>(pos) * (a.rot / 2);
             float4(&cs)[4][kChunks] = sh.cs[tl];
             if (a.interleaved) {  // pairs 4e .. 4e + 3, each angle for both elements
@@ -465,34 +505,55 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, Shared<D>& sh,
 
     // Every thread of a warp makes the same number of turns (shuffles inside).
     const int turns = (tokens * rows + kLanes - 1) / kLanes;
-    for (int i = 0; i < turns; i += kAhead) {
+    const int64_t head = KV4 ? a.page_size : static_cast<int64_t>(a.page_size) * D;  // a head's share of a page
+    constexpr int kItems = KIND == kKeyAndValue ? 1 : 2;
+    for (int i = 0; i < turns; i += kItems) {
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            if (i + u < turns) {
-                const int tl = min(now.tl, tokens - 1);
-                const int64_t page = sh.page[tl];
-                append_row<D, BF16, KV4, QUERY>(a, raw[u], first + tl, now.r, now.tl < tokens && page >= 0, page,
-                                                sh.off[tl], &sh.cs[tl][0][c]);
-                next(now);
-                load(u);
+        for (int u = 0; u < kItems; ++u) {
+            if (u > 0 && i + u >= turns) break;
+            const int tl = min(now.tl, tokens - 1);
+            const int64_t at = sh.place[tl], place = at + now.h * head;
+            const uint32_t t = first + tl, h = now.h;
+            const bool on = now.tl < tokens && at >= 0;
+            const float* angles = reinterpret_cast<const float*>(&sh.cs[0][0][0]);
+            const int angle = 16 * kChunks * tl + 4 * c;  // sh.cs[tl][0][c]
+            next(now);
+            append_row<D, BF16, KV4, KIND == kKeyAndValue ? kKey : KIND>(a, raw[u], t, h, on, place, angles, angle);
+            load(u);
+            if constexpr (KIND == kKeyAndValue) {
+                append_row<D, BF16, KV4, kValue>(a, raw[1], t, h, on, place, angles, angle);
+                load(1);
             }
         }
     }
 }
 
-// The first blocks take key and value rows (more work each), the rest query rows.
+// The first blocks take key and value rows (more work each), the rest query
+// rows: spread evenly among each other they took 12 us longer at 16000 tokens,
+// for the last long blocks start late.
 template <int D, bool BF16, bool KV4>
 __global__ void __launch_bounds__(kThreads, 5) cache_append_kernel(const __grid_constant__ AppendArgs a) {
     __shared__ Shared<D> sh;
     grid_dependency();
     const bool query = blockIdx.x >= a.kv_blocks;
     const uint32_t per = query ? a.q_tokens : a.kv_tokens;
-    const uint32_t first = (query ? blockIdx.x - a.kv_blocks : blockIdx.x) * per;
+    const uint32_t index = query ? blockIdx.x - a.kv_blocks : (a.apart ? blockIdx.x / 2 : blockIdx.x);
+    const uint32_t first = index * per;
     const int tokens = static_cast<int>(min(static_cast<int64_t>(per), a.T - first));
-    if (query)
-        append_block<D, BF16, KV4, true>(a, sh, first, tokens);
-    else
-        append_block<D, BF16, KV4, false>(a, sh, first, tokens);
+    if (query) {
+        append_block<D, BF16, KV4, kQuery>(a, sh, first, tokens);
+        return;
+    }
+    if constexpr (KV4) {
+        if (a.apart) {
+            if (blockIdx.x % 2 == 0)
+                append_block<D, BF16, KV4, kKey>(a, sh, first, tokens);
+            else
+                append_block<D, BF16, KV4, kValue>(a, sh, first, tokens);
+            return;
+        }
+    }
+    append_block<D, BF16, KV4, kKeyAndValue>(a, sh, first, tokens);
 }
 
 template <int D, bool BF16>
@@ -512,7 +573,11 @@ cudaError_t append_launch(AppendArgs a, int D, bool bf16, bool kv4, int sms, cud
         return static_cast<uint32_t>(std::max<int64_t>(std::min(most, a.T / (3 * sms)), 1));
     };
     a.kv_tokens = tokens(2 * a.Hkv);
-    a.kv_blocks = static_cast<uint32_t>((a.T + a.kv_tokens - 1) / a.kv_tokens);
+    // Few tokens into 4 bits: one thread's k and then v would take longer than the
+    // loads (64 tokens 3.6 -> 3.3 us, 300 6.6 -> 5.7; but 850 9.6 -> 11.1, and 16
+    // bits, whose rows take few instructions, 2.4 -> 2.7 at 64).
+    a.apart = kv4 && a.T <= 2 * sms;
+    a.kv_blocks = static_cast<uint32_t>((a.T + a.kv_tokens - 1) / a.kv_tokens) * (a.apart ? 2u : 1u);
     unsigned grid = a.kv_blocks;
     if (a.H > 0) {
         a.q_tokens = tokens(a.H);

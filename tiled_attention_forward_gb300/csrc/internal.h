@@ -214,6 +214,7 @@ struct AppendArgs {
     uint32_t kv_blocks;   // blocks of key and value rows, tokens of a block (set by append_launch)
     uint32_t kv_tokens;
     uint32_t q_tokens;
+    int apart;            // 4-bit: key rows and value rows have blocks of their own; likewise
 };
 cudaError_t append_launch(AppendArgs a, int D, bool bf16, bool kv4, int sms, cudaStream_t s);
 cudaError_t append_read_and_clear_error_word(uint32_t* out);
