@@ -26,10 +26,10 @@
 //
 // Measured (GB300): 8191 tokens of 16 + 2 * 2 heads, D = 64, 16 bits (45 MB)
 // 12.3 us, of which about 2.5 are the launch; 16000 tokens of 32 + 2 * 8 heads, D
-// = 128, 73 us in 16 bits (5.9 TB/s) and 87 us into 4 bits (422 MB with the
+// = 128, 74 us in 16 bits (5.8 TB/s) and 86 us into 4 bits (422 MB with the
 // values held, 4.9 TB/s), bound by issue slots (about 300 instructions for 16
 // bytes of a key or value row) and latency.  64 tokens take 2.4 us, into 4 bits
-// 3.3.  Two rows ahead and five blocks an SM: four blocks took 91 us (3 % less in
+// 3.3.  Two rows ahead and five blocks an SM: four blocks took 89 us (3 % less in
 // the small 16-bit prompt), six too.  16 rows a thread: 8 took 4 us more (blocks'
 // starts), 32 three.
 #include <algorithm>
@@ -198,9 +198,9 @@ __device__ __forceinline__ bool quantise(const float (&x)[8], bool rotated, int 
 
 // The same to twice fp32's precision: values are unevaluated sums h + l of two
 // floats, products by fma and sums by the two-sum of Knuth (fp64 would take 10
-// times as long on this part).  From the raw elements of a group's rows and of
-// their partners, which its four lanes (from `base` on) hold, with whether and by
-// which angles they turn.  The whole warp calls it and takes one element a lane:
+// times as long on this part).  From the raw elements that a group's four lanes
+// (from `base` on) hold, and their partners' that lanes `from` hold, with whether
+// and by which angles they turn.  The whole warp calls it and takes one element a lane:
 // with 8 a lane it was four times as many instructions, which a call for few
 // tokens waits for (64 tokens 5.3 -> 3.3 us, 16000 91 -> 87), and whole warps
 // never run this as often as to hide it.
@@ -225,15 +225,15 @@ struct Exact {
     uint32_t params;   // zero << 16 | scale
 };
 template <bool BF16, int CHUNKS>
-__device__ __noinline__ Exact requantise(uint4 raw, uint4 other, int base, bool swap, bool turns, const float* angles,
+__device__ __noinline__ Exact requantise(uint4 raw, int from, int base, bool swap, bool turns, const float* angles,
                                          int at) {
     const int lane = threadIdx.x % 32, e = lane % 8, owner = base + lane / 8;
-    auto pick = [&](const uint4& v) {
-        const uint32_t a = __shfl_sync(0xffffffffu, v.x, owner), b = __shfl_sync(0xffffffffu, v.y, owner);
-        const uint32_t c = __shfl_sync(0xffffffffu, v.z, owner), d = __shfl_sync(0xffffffffu, v.w, owner);
+    auto pick = [&](int who) {
+        const uint32_t a = __shfl_sync(0xffffffffu, raw.x, who), b = __shfl_sync(0xffffffffu, raw.y, who);
+        const uint32_t c = __shfl_sync(0xffffffffu, raw.z, who), d = __shfl_sync(0xffffffffu, raw.w, who);
         return e < 4 ? (e < 2 ? a : b) : (e < 6 ? c : d);
     };
-    const uint32_t wx = pick(raw), wy = pick(other);
+    const uint32_t wx = pick(owner), wy = pick(__shfl_sync(0xffffffffu, from, owner));
     turns = __shfl_sync(0xffffffffu, turns, owner);
     at = __shfl_sync(0xffffffffu, at, owner) + (e / 4) * 8 * CHUNKS + e % 4;
     Two x = {element<BF16>(wx, e & 1), 0.f};
@@ -320,7 +320,7 @@ __device__ __forceinline__ void append_row(const AppendArgs& a, const uint4& raw
                                            int64_t place, const float* angles, int at) {
     constexpr int kChunks = D / 8;
     const int c = threadIdx.x % kChunks, lane = threadIdx.x % 32;
-    uint4 rounded = raw, other = raw;
+    uint4 rounded = raw;
     bool turns = false;
     int from = lane;  // the lane of this thread's partner elements
     float x[8];
@@ -337,6 +337,7 @@ __device__ __forceinline__ void append_row(const AppendArgs& a, const uint4& raw
             for (int e = 0; e < 8; ++e) y[e] = x[e ^ 1];
         } else {
             from = lane - c + (turns ? (c < half_chunks ? c + half_chunks : c - half_chunks) : c);
+            uint4 other;
             other.x = __shfl_sync(0xffffffffu, raw.x, from);
             other.y = __shfl_sync(0xffffffffu, raw.y, from);
             other.z = __shfl_sync(0xffffffffu, raw.z, from);
@@ -373,7 +374,7 @@ __device__ __forceinline__ void append_row(const AppendArgs& a, const uint4& raw
         for (uint32_t left = __ballot_sync(0xffffffffu, unsure && on); left != 0u;) {
             const int base = (__ffs(left) - 1) & ~3;
             left &= ~(15u << base);
-            const Exact exact = requantise<BF16, kChunks>(raw, other, base, a.interleaved, turns, angles, at);
+            const Exact exact = requantise<BF16, kChunks>(raw, from, base, a.interleaved, turns, angles, at);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float t = __shfl_sync(0xffffffffu, exact.t, (lane % 4) * 8 + e);
