@@ -596,3 +596,31 @@ def test_append_kv4_rotated_codes_are_the_definitions(D, rot, dtype, interleaved
     want = torch.where(scale[..., None] > 0, q, 0.0).clamp(0, 15).round().flatten(-2)
     codes = R.unpack(cache[0].cpu().transpose(1, 2).reshape(T, Hkv, D // 2), "k").double()
     assert torch.equal(codes, want)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_append_kv4_rotated_infinities_take_the_ends(interleaved):
+    """An infinite element makes both of its rotated pair infinite: they stand for
+    fp16's ends, beside which the group's other elements keep their codes."""
+    T, D, ps = 320, 64, 16
+    g = torch.Generator().manual_seed(28)
+    k = torch.randn(T, 1, D, generator=g) * 2.0 ** torch.randint(0, 16, (T, 1, 1), generator=g)
+    k[torch.arange(T), 0, torch.randint(0, D, (T,), generator=g)] = math.inf
+    k[::2] = -k[::2]
+    k = k.to(torch.bfloat16)
+    pos = torch.randint(1, 512, (T,), generator=g, dtype=torch.int32)
+    cos, sin = R.tables(512, D)
+    assert (cos[1:] != 0).all() and (sin[1:] != 0).all()
+    cache = new_cache(True, T // ps, 1, ps, D, torch.bfloat16, 0.0)
+    fattn.cache_append_kv4(k.cuda(), k.cuda(), *cache, torch.arange(T).cuda(), pos=pos.cuda(), cos=cos.cuda(),
+                           sin=sin.cuda(), interleaved=interleaved)
+    ok()
+    x = R.rotate(k, pos, cos, sin, interleaved)[0].clamp(-65504, 65504).unflatten(-1, (-1, 32))
+    assert (x.abs() == 65504).flatten(1).sum(1).ge(2).all()
+    lo, hi = x.amin(-1), x.amax(-1)
+    scale, zero = ((hi - lo) / 15).float().half().double(), lo.float().half().double()
+    got = cache[1].cpu().double().transpose(1, 2).reshape(T, 1, D // 32, 2)
+    assert torch.equal(got[..., 0], scale) and torch.equal(got[..., 1], zero)
+    want = ((x - zero[..., None]) / scale[..., None]).clamp(0, 15).round().flatten(-2)
+    codes = R.unpack(cache[0].cpu().transpose(1, 2).reshape(T, 1, D // 2), "k").double()
+    assert torch.equal(codes, want)
