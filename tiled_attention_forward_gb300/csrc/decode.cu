@@ -36,7 +36,7 @@
 //
 // Measured (GB300, D = 128, the 64 sequences above, 1.11 GB of 16-bit rows):
 // 165 us, 6.7 TB/s, the rate of a plain copy.  In 4 bits the same call (347 MB)
-// takes 85 us, 4.1 TB/s, and 3 sequences of 120001 keys (461 MB) 96 us, 4.8
+// takes 85 us, 4.1 TB/s, and 3 sequences of 120001 keys (461 MB) 95 us, 4.9
 // TB/s: there the integer pipe (57 % busy at two cycles an operation) and the
 // issue slots (63 %) bound it, with 23 warp instructions a key.
 #include <cuda_bf16.h>
