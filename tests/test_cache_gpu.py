@@ -68,7 +68,8 @@ def check_quantised(x, mag, codes, scales, which, what):
 @pytest.mark.parametrize("kv4", [False, True])
 @pytest.mark.parametrize("dtype,D,H,Hkv,T,ps,rot", [
     ("bf16", 128, 4, 2, 67, 16, 128), ("fp16", 64, 8, 1, 33, 48, 32), ("bf16", 64, 5, 5, 1, 16, 64),
-    ("fp16", 128, 3, 1, 3, 32, 16), ("bf16", 128, 40, 8, 9, 64, 64), ("fp16", 64, 1, 1, 130, 16, 0)])
+    ("fp16", 128, 3, 1, 3, 32, 16), ("bf16", 128, 40, 8, 9, 64, 64), ("fp16", 64, 1, 1, 130, 16, 0),
+    ("fp16", 64, 2, 1, 20001, 16, 64), ("bf16", 128, 1, 1, 9001, 32, 128)])  # the most tokens that a block takes
 def test_append(dtype, D, H, Hkv, T, ps, rot, kv4, interleaved):
     dt = DT[dtype]
     P = -(-T // ps) + 2

@@ -25,13 +25,12 @@
 // instructions (4-bit prompt 104 -> 91 us).
 //
 // Measured (GB300): 8191 tokens of 16 + 2 * 2 heads, D = 64, 16 bits (45 MB)
-// 12.3 us, of which about 2.5 are the launch; 16000 tokens of 32 + 2 * 8 heads, D
+// 10.6 us, of which about 2.5 are the launch; 16000 tokens of 32 + 2 * 8 heads, D
 // = 128, 74 us in 16 bits (5.8 TB/s) and 86 us into 4 bits (422 MB with the
 // values held, 4.9 TB/s), bound by issue slots (about 300 instructions for 16
-// bytes of a key or value row) and latency.  64 tokens take 2.4 us, into 4 bits
-// 3.3.  Two rows ahead and five blocks an SM: four blocks took 89 us (3 % less in
-// the small 16-bit prompt), six too.  16 rows a thread: 8 took 4 us more (blocks'
-// starts), 32 three.
+// bytes of a key or value row) and latency.  64 tokens take 2.6 us, into 4 bits
+// 3.3.  Two rows ahead and five blocks an SM: four blocks took 89 us, six 91.
+// Up to 16 rows a thread: 8 took 4 us more (blocks' starts), 32 three.
 #include <algorithm>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -47,7 +46,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kTurns = 16;      // rows that a thread takes, where there are enough
-constexpr int kMaxTokens = 16;  // tokens of a block
 constexpr float kFp16Max = 65504.f;
 constexpr float kTwo23 = 8388608.f;  // an integer added to it stands in the low bits
 
@@ -302,15 +300,19 @@ struct Item {
     int h;
 };
 
+// A block's shared memory, of which a launch takes what its tokens need.
 template <int D>
 struct Shared {
     static constexpr int kChunks = D / 8;
+    static constexpr int kMaxTokens = D == 128 ? 16 : 64;  // (32 at D = 128: 2 % longer with two K/V heads)
     // Where the token's row of head 0 is in the cache: in rows (4 bits) or in
     // elements (16 bits).  -1: nothing of the token is written.
     int64_t place[kMaxTokens];
     // Each token's angles, as the thread of chunk c multiplies by them: cos of
     // its first 4 elements, signed sin of them, then of its other 4.
     float4 cs[kMaxTokens][4][kChunks];
+
+    static size_t bytes(uint32_t tokens) { return sizeof(place) + tokens * sizeof(cs[0]); }
 };
 
 // One row's 8 elements: rotation, outputs, cache.  Whole warps call it, with
@@ -534,7 +536,8 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, Shared<D>& sh,
 // for the last long blocks start late.
 template <int D, bool BF16, bool KV4>
 __global__ void __launch_bounds__(kThreads, 5) cache_append_kernel(const __grid_constant__ AppendArgs a) {
-    __shared__ Shared<D> sh;
+    extern __shared__ __align__(16) uint8_t smem[];
+    Shared<D>& sh = *reinterpret_cast<Shared<D>*>(smem);
     grid_dependency();
     const bool query = blockIdx.x >= a.kv_blocks;
     const uint32_t per = query ? a.q_tokens : a.kv_tokens;
@@ -559,29 +562,38 @@ __global__ void __launch_bounds__(kThreads, 5) cache_append_kernel(const __grid_
 
 template <int D, bool BF16>
 cudaError_t launch_kind(const AppendArgs& a, bool kv4, unsigned grid, cudaStream_t s) {
-    return kv4 ? launch_overlapped(cache_append_kernel<D, BF16, true>, grid, kThreads, 0, s, a)
-               : launch_overlapped(cache_append_kernel<D, BF16, false>, grid, kThreads, 0, s, a);
+    const size_t smem = Shared<D>::bytes(std::max(a.kv_tokens, a.q_tokens));
+    return kv4 ? launch_overlapped(cache_append_kernel<D, BF16, true>, grid, kThreads, smem, s, a)
+               : launch_overlapped(cache_append_kernel<D, BF16, false>, grid, kThreads, smem, s, a);
 }
 
 }  // namespace
 
 cudaError_t append_launch(AppendArgs a, int D, bool bf16, bool kv4, int sms, cudaStream_t s) {
-    // Tokens per block: one while that leaves SMs without a block, then as many
-    // as give a block's threads kTurns rows each.
-    const int lanes = kThreads / (D / 8);
-    auto tokens = [&](int rows) {
-        const int64_t most = std::min<int64_t>(std::max(kTurns * lanes / rows, 1), kMaxTokens);
-        return static_cast<uint32_t>(std::max<int64_t>(std::min(most, a.T / (3 * sms)), 1));
+    // Tokens of a block.  16 bits: as give its threads so many rows that all blocks
+    // are on the SMs at once, five each, up to kTurns (8191 tokens of 16 + 2 * 2
+    // heads, D = 64: 10.6 us; with a wave and a half of blocks 13.0).  4 bits: as
+    // leave three blocks of either kind per SM, as key and value rows take several
+    // times as long as query rows (4000 tokens of 32 + 2 * 8 heads 27 us; one wave
+    // 34).  A block of key and value rows has one of each per thread at least.
+    const int64_t lanes = kThreads / (D / 8), wave = lanes * 5 * sms;
+    const int64_t turns = std::min<int64_t>((a.T * (a.H + 2 * a.Hkv) + wave - 1) / wave, kTurns);
+    auto tokens = [&](int64_t rows, int64_t least) {
+        auto of = [&](int64_t turns) { return std::max<int64_t>(turns * lanes / rows, 1); };
+        const int64_t n = kv4 ? std::min(a.T / (3 * sms), of(kTurns)) : of(turns);
+        const int64_t most = D == 128 ? Shared<128>::kMaxTokens : Shared<64>::kMaxTokens;
+        return static_cast<uint32_t>(std::min(std::max(n, of(least)), most));
     };
-    a.kv_tokens = tokens(2 * a.Hkv);
+    a.kv_tokens = tokens(2 * a.Hkv, 2);
     // Few tokens into 4 bits: one thread's k and then v would take longer than the
     // loads (64 tokens 3.6 -> 3.3 us, 300 6.6 -> 5.7; but 850 9.6 -> 11.1, and 16
     // bits, whose rows take few instructions, 2.4 -> 2.7 at 64).
     a.apart = kv4 && a.T <= 2 * sms;
     a.kv_blocks = static_cast<uint32_t>((a.T + a.kv_tokens - 1) / a.kv_tokens) * (a.apart ? 2u : 1u);
     unsigned grid = a.kv_blocks;
+    a.q_tokens = 0;
     if (a.H > 0) {
-        a.q_tokens = tokens(a.H);
+        a.q_tokens = tokens(a.H, 1);
         grid += static_cast<unsigned>((a.T + a.q_tokens - 1) / a.q_tokens);
     }
     if (D == 128) return bf16 ? launch_kind<128, true>(a, kv4, grid, s) : launch_kind<128, false>(a, kv4, grid, s);
