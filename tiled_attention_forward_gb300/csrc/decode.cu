@@ -57,7 +57,6 @@ constexpr int kPart = 16;                 // keys that lie in one page and take 
 constexpr int kMaxCtas = 320;             // parts in the workspace: two per CTA
 constexpr int kAloneUnits = 2;            // longest target that one warp takes alone
 constexpr int kMaxParts = 64;             // CTAs a sequence is cut between: one CTA joins the parts
-constexpr float kLeastFactor = 1.2e-38f;  // keeps masked scores -inf at scale 0
 constexpr float kLow = -3.0e38f;          // the running max of a row that has seen no key
 constexpr float kRescaleThreshold = 8.0f; // log2 units: P <= 2^8 while the max is stale
 

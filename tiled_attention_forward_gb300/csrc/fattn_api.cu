@@ -23,6 +23,11 @@ static_assert(static_cast<long long>(kUnfusedStaticBytes) == FATTN_UNFUSED_STATI
               "static workspace size must match the public header");
 constexpr float kLog2e = 1.4426950408889634f;
 
+// The tensor-core forward sets masked scores to -inf and multiplies by the scale
+// afterwards, where -inf * 0 would be NaN: a scale of 0, or one that underflows,
+// is raised to about the smallest normal number, beside which no score differs from 0.
+float score_factor(float scale) { return std::max(scale * kLog2e, kLeastFactor); }
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0u; }
 
 size_t elem_bytes(int dtype) { return dtype == FATTN_F32 ? 4u : 2u; }
@@ -391,7 +396,6 @@ int fattn_fwd_gqa(const void* q, const void* k, const void* v, void* o, float* l
     if (st != FATTN_OK || empty) return st;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_h);
     const int64_t BH = B * H;
-    const float scale_log2 = scale * kLog2e;
 
     if (dtype == FATTN_F32) {
         int sms = 0;
@@ -399,7 +403,7 @@ int fattn_fwd_gqa(const void* q, const void* k, const void* v, void* o, float* l
         if (st != FATTN_OK) return st;
         cudaError_t e = ffma_launch(static_cast<const float*>(q), static_cast<const float*>(k),
                                     static_cast<const float*>(v), static_cast<float*>(o), lse, BH, H,
-                                    Hkv, N, D, scale_log2, causal != 0, stream);
+                                    Hkv, N, D, scale * kLog2e, causal != 0, stream);
         return e == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
     }
 
@@ -421,7 +425,7 @@ int fattn_fwd_gqa(const void* q, const void* k, const void* v, void* o, float* l
     a.num_qblk = static_cast<int>(ceil_div(N, int64_t(kTcBM) * kTcQTiles));
     a.num_tasks = a.num_qblk * a.BH;
     a.head_group = causal_head_group(BH, H, Hkv, N, D);
-    a.scale_log2 = scale_log2;
+    a.scale_log2 = score_factor(scale);
     a.timeout_ns = kDefaultTimeoutNs;
     const int grid = static_cast<int>(std::min<int64_t>(a.num_tasks, sms));
     cudaError_t e = tc_launch(a, static_cast<int>(D), bf16, causal != 0, grid, stream);
@@ -1024,7 +1028,7 @@ int fattn_fwd_packed(const void* q, const void* k, const void* v, void* o, float
     a.Hkv = static_cast<int>(Hkv);
     a.BH = a.H;
     a.head_group = causal_head_group(H, H, Hkv, T, D);  // as one sequence of all tokens
-    a.scale_log2 = scale * kLog2e;
+    a.scale_log2 = score_factor(scale);
     a.timeout_ns = kDefaultTimeoutNs;
     a.plan = static_cast<PackedPlan*>(workspace);
     a.cu = cu_seqlens;

@@ -10,6 +10,7 @@
 namespace fattn {
 
 constexpr int kMaxDevices = 64;
+constexpr float kLeastFactor = 1.2e-38f;  // a score factor of 0 becomes this: a masked score stays -inf times it
 
 // Raises one kernel's dynamic shared-memory limit once per device.  Each call
 // site passes its own flag array; the flags are atomics, so host threads that
