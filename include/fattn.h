@@ -403,13 +403,16 @@ FATTN_API int fattn_cache_append(const void* q, const void* k, const void* v, vo
  * clamp(round((x - zero) / scale), 0, 15), ties to even, 0 where scale is 0; in
  * fp32, and to twice its precision where fp32 cannot tell to which side one of
  * them rounds.
- * Elements past +-65504 are held as +-65504; a NaN takes no part in its
- * group's scale and is held as the group's zero.
+ * Elements past +-65504 are taken as +-65504; a NaN takes no part in its
+ * group's scale and is held as the group's zero.  As the scale is rounded to
+ * nearest, the largest element of a group may be held a little (at most half a
+ * unit of the scale's last place, 15 times) above its value, and so above 65504.
  *
  *   held     : 0 = k_out receives the rotated k rounded to `dtype`, and v_out
  *              v itself; otherwise both receive the values that the cache now
  *              stands for, rounded to `dtype` (a prompt's own attention then
- *              sees what later steps will read).  Either may be NULL.
+ *              sees what later steps will read; in fp16 what is past 65504 is
+ *              written as 65504).  Either may be NULL.
  *   strides  : host array of 12: q, k, v, q_out, k_out, v_out.
  * Everything else as fattn_cache_append.
  */
@@ -463,7 +466,8 @@ FATTN_API int fattn_decode(const void* q, void* o, float* lse, const int64_t* st
 /*
  * fattn_decode_kv4 -- fattn_decode over a 4-bit cache (above).  q and o are
  * `dtype`; K's codes enter the products exactly and its scales in fp32, V is
- * taken as fp16(code * scale + zero), and the weights are rounded to fp16.
+ * taken as 2 fp16((code * scale + zero) / 2), and the weights are rounded to
+ * fp16.  An o in fp16 holds +-65504 for what is past it.
  */
 FATTN_API int fattn_decode_kv4(const void* q, void* o, float* lse, const int64_t* strides,
                      const void* k_codes, const void* k_scales, const void* v_codes,

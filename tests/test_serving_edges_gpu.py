@@ -1,16 +1,19 @@
 """The serving operators at the edges of what their contracts allow, against plain
 64-bit forms (tests/serving_ref.py)."""
+import math
 
 import pytest
 import torch
 
 import tiled_attention_forward_gb300 as fattn
 from tests import serving_ref as R
+from tests.test_cache_gpu import append, check_decode, make_decode, new_cache, run_decode
 from tests.test_packed_gpu import check_packed, make
 
 pytestmark = pytest.mark.gpu
 
 DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
+
 
 def ok():
     torch.cuda.synchronize()
@@ -34,3 +37,84 @@ def test_scale_zero_is_the_mean_of_the_visible_values(dtype, D, causal, scale):
         ok()
         one = torch.tensor([0, N], dtype=torch.int32)
         check_packed(*(t[0].transpose(0, 1) for t in (q, k, v)), one, causal, scale, o[0].transpose(0, 1), lse[0], "dense")
+
+
+def rows_at_the_ends(T, Hkv, D, dt, seed):
+    """Rows whose groups of 32 reach the ends of fp16's range, in several ways."""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(T, Hkv, D // 32, 32, generator=g) * 10.0 ** torch.randint(0, 4, (T, Hkv, D // 32, 1), generator=g)
+    big = 1e5 if dt == torch.bfloat16 else 65504.0
+    kinds = [(0.0, big), (-big, big), (0.0, math.inf), (-math.inf, math.inf), (None, 65504.0), (None, math.inf),
+             (-60000.0, 65504.0), (60000.0, big), (-math.inf, None), (None, None)]
+    pick = torch.randint(0, len(kinds), (T, Hkv, D // 32), generator=g)
+    for i, (lo, hi) in enumerate(kinds):
+        m = pick == i
+        sub = x[m]
+        if lo is not None and hi is not None:
+            a, b = max(lo, -65504.0), min(hi, 65504.0)
+            sub = a + (b - a) * torch.rand(sub.shape, generator=g)
+        if lo is not None:
+            sub[:, 3] = lo
+        if hi is not None:
+            sub[:, 7] = hi
+        x[m] = sub
+    return x.flatten(-2).to(dt)
+
+
+@pytest.mark.parametrize("held", [True, False])
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("fp16", 64), ("fp16", 128), ("bf16", 64)])
+def test_kv4_values_at_the_ends_of_the_range_stay_finite(dtype, D, held):
+    """What the append holds for elements at and past +-65504 may lie a little
+    past it (the scale is rounded, to nearest): outputs in 16 bits and the
+    attention over such rows are finite all the same, and right."""
+    dt, T, Hkv, H, ps = DT[dtype], 160, 2, 8, 16
+    v = rows_at_the_ends(T, Hkv, D, dt, D)
+    k = rows_at_the_ends(T, Hkv, D, dt, D + 1)
+    cache = new_cache(True, T // ps, Hkv, ps, D, dt, 0.0)
+    k_out, v_out = (torch.empty(T, Hkv, D, dtype=dt, device="cuda") for _ in range(2))
+    fattn.cache_append_kv4(k.cuda(), v.cuda(), *cache, torch.arange(T).cuda(), k_out=k_out, v_out=v_out, held=held)
+    ok()
+    past = 0
+    for which, x, out, c, s in (("k", k, k_out, *cache[:2]), ("v", v, v_out, *cache[2:])):
+        c, s = (t.cpu().transpose(1, 2).flatten(0, 1) for t in (c, s))  # [T, Hkv, ..]
+        assert torch.isfinite(s).all()
+        if not held:
+            assert torch.equal(out.cpu(), x)
+            continue
+        val = R.held(c, s, which)
+        past += (val > 65519.0).sum().item()
+        size = val.abs() + 16 * s[..., 0].double().repeat_interleave(32, -1)
+        if dt == torch.float16:
+            val = val.clamp(-65504, 65504)  # the nearest that fp16 has
+        R.check(out, val, R.u_of(dt) * (1 + 2.0 ** -10) * val.abs() + 2.0 ** -23 * size + R.tiny(dt), which)
+    assert past > 20 or not held
+    # attention: keys of ordinary size first, then the extreme ones (weights decided by few keys: scores of some 100)
+    g = torch.Generator().manual_seed(3)
+    table = torch.arange(T // ps, dtype=torch.int32)[None].repeat(5, 1).cuda()
+    lens = torch.tensor([T, 1, 17, 33, T - 5], dtype=torch.int32).cuda()
+    for kk, scale in ((torch.randn(T, Hkv, D, generator=g).to(dt), 0.2), (k, 2.0 ** -17)):
+        fattn.cache_append_kv4(kk.cuda(), v.cuda(), *cache, torch.arange(T).cuda())
+        for Nq in (1, 3, 8):
+            q = torch.randn(5, H, Nq, D, generator=g).to(dt).cuda()
+            o, lse = fattn.decode_kv4(q, *cache, table, lens, scale=scale)
+            ok()
+            check_saturated(q, cache, table, lens, scale, o, lse)
+
+
+def check_saturated(q, cache, table, lens, scale, o, lse):
+    """check_decode's bounds, with outputs in fp16 cut to +-65504."""
+    B, H, Nq, D = q.shape
+    cache, table = [t.cpu() for t in cache], table.cpu()
+    for b, n in enumerate(lens.tolist()):
+        ends = [max(0, n - Nq + 1 + i) for i in range(Nq)]
+        rows = [R.gather(t, table[b], n) for t in cache]
+        k, v = R.held(rows[0], rows[1], "k"), R.held(rows[2], rows[3], "v")
+        off = (rows[3][..., 1].double().abs() + 16 * rows[3][..., 0].double()).repeat_interleave(32, -1)
+        ro, rl, av, worst = R.attend(q[b].cpu().double(), k, v, scale, ends)
+        _, _, v_err, _ = R.attend(q[b].cpu().double(), k, 2.0 ** -11 * (v.abs() + off), scale, ends)
+        bo, bl = R.attend_bounds(ro, rl, av, worst, D, q.dtype, 2.0 ** -11, v_err)
+        if q.dtype == torch.float16:
+            ro = ro.clamp(-65504, 65504)
+        seen = torch.tensor([e > 0 for e in ends])
+        R.check(o[b].cpu()[:, seen], ro[:, seen], bo[:, seen], "O of %d" % n)
+        R.check(lse[b].cpu()[:, seen], rl[:, seen], bl[:, seen], "LSE of %d" % n)

@@ -81,6 +81,18 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// pack8 with fp16's ends for what is past them: the values that a 4-bit group
+// stands for, of which the largest may be (its scale is rounded to nearest).
+template <bool BF16>
+__device__ __forceinline__ uint4 pack8_finite(const float (&x)[8]) {
+    if (BF16) return pack8<BF16>(x);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // An 8 x 8 matrix of nibbles, one row per lane of a set of 8 lanes, transposed:
 // lane n's nibble p becomes lane p's nibble n.  kLane[b]: the lane-id bit that
 // stands for bit b of the set's index n.
@@ -409,7 +421,7 @@ __device__ __forceinline__ void append_row(const AppendArgs& a, const uint4& raw
                 add2(x[e], x[e + 1], code[e], code[e + 1], -kTwo23, -kTwo23);
                 fma2(x[e], x[e + 1], x[e], x[e + 1], s, s, z, z);
             }
-            rounded = pack8<BF16>(x);
+            rounded = pack8_finite<BF16>(x);
         }
     } else if (on) {
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(kIsV ? a.v_pages : a.k_pages) + place + 8 * c) = rounded;

@@ -137,6 +137,12 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
+// The same in fp16, with +-65504 for what is past it (NaN stays NaN).
+__device__ __forceinline__ uint32_t pack_finite(float lo, float hi) {
+    uint32_t w;
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+    return w;
+}
 __device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
 __device__ __forceinline__ uint32_t as_u32(__half2 x) { return *reinterpret_cast<const uint32_t*>(&x); }
 
@@ -223,17 +229,20 @@ __device__ __forceinline__ int units_of(int len) {
     return max(1, static_cast<int>((static_cast<uint32_t>(len) + UNIT - 1) / UNIT));
 }
 
-// Writes 4 dims of one query row (of K/V head kvh) from its unnormalised sum.
-template <int D, bool BF16>
+// Writes 4 dims of one query row (of K/V head kvh) from its unnormalised sum: 4
+// bits, of half the values (Warp::accumulate), whose mean may lie a little past
+// fp16's range, as the values do.
+template <int D, bool BF16, bool KV4>
 __device__ __forceinline__ void store_out(const DecodeArgs& a, int b, int kvh, int row, int d, const float (&acc)[4],
                                           float mx, float sum) {
     const int share = a.H / a.Hkv;
     if (row >= share * a.Nq) return;
     const int h = kvh * share + row / a.Nq, i = row % a.Nq;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // 0: the row sees no key
+    const float inv = sum == 0.f ? 0.f : (KV4 ? 2.f : 1.f) / sum;  // 0: the row sees no key
+    auto pack = [](float x, float y) { return KV4 && !BF16 ? pack_finite(x, y) : pack16<BF16>(x, y); };
     uint16_t* o = static_cast<uint16_t*>(a.o) + b * a.o_bs + h * a.o_hs + i * a.o_ns + d;
     *reinterpret_cast<uint2*>(o) =
-        make_uint2(pack16<BF16>(acc[0] * inv, acc[1] * inv), pack16<BF16>(acc[2] * inv, acc[3] * inv));
+        make_uint2(pack(acc[0] * inv, acc[1] * inv), pack(acc[2] * inv, acc[3] * inv));
     if (d == 0 && a.lse != nullptr)
         a.lse[(static_cast<int64_t>(b) * a.H + h) * a.Nq + i] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
 }
@@ -503,9 +512,11 @@ struct Warp {
             // ldmatrix, transposed, on the codes' 16-bit pieces (4 codes each): lane
             // (g, t) gets piece g of a 16-byte chunk for keys 2t and 2t+1 side by
             // side, 4 pairs of codes.  Each pair is made fp16 by setting exponent
-            // bits (1024 + c, or 64 + c where the code sits 4 bits higher), taking
-            // that off again (exact), and one fused c scale + zero.  Which dims the
-            // lane's rows of O^T are is dim_of().
+            // bits (512 + c/2, or 32 + c/2 where the code sits 4 bits higher), taking
+            // that off again (exact), and one fused (c/2) scale + zero/2: half the
+            // value, as 15 scale + zero of a group whose largest element is 65504
+            // can lie past fp16's range (its scale is rounded to nearest).  Which
+            // dims the lane's rows of O^T are is dim_of().
             const int g = lane / 4, t = lane % 4;
             uint32_t x[2][D / 32];                   // [keys 0-7, 8-15][chunk]
             const uint32_t row = base + ((lane & 7) + (lane & 8)) * S::kVRow + (lane >> 4) * 16;
@@ -528,7 +539,7 @@ struct Warp {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     sc[u][i] = __byte_perm(m0[i], m1[i], 0x5410);
-                    ze[u][i] = __byte_perm(m0[i], m1[i], 0x7632);
+                    ze[u][i] = as_u32(__hmul2(as_half2(__byte_perm(m0[i], m1[i], 0x7632)), as_half2(0x38003800u)));
                 }
             }
 #pragma unroll
@@ -539,7 +550,7 @@ struct Warp {
                     const uint32_t piece = (j & 1) ? x[u][j / 2] >> 8 : x[u][j / 2];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const uint32_t magic = h ? 0x54005400u : 0x64006400u;
+                        const uint32_t magic = h ? 0x50005000u : 0x60006000u;
                         const uint32_t up = (piece & (h ? 0x00f000f0u : 0x000f000fu)) | magic;
                         const __half2 c = __hsub2(as_half2(up), as_half2(magic));
                         v[2 * u + h] = as_u32(__hfma2(c, as_half2(sc[u][j & 1]), as_half2(ze[u][j & 1])));
@@ -935,7 +946,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
                         if (4 * lane < D) {
                             const float4 v = *reinterpret_cast<const float4*>(mine + r * C::kPitch + 4 * lane);
                             const float acc[4] = {v.x, v.y, v.z, v.w};
-                            store_out<D, BF16>(a, my_b, kvh, rb * C::kRows + n * 8 + r, 4 * lane, acc, mx, sum);
+                            store_out<D, BF16, KV4>(a, my_b, kvh, rb * C::kRows + n * 8 + r, 4 * lane, acc, mx, sum);
                         }
                     }
                     __syncwarp();
@@ -991,7 +1002,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
                 acc[3] = fmaf(wt, v.w, acc[3]);
             }
             if (whole) {
-                store_out<D, BF16>(a, b, kvh, rb * C::kRows + r, d, acc, mx, sum);
+                store_out<D, BF16, KV4>(a, b, kvh, rb * C::kRows + r, d, acc, mx, sum);
             } else {
                 __stcg(reinterpret_cast<float4*>(part + 2 * C::kRows + r * D + d), make_float4(acc[0], acc[1], acc[2], acc[3]));
                 if (d == 0) {
@@ -1042,7 +1053,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
                             acc[3] = fmaf(wt, v[y].w, acc[3] * wo);
                         }
                     }
-                    store_out<D, BF16>(a, b, kvh, rb * C::kRows + r, d, acc, mx, sum);
+                    store_out<D, BF16, KV4>(a, b, kvh, rb * C::kRows + r, d, acc, mx, sum);
                 }
             }
         }
