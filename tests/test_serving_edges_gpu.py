@@ -118,3 +118,45 @@ def check_saturated(q, cache, table, lens, scale, o, lse):
         seen = torch.tensor([e > 0 for e in ends])
         R.check(o[b].cpu()[:, seen], ro[:, seen], bo[:, seen], "O of %d" % n)
         R.check(lse[b].cpu()[:, seen], rl[:, seen], bl[:, seen], "LSE of %d" % n)
+
+
+def exact_codes(x, scales):
+    """Codes of x (float64, exact) against the stored scales and zeros, from the definition."""
+    s, z = (scales[..., i].double().repeat_interleave(32, -1) for i in range(2))
+    q = torch.where(s > 0, (x - z) / torch.where(s > 0, s, 1.0), 0.0)
+    return q.clamp(0, 15).round(), ((q - q.floor() - 0.5).abs() < 1e-5) & (q - q.floor() != 0.5)
+
+
+@pytest.mark.parametrize("rot", [0, 16])
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("fp16", 64), ("fp16", 128), ("bf16", 64)])
+def test_append_kv4_codes_where_differences_are_not_exact(dtype, D, rot):
+    """Elements beside a zero of quite another size: x - zero takes more than 24
+    bits and lies next to a border of two codes.  Every code of a row that does
+    not turn is the exact quotient's rounding."""
+    dt, T, ps = DT[dtype], 320, 16
+    g = torch.Generator().manual_seed(D + rot)
+    e = 2.0 ** -torch.randint(17, 25, (T, 1, D // 32, 1), generator=g).double()       # tiny, exact in both types
+    step = 2.0 ** torch.randint(-2, 3, (T, 1, D // 32, 1), generator=g).double()
+    k = torch.randint(0, 15, (T, 1, D // 32, 32), generator=g).double()
+    # even tokens: a tiny zero under multiples of half steps; odd ones: a zero of -13/2 steps under tiny elements
+    low = torch.where(torch.randint(0, 2, e.shape, generator=g) > 0, e, -e)
+    x = (k + 0.5) * step
+    x[..., 0], x[..., 1] = low[..., 0], 15 * step[..., 0]
+    y = torch.where(torch.randint(0, 2, k.shape, generator=g) > 0, e, -e) * torch.randint(1, 4, k.shape, generator=g)
+    y[..., 0], y[..., 1] = -6.5 * step[..., 0], 8.5 * step[..., 0]
+    x[1::2] = y[1::2]
+    x = x.flatten(-2).to(dt)
+    cache = new_cache(True, T // ps, 1, ps, D, dt, 0.0)
+    kw = {}
+    if rot:
+        cos, sin = (t.cuda() for t in R.tables(64, rot))
+        kw = dict(pos=torch.zeros(T, dtype=torch.int32).cuda(), cos=cos, sin=sin)  # position 0: the turn changes nothing
+    fattn.cache_append_kv4(x.cuda(), x.cuda(), *cache, torch.arange(T).cuda(), **kw)
+    ok()
+    near = 0
+    for which, codes, scales in (("k", *cache[:2]), ("v", *cache[2:])):
+        codes, scales = (t.cpu().transpose(1, 2).flatten(0, 1) for t in (codes, scales))
+        want, close = exact_codes(x.double(), scales)
+        near += close.sum().item()
+        assert torch.equal(R.unpack(codes, which).double(), want), which
+    assert near > 1000

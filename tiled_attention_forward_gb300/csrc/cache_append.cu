@@ -155,8 +155,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // zero, the scale or a code -- is too close to its border for fp32 to tell the
 // side: about one group in a thousand, which requantise() then settles.  (A
 // code on the wrong side is off by a whole step, and a reader of the cache
-// could not tell that from an error.)  Exact x needs this for the scale alone:
-// its quotients are exact ties or well away from one.
+// could not tell that from an error.)  Exact x needs this for the scale, and for
+// a code where x - zero takes more than 24 bits (elements of very different
+// size): of an exact difference the quotient is an exact tie or more than half
+// a unit of its last place away from one.  16-bit values are often at a tie, so
+// that is asked only of threads that have one.
 __device__ __forceinline__ bool quantise(const float (&x)[8], bool rotated, int partner, float (&t)[8], __half& scale,
                                          __half& zero) {
     float lo = min3(x[0], x[1], x[2]), hi = max3(x[0], x[1], x[2]);
@@ -202,7 +205,15 @@ __device__ __forceinline__ bool quantise(const float (&x)[8], bool rotated, int 
         worst = max3(worst, fabsf(q0), fabsf(q1));
     }
     // The quotient's own error: 16 * 2 roundings, and that of x in steps.
-    if (rotated) near = near || worst > 0.5f - fmaf(err, inv, 2.0e-6f);
+    if (worst > 0.5f - fmaf(err, inv, 2.0e-6f)) {
+        bool exact = !rotated;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float d = __fsub_rn(x[e], z);  // exact where both of its terms come back
+            exact = exact && __fadd_rn(d, z) == x[e] && __fsub_rn(x[e], d) == z;
+        }
+        near = near || !exact;
+    }
     return near;
 }
 
