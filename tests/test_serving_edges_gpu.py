@@ -160,3 +160,33 @@ def test_append_kv4_codes_where_differences_are_not_exact(dtype, D, rot):
         near += close.sum().item()
         assert torch.equal(R.unpack(codes, which).double(), want), which
     assert near > 1000
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_append_kv4_pairs_far_past_the_range(interleaved):
+    """Pairs of some 10^7 that turn until one of them lies within +-65504: its
+    fp32 error is that of the pair's size, hundreds of times the range's own.
+    Codes, scales and zeros are those of the rotation in 64 bits."""
+    T, D, ps = 4000, 64, 16
+    g = torch.Generator().manual_seed(31)
+    cos, sin = R.tables(4096, D)
+    pos = torch.randint(1, 4096, (T,), generator=g, dtype=torch.int32)
+    c, s = cos.double()[pos.long()], sin.double()[pos.long()]
+    b = (1 + torch.rand(T, D // 2, generator=g).double()) * 2.0 ** 24 * c     # along (sin, cos): turns to (0, 1)
+    a = b * s / c
+    k = torch.stack([a, b], -1).flatten(-2) if interleaved else torch.cat([a, b], -1)
+    k = k[:, None].to(torch.bfloat16)
+    cache = new_cache(True, T // ps, 1, ps, D, torch.bfloat16, 0.0)
+    fattn.cache_append_kv4(k.cuda(), k.cuda(), *cache, torch.arange(T).cuda(), pos=pos.cuda(), cos=cos.cuda(),
+                           sin=sin.cuda(), interleaved=interleaved)
+    ok()
+    x = R.rotate(k, pos, cos, sin, interleaved)[0].clamp(-65504, 65504).unflatten(-1, (-1, 32))
+    assert (x.abs() < 60000).sum() > T * D // 8
+    lo, hi = x.amin(-1), x.amax(-1)
+    scale, zero = ((hi - lo) / 15).float().half().double(), lo.float().half().double()
+    got = cache[1].cpu().double().transpose(1, 2).reshape(T, 1, D // 32, 2)
+    assert torch.equal(got[..., 0], scale) and torch.equal(got[..., 1], zero)
+    q = (x - zero[..., None]) / torch.where(scale > 0, scale, 1.0)[..., None]
+    want = torch.where(scale[..., None] > 0, q, 0.0).clamp(0, 15).round().flatten(-2)
+    codes = R.unpack(cache[0].cpu().transpose(1, 2).reshape(T, 1, D // 2), "k").double()
+    assert torch.equal(codes, want)

@@ -171,12 +171,12 @@ __device__ __forceinline__ bool quantise(const float (&x)[8], bool rotated, int 
         hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, m));
     }
     if (!(lo <= hi)) lo = hi = 0.f;  // nothing but NaN
+    float most = fmaxf(-lo, hi);     // (before the clamp: pairs far past the range may turn into it)
     lo = fminf(fmaxf(lo, -kFp16Max), kFp16Max) + 0.f;  // (+ 0: never -0, whose bits differ from 0's below)
     hi = fminf(fmaxf(hi, -kFp16Max), kFp16Max);
     const float step = (hi - lo) * (1.f / 15.f);
     scale = __float2half_rn(step);
     zero = __float2half_rn(lo);
-    float most = fmaxf(-lo, hi);
     most = fmaxf(most, __shfl_sync(0xffffffffu, most, partner));
     const float err = rotated ? 2.6e-7f * most : 0.f;  // 3 sqrt(2) 2^-24
     const float es = fmaf(0.14f, err, 2.4e-7f * step);  // 2 err / 15 and three roundings
