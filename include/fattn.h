@@ -442,7 +442,7 @@ FATTN_API int64_t fattn_decode_workspace_bytes(int64_t B, int64_t H, int64_t Hkv
  * page_size], place j mod page_size.  A row that sees no key gets O = 0 and
  * LSE = -inf.  What a page holds behind the last token never reaches O.  (With
  * Nq > 1 a NaN or infinity in V of one of the newest Nq tokens also reaches the
- * rows before it, whose weight of it is 0.)
+ * rows before it that see any key, whose weight of it is 0.)
  *
  *   q, o        : [B, H, Nq, D]; `strides` is a host array of 6: batch, head
  *                 and token stride of q, then of o.  o overlaps nothing else.

@@ -190,3 +190,21 @@ def test_append_kv4_pairs_far_past_the_range(interleaved):
     want = torch.where(scale[..., None] > 0, q, 0.0).clamp(0, 15).round().flatten(-2)
     codes = R.unpack(cache[0].cpu().transpose(1, 2).reshape(T, 1, D // 2), "k").double()
     assert torch.equal(codes, want)
+
+
+@pytest.mark.parametrize("kv4", [False, True])
+def test_decode_rows_without_keys_beside_values_that_are_not_finite(kv4):
+    """More new tokens than the sequence has: the rows before its first key are O
+    = 0, LSE = -inf, whatever its values hold; alone, joined and cut between CTAs."""
+    B, H, Hkv, Nq, D, ps = 700, 4, 2, 6, 64, 16
+    for lens in ([2], [3] * B, [4, 9000, 1]):  # few keys; a warp each; beside a sequence that is cut
+        q, cache, table, seq = make_decode(kv4, lens, H, Hkv, Nq, D, ps, "fp16", 40)
+        for t in cache[2:] if kv4 else cache[1:]:
+            if t.dtype == torch.float16:
+                t.fill_(math.nan)
+        o, lse = run_decode(kv4, q, cache, table, seq)
+        ok()
+        for b, n in enumerate(lens[:40]):
+            empty = max(0, Nq - n)
+            assert (o[b, :, :empty] == 0).all() and (lse[b, :, :empty] == -math.inf).all()
+            assert torch.isnan(o[b, :, empty:]).all() and torch.isfinite(lse[b, :, empty:]).all()

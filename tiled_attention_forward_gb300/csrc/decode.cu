@@ -238,13 +238,14 @@ __device__ __forceinline__ void store_out(const DecodeArgs& a, int b, int kvh, i
     const int share = a.H / a.Hkv;
     if (row >= share * a.Nq) return;
     const int h = kvh * share + row / a.Nq, i = row % a.Nq;
-    const float inv = sum == 0.f ? 0.f : (KV4 ? 2.f : 1.f) / sum;  // 0: the row sees no key
+    const bool none = sum == 0.f;  // the row sees no key (its sum of values: 0, or 0 times what is not finite)
+    const float inv = (KV4 ? 2.f : 1.f) / sum;
     auto pack = [](float x, float y) { return KV4 && !BF16 ? pack_finite(x, y) : pack16<BF16>(x, y); };
     uint16_t* o = static_cast<uint16_t*>(a.o) + b * a.o_bs + h * a.o_hs + i * a.o_ns + d;
     *reinterpret_cast<uint2*>(o) =
-        make_uint2(pack(acc[0] * inv, acc[1] * inv), pack(acc[2] * inv, acc[3] * inv));
+        none ? make_uint2(0u, 0u) : make_uint2(pack(acc[0] * inv, acc[1] * inv), pack(acc[2] * inv, acc[3] * inv));
     if (d == 0 && a.lse != nullptr)
-        a.lse[(static_cast<int64_t>(b) * a.H + h) * a.Nq + i] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+        a.lse[(static_cast<int64_t>(b) * a.H + h) * a.Nq + i] = none ? -INFINITY : (mx + log2f(sum)) * kLn2;
 }
 
 // ---- one warp's keys ----------------------------------------------------------
