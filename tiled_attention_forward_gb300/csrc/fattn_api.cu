@@ -780,13 +780,15 @@ int run_append(AppendArgs& a, const int64_t* strides, int64_t num_pages, int64_t
     } else {
         const int64_t inner = Hkv * page_size * D;
         if (!stride_ok(a.page_stride) || a.page_stride < inner) return FATTN_ERR_INVALID_ARG;
-        if (num_pages * a.page_stride > kMaxElements) return FATTN_ERR_UNSUPPORTED;
+        if (a.page_stride > kMaxElements / std::max<int64_t>(num_pages, 1)) return FATTN_ERR_UNSUPPORTED;
         cache[0] = rows_view(a.k_pages, num_pages, a.page_stride, 1, 0, inner);
         cache[1] = rows_view(a.v_pages, num_pages, a.page_stride, 1, 0, inner);
     }
+    // (Positions are int32: no row past 2^31 is read.)
+    const int64_t table_bytes = std::min<int64_t>(a.max_pos, int64_t(1) << 31) * (rot / 2) * 4;
     const View tables[4] = {dense_view(a.slots, T * 8), dense_view(rot > 0 ? a.pos : nullptr, T * 4),
-                            dense_view(rot > 0 ? a.cos : nullptr, a.max_pos * (rot / 2) * 4),
-                            dense_view(rot > 0 ? a.sin : nullptr, a.max_pos * (rot / 2) * 4)};
+                            dense_view(rot > 0 ? a.cos : nullptr, table_bytes),
+                            dense_view(rot > 0 ? a.sin : nullptr, table_bytes)};
     for (int i = 0; i < 4; ++i) {
         for (int j = 0; j < 6; ++j)
             if (views_overlap(cache[i], views[j])) return FATTN_ERR_INVALID_ARG;
@@ -866,7 +868,7 @@ int run_decode(DecodeArgs& a, const int64_t* strides, int64_t num_pages, int64_t
     const int64_t inner = Hkv * page_size * D;
     if (!kv4) {
         if (!stride_ok(a.page_stride) || a.page_stride < inner) return FATTN_ERR_INVALID_ARG;
-        if (num_pages * a.page_stride > kMaxElements) return FATTN_ERR_UNSUPPORTED;
+        if (a.page_stride > kMaxElements / std::max<int64_t>(num_pages, 1)) return FATTN_ERR_UNSUPPORTED;
     }
     const int64_t page_bytes = kv4 ? page_rows * (D / 2)
                                    : (num_pages > 0 ? 2 * ((num_pages - 1) * a.page_stride + inner) : 0);
