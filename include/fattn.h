@@ -445,7 +445,8 @@ FATTN_API int64_t fattn_decode_workspace_bytes(int64_t B, int64_t H, int64_t Hkv
  * rows before it that see any key, whose weight of it is 0.)
  *
  *   q, o        : [B, H, Nq, D]; `strides` is a host array of 6: batch, head
- *                 and token stride of q, then of o.  o overlaps nothing else.
+ *                 and token stride of q, then of o.  o overlaps nothing else
+ *                 (it may be another slice of the tensor that q is a slice of).
  *   lse         : fp32 [B, H, Nq] contiguous, or NULL.
  *   block_table : device int32 [B][table_width].
  *   seq_lens    : device int32 [B], 0 <= seq_lens[b] <= table_width*page_size

@@ -208,3 +208,20 @@ def test_decode_rows_without_keys_beside_values_that_are_not_finite(kv4):
             empty = max(0, Nq - n)
             assert (o[b, :, :empty] == 0).all() and (lse[b, :, :empty] == -math.inf).all()
             assert torch.isnan(o[b, :, empty:]).all() and torch.isfinite(lse[b, :, empty:]).all()
+
+
+@pytest.mark.parametrize("kv4", [False, True])
+@pytest.mark.parametrize("Nq", [1, 3])
+def test_decode_output_beside_its_query_in_one_tensor(kv4, Nq):
+    B, H, Hkv, D = 3, 8, 2, 64
+    q, cache, table, lens = make_decode(kv4, [100, 3, 33], H, Hkv, Nq, D, 32, "fp16", 60)
+    want, want_l = run_decode(kv4, q, cache, table, lens)
+    both = torch.full((B, Nq, 2 * H + 1, D), 7.0, dtype=q.dtype, device="cuda")
+    both[:, :, :H] = q.transpose(1, 2)
+    out = both[:, :, H:2 * H].transpose(1, 2)
+    o, lse = run_decode(kv4, both[:, :, :H].transpose(1, 2), cache, table, lens, out=out)
+    ok()
+    assert o is out and torch.equal(o, want) and torch.equal(lse, want_l)
+    assert torch.equal(both[:, :, :H].transpose(1, 2), q) and (both[:, :, 2 * H:] == 7).all()
+    with pytest.raises(fattn.FattnError):
+        run_decode(kv4, both[:, :, :H].transpose(1, 2), cache, table, lens, out=both[:, :, H - 1:2 * H - 1].transpose(1, 2))

@@ -26,3 +26,34 @@ def test_sizes_within_the_limits_are_accepted():
     assert call_decode(P=4, page_stride=1 << 50, **far) == NO_DEVICE
     assert call_append(P=1, page_stride=1 << 52, **far) == NO_DEVICE
     assert call_append(max_pos=1 << 62, cos=20 * A, sin=30 * A) == NO_DEVICE  # rows that no int32 position names
+
+
+def decode_slices(H=4, Nq=1, D=64, B=3, gap=0, order="bnh", **kw):
+    """q and o as neighbouring slices of one tensor [B, Nq, 2 H + 4, D] (or head-major within a batch)."""
+    row = (2 * H + 4) * D
+    st = [Nq * row, D, row] if order == "bnh" else [Nq * row, Nq * D, D]
+    o = A + 2 * (H * (D if order == "bnh" else Nq * D) + gap)
+    return call_decode(q=A, o=o, strides=st * 2, B=B, H=H, Hkv=2, Nq=Nq, D=D, lse=1 << 50, kp=1 << 51, vp=1 << 52,
+                       table=1 << 53, lens=1 << 54, ws=1 << 55, **kw)
+
+
+def test_decode_refuses_an_output_in_its_query():
+    for order in ("bnh", "bhn"):
+        for Nq in (1, 3):
+            room = 4 * 64 * (1 if order == "bnh" else Nq)  # behind o, before the next token's or batch's q
+            for gap in (-8, -64, room + 8):
+                assert decode_slices(Nq=Nq, gap=gap, order=order) == INVALID, (order, Nq, gap)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-GPU path")
+def test_decode_takes_an_output_beside_its_query_in_one_tensor():
+    for order in ("bnh", "bhn"):
+        for Nq in (1, 3):
+            for B in (1, 3):
+                for gap in (0, 8, 4 * 64):
+                    assert decode_slices(Nq=Nq, B=B, gap=gap * (1 if order == "bnh" else Nq), order=order) == NO_DEVICE
+    # head-major q, token-major o, each in its own part of a batch's block of one tensor
+    assert call_decode(q=A, o=A + 2 * 1024, strides=[2048, 192, 64, 2048, 64, 256], B=5, H=4, Nq=3,
+                       lse=1 << 50) == NO_DEVICE
+    assert call_decode(q=A, o=A + 2 * 760, strides=[2048, 192, 64, 2048, 64, 256], B=5, H=4, Nq=3,
+                       lse=1 << 50) == INVALID

@@ -138,6 +138,54 @@ bool views_overlap(const View& a, const View& b) {
     return true;
 }
 
+// 16-bit rows of D elements at three strides, in bytes; s ascending, dimensions
+// of one element left out (n = 1, s = 0).
+struct Rows3 {
+    uintptr_t p, row;
+    uintptr_t n[3], s[3];
+    uintptr_t below(uintptr_t m) const {  // extent of what is stepped by less than m
+        uintptr_t x = row;
+        for (int i = 0; i < 3; ++i)
+            if (s[i] < m) x += (n[i] - 1) * s[i];
+        return x;
+    }
+};
+
+Rows3 rows3(const void* p, const int64_t (&n)[3], const int64_t* s, int64_t D) {
+    Rows3 r = {reinterpret_cast<uintptr_t>(p), static_cast<uintptr_t>(2 * D), {}, {}};
+    for (int i = 0; i < 3; ++i) {
+        r.n[i] = static_cast<uintptr_t>(n[i]);
+        r.s[i] = n[i] > 1 ? static_cast<uintptr_t>(2 * s[i]) : 0;
+    }
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2; ++j)
+            if (r.s[j] > r.s[j + 1]) {
+                std::swap(r.s[j], r.s[j + 1]);
+                std::swap(r.n[j], r.n[j + 1]);
+            }
+    return r;
+}
+
+// Whether two sets of rows share a byte: their whole ranges do, and so do they
+// modulo each stride m of one whose multiples all larger strides of both are
+// (slices of one tensor lie apart within such a period).
+bool rows3_overlap(const Rows3& a, const Rows3& b) {
+    const uintptr_t all = UINTPTR_MAX;
+    if (!(a.p < b.p + b.below(all) && b.p < a.p + a.below(all))) return false;
+    for (int level = 0; level < 6; ++level) {
+        const uintptr_t m = level < 3 ? a.s[level] : b.s[level - 3];
+        if (m == 0) continue;
+        bool whole = true;
+        for (int i = 0; i < 3; ++i)
+            whole = whole && (a.s[i] < m || a.s[i] % m == 0) && (b.s[i] < m || b.s[i] % m == 0);
+        const uintptr_t na = a.below(m), nb = b.below(m);
+        if (!whole || na > m || nb > m) continue;
+        const uintptr_t d = b.p >= a.p ? (b.p - a.p) % m : (m - (a.p - b.p) % m) % m;  // b's place in a's period
+        if (d >= na && d + nb <= m) return false;
+    }
+    return true;
+}
+
 bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0 && s <= kMaxElements; }
 
 // Sizes of a paged cache and of its rows.
@@ -847,23 +895,16 @@ int run_decode(DecodeArgs& a, const int64_t* strides, int64_t num_pages, int64_t
         (reinterpret_cast<uintptr_t>(a.lse) & 3u) || (reinterpret_cast<uintptr_t>(a.block_table) & 3u) ||
         (reinterpret_cast<uintptr_t>(a.seq_lens) & 3u))
         return FATTN_ERR_MISALIGNED;
-    // Whole ranges; o's rows must not run into one another: some order of its
-    // strides nests.
-    auto extent = [&](const int64_t* s) { return 2 * ((B - 1) * s[0] + (H - 1) * s[1] + (Nq - 1) * s[2] + D); };
-    {
-        int64_t n[3] = {B, H, Nq}, s[3] = {strides[3], strides[4], strides[5]};
-        for (int i = 0; i < 2; ++i)
-            for (int j = 0; j < 2; ++j)
-                if (s[j] > s[j + 1]) {
-                    std::swap(s[j], s[j + 1]);
-                    std::swap(n[j], n[j + 1]);
-                }
-        int64_t inner = D;
-        for (int i = 0; i < 3; ++i) {
-            if (n[i] > 1 && s[i] < inner) return FATTN_ERR_INVALID_ARG;
-            if (n[i] > 1) inner = (n[i] - 1) * s[i] + inner;
-        }
+    // o's rows must not run into one another: its strides nest.
+    const int64_t sizes[3] = {B, H, Nq};
+    const Rows3 q_rows = rows3(a.q, sizes, strides, D), o_rows = rows3(a.o, sizes, strides + 3, D);
+    uintptr_t nested = o_rows.row;
+    for (int i = 0; i < 3; ++i) {
+        if (o_rows.n[i] <= 1) continue;
+        if (o_rows.s[i] < nested) return FATTN_ERR_INVALID_ARG;
+        nested += (o_rows.n[i] - 1) * o_rows.s[i];
     }
+    if (rows3_overlap(q_rows, o_rows)) return FATTN_ERR_INVALID_ARG;
     const int64_t page_rows = num_pages * page_size * Hkv;
     const int64_t inner = Hkv * page_size * D;
     if (!kv4) {
@@ -873,15 +914,15 @@ int run_decode(DecodeArgs& a, const int64_t* strides, int64_t num_pages, int64_t
     const int64_t page_bytes = kv4 ? page_rows * (D / 2)
                                    : (num_pages > 0 ? 2 * ((num_pages - 1) * a.page_stride + inner) : 0);
     const int64_t scale_bytes = kv4 ? page_rows * (D / kKv4Group) * 4 : 0;
-    const View in[7] = {dense_view(a.q, extent(strides)),          dense_view(a.k_pages, page_bytes),
-                        dense_view(a.v_pages, page_bytes),         dense_view(a.k_scales, scale_bytes),
-                        dense_view(a.v_scales, scale_bytes),       dense_view(a.block_table, B * table_width * 4),
+    auto range = [](const Rows3& r) { return dense_view(reinterpret_cast<const void*>(r.p), r.below(UINTPTR_MAX)); };
+    const View in[7] = {range(q_rows),                       dense_view(a.k_pages, page_bytes),
+                        dense_view(a.v_pages, page_bytes),   dense_view(a.k_scales, scale_bytes),
+                        dense_view(a.v_scales, scale_bytes), dense_view(a.block_table, B * table_width * 4),
                         dense_view(a.seq_lens, B * 4)};
-    const View out[3] = {dense_view(a.o, extent(strides + 3)), dense_view(a.lse, B * H * Nq * 4),
-                         dense_view(a.workspace, need)};
+    const View out[3] = {range(o_rows), dense_view(a.lse, B * H * Nq * 4), dense_view(a.workspace, need)};
     for (int i = 0; i < 3; ++i) {
-        for (const View& v : in)
-            if (views_overlap(out[i], v)) return FATTN_ERR_INVALID_ARG;
+        for (int j = i == 0 ? 1 : 0; j < 7; ++j)  // (o beside q: above)
+            if (views_overlap(out[i], in[j])) return FATTN_ERR_INVALID_ARG;
         for (int j = i + 1; j < 3; ++j)
             if (views_overlap(out[i], out[j])) return FATTN_ERR_INVALID_ARG;
     }
