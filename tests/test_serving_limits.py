@@ -57,3 +57,11 @@ def test_decode_takes_an_output_beside_its_query_in_one_tensor():
                        lse=1 << 50) == NO_DEVICE
     assert call_decode(q=A, o=A + 2 * 760, strides=[2048, 192, 64, 2048, 64, 256], B=5, H=4, Nq=3,
                        lse=1 << 50) == INVALID
+
+
+def test_decode_workspace_without_kv_heads_is_enough_for_any():
+    for H in (1, 6, 8, 40, 64):
+        for Nq in (1, 2, 5):
+            for D in (64, 128):
+                most = max(fattn.decode_workspace_bytes(2, H, Nq, D, Hkv) for Hkv in range(1, H + 1) if H % Hkv == 0)
+                assert fattn.decode_workspace_bytes(2, H, Nq, D) == most

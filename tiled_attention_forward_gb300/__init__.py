@@ -497,8 +497,10 @@ def cache_append_kv4(k, v, k_codes, k_scales, v_codes, v_scales, slots, pos=None
 
 
 def decode_workspace_bytes(B, H, Nq, D, Hkv=None):
-    """Bytes of workspace ``decode`` and ``decode_kv4`` need (whatever the sequences' lengths)."""
-    return int(load().fattn_decode_workspace_bytes(int(B), int(H), int(H if Hkv is None else Hkv), int(Nq), int(D)))
+    """Bytes of workspace ``decode`` and ``decode_kv4`` need (whatever the
+    sequences' lengths); without ``Hkv`` what is enough for any number of K/V
+    heads (the most query rows a K/V head take the most)."""
+    return int(load().fattn_decode_workspace_bytes(int(B), int(H), int(1 if Hkv is None else Hkv), int(Nq), int(D)))
 
 
 def _decode_defaults(q, Hkv, scale, out, lse, workspace, return_lse, stream):
