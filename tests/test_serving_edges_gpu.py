@@ -211,6 +211,110 @@ def test_decode_rows_without_keys_beside_values_that_are_not_finite(kv4):
 
 
 @pytest.mark.parametrize("kv4", [False, True])
+def test_captured_steps_read_what_they_append(kv4):
+    """A graph of several steps, each an append followed at once by the attention
+    over it, and a prompt's append followed by the packed attention of its rows:
+    the kernels of a replay start while the one before them ends.  Two graphs
+    with caches of their own replay at once; tokens, slots, positions and lengths
+    change between replays.  Results and caches are those of calls that wait."""
+    B, H, Hkv, D, ps, width, steps, T = 3, 8, 2, 128, 16, 8, 4, 200
+    dt = torch.bfloat16
+    cos, sin = (t.cuda() for t in R.tables(256, D))
+    table = torch.randperm(B * width, generator=torch.Generator().manual_seed(50)).to(torch.int32).view(B, width)
+    table_d = table.cuda()
+
+    class Side:
+        def __init__(self):
+            self.cache = new_cache(kv4, B * width, Hkv, ps, D, dt, 0.0)
+            self.prompt = new_cache(kv4, -(-T // ps), Hkv, ps, D, dt, 0.0)
+            self.x = torch.zeros(steps, B, H + 2 * Hkv, D, dtype=dt, device="cuda")
+            self.slots = torch.zeros(steps, B, dtype=torch.int64, device="cuda")
+            self.pos = torch.zeros(steps, B, dtype=torch.int32, device="cuda")
+            self.lens = torch.ones(steps, B, dtype=torch.int32, device="cuda")
+            self.px = torch.zeros(T, H + 2 * Hkv, D, dtype=dt, device="cuda")
+            self.pslots = torch.arange(T, device="cuda")
+            self.ppos = torch.arange(T, dtype=torch.int32, device="cuda")
+            self.cu = torch.tensor([0, 60, 61, T], dtype=torch.int32, device="cuda")
+            self.qr = torch.zeros(steps, B, H, D, dtype=dt, device="cuda")
+            self.o = torch.zeros(steps, B, H, 1, D, dtype=dt, device="cuda")
+            self.lse = torch.zeros(steps, B, H, 1, device="cuda")
+            self.pk = torch.zeros(T, Hkv, D, dtype=dt, device="cuda")
+            self.pv = torch.zeros(T, Hkv, D, dtype=dt, device="cuda")
+            self.po = torch.zeros(T, H, D, dtype=dt, device="cuda")
+            self.plse = torch.zeros(H, T, device="cuda")
+            self.ws = torch.empty(fattn.decode_workspace_bytes(B, H, 1, D, Hkv), dtype=torch.uint8, device="cuda")
+            self.pws = torch.empty(fattn.packed_workspace_bytes(3, T), dtype=torch.uint8, device="cuda")
+
+        def run(self, wait=lambda: None):
+            turn = dict(cos=cos, sin=sin)
+            pq, pk, pv = self.px[:, :H], self.px[:, H:H + Hkv], self.px[:, H + Hkv:]
+            append(kv4, pk, pv, self.prompt, self.pslots, pos=self.ppos, q=pq, q_out=pq, k_out=self.pk, v_out=self.pv,
+                   held=True, **turn)
+            wait()
+            fattn.fwd_packed(pq, self.pk, self.pv if kv4 else pv, self.cu, out=self.po, lse=self.plse,
+                             workspace=self.pws)
+            wait()
+            for i in range(steps):
+                x = self.x[i]
+                append(kv4, x[:, H:H + Hkv], x[:, H + Hkv:], self.cache, self.slots[i], pos=self.pos[i], q=x[:, :H],
+                       q_out=self.qr[i], **turn)
+                wait()
+                run_decode(kv4, self.qr[i].unsqueeze(2), self.cache, table_d, self.lens[i], out=self.o[i],
+                           lse=self.lse[i], workspace=self.ws)
+                wait()
+
+        def outputs(self):
+            return [self.qr, self.o, self.lse, self.pk, self.pv, self.po, self.plse, *self.cache, *self.prompt]
+
+    sides, want = [Side(), Side()], Side()
+    sides[0].run()  # (modules are loaded before a capture)
+    for t in sides[0].outputs():
+        t.zero_()
+    graphs = []
+    for side in sides:
+        s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            with torch.cuda.graph(g, stream=s):
+                side.run()
+        torch.cuda.current_stream().wait_stream(s)
+        graphs.append((g, s))
+    g = torch.Generator().manual_seed(51)
+    at = torch.tensor([0, 17, 100])
+    for t in want.outputs():
+        t.zero_()
+    for side in sides:
+        for t in side.outputs():
+            t.zero_()
+    for _ in range(5):
+        x = torch.randn(steps, B, H + 2 * Hkv, D, generator=g).to(dt)
+        px = torch.randn(T, H + 2 * Hkv, D, generator=g).to(dt)
+        pslots = torch.randperm(T, generator=g)
+        for side in sides + [want]:
+            side.x.copy_(x)
+            side.px.copy_(px)
+            side.pslots.copy_(pslots)
+            for i in range(steps):
+                j = at + i
+                side.slots[i] = (table[torch.arange(B), j // ps].long() * ps + j % ps).cuda()
+                side.pos[i] = j.to(torch.int32).cuda()
+                side.lens[i] = (j + 1).to(torch.int32).cuda()
+        torch.cuda.synchronize()
+        for graph, s in graphs:
+            with torch.cuda.stream(s):
+                graph.replay()
+        ok()
+        want.run(wait=torch.cuda.synchronize)
+        ok()
+        for side in sides:
+            for i, (a, b) in enumerate(zip(side.outputs(), want.outputs())):
+                assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), i
+        check_decode(kv4, want.qr[-1].unsqueeze(2), want.cache, table_d, want.lens[-1], fattn._default_scale(D),
+                     sides[0].o[-1], sides[0].lse[-1])
+        at = at + steps
+
+
+@pytest.mark.parametrize("kv4", [False, True])
 @pytest.mark.parametrize("Nq", [1, 3])
 def test_decode_output_beside_its_query_in_one_tensor(kv4, Nq):
     B, H, Hkv, D = 3, 8, 2, 64
@@ -225,3 +329,60 @@ def test_decode_output_beside_its_query_in_one_tensor(kv4, Nq):
     assert torch.equal(both[:, :, :H].transpose(1, 2), q) and (both[:, :, 2 * H:] == 7).all()
     with pytest.raises(fattn.FattnError):
         run_decode(kv4, both[:, :, :H].transpose(1, 2), cache, table, lens, out=both[:, :, H - 1:2 * H - 1].transpose(1, 2))
+
+
+@pytest.mark.parametrize("kv4", [False, True])
+@pytest.mark.parametrize("captured", [False, True])
+def test_inputs_made_on_another_stream(captured, kv4):
+    """Tokens that another stream makes, late: the append waits for the event and for
+    the kernel before it on its own stream, eager and in a graph with a fork and a join."""
+    B, H, Hkv, D, ps, n = 4, 8, 2, 64, 16, 90
+    dt = torch.float16
+    q, cache, table, lens = make_decode(kv4, [n] * B, H, Hkv, 1, D, ps, "fp16", 61)
+    j = torch.full((B,), n - 1)
+    slots = (table.cpu().long()[torch.arange(B), j // ps] * ps + j % ps).cuda()
+    src = torch.zeros(B, H + 2 * Hkv, D, dtype=dt, device="cuda")
+    x = torch.zeros_like(src)
+    slow = torch.zeros(1 << 27, device="cuda")
+    o, lse = torch.zeros(B, H, 1, D, dtype=dt, device="cuda"), torch.zeros(B, H, 1, device="cuda")
+    ws = torch.empty(fattn.decode_workspace_bytes(B, H, 1, D, Hkv), dtype=torch.uint8, device="cuda")
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def step(kv_cache, out, l):
+        append(kv4, x[:, H:H + Hkv], x[:, H + Hkv:], kv_cache, slots, stream=torch.cuda.current_stream())
+        run_decode(kv4, x[:, :H].unsqueeze(2), kv_cache, table, lens, out=out, lse=l, workspace=ws,
+                   stream=torch.cuda.current_stream())
+
+    def both():
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            slow.add_(1.0)          # some 150 us
+            x.copy_(src)
+        append(kv4, src[:, H:H + Hkv], src[:, H + Hkv:], cache, slots, stream=main)  # a kernel right before the join
+        main.wait_stream(side)
+        step(cache, o, lse)
+
+    main.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(main):
+        both()
+        if captured:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=main):
+                both()
+        g = torch.Generator(device="cuda").manual_seed(62)
+        for _ in range(4):
+            src.copy_(torch.randn(src.shape, generator=g, device="cuda"))
+            x.fill_(9.0)
+            other = [t.clone() for t in cache]
+            if captured:
+                graph.replay()
+            else:
+                both()
+            torch.cuda.synchronize()
+            assert torch.equal(x, src)
+            want, want_l = torch.zeros_like(o), torch.zeros_like(lse)
+            step(other, want, want_l)
+            ok()
+            assert torch.equal(o, want) and torch.equal(lse, want_l)
+            for a, b in zip(cache, other):
+                assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
