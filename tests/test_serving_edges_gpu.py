@@ -386,3 +386,26 @@ def test_inputs_made_on_another_stream(captured, kv4):
             assert torch.equal(o, want) and torch.equal(lse, want_l)
             for a, b in zip(cache, other):
                 assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("kv4", [False, True])
+def test_decode_lse_has_the_accuracy_of_32_bits(kv4, D, dtype):
+    """Over sequences of one key the LSE is the score itself.  4 bits: partial sums
+    are some three times the score (codes about 7.5, taken off again by the
+    zeros); with a dozen roundings of 2^-24 at most each, the root mean square
+    of the error is 3 * sqrt(12 / 3) * 2^-24 = 3.6e-7 of the score's, below 2^-21."""
+    B, H, Hkv, ps = 300, 16, 4, 16
+    q, cache, table, lens = make_decode(kv4, [1] * B, H, Hkv, 1, D, ps, dtype, 70, q_std=3.0)
+    scale = 0.125
+    _, lse = run_decode(kv4, q, cache, table, lens, scale=scale)
+    ok()
+    if kv4:
+        rows = [t[table[:, 0].long(), :, 0].cpu() for t in cache]
+        k = R.held(rows[0], rows[1], "k")                    # [B, Hkv, D]
+    else:
+        k = cache[0][table[:, 0].long(), :, 0].cpu().double()
+    want = (q.cpu().double()[:, :, 0] * k.repeat_interleave(H // Hkv, 1)).sum(-1) * scale
+    err = lse.cpu().double()[..., 0] - want
+    assert err.pow(2).mean().sqrt() <= 2.0 ** -21 * want.pow(2).mean().sqrt()

@@ -433,6 +433,13 @@ struct Warp {
             // times that), which the tensor cores multiply exactly, the scales
             // in fp32, and the zeros as one more product, (zero, zero) with
             // (high, low) part of the sum of q, group t in lane t.
+            // The sum of products keeps a fixed number of bits below the largest
+            // exponent, and a subnormal's is taken as 2^-14 whatever its leading
+            // zeros.  With the 11 bits of an fp16 q that cost scores 1e-6 of
+            // their size (bf16's 8 bits: 1e-7, fp32's own), so there the codes
+            // sit two bits higher, for one more shift a word.
+            constexpr int kUp = BF16 ? 0 : 2;
+            constexpr uint32_t kLoCode = 0x000f000fu << kUp, kHiCode = 0x00f000f0u << kUp;
             const int g = lane / 4, t = lane % 4;
             uint32_t w[2][D / 32], meta[2][D / 32];
             uint32_t z[4] = {0u, 0u, 0u, 0u};
@@ -455,11 +462,11 @@ struct Warp {
                 uint32_t a0[4], a1[4];
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const uint32_t hi = w[u][i] >> 8;
-                    a0[u] = w[u][i] & 0x000f000fu;
-                    a0[u + 2] = w[u][i] & 0x00f000f0u;
-                    a1[u] = hi & 0x000f000fu;
-                    a1[u + 2] = hi & 0x00f000f0u;
+                    const uint32_t lo = w[u][i] << kUp, hi = w[u][i] >> (8 - kUp);
+                    a0[u] = lo & kLoCode;
+                    a0[u + 2] = lo & kHiCode;
+                    a1[u] = hi & kLoCode;
+                    a1[u + 2] = hi & kHiCode;
                 }
                 const float sc0 = __low2float(as_half2(meta[0][i])), sc1 = __low2float(as_half2(meta[1][i]));
 #pragma unroll
@@ -476,7 +483,7 @@ struct Warp {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int x = 0; x < 4; ++x) s[n][x] = fmaf(s[n][x], 16777216.f, zs[n][x]);
+                for (int x = 0; x < 4; ++x) s[n][x] = fmaf(s[n][x], 16777216.f / (1 << kUp), zs[n][x]);
         }
     }
 
