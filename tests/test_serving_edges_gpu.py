@@ -409,3 +409,31 @@ def test_decode_lse_has_the_accuracy_of_32_bits(kv4, D, dtype):
     want = (q.cpu().double()[:, :, 0] * k.repeat_interleave(H // Hkv, 1)).sum(-1) * scale
     err = lse.cpu().double()[..., 0] - want
     assert err.pow(2).mean().sqrt() <= 2.0 ** -21 * want.pow(2).mean().sqrt()
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("kv4", [False, True])
+def test_decode_small_weights_keep_their_bits(kv4, dtype):
+    """One key in sixteen outweighs the others 2^17 times, but has the value 0: what
+    is left is the others' weights, each rounded to a 16-bit type once."""
+    n, H, Hkv, D, ps = 600, 4, 2, 64, 16
+    dt = DT[dtype]
+    q, cache, table, lens = make_decode(kv4, [n], H, Hkv, 1, D, ps, dtype, 80)
+    q.zero_()
+    q[..., 0] = 1.0
+    # the score below the large one's, as a number of the type, whose weight lies worst between the multiples of 2^-24
+    xs = torch.arange(11.0, 13.0, 1.0 / 128).to(torch.bfloat16 if dtype == "bf16" else torch.float16).double()
+    w = torch.exp(-xs) * 2.0 ** 24
+    x = xs[((w - w.floor() - 0.5).abs() + (w > 160) + (w < 60)).argmin()].item()
+    for j in range(n):
+        large, at = j % 16 == 5, (table[0, j // ps], slice(None), j % ps)
+        if kv4:
+            cache[1][at] = cache[3][at] = 0.0
+            cache[1][at][..., 1] = 0.0 if large else -x
+            cache[3][at][..., 1] = 0.0 if large else 1.0
+        else:
+            cache[0][at] = 0.0 if large else -x
+            cache[1][at] = 0.0 if large else 1.0
+    o, lse = run_decode(kv4, q, cache, table, lens, scale=1.0)
+    ok()
+    check_decode(kv4, q, cache, table, lens, 1.0, o, lse)

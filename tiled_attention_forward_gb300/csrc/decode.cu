@@ -59,6 +59,11 @@ constexpr int kAloneUnits = 2;            // longest target that one warp takes 
 constexpr int kMaxParts = 64;             // CTAs a sequence is cut between: one CTA joins the parts
 constexpr float kLow = -3.0e38f;          // the running max of a row that has seen no key
 constexpr float kRescaleThreshold = 8.0f; // log2 units: P <= 2^8 while the max is stale
+// Weights that enter the products as fp16 numbers are taken 2^kUp times: up to
+// 2^15 while the max is stale, and with all their bits down to 2^-21 of the
+// largest, not 2^-14: the small weights of a long sequence add up.
+template <bool BF16, bool KV4>
+constexpr float kUp = BF16 && !KV4 ? 0.f : 7.f;
 
 // ---- instructions ----------------------------------------------------------
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
@@ -245,7 +250,8 @@ __device__ __forceinline__ void store_out(const DecodeArgs& a, int b, int kvh, i
     *reinterpret_cast<uint2*>(o) =
         none ? make_uint2(0u, 0u) : make_uint2(pack(acc[0] * inv, acc[1] * inv), pack(acc[2] * inv, acc[3] * inv));
     if (d == 0 && a.lse != nullptr)
-        a.lse[(static_cast<int64_t>(b) * a.H + h) * a.Nq + i] = none ? -INFINITY : (mx + log2f(sum)) * kLn2;
+        a.lse[(static_cast<int64_t>(b) * a.H + h) * a.Nq + i] =
+            none ? -INFINITY : (mx + kUp<BF16, KV4> + log2f(sum * exp2f(-kUp<BF16, KV4>))) * kLn2;
 }
 
 // ---- one warp's keys ----------------------------------------------------------
@@ -256,7 +262,7 @@ struct Warp {
     uint32_t q[NT][kQ][2];              // B fragments of Q^T
     uint32_t qsum[NT];                  // 4 bits: (high, low) part of the sum of q over group t
     float f[NT][2];                     // log2-score of one unit of S, rows 2t and 2t+1 (> 0)
-    float m[NT][2], l[NT][2];
+    float m[NT][2], l[NT][2];           // the max (less kUp) that a row's weights are relative to; their sum
     float o[NT][kQ][4];
 
     // Query rows of K/V head kvh, row block rb.  Lane (g, t) = (lane/4, lane%4).
@@ -438,8 +444,8 @@ struct Warp {
             // zeros.  With the 11 bits of an fp16 q that cost scores 1e-6 of
             // their size (bf16's 8 bits: 1e-7, fp32's own), so there the codes
             // sit two bits higher, for one more shift a word.
-            constexpr int kUp = BF16 ? 0 : 2;
-            constexpr uint32_t kLoCode = 0x000f000fu << kUp, kHiCode = 0x00f000f0u << kUp;
+            constexpr int kShift = BF16 ? 0 : 2;
+            constexpr uint32_t kLoCode = 0x000f000fu << kShift, kHiCode = 0x00f000f0u << kShift;
             const int g = lane / 4, t = lane % 4;
             uint32_t w[2][D / 32], meta[2][D / 32];
             uint32_t z[4] = {0u, 0u, 0u, 0u};
@@ -462,7 +468,7 @@ struct Warp {
                 uint32_t a0[4], a1[4];
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const uint32_t lo = w[u][i] << kUp, hi = w[u][i] >> (8 - kUp);
+                    const uint32_t lo = w[u][i] << kShift, hi = w[u][i] >> (8 - kShift);
                     a0[u] = lo & kLoCode;
                     a0[u + 2] = lo & kHiCode;
                     a1[u] = hi & kLoCode;
@@ -483,7 +489,7 @@ struct Warp {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int x = 0; x < 4; ++x) s[n][x] = fmaf(s[n][x], 16777216.f / (1 << kUp), zs[n][x]);
+                for (int x = 0; x < 4; ++x) s[n][x] = fmaf(s[n][x], 16777216.f / (1 << kShift), zs[n][x]);
         }
     }
 
@@ -607,7 +613,7 @@ struct Warp {
 #pragma unroll
                 for (int u = 1; u < P; ++u) mx[n][x] = fmaxf(mx[n][x], fmaxf(s[u][n][x], s[u][n][x + 2]));
                 mx[n][x] *= f[n][x];
-                grow |= mx[n][x] > m[n][x] + kRescaleThreshold;
+                grow |= mx[n][x] > m[n][x] + (kRescaleThreshold + kUp<BF16, KV4>);
             }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -617,7 +623,7 @@ struct Warp {
                     float top = mx[n][x];
 #pragma unroll
                     for (int d = 4; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                    const float mn = fmaxf(m[n][x], top);
+                    const float mn = fmaxf(m[n][x], top - kUp<BF16, KV4>);
                     const float alpha = ex2(m[n][x] - mn);
                     m[n][x] = mn;
                     l[n][x] *= alpha;
