@@ -307,8 +307,9 @@ FATTN_API int fattn_fwd_unfused_static(const void* q, const void* k, const void*
  * every row starts on a 16-byte boundary.  Tables in device memory
  * (cu_seqlens, slots, pos, block_table, seq_lens) are read by the kernels, so
  * an entry out of range cannot be refused before the launch: the kernels skip
- * what it names, touch no memory outside the buffers, and
- * fattn_get_device_status then returns FATTN_ERR_INVALID_ARG.
+ * what it names (a sequence length outside its table is cut to 0 or to the
+ * table), touch no memory outside the buffers, and fattn_get_device_status then
+ * returns FATTN_ERR_INVALID_ARG.
  * A kernel of these calls may be set up while the one before it on the stream
  * still runs; it waits for that to complete before it touches memory.
  *
@@ -343,7 +344,7 @@ FATTN_API int64_t fattn_packed_workspace_bytes(int64_t B, int64_t T);
  *   q, k, v, o : `strides` is a host array of 8: token and head stride of q, k,
  *                v, o.  A stride of a dimension of more than one is positive.
  *                o overlaps nothing else.
- *   lse        : fp32 [H, T], or NULL.
+ *   lse        : fp32 [H, T], or NULL.  (No backward of packed sequences takes it.)
  *   cu_seqlens : device int32 [B + 1], not decreasing, 0 <= cu_seqlens[0],
  *                cu_seqlens[B] <= T; sequences may be empty.  Rows that belong
  *                to no sequence are left as they were, and what q, k and v hold
@@ -450,7 +451,8 @@ FATTN_API int64_t fattn_decode_workspace_bytes(int64_t B, int64_t H, int64_t Hkv
  *   lse         : fp32 [B, H, Nq] contiguous, or NULL.
  *   block_table : device int32 [B][table_width].
  *   seq_lens    : device int32 [B], 0 <= seq_lens[b] <= table_width*page_size
- *                 (and table_width*page_size < 2^31 - 65536).
+ *                 (and table_width*page_size < 2^31 - 65536).  One outside that
+ *                 is cut to its nearer end, computed, and reported.
  *   workspace   : caller-owned, fattn_decode_workspace_bytes, 16-byte aligned;
  *                 contents ignored on entry.  Calls that run at the same time
  *                 (two streams, two graphs) need workspaces of their own.

@@ -25,11 +25,13 @@
 // instructions (4-bit prompt 104 -> 91 us).
 //
 // Measured (GB300): 8191 tokens of 16 + 2 * 2 heads, D = 64, 16 bits (45 MB)
-// 10.6 us, of which about 2.5 are the launch; 16000 tokens of 32 + 2 * 8 heads, D
-// = 128, 74 us in 16 bits (5.8 TB/s) and 86 us into 4 bits (422 MB with the
-// values held, 4.9 TB/s), bound by issue slots (about 300 instructions for 16
-// bytes of a key or value row) and latency.  64 tokens take 2.6 us, into 4 bits
-// 3.3.  Two rows ahead and five blocks an SM: four blocks took 89 us, six 91.
+// 10.9 us, of which about 2.5 are the launch; 16000 tokens of 32 + 2 * 8 heads, D
+// = 128, 74 us in 16 bits (5.8 TB/s) and 87 us into 4 bits (422 MB with the
+// values held, 4.9 TB/s), bound by the latency of its loads and by issue slots
+// (63 % busy, about 300 instructions for 16 bytes of a key or value row).  64
+// tokens of 32 + 2 * 8 heads, D = 128, take 2.5 us; 17 of 16 + 2 * 16 heads, D =
+// 64, into 4 bits 3.3.  (16000 tokens into 4 bits:) two rows ahead and five
+// blocks an SM: four blocks took 89 us, six 91.
 // Up to 16 rows a thread: 8 took 4 us more (blocks' starts), 32 three.
 #include <algorithm>
 #include <cuda_bf16.h>
@@ -223,7 +225,7 @@ __device__ __forceinline__ bool quantise(const float (&x)[8], bool rotated, int 
 // (from `base` on) hold, and their partners' that lanes `from` hold, with whether
 // and by which angles they turn.  The whole warp calls it and takes one element a lane:
 // with 8 a lane it was four times as many instructions, which a call for few
-// tokens waits for (64 tokens 5.3 -> 3.3 us, 16000 91 -> 87), and whole warps
+// tokens waits for (64 tokens 4.1 -> 3.3 us, 16000 91 -> 87), and whole warps
 // never run this as often as to hide it.
 struct Two {
     float h, l;

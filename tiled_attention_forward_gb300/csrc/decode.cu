@@ -35,10 +35,12 @@
 // that costs one instruction otherwise.  Sums stay in the lanes until the end.
 //
 // Measured (GB300, D = 128, the 64 sequences above, 1.11 GB of 16-bit rows):
-// 165 us, 6.7 TB/s, the rate of a plain copy.  In 4 bits the same call (347 MB)
-// takes 85 us, 4.1 TB/s, and 3 sequences of 120001 keys (461 MB) 95 us, 4.9
-// TB/s: there the integer pipe (57 % busy at two cycles an operation) and the
-// issue slots (63 %) bound it, with 23 warp instructions a key.
+// 165 to 168 us, 6.7 TB/s, the rate of a plain copy.  In 4 bits the same call
+// (347 MB) takes 86 us, 4.0 TB/s, and 3 sequences of 120001 keys (461 MB) 96 us,
+// 4.8 TB/s.  No unit is full there (integer pipe 58 %, issue slots 63 %): four
+// warps a scheduler, each one chain of dependent steps of 23 warp instructions a
+// key, wait for fixed latencies and for the math pipe; and the ragged batch
+// pays for 512 targets' starts and joins, with no copy in flight meanwhile.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -1091,8 +1093,8 @@ cudaError_t launch_one(const DecodeArgs& a, int sms, cudaStream_t s) {
 int row_tiles(int64_t rows) { return rows <= 8 ? 1 : (rows <= 16 ? 2 : 4); }
 
 // Whether short targets may be taken by one warp each: only where a CTA's share
-// holds two targets or more on average.  (200 sequences of up to 300 tokens, 8
-// K/V heads: 42.6 -> 33.6 us.  The kernel that can loses 2 % on long sequences
+// holds two targets or more on average.  (200 sequences of up to 300 tokens, 32
+// heads on 8, D = 128, 4 bits: 42.6 -> 33.6 us.  The kernel that can loses 2 % on long sequences
 // and 4 to 10 % on the smallest calls to the registers that this takes, and
 // with 32 query rows 6 to 10 % everywhere, so that form does not exist.)
 template <int D, bool BF16, bool KV4, int NT>

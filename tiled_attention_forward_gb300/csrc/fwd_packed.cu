@@ -11,13 +11,14 @@
 // atomics, which moves tasks in time and changes no result (a task's rows are
 // written by one CTA, from its own inputs).
 //
-// Measured (GB300, bf16, 32 heads on 8, D = 128, causal): a prompt of 16000
-// tokens beside three short ones 1.28 ms = 1630 TFLOP/s, the dense forward's
-// rate (0.84 of the measured peak); 16 prompts of 1 to 4096 tokens 281 us = 1267
-// TFLOP/s.  The forward's own chain bounds both (fwd_tc_kernel.cuh); the mix
+// Measured (GB300, bf16, 32 heads on 8, D = 128, causal, in a stream of calls on
+// changing inputs): a prompt of 16000 tokens beside three short ones 1.30 to 1.32
+// ms = 1590 to 1610 TFLOP/s, the dense forward's rate (0.83 of the measured peak);
+// 16 prompts of 1 to 4096 tokens 298 us = 1195 TFLOP/s (replayed from a graph 281).
+// The forward's own chain bounds both (fwd_tc_kernel.cuh); the mix
 // pays about 2.8 us at each of the 15 task changes of a CTA, and 8 % more scores
 // than the mask leaves (whole 128 x 128 tiles).  Five prompts of up to 128
-// tokens take 8.7 us, of which the list is about 1.
+// tokens take 9.2 us (graph 8.5), of which the list is about 1.
 #include "fwd_tc_kernel.cuh"
 
 namespace fattn {
