@@ -480,6 +480,151 @@ FATTN_API int fattn_decode_kv4(const void* q, void* o, float* lse, const int64_t
                      int64_t Nq, int64_t D, float scale, int dtype, fattn_stream_t stream);
 
 /*
+ * fattn_decode_shared -- fattn_decode of B sequences that share a long prefix
+ * (16 bits): row i of sequence b sees all keys of the prefix and its own keys 0 ..
+ * seq_lens[b] - Nq + i.  The prefix's K and V are read once for the whole batch
+ * and not once a sequence.
+ *
+ *   prefix_table : device int32 [prefix_width], the pages of the prefix, in order,
+ *                in the pool that also holds the sequences' own pages.
+ *   prefix_len   : device int32 [1], its tokens, 0 <= *prefix_len <= prefix_width *
+ *                page_size (< 2^31 - 65536); one outside that is cut to its nearer
+ *                end, computed, and reported.  A page out of range is reported, and
+ *                its keys and values are taken as zeros.
+ *   block_table, seq_lens : the sequences' own tokens, behind the prefix (the Nq
+ *                newest among them).  A row that sees no own key attends to the
+ *                prefix alone.
+ *   workspace    : caller-owned, fattn_decode_shared_workspace_bytes, 16-byte
+ *                aligned; contents ignored on entry.  Calls that run at the same
+ *                time need workspaces of their own.
+ * The stride of a dimension of q of more than one is positive.  With prefix_width
+ * = 0 this is fattn_decode.  Everything else as fattn_decode.  Two launches (the
+ * prefix, the sequences' own keys and the join).  (B = 1 with many rows serves a
+ * chunk of new tokens over a long cached prefix.)
+ */
+FATTN_API int64_t fattn_decode_shared_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t D);
+FATTN_API int fattn_decode_shared(const void* q, void* o, float* lse, const int64_t* strides,
+                        const void* k_pages, const void* v_pages, int64_t page_stride, int64_t num_pages,
+                        int64_t page_size, const int32_t* prefix_table, int64_t prefix_width,
+                        const int32_t* prefix_len, const int32_t* block_table, int64_t table_width,
+                        const int32_t* seq_lens, void* workspace, int64_t workspace_bytes, int64_t B,
+                        int64_t H, int64_t Hkv, int64_t Nq, int64_t D, float scale, int dtype,
+                        fattn_stream_t stream);
+
+/*
+ * ---- Positions with several axes -------------------------------------------
+ *
+ * Image and video tokens have a position on each of several axes (time, height,
+ * width).  Pair i of a row's rot/2 pairs turns by angle i of the position on the
+ * axis axis_of_pair[i]: `pos` is device int32 [axes][tokens], axis_of_pair a host
+ * array of rot/2 bytes, each below `axes` (1 to 8), and read during the call only.
+ * Which pairs belong to which axis (in sections, in turn) and which angles the
+ * tables hold is the caller's choice.
+ */
+
+/*
+ * fattn_cache_append_axes, fattn_cache_append_kv4_axes -- fattn_cache_append and
+ * fattn_cache_append_kv4 with such positions; a token one of whose positions is
+ * out of range is skipped and reported.  Everything else as there.
+ */
+FATTN_API int fattn_cache_append_axes(const void* q, const void* k, const void* v, void* q_out, void* k_out,
+                            const int64_t* strides, void* k_pages, void* v_pages, int64_t page_stride,
+                            int64_t num_pages, int64_t page_size, const int64_t* slots, const int32_t* pos,
+                            const uint8_t* axis_of_pair, int64_t axes, const float* cos, const float* sin,
+                            int64_t max_pos, int64_t rot, int interleaved, int64_t T, int64_t H, int64_t Hkv,
+                            int64_t D, int dtype, fattn_stream_t stream);
+FATTN_API int fattn_cache_append_kv4_axes(const void* q, const void* k, const void* v, void* q_out, void* k_out,
+                                void* v_out, const int64_t* strides, void* k_codes, void* k_scales,
+                                void* v_codes, void* v_scales, int64_t num_pages, int64_t page_size,
+                                const int64_t* slots, const int32_t* pos, const uint8_t* axis_of_pair,
+                                int64_t axes, const float* cos, const float* sin, int64_t max_pos, int64_t rot,
+                                int interleaved, int held, int64_t T, int64_t H, int64_t Hkv, int64_t D,
+                                int dtype, fattn_stream_t stream);
+
+/*
+ * fattn_rotate -- the same rotation of q and k for calls that keep no cache
+ * (training, fattn_fwd, fattn_fwd_cross), and its gradient.
+ *
+ *   q, q_out : [B, H, N, D]; k, k_out: [B, Hkv, N, D], or both NULL (Hkv is then
+ *              ignored).  `strides` is a host array of 12: batch, head and token
+ *              stride of q, k, q_out, k_out (those of NULL tensors are ignored), so
+ *              that inputs can be slices of a projection [B, N, heads, D] and
+ *              outputs the dense tensors that fattn_fwd takes, or the other way
+ *              round.  An output may be its own input (same pointer and strides);
+ *              it overlaps nothing else, and its rows lie apart.
+ *   pos      : device int32 [axes][B][N], 0 <= pos < max_pos; rows of a token one
+ *              of whose positions is out of range are left as they were, and
+ *              reported.
+ *   inverse  : 0 = (a, b) -> (a cos - b sin, b cos + a sin); otherwise by the
+ *              opposite angles, which is the gradient: with dq, dk in place of q, k
+ *              it gives the gradients of the rows before they turned.
+ *   cos, sin, max_pos, rot, interleaved : as fattn_cache_append; rows' elements
+ *              past rot are copied.  One launch; fp32 products, one rounding.
+ */
+FATTN_API int fattn_rotate(const void* q, const void* k, void* q_out, void* k_out, const int64_t* strides,
+                 const int32_t* pos, const uint8_t* axis_of_pair, int64_t axes, const float* cos,
+                 const float* sin, int64_t max_pos, int64_t rot, int interleaved, int inverse, int64_t B,
+                 int64_t H, int64_t Hkv, int64_t N, int64_t D, int dtype, fattn_stream_t stream);
+
+/*
+ * ---- Cross attention ---------------------------------------------------------
+ *
+ * Queries of one length over keys of another, such as an encoder's states: rows of
+ * 16-bit elements (FATTN_F32 -> FATTN_ERR_UNSUPPORTED) by strides as in the serving
+ * calls; the stride of a dimension of more than one is positive (and below 2^39).
+ */
+
+/*
+ * fattn_fwd_cross -- O and LSE of q, o [B, H, Nq, D] over k, v [B, Hkv, Nk, D], H a
+ * multiple of Hkv:
+ *
+ *     O[b,h,i] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q[b,h,i] . k_j),
+ *     j = 0 .. kv_lens[b] - 1,   LSE = ln sum_j p_j
+ *
+ *   strides   : host array of 12: batch, head and token stride of q, k, v, o.
+ *   lse       : fp32 [B, H, Nq] contiguous, or NULL.
+ *   kv_lens   : device int32 [B], 0 <= kv_lens[b] <= Nk, or NULL (Nk each).  One
+ *               outside that is cut to its nearer end, computed, and reported.
+ *               What k and v hold behind it never reaches a result.  A row without
+ *               keys (kv_lens[b] = 0, Nk = 0) gets O = 0 and LSE = -inf.
+ *   workspace : caller-owned, fattn_cross_workspace_bytes, 16-byte aligned;
+ *               contents ignored on entry.  Calls that run at the same time need
+ *               workspaces of their own.
+ * o overlaps nothing else (it may be another slice of the tensor that q is a slice
+ * of).  Up to 32 rows (H/Hkv * Nq) per K/V head, such as a decoder's single tokens,
+ * take the kernel of fattn_decode, more the tensor-core forward, whose keys are
+ * cut into parts where there are few rows.  One launch, or two (the join).  The
+ * result is the same for every run of the same call.
+ */
+FATTN_API int64_t fattn_cross_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t Nk, int64_t D);
+FATTN_API int fattn_fwd_cross(const void* q, const void* k, const void* v, void* o, float* lse,
+                    const int64_t* strides, const int32_t* kv_lens, void* workspace,
+                    int64_t workspace_bytes, int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t Nk,
+                    int64_t D, float scale, int dtype, fattn_stream_t stream);
+
+/*
+ * fattn_bwd_cross -- its gradients: dq [B, H, Nq, D] and dk, dv [B, Hkv, Nk, D] of
+ * L = sum(dout * O), from the forward's o and lse, by the formulas of
+ * fattn_bwd_gqa.  dk and dv are sums over the query heads that share a K/V head;
+ * rows of keys behind kv_lens[b] are zeros, and so is dq where there are no keys.
+ *
+ *   strides   : host array of 24: batch, head and token stride of q, k, v, o,
+ *               dout, dq, dk, dv.
+ *   lse       : fp32 [B, H, Nq] contiguous.
+ *   workspace : caller-owned, fattn_bwd_cross_workspace_bytes, 16-byte aligned;
+ *               contents ignored on entry.
+ * dq, dk and dv overlap nothing else (each may be another slice of a tensor that
+ * others are slices of).  No atomics: the result is the same for every run.
+ */
+FATTN_API int64_t fattn_bwd_cross_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t Nk,
+                                        int64_t D);
+FATTN_API int fattn_bwd_cross(const void* q, const void* k, const void* v, const void* o, const void* dout,
+                    const float* lse, void* dq, void* dk, void* dv, const int64_t* strides,
+                    const int32_t* kv_lens, void* workspace, int64_t workspace_bytes, int64_t B, int64_t H,
+                    int64_t Hkv, int64_t Nq, int64_t Nk, int64_t D, float scale, int dtype,
+                    fattn_stream_t stream);
+
+/*
  * fattn_plan -- host-only description of the launch fattn_fwd would make for
  * these arguments (no CUDA call when num_sms > 0).  Fills `out` with:
  *   out[0] path       : 0 = none (empty problem), 1 = FFMA fp32, 2 = tcgen05 bf16/fp16

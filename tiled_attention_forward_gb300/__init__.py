@@ -23,7 +23,9 @@ __all__ = ["fwd", "fwd_host", "bwd", "bwd_host", "bwd_workspace_bytes", "fwd_unf
            "UNFUSED_STATIC_BYTES", "plan", "get_device_status", "selftest_wait_timeout",
            "status_string", "library_path", "load", "FattnError", "FattnLibraryMissing",
            "DTYPE_CODES", "STATUS", "cache_append", "cache_append_kv4", "decode", "decode_kv4",
-           "decode_workspace_bytes", "KV4_GROUP", "fwd_packed", "packed_workspace_bytes"]
+           "decode_workspace_bytes", "KV4_GROUP", "fwd_packed", "packed_workspace_bytes", "decode_shared",
+           "decode_shared_workspace_bytes", "rotate", "rotary_axes", "fwd_cross", "cross_workspace_bytes", "bwd_cross",
+           "bwd_cross_workspace_bytes"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libfattn.so")
@@ -95,6 +97,17 @@ def load():
     lib.fattn_decode_workspace_bytes.restype = i64
     lib.fattn_decode.argtypes = ([vp] * 6 + [i64] * 3 + [vp, i64, vp, vp] + [i64] * 6 + [f32, ci, vp])
     lib.fattn_decode_kv4.argtypes = ([vp] * 8 + [i64] * 2 + [vp, i64, vp, vp] + [i64] * 6 + [f32, ci, vp])
+    lib.fattn_decode_shared.argtypes = ([vp] * 6 + [i64] * 3 + [vp, i64, vp, vp, i64, vp, vp] + [i64] * 6 + [f32, ci, vp])
+    lib.fattn_cache_append_axes.argtypes = ([vp] * 8 + [i64] * 3 + [vp] * 3 + [i64] + [vp] * 2 + [i64] * 2 + [ci] +
+                                            [i64] * 4 + [ci, vp])
+    lib.fattn_cache_append_kv4_axes.argtypes = ([vp] * 11 + [i64] * 2 + [vp] * 3 + [i64] + [vp] * 2 + [i64] * 2 +
+                                                [ci] * 2 + [i64] * 4 + [ci, vp])
+    lib.fattn_rotate.argtypes = [vp] * 7 + [i64] + [vp] * 2 + [i64] * 2 + [ci] * 2 + [i64] * 5 + [ci, vp]
+    lib.fattn_fwd_cross.argtypes = [vp] * 8 + [i64] * 7 + [f32, ci, vp]
+    lib.fattn_bwd_cross.argtypes = [vp] * 12 + [i64] * 7 + [f32, ci, vp]
+    for f, n in (("decode_shared", 5), ("cross", 6), ("bwd_cross", 6)):
+        getattr(lib, "fattn_%s_workspace_bytes" % f).argtypes = [i64] * n
+        getattr(lib, "fattn_%s_workspace_bytes" % f).restype = i64
     lib.fattn_get_device_status.argtypes = [vp]
     lib.fattn_selftest_wait_timeout.argtypes = [ctypes.c_uint64, vp]
     lib.fattn_status_string.argtypes = [ci]
@@ -103,6 +116,8 @@ def load():
     for f in ("fattn_fwd", "fattn_fwd_gqa", "fattn_fwd_host", "fattn_fwd_unfused", "fattn_bwd", "fattn_bwd_gqa", "fattn_bwd_host",
               "fattn_fwd_unfused_static", "fattn_plan", "fattn_plan_head_group",
               "fattn_fwd_packed", "fattn_cache_append", "fattn_cache_append_kv4", "fattn_decode", "fattn_decode_kv4",
+              "fattn_decode_shared", "fattn_cache_append_axes", "fattn_cache_append_kv4_axes", "fattn_rotate",
+              "fattn_fwd_cross", "fattn_bwd_cross",
               "fattn_get_device_status",
               "fattn_selftest_wait_timeout", "fattn_version"):
         getattr(lib, f).restype = ci
@@ -453,8 +468,20 @@ def fwd_packed(q, k, v, cu_seqlens, causal=True, scale=None, out=None, lse=None,
     return out, lse
 
 
+def rotary_axes(sections):
+    """Which axis each pair of a row turns by, for ``axes``: sections[a]
+    consecutive pairs by axis a (``rotary_axes((16, 24, 24))``: 16 pairs by the
+    first of three axes, 24 by each of the others).  Other orders are written
+    out, one axis a pair: ``bytes(i % 3 for i in range(64))``."""
+    return b"".join(bytes([a]) * n for a, n in enumerate(sections))
+
+
+def _axes(axes):
+    return axes if axes is None or isinstance(axes, bytes) else bytes(axes)
+
+
 def cache_append(k, v, k_pages, v_pages, slots, pos=None, cos=None, sin=None, interleaved=False, q=None,
-                 q_out=None, k_out=None, stream=None):
+                 q_out=None, k_out=None, stream=None, axes=None):
     """Appends T new tokens to a 16-bit paged cache, rotating k and q by position.
 
     k, v: [T, Hkv, D] CUDA tensors (float16 or bfloat16, D in {64, 128}), q
@@ -465,13 +492,16 @@ def cache_append(k, v, k_pages, v_pages, slots, pos=None, cos=None, sin=None, in
     slot skips its token.  pos: int32 [T], rows of cos and sin, float32
     [max_pos, rot/2] (rot a multiple of 16, the first rot elements of a row
     turn: element i with i + rot/2, or 2i with 2i+1 when ``interleaved``);
-    without cos and sin nothing turns.  Returns (q_out, k_out): q rotated (None
+    without cos and sin nothing turns.  ``axes`` (positions with several axes,
+    as image and video tokens have them): the axis of each of the rot/2 pairs,
+    as ``rotary_axes`` gives them; pos is then int32 [axes, T], and pair i turns
+    by the position on its own axis.  Returns (q_out, k_out): q rotated (None
     without q; allocated here when None) and, where ``k_out`` is given, k as
     the cache holds it.  ``q_out`` may be q itself.  An index out of range is
     skipped and reported by ``get_device_status``."""
     if q is not None and q_out is None:
         q_out = _new(q.shape, q.dtype, q, stream)
-    rc = _binding().cache_append(k, v, k_pages, v_pages, slots, pos, cos, sin, 1 if interleaved else 0, q, q_out, k_out,
+    rc = _binding().cache_append(k, v, k_pages, v_pages, slots, pos, _axes(axes), cos, sin, 1 if interleaved else 0, q, q_out, k_out,
                                  _handle(stream, k))
     if rc != 0:
         raise FattnError(rc, "fattn_cache_append")
@@ -479,7 +509,8 @@ def cache_append(k, v, k_pages, v_pages, slots, pos=None, cos=None, sin=None, in
 
 
 def cache_append_kv4(k, v, k_codes, k_scales, v_codes, v_scales, slots, pos=None, cos=None, sin=None,
-                     interleaved=False, q=None, q_out=None, k_out=None, v_out=None, held=False, stream=None):
+                     interleaved=False, q=None, q_out=None, k_out=None, v_out=None, held=False, stream=None,
+                     axes=None):
     """``cache_append`` into a 4-bit cache: k_codes, v_codes uint8 [pages, Hkv,
     page_size, D/2]; k_scales, v_scales float16 [pages, Hkv, page_size, D/32,
     2] = (scale, zero) of each group of 32 elements (the nibble order is in
@@ -488,7 +519,7 @@ def cache_append_kv4(k, v, k_codes, k_scales, v_codes, v_scales, slots, pos=None
     cache now stands for."""
     if q is not None and q_out is None:
         q_out = _new(q.shape, q.dtype, q, stream)
-    rc = _binding().cache_append_kv4(k, v, k_codes, k_scales, v_codes, v_scales, slots, pos, cos, sin,
+    rc = _binding().cache_append_kv4(k, v, k_codes, k_scales, v_codes, v_scales, slots, pos, _axes(axes), cos, sin,
                                      1 if interleaved else 0, q, q_out, k_out, v_out, 1 if held else 0,
                                      _handle(stream, k))
     if rc != 0:
@@ -553,6 +584,126 @@ def decode_kv4(q, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens, s
     if rc != 0:
         raise FattnError(rc, "fattn_decode_kv4")
     return out, lse
+
+
+def decode_shared_workspace_bytes(B, H, Nq, D, Hkv):
+    """Bytes of workspace ``decode_shared`` needs (whatever the lengths)."""
+    return int(load().fattn_decode_shared_workspace_bytes(int(B), int(H), int(Hkv), int(Nq), int(D)))
+
+
+def decode_shared(q, k_pages, v_pages, prefix_table, prefix_len, block_table, seq_lens, scale=None, out=None, lse=None,
+                  workspace=None, return_lse=True, stream=None):
+    """``decode`` of sequences that share a long prefix, whose keys and values are
+    read once for the whole batch.
+
+    prefix_table: int32 [pages], the pages of the prefix in the same pool;
+    prefix_len: int32 [1] on the GPU, its tokens.  block_table and seq_lens are
+    those of each sequence's own tokens behind it.  Token i of the Nq sees the
+    whole prefix and own keys 0 .. seq_lens[b] - Nq + i.  ``workspace``: at least
+    ``decode_shared_workspace_bytes`` bytes.  Everything else as ``decode``."""
+    if scale is None or out is None or workspace is None or (return_lse and lse is None):
+        B, H, Nq, D = _dims("q", q, 4)
+        if workspace is None:
+            need = decode_shared_workspace_bytes(B, H, Nq, D, _dims("k_pages", k_pages, 4)[1])
+            workspace = _new(max(need, 16), torch.uint8, q, stream)
+        scale, out, lse, workspace = _decode_defaults(q, 1, scale, out, lse, workspace, return_lse, stream)
+    if not return_lse:
+        lse = None
+    rc = _binding().decode_shared(q, k_pages, v_pages, prefix_table, prefix_len, block_table, seq_lens, scale, out, lse,
+                                  workspace, _handle(stream, q))
+    if rc != 0:
+        raise FattnError(rc, "fattn_decode_shared")
+    return out, lse
+
+
+# ---------------------------------------------------------------------------
+# Positions with several axes; cross attention
+# ---------------------------------------------------------------------------
+def rotate(q, pos, cos, sin, axes=None, interleaved=False, inverse=False, k=None, q_out=None, k_out=None, stream=None):
+    """Rotates queries and keys by their positions, for attention that keeps no
+    cache (``fwd``, ``fwd_cross``), and with ``inverse`` their gradients.
+
+    q: [B, H, N, D]; k (optional): [B, Hkv, N, D]; float16 or bfloat16 CUDA
+    tensors, D in {64, 128}, any batch, head and token strides (slices of a
+    projection [B, N, heads, D]), last dimension contiguous.  pos: int32 [B, N],
+    rows of cos and sin, float32 [max_pos, rot/2]; with ``axes`` (see
+    ``rotary_axes``) int32 [axes, B, N], pair i turning by the position on its own
+    axis.  (a, b) -> (a cos - b sin, b cos + a sin), ``inverse`` by the opposite
+    angles: the gradients of q and k are ``rotate(dq, ..., k=dk, inverse=True)``.
+    Returns (q_out, k_out), allocated here as the contiguous [B, H, N, D] that
+    ``fwd`` takes when None; they may have strides of their own, or be q and k.
+    Rows whose position is out of range are left as they were, and reported by
+    ``get_device_status``."""
+    if q_out is None:
+        q_out = _new(q.shape, q.dtype, q, stream)
+    if k is not None and k_out is None:
+        k_out = _new(k.shape, k.dtype, k, stream)
+    rc = _binding().rotate(q, k, q_out, k_out, pos, _axes(axes), cos, sin, 1 if interleaved else 0, 1 if inverse else 0,
+                           _handle(stream, q))
+    if rc != 0:
+        raise FattnError(rc, "fattn_rotate")
+    return q_out, k_out
+
+
+def cross_workspace_bytes(B, H, Nq, Nk, D, Hkv):
+    """Bytes of workspace ``fwd_cross`` needs."""
+    return int(load().fattn_cross_workspace_bytes(int(B), int(H), int(Hkv), int(Nq), int(Nk), int(D)))
+
+
+def fwd_cross(q, k, v, kv_lens=None, scale=None, out=None, lse=None, workspace=None, return_lse=True, stream=None):
+    """Cross attention: queries of one length over keys of another, such as an
+    encoder's states.
+
+    q: [B, H, Nq, D]; k, v: [B, Hkv, Nk, D] with H a multiple of Hkv; float16 or
+    bfloat16 CUDA tensors, D in {64, 128}, any batch, head and token strides
+    (slices of a projection [B, N, heads, D]), last dimension contiguous.
+    kv_lens (optional): int32 [B] on the GPU; entry b sees its first kv_lens[b]
+    keys, and what k and v hold behind them is not used.  Returns (o, lse) like
+    ``fwd``: o [B, H, Nq, D], lse float32 [B, H, Nq]; rows without keys give o =
+    0, lse = -inf.  ``workspace``: a CUDA uint8 tensor of at least
+    ``cross_workspace_bytes`` bytes (allocated here when None); calls running at
+    the same time need one each."""
+    if scale is None or out is None or workspace is None or (return_lse and lse is None):
+        B, H, Nq, D = _dims("q", q, 4)
+        scale = _default_scale(D) if scale is None else scale
+        if out is None:
+            out = _new((B, H, Nq, D), q.dtype, q, stream)
+        if return_lse and lse is None:
+            lse = _new((B, H, Nq), torch.float32, q, stream)
+        if workspace is None:
+            _, Hkv, Nk, _ = _dims("k", k, 4)
+            workspace = _new(max(cross_workspace_bytes(B, H, Nq, Nk, D, Hkv), 16), torch.uint8, q, stream)
+    if not return_lse:
+        lse = None
+    rc = _binding().fwd_cross(q, k, v, kv_lens, scale, out, lse, workspace, _handle(stream, q))
+    if rc != 0:
+        raise FattnError(rc, "fattn_fwd_cross")
+    return out, lse
+
+
+def bwd_cross_workspace_bytes(B, H, Nq, Nk, D, Hkv):
+    """Bytes of workspace ``bwd_cross`` needs."""
+    return int(load().fattn_bwd_cross_workspace_bytes(int(B), int(H), int(Hkv), int(Nq), int(Nk), int(D)))
+
+
+def bwd_cross(q, k, v, o, lse, dout, kv_lens=None, scale=None, dq=None, dk=None, dv=None, workspace=None, stream=None):
+    """Gradients of ``fwd_cross``: (dq, dk, dv) of sum(dout * O), where (o, lse) is
+    what ``fwd_cross`` returned for (q, k, v, kv_lens).  All tensors by strides as
+    there; dq, dk and dv are allocated here (contiguous) when None.  dk and dv
+    are summed over the query heads of a K/V head, and zero behind kv_lens[b]."""
+    if scale is None or workspace is None or dq is None or dk is None or dv is None:
+        B, H, Nq, D = _dims("q", q, 4)
+        _, Hkv, Nk, _ = _dims("k", k, 4)
+        scale = _default_scale(D) if scale is None else scale
+        dq = _new(q.shape, q.dtype, q, stream) if dq is None else dq
+        dk = _new(k.shape, k.dtype, k, stream) if dk is None else dk
+        dv = _new(v.shape, v.dtype, v, stream) if dv is None else dv
+        if workspace is None:
+            workspace = _new(max(bwd_cross_workspace_bytes(B, H, Nq, Nk, D, Hkv), 16), torch.uint8, q, stream)
+    rc = _binding().bwd_cross(q, k, v, o, dout, lse, kv_lens, scale, dq, dk, dv, workspace, _handle(stream, q))
+    if rc != 0:
+        raise FattnError(rc, "fattn_bwd_cross")
+    return dq, dk, dv
 
 
 def plan(B, H, N, D, causal=False, dtype=torch.bfloat16, num_sms=0):

@@ -1,6 +1,7 @@
-// binding.cpp -- argument marshalling of the serving calls for Python
-// (fwd_packed, cache_append, cache_append_kv4, decode, decode_kv4): torch
-// tensors in, the C ABI of include/fattn.h out, nothing else.
+// binding.cpp -- argument marshalling of the calls on rows by strides for Python
+// (fwd_packed, cache_append, cache_append_kv4, decode, decode_kv4, decode_shared,
+// rotate, fwd_cross, bwd_cross): torch tensors in, the C ABI of include/fattn.h
+// out, nothing else.
 //
 // A decode step's kernels take 3 to 9 us, and checking and converting a dozen
 // tensors in Python took 8 to 14 us of every call; here it takes under 1 us.
@@ -66,6 +67,21 @@ struct Args {
     }
     void done() const {
         if (left != 0) throw Refused("too many arguments");
+    }
+};
+
+// The axis of each pair: a bytes object of rot/2, or None.
+struct Axes {
+    const uint8_t* of_pair = nullptr;
+    int64_t n = 0;  // pairs
+    explicit Axes(PyObject* o) {
+        if (o == Py_None) return;
+        if (!PyBytes_Check(o)) throw Refused("axes must be bytes");
+        of_pair = reinterpret_cast<const uint8_t*>(PyBytes_AS_STRING(o));
+        n = PyBytes_GET_SIZE(o);
+    }
+    void check(int64_t rot) const {
+        if (n != rot / 2) throw Refused("axes must name one axis for each of the rot/2 = " + std::to_string(rot / 2) + " pairs");
     }
 };
 
@@ -225,9 +241,10 @@ PyObject* py_fwd_packed(PyObject*, PyObject* const* args, Py_ssize_t n) {
     });
 }
 
-// What both appends take after the cache: slots, pos, cos, sin, interleaved, q, q_out, k_out.
+// What both appends take after the cache: slots, pos, axes, cos, sin, interleaved, q, q_out, k_out.
 struct Append {
-    int64_t T, H = 0, Hkv, D, max_pos = 0, rot = 0;
+    int64_t T, H = 0, Hkv, D, max_pos = 0, rot = 0, axes = 0;
+    const uint8_t* axis_of_pair = nullptr;
     int interleaved;
     const int64_t* slots;
     const int32_t* pos = nullptr;
@@ -240,7 +257,9 @@ struct Append {
         Hkv = k.size(1);
         D = k.size(2);
         const at::Tensor& slots_t = a.tensor("slots");
-        const at::Tensor *pos_t = a.maybe("pos"), *cos_t = a.maybe("cos"), *sin_t = a.maybe("sin");
+        const at::Tensor* pos_t = a.maybe("pos");
+        const Axes which(a.next());
+        const at::Tensor *cos_t = a.maybe("cos"), *sin_t = a.maybe("sin");
         interleaved = static_cast<int>(a.integer());
         q = a.maybe("q");
         q_out = a.maybe("q_out");
@@ -253,7 +272,15 @@ struct Append {
                 throw Refused("a rotation needs pos, and cos and sin [max_pos, rot/2]");
             max_pos = cos_t->size(0);
             rot = 2 * cos_t->size(1);
-            pos = static_cast<int32_t*>(p.dense("pos", *pos_t, at::kInt, {T}));
+            if (which.of_pair) {
+                which.check(rot);
+                axes = pos_t->dim() == 2 ? pos_t->size(0) : 0;
+                axis_of_pair = which.of_pair;
+                pos = static_cast<int32_t*>(p.dense("pos", *pos_t, at::kInt, {axes, T}));
+                if (axes == 0) throw Refused("pos must be [axes, T]");
+            } else {
+                pos = static_cast<int32_t*>(p.dense("pos", *pos_t, at::kInt, {T}));
+            }
             cos = static_cast<float*>(p.dense("cos", *cos_t, at::kFloat, {max_pos, rot / 2}));
             sin = static_cast<float*>(p.dense("sin", *sin_t, at::kFloat, {max_pos, rot / 2}));
         }
@@ -275,6 +302,11 @@ PyObject* py_cache_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
         a.done();
         const Pages c(p, kp, vp, x.Hkv, x.D);
         return run(p, stream, [&](fattn_stream_t s) {
+            if (x.axes > 0)
+                return fattn_cache_append_axes(ptr(x.q), k.data_ptr(), v.data_ptr(), ptr(x.q_out), ptr(x.k_out), x.strides,
+                                               c.k, c.v, c.stride, c.pages, c.page_size, x.slots, x.pos, x.axis_of_pair,
+                                               x.axes, x.cos, x.sin, x.max_pos, x.rot, x.interleaved, x.T, x.H, x.Hkv, x.D,
+                                               p.dtype, s);
             return fattn_cache_append(ptr(x.q), k.data_ptr(), v.data_ptr(), ptr(x.q_out), ptr(x.k_out), x.strides, c.k, c.v,
                                       c.stride, c.pages, c.page_size, x.slots, x.pos, x.cos, x.sin, x.max_pos, x.rot,
                                       x.interleaved, x.T, x.H, x.Hkv, x.D, p.dtype, s);
@@ -296,6 +328,11 @@ PyObject* py_cache_append_kv4(PyObject*, PyObject* const* args, Py_ssize_t n) {
         p.rows("v_out", v_out, {x.T, x.Hkv, x.D}, x.strides + 10);
         const PagesKv4 c(p, kc, ks, vc, vs, x.Hkv, x.D);
         return run(p, stream, [&](fattn_stream_t s) {
+            if (x.axes > 0)
+                return fattn_cache_append_kv4_axes(ptr(x.q), k.data_ptr(), v.data_ptr(), ptr(x.q_out), ptr(x.k_out),
+                                                   ptr(v_out), x.strides, c.kc, c.ks, c.vc, c.vs, c.pages, c.page_size,
+                                                   x.slots, x.pos, x.axis_of_pair, x.axes, x.cos, x.sin, x.max_pos, x.rot,
+                                                   x.interleaved, held, x.T, x.H, x.Hkv, x.D, p.dtype, s);
             return fattn_cache_append_kv4(ptr(x.q), k.data_ptr(), v.data_ptr(), ptr(x.q_out), ptr(x.k_out), ptr(v_out),
                                           x.strides, c.kc, c.ks, c.vc, c.vs, c.pages, c.page_size, x.slots, x.pos, x.cos,
                                           x.sin, x.max_pos, x.rot, x.interleaved, held, x.T, x.H, x.Hkv, x.D, p.dtype, s);
@@ -369,6 +406,142 @@ PyObject* py_decode_kv4(PyObject*, PyObject* const* args, Py_ssize_t n) {
     });
 }
 
+PyObject* py_decode_shared(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        Args a{args, n};
+        const at::Tensor &q = a.tensor("q"), &kp = a.tensor("k_pages"), &vp = a.tensor("v_pages");
+        const at::Tensor &pt = a.tensor("prefix_table"), &pl = a.tensor("prefix_len");
+        const Place p(q, "q", 4);
+        const Decode x(a, p, q);
+        const int64_t stream = a.integer();
+        a.done();
+        const int64_t Hkv = kp.dim() == 4 ? kp.size(1) : 0;
+        const Pages c(p, kp, vp, Hkv, x.D);
+        const int64_t width = pt.dim() == 1 ? pt.size(0) : -1;
+        const int32_t* prefix = static_cast<int32_t*>(p.dense("prefix_table", pt, at::kInt, {width}));
+        const int32_t* len = static_cast<int32_t*>(p.dense("prefix_len", pl, at::kInt, {1}));
+        return run(p, stream, [&](fattn_stream_t s) {
+            return fattn_decode_shared(q.data_ptr(), x.out->data_ptr(), x.lse, x.strides, c.k, c.v, c.stride, c.pages,
+                                       c.page_size, prefix, width, len, x.table, x.width, x.lens, x.ws, x.ws_bytes, x.B,
+                                       x.H, Hkv, x.Nq, x.D, x.scale, p.dtype, s);
+        });
+    });
+}
+
+PyObject* py_rotate(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        Args a{args, n};
+        const at::Tensor& q = a.tensor("q");
+        const at::Tensor *k = a.maybe("k"), &q_out = a.tensor("q_out"), *k_out = a.maybe("k_out");
+        const at::Tensor& pos_t = a.tensor("pos");
+        const Axes which(a.next());
+        const at::Tensor &cos_t = a.tensor("cos"), &sin_t = a.tensor("sin");
+        const int interleaved = static_cast<int>(a.integer()), inverse = static_cast<int>(a.integer());
+        const int64_t stream = a.integer();
+        a.done();
+        const Place p(q, "q", 4);
+        const int64_t B = q.size(0), H = q.size(1), N = q.size(2), D = q.size(3);
+        const int64_t Hkv = k && k->dim() == 4 ? k->size(1) : 0;
+        if ((k != nullptr) != (k_out != nullptr)) throw Refused("k_out needs k");
+        if (k && k->dim() != 4) throw Refused("k must have 4 dimensions");
+        if (cos_t.dim() != 2) throw Refused("cos and sin must be [max_pos, rot/2]");
+        const int64_t max_pos = cos_t.size(0), rot = 2 * cos_t.size(1);
+        int64_t st[12], axes = 1;
+        p.rows("q", &q, {B, H, N, D}, st);
+        p.rows("k", k, {B, Hkv, N, D}, st + 3);
+        p.rows("q_out", &q_out, {B, H, N, D}, st + 6);
+        p.rows("k_out", k_out, {B, Hkv, N, D}, st + 9);
+        const int32_t* pos;
+        static const uint8_t one_axis[64] = {};
+        const uint8_t* of_pair = one_axis;
+        if (which.of_pair) {
+            which.check(rot);
+            of_pair = which.of_pair;
+            axes = pos_t.dim() == 3 ? pos_t.size(0) : 0;
+            pos = static_cast<int32_t*>(p.dense("pos", pos_t, at::kInt, {axes, B, N}));
+        } else {
+            pos = static_cast<int32_t*>(p.dense("pos", pos_t, at::kInt, {B, N}));
+        }
+        const float* cos = static_cast<float*>(p.dense("cos", cos_t, at::kFloat, {max_pos, rot / 2}));
+        const float* sin = static_cast<float*>(p.dense("sin", sin_t, at::kFloat, {max_pos, rot / 2}));
+        return run(p, stream, [&](fattn_stream_t s) {
+            return fattn_rotate(q.data_ptr(), ptr(k), q_out.data_ptr(), ptr(k_out), st, pos, of_pair, axes, cos, sin, max_pos,
+                                rot, interleaved, inverse, B, H, Hkv, N, D, p.dtype, s);
+        });
+    });
+}
+
+// Sizes of cross attention, from q and k.
+struct Cross {
+    int64_t B, H, Nq, D, Hkv, Nk;
+    const int32_t* lens = nullptr;
+    Cross(const at::Tensor& q, const at::Tensor& k) {
+        if (k.dim() != 4) throw Refused("k must have 4 dimensions");
+        B = q.size(0), H = q.size(1), Nq = q.size(2), D = q.size(3);
+        Hkv = k.size(1), Nk = k.size(2);
+    }
+    void take_lens(const Place& p, const at::Tensor* t) {
+        if (t) lens = static_cast<int32_t*>(p.dense("kv_lens", *t, at::kInt, {B}));
+    }
+};
+
+PyObject* py_fwd_cross(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        Args a{args, n};
+        const at::Tensor &q = a.tensor("q"), &k = a.tensor("k"), &v = a.tensor("v"), *lens = a.maybe("kv_lens");
+        const float scale = static_cast<float>(a.number());
+        const at::Tensor& out = a.tensor("out");
+        const at::Tensor* lse = a.maybe("lse");
+        const at::Tensor& ws = a.tensor("workspace");
+        const int64_t stream = a.integer();
+        a.done();
+        const Place p(q, "q", 4);
+        Cross x(q, k);
+        int64_t st[12], ws_bytes;
+        p.rows("q", &q, {x.B, x.H, x.Nq, x.D}, st);
+        p.rows("k", &k, {x.B, x.Hkv, x.Nk, x.D}, st + 3);
+        p.rows("v", &v, {x.B, x.Hkv, x.Nk, x.D}, st + 6);
+        p.rows("out", &out, {x.B, x.H, x.Nq, x.D}, st + 9);
+        x.take_lens(p, lens);
+        float* l = lse ? static_cast<float*>(p.dense("lse", *lse, at::kFloat, {x.B, x.H, x.Nq})) : nullptr;
+        void* w = p.workspace(ws, &ws_bytes);
+        return run(p, stream, [&](fattn_stream_t s) {
+            return fattn_fwd_cross(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), l, st, x.lens, w, ws_bytes, x.B,
+                                   x.H, x.Hkv, x.Nq, x.Nk, x.D, scale, p.dtype, s);
+        });
+    });
+}
+
+PyObject* py_bwd_cross(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        Args a{args, n};
+        const char* names[8] = {"q", "k", "v", "o", "dout", "dq", "dk", "dv"};
+        const at::Tensor* t[8];
+        for (int i = 0; i < 5; ++i) t[i] = &a.tensor(names[i]);
+        const at::Tensor &lse = a.tensor("lse"), *lens = a.maybe("kv_lens");
+        const float scale = static_cast<float>(a.number());
+        for (int i = 5; i < 8; ++i) t[i] = &a.tensor(names[i]);
+        const at::Tensor& ws = a.tensor("workspace");
+        const int64_t stream = a.integer();
+        a.done();
+        const Place p(*t[0], "q", 4);
+        Cross x(*t[0], *t[1]);
+        int64_t st[24], ws_bytes;
+        for (int i = 0; i < 8; ++i) {
+            const bool of_keys = i == 1 || i == 2 || i >= 6;
+            p.rows(names[i], t[i], {x.B, of_keys ? x.Hkv : x.H, of_keys ? x.Nk : x.Nq, x.D}, st + 3 * i);
+        }
+        x.take_lens(p, lens);
+        const float* l = static_cast<float*>(p.dense("lse", lse, at::kFloat, {x.B, x.H, x.Nq}));
+        void* w = p.workspace(ws, &ws_bytes);
+        return run(p, stream, [&](fattn_stream_t s) {
+            return fattn_bwd_cross(t[0]->data_ptr(), t[1]->data_ptr(), t[2]->data_ptr(), t[3]->data_ptr(), t[4]->data_ptr(), l,
+                                   t[5]->data_ptr(), t[6]->data_ptr(), t[7]->data_ptr(), st, x.lens, w, ws_bytes, x.B, x.H,
+                                   x.Hkv, x.Nq, x.Nk, x.D, scale, p.dtype, s);
+        });
+    });
+}
+
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 constexpr PyMethodDef method(const char* name) {
     return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(F)), METH_FASTCALL, nullptr};
@@ -379,6 +552,10 @@ PyMethodDef methods[] = {method<py_fwd_packed>("fwd_packed"),
                          method<py_cache_append_kv4>("cache_append_kv4"),
                          method<py_decode>("decode"),
                          method<py_decode_kv4>("decode_kv4"),
+                         method<py_decode_shared>("decode_shared"),
+                         method<py_rotate>("rotate"),
+                         method<py_fwd_cross>("fwd_cross"),
+                         method<py_bwd_cross>("bwd_cross"),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_fattn_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -444,7 +444,7 @@ __device__ __forceinline__ void append_row(const AppendArgs& a, const uint4& raw
 }
 
 // The rows of one kind of tokens [first, first + tokens).
-template <int D, bool BF16, bool KV4, Kind KIND>
+template <int D, bool BF16, bool KV4, bool AXES, Kind KIND>
 __device__ __forceinline__ void append_block(const AppendArgs& a, Shared<D>& sh, uint32_t first, int tokens) {
     constexpr int kChunks = D / 8;                  // threads per row
     constexpr int kLanes = kThreads / kChunks;      // row lanes of a block
@@ -492,7 +492,14 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, Shared<D>& sh,
         const int tl = x / pieces, e = x - tl * pieces;
         int64_t slot = a.slots[first + tl];
         const int pos = a.rot > 0 ? a.pos[first + tl] : 0;
-        if (slot >= 0 && (slot >= a.num_slots || (a.rot > 0 && (pos < 0 || pos >= a.max_pos)))) {
+        bool outside = a.rot > 0 && (pos < 0 || pos >= a.max_pos);
+        if constexpr (AXES) {  // (rot > 0: the launch)
+            for (int ax = 1; ax < a.axes; ++ax) {
+                const int p = a.pos[ax * a.T + first + tl];
+                outside = outside || p < 0 || p >= a.max_pos;
+            }
+        }
+        if (slot >= 0 && (slot >= a.num_slots || outside)) {
             if (e == 0) atomicOr(&g_append_error_word, 1u << kDevErrInvalidArg);
             slot = -1;
         }
@@ -509,7 +516,35 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, Shared<D>& sh,
         if (slot >= 0 && turn) {
             const int64_t at = static_cast<int64_t>(pos) * (a.rot / 2);
             float4(&cs)[4][kChunks] = sh.cs[tl];
-            if (a.interleaved) {  // pairs 4e .. 4e + 3, each angle for both elements
+            if constexpr (AXES) {
+                // Angle i of the position on its own axis: pairs of a chunk may have
+                // several, so each is looked up for itself (once a token and block).
+                auto angle = [&](int i, float& co, float& si) {
+                    const int64_t w = static_cast<int64_t>(a.pos[a.axis[i] * a.T + first + tl]) * (a.rot / 2) + i;
+                    co = a.cos[w];
+                    si = a.sin[w];
+                };
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    float co[4], si[4];
+                    if (a.interleaved) {
+                        angle(4 * e + 2 * u, co[0], si[0]);
+                        angle(4 * e + 2 * u + 1, co[2], si[2]);
+                        co[1] = co[0], si[1] = si[0], co[3] = co[2], si[3] = si[2];
+                        si[0] = -si[0], si[2] = -si[2];
+                    } else {
+                        const bool second = e >= a.rot / 16;
+                        const int i = 8 * (second ? e - a.rot / 16 : e) + 4 * u;
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            angle(i + x, co[x], si[x]);
+                            if (!second) si[x] = -si[x];
+                        }
+                    }
+                    cs[2 * u][e] = make_float4(co[0], co[1], co[2], co[3]);
+                    cs[2 * u + 1][e] = make_float4(si[0], si[1], si[2], si[3]);
+                }
+            } else if (a.interleaved) {  // pairs 4e .. 4e + 3, each angle for both elements
                 const float4 co = *reinterpret_cast<const float4*>(a.cos + at + 4 * e);
                 const float4 si = *reinterpret_cast<const float4*>(a.sin + at + 4 * e);
                 cs[0][e] = make_float4(co.x, co.x, co.y, co.y);
@@ -559,7 +594,7 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, Shared<D>& sh,
 // The first blocks take key and value rows (more work each), the rest query
 // rows: spread evenly among each other they took 12 us longer at 16000 tokens,
 // for the last long blocks start late.
-template <int D, bool BF16, bool KV4>
+template <int D, bool BF16, bool KV4, bool AXES>
 __global__ void __launch_bounds__(kThreads, 5) cache_append_kernel(const __grid_constant__ AppendArgs a) {
     extern __shared__ __align__(16) uint8_t smem[];
     Shared<D>& sh = *reinterpret_cast<Shared<D>*>(smem);
@@ -570,26 +605,29 @@ __global__ void __launch_bounds__(kThreads, 5) cache_append_kernel(const __grid_
     const uint32_t first = index * per;
     const int tokens = static_cast<int>(min(static_cast<int64_t>(per), a.T - first));
     if (query) {
-        append_block<D, BF16, KV4, kQuery>(a, sh, first, tokens);
+        append_block<D, BF16, KV4, AXES, kQuery>(a, sh, first, tokens);
         return;
     }
     if constexpr (KV4) {
         if (a.apart) {
             if (blockIdx.x % 2 == 0)
-                append_block<D, BF16, KV4, kKey>(a, sh, first, tokens);
+                append_block<D, BF16, KV4, AXES, kKey>(a, sh, first, tokens);
             else
-                append_block<D, BF16, KV4, kValue>(a, sh, first, tokens);
+                append_block<D, BF16, KV4, AXES, kValue>(a, sh, first, tokens);
             return;
         }
     }
-    append_block<D, BF16, KV4, kKeyAndValue>(a, sh, first, tokens);
+    append_block<D, BF16, KV4, AXES, kKeyAndValue>(a, sh, first, tokens);
 }
 
 template <int D, bool BF16>
 cudaError_t launch_kind(const AppendArgs& a, bool kv4, unsigned grid, cudaStream_t s) {
     const size_t smem = Shared<D>::bytes(std::max(a.kv_tokens, a.q_tokens));
-    return kv4 ? launch_overlapped(cache_append_kernel<D, BF16, true>, grid, kThreads, smem, s, a)
-               : launch_overlapped(cache_append_kernel<D, BF16, false>, grid, kThreads, smem, s, a);
+    if (a.axes > 0)
+        return kv4 ? launch_overlapped(cache_append_kernel<D, BF16, true, true>, grid, kThreads, smem, s, a)
+                   : launch_overlapped(cache_append_kernel<D, BF16, false, true>, grid, kThreads, smem, s, a);
+    return kv4 ? launch_overlapped(cache_append_kernel<D, BF16, true, false>, grid, kThreads, smem, s, a)
+               : launch_overlapped(cache_append_kernel<D, BF16, false, false>, grid, kThreads, smem, s, a);
 }
 
 }  // namespace

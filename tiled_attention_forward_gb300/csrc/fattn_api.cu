@@ -4,6 +4,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <utility>
 #include <cudaTypedefs.h>
@@ -295,6 +296,132 @@ cudaError_t packed_encode_map(CUtensorMap* map, const void* p, int64_t T, int64_
                               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// One 16-bit tensor of n2 x n1 x n0 rows of D elements (batch entries, heads,
+// tokens; s: their strides) as a map {D, n0, n1, n2} with the given box of rows.
+// Strides of dimensions of one element, which nothing steps by, may be anything.
+struct RowsMap {
+    const void* p;
+    int64_t n2, n1, n0;
+    const int64_t* s;  // strides of n2, n1, n0
+    int box0, box1, box2;
+};
+cudaError_t rows_encode_map(CUtensorMap* map, const RowsMap& m, int64_t D, bool bf16) {
+    auto encode = get_encode_fn();
+    if (!encode) return cudaErrorNotSupported;
+    auto step = [&](int64_t n, int64_t s) { return static_cast<cuuint64_t>(2 * (n > 1 ? s : D)); };
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(m.n0),
+                                static_cast<cuuint64_t>(m.n1), static_cast<cuuint64_t>(m.n2)};
+    const cuuint64_t strides[3] = {step(m.n0, m.s[2]), step(m.n1, m.s[1]), step(m.n2, m.s[0])};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(m.box0), static_cast<cuuint32_t>(m.box1),
+                               static_cast<cuuint32_t>(m.box2)};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    const CUresult r = encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                              const_cast<void*>(m.p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// The strides (batch entry, head, token) of `n` rows: multiples of 8, positive
+// where stepped by, within what a tensor map holds.
+int check_strides(const int64_t* s, const int64_t (&n)[3]) {
+    if (n[0] == 0 || n[1] == 0 || n[2] == 0) return FATTN_OK;  // no rows
+    for (int i = 0; i < 3; ++i) {
+        if (!stride_ok(s[i]) || (n[i] > 1 && s[i] == 0)) return FATTN_ERR_INVALID_ARG;
+        if (s[i] >= (int64_t(1) << 39) || s[i] > kMaxElements / n[i]) return FATTN_ERR_UNSUPPORTED;
+    }
+    return FATTN_OK;
+}
+
+// Whether rows lie apart from one another: their strides nest.
+bool rows3_nested(const Rows3& r) {
+    uintptr_t inside = r.row;
+    for (int i = 0; i < 3; ++i) {
+        if (r.n[i] <= 1) continue;
+        if (r.s[i] < inside) return false;
+        inside += (r.n[i] - 1) * r.s[i];
+    }
+    return true;
+}
+
+View range_of(const Rows3& r) { return dense_view(reinterpret_cast<const void*>(r.p), r.below(UINTPTR_MAX)); }
+
+// How the rows of a K/V head (`share` query heads, Nq tokens, and where `merge`
+// B batch entries too) are cut into tiles of at most 128: boxes of tokens, heads
+// and entries, the fewest.
+struct RowTiles {
+    int box_i, box_h, box_b, n_i, n_h;
+    int64_t tiles, pairs;
+};
+RowTiles row_tiles_of(int64_t share, int64_t Nq, int64_t B, bool merge) {
+    RowTiles t = {};
+    int64_t best = INT64_MAX;
+    for (int64_t bh = 1; bh <= std::min<int64_t>(share, kTcBM); ++bh) {
+        const int64_t bi = std::min<int64_t>(Nq, kTcBM / bh);
+        const int64_t n = ceil_div(Nq, bi) * ceil_div(share, bh);
+        if (n < best) {
+            best = n;
+            t.box_i = static_cast<int>(bi);
+            t.box_h = static_cast<int>(bh);
+        }
+    }
+    t.n_i = static_cast<int>(ceil_div(Nq, t.box_i));
+    t.n_h = static_cast<int>(ceil_div(share, t.box_h));
+    t.box_b = merge && best == 1 ? static_cast<int>(std::min<int64_t>(B, kTcBM / (share * Nq))) : 1;
+    t.tiles = best * (merge ? ceil_div(B, t.box_b) : 1);
+    t.pairs = ceil_div(t.tiles, 2);
+    return t;
+}
+void set_tiles(RowsArgs& a, const RowTiles& t) {
+    a.box_i = t.box_i;
+    a.box_h = t.box_h;
+    a.box_b = t.box_b;
+    a.box_bytes = static_cast<uint32_t>(t.box_i * t.box_h * t.box_b * 128);
+    a.n_i = t.n_i;
+    a.n_h = t.n_h;
+    a.tiles = static_cast<int>(t.tiles);
+    a.pairs = static_cast<int>(t.pairs);
+}
+
+// Parts of rows in a workspace: maxima and sums, then the values' sums.
+int64_t part_rows(int64_t sources, int64_t Hkv, const RowTiles& t) { return sources * Hkv * t.tiles * kTcBM; }
+int64_t part_bytes(int64_t rows, int64_t pitch, int64_t D) { return rows * pitch * (8 + 4 * D); }
+
+// Cross attention: few rows per K/V head take the kernel of decode steps, which
+// streams the keys once for up to 32 rows; so does a call without keys, which only
+// writes zeros.
+bool cross_few_rows(int64_t share, int64_t Nq, int64_t Nk) { return share * Nq <= 32 || Nk == 0; }
+// Parts that the keys are cut into.
+int cross_splits(int64_t B, int64_t Hkv, const RowTiles& t, int64_t Nk) {
+    const int64_t targets = B * Hkv * t.pairs, tiles = ceil_div(Nk, kTcBN);
+    int best = 1;
+    if (targets >= 2 * kSplitCtas) return best;
+    uint32_t least = split_cost(static_cast<int>(targets), static_cast<int>(tiles), kSplitCtas, 1);
+    const int most = static_cast<int>(std::min<int64_t>(max_splits(targets), tiles));
+    for (int s = 2; s <= most; ++s) {
+        const uint32_t cost = split_cost(static_cast<int>(targets), static_cast<int>(tiles), kSplitCtas, s);
+        if (cost < least) {
+            least = cost;
+            best = s;
+        }
+    }
+    return best;
+}
+
+// Sizes of cross attention (dtype, head counts, lengths).
+int validate_cross(int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t Nk, int64_t D, float scale, int dtype) {
+    if (dtype != FATTN_F32 && dtype != FATTN_F16 && dtype != FATTN_BF16) return FATTN_ERR_INVALID_ARG;
+    if (B < 0 || H < 0 || Nq < 0 || Nk < 0 || D < 0) return FATTN_ERR_INVALID_ARG;
+    if (Hkv <= 0 || H % Hkv != 0) return FATTN_ERR_INVALID_ARG;
+    if (!std::isfinite(scale) || scale < 0.f) return FATTN_ERR_INVALID_ARG;
+    if (dtype == FATTN_F32 || (D != 64 && D != 128)) return FATTN_ERR_UNSUPPORTED;
+    const int64_t lim = int64_t(1) << 30;
+    if (B > lim || H > (int64_t(1) << 16) || Nq > lim || Nk > lim || B * H > lim || B * H * Nq > (int64_t(1) << 40) ||
+        B * Hkv * Nk > (int64_t(1) << 40))
+        return FATTN_ERR_UNSUPPORTED;
+    return FATTN_OK;
 }
 
 }  // namespace
@@ -781,12 +908,30 @@ int fattn_bwd_host(const void* q_host, const void* k_host, const void* v_host, c
 
 namespace {
 
-// fattn_cache_append and fattn_cache_append_kv4: `a` comes filled but for what
+// Which axis each pair turns by, into a kernel's arguments.
+int check_axes(const uint8_t* axis_of_pair, int64_t axes, int64_t rot, int64_t D, uint8_t (&axis)[64]) {
+    if (axes < 1 || rot < 0 || rot > D || (rot > 0 && !axis_of_pair)) return FATTN_ERR_INVALID_ARG;
+    if (axes > kMaxAxes || rot % 16 != 0) return FATTN_ERR_UNSUPPORTED;
+    for (int64_t i = 0; i < rot / 2; ++i) {
+        if (axis_of_pair[i] >= axes) return FATTN_ERR_INVALID_ARG;
+        axis[i] = axis_of_pair[i];
+    }
+    return FATTN_OK;
+}
+
+// fattn_cache_append, fattn_cache_append_kv4 and their forms with axes: `a` comes filled but for what
 // is derived here.
-int run_append(AppendArgs& a, const int64_t* strides, int64_t num_pages, int64_t page_size, int64_t rot,
-               int64_t T, int64_t H, int64_t Hkv, int64_t D, int dtype, bool kv4, fattn_stream_t stream_h) {
+// (`axis_of_pair`: with several axes, the host array of rot/2 of them.)
+int run_append(AppendArgs& a, const uint8_t* axis_of_pair, int64_t axes, const int64_t* strides, int64_t num_pages,
+               int64_t page_size, int64_t rot, int64_t T, int64_t H, int64_t Hkv, int64_t D, int dtype, bool kv4,
+               fattn_stream_t stream_h) {
     int st = validate_cache(num_pages, page_size, Hkv, D, dtype);
     if (st != FATTN_OK) return st;
+    if (axes > 0) {
+        st = check_axes(axis_of_pair, axes, rot, D, a.axis);
+        if (st != FATTN_OK) return st;
+        a.axes = rot > 0 ? static_cast<int>(axes) : 0;
+    }
     if (T < 0 || rot < 0 || rot > D || !strides) return FATTN_ERR_INVALID_ARG;
     if (rot % 16 != 0) return FATTN_ERR_UNSUPPORTED;
     if (T == 0) return FATTN_OK;
@@ -834,7 +979,7 @@ int run_append(AppendArgs& a, const int64_t* strides, int64_t num_pages, int64_t
     }
     // (Positions are int32: no row past 2^31 is read.)
     const int64_t table_bytes = std::min<int64_t>(a.max_pos, int64_t(1) << 31) * (rot / 2) * 4;
-    const View tables[4] = {dense_view(a.slots, T * 8), dense_view(rot > 0 ? a.pos : nullptr, T * 4),
+    const View tables[4] = {dense_view(a.slots, T * 8), dense_view(rot > 0 ? a.pos : nullptr, T * 4 * std::max<int64_t>(axes, 1)),
                             dense_view(rot > 0 ? a.cos : nullptr, table_bytes),
                             dense_view(rot > 0 ? a.sin : nullptr, table_bytes)};
     for (int i = 0; i < 4; ++i) {
@@ -871,16 +1016,21 @@ int run_append(AppendArgs& a, const int64_t* strides, int64_t num_pages, int64_t
     return e == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
 }
 
-// fattn_decode and fattn_decode_kv4.
-int run_decode(DecodeArgs& a, const int64_t* strides, int64_t num_pages, int64_t page_size, int64_t table_width,
-               int64_t ws_bytes, int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t D, float scale, int dtype,
-               bool kv4, fattn_stream_t stream_h) {
+// What fattn_decode, fattn_decode_kv4 and fattn_decode_shared check and fill in
+// alike.  `need`: bytes of workspace (0: sizes past their limits); `more`: further
+// inputs in device memory.  *empty: nothing to do.
+int check_decode(DecodeArgs& a, const int64_t* strides, int64_t num_pages, int64_t page_size, int64_t table_width,
+                 int64_t ws_bytes, int64_t need, std::initializer_list<View> more, int64_t B, int64_t H, int64_t Hkv,
+                 int64_t Nq, int64_t D, float scale, int dtype, bool kv4, bool* empty, int* sms) {
+    *empty = false;
     int st = validate_cache(num_pages, page_size, Hkv, D, dtype);
     if (st != FATTN_OK) return st;
     if (B < 0 || H < 0 || Nq < 0 || table_width < 0 || !strides || H % Hkv != 0) return FATTN_ERR_INVALID_ARG;
     if (!std::isfinite(scale) || scale < 0.f) return FATTN_ERR_INVALID_ARG;
-    if (B == 0 || H == 0 || Nq == 0) return FATTN_OK;
-    const int64_t need = fattn_decode_workspace_bytes(B, H, Hkv, Nq, D);
+    if (B == 0 || H == 0 || Nq == 0) {
+        *empty = true;
+        return FATTN_OK;
+    }
     // Key indices are ints, and the last unit of keys ends past the last key.
     if (need <= 0 || table_width > (0x7fffffffll - 65536) / page_size) return FATTN_ERR_UNSUPPORTED;
     if (!a.q || !a.o || !a.k_pages || !a.v_pages || (kv4 && (!a.k_scales || !a.v_scales)) || !a.seq_lens ||
@@ -898,13 +1048,7 @@ int run_decode(DecodeArgs& a, const int64_t* strides, int64_t num_pages, int64_t
     // o's rows must not run into one another: its strides nest.
     const int64_t sizes[3] = {B, H, Nq};
     const Rows3 q_rows = rows3(a.q, sizes, strides, D), o_rows = rows3(a.o, sizes, strides + 3, D);
-    uintptr_t nested = o_rows.row;
-    for (int i = 0; i < 3; ++i) {
-        if (o_rows.n[i] <= 1) continue;
-        if (o_rows.s[i] < nested) return FATTN_ERR_INVALID_ARG;
-        nested += (o_rows.n[i] - 1) * o_rows.s[i];
-    }
-    if (rows3_overlap(q_rows, o_rows)) return FATTN_ERR_INVALID_ARG;
+    if (!rows3_nested(o_rows) || rows3_overlap(q_rows, o_rows)) return FATTN_ERR_INVALID_ARG;
     const int64_t page_rows = num_pages * page_size * Hkv;
     const int64_t inner = Hkv * page_size * D;
     if (!kv4) {
@@ -914,20 +1058,20 @@ int run_decode(DecodeArgs& a, const int64_t* strides, int64_t num_pages, int64_t
     const int64_t page_bytes = kv4 ? page_rows * (D / 2)
                                    : (num_pages > 0 ? 2 * ((num_pages - 1) * a.page_stride + inner) : 0);
     const int64_t scale_bytes = kv4 ? page_rows * (D / kKv4Group) * 4 : 0;
-    auto range = [](const Rows3& r) { return dense_view(reinterpret_cast<const void*>(r.p), r.below(UINTPTR_MAX)); };
-    const View in[7] = {range(q_rows),                       dense_view(a.k_pages, page_bytes),
+    const View in[7] = {range_of(q_rows),                     dense_view(a.k_pages, page_bytes),
                         dense_view(a.v_pages, page_bytes),   dense_view(a.k_scales, scale_bytes),
                         dense_view(a.v_scales, scale_bytes), dense_view(a.block_table, B * table_width * 4),
                         dense_view(a.seq_lens, B * 4)};
-    const View out[3] = {range(o_rows), dense_view(a.lse, B * H * Nq * 4), dense_view(a.workspace, need)};
+    const View out[3] = {range_of(o_rows), dense_view(a.lse, B * H * Nq * 4), dense_view(a.workspace, need)};
     for (int i = 0; i < 3; ++i) {
         for (int j = i == 0 ? 1 : 0; j < 7; ++j)  // (o beside q: above)
             if (views_overlap(out[i], in[j])) return FATTN_ERR_INVALID_ARG;
+        for (const View& x : more)
+            if (views_overlap(out[i], x)) return FATTN_ERR_INVALID_ARG;
         for (int j = i + 1; j < 3; ++j)
             if (views_overlap(out[i], out[j])) return FATTN_ERR_INVALID_ARG;
     }
-    int sms = 0;
-    st = current_sm_count(&sms);
+    st = current_sm_count(sms);
     if (st != FATTN_OK) return st;
     a.q_bs = strides[0];
     a.q_hs = strides[1];
@@ -943,6 +1087,19 @@ int run_decode(DecodeArgs& a, const int64_t* strides, int64_t num_pages, int64_t
     a.Hkv = static_cast<int>(Hkv);
     a.Nq = static_cast<int>(Nq);
     a.scale_log2 = scale * kLog2e;
+    return FATTN_OK;
+}
+
+// fattn_decode and fattn_decode_kv4.
+int run_decode(DecodeArgs& a, const int64_t* strides, int64_t num_pages, int64_t page_size, int64_t table_width,
+               int64_t ws_bytes, int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t D, float scale, int dtype,
+               bool kv4, fattn_stream_t stream_h) {
+    const int64_t need = Hkv > 0 ? fattn_decode_workspace_bytes(B, H, Hkv, Nq, D) : 0;
+    bool empty = false;
+    int sms = 0;
+    const int st = check_decode(a, strides, num_pages, page_size, table_width, ws_bytes, need, {}, B, H, Hkv, Nq, D,
+                                scale, dtype, kv4, &empty, &sms);
+    if (st != FATTN_OK || empty) return st;
     const cudaError_t e = decode_launch(a, static_cast<int>(D), dtype == FATTN_BF16, kv4, sms,
                                         reinterpret_cast<cudaStream_t>(stream_h));
     return e == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
@@ -950,11 +1107,13 @@ int run_decode(DecodeArgs& a, const int64_t* strides, int64_t num_pages, int64_t
 
 }  // namespace
 
-int fattn_cache_append(const void* q, const void* k, const void* v, void* q_out, void* k_out,
-                       const int64_t* strides, void* k_pages, void* v_pages, int64_t page_stride,
-                       int64_t num_pages, int64_t page_size, const int64_t* slots, const int32_t* pos,
-                       const float* cos, const float* sin, int64_t max_pos, int64_t rot, int interleaved,
-                       int64_t T, int64_t H, int64_t Hkv, int64_t D, int dtype, fattn_stream_t stream_h) {
+namespace {
+
+int append16(const void* q, const void* k, const void* v, void* q_out, void* k_out, const int64_t* strides,
+             void* k_pages, void* v_pages, int64_t page_stride, int64_t num_pages, int64_t page_size,
+             const int64_t* slots, const int32_t* pos, const uint8_t* axis_of_pair, int64_t axes, const float* cos,
+             const float* sin, int64_t max_pos, int64_t rot, int interleaved, int64_t T, int64_t H, int64_t Hkv,
+             int64_t D, int dtype, fattn_stream_t stream_h) {
     AppendArgs a;
     std::memset(&a, 0, sizeof(a));
     a.q = q;
@@ -971,15 +1130,15 @@ int fattn_cache_append(const void* q, const void* k, const void* v, void* q_out,
     a.sin = sin;
     a.max_pos = max_pos;
     a.interleaved = interleaved != 0;
-    return run_append(a, strides, num_pages, page_size, rot, T, H, Hkv, D, dtype, false, stream_h);
+    return run_append(a, axis_of_pair, axes, strides, num_pages, page_size, rot, T, H, Hkv, D, dtype, false, stream_h);
 }
 
-int fattn_cache_append_kv4(const void* q, const void* k, const void* v, void* q_out, void* k_out, void* v_out,
-                           const int64_t* strides, void* k_codes, void* k_scales, void* v_codes,
-                           void* v_scales, int64_t num_pages, int64_t page_size, const int64_t* slots,
-                           const int32_t* pos, const float* cos, const float* sin, int64_t max_pos,
-                           int64_t rot, int interleaved, int held, int64_t T, int64_t H, int64_t Hkv,
-                           int64_t D, int dtype, fattn_stream_t stream_h) {
+int append_kv4(const void* q, const void* k, const void* v, void* q_out, void* k_out, void* v_out,
+               const int64_t* strides, void* k_codes, void* k_scales, void* v_codes, void* v_scales,
+               int64_t num_pages, int64_t page_size, const int64_t* slots, const int32_t* pos,
+               const uint8_t* axis_of_pair, int64_t axes, const float* cos, const float* sin, int64_t max_pos,
+               int64_t rot, int interleaved, int held, int64_t T, int64_t H, int64_t Hkv, int64_t D, int dtype,
+               fattn_stream_t stream_h) {
     AppendArgs a;
     std::memset(&a, 0, sizeof(a));
     a.q = q;
@@ -999,7 +1158,52 @@ int fattn_cache_append_kv4(const void* q, const void* k, const void* v, void* q_
     a.max_pos = max_pos;
     a.interleaved = interleaved != 0;
     a.held = held != 0;
-    return run_append(a, strides, num_pages, page_size, rot, T, H, Hkv, D, dtype, true, stream_h);
+    return run_append(a, axis_of_pair, axes, strides, num_pages, page_size, rot, T, H, Hkv, D, dtype, true, stream_h);
+}
+
+}  // namespace
+
+int fattn_cache_append(const void* q, const void* k, const void* v, void* q_out, void* k_out,
+                       const int64_t* strides, void* k_pages, void* v_pages, int64_t page_stride,
+                       int64_t num_pages, int64_t page_size, const int64_t* slots, const int32_t* pos,
+                       const float* cos, const float* sin, int64_t max_pos, int64_t rot, int interleaved,
+                       int64_t T, int64_t H, int64_t Hkv, int64_t D, int dtype, fattn_stream_t stream_h) {
+    return append16(q, k, v, q_out, k_out, strides, k_pages, v_pages, page_stride, num_pages, page_size, slots, pos,
+                    nullptr, 0, cos, sin, max_pos, rot, interleaved, T, H, Hkv, D, dtype, stream_h);
+}
+
+int fattn_cache_append_axes(const void* q, const void* k, const void* v, void* q_out, void* k_out,
+                            const int64_t* strides, void* k_pages, void* v_pages, int64_t page_stride,
+                            int64_t num_pages, int64_t page_size, const int64_t* slots, const int32_t* pos,
+                            const uint8_t* axis_of_pair, int64_t axes, const float* cos, const float* sin,
+                            int64_t max_pos, int64_t rot, int interleaved, int64_t T, int64_t H, int64_t Hkv,
+                            int64_t D, int dtype, fattn_stream_t stream_h) {
+    if (axes < 1) return FATTN_ERR_INVALID_ARG;
+    return append16(q, k, v, q_out, k_out, strides, k_pages, v_pages, page_stride, num_pages, page_size, slots, pos,
+                    axis_of_pair, axes, cos, sin, max_pos, rot, interleaved, T, H, Hkv, D, dtype, stream_h);
+}
+
+int fattn_cache_append_kv4(const void* q, const void* k, const void* v, void* q_out, void* k_out, void* v_out,
+                           const int64_t* strides, void* k_codes, void* k_scales, void* v_codes,
+                           void* v_scales, int64_t num_pages, int64_t page_size, const int64_t* slots,
+                           const int32_t* pos, const float* cos, const float* sin, int64_t max_pos,
+                           int64_t rot, int interleaved, int held, int64_t T, int64_t H, int64_t Hkv,
+                           int64_t D, int dtype, fattn_stream_t stream_h) {
+    return append_kv4(q, k, v, q_out, k_out, v_out, strides, k_codes, k_scales, v_codes, v_scales, num_pages, page_size,
+                      slots, pos, nullptr, 0, cos, sin, max_pos, rot, interleaved, held, T, H, Hkv, D, dtype, stream_h);
+}
+
+int fattn_cache_append_kv4_axes(const void* q, const void* k, const void* v, void* q_out, void* k_out,
+                                void* v_out, const int64_t* strides, void* k_codes, void* k_scales,
+                                void* v_codes, void* v_scales, int64_t num_pages, int64_t page_size,
+                                const int64_t* slots, const int32_t* pos, const uint8_t* axis_of_pair,
+                                int64_t axes, const float* cos, const float* sin, int64_t max_pos, int64_t rot,
+                                int interleaved, int held, int64_t T, int64_t H, int64_t Hkv, int64_t D,
+                                int dtype, fattn_stream_t stream_h) {
+    if (axes < 1) return FATTN_ERR_INVALID_ARG;
+    return append_kv4(q, k, v, q_out, k_out, v_out, strides, k_codes, k_scales, v_codes, v_scales, num_pages, page_size,
+                      slots, pos, axis_of_pair, axes, cos, sin, max_pos, rot, interleaved, held, T, H, Hkv, D, dtype,
+                      stream_h);
 }
 
 int64_t fattn_packed_workspace_bytes(int64_t B, int64_t T) {
@@ -1134,6 +1338,386 @@ int fattn_decode_kv4(const void* q, void* o, float* lse, const int64_t* strides,
                       dtype, true, stream_h);
 }
 
+int64_t fattn_decode_shared_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t D) {
+    const int64_t own = fattn_decode_workspace_bytes(B, H, Hkv, Nq, D);
+    if (own <= 0 || H > (int64_t(1) << 16)) return 0;
+    const RowTiles t = row_tiles_of(H / Hkv, Nq, B, true);
+    const int64_t rows = part_rows(1, Hkv, t);
+    return ceil_div(own, 16) * 16 + 16 + part_bytes(rows, max_splits(Hkv * t.pairs), D);
+}
+
+int fattn_decode_shared(const void* q, void* o, float* lse, const int64_t* strides, const void* k_pages,
+                        const void* v_pages, int64_t page_stride, int64_t num_pages, int64_t page_size,
+                        const int32_t* prefix_table, int64_t prefix_width, const int32_t* prefix_len,
+                        const int32_t* block_table, int64_t table_width, const int32_t* seq_lens,
+                        void* workspace, int64_t workspace_bytes, int64_t B, int64_t H, int64_t Hkv, int64_t Nq,
+                        int64_t D, float scale, int dtype, fattn_stream_t stream_h) {
+    if (prefix_width < 0) return FATTN_ERR_INVALID_ARG;
+    if (prefix_width == 0)  // no prefix
+        return fattn_decode(q, o, lse, strides, k_pages, v_pages, page_stride, num_pages, page_size, block_table,
+                            table_width, seq_lens, workspace, workspace_bytes, B, H, Hkv, Nq, D, scale, dtype, stream_h);
+    SharedDecodeArgs d;
+    std::memset(static_cast<void*>(&d), 0, sizeof(d));
+    d.q = q;
+    d.o = o;
+    d.lse = lse;
+    d.k_pages = k_pages;
+    d.v_pages = v_pages;
+    d.page_stride = page_stride;
+    d.block_table = block_table;
+    d.seq_lens = seq_lens;
+    d.workspace = workspace;
+    const int64_t need = Hkv > 0 && H > 0 ? fattn_decode_shared_workspace_bytes(B, H, Hkv, Nq, D) : 0;
+    // (What lies past these limits is refused below, before its extent could overflow.)
+    const int64_t width = std::min<int64_t>(prefix_width, int64_t(1) << 31);
+    bool empty = false;
+    int sms = 0;
+    int st = check_decode(d, strides, num_pages, page_size, table_width, workspace_bytes, need,
+                          {dense_view(prefix_table, width * 4), dense_view(prefix_len, 4)}, B, H, Hkv, Nq, D, scale,
+                          dtype, false, &empty, &sms);
+    if (st != FATTN_OK && st != FATTN_ERR_NO_DEVICE) return st;
+    if (empty) return FATTN_OK;
+    const int no_device = st;
+    if (!prefix_table || !prefix_len || num_pages == 0) return FATTN_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(prefix_table) & 3u) || (reinterpret_cast<uintptr_t>(prefix_len) & 3u))
+        return FATTN_ERR_MISALIGNED;
+    if (prefix_width > (0x7fffffffll - 65536) / page_size) return FATTN_ERR_UNSUPPORTED;
+    // A tensor map's strides are below 2^40 bytes.
+    if (page_stride >= (int64_t(1) << 39)) return FATTN_ERR_UNSUPPORTED;
+    const int64_t n_q[3] = {B, H, Nq};
+    st = check_strides(strides, n_q);
+    if (st != FATTN_OK) return st;
+    const RowTiles t = row_tiles_of(H / Hkv, Nq, B, true);
+    const int pitch = max_splits(Hkv * t.pairs);
+    if (Hkv * t.pairs * pitch > (int64_t(1) << 30)) return FATTN_ERR_UNSUPPORTED;
+    if (no_device != FATTN_OK) return no_device;
+
+    RowsArgs a;
+    std::memset(static_cast<void*>(&a), 0, sizeof(a));
+    const bool bf16 = dtype == FATTN_BF16;
+    const int piece = static_cast<int>(std::min<int64_t>(page_size & -page_size, kTcBN));
+    const int64_t page_strides[3] = {page_stride, page_size * D, D};
+    if (rows_encode_map(&a.tmap_q, {q, B, H, Nq, strides, t.box_i, t.box_h, t.box_b}, D, bf16) != cudaSuccess ||
+        rows_encode_map(&a.tmap_k, {k_pages, num_pages, Hkv, page_size, page_strides, piece, 1, 1}, D, bf16) != cudaSuccess ||
+        rows_encode_map(&a.tmap_v, {v_pages, num_pages, Hkv, page_size, page_strides, piece, 1, 1}, D, bf16) != cudaSuccess)
+        return FATTN_ERR_CUDA;
+    set_tiles(a, t);
+    uint8_t* ws = static_cast<uint8_t*>(workspace) + ceil_div(fattn_decode_workspace_bytes(B, H, Hkv, Nq, D), 16) * 16;
+    a.part_count = reinterpret_cast<int32_t*>(ws);
+    a.part_o = reinterpret_cast<float*>(ws + 16);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + part_rows(1, Hkv, t) * pitch * D);
+    a.part_pitch = pitch;
+    a.lens = prefix_len;
+    a.table = prefix_table;
+    a.H = static_cast<int>(H);
+    a.Hkv = static_cast<int>(Hkv);
+    a.scale_log2 = score_factor(scale);
+    a.timeout_ns = kDefaultTimeoutNs;
+    a.num_pages = static_cast<int>(num_pages);
+    a.page_size = static_cast<int>(page_size);
+    a.piece = piece;
+    a.max_keys = static_cast<int>(prefix_width * page_size);
+    a.sources = 1;
+    a.B = static_cast<int>(B);
+    a.Nq = static_cast<int>(Nq);
+    a.share = static_cast<int>(H / Hkv);
+    const int grid = static_cast<int>(std::min<int64_t>(Hkv * t.pairs * pitch, sms));
+    if (rows_launch(a, static_cast<int>(D), bf16, grid, reinterpret_cast<cudaStream_t>(stream_h)) != cudaSuccess)
+        return FATTN_ERR_CUDA;
+    d.part_o = a.part_o;
+    d.part_ml = a.part_ml;
+    d.part_count = a.part_count;
+    d.part_pitch = pitch;
+    d.box_i = t.box_i;
+    d.box_h = t.box_h;
+    d.box_b = t.box_b;
+    d.n_i = t.n_i;
+    d.n_h = t.n_h;
+    d.tiles = a.tiles;
+    const cudaError_t e = decode_shared_launch(d, static_cast<int>(D), bf16, sms, reinterpret_cast<cudaStream_t>(stream_h));
+    return e == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
+}
+
+int64_t fattn_cross_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t Nk, int64_t D) {
+    if (B <= 0 || H <= 0 || Nq <= 0 || validate_cross(B, H, Hkv, Nq, Nk, D, 1.f, FATTN_BF16) != FATTN_OK) return 0;
+    if (cross_few_rows(H / Hkv, Nq, Nk)) return decode_workspace_bytes(B, H, Hkv, Nq, D);
+    const RowTiles t = row_tiles_of(H / Hkv, Nq, B, false);
+    const int splits = cross_splits(B, Hkv, t, Nk);
+    return splits > 1 ? part_bytes(part_rows(B, Hkv, t), splits, D) : 16;
+}
+
+int fattn_fwd_cross(const void* q, const void* k, const void* v, void* o, float* lse, const int64_t* strides,
+                    const int32_t* kv_lens, void* workspace, int64_t workspace_bytes, int64_t B, int64_t H,
+                    int64_t Hkv, int64_t Nq, int64_t Nk, int64_t D, float scale, int dtype,
+                    fattn_stream_t stream_h) {
+    int st = validate_cross(B, H, Hkv, Nq, Nk, D, scale, dtype);
+    if (st != FATTN_OK) return st;
+    if (!strides) return FATTN_ERR_INVALID_ARG;
+    if (B == 0 || H == 0 || Nq == 0) return FATTN_OK;
+    if (!q || !o || (Nk > 0 && (!k || !v)) || !workspace) return FATTN_ERR_INVALID_ARG;
+    const int64_t need = fattn_cross_workspace_bytes(B, H, Hkv, Nq, Nk, D);
+    if (need <= 0) return FATTN_ERR_UNSUPPORTED;
+    if (workspace_bytes < need) return FATTN_ERR_INVALID_ARG;
+    const int64_t n_q[3] = {B, H, Nq}, n_k[3] = {B, Hkv, Nk};
+    for (int i = 0; i < 4; ++i) {
+        st = check_strides(strides + 3 * i, i == 1 || i == 2 ? n_k : n_q);
+        if (st != FATTN_OK) return st;
+    }
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(workspace) ||
+        (reinterpret_cast<uintptr_t>(lse) & 3u) || (reinterpret_cast<uintptr_t>(kv_lens) & 3u))
+        return FATTN_ERR_MISALIGNED;
+    const Rows3 rq = rows3(q, n_q, strides, D), ro = rows3(o, n_q, strides + 9, D);
+    if (!rows3_nested(ro) || rows3_overlap(rq, ro)) return FATTN_ERR_INVALID_ARG;
+    View in[4] = {range_of(rq), View(), View(), dense_view(kv_lens, B * 4)};
+    if (Nk > 0) {
+        const Rows3 rk = rows3(k, n_k, strides + 3, D), rv = rows3(v, n_k, strides + 6, D);
+        if (rows3_overlap(rk, ro) || rows3_overlap(rv, ro)) return FATTN_ERR_INVALID_ARG;
+        in[1] = range_of(rk);
+        in[2] = range_of(rv);
+    }
+    const View out[3] = {range_of(ro), dense_view(lse, B * H * Nq * 4), dense_view(workspace, need)};
+    for (int i = 0; i < 3; ++i) {
+        for (int j = i == 0 ? 3 : 0; j < 4; ++j)  // (o beside q, k and v: above)
+            if (views_overlap(out[i], in[j])) return FATTN_ERR_INVALID_ARG;
+        for (int j = i + 1; j < 3; ++j)
+            if (views_overlap(out[i], out[j])) return FATTN_ERR_INVALID_ARG;
+    }
+    const bool few = cross_few_rows(H / Hkv, Nq, Nk);
+    const RowTiles t = row_tiles_of(H / Hkv, Nq, B, false);
+    const int splits = few ? 1 : cross_splits(B, Hkv, t, Nk);
+    if (!few && B * Hkv * t.pairs * splits > (int64_t(1) << 30)) return FATTN_ERR_UNSUPPORTED;
+    int sms = 0;
+    st = current_sm_count(&sms);
+    if (st != FATTN_OK) return st;
+    const bool bf16 = dtype == FATTN_BF16;
+    const cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_h);
+    if (few) {
+        CrossDecodeArgs a;
+        std::memset(static_cast<void*>(&a), 0, sizeof(a));
+        a.q = q;
+        a.o = o;
+        a.lse = lse;
+        a.q_bs = strides[0], a.q_hs = strides[1], a.q_ns = strides[2];
+        a.k_bs = strides[3], a.k_hs = strides[4], a.k_ns = strides[5];
+        a.v_bs = strides[6], a.v_hs = strides[7], a.v_ns = strides[8];
+        a.o_bs = strides[9], a.o_hs = strides[10], a.o_ns = strides[11];
+        a.k_pages = k;
+        a.v_pages = v;
+        a.seq_lens = kv_lens;
+        a.workspace = workspace;
+        a.page_size = 16;  // (no pages: a stage of keys)
+        a.B = static_cast<int>(B);
+        a.H = static_cast<int>(H);
+        a.Hkv = static_cast<int>(Hkv);
+        a.Nq = static_cast<int>(Nq);
+        a.Nk = static_cast<int>(Nk);
+        a.scale_log2 = scale * kLog2e;
+        const cudaError_t e = decode_cross_launch(a, static_cast<int>(D), bf16, sms, stream);
+        return e == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
+    }
+    RowsArgs a;
+    std::memset(static_cast<void*>(&a), 0, sizeof(a));
+    const int keys = static_cast<int>(kTcBN);
+    if (rows_encode_map(&a.tmap_q, {q, B, H, Nq, strides, t.box_i, t.box_h, 1}, D, bf16) != cudaSuccess ||
+        rows_encode_map(&a.tmap_k, {k, B, Hkv, Nk, strides + 3, keys, 1, 1}, D, bf16) != cudaSuccess ||
+        rows_encode_map(&a.tmap_v, {v, B, Hkv, Nk, strides + 6, keys, 1, 1}, D, bf16) != cudaSuccess)
+        return FATTN_ERR_CUDA;
+    set_tiles(a, t);
+    a.o = o;
+    a.lse = lse;
+    a.o_bs = strides[9], a.o_hs = strides[10], a.o_ns = strides[11];
+    a.lens = kv_lens;
+    a.splits = splits;
+    a.part_pitch = splits;
+    if (splits > 1) {
+        a.part_o = static_cast<float*>(workspace);
+        a.part_ml = reinterpret_cast<float2*>(a.part_o + part_rows(B, Hkv, t) * splits * D);
+    }
+    a.H = static_cast<int>(H);
+    a.Hkv = static_cast<int>(Hkv);
+    a.scale_log2 = score_factor(scale);
+    a.timeout_ns = kDefaultTimeoutNs;
+    a.piece = keys;
+    a.max_keys = static_cast<int>(Nk);
+    a.sources = static_cast<int>(B);
+    a.B = static_cast<int>(B);
+    a.Nq = static_cast<int>(Nq);
+    a.share = static_cast<int>(H / Hkv);
+    const int grid = static_cast<int>(std::min<int64_t>(B * Hkv * t.pairs * splits, sms));
+    cudaError_t e = rows_launch(a, static_cast<int>(D), bf16, grid, stream);
+    if (e == cudaSuccess && splits > 1) e = rows_join_launch(a, static_cast<int>(D), bf16, stream);
+    return e == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
+}
+
+int64_t fattn_bwd_cross_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t Nk, int64_t D) {
+    if (B <= 0 || H <= 0 || Nq <= 0 || Nk < 0 || validate_cross(B, H, Hkv, Nq, Nk, D, 1.f, FATTN_BF16) != FATTN_OK)
+        return 0;
+    return fattn_bwd_workspace_bytes(B, H, Nq);
+}
+
+int fattn_bwd_cross(const void* q, const void* k, const void* v, const void* o, const void* dout, const float* lse,
+                    void* dq, void* dk, void* dv, const int64_t* strides, const int32_t* kv_lens, void* workspace,
+                    int64_t workspace_bytes, int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t Nk, int64_t D,
+                    float scale, int dtype, fattn_stream_t stream_h) {
+    int st = validate_cross(B, H, Hkv, Nq, Nk, D, scale, dtype);
+    if (st != FATTN_OK) return st;
+    if (!strides) return FATTN_ERR_INVALID_ARG;
+    if (B == 0 || H == 0 || (Nq == 0 && Nk == 0)) return FATTN_OK;
+    if ((Nq > 0 && (!q || !o || !dout || !lse || !dq || !workspace)) || (Nk > 0 && (!k || !v || !dk || !dv)))
+        return FATTN_ERR_INVALID_ARG;
+    const int64_t need = fattn_bwd_cross_workspace_bytes(B, H, Hkv, Nq, Nk, D);
+    if (need <= 0 && Nq > 0) return FATTN_ERR_UNSUPPORTED;
+    if (workspace_bytes < need) return FATTN_ERR_INVALID_ARG;
+    // q, k, v, o, dout, dq, dk, dv
+    const void* ptrs[8] = {q, k, v, o, dout, dq, dk, dv};
+    const bool of_keys[8] = {false, true, true, false, false, false, true, true};
+    const int64_t n_q[3] = {B, H, Nq}, n_k[3] = {B, Hkv, Nk};
+    Rows3 rows[8] = {};
+    for (int i = 0; i < 8; ++i) {
+        st = check_strides(strides + 3 * i, of_keys[i] ? n_k : n_q);
+        if (st != FATTN_OK) return st;
+        if (!aligned16(ptrs[i])) return FATTN_ERR_MISALIGNED;
+        const bool empty = (of_keys[i] ? Nk : Nq) == 0;
+        ptrs[i] = empty ? nullptr : ptrs[i];
+        if (!empty) rows[i] = rows3(ptrs[i], of_keys[i] ? n_k : n_q, strides + 3 * i, D);
+    }
+    if (!aligned16(workspace) || (reinterpret_cast<uintptr_t>(lse) & 3u) || (reinterpret_cast<uintptr_t>(kv_lens) & 3u))
+        return FATTN_ERR_MISALIGNED;
+    const View small[3] = {dense_view(lse, B * H * Nq * 4), dense_view(kv_lens, B * 4), dense_view(workspace, need)};
+    for (int i = 5; i < 8; ++i) {
+        if (!ptrs[i]) continue;
+        if (!rows3_nested(rows[i])) return FATTN_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (ptrs[j] && rows3_overlap(rows[i], rows[j])) return FATTN_ERR_INVALID_ARG;
+        for (const View& x : small)
+            if (views_overlap(range_of(rows[i]), x)) return FATTN_ERR_INVALID_ARG;
+    }
+    for (int j = 0; j < 5; ++j)
+        if (ptrs[j] && views_overlap(small[2], range_of(rows[j]))) return FATTN_ERR_INVALID_ARG;
+    if (views_overlap(small[2], small[0]) || views_overlap(small[2], small[1])) return FATTN_ERR_INVALID_ARG;
+    const int64_t tiles_q = ceil_div(Nq, 128), tiles_k = ceil_div(Nk, 128);
+    if (tiles_q * B * H > 0x7fffffffll || tiles_k * B * Hkv > 0x7fffffffll || tiles_q * (H / Hkv) > 0x7fffffffll)
+        return FATTN_ERR_UNSUPPORTED;
+    int sms = 0;
+    st = current_sm_count(&sms);
+    if (st != FATTN_OK) return st;
+    const bool bf16 = dtype == FATTN_BF16;
+    CrossBwdArgs a;
+    std::memset(static_cast<void*>(&a), 0, sizeof(a));
+    CUtensorMap* maps[5] = {&a.tmap_q, &a.tmap_k, &a.tmap_v, nullptr, &a.tmap_do};
+    for (int i = 0; i < 5; ++i)  // (without queries or keys nothing is loaded)
+        if (maps[i] && Nq > 0 && Nk > 0 && rows_encode_map(maps[i], {ptrs[i], B, of_keys[i] ? Hkv : H, of_keys[i] ? Nk : Nq, strides + 3 * i,
+                                                 128, 1, 1}, D, bf16) != cudaSuccess)
+            return FATTN_ERR_CUDA;
+    a.ws = static_cast<float*>(workspace);
+    a.dq = dq;
+    a.dk = dk;
+    a.dv = dv;
+    a.N = static_cast<int>(Nq);
+    a.Npad = static_cast<int>(bwd_padded_rows(Nq));
+    a.BH = static_cast<int>(B * H);
+    a.H = static_cast<int>(H);
+    a.Hkv = static_cast<int>(Hkv);
+    a.BHkv = static_cast<int>(B * Hkv);
+    a.num_tiles = static_cast<int>(tiles_q);
+    a.sl2 = scale * kLog2e;
+    a.scale = scale;
+    a.timeout_ns = kDefaultTimeoutNs;
+    a.Nk = static_cast<int>(Nk);
+    a.tiles_k = static_cast<int>(tiles_k);
+    a.lens = kv_lens;
+    a.o = o;
+    a.dout = dout;
+    a.lse = lse;
+    a.o_bs = strides[9], a.o_hs = strides[10], a.o_ns = strides[11];
+    a.do_bs = strides[12], a.do_hs = strides[13], a.do_ns = strides[14];
+    a.dq_bs = strides[15], a.dq_hs = strides[16], a.dq_ns = strides[17];
+    a.dk_bs = strides[18], a.dk_hs = strides[19], a.dk_ns = strides[20];
+    a.dv_bs = strides[21], a.dv_hs = strides[22], a.dv_ns = strides[23];
+    const cudaError_t e = bwd_cross_launch(a, static_cast<int>(D), bf16, reinterpret_cast<cudaStream_t>(stream_h));
+    return e == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
+}
+
+int fattn_rotate(const void* q, const void* k, void* q_out, void* k_out, const int64_t* strides, const int32_t* pos,
+                 const uint8_t* axis_of_pair, int64_t axes, const float* cos, const float* sin, int64_t max_pos,
+                 int64_t rot, int interleaved, int inverse, int64_t B, int64_t H, int64_t Hkv, int64_t N, int64_t D,
+                 int dtype, fattn_stream_t stream_h) {
+    if (dtype != FATTN_F32 && dtype != FATTN_F16 && dtype != FATTN_BF16) return FATTN_ERR_INVALID_ARG;
+    if (B < 0 || H < 0 || N < 0 || D < 0 || max_pos < 0 || !strides) return FATTN_ERR_INVALID_ARG;
+    if ((k == nullptr) != (k_out == nullptr)) return FATTN_ERR_INVALID_ARG;
+    if (!k) Hkv = 0;
+    if (k && Hkv <= 0) return FATTN_ERR_INVALID_ARG;
+    if (dtype == FATTN_F32 || (D != 64 && D != 128)) return FATTN_ERR_UNSUPPORTED;
+    RotateArgs a;
+    std::memset(static_cast<void*>(&a), 0, sizeof(a));
+    int st = check_axes(axis_of_pair, axes, rot, D, a.axis);
+    if (st != FATTN_OK) return st;
+    if (B == 0 || H == 0 || N == 0) return FATTN_OK;
+    const int64_t lim = int64_t(1) << 30;
+    if (B > lim || N > lim || B * N > lim || H > (int64_t(1) << 16) || Hkv > (int64_t(1) << 16))
+        return FATTN_ERR_UNSUPPORTED;
+    if (!q || !q_out || (rot > 0 && (!pos || !cos || !sin))) return FATTN_ERR_INVALID_ARG;
+    // q, k, q_out, k_out
+    const void* ptrs[4] = {q, k, q_out, k_out};
+    const int64_t n_q[3] = {B, H, N}, n_k[3] = {B, Hkv, N};
+    Rows3 rows[4] = {};
+    for (int i = 0; i < 4; ++i) {
+        if (!ptrs[i]) continue;
+        const int64_t* s = strides + 3 * i;
+        const int64_t(&n)[3] = i % 2 ? n_k : n_q;
+        for (int x = 0; x < 3; ++x) {
+            if (!stride_ok(s[x])) return FATTN_ERR_INVALID_ARG;
+            if (s[x] > kMaxElements / n[x]) return FATTN_ERR_UNSUPPORTED;
+        }
+        if (!aligned16(ptrs[i])) return FATTN_ERR_MISALIGNED;
+        rows[i] = rows3(ptrs[i], n, s, D);
+    }
+    if (rot > 0 && ((reinterpret_cast<uintptr_t>(pos) & 3u) || !aligned16(cos) || !aligned16(sin)))
+        return FATTN_ERR_MISALIGNED;
+    // (Positions are int32: no row past 2^31 is read.)
+    const int64_t table_bytes = std::min<int64_t>(max_pos, int64_t(1) << 31) * (rot / 2) * 4;
+    const View tables[3] = {dense_view(rot > 0 ? pos : nullptr, axes * B * N * 4),
+                            dense_view(rot > 0 ? cos : nullptr, table_bytes),
+                            dense_view(rot > 0 ? sin : nullptr, table_bytes)};
+    for (int i = 2; i < 4; ++i) {
+        if (!ptrs[i]) continue;
+        if (!rows3_nested(rows[i])) return FATTN_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j) {
+            if (!ptrs[j]) continue;
+            bool itself = j == i - 2 && ptrs[j] == ptrs[i];  // in place
+            for (int x = 0; x < 3 && itself; ++x)
+                itself = (i % 2 ? n_k : n_q)[x] == 1 || strides[3 * i + x] == strides[3 * j + x];
+            if (!itself && rows3_overlap(rows[i], rows[j])) return FATTN_ERR_INVALID_ARG;
+        }
+        for (const View& x : tables)
+            if (views_overlap(range_of(rows[i]), x)) return FATTN_ERR_INVALID_ARG;
+    }
+    int sms = 0;
+    st = current_sm_count(&sms);
+    if (st != FATTN_OK) return st;
+    for (int t = 0; t < 2; ++t) {
+        a.x[t] = ptrs[t];
+        a.y[t] = const_cast<void*>(ptrs[2 + t]);
+        a.x_bs[t] = strides[3 * t], a.x_hs[t] = strides[3 * t + 1], a.x_ns[t] = strides[3 * t + 2];
+        a.y_bs[t] = strides[6 + 3 * t], a.y_hs[t] = strides[7 + 3 * t], a.y_ns[t] = strides[8 + 3 * t];
+    }
+    a.heads[0] = static_cast<int>(H);
+    a.heads[1] = static_cast<int>(Hkv);
+    a.pos = pos;
+    a.cos = cos;
+    a.sin = sin;
+    a.max_pos = max_pos;
+    a.tokens = B * N;
+    a.N = static_cast<int>(N);
+    a.rot = static_cast<int>(rot);
+    a.interleaved = interleaved != 0;
+    a.inverse = inverse != 0;
+    a.axes = rot > 0 ? static_cast<int>(axes) : 0;
+    const cudaError_t e = rotate_launch(a, static_cast<int>(D), dtype == FATTN_BF16, sms,
+                                        reinterpret_cast<cudaStream_t>(stream_h));
+    return e == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
+}
+
 int fattn_get_device_status(fattn_stream_t stream_h) {
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_h);
     if (cudaStreamSynchronize(stream) != cudaSuccess) return FATTN_ERR_CUDA;
@@ -1145,6 +1729,13 @@ int fattn_get_device_status(fattn_stream_t stream_h) {
         decode_read_and_clear_error_word(&word_decode) != cudaSuccess ||
         packed_read_and_clear_error_word(&word_packed) != cudaSuccess)
         return FATTN_ERR_CUDA;
+    for (auto* read : {rows_read_and_clear_error_word, bwd_cross_read_and_clear_error_word,
+                       decode_shared_read_and_clear_error_word, decode_cross_read_and_clear_error_word,
+                       rotate_read_and_clear_error_word}) {
+        uint32_t more = 0;
+        if (read(&more) != cudaSuccess) return FATTN_ERR_CUDA;
+        word |= more;
+    }
     word |= word_unfused | word_bwd | word_append | word_decode | word_packed;
     if (word & (1u << FATTN_ERR_INTERNAL)) return FATTN_ERR_INTERNAL;
     if (word & (1u << FATTN_ERR_TIMEOUT)) return FATTN_ERR_TIMEOUT;

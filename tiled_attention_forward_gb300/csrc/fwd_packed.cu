@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PlanArg
 template <int D, bool BF16, bool CAUSAL>
 cudaError_t launch_one(const PackedArgs& a, int capacity, int grid, cudaStream_t stream) {
     using L = TcLayout<D>;
-    auto* fn = attn_fwd_tc_kernel<D, BF16, CAUSAL, true>;
+    auto* fn = attn_fwd_tc_kernel<D, BF16, CAUSAL, kPacked>;
     static std::atomic<bool> done[kMaxDevices] = {};
     cudaError_t e = opt_in_smem_once(fn, L::kAlloc, done);
     if (e != cudaSuccess) return e;

@@ -23,7 +23,7 @@ __global__ void wait_selftest_kernel(uint64_t timeout_ns) {
 template <int D, bool BF16, bool CAUSAL>
 cudaError_t launch_one(const TcArgs& a, int grid, cudaStream_t stream) {
     using L = TcLayout<D>;
-    auto* fn = attn_fwd_tc_kernel<D, BF16, CAUSAL, false>;
+    auto* fn = attn_fwd_tc_kernel<D, BF16, CAUSAL, kDense>;
     // The opt-in above 48 KB of dynamic shared memory is per device: set it
     // once for every device this instantiation is launched on.
     static std::atomic<bool> done[kMaxDevices] = {};

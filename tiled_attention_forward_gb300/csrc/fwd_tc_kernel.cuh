@@ -58,13 +58,17 @@
 
 namespace fattn {
 
-// Two kinds of problem share the kernel: dense [B,H,N,D] batches (TcArgs), and
+// Three kinds of problem share the kernel: dense [B,H,N,D] batches (TcArgs);
 // packed sequences of different lengths (PackedArgs), whose Q blocks come from
-// a list in device memory and whose rows are addressed by strides.  Each
+// a list in device memory and whose rows are addressed by strides; and rows over
+// keys of a length of their own (RowsArgs): the query rows that share a K/V head
+// are stacked into tiles whatever heads and batch entries they belong to, every
+// row sees every key, and the keys of a tile may be cut between CTAs.  Each
 // translation unit that includes this file instantiates one of them and has
 // the error word and the task counters of its own kernels.
-template <bool PACKED>
-using ArgsOf = std::conditional_t<PACKED, PackedArgs, TcArgs>;
+enum Kind { kDense, kPacked, kRows };
+template <Kind KIND>
+using ArgsOf = std::conditional_t<KIND == kPacked, PackedArgs, std::conditional_t<KIND == kRows, RowsArgs, TcArgs>>;
 
 // Bit k set <=> a kernel on this device hit fattn_status k (only TIMEOUT today).
 static __device__ uint32_t g_error_word;
@@ -122,11 +126,45 @@ __device__ __forceinline__ PackedPlan* plan_of(const PackedArgs& a) {
     return reinterpret_cast<PackedPlan*>(reinterpret_cast<uint8_t*>(a.plan) + blockIdx.x * a.plan_stride);
 }
 
+// Rows: the number of parts that this launch's keys are cut into (in the CTA's
+// shared memory, beside the TMEM base and the abort flag).
+template <int D>
+__device__ __forceinline__ int* splits_word() {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    return reinterpret_cast<int*>(smem_raw + TcLayout<D>::kMiscOff + 8);
+}
+
+// Rows: keys of a source that every row sees.
+__device__ __forceinline__ int visible_keys(const RowsArgs& a, int source, bool report) {
+    if (a.lens == nullptr) return a.max_keys;
+    const int len = a.lens[source];
+    if (len < 0 || len > a.max_keys) {
+        if (report) atomicOr(&g_error_word, 1u << kDevErrInvalidArg);
+        return len < 0 ? 0 : a.max_keys;
+    }
+    return len;
+}
+
+// Rows: which query row thread `trow` of tile u is (false: none).
+struct RowPlace {
+    int b, h, i;  // batch entry, head among those of the K/V head, token
+};
+__device__ __forceinline__ bool row_place(const RowsArgs& a, int source, int u, int trow, RowPlace& r) {
+    const int per_b = a.n_h * a.n_i;
+    const int ub = u / per_b, uh = (u - ub * per_b) / a.n_i, ui = u % a.n_i;
+    const int per_box = a.box_h * a.box_i;
+    const int tb = trow / per_box, th = (trow - tb * per_box) / a.box_i, ti = trow % a.box_i;
+    r.i = ui * a.box_i + ti;
+    r.h = uh * a.box_h + th;
+    r.b = source + ub * a.box_b + tb;
+    return u < a.tiles && tb < a.box_b && r.i < a.Nq && r.h < a.share && r.b < a.B;
+}
+
 struct Task {
-    int bh;     // query head (dense: b * H + h)
-    int q0;     // first row of the Q block within its sequence
-    int n;      // rows and keys of the sequence
-    int start;  // packed: the sequence's first token
+    int bh;     // query head (dense: b * H + h; rows: source * Hkv + K/V head)
+    int q0;     // first row of the Q block within its sequence (rows: the first tile's index)
+    int n;      // rows and keys of the sequence (rows: keys of the task)
+    int start;  // packed: the sequence's first token; rows: the task's first key
     int nb[2];  // K/V tiles visited by Q tile 0 / 1 (0: tile has no valid row)
     int nbmax;
 };
@@ -141,13 +179,36 @@ struct Task {
 // Packed: the list of Q blocks (sequence start, its length, block) is sorted
 // longest first; heads in groups of a.head_group (the K/V of all tokens of a
 // group fits in L2), and within a group block by block, heads inner.
-template <bool CAUSAL, bool EQUAL = false, bool PACKED = false>
-__device__ __forceinline__ Task decode_task(int t, const ArgsOf<PACKED>& a) {
+//
+// Rows: sources and their K/V heads outermost, then the parts that the keys are
+// cut into, the tile pairs of a K/V head innermost: CTAs that run together
+// stream the same keys.
+template <bool CAUSAL, bool EQUAL = false, Kind KIND = kDense>
+__device__ __forceinline__ Task decode_task(int t, const ArgsOf<KIND>& a) {
     Task k;
+    if constexpr (KIND == kRows) {
+        const int splits = *splits_word<EQUAL ? 64 : 128>();
+        const int pair = t % a.pairs;
+        t /= a.pairs;
+        const int split = t % splits;
+        k.bh = t / splits;
+        k.q0 = 2 * pair;
+        const int len = visible_keys(a, k.bh / a.Hkv, false);
+        const int tiles = (len + kTcBN - 1) / kTcBN;
+        const int per = (tiles + splits - 1) / splits;
+        const int first = min(split * per, tiles), last = min(first + per, tiles);
+        k.start = first * kTcBN;
+        k.n = min(len, last * kTcBN) - k.start;
+        // A part without keys visits one tile, all of it masked.
+        k.nbmax = max(last - first, 1);
+        k.nb[0] = k.nbmax;
+        k.nb[1] = EQUAL || k.q0 + 1 < a.tiles ? k.nbmax : 0;
+        return k;
+    } else {
     int qblk;
     k.n = a.N;
     k.start = 0;
-    if constexpr (PACKED) {
+    if constexpr (KIND == kPacked) {
         const PackedPlan* plan = plan_of(a);
         const int blocks = plan->blocks;
         const int per_group = a.head_group * blocks;
@@ -193,6 +254,7 @@ __device__ __forceinline__ Task decode_task(int t, const ArgsOf<PACKED>& a) {
         k.nb[1] = k.nbmax;
     }
     return k;
+    }
 }
 
 // The counter slot of this launch.
@@ -311,16 +373,18 @@ __device__ __forceinline__ void release_task(const TaskRing& r, int kt) {
 }
 
 // Tasks of this launch, and whether a published task is the end of the schedule.
-template <bool PACKED>
-__device__ __forceinline__ int num_tasks_of(const ArgsOf<PACKED>& a) {
-    if constexpr (PACKED)
+template <int D, Kind KIND>
+__device__ __forceinline__ int num_tasks_of(const ArgsOf<KIND>& a) {
+    if constexpr (KIND == kPacked)
         return plan_of(a)->blocks * a.H;
+    else if constexpr (KIND == kRows)
+        return a.sources * a.Hkv * a.pairs * *splits_word<D>();
     else
         return a.num_tasks;
 }
-template <bool PACKED>
-__device__ __forceinline__ bool schedule_ended(int t, const ArgsOf<PACKED>& a) {
-    if constexpr (PACKED)
+template <Kind KIND>
+__device__ __forceinline__ bool schedule_ended(int t, const ArgsOf<KIND>& a) {
+    if constexpr (KIND != kDense)
         return t == static_cast<int>(kEndOfSchedule);
     else
         return t >= a.num_tasks;
@@ -396,9 +460,9 @@ __device__ __forceinline__ void list_blocks(const PackedArgs& a, int4* scratch) 
     }
 }
 
-// Packed: the V rows of a tile behind its sequence's last key (`rows` of the
-// tile belong to it) are those of the next sequence, or whatever the caller
-// keeps behind the last one.  Their weights are 0, but 0 * NaN is not: one warp
+// Packed and rows: the V rows of a tile behind its last key (`rows` of the tile
+// belong to it) are those of the next sequence, or whatever the caller keeps
+// behind the last one (padding, the rest of a page).  Their weights are 0, but 0 * NaN is not: one warp
 // clears them.  Rows of an atom are contiguous (the swizzle stays within a
 // row's 128 bytes).
 template <int D>
@@ -412,24 +476,50 @@ __device__ __forceinline__ void zero_v_tail(uint8_t* tile, int rows) {
     __syncwarp();
 }
 
+// Rows: the box of q that tile i of a task is (a tile past the last one lies
+// behind the last batch entry, where a copy brings zeros).
+struct QBox {
+    int i, h, b;
+};
+__device__ __forceinline__ QBox q_box(const RowsArgs& a, const Task& tk, int i) {
+    const int u = tk.q0 + i, per_b = a.n_h * a.n_i;
+    QBox q;
+    q.i = (u % a.n_i) * a.box_i;
+    q.h = (tk.bh % a.Hkv) * a.share + (u % per_b) / a.n_i * a.box_h;
+    q.b = u < a.tiles ? tk.bh / a.Hkv + u / per_b * a.box_b : a.B;
+    return q;
+}
+
 // ---------------------------------------------------------------------------
-// TMA producer (one warp; one elected lane issues the copies)
+// TMA producer (one warp; one elected lane issues the copies; rows: a lane a piece)
 // ---------------------------------------------------------------------------
-template <int D, bool CAUSAL, bool PACKED>
-__device__ void producer_role(const ArgsOf<PACKED>& a, uint8_t* smem, const Bars& bars,
+template <int D, bool CAUSAL, Kind KIND>
+__device__ void producer_role(const ArgsOf<KIND>& a, uint8_t* smem, const Bars& bars,
                               volatile uint32_t* abort_flag) {
     using L = TcLayout<D>;
     uint32_t kv_it = 0;
     uint32_t qcnt[2] = {0u, 0u};
     bool ok = true;
-    const int num_tasks = num_tasks_of<PACKED>(a);
-    const uint64_t keep = l2_policy_evict_last();   // K/V: re-read by the other Q blocks of the head
+    const int num_tasks = num_tasks_of<D, KIND>(a);
     const uint64_t once = l2_policy_evict_first();  // Q: read once
+    uint64_t keep = l2_policy_evict_last();         // K/V: re-read by the other Q blocks of the head
+    if constexpr (KIND == kRows) {
+        if (a.pairs == 1) keep = once;
+    }
 
     auto load_q = [&](int i, const Task& tk) {
         ok = warp_wait(&bars.q_empty[i], (qcnt[i] & 1u) ^ 1u, abort_flag, a.timeout_ns);
         if (!ok) return;
-        if (elect_one_sync()) {
+        if constexpr (KIND == kRows) {
+            if (elect_one_sync()) {
+                mbar_arrive_expect_tx(&bars.q_full[i], L::kAtoms * a.box_bytes);
+                const QBox q = q_box(a, tk, i);
+#pragma unroll
+                for (int at = 0; at < L::kAtoms; ++at)
+                    tma_load_4d_hint(smem + L::kQOff + i * L::kQTileBytes + at * kTcBM * L::kAtomRowBytes, &a.tmap_q,
+                                     &bars.q_full[i], at * 64, q.i, q.h, q.b, once);
+            }
+        } else if (elect_one_sync()) {
             mbar_arrive_expect_tx(&bars.q_full[i], L::kQTileBytes);
             uint8_t* dst = smem + L::kQOff + i * L::kQTileBytes;
 #pragma unroll
@@ -440,12 +530,40 @@ __device__ void producer_role(const ArgsOf<PACKED>& a, uint8_t* smem, const Bars
         __syncwarp();
         ++qcnt[i];
     };
-    auto load_kv = [&](const CUtensorMap* map, int j, int kvh, int start) {
+    // Rows: this lane's piece of the K/V tiles, and its page of tile j (a page that
+    // is none lies outside the pool, where a copy brings zeros).
+    auto page_of = [&](const Task& tk, int j) -> int {
+        if constexpr (KIND == kRows) {
+            const int key = tk.start + j * kTcBN + static_cast<int>(threadIdx.x % 32) * a.piece;
+            if (a.table == nullptr || j >= tk.nbmax || key >= tk.start + min(tk.n, (j + 1) * kTcBN)) return a.num_pages;
+            const int page = a.table[key / a.page_size];
+            if (static_cast<uint32_t>(page) < static_cast<uint32_t>(a.num_pages)) return page;
+            atomicOr(&g_error_word, 1u << kDevErrInvalidArg);
+            return a.num_pages;
+        } else {
+            return 0;
+        }
+    };
+    auto load_kv = [&](const CUtensorMap* map, int j, int kvh, const Task& tk, int page) {
+        const int start = tk.start;
         const uint32_t slot = kv_it % L::kStages;
         const uint32_t round = kv_it / L::kStages;
         ok = warp_wait(&bars.kv_empty[slot], (round & 1u) ^ 1u, abort_flag, a.timeout_ns);
         if (!ok) return;
-        if (elect_one_sync()) {
+        if constexpr (KIND == kRows) {
+            if (elect_one_sync()) mbar_arrive_expect_tx(&bars.kv_full[slot], L::kKVTileBytes);
+            __syncwarp();
+            uint8_t* dst = smem + L::kKVOff + slot * L::kKVTileBytes;
+            const int lane = threadIdx.x % 32, row = lane * a.piece;
+            if (row < kTcBN) {
+                const int key = start + j * kTcBN + row;
+#pragma unroll
+                for (int at = 0; at < L::kAtoms; ++at)
+                    tma_load_4d_hint(dst + at * kTcBN * L::kAtomRowBytes + row * L::kAtomRowBytes, map,
+                                     &bars.kv_full[slot], at * 64, a.table ? key % a.page_size : key, kvh,
+                                     a.table ? page : tk.bh / a.Hkv, keep);
+            }
+        } else if (elect_one_sync()) {
             mbar_arrive_expect_tx(&bars.kv_full[slot], L::kKVTileBytes);
             uint8_t* dst = smem + L::kKVOff + slot * L::kKVTileBytes;
 #pragma unroll
@@ -491,19 +609,22 @@ __device__ void producer_role(const ArgsOf<PACKED>& a, uint8_t* smem, const Bars
             break;
         }
         if (!publish(kt, t)) break;
-        const Task tk = decode_task<CAUSAL, L::kRot, PACKED>(t, a);
-        const int kvh = kv_head_of(tk.bh, a.H, a.Hkv);
+        const Task tk = decode_task<CAUSAL, L::kRot, KIND>(t, a);
+        const int kvh = KIND == kRows ? tk.bh % a.Hkv : kv_head_of(tk.bh, a.H, a.Hkv);
+        int page = page_of(tk, 0);
         load_q(0, tk);
         if (!ok) break;
-        load_kv(&a.tmap_k, 0, kvh, tk.start);
+        load_kv(&a.tmap_k, 0, kvh, tk, page);
         if (!ok) break;
         if (tk.nb[1] > 0) {
             load_q(1, tk);
             if (!ok) break;
         }
         for (int j = 0; j < tk.nbmax && ok; ++j) {
-            load_kv(&a.tmap_v, j, kvh, tk.start);
-            if (ok && j + 1 < tk.nbmax) load_kv(&a.tmap_k, j + 1, kvh, tk.start);
+            const int next_page = page_of(tk, j + 1);
+            load_kv(&a.tmap_v, j, kvh, tk, page);
+            if (ok && j + 1 < tk.nbmax) load_kv(&a.tmap_k, j + 1, kvh, tk, next_page);
+            page = next_page;
         }
         if (!ok) break;
         // The next task is taken only now, a few K/V tiles before this CTA
@@ -513,7 +634,15 @@ __device__ void producer_role(const ArgsOf<PACKED>& a, uint8_t* smem, const Bars
         // done; fetched into L2 now, they land in shared memory at L2 latency.
         t = fetch();
         if (t < num_tasks && elect_one_sync()) {
-            const Task nx = decode_task<CAUSAL, L::kRot, PACKED>(t, a);
+            const Task nx = decode_task<CAUSAL, L::kRot, KIND>(t, a);
+            if constexpr (KIND == kRows) {
+                for (int i = 0; i < 2; ++i) {
+                    const QBox q = q_box(a, nx, i);
+                    if (nx.q0 + i < a.tiles)
+#pragma unroll
+                        for (int at = 0; at < L::kAtoms; ++at) tma_prefetch_4d(&a.tmap_q, at * 64, q.i, q.h, q.b);
+                }
+            } else
 #pragma unroll
             for (int i = 0; i < 2; ++i)
                 if (nx.q0 + i * kTcBM < nx.n)
@@ -564,8 +693,8 @@ __device__ __forceinline__ uint32_t p_bar(int tile, int j) {
     return kPBar + 2u * static_cast<uint32_t>(tile) + (static_cast<uint32_t>(j) & 1u);
 }
 
-template <int D, bool BF16, bool CAUSAL, bool HELPER, bool PACKED>
-__device__ void mma_pair_role(const ArgsOf<PACKED>& a, uint8_t* smem, const Bars& bars, uint32_t tmem_base,
+template <int D, bool BF16, bool CAUSAL, bool HELPER, Kind KIND>
+__device__ void mma_pair_role(const ArgsOf<KIND>& a, uint8_t* smem, const Bars& bars, uint32_t tmem_base,
                               volatile uint32_t* abort_flag) {
     using L = TcLayout<D>;
     static_assert(!L::kRot, "the three-buffer layout has its own MMA role");
@@ -670,8 +799,8 @@ __device__ void mma_pair_role(const ArgsOf<PACKED>& a, uint8_t* smem, const Bars
 
     for (int kt = 0;; ++kt) {
         const int t = next_task(kt);
-        if (schedule_ended<PACKED>(t, a)) break;
-        const Task tk = decode_task<CAUSAL, false, PACKED>(t, a);
+        if (schedule_ended<KIND>(t, a)) break;
+        const Task tk = decode_task<CAUSAL, false, KIND>(t, a);
         uint32_t kslot, vslot;
         // Prologue: S_0(0), S_1(0).
         wait_q(0);
@@ -697,7 +826,7 @@ __device__ void mma_pair_role(const ArgsOf<PACKED>& a, uint8_t* smem, const Bars
         for (int j = 0; j < tk.nbmax; ++j) {
             const bool has_next = j + 1 < tk.nbmax;
             wait_kv(vslot);                  // V_j
-            if (PACKED && HELPER && ok)
+            if (KIND != kDense && HELPER && ok)
                 zero_v_tail<D>(smem + L::kKVOff + vslot * L::kKVTileBytes, tk.n - j * kTcBN);
             if (has_next) wait_kv(kslot);    // K_{j+1}
             sync();
@@ -758,8 +887,8 @@ __device__ void mma_pair_role(const ArgsOf<PACKED>& a, uint8_t* smem, const Bars
 // s_full[b * 2 + i] has one waiting warpgroup (tile i), which sees every phase;
 // the MMA warp takes P in product order on the kPBar named barriers.
 
-template <bool BF16, bool CAUSAL, bool HELPER, bool PACKED>
-__device__ void mma_pair_role_rot(const ArgsOf<PACKED>& a, uint8_t* smem, const Bars& bars, uint32_t tmem_base,
+template <bool BF16, bool CAUSAL, bool HELPER, Kind KIND>
+__device__ void mma_pair_role_rot(const ArgsOf<KIND>& a, uint8_t* smem, const Bars& bars, uint32_t tmem_base,
                                   volatile uint32_t* abort_flag) {
     // Issuing warp and helper warp as in mma_pair_role: the helper does every
     // mbarrier wait and meets the issuing warp on the named barrier kMmaSync;
@@ -831,8 +960,8 @@ __device__ void mma_pair_role_rot(const ArgsOf<PACKED>& a, uint8_t* smem, const 
 
     for (int kt = 0;; ++kt) {
         const int t = next_task(kt);
-        if (schedule_ended<PACKED>(t, a)) break;
-        const Task tk = decode_task<CAUSAL, true, PACKED>(t, a);
+        if (schedule_ended<KIND>(t, a)) break;
+        const Task tk = decode_task<CAUSAL, true, KIND>(t, a);
         const int nb = tk.nbmax;
         // Prologue: S_0(0), S_1(0), S_0(1).
         wait_q(0);
@@ -858,7 +987,7 @@ __device__ void mma_pair_role_rot(const ArgsOf<PACKED>& a, uint8_t* smem, const 
         for (int j = 0; j < nb; ++j) {
             const uint32_t k0 = sbase + 2u * j;
             const uint32_t vs = wait_pos(kv_base + 2u * j + 1u);  // V_j
-            if (PACKED && HELPER && ok)
+            if (KIND != kDense && HELPER && ok)
                 zero_v_tail<D>(smem + L::kKVOff + vs * L::kKVTileBytes, tk.n - j * kTcBN);
             uint32_t ks2 = 0;                                     // K_{j+2}
             if (j + 2 < nb) ks2 = wait_pos(kv_base + 2u * (j + 2));
@@ -913,8 +1042,8 @@ __device__ void mma_pair_role_rot(const ArgsOf<PACKED>& a, uint8_t* smem, const 
 // as the ring delivers them -- waiting on nothing else, so that the issuing
 // warp, which runs the same schedule to its end, meets every barrier it
 // waits on (see kPBar).
-template <bool CAUSAL, bool EQUAL, bool PACKED>
-__device__ __noinline__ void softmax_dry_tail(const ArgsOf<PACKED>& a, TaskRing tasks, int tile, int j0,
+template <bool CAUSAL, bool EQUAL, Kind KIND>
+__device__ __noinline__ void softmax_dry_tail(const ArgsOf<KIND>& a, TaskRing tasks, int tile, int j0,
                                               int nb0, int kt1, volatile uint32_t* abort_flag) {
     for (int j = j0; j < nb0; ++j) {
         __syncwarp();
@@ -922,9 +1051,9 @@ __device__ __noinline__ void softmax_dry_tail(const ArgsOf<PACKED>& a, TaskRing 
     }
     for (int kt = kt1;; ++kt) {
         const int t = read_task(tasks, kt, abort_flag, a.timeout_ns);
-        if (schedule_ended<PACKED>(t, a)) break;
+        if (schedule_ended<KIND>(t, a)) break;
         release_task(tasks, kt);
-        const Task tk = decode_task<CAUSAL, EQUAL, PACKED>(t, a);
+        const Task tk = decode_task<CAUSAL, EQUAL, KIND>(t, a);
         for (int j = 0; j < tk.nb[tile]; ++j) {
             __syncwarp();
             named_barrier_arrive(p_bar(tile, j), kPBarThreads);
@@ -932,8 +1061,8 @@ __device__ __noinline__ void softmax_dry_tail(const ArgsOf<PACKED>& a, TaskRing 
     }
 }
 
-template <int D, bool BF16, bool CAUSAL, bool PACKED>
-__device__ void softmax_role(const ArgsOf<PACKED>& a, const Bars& bars, uint32_t tmem_base,
+template <int D, bool BF16, bool CAUSAL, Kind KIND>
+__device__ void softmax_role(const ArgsOf<KIND>& a, const Bars& bars, uint32_t tmem_base,
                              volatile uint32_t* abort_flag) {
     constexpr bool kRot = TcLayout<D>::kRot;  // D = 64: three rotating S buffers
     const int warp = threadIdx.x / 32;
@@ -951,9 +1080,9 @@ __device__ void softmax_role(const ArgsOf<PACKED>& a, const Bars& bars, uint32_t
     uint32_t sbase = 0;    // D = 64: S products of both tiles in earlier tasks
     for (int kt = 0;; ++kt) {
         const int t = read_task(bars.tasks, kt, abort_flag, a.timeout_ns);
-        if (schedule_ended<PACKED>(t, a)) break;
+        if (schedule_ended<KIND>(t, a)) break;
         release_task(bars.tasks, kt);
-        const Task tk = decode_task<CAUSAL, kRot, PACKED>(t, a);
+        const Task tk = decode_task<CAUSAL, kRot, KIND>(t, a);
         const int nb = tk.nb[tile];
         if constexpr (!kRot) {
             if (nb == 0) continue;  // tile past N (the three-buffer layout computes it anyway)
@@ -963,7 +1092,7 @@ __device__ void softmax_role(const ArgsOf<PACKED>& a, const Bars& bars, uint32_t
         // keys < lim are visible to this row (packed causal: a row that is
         // stored lies below n, so row + 1 alone bounds it, and n need not be
         // kept in a register of its own)
-        const int lim = CAUSAL ? (PACKED ? row + 1 : min(row + 1, tk.n)) : tk.n;
+        const int lim = CAUSAL ? (KIND == kPacked ? row + 1 : min(row + 1, tk.n)) : tk.n;
 
         float m_run = -INFINITY;  // running max of scale*log2(e)*s
         // bf16: O is normalised by the running sum of the 16-bit P values fed
@@ -991,7 +1120,7 @@ __device__ void softmax_role(const ArgsOf<PACKED>& a, const Bars& bars, uint32_t
             const bool ok = warp_wait(&bars.s_full[kRot ? b * 2 + tile : b], use & 1u, abort_flag,
                                       a.timeout_ns);
             if (!ok) {
-                softmax_dry_tail<CAUSAL, kRot, PACKED>(a, bars.tasks, tile, j, nb, kt + 1, abort_flag);
+                softmax_dry_tail<CAUSAL, kRot, KIND>(a, bars.tasks, tile, j, nb, kt + 1, abort_flag);
                 return;
             }
             tc_fence_after();
@@ -1015,7 +1144,7 @@ __device__ void softmax_role(const ArgsOf<PACKED>& a, const Bars& bars, uint32_t
 
             const int kb = j * kTcBN;
             const bool need_mask =
-                (!(CAUSAL && PACKED) && kb + kTcBN > tk.n) || (CAUSAL && kb + kTcBN - 1 > row0);
+                (!(CAUSAL && KIND == kPacked) && kb + kTcBN > tk.n) || (CAUSAL && kb + kTcBN - 1 > row0);
             float mblk = fmaxf(fmaxf(cmx[0], cmx[1]), fmaxf(cmx[2], cmx[3]));
             if (need_mask) {
                 // Keys past N or past the row: masked here, and the row max
@@ -1048,7 +1177,7 @@ __device__ void softmax_role(const ArgsOf<PACKED>& a, const Bars& bars, uint32_t
                         // (at D = 128 the commit of S_i(j) already implies it).
                         if (!warp_wait(&bars.o_ready[tile], (pv_base + j - 1) & 1u, abort_flag,
                                        a.timeout_ns)) {
-                            softmax_dry_tail<CAUSAL, kRot, PACKED>(a, bars.tasks, tile, j, nb, kt + 1,
+                            softmax_dry_tail<CAUSAL, kRot, KIND>(a, bars.tasks, tile, j, nb, kt + 1,
                                                            abort_flag);
                             return;
                         }
@@ -1120,18 +1249,56 @@ __device__ void softmax_role(const ArgsOf<PACKED>& a, const Bars& bars, uint32_t
         const bool ok = warp_wait(&bars.o_full[tile], ocnt & 1u, abort_flag, a.timeout_ns);
         ++ocnt;
         if (!ok) {
-            softmax_dry_tail<CAUSAL, kRot, PACKED>(a, bars.tasks, tile, 0, 0, kt + 1, abort_flag);
+            softmax_dry_tail<CAUSAL, kRot, KIND>(a, bars.tasks, tile, 0, 0, kt + 1, abort_flag);
             return;
         }
         tc_fence_after();
-        const float inv_l = 1.f / (kRoundedSum ? l_run : l_exact);
+        float inv_l = 1.f / (kRoundedSum ? l_run : l_exact);
         bool valid;
         uint8_t* orow = reinterpret_cast<uint8_t*>(a.o);
         int64_t lse_at;
-        if constexpr (PACKED) {
+        if constexpr (KIND == kRows) {
+            const Task te = decode_task<CAUSAL, kRot, KIND>(t, a);
+            const int u = te.q0 + tile, source = te.bh / a.Hkv, kvh = te.bh % a.Hkv;
+            if (!(l_exact > 0.f) && m_run == -INFINITY) inv_l = 0.f;  // no key: O = 0, and its part weighs nothing
+            RowPlace r;
+            valid = row_place(a, source, u, trow, r);
+            if (a.part_o != nullptr) {
+                // A part: the sum of values not yet divided, by the weights' unrounded sum.
+                const int split = t / a.pairs % *splits_word<D>();
+                const int64_t at = ((static_cast<int64_t>(te.bh) * a.tiles + u) * kTcBM + trow) * a.part_pitch + split;
+                const float f = inv_l * l_exact;
+                float* dst = a.part_o + at * D;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t x[32];
+                    tmem_ld32(tO + c * 32, x);
+                    tmem_wait_ld();
+                    reg_fence(x);
+                    if (valid) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            __stcg(reinterpret_cast<float4*>(dst + c * 32 + e),
+                                   make_float4(__uint_as_float(x[e]) * f, __uint_as_float(x[e + 1]) * f,
+                                               __uint_as_float(x[e + 2]) * f, __uint_as_float(x[e + 3]) * f));
+                    }
+                }
+                if (valid) __stcg(a.part_ml + at, make_float2(m_run, l_exact));
+                tc_fence_before();
+                if constexpr (kRot) {
+                    pv_base += static_cast<uint32_t>(nb);
+                    sbase += static_cast<uint32_t>(tk.nb[0] + tk.nb[1]);
+                }
+                continue;
+            }
+            const int h = kvh * a.share + r.h;
+            orow += 2 * (r.b * a.o_bs + h * a.o_hs + r.i * a.o_ns);
+            lse_at = (static_cast<int64_t>(r.b) * a.H + h) * a.Nq + r.i;
+        } else
+        if constexpr (KIND == kPacked) {
             // Decoded again: its fields would otherwise hold registers through
             // the loop above, which needs a whole score row in them.
-            const Task te = decode_task<CAUSAL, kRot, PACKED>(t, a);
+            const Task te = decode_task<CAUSAL, kRot, KIND>(t, a);
             const int r = te.q0 + tile * kTcBM + trow;
             valid = r < te.n;
             orow += 2 * (static_cast<int64_t>(te.start + r) * a.o_ts + static_cast<int64_t>(te.bh) * a.o_hs);
@@ -1169,8 +1336,8 @@ __device__ void softmax_role(const ArgsOf<PACKED>& a, const Bars& bars, uint32_t
     }
 }
 
-template <int D, bool BF16, bool CAUSAL, bool PACKED>
-__global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_tc_kernel(const __grid_constant__ ArgsOf<PACKED> a) {
+template <int D, bool BF16, bool CAUSAL, Kind KIND>
+__global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_tc_kernel(const __grid_constant__ ArgsOf<KIND> a) {
     using L = TcLayout<D>;
     // 128-byte-swizzled TMA destinations and MMA operands need 1024-byte
     // aligned tiles.  Should the runtime ever place the dynamic window
@@ -1212,7 +1379,26 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_tc_kernel(const __grid
         tmem_alloc(misc, L::kTmemCols);
         tmem_relinquish();
     }
-    if constexpr (PACKED) {
+    if constexpr (KIND == kRows) {
+        grid_dependency();
+        if (warp == 0) {
+            int splits = a.splits;
+            if (splits == 0) {
+                // From the length, which only the device knows: the cheapest of what the workspace has room for.
+                const int tiles = (visible_keys(a, 0, blockIdx.x == 0 && lane == 0) + kTcBN - 1) / kTcBN;
+                const int targets = a.sources * a.Hkv * a.pairs;
+                uint32_t best = 0xffffffffu;
+                for (int s = lane + 1; s <= a.part_pitch; s += 32)
+                    best = min(best, split_cost(targets, tiles, gridDim.x, s) * 256u + static_cast<uint32_t>(s));
+                splits = static_cast<int>(__reduce_min_sync(0xffffffffu, best) % 256u);
+                if (blockIdx.x == 0 && lane == 0) *a.part_count = splits;
+            } else if (a.lens != nullptr && blockIdx.x == 0) {
+                for (int b = lane; b < a.sources; b += 32) visible_keys(a, b, true);
+            }
+            if (lane == 0) *splits_word<D>() = splits;
+        }
+    }
+    if constexpr (KIND == kPacked) {
         // Waits for the kernel before it on the stream (the one that writes the
         // list, where that is a launch of its own).
         grid_dependency();
@@ -1234,23 +1420,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_tc_kernel(const __grid
 
     if (warp < 8) {
         regs_increase<kSoftmaxRegs>();
-        softmax_role<D, BF16, CAUSAL, PACKED>(a, bars, tmem_base, abort_flag);
+        softmax_role<D, BF16, CAUSAL, KIND>(a, bars, tmem_base, abort_flag);
     } else {
         regs_decrease<kControlRegs>();
         if (warp == 8 || warp == 10) {  // the issuing warp and its helper
             if constexpr (L::kRot) {
                 if (warp == 8)
-                    mma_pair_role_rot<BF16, CAUSAL, false, PACKED>(a, smem, bars, tmem_base, abort_flag);
+                    mma_pair_role_rot<BF16, CAUSAL, false, KIND>(a, smem, bars, tmem_base, abort_flag);
                 else
-                    mma_pair_role_rot<BF16, CAUSAL, true, PACKED>(a, smem, bars, tmem_base, abort_flag);
+                    mma_pair_role_rot<BF16, CAUSAL, true, KIND>(a, smem, bars, tmem_base, abort_flag);
             } else {
                 if (warp == 8)
-                    mma_pair_role<D, BF16, CAUSAL, false, PACKED>(a, smem, bars, tmem_base, abort_flag);
+                    mma_pair_role<D, BF16, CAUSAL, false, KIND>(a, smem, bars, tmem_base, abort_flag);
                 else
-                    mma_pair_role<D, BF16, CAUSAL, true, PACKED>(a, smem, bars, tmem_base, abort_flag);
+                    mma_pair_role<D, BF16, CAUSAL, true, KIND>(a, smem, bars, tmem_base, abort_flag);
             }
         } else if (warp == 9) {
-            producer_role<D, CAUSAL, PACKED>(a, smem, bars, abort_flag);
+            producer_role<D, CAUSAL, KIND>(a, smem, bars, abort_flag);
         }
     }
     __syncwarp();

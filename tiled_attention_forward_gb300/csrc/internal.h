@@ -110,6 +110,53 @@ constexpr int kSmallPlanBytes = 16 * (1 + kSmallPlan);
 cudaError_t packed_launch(const PackedArgs& a, int D, bool bf16, bool causal, int capacity, int grid, cudaStream_t s);
 cudaError_t packed_read_and_clear_error_word(uint32_t* out);
 
+// ---- rows over keys of a length of their own, on the tensor-core path -------------
+// (fwd_rows.cu: cross attention, and the prefix that a batch shares)
+struct RowsArgs : TcArgs {  // N, BH, num_qblk, num_tasks and head_group are unused
+    // tmap_q: {D, Nq, H, B}, box {64, box_i, box_h, box_b}, a tile's rows in that
+    // order (at most 128).  tmap_k, tmap_v: {D, keys, Hkv, sources}, or {D,
+    // page_size, Hkv, pages} with a table; box {64, piece, 1, 1}.
+    int64_t o_bs, o_hs, o_ns;  // batch, head and token stride of o, elements
+    const int32_t* lens;       // keys of each source, or nullptr: max_keys
+    const int32_t* table;      // pages of the one source's keys, or nullptr
+    float* part_o;             // fp32 [sources][Hkv][tiles][128][part_pitch][D], or nullptr: O and LSE are written
+    float2* part_ml;           // .. [part_pitch]: max (log2 units) and sum of the weights
+    int32_t* part_count;       // receives the parts of a launch that chooses them itself
+    int part_pitch;            // parts that the workspace has room for
+    int splits;                // parts that the keys are cut into; 0: chosen by the length
+    int num_pages;
+    int page_size;
+    int piece;                 // keys of a copy
+    int max_keys;
+    int sources;               // batch entries with keys of their own, or 1
+    int B;
+    int Nq;
+    int share;                 // query heads of a K/V head
+    int box_i, box_h, box_b;   // tokens, heads, batch entries of a tile
+    uint32_t box_bytes;        // of the tile's 64-element columns
+    int n_i, n_h;              // tiles along tokens and heads
+    int tiles;                 // tiles of a K/V head of a source
+    int pairs;                 // ceil(tiles / 2)
+};
+// What cutting the keys of `targets` tasks of `tiles` K/V tiles into s parts costs:
+// a task takes as long as its tiles and two more (its start and its epilogue), and
+// each part is read again when they are joined.
+__host__ __device__ inline uint32_t split_cost(int targets, int tiles, int ctas, int s) {
+    const int64_t waves = (static_cast<int64_t>(targets) * s + ctas - 1) / ctas;
+    const int64_t cost = 16 * waves * ((tiles + s - 1) / s + 2) + s;
+    return cost > 0xffffff ? 0xffffffu : static_cast<uint32_t>(cost);
+}
+constexpr int kMaxSplits = 128;
+constexpr int kSplitCtas = 152;  // CTAs that workspaces are sized for
+// Parts that `targets` tasks may be cut into: two waves of tasks.
+inline int max_splits(int64_t targets) {
+    const int64_t n = 2 * kSplitCtas / (targets > 0 ? targets : 1);
+    return static_cast<int>(n < 1 ? 1 : (n > kMaxSplits ? kMaxSplits : n));
+}
+cudaError_t rows_launch(const RowsArgs& a, int D, bool bf16, int grid, cudaStream_t s);
+cudaError_t rows_join_launch(const RowsArgs& a, int D, bool bf16, cudaStream_t s);
+cudaError_t rows_read_and_clear_error_word(uint32_t* out);
+
 // ---- CUDA-core path (fp32), fwd_ffma.cu --------------------------------------
 constexpr int kFfmaBr = 128;      // Q rows per CTA
 int ffma_bc(int D);               // keys per K/V tile
@@ -181,6 +228,41 @@ cudaError_t bwd_launch(const BwdArgs& a, const void* o, const void* dout, const 
                        bool bf16, bool causal, cudaStream_t s);
 cudaError_t bwd_read_and_clear_error_word(uint32_t* out);
 
+struct CrossBwdArgs : BwdArgs {  // tmaps {D, Nq or Nk, heads, B}; N = Nq, num_tiles = Npad / 128
+    int Nk;
+    int tiles_k;               // ceil(Nk / 128)
+    const int32_t* lens;       // visible keys of each batch entry, or nullptr: Nk
+    int64_t dq_bs, dq_hs, dq_ns, dk_bs, dk_hs, dk_ns, dv_bs, dv_hs, dv_ns;  // element strides
+    const void* o;             // the row statistics' inputs, by strides
+    const void* dout;
+    const float* lse;
+    int64_t o_bs, o_hs, o_ns, do_bs, do_hs, do_ns;
+};
+cudaError_t bwd_cross_launch(const CrossBwdArgs& a, int D, bool bf16, cudaStream_t s);
+cudaError_t bwd_cross_read_and_clear_error_word(uint32_t* out);
+
+// ---- rotation by positions with several axes, rotate.cu ----------------------------
+constexpr int kMaxAxes = 8;
+struct RotateArgs {
+    const void* x[2];      // q and k [B][heads][N][D] by strides (k: or nullptr)
+    void* y[2];
+    int64_t x_bs[2], x_hs[2], x_ns[2], y_bs[2], y_hs[2], y_ns[2];
+    int heads[2];
+    const int32_t* pos;    // [axes][B][N]
+    const float* cos;      // [max_pos][rot/2]
+    const float* sin;
+    int64_t max_pos;
+    int64_t tokens;        // B * N
+    int N;
+    int rot;
+    int interleaved;
+    int inverse;
+    int axes;
+    alignas(8) uint8_t axis[64];  // of each pair
+};
+cudaError_t rotate_launch(const RotateArgs& a, int D, bool bf16, int sms, cudaStream_t s);
+cudaError_t rotate_read_and_clear_error_word(uint32_t* out);
+
 // ---- paged cache: append (cache_append.cu) and attention (decode.cu) --------
 constexpr uint32_t kDevErrInvalidArg = 1u;  // error-word bit: an index in device memory is out of range
 constexpr int kKv4Group = 32;               // elements of a 4-bit row that share one scale and zero
@@ -216,6 +298,8 @@ struct AppendArgs {
     uint32_t kv_tokens;
     uint32_t q_tokens;
     int apart;            // 4-bit: key rows and value rows have blocks of their own; likewise
+    int axes;             // 0: pos is [T]; else [axes][T], and pair i turns by the position on axis[i]
+    uint8_t axis[64];
 };
 cudaError_t append_launch(AppendArgs a, int D, bool bf16, bool kv4, int sms, cudaStream_t s);
 cudaError_t append_read_and_clear_error_word(uint32_t* out);
@@ -242,6 +326,21 @@ struct DecodeArgs {
     int Nq;
     float scale_log2;
 };
+struct SharedDecodeArgs : DecodeArgs {  // the parts of the prefix, as RowsArgs has them (one source)
+    const float* part_o;
+    const float2* part_ml;
+    const int32_t* part_count;
+    int part_pitch;
+    int box_i, box_h, box_b, n_i, n_h, tiles;
+};
+struct CrossDecodeArgs : DecodeArgs {  // k_pages and v_pages: [B][Nk][Hkv][D] by strides; seq_lens may be nullptr
+    int64_t k_bs, k_hs, k_ns, v_bs, v_hs, v_ns;
+    int Nk;
+};
+cudaError_t decode_shared_launch(const SharedDecodeArgs& a, int D, bool bf16, int sms, cudaStream_t s);
+cudaError_t decode_shared_read_and_clear_error_word(uint32_t* out);
+cudaError_t decode_cross_launch(const CrossDecodeArgs& a, int D, bool bf16, int sms, cudaStream_t s);
+cudaError_t decode_cross_read_and_clear_error_word(uint32_t* out);
 cudaError_t decode_launch(const DecodeArgs& a, int D, bool bf16, bool kv4, int sms, cudaStream_t s);
 int64_t decode_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t D);
 cudaError_t decode_read_and_clear_error_word(uint32_t* out);
