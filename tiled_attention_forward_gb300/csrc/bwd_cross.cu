@@ -86,13 +86,16 @@ cudaError_t launch_all(const CrossBwdArgs& a, cudaStream_t s) {
     auto* kkv = attn_bwd_kernel<D, BF16, true, false, true>;
     if ((e = opt_in_smem_once(kkv, BwdLayout<D, true>::kBytes, kv_done)) != cudaSuccess) return e;
     if (a.tiles_k > 0) {
-        kkv<<<static_cast<unsigned>(a.tiles_k * a.BHkv), kBwdThreads, BwdLayout<D, true>::kBytes, s>>>(a);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        e = launch_overlapped(kkv, static_cast<unsigned>(a.tiles_k * a.BHkv), kBwdThreads, BwdLayout<D, true>::kBytes, s, a);
+        if (e != cudaSuccess) return e;
     }
     if (a.num_tiles == 0) return cudaSuccess;
     auto* kq = attn_bwd_kernel<D, BF16, false, false, true>;
     if ((e = opt_in_smem_once(kq, BwdLayout<D, false>::kBytes, q_done)) != cudaSuccess) return e;
-    kq<<<static_cast<unsigned>(a.num_tiles * a.BH), kBwdThreads, BwdLayout<D, false>::kBytes, s>>>(a);
+    const unsigned grid_q = static_cast<unsigned>(a.num_tiles * a.BH);
+    // (Behind the key kernel only: it reads and writes without waiting first.)
+    if (a.tiles_k > 0) return launch_overlapped(kq, grid_q, kBwdThreads, BwdLayout<D, false>::kBytes, s, a);
+    kq<<<grid_q, kBwdThreads, BwdLayout<D, false>::kBytes, s>>>(a);
     return cudaGetLastError();
 }
 

@@ -288,16 +288,25 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_kernel(const __grid_c
     extern __shared__ __align__(1024) uint8_t smem[];
     if ((smem_u32(smem) & 1023u) != 0u) {
         if (threadIdx.x == 0) atomicOr(&g_error_word, 1u << kDevErrInternal);
+        if constexpr (CROSS) asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
     }
     const BwdBars bars = bwd_bars<D, KV>(smem);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    // Cross: the key kernel waits for the row statistics and lets the query kernel
+    // start while its own last CTAs run, which reads nothing of it (and what it
+    // reads is complete once all CTAs here have passed); that one's end waits for it.
+    if constexpr (CROSS && KV) grid_dependency();
+    auto wait_key_kernel = [&]() {
+        if constexpr (CROSS && !KV) asm volatile("griddepcontrol.wait;" ::: "memory");
+    };
     int keys = a.N;  // keys that the task sees
     if constexpr (CROSS) keys = bwd_visible_keys<KV>(a);
     const BwdTask tk = bwd_task<KV, CAUSAL, CROSS>(a, keys);
     if constexpr (CROSS) {
         if (tk.n == 0) {
             bwd_store_zeros<D, KV>(a, tk);
+            wait_key_kernel();
             return;
         }
     }
@@ -837,6 +846,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_kernel(const __grid_c
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
+    wait_key_kernel();
 }
 
 }  // namespace

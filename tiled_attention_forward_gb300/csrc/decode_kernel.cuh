@@ -60,10 +60,16 @@ namespace {
 // the error word of its own kernels.
 __device__ uint32_t g_decode_error_word;
 
-enum Mode { kCache, kBehindPrefix, kCross };
+//   kBehindPrefix: writes its rows as a part, beside those of the prefix.
+//   kWithPrefix: every sequence reads the prefix for itself.  Its keys come first,
+//   up to a whole unit of virtual keys (those behind its last are masked), then the
+//   sequence's own.
+enum Mode { kCache, kBehindPrefix, kWithPrefix, kCross };
 template <Mode MODE>
-using DecodeArgsOf =
-    std::conditional_t<MODE == kCross, CrossDecodeArgs, std::conditional_t<MODE == kBehindPrefix, SharedDecodeArgs, DecodeArgs>>;
+using DecodeArgsOf = std::conditional_t<
+    MODE == kCross, CrossDecodeArgs,
+    std::conditional_t<MODE == kBehindPrefix, SharedDecodeArgs,
+                       std::conditional_t<MODE == kWithPrefix, PrefixDecodeArgs, DecodeArgs>>>;
 
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kWarps = 8;
@@ -235,6 +241,30 @@ __device__ __forceinline__ int cta_of(int64_t unit, int64_t units, int ctas) {
     return c;
 }
 
+// What an earlier kernel may have written; behind a prefix, whose kernel this one
+// may start beside, from L2.
+template <typename ARGS, typename T>
+__device__ __forceinline__ T read(const T* p) {
+    if constexpr (std::is_same_v<ARGS, SharedDecodeArgs>)
+        return __ldcg(p);
+    else
+        return *p;
+}
+
+// The prefix's keys, and the virtual keys that they take.
+struct Prefix {
+    int keys, end;
+};
+__device__ __forceinline__ Prefix prefix_of(const PrefixDecodeArgs& a, bool report) {
+    int len = *a.prefix_len;
+    if (len < 0 || len > a.prefix_max) {
+        if (report) atomicOr(&g_decode_error_word, 1u << kDevErrInvalidArg);
+        len = len < 0 ? 0 : a.prefix_max;
+    }
+    constexpr int kUnit = Stage<128, false, 1>::kUnit;  // of all 16-bit stages
+    return {len, (len + kUnit - 1) / kUnit * kUnit};
+}
+
 template <typename ARGS>
 __device__ __forceinline__ int visible_len(const ARGS& a, int b, bool report) {
     if constexpr (std::is_same_v<ARGS, CrossDecodeArgs>) {
@@ -246,8 +276,11 @@ __device__ __forceinline__ int visible_len(const ARGS& a, int b, bool report) {
         }
         return len;
     }
+    if constexpr (std::is_same_v<ARGS, PrefixDecodeArgs>) {
+        return prefix_of(a, false).end + visible_len(static_cast<const DecodeArgs&>(a), b, report);
+    }
     const int64_t most = a.table_width * a.page_size;
-    const int len = a.seq_lens[b];
+    const int len = read<ARGS>(a.seq_lens + b);
     if (len < 0 || len > most) {
         if (report) atomicOr(&g_decode_error_word, 1u << kDevErrInvalidArg);
         return len < 0 ? 0 : static_cast<int>(most);
@@ -262,45 +295,23 @@ __device__ __forceinline__ int units_of(int len) {
 // Writes 4 dims of one query row (of K/V head kvh) from its unnormalised sum: 4
 // bits, of half the values (Warp::accumulate), whose mean may lie a little past
 // fp16's range, as the values do.
-// Behind a prefix: the prefix's parts of the row are joined to it first.
+// Behind a prefix: as the last part of the row, which is joined to the prefix's.
 template <int D, bool BF16, bool KV4, typename ARGS>
-__device__ __forceinline__ void store_out(const ARGS& a, int b, int kvh, int row, int d, const float (&own)[4],
+__device__ __forceinline__ void store_out(const ARGS& a, int b, int kvh, int row, int d, const float (&acc)[4],
                                           float mx, float sum) {
     const int share = a.H / a.Hkv;
     if (row >= share * a.Nq) return;
     const int h = kvh * share + row / a.Nq, i = row % a.Nq;
-    float acc[4] = {own[0], own[1], own[2], own[3]};
     if constexpr (std::is_same_v<ARGS, SharedDecodeArgs>) {
         const int hq = row / a.Nq;
         const int u = (b / a.box_b * a.n_h + hq / a.box_h) * a.n_i + i / a.box_i;
         const int trow = ((b % a.box_b) * a.box_h + hq % a.box_h) * a.box_i + i % a.box_i;
-        const int64_t at = ((static_cast<int64_t>(kvh) * a.tiles + u) * kTcBM + trow) * a.part_pitch;
-        const int parts = __ldcg(a.part_count);
-        const float2* ml = a.part_ml + at;
-        const float4* po = reinterpret_cast<const float4*>(a.part_o + at * D + d);
-        constexpr int kAtOnce = 4;
-        for (int y0 = 0; y0 < parts; y0 += kAtOnce) {
-            float2 w[kAtOnce];
-            float4 v[kAtOnce];
-#pragma unroll
-            for (int y = 0; y < kAtOnce; ++y) {
-                const int z = min(y0 + y, parts - 1);
-                w[y] = __ldcg(ml + z);
-                v[y] = __ldcg(po + z * (D / 4));
-            }
-#pragma unroll
-            for (int y = 0; y < kAtOnce; ++y) {
-                if (y0 + y >= parts) continue;
-                const float mn = fmaxf(mx, w[y].x);
-                const float wo = ex2(mx - mn), wt = ex2(w[y].x - mn);
-                mx = mn;
-                sum = fmaf(wt, w[y].y, sum * wo);
-                acc[0] = fmaf(wt, v[y].x, acc[0] * wo);
-                acc[1] = fmaf(wt, v[y].y, acc[1] * wo);
-                acc[2] = fmaf(wt, v[y].z, acc[2] * wo);
-                acc[3] = fmaf(wt, v[y].w, acc[3] * wo);
-            }
-        }
+        const int64_t at = ((static_cast<int64_t>(kvh) * a.tiles + u) * kTcBM + trow) * a.part_pitch + a.part_pitch - 1;
+        const bool empty = sum == 0.f;  // (as below)
+        __stcg(reinterpret_cast<float4*>(a.part_o + at * D + d),
+               empty ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(acc[0], acc[1], acc[2], acc[3]));
+        if (d == 0) __stcg(a.part_ml + at, empty ? make_float2(-INFINITY, 0.f) : make_float2(mx, sum));
+        return;
     }
     const bool none = sum == 0.f;  // the row sees no key (its sum of values: 0, or 0 times what is not finite)
     const float inv = (KV4 ? 2.f : 1.f) / sum;
@@ -325,7 +336,8 @@ struct Warp {
     float o[NT][kQ][4];
 
     // Query rows of K/V head kvh, row block rb.  Lane (g, t) = (lane/4, lane%4).
-    __device__ __forceinline__ void load_q(const DecodeArgs& a, int b, int kvh, int rb) {
+    template <typename ARGS>
+    __device__ __forceinline__ void load_q(const ARGS& a, int b, int kvh, int rb) {
         const int lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
         const int rows = (a.H / a.Hkv) * a.Nq;
 #pragma unroll
@@ -338,8 +350,8 @@ struct Warp {
             if constexpr (!KV4) {
 #pragma unroll
                 for (int kk = 0; kk < kQ; ++kk) {
-                    q[n][kk][0] = src ? *reinterpret_cast<const uint32_t*>(src + 16 * kk + 2 * t) : 0u;
-                    q[n][kk][1] = src ? *reinterpret_cast<const uint32_t*>(src + 16 * kk + 8 + 2 * t) : 0u;
+                    q[n][kk][0] = src ? read<ARGS>(reinterpret_cast<const uint32_t*>(src + 16 * kk + 2 * t)) : 0u;
+                    q[n][kk][1] = src ? read<ARGS>(reinterpret_cast<const uint32_t*>(src + 16 * kk + 8 + 2 * t)) : 0u;
                 }
                 f[n][0] = f[n][1] = fmaxf(a.scale_log2, kLeastFactor);
                 qsum[n] = 0u;
@@ -674,7 +686,9 @@ struct Warp {
     // The stage's keys: `key` is the first one's index, ends[n][x] the number of
     // keys that row 2t + x sees (tested when `masked`); bit p of `skip`: part p
     // holds nothing.
-    __device__ __forceinline__ void keys(uint32_t stage, int key, bool masked, uint32_t skip, const int (&ends)[NT][2]) {
+    // (`cap`: keys from there on are hidden from every row.)
+    __device__ __forceinline__ void keys(uint32_t stage, int key, bool masked, uint32_t skip, const int (&ends)[NT][2],
+                                         int cap = 0x7fffffff) {
         const int lane = threadIdx.x % 32, g = lane / 4;
         constexpr int P = S::kParts;
         float s[P][NT][4];
@@ -687,7 +701,7 @@ struct Warp {
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
-                        if (key + u * kPart + g + (x & 2) * 4 >= ends[n][x & 1] || ((skip >> u) & 1u))
+                        if (key + u * kPart + g + (x & 2) * 4 >= min(ends[n][x & 1], cap) || ((skip >> u) & 1u))
                             s[u][n][x] = -INFINITY;
         }
         float mx[NT][2];
@@ -758,7 +772,20 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
     const int row_blocks = (rows + C::kRows - 1) / C::kRows;
     const int per_key = a.Hkv * row_blocks;  // targets of one sequence
 
-    grid_dependency();
+    if constexpr (MODE == kBehindPrefix) {
+        // The kernel before this one, the prefix's, writes nothing that this one
+        // reads, and what came before that is complete once all its CTAs let this
+        // one start: only the end waits for it (wait_prefix).  What an earlier
+        // kernel may have written is read through L2.
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    } else {
+        grid_dependency();
+    }
+    auto wait_prefix = [&]() {
+        if constexpr (MODE == kBehindPrefix) asm volatile("griddepcontrol.wait;" ::: "memory");
+    };
+    Prefix prefix = {0, 0};
+    if constexpr (MODE == kWithPrefix) prefix = prefix_of(a, blockIdx.x == 0 && tid == 0);
     // All units of the call, and this CTA's share of them.  A target (K/V head
     // and row block of a sequence) counts C::kTargetCost units more than it has, so
     // that shares of many short sequences take no longer than others.
@@ -804,7 +831,10 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
     const int cta = blockIdx.x;
     const int ctas = static_cast<int>(min(min(static_cast<int64_t>(gridDim.x), units),
                                           max(units * kMaxParts / most, static_cast<int64_t>(1))));
-    if (cta >= ctas) return;
+    if (cta >= ctas) {
+        wait_prefix();
+        return;
+    }
     const int64_t begin = share_begin(units, cta, ctas), end = share_begin(units, cta + 1, ctas);
     // The sequence of unit `begin`: prefix sums, kThreads sequences at a time.
     int b;
@@ -923,12 +953,14 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
 
         int ends[NT][2];
         const int min_end = MODE == kCross ? my_len : my_len - a.Nq + 1;
+        const int first_end = MODE == kWithPrefix ? max(min_end, prefix.end) : min_end;  // every row sees the prefix
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const int r = rb * C::kRows + n * 8 + (lane % 4) * 2 + x;
                 ends[n][x] = MODE != kCross && r < rows ? min_end + r % a.Nq : my_len;  // rows that are none: anything finite
+                if constexpr (MODE == kWithPrefix) ends[n][x] = max(ends[n][x], prefix.end);
             }
 
         // This warp's keys: kKeys at first + stride i.
@@ -947,13 +979,21 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
                 r.p[0] = 0;
                 return r;
             }
+            if constexpr (MODE == kWithPrefix) {
+                const bool own = key >= prefix.end;
+                const int k = own ? key - prefix.end : key;
+                r.p[0] = i < turns && key < (own ? last : prefix.keys)
+                             ? (own ? table : a.prefix_table)[page_shift >= 0 ? k >> page_shift : k / a.page_size] : 0;
+                return r;
+            }
 #pragma unroll
             for (int u = 0; u < S::kParts; ++u) {
                 const int k = key + u * kPart;
                 if (u > 0 && one_page)
                     r.p[u] = r.p[0];
                 else
-                    r.p[u] = i < turns && k < last ? table[page_shift >= 0 ? k >> page_shift : k / a.page_size] : 0;
+                    r.p[u] = i < turns && k < last
+                                 ? read<DecodeArgsOf<MODE>>(table + (page_shift >= 0 ? k >> page_shift : k / a.page_size)) : 0;
             }
             return r;
         };
@@ -968,6 +1008,24 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
                         w.template copy_rows<true>(a, source, at, my_b, key, kPart);
                     else
                         w.template copy_rows<false>(a, source, at, my_b, key, last - key);
+                    cp_async_commit();
+                    return;
+                }
+                if constexpr (MODE == kWithPrefix) {
+                    const bool own = key >= prefix.end;
+                    const int k = own ? key - prefix.end : key, left = (own ? last : prefix.keys) - key;
+                    const int off = page_shift >= 0 ? k & (a.page_size - 1) : k % a.page_size;
+                    int page = pages.p[0], valid = left;
+                    skip &= ~(1u << stage);
+                    if (left > 0 && static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.num_pages)) {
+                        if (lane == 0) atomicOr(&g_decode_error_word, 1u << kDevErrInvalidArg);
+                        if (own) skip |= 1u << stage;  // (a page of the prefix: zeros that are seen)
+                        page = valid = 0;
+                    }
+                    if (valid >= S::kKeys)
+                        w.template copy<true>(w.rows_of(a, source, page, off), at, 0, 0, kPart);
+                    else
+                        w.template copy<false>(w.rows_of(a, source, left > 0 ? page : 0, off), at, 0, 0, valid);
                     cp_async_commit();
                     return;
                 }
@@ -1018,7 +1076,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
             for (int i = 0; i < C::kStages - 1; ++i) start(i, early[i]);
             pages = early[C::kStages - 1];
         }
-        w.load_q(a, my_b, kvh, rb);
+        w.template load_q<DecodeArgsOf<MODE>>(a, my_b, kvh, rb);
         for (int i = 0; i < turns; ++i) {
             start(i + C::kStages - 1, pages);
             pages = pages_at(i + C::kStages);  // needed one turn later
@@ -1027,7 +1085,12 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
             const int stage = i % C::kStages;
             const int key = first + i * stride;
             const uint32_t none = (skip >> (stage * S::kParts)) & ((1u << S::kParts) - 1u);
-            w.keys(ring + stage * S::kBytes, key, key + S::kKeys > min_end || none != 0u, none, ends);
+            if constexpr (MODE == kWithPrefix) {
+                const int cap = key < prefix.end ? prefix.keys : 0x7fffffff;
+                w.keys(ring + stage * S::kBytes, key, key + S::kKeys > min(first_end, cap) || none != 0u, none, ends, cap);
+            } else {
+                w.keys(ring + stage * S::kBytes, key, key + S::kKeys > first_end || none != 0u, none, ends);
+            }
             __syncwarp();  // every lane is done with the stage before it is filled again
         }
         cp_async_wait<0>();
@@ -1174,6 +1237,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
         __syncthreads();  // the joined memory becomes the ring again
         b = next_b;
     }
+    wait_prefix();
 }
 
 template <int D, bool BF16, bool KV4, int NT, bool ALONE, Mode MODE>

@@ -410,6 +410,13 @@ int cross_splits(int64_t B, int64_t Hkv, const RowTiles& t, int64_t Nk) {
     return best;
 }
 
+// A shared prefix of up to `keys` tokens: whether every sequence reads it for itself,
+// in one launch of the decode kernel.  Where one does it is read once anyway.
+constexpr int64_t kReadByEach = 64ll << 20;
+bool shared_read_by_each(int64_t B, int64_t share, int64_t Hkv, int64_t Nq, int64_t D, int64_t keys) {
+    return share * Nq <= 32 && (B == 1 || keys <= kReadByEach / (B * Hkv * 4 * D));
+}
+
 // Sizes of cross attention (dtype, head counts, lengths).
 int validate_cross(int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t Nk, int64_t D, float scale, int dtype) {
     if (dtype != FATTN_F32 && dtype != FATTN_F16 && dtype != FATTN_BF16) return FATTN_ERR_INVALID_ARG;
@@ -1343,7 +1350,7 @@ int64_t fattn_decode_shared_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, i
     if (own <= 0 || H > (int64_t(1) << 16)) return 0;
     const RowTiles t = row_tiles_of(H / Hkv, Nq, B, true);
     const int64_t rows = part_rows(1, Hkv, t);
-    return ceil_div(own, 16) * 16 + 16 + part_bytes(rows, max_splits(Hkv * t.pairs), D);
+    return ceil_div(own, 16) * 16 + 16 + part_bytes(rows, max_splits(Hkv * t.pairs) + 1, D);
 }
 
 int fattn_decode_shared(const void* q, void* o, float* lse, const int64_t* strides, const void* k_pages,
@@ -1381,16 +1388,29 @@ int fattn_decode_shared(const void* q, void* o, float* lse, const int64_t* strid
     if (!prefix_table || !prefix_len || num_pages == 0) return FATTN_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(prefix_table) & 3u) || (reinterpret_cast<uintptr_t>(prefix_len) & 3u))
         return FATTN_ERR_MISALIGNED;
-    if (prefix_width > (0x7fffffffll - 65536) / page_size) return FATTN_ERR_UNSUPPORTED;
+    // (Keys of the prefix and of a sequence are numbered in ints.)
+    if (prefix_width > (0x7fffffffll - 131072) / page_size || prefix_width + table_width > (0x7fffffffll - 131072) / page_size)
+        return FATTN_ERR_UNSUPPORTED;
     // A tensor map's strides are below 2^40 bytes.
     if (page_stride >= (int64_t(1) << 39)) return FATTN_ERR_UNSUPPORTED;
     const int64_t n_q[3] = {B, H, Nq};
     st = check_strides(strides, n_q);
     if (st != FATTN_OK) return st;
     const RowTiles t = row_tiles_of(H / Hkv, Nq, B, true);
-    const int pitch = max_splits(Hkv * t.pairs);
+    const int most = max_splits(Hkv * t.pairs), pitch = most + 1;
     if (Hkv * t.pairs * pitch > (int64_t(1) << 30)) return FATTN_ERR_UNSUPPORTED;
     if (no_device != FATTN_OK) return no_device;
+    if (shared_read_by_each(B, H / Hkv, Hkv, Nq, D, prefix_width * page_size)) {
+        PrefixDecodeArgs p;
+        std::memset(static_cast<void*>(&p), 0, sizeof(p));
+        static_cast<DecodeArgs&>(p) = d;
+        p.prefix_table = prefix_table;
+        p.prefix_len = prefix_len;
+        p.prefix_max = static_cast<int>(prefix_width * page_size);
+        const cudaError_t e = decode_prefix_launch(p, static_cast<int>(D), dtype == FATTN_BF16, sms,
+                                                   reinterpret_cast<cudaStream_t>(stream_h));
+        return e == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
+    }
 
     RowsArgs a;
     std::memset(static_cast<void*>(&a), 0, sizeof(a));
@@ -1407,6 +1427,11 @@ int fattn_decode_shared(const void* q, void* o, float* lse, const int64_t* strid
     a.part_o = reinterpret_cast<float*>(ws + 16);
     a.part_ml = reinterpret_cast<float2*>(a.part_o + part_rows(1, Hkv, t) * pitch * D);
     a.part_pitch = pitch;
+    a.max_parts = most;
+    a.own_part = 1;
+    a.o = o;
+    a.lse = lse;
+    a.o_bs = strides[3], a.o_hs = strides[4], a.o_ns = strides[5];
     a.lens = prefix_len;
     a.table = prefix_table;
     a.H = static_cast<int>(H);
@@ -1421,12 +1446,11 @@ int fattn_decode_shared(const void* q, void* o, float* lse, const int64_t* strid
     a.B = static_cast<int>(B);
     a.Nq = static_cast<int>(Nq);
     a.share = static_cast<int>(H / Hkv);
-    const int grid = static_cast<int>(std::min<int64_t>(Hkv * t.pairs * pitch, sms));
+    const int grid = static_cast<int>(std::min<int64_t>(Hkv * t.pairs * most, sms));
     if (rows_launch(a, static_cast<int>(D), bf16, grid, reinterpret_cast<cudaStream_t>(stream_h)) != cudaSuccess)
         return FATTN_ERR_CUDA;
     d.part_o = a.part_o;
     d.part_ml = a.part_ml;
-    d.part_count = a.part_count;
     d.part_pitch = pitch;
     d.box_i = t.box_i;
     d.box_h = t.box_h;
@@ -1434,7 +1458,8 @@ int fattn_decode_shared(const void* q, void* o, float* lse, const int64_t* strid
     d.n_i = t.n_i;
     d.n_h = t.n_h;
     d.tiles = a.tiles;
-    const cudaError_t e = decode_shared_launch(d, static_cast<int>(D), bf16, sms, reinterpret_cast<cudaStream_t>(stream_h));
+    cudaError_t e = decode_shared_launch(d, static_cast<int>(D), bf16, sms, reinterpret_cast<cudaStream_t>(stream_h));
+    if (e == cudaSuccess) e = rows_join_launch(a, static_cast<int>(D), bf16, reinterpret_cast<cudaStream_t>(stream_h));
     return e == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
 }
 
@@ -1527,8 +1552,9 @@ int fattn_fwd_cross(const void* q, const void* k, const void* v, void* o, float*
     a.lse = lse;
     a.o_bs = strides[9], a.o_hs = strides[10], a.o_ns = strides[11];
     a.lens = kv_lens;
-    a.splits = splits;
+    a.max_parts = splits;
     a.part_pitch = splits;
+    a.part_tiles = static_cast<int>(ceil_div(ceil_div(Nk, kTcBN), splits));
     if (splits > 1) {
         a.part_o = static_cast<float*>(workspace);
         a.part_ml = reinterpret_cast<float2*>(a.part_o + part_rows(B, Hkv, t) * splits * D);

@@ -8,45 +8,79 @@ namespace {
 
 constexpr int kJoinThreads = 256;
 
-// A warp a row of the output: the parts in the order of their keys.
+// A warp a row of the output: lanes weigh the parts, four at most each, then take
+// D/32 elements of every part, kAtOnce parts on their way at once.  In the order of
+// the keys, so that the result does not depend on anything else.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kJoinThreads) rows_join_kernel(const __grid_constant__ RowsArgs a) {
-    constexpr int kPer = D / 32;  // elements a lane
+    constexpr int kPer = D / 32, kAtOnce = 8;
+    static_assert(kMaxSplits + 1 <= 5 * 32, "parts of a row in the lanes");
     const int64_t w = (static_cast<int64_t>(blockIdx.x) * kJoinThreads + threadIdx.x) / 32;
     const int lane = threadIdx.x % 32;
-    grid_dependency();
-    if (w >= static_cast<int64_t>(a.B) * a.H * a.Nq) return;
     const int i = static_cast<int>(w % a.Nq);
     const int64_t bh = w / a.Nq;
     const int b = static_cast<int>(bh / a.H), h = static_cast<int>(bh % a.H);
     const int kvh = h / a.share, hq = h % a.share;
-    const int u = (hq / a.box_h) * a.n_i + i / a.box_i, trow = (hq % a.box_h) * a.box_i + i % a.box_i;
-    const int64_t at = (((static_cast<int64_t>(b) * a.Hkv + kvh) * a.tiles + u) * kTcBM + trow) * a.part_pitch;
+    const int source = a.sources > 1 ? b : 0, among = b - source;  // (one source: the entry among its rows)
+    const int u = (among / a.box_b * a.n_h + hq / a.box_h) * a.n_i + i / a.box_i;
+    const int trow = ((among % a.box_b) * a.box_h + hq % a.box_h) * a.box_i + i % a.box_i;
+    const int64_t at = (((static_cast<int64_t>(source) * a.Hkv + kvh) * a.tiles + u) * kTcBM + trow) * a.part_pitch;
+    grid_dependency();
+    if (w >= static_cast<int64_t>(a.B) * a.H * a.Nq) return;
+    int parts;
+    if (a.part_tiles == 0) {
+        parts = __ldcg(a.part_count);
+    } else {
+        const int tiles = (visible_keys(a, source, false) + kTcBN - 1) / kTcBN;
+        parts = max((tiles + a.part_tiles - 1) / a.part_tiles, 1);
+    }
+    const int all = parts + (a.own_part ? 1 : 0);
+    auto place = [&](int s) { return at + (s < parts ? s : a.part_pitch - 1); };
+    float2 ml[5];
     float m = -INFINITY;
-    for (int s = lane; s < a.splits; s += 32) m = fmaxf(m, __ldcg(a.part_ml + at + s).x);
+#pragma unroll
+    for (int x = 0; x < 5; ++x) {
+        const int s = lane + 32 * x;
+        ml[x] = s < all ? __ldcg(a.part_ml + place(s)) : make_float2(-INFINITY, 0.f);
+        m = fmaxf(m, ml[x].x);
+    }
 #pragma unroll
     for (int d = 16; d > 0; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     const bool none = m == -INFINITY;
-    float sum = 0.f, acc[kPer];
+    float acc[kPer];
 #pragma unroll
     for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < a.splits; ++s) {
-        const float2 ml = __ldcg(a.part_ml + at + s);
-        const float wt = none ? 0.f : ex2_approx(ml.x - m);
-        sum = fmaf(wt, ml.y, sum);
-        const float* src = a.part_o + (at + s) * D + lane * kPer;
-        float v[kPer];
-        if constexpr (kPer == 4) {
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
-            v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-        } else {
-            const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
-            v[0] = x.x, v[1] = x.y;
-        }
+    float sum = 0.f;
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) acc[e] = fmaf(wt, v[e], acc[e]);
+    for (int x = 0; x < 5; ++x) {
+        if (32 * x >= all) break;
+        const float mine = none ? 0.f : ex2_approx(ml[x].x - m);
+        sum = fmaf(mine, ml[x].y, sum);
+        const int upto = min(32, all - 32 * x);
+        for (int s0 = 0; s0 < upto; s0 += kAtOnce) {
+            float v[kAtOnce][kPer];
+#pragma unroll
+            for (int y = 0; y < kAtOnce; ++y) {
+                const float* src = a.part_o + place(32 * x + min(s0 + y, upto - 1)) * D + lane * kPer;
+                if constexpr (kPer == 4) {
+                    const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
+                    v[y][0] = f.x, v[y][1] = f.y, v[y][2] = f.z, v[y][3] = f.w;
+                } else {
+                    const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
+                    v[y][0] = f.x, v[y][1] = f.y;
+                }
+            }
+#pragma unroll
+            for (int y = 0; y < kAtOnce; ++y) {
+                const float wt = __shfl_sync(0xffffffffu, mine, min(s0 + y, 31));
+                if (s0 + y < upto)
+#pragma unroll
+                    for (int e = 0; e < kPer; ++e) acc[e] = fmaf(wt, v[y][e], acc[e]);
+            }
+        }
     }
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
     const float inv = none ? 0.f : 1.f / sum;
     uint16_t* o = static_cast<uint16_t*>(a.o) + b * a.o_bs + h * a.o_hs + i * a.o_ns + lane * kPer;
     if constexpr (kPer == 4)

@@ -126,12 +126,16 @@ __device__ __forceinline__ PackedPlan* plan_of(const PackedArgs& a) {
     return reinterpret_cast<PackedPlan*>(reinterpret_cast<uint8_t*>(a.plan) + blockIdx.x * a.plan_stride);
 }
 
-// Rows: the number of parts that this launch's keys are cut into (in the CTA's
-// shared memory, beside the TMEM base and the abort flag).
+// Rows: how this launch cuts the keys (in the CTA's shared memory, beside the TMEM
+// base and the abort flag).
+struct Cut {
+    int parts;  // of the longest source
+    int tiles;  // K/V tiles of a part
+};
 template <int D>
-__device__ __forceinline__ int* splits_word() {
+__device__ __forceinline__ Cut* cut_of() {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    return reinterpret_cast<int*>(smem_raw + TcLayout<D>::kMiscOff + 8);
+    return reinterpret_cast<Cut*>(smem_raw + TcLayout<D>::kMiscOff + 8);
 }
 
 // Rows: keys of a source that every row sees.
@@ -187,20 +191,20 @@ template <bool CAUSAL, bool EQUAL = false, Kind KIND = kDense>
 __device__ __forceinline__ Task decode_task(int t, const ArgsOf<KIND>& a) {
     Task k;
     if constexpr (KIND == kRows) {
-        const int splits = *splits_word<EQUAL ? 64 : 128>();
+        const Cut cut = *cut_of<EQUAL ? 64 : 128>();
         const int pair = t % a.pairs;
         t /= a.pairs;
-        const int split = t % splits;
-        k.bh = t / splits;
+        const int part = t % cut.parts;
+        k.bh = t / cut.parts;
         k.q0 = 2 * pair;
         const int len = visible_keys(a, k.bh / a.Hkv, false);
         const int tiles = (len + kTcBN - 1) / kTcBN;
-        const int per = (tiles + splits - 1) / splits;
-        const int first = min(split * per, tiles), last = min(first + per, tiles);
+        const int first = min(part * cut.tiles, tiles), last = min(first + cut.tiles, tiles);
         k.start = first * kTcBN;
         k.n = min(len, last * kTcBN) - k.start;
-        // A part without keys visits one tile, all of it masked.
-        k.nbmax = max(last - first, 1);
+        // Parts behind a shorter source's last are no tasks (nbmax = 0); a source
+        // without keys visits one tile, all of it masked.
+        k.nbmax = part == 0 ? max(last - first, 1) : last - first;
         k.nb[0] = k.nbmax;
         k.nb[1] = EQUAL || k.q0 + 1 < a.tiles ? k.nbmax : 0;
         return k;
@@ -378,7 +382,7 @@ __device__ __forceinline__ int num_tasks_of(const ArgsOf<KIND>& a) {
     if constexpr (KIND == kPacked)
         return plan_of(a)->blocks * a.H;
     else if constexpr (KIND == kRows)
-        return a.sources * a.Hkv * a.pairs * *splits_word<D>();
+        return a.sources * a.Hkv * a.pairs * cut_of<D>()->parts;
     else
         return a.num_tasks;
 }
@@ -603,6 +607,12 @@ __device__ void producer_role(const ArgsOf<KIND>& a, uint8_t* smem, const Bars& 
     };
 
     int t = static_cast<int>(blockIdx.x);
+    // Rows: past the parts that a shorter source does not have.
+    auto skip_none = [&]() {
+        if constexpr (KIND == kRows)
+            while (t < num_tasks && decode_task<CAUSAL, L::kRot, KIND>(t, a).nbmax == 0) t = fetch();
+    };
+    skip_none();
     for (int kt = 0; ok; ++kt) {
         if (t >= num_tasks) {
             publish(kt, static_cast<int>(kEndOfSchedule));
@@ -633,6 +643,7 @@ __device__ void producer_role(const ArgsOf<KIND>& a, uint8_t* smem, const Bars& 
         // loads can only start when this task's last score products are
         // done; fetched into L2 now, they land in shared memory at L2 latency.
         t = fetch();
+        skip_none();
         if (t < num_tasks && elect_one_sync()) {
             const Task nx = decode_task<CAUSAL, L::kRot, KIND>(t, a);
             if constexpr (KIND == kRows) {
@@ -1265,8 +1276,8 @@ __device__ void softmax_role(const ArgsOf<KIND>& a, const Bars& bars, uint32_t t
             valid = row_place(a, source, u, trow, r);
             if (a.part_o != nullptr) {
                 // A part: the sum of values not yet divided, by the weights' unrounded sum.
-                const int split = t / a.pairs % *splits_word<D>();
-                const int64_t at = ((static_cast<int64_t>(te.bh) * a.tiles + u) * kTcBM + trow) * a.part_pitch + split;
+                const int part = t / a.pairs % cut_of<D>()->parts;
+                const int64_t at = ((static_cast<int64_t>(te.bh) * a.tiles + u) * kTcBM + trow) * a.part_pitch + part;
                 const float f = inv_l * l_exact;
                 float* dst = a.part_o + at * D;
 #pragma unroll
@@ -1382,20 +1393,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_tc_kernel(const __grid
     if constexpr (KIND == kRows) {
         grid_dependency();
         if (warp == 0) {
-            int splits = a.splits;
-            if (splits == 0) {
+            Cut cut = {a.max_parts, a.part_tiles};
+            if (cut.tiles == 0) {
                 // From the length, which only the device knows: the cheapest of what the workspace has room for.
                 const int tiles = (visible_keys(a, 0, blockIdx.x == 0 && lane == 0) + kTcBN - 1) / kTcBN;
                 const int targets = a.sources * a.Hkv * a.pairs;
                 uint32_t best = 0xffffffffu;
-                for (int s = lane + 1; s <= a.part_pitch; s += 32)
+                for (int s = lane + 1; s <= a.max_parts; s += 32)
                     best = min(best, split_cost(targets, tiles, gridDim.x, s) * 256u + static_cast<uint32_t>(s));
-                splits = static_cast<int>(__reduce_min_sync(0xffffffffu, best) % 256u);
-                if (blockIdx.x == 0 && lane == 0) *a.part_count = splits;
+                const int parts = static_cast<int>(__reduce_min_sync(0xffffffffu, best) % 256u);
+                cut.tiles = max((tiles + parts - 1) / parts, 1);
+                cut.parts = max((tiles + cut.tiles - 1) / cut.tiles, 1);
+                if (blockIdx.x == 0 && lane == 0) *a.part_count = cut.parts;
             } else if (a.lens != nullptr && blockIdx.x == 0) {
                 for (int b = lane; b < a.sources; b += 32) visible_keys(a, b, true);
             }
-            if (lane == 0) *splits_word<D>() = splits;
+            if (lane == 0) *cut_of<D>() = cut;
         }
     }
     if constexpr (KIND == kPacked) {

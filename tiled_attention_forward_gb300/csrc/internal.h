@@ -123,7 +123,9 @@ struct RowsArgs : TcArgs {  // N, BH, num_qblk, num_tasks and head_group are unu
     float2* part_ml;           // .. [part_pitch]: max (log2 units) and sum of the weights
     int32_t* part_count;       // receives the parts of a launch that chooses them itself
     int part_pitch;            // parts that the workspace has room for
-    int splits;                // parts that the keys are cut into; 0: chosen by the length
+    int max_parts;             // of those, the ones that the keys may be cut into
+    int part_tiles;            // K/V tiles of a part; 0: chosen by the length
+    int own_part;              // the last part of the workspace is joined too
     int num_pages;
     int page_size;
     int piece;                 // keys of a copy
@@ -326,13 +328,18 @@ struct DecodeArgs {
     int Nq;
     float scale_log2;
 };
-struct SharedDecodeArgs : DecodeArgs {  // the parts of the prefix, as RowsArgs has them (one source)
-    const float* part_o;
-    const float2* part_ml;
-    const int32_t* part_count;
+struct SharedDecodeArgs : DecodeArgs {  // the parts, as RowsArgs has them (one source); the last is the own keys'
+    float* part_o;
+    float2* part_ml;
     int part_pitch;
     int box_i, box_h, box_b, n_i, n_h, tiles;
 };
+struct PrefixDecodeArgs : DecodeArgs {
+    const int32_t* prefix_table;  // [prefix_max / page_size]
+    const int32_t* prefix_len;    // [1]
+    int prefix_max;
+};
+cudaError_t decode_prefix_launch(const PrefixDecodeArgs& a, int D, bool bf16, int sms, cudaStream_t s);
 struct CrossDecodeArgs : DecodeArgs {  // k_pages and v_pages: [B][Nk][Hkv][D] by strides; seq_lens may be nullptr
     int64_t k_bs, k_hs, k_ns, v_bs, v_hs, v_ns;
     int Nk;
