@@ -393,21 +393,10 @@ int64_t part_bytes(int64_t rows, int64_t pitch, int64_t D) { return rows * pitch
 // streams the keys once for up to 32 rows; so does a call without keys, which only
 // writes zeros.
 bool cross_few_rows(int64_t share, int64_t Nq, int64_t Nk) { return share * Nq <= 32 || Nk == 0; }
-// Parts that the keys are cut into.
+// Parts that the keys may be cut into (the device chooses, by the lengths): two
+// waves of tasks, where that leaves parts of two tiles.  1: they are not.
 int cross_splits(int64_t B, int64_t Hkv, const RowTiles& t, int64_t Nk) {
-    const int64_t targets = B * Hkv * t.pairs, tiles = ceil_div(Nk, kTcBN);
-    int best = 1;
-    if (targets >= 2 * kSplitCtas) return best;
-    uint32_t least = split_cost(static_cast<int>(targets), static_cast<int>(tiles), kSplitCtas, 1);
-    const int most = static_cast<int>(std::min<int64_t>(max_splits(targets), tiles));
-    for (int s = 2; s <= most; ++s) {
-        const uint32_t cost = split_cost(static_cast<int>(targets), static_cast<int>(tiles), kSplitCtas, s);
-        if (cost < least) {
-            least = cost;
-            best = s;
-        }
-    }
-    return best;
+    return static_cast<int>(std::min<int64_t>(max_splits(B * Hkv * t.pairs), std::max<int64_t>(ceil_div(Nk, 2 * kTcBN), 1)));
 }
 
 // A shared prefix of up to `keys` tokens: whether every sequence reads it for itself,
@@ -1468,7 +1457,7 @@ int64_t fattn_cross_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t N
     if (cross_few_rows(H / Hkv, Nq, Nk)) return decode_workspace_bytes(B, H, Hkv, Nq, D);
     const RowTiles t = row_tiles_of(H / Hkv, Nq, B, false);
     const int splits = cross_splits(B, Hkv, t, Nk);
-    return splits > 1 ? part_bytes(part_rows(B, Hkv, t), splits, D) : 16;
+    return splits > 1 ? 16 + part_bytes(part_rows(B, Hkv, t), splits, D) : 16;
 }
 
 int fattn_fwd_cross(const void* q, const void* k, const void* v, void* o, float* lse, const int64_t* strides,
@@ -1554,9 +1543,9 @@ int fattn_fwd_cross(const void* q, const void* k, const void* v, void* o, float*
     a.lens = kv_lens;
     a.max_parts = splits;
     a.part_pitch = splits;
-    a.part_tiles = static_cast<int>(ceil_div(ceil_div(Nk, kTcBN), splits));
     if (splits > 1) {
-        a.part_o = static_cast<float*>(workspace);
+        a.part_count = static_cast<int32_t*>(workspace);
+        a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 16);
         a.part_ml = reinterpret_cast<float2*>(a.part_o + part_rows(B, Hkv, t) * splits * D);
     }
     a.H = static_cast<int>(H);

@@ -9,8 +9,8 @@ namespace {
 constexpr int kJoinThreads = 256;
 
 // A warp a row of the output: lanes weigh the parts, four at most each, then take
-// D/32 elements of every part, kAtOnce parts on their way at once.  In the order of
-// the keys, so that the result does not depend on anything else.
+// D/32 elements of every part, kAtOnce parts on their way at once.  In one order
+// (own keys, then the prefix's), so that the result does not depend on anything else.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kJoinThreads) rows_join_kernel(const __grid_constant__ RowsArgs a) {
     constexpr int kPer = D / 32, kAtOnce = 8;
@@ -27,21 +27,35 @@ __global__ void __launch_bounds__(kJoinThreads) rows_join_kernel(const __grid_co
     const int64_t at = (((static_cast<int64_t>(source) * a.Hkv + kvh) * a.tiles + u) * kTcBM + trow) * a.part_pitch;
     grid_dependency();
     if (w >= static_cast<int64_t>(a.B) * a.H * a.Nq) return;
-    int parts;
-    if (a.part_tiles == 0) {
-        parts = __ldcg(a.part_count);
-    } else {
-        const int tiles = (visible_keys(a, source, false) + kTcBN - 1) / kTcBN;
-        parts = max((tiles + a.part_tiles - 1) / a.part_tiles, 1);
-    }
-    const int all = parts + (a.own_part ? 1 : 0);
-    auto place = [&](int s) { return at + (s < parts ? s : a.part_pitch - 1); };
+    // What does not depend on the number of parts is on its way with it: the places
+    // that may hold one (what lies in those that hold none is not used), the own
+    // keys' part as place 0.
+    auto place = [&](int s) { return at + (a.own_part ? (s == 0 ? a.part_pitch - 1 : s - 1) : s); };
+    const int most = a.max_parts + a.own_part;
+    const int per = __ldcg(a.part_count);
+    const int tiles = (visible_keys(a, source, false) + kTcBN - 1) / kTcBN;
     float2 ml[5];
+    float early[kAtOnce][kPer];
+#pragma unroll
+    for (int x = 0; x < 5; ++x)
+        if (lane + 32 * x < most) ml[x] = __ldcg(a.part_ml + place(lane + 32 * x));
+    auto load = [&](float (&v)[kPer], int s) {
+        const float* src = a.part_o + place(s) * D + lane * kPer;
+        if constexpr (kPer == 4) {
+            const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
+            v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+        } else {
+            const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
+            v[0] = f.x, v[1] = f.y;
+        }
+    };
+#pragma unroll
+    for (int y = 0; y < kAtOnce; ++y) load(early[y], min(y, most - 1));
+    const int all = max((tiles + per - 1) / per, 1) + a.own_part;
     float m = -INFINITY;
 #pragma unroll
     for (int x = 0; x < 5; ++x) {
-        const int s = lane + 32 * x;
-        ml[x] = s < all ? __ldcg(a.part_ml + place(s)) : make_float2(-INFINITY, 0.f);
+        if (lane + 32 * x >= all) ml[x] = make_float2(-INFINITY, 0.f);
         m = fmaxf(m, ml[x].x);
     }
 #pragma unroll
@@ -59,23 +73,17 @@ __global__ void __launch_bounds__(kJoinThreads) rows_join_kernel(const __grid_co
         const int upto = min(32, all - 32 * x);
         for (int s0 = 0; s0 < upto; s0 += kAtOnce) {
             float v[kAtOnce][kPer];
+            if (s0 + kAtOnce < upto || x < 4)  // the next ones
 #pragma unroll
-            for (int y = 0; y < kAtOnce; ++y) {
-                const float* src = a.part_o + place(32 * x + min(s0 + y, upto - 1)) * D + lane * kPer;
-                if constexpr (kPer == 4) {
-                    const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
-                    v[y][0] = f.x, v[y][1] = f.y, v[y][2] = f.z, v[y][3] = f.w;
-                } else {
-                    const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
-                    v[y][0] = f.x, v[y][1] = f.y;
-                }
-            }
+                for (int y = 0; y < kAtOnce; ++y) load(v[y], min(32 * x + s0 + kAtOnce + y, all - 1));
 #pragma unroll
             for (int y = 0; y < kAtOnce; ++y) {
                 const float wt = __shfl_sync(0xffffffffu, mine, min(s0 + y, 31));
                 if (s0 + y < upto)
 #pragma unroll
-                    for (int e = 0; e < kPer; ++e) acc[e] = fmaf(wt, v[y][e], acc[e]);
+                    for (int e = 0; e < kPer; ++e) acc[e] = fmaf(wt, early[y][e], acc[e]);
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) early[y][e] = v[y][e];
             }
         }
     }

@@ -121,6 +121,17 @@ struct TcLayout {
     static_assert((kRot ? 384 : 256) + 2 * D <= 512, "TMEM budget");
 };
 
+// Rows whose keys are cut: a Q tile is free once the four warps of its softmax
+// warpgroup have written the part (its memory serves that), else once the last
+// score product has read it.
+template <Kind KIND>
+__device__ __forceinline__ bool frees_q(const ArgsOf<KIND>& a) {
+    if constexpr (KIND == kRows)
+        return a.part_o != nullptr;
+    else
+        return false;
+}
+
 // The list of Q blocks that this CTA follows.
 __device__ __forceinline__ PackedPlan* plan_of(const PackedArgs& a) {
     return reinterpret_cast<PackedPlan*>(reinterpret_cast<uint8_t*>(a.plan) + blockIdx.x * a.plan_stride);
@@ -147,6 +158,45 @@ __device__ __forceinline__ int visible_keys(const RowsArgs& a, int source, bool 
         return len < 0 ? 0 : a.max_keys;
     }
     return len;
+}
+
+// Rows: how to cut the keys, from the sources' lengths, which only the device knows
+// (a whole warp).  With k waves of tasks a part is as short as lets the tasks of all
+// sources fit, and a task takes two tiles' time more than its tiles (its start and
+// its epilogue); every part is read again when they are joined.
+__device__ __forceinline__ Cut choose_cut(const RowsArgs& a, bool report) {
+    const int lane = threadIdx.x % 32, each = a.Hkv * a.pairs, ctas = static_cast<int>(gridDim.x);
+    auto tiles_of = [&](int b) { return (visible_keys(a, b, false) + kTcBN - 1) / kTcBN; };
+    int mine = 0, most = 0, first = 0;
+    for (int b = lane; b < a.sources; b += 32) {
+        const int tiles = (visible_keys(a, b, report) + kTcBN - 1) / kTcBN;
+        if (b == lane) first = tiles;
+        mine += tiles;
+        most = max(most, tiles);
+    }
+    const int total = __reduce_add_sync(0xffffffffu, mine);
+    most = max(__reduce_max_sync(0xffffffffu, most), 1);
+    auto tasks = [&](int per) {
+        int n = lane < a.sources ? max((first + per - 1) / per, 1) : 0;
+        for (int b = lane + 32; b < a.sources; b += 32) n += max((tiles_of(b) + per - 1) / per, 1);
+        return static_cast<int64_t>(__reduce_add_sync(0xffffffffu, n)) * each;
+    };
+    const int least = (most + a.max_parts - 1) / a.max_parts;  // what the workspace has room for
+    int best = most, best_cost = 0x7fffffff;
+#pragma unroll 1
+    for (int waves = 1; waves <= 2; ++waves) {
+        const int room = waves * ctas;
+        const int64_t even = (static_cast<int64_t>(total) * each + room - 1) / room;
+        int per = max(static_cast<int>(min(even, static_cast<int64_t>(most))), max(least, 1));
+        while (per < most && tasks(per) > room) per += max(per / 16, 1);
+        per = min(per, most);
+        const int cost = 16 * waves * (per + 2) + most / per;
+        if (cost < best_cost && (per < most || waves == 1)) {
+            best_cost = cost;
+            best = per;
+        }
+    }
+    return {(most + best - 1) / best, best};
 }
 
 // Rows: which query row thread `trow` of tile u is (false: none).
@@ -199,7 +249,7 @@ __device__ __forceinline__ Task decode_task(int t, const ArgsOf<KIND>& a) {
         k.q0 = 2 * pair;
         const int len = visible_keys(a, k.bh / a.Hkv, false);
         const int tiles = (len + kTcBN - 1) / kTcBN;
-        const int first = min(part * cut.tiles, tiles), last = min(first + cut.tiles, tiles);
+        const int first = min(part * cut.tiles, tiles), last = min(first + cut.tiles, tiles);  // (no product overflows)
         k.start = first * kTcBN;
         k.n = min(len, last * kTcBN) - k.start;
         // Parts behind a shorter source's last are no tasks (nbmax = 0); a source
@@ -793,7 +843,7 @@ __device__ void mma_pair_role(const ArgsOf<KIND>& a, uint8_t* smem, const Bars& 
             if (elect_one_sync()) {
                 issue_qk(i, kslot);
                 mma_commit(&bars.s_full[i]);
-                if (j == tk.nb[i] - 1) mma_commit(&bars.q_empty[i]);
+                if (j == tk.nb[i] - 1 && !frees_q<KIND>(a)) mma_commit(&bars.q_empty[i]);
             }
             __syncwarp();
         }
@@ -949,6 +999,7 @@ __device__ void mma_pair_role_rot(const ArgsOf<KIND>& a, uint8_t* smem, const Ba
         return t;
     };
     const bool issuer = !HELPER;
+    const bool frees = !frees_q<KIND>(a);  // the products free a Q tile
     // S product into buffer b: Q tile i against the K tile in ring slot ks.
     auto issue_s = [&](uint32_t b, int i, uint32_t ks) {
         const uint64_t adesc = kmaj_desc + ((q_smem + i * L::kQTileBytes) >> 4);
@@ -984,13 +1035,13 @@ __device__ void mma_pair_role_rot(const ArgsOf<KIND>& a, uint8_t* smem, const Ba
         if (issuer && ok) {
             if (elect_one_sync()) {
                 issue_s(sbase % 3u, 0, ks);
-                if (nb == 1) mma_commit(&bars.q_empty[0]);
+                if (nb == 1 && frees) mma_commit(&bars.q_empty[0]);
                 issue_s((sbase + 1u) % 3u, 1, ks);
                 mma_commit(&bars.kv_empty[ks]);
-                if (nb == 1) mma_commit(&bars.q_empty[1]);
+                if (nb == 1 && frees) mma_commit(&bars.q_empty[1]);
                 if (nb > 1) {
                     issue_s((sbase + 2u) % 3u, 0, ks_next);
-                    if (nb == 2) mma_commit(&bars.q_empty[0]);
+                    if (nb == 2 && frees) mma_commit(&bars.q_empty[0]);
                 }
             }
             __syncwarp();
@@ -1011,7 +1062,7 @@ __device__ void mma_pair_role_rot(const ArgsOf<KIND>& a, uint8_t* smem, const Ba
                     if (j + 1 < nb) {  // S_1(j+1) into the buffer P_0(j) leaves
                         issue_s(k0 % 3u, 1, ks_next);
                         mma_commit(&bars.kv_empty[ks_next]);
-                        if (j + 1 == nb - 1) mma_commit(&bars.q_empty[1]);
+                        if (j + 1 == nb - 1 && frees) mma_commit(&bars.q_empty[1]);
                     }
                 }
                 __syncwarp();
@@ -1024,7 +1075,7 @@ __device__ void mma_pair_role_rot(const ArgsOf<KIND>& a, uint8_t* smem, const Ba
                     mma_commit(&bars.kv_empty[vs]);
                     if (j + 2 < nb) {  // S_0(j+2) into the buffer P_1(j) leaves
                         issue_s((k0 + 1u) % 3u, 0, ks2);
-                        if (j + 2 == nb - 1) mma_commit(&bars.q_empty[0]);
+                        if (j + 2 == nb - 1 && frees) mma_commit(&bars.q_empty[0]);
                     }
                 }
                 __syncwarp();
@@ -1073,7 +1124,7 @@ __device__ __noinline__ void softmax_dry_tail(const ArgsOf<KIND>& a, TaskRing ta
 }
 
 template <int D, bool BF16, bool CAUSAL, Kind KIND>
-__device__ void softmax_role(const ArgsOf<KIND>& a, const Bars& bars, uint32_t tmem_base,
+__device__ void softmax_role(const ArgsOf<KIND>& a, const Bars& bars, uint8_t* q_tiles, uint32_t tmem_base,
                              volatile uint32_t* abort_flag) {
     constexpr bool kRot = TcLayout<D>::kRot;  // D = 64: three rotating S buffers
     const int warp = threadIdx.x / 32;
@@ -1082,6 +1133,10 @@ __device__ void softmax_role(const ArgsOf<KIND>& a, const Bars& bars, uint32_t t
     const uint32_t lane_field = static_cast<uint32_t>((warp % 4) * 32) << 16;
     const uint32_t tO = tmem_base + lane_field + (kRot ? 3 : 2) * kTcBN + tile * D;
     const float sl2 = a.scale_log2;
+    // Rows: behind a tile's box lies whatever shared memory held; those rows are never
+    // stored, and have no say in when the others are rescaled (which moves roundings).
+    bool in_box = true;
+    if constexpr (KIND == kRows) in_box = static_cast<uint32_t>(trow) * 128u < a.box_bytes;
 
     // Barrier phases: D = 128 counts the S products of this tile on
     // s_full[tile]; D = 64 counts them per buffer on s_full[b * 2 + tile].
@@ -1181,7 +1236,7 @@ __device__ void softmax_role(const ArgsOf<KIND>& a, const Bars& bars, uint32_t t
                 // Rescale O and l only when some row of the warp saw its max
                 // rise by more than the threshold; otherwise keep the stale
                 // max for P and l alike (exact in exact arithmetic, P <= 2^8).
-                const bool grow = (m_new - m_run) > kRescaleThreshold;
+                const bool grow = in_box && (m_new - m_run) > kRescaleThreshold;
                 if (__any_sync(0xffffffffu, grow)) {
                     if (kRot) {
                         // O_i holds P.V_i(j-1) only once that product is done
@@ -1277,24 +1332,42 @@ __device__ void softmax_role(const ArgsOf<KIND>& a, const Bars& bars, uint32_t t
             if (a.part_o != nullptr) {
                 // A part: the sum of values not yet divided, by the weights' unrounded sum.
                 const int part = t / a.pairs % cut_of<D>()->parts;
+                // 32 rows of 32 elements at a time go through 4 KB of the task's Q tile,
+                // which no product reads any more, so that a warp writes whole lines (a
+                // row a thread straight to memory took 12 k cycles for a tile of 128
+                // elements).
                 const int64_t at = ((static_cast<int64_t>(te.bh) * a.tiles + u) * kTcBM + trow) * a.part_pitch + part;
                 const float f = inv_l * l_exact;
-                float* dst = a.part_o + at * D;
+                const int lane = threadIdx.x % 32;
+                const uint32_t stored = __ballot_sync(0xffffffffu, valid);
+                const int64_t row_step = static_cast<int64_t>(a.part_pitch) * D;
+                float* dst = a.part_o + (at - lane * static_cast<int64_t>(a.part_pitch)) * D + 4 * (lane % 8);
+                uint8_t* stage = q_tiles + tile * TcLayout<D>::kQTileBytes + (warp % 4) * 4096;
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t x[32];
                     tmem_ld32(tO + c * 32, x);
                     tmem_wait_ld();
                     reg_fence(x);
-                    if (valid) {
+                    __syncwarp();
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            __stcg(reinterpret_cast<float4*>(dst + c * 32 + e),
-                                   make_float4(__uint_as_float(x[e]) * f, __uint_as_float(x[e + 1]) * f,
-                                               __uint_as_float(x[e + 2]) * f, __uint_as_float(x[e + 3]) * f));
+                    for (int e = 0; e < 8; ++e)
+                        *reinterpret_cast<float4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+                            make_float4(__uint_as_float(x[4 * e]) * f, __uint_as_float(x[4 * e + 1]) * f,
+                                        __uint_as_float(x[4 * e + 2]) * f, __uint_as_float(x[4 * e + 3]) * f);
+                    __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int r = 4 * e + lane / 8;
+                        const float4 y = *reinterpret_cast<const float4*>(stage + r * 128 + (((lane % 8) ^ (r & 7)) << 4));
+                        if ((stored >> r) & 1u) __stcg(reinterpret_cast<float4*>(dst + r * row_step + c * 32), y);
                     }
                 }
                 if (valid) __stcg(a.part_ml + at, make_float2(m_run, l_exact));
+                // The tile may be loaded again (through the async proxy).
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.q_empty[tile]);
                 tc_fence_before();
                 if constexpr (kRot) {
                     pv_base += static_cast<uint32_t>(nb);
@@ -1368,7 +1441,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_tc_kernel(const __grid
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.q_full[i], 1);
-            mbar_init(&bars.q_empty[i], 1);
+            mbar_init(&bars.q_empty[i], frees_q<KIND>(a) ? 4 : 1);
             mbar_init(&bars.o_full[i], 1);
             if (L::kRot) mbar_init(&bars.o_ready[i], 1);
         }
@@ -1391,22 +1464,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_tc_kernel(const __grid
         tmem_relinquish();
     }
     if constexpr (KIND == kRows) {
+        if (warp == 9 && lane < 3) tma_prefetch_desc(lane == 0 ? &a.tmap_q : (lane == 1 ? &a.tmap_k : &a.tmap_v));
         grid_dependency();
         if (warp == 0) {
-            Cut cut = {a.max_parts, a.part_tiles};
-            if (cut.tiles == 0) {
-                // From the length, which only the device knows: the cheapest of what the workspace has room for.
-                const int tiles = (visible_keys(a, 0, blockIdx.x == 0 && lane == 0) + kTcBN - 1) / kTcBN;
-                const int targets = a.sources * a.Hkv * a.pairs;
-                uint32_t best = 0xffffffffu;
-                for (int s = lane + 1; s <= a.max_parts; s += 32)
-                    best = min(best, split_cost(targets, tiles, gridDim.x, s) * 256u + static_cast<uint32_t>(s));
-                const int parts = static_cast<int>(__reduce_min_sync(0xffffffffu, best) % 256u);
-                cut.tiles = max((tiles + parts - 1) / parts, 1);
-                cut.parts = max((tiles + cut.tiles - 1) / cut.tiles, 1);
-                if (blockIdx.x == 0 && lane == 0) *a.part_count = cut.parts;
-            } else if (a.lens != nullptr && blockIdx.x == 0) {
-                for (int b = lane; b < a.sources; b += 32) visible_keys(a, b, true);
+            Cut cut;
+            if (a.part_o != nullptr) {
+                cut = choose_cut(a, blockIdx.x == 0);
+                if (blockIdx.x == 0 && lane == 0) *a.part_count = cut.tiles;
+            } else {
+                cut.parts = 1;
+                cut.tiles = 0x3fffffff;  // (of all keys)
+                if (a.lens != nullptr && blockIdx.x == 0)
+                    for (int b = lane; b < a.sources; b += 32) visible_keys(a, b, true);
             }
             if (lane == 0) *cut_of<D>() = cut;
         }
@@ -1421,7 +1490,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_tc_kernel(const __grid
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
     }
-    if (warp == 9 && lane == 0) {
+    if (KIND != kRows && warp == 9 && lane == 0) {
         tma_prefetch_desc(&a.tmap_q);
         tma_prefetch_desc(&a.tmap_k);
         tma_prefetch_desc(&a.tmap_v);
@@ -1433,7 +1502,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_tc_kernel(const __grid
 
     if (warp < 8) {
         regs_increase<kSoftmaxRegs>();
-        softmax_role<D, BF16, CAUSAL, KIND>(a, bars, tmem_base, abort_flag);
+        softmax_role<D, BF16, CAUSAL, KIND>(a, bars, smem + L::kQOff, tmem_base, abort_flag);
     } else {
         regs_decrease<kControlRegs>();
         if (warp == 8 || warp == 10) {  // the issuing warp and its helper

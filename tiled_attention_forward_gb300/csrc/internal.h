@@ -121,11 +121,10 @@ struct RowsArgs : TcArgs {  // N, BH, num_qblk, num_tasks and head_group are unu
     const int32_t* table;      // pages of the one source's keys, or nullptr
     float* part_o;             // fp32 [sources][Hkv][tiles][128][part_pitch][D], or nullptr: O and LSE are written
     float2* part_ml;           // .. [part_pitch]: max (log2 units) and sum of the weights
-    int32_t* part_count;       // receives the parts of a launch that chooses them itself
+    int32_t* part_count;       // receives the K/V tiles of a part, which the launch chooses
     int part_pitch;            // parts that the workspace has room for
     int max_parts;             // of those, the ones that the keys may be cut into
-    int part_tiles;            // K/V tiles of a part; 0: chosen by the length
-    int own_part;              // the last part of the workspace is joined too
+    int own_part;              // 1: the last part of the workspace is joined too
     int num_pages;
     int page_size;
     int piece;                 // keys of a copy
@@ -140,14 +139,6 @@ struct RowsArgs : TcArgs {  // N, BH, num_qblk, num_tasks and head_group are unu
     int tiles;                 // tiles of a K/V head of a source
     int pairs;                 // ceil(tiles / 2)
 };
-// What cutting the keys of `targets` tasks of `tiles` K/V tiles into s parts costs:
-// a task takes as long as its tiles and two more (its start and its epilogue), and
-// each part is read again when they are joined.
-__host__ __device__ inline uint32_t split_cost(int targets, int tiles, int ctas, int s) {
-    const int64_t waves = (static_cast<int64_t>(targets) * s + ctas - 1) / ctas;
-    const int64_t cost = 16 * waves * ((tiles + s - 1) / s + 2) + s;
-    return cost > 0xffffff ? 0xffffffu : static_cast<uint32_t>(cost);
-}
 constexpr int kMaxSplits = 128;
 constexpr int kSplitCtas = 152;  // CTAs that workspaces are sized for
 // Parts that `targets` tasks may be cut into: two waves of tasks.
