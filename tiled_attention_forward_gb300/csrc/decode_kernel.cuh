@@ -72,8 +72,6 @@ using DecodeArgsOf = std::conditional_t<
                        std::conditional_t<MODE == kWithPrefix, PrefixDecodeArgs, DecodeArgs>>>;
 
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
 constexpr int kPart = 16;                 // keys that lie in one page and take one pass of the products
 constexpr int kMaxCtas = 320;             // parts in the workspace: two per CTA
 constexpr int kAloneUnits = 2;            // longest target that one warp takes alone
@@ -178,14 +176,14 @@ __device__ __forceinline__ uint32_t as_u32(__half2 x) { return *reinterpret_cast
 // 4 bits: K codes (D/2 a key), K scales (D/8 a key), then V rows of codes and
 // scales, 16 bytes wider than the codes: lanes that take keys 2t of 8 bytes (4
 // at D = 64) then meet 32 different banks.
-template <int D, bool KV4, int NT>
+template <int D, bool KV4, int NT, int WARPS>
 struct Stage {
     // Keys of a warp's stage.  4 bits: two parts of 16, whose loop, votes and
     // addresses are paid once, where registers allow; 16 bits: one, as a stage
     // is 4 times as large.
     static constexpr int kKeys = KV4 && NT == 1 ? 32 : 16;
     static constexpr int kParts = kKeys / kPart;
-    static constexpr int kUnit = kWarps * kKeys;  // keys of a unit
+    static constexpr int kUnit = WARPS * kKeys;  // keys of a unit
     static constexpr int kCode = D / 2, kMeta = D / kKv4Group * 4;
     static constexpr int kVRow = KV4 ? kCode + 16 : 2 * D;
     static constexpr int kKMetaOff = kKeys * kCode;
@@ -193,20 +191,21 @@ struct Stage {
     static constexpr int kBytes = kVOff + kKeys * kVRow;
 };
 
-template <int D, bool KV4, int NT>
+template <int D, bool KV4, int NT, int WARPS>
 struct Config {
-    static constexpr int kStages = KV4 ? (NT == 1 ? 2 : 4) : 3;
-    static constexpr int kCtasPerSm = NT == 4 || (D == 128 && (NT == 2 || !KV4)) ? 1 : 2;
+    static constexpr int kWarps = WARPS, kThreads = 32 * WARPS;
+    static constexpr int kStages = KV4 ? (NT == 1 ? 2 : 4) : (WARPS == 6 ? 2 : 3);
+    static constexpr int kCtasPerSm = WARPS == 8 && (NT == 4 || (D == 128 && (NT == 2 || !KV4))) ? 1 : 2;
     static constexpr int kRows = 8 * NT;
     // What starting and joining a target costs, in units of keys.
-    static constexpr int kTargetCost = KV4 ? 2 : 4;
-    static constexpr int kRing = kWarps * kStages * Stage<D, KV4, NT>::kBytes;
+    static constexpr int kTargetCost = KV4 ? 2 : 32 / WARPS;
+    static constexpr int kRing = kWarps * kStages * Stage<D, KV4, NT, WARPS>::kBytes;
     // The warps' O is joined in the same memory.
     static constexpr int kPitch = D + 4;  // of a row of O there
     static constexpr int kJoin = kWarps * kRows * kPitch * 4;
     static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
     static_assert(kSmem * kCtasPerSm <= 224 * 1024, "shared memory budget");
-    static_assert(8 * kPitch * 4 <= kStages * Stage<D, KV4, NT>::kBytes, "a warp's O, eight rows at a time, in its ring");
+    static_assert(8 * kPitch * 4 <= kStages * Stage<D, KV4, NT, WARPS>::kBytes, "a warp's O, eight rows at a time, in its ring");
 };
 
 // A part of a cut sequence: per row the max (log2 units), the sum, then O.
@@ -241,16 +240,6 @@ __device__ __forceinline__ int cta_of(int64_t unit, int64_t units, int ctas) {
     return c;
 }
 
-// What an earlier kernel may have written; behind a prefix, whose kernel this one
-// may start beside, from L2.
-template <typename ARGS, typename T>
-__device__ __forceinline__ T read(const T* p) {
-    if constexpr (std::is_same_v<ARGS, SharedDecodeArgs>)
-        return __ldcg(p);
-    else
-        return *p;
-}
-
 // The prefix's keys, and the virtual keys that they take.
 struct Prefix {
     int keys, end;
@@ -261,7 +250,7 @@ __device__ __forceinline__ Prefix prefix_of(const PrefixDecodeArgs& a, bool repo
         if (report) atomicOr(&g_decode_error_word, 1u << kDevErrInvalidArg);
         len = len < 0 ? 0 : a.prefix_max;
     }
-    constexpr int kUnit = Stage<128, false, 1>::kUnit;  // of all 16-bit stages
+    constexpr int kUnit = 128;  // of the largest units of 16-bit keys
     return {len, (len + kUnit - 1) / kUnit * kUnit};
 }
 
@@ -276,11 +265,8 @@ __device__ __forceinline__ int visible_len(const ARGS& a, int b, bool report) {
         }
         return len;
     }
-    if constexpr (std::is_same_v<ARGS, PrefixDecodeArgs>) {
-        return prefix_of(a, false).end + visible_len(static_cast<const DecodeArgs&>(a), b, report);
-    }
     const int64_t most = a.table_width * a.page_size;
-    const int len = read<ARGS>(a.seq_lens + b);
+    const int len = a.seq_lens[b];
     if (len < 0 || len > most) {
         if (report) atomicOr(&g_decode_error_word, 1u << kDevErrInvalidArg);
         return len < 0 ? 0 : static_cast<int>(most);
@@ -325,9 +311,9 @@ __device__ __forceinline__ void store_out(const ARGS& a, int b, int kvh, int row
 }
 
 // ---- one warp's keys ----------------------------------------------------------
-template <int D, bool BF16, bool KV4, int NT>
+template <int D, bool BF16, bool KV4, int NT, int WARPS>
 struct Warp {
-    using S = Stage<D, KV4, NT>;
+    using S = Stage<D, KV4, NT, WARPS>;
     static constexpr int kQ = D / 16;   // k-steps of S^T, m-tiles of O^T
     uint32_t q[NT][kQ][2];              // B fragments of Q^T
     uint32_t qsum[NT];                  // 4 bits: (high, low) part of the sum of q over group t
@@ -336,8 +322,7 @@ struct Warp {
     float o[NT][kQ][4];
 
     // Query rows of K/V head kvh, row block rb.  Lane (g, t) = (lane/4, lane%4).
-    template <typename ARGS>
-    __device__ __forceinline__ void load_q(const ARGS& a, int b, int kvh, int rb) {
+    __device__ __forceinline__ void load_q(const DecodeArgs& a, int b, int kvh, int rb) {
         const int lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
         const int rows = (a.H / a.Hkv) * a.Nq;
 #pragma unroll
@@ -350,8 +335,8 @@ struct Warp {
             if constexpr (!KV4) {
 #pragma unroll
                 for (int kk = 0; kk < kQ; ++kk) {
-                    q[n][kk][0] = src ? read<ARGS>(reinterpret_cast<const uint32_t*>(src + 16 * kk + 2 * t)) : 0u;
-                    q[n][kk][1] = src ? read<ARGS>(reinterpret_cast<const uint32_t*>(src + 16 * kk + 8 + 2 * t)) : 0u;
+                    q[n][kk][0] = src ? *reinterpret_cast<const uint32_t*>(src + 16 * kk + 2 * t) : 0u;
+                    q[n][kk][1] = src ? *reinterpret_cast<const uint32_t*>(src + 16 * kk + 8 + 2 * t) : 0u;
                 }
                 f[n][0] = f[n][1] = fmaxf(a.scale_log2, kLeastFactor);
                 qsum[n] = 0u;
@@ -754,12 +739,13 @@ struct Warp {
     }
 };
 
-template <int D, bool BF16, bool KV4, int NT, bool ALONE, Mode MODE>
-__global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
+template <int D, bool BF16, bool KV4, int NT, bool ALONE, Mode MODE, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, Config<D, KV4, NT, WARPS>::kCtasPerSm)
     decode_kernel(const __grid_constant__ DecodeArgsOf<MODE> a) {
     static_assert(MODE == kCache || !KV4, "16-bit keys");
-    using C = Config<D, KV4, NT>;
-    using S = Stage<D, KV4, NT>;
+    using C = Config<D, KV4, NT, WARPS>;
+    using S = Stage<D, KV4, NT, WARPS>;
+    constexpr int kWarps = WARPS, kThreads = 32 * WARPS;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t s_scan[kWarps];
     __shared__ int s_most[kWarps];
@@ -772,20 +758,12 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
     const int row_blocks = (rows + C::kRows - 1) / C::kRows;
     const int per_key = a.Hkv * row_blocks;  // targets of one sequence
 
-    if constexpr (MODE == kBehindPrefix) {
-        // The kernel before this one, the prefix's, writes nothing that this one
-        // reads, and what came before that is complete once all its CTAs let this
-        // one start: only the end waits for it (wait_prefix).  What an earlier
-        // kernel may have written is read through L2.
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    } else {
-        grid_dependency();
-    }
-    auto wait_prefix = [&]() {
-        if constexpr (MODE == kBehindPrefix) asm volatile("griddepcontrol.wait;" ::: "memory");
-    };
+    grid_dependency();
     Prefix prefix = {0, 0};
     if constexpr (MODE == kWithPrefix) prefix = prefix_of(a, blockIdx.x == 0 && tid == 0);
+    auto visible_len = [&](const auto& args, int seq, bool report) {
+        return fattn::visible_len(args, seq, report) + (MODE == kWithPrefix ? prefix.end : 0);
+    };
     // All units of the call, and this CTA's share of them.  A target (K/V head
     // and row block of a sequence) counts C::kTargetCost units more than it has, so
     // that shares of many short sequences take no longer than others.
@@ -831,10 +809,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
     const int cta = blockIdx.x;
     const int ctas = static_cast<int>(min(min(static_cast<int64_t>(gridDim.x), units),
                                           max(units * kMaxParts / most, static_cast<int64_t>(1))));
-    if (cta >= ctas) {
-        wait_prefix();
-        return;
-    }
+    if (cta >= ctas) return;
     const int64_t begin = share_begin(units, cta, ctas), end = share_begin(units, cta + 1, ctas);
     // The sequence of unit `begin`: prefix sums, kThreads sequences at a time.
     int b;
@@ -882,7 +857,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
     uint32_t ring = smem_addr(smem) + warp * C::kStages * S::kBytes;
     const int page_shift = (a.page_size & (a.page_size - 1)) == 0 ? __ffs(a.page_size) - 1 : -1;
     const bool one_page = a.page_size % S::kKeys == 0;  // a stage never crosses pages
-    Warp<D, BF16, KV4, NT> w;
+    Warp<D, BF16, KV4, NT, WARPS> w;
     int64_t at = begin;
     int next_b = b;
     while (at < end) {
@@ -968,7 +943,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
         const int first = alone ? 0 : t0 * S::kUnit + warp * S::kKeys;
         const int last = alone ? (warp < batch ? my_len : 0) : min(len, t1 * S::kUnit);
         const int turns = first < last ? (last - first + stride - 1) / stride : 0;
-        const typename Warp<D, BF16, KV4, NT>::Source source = w.template source<DecodeArgsOf<MODE>>(a, kvh);
+        const typename Warp<D, BF16, KV4, NT, WARPS>::Source source = w.template source<DecodeArgsOf<MODE>>(a, kvh);
         struct Pages {
             int p[S::kParts];
         };
@@ -992,8 +967,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
                 if (u > 0 && one_page)
                     r.p[u] = r.p[0];
                 else
-                    r.p[u] = i < turns && k < last
-                                 ? read<DecodeArgsOf<MODE>>(table + (page_shift >= 0 ? k >> page_shift : k / a.page_size)) : 0;
+                    r.p[u] = i < turns && k < last ? table[page_shift >= 0 ? k >> page_shift : k / a.page_size] : 0;
             }
             return r;
         };
@@ -1076,7 +1050,7 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
             for (int i = 0; i < C::kStages - 1; ++i) start(i, early[i]);
             pages = early[C::kStages - 1];
         }
-        w.template load_q<DecodeArgsOf<MODE>>(a, my_b, kvh, rb);
+        w.load_q(a, my_b, kvh, rb);
         for (int i = 0; i < turns; ++i) {
             start(i + C::kStages - 1, pages);
             pages = pages_at(i + C::kStages);  // needed one turn later
@@ -1237,18 +1211,21 @@ __global__ void __launch_bounds__(kThreads, Config<D, KV4, NT>::kCtasPerSm)
         __syncthreads();  // the joined memory becomes the ring again
         b = next_b;
     }
-    wait_prefix();
 }
+
+// Warps of a CTA.
+template <int D, int NT, Mode MODE>
+constexpr int kWarpsOf = MODE == kBehindPrefix && D == 128 && NT == 1 ? 6 : 8;
 
 template <int D, bool BF16, bool KV4, int NT, bool ALONE, Mode MODE>
 cudaError_t launch_one(const DecodeArgsOf<MODE>& a, int sms, cudaStream_t s) {
-    using C = Config<D, KV4, NT>;
-    auto* fn = decode_kernel<D, BF16, KV4, NT, ALONE, MODE>;
+    using C = Config<D, KV4, NT, kWarpsOf<D, NT, MODE>>;
+    auto* fn = decode_kernel<D, BF16, KV4, NT, ALONE, MODE, C::kWarps>;
     static std::atomic<bool> done[kMaxDevices] = {};
     cudaError_t e = opt_in_smem_once(fn, C::kSmem, done);
     if (e != cudaSuccess) return e;
     const int grid = sms * C::kCtasPerSm < kMaxCtas ? sms * C::kCtasPerSm : kMaxCtas;
-    return launch_overlapped(fn, grid, kThreads, C::kSmem, s, a);
+    return launch_overlapped(fn, grid, C::kThreads, C::kSmem, s, a);
 }
 
 // Tiles of 8 query rows that share one pass over the keys.
@@ -1263,7 +1240,7 @@ template <int D, bool BF16, bool KV4, int NT, Mode MODE>
 cudaError_t launch_targets(const DecodeArgsOf<MODE>& a, int sms, cudaStream_t s) {
     if constexpr (NT <= 2) {
         const int64_t targets = static_cast<int64_t>(a.B) * a.Hkv;
-        if (targets >= 2 * sms * Config<D, KV4, NT>::kCtasPerSm) return launch_one<D, BF16, KV4, NT, true, MODE>(a, sms, s);
+        if (targets >= 2 * sms * Config<D, KV4, NT, kWarpsOf<D, NT, MODE>>::kCtasPerSm) return launch_one<D, BF16, KV4, NT, true, MODE>(a, sms, s);
     }
     return launch_one<D, BF16, KV4, NT, false, MODE>(a, sms, s);
 }

@@ -1435,9 +1435,6 @@ int fattn_decode_shared(const void* q, void* o, float* lse, const int64_t* strid
     a.B = static_cast<int>(B);
     a.Nq = static_cast<int>(Nq);
     a.share = static_cast<int>(H / Hkv);
-    const int grid = static_cast<int>(std::min<int64_t>(Hkv * t.pairs * most, sms));
-    if (rows_launch(a, static_cast<int>(D), bf16, grid, reinterpret_cast<cudaStream_t>(stream_h)) != cudaSuccess)
-        return FATTN_ERR_CUDA;
     d.part_o = a.part_o;
     d.part_ml = a.part_ml;
     d.part_pitch = pitch;
@@ -1447,7 +1444,10 @@ int fattn_decode_shared(const void* q, void* o, float* lse, const int64_t* strid
     d.n_i = t.n_i;
     d.n_h = t.n_h;
     d.tiles = a.tiles;
+    // The own keys first: their K and V would push the prefix's parts out of L2.
+    const int grid = static_cast<int>(std::min<int64_t>(Hkv * t.pairs * most, sms));
     cudaError_t e = decode_shared_launch(d, static_cast<int>(D), bf16, sms, reinterpret_cast<cudaStream_t>(stream_h));
+    if (e == cudaSuccess) e = rows_launch(a, static_cast<int>(D), bf16, grid, reinterpret_cast<cudaStream_t>(stream_h));
     if (e == cudaSuccess) e = rows_join_launch(a, static_cast<int>(D), bf16, reinterpret_cast<cudaStream_t>(stream_h));
     return e == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
 }

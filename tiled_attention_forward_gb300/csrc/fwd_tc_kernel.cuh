@@ -152,7 +152,7 @@ __device__ __forceinline__ Cut* cut_of() {
 // Rows: keys of a source that every row sees.
 __device__ __forceinline__ int visible_keys(const RowsArgs& a, int source, bool report) {
     if (a.lens == nullptr) return a.max_keys;
-    const int len = a.lens[source];
+    const int len = __ldcg(a.lens + source);
     if (len < 0 || len > a.max_keys) {
         if (report) atomicOr(&g_error_word, 1u << kDevErrInvalidArg);
         return len < 0 ? 0 : a.max_keys;
@@ -186,8 +186,10 @@ __device__ __forceinline__ Cut choose_cut(const RowsArgs& a, bool report) {
 #pragma unroll 1
     for (int waves = 1; waves <= 2; ++waves) {
         const int room = waves * ctas;
-        const int64_t even = (static_cast<int64_t>(total) * each + room - 1) / room;
-        int per = max(static_cast<int>(min(even, static_cast<int64_t>(most))), max(least, 1));
+        const int64_t all = static_cast<int64_t>(total) * each + room - 1;  // (a 64-bit division takes a microsecond)
+        int per = (all >> 31) == 0 ? static_cast<int>(static_cast<uint32_t>(all) / static_cast<uint32_t>(room))
+                                   : static_cast<int>(min(all / room, static_cast<int64_t>(most)));
+        per = max(min(per, most), max(least, 1));
         while (per < most && tasks(per) > room) per += max(per / 16, 1);
         per = min(per, most);
         const int cost = 16 * waves * (per + 2) + most / per;
@@ -590,7 +592,7 @@ __device__ void producer_role(const ArgsOf<KIND>& a, uint8_t* smem, const Bars& 
         if constexpr (KIND == kRows) {
             const int key = tk.start + j * kTcBN + static_cast<int>(threadIdx.x % 32) * a.piece;
             if (a.table == nullptr || j >= tk.nbmax || key >= tk.start + min(tk.n, (j + 1) * kTcBN)) return a.num_pages;
-            const int page = a.table[key / a.page_size];
+            const int page = __ldcg(a.table + key / a.page_size);
             if (static_cast<uint32_t>(page) < static_cast<uint32_t>(a.num_pages)) return page;
             atomicOr(&g_error_word, 1u << kDevErrInvalidArg);
             return a.num_pages;
@@ -657,10 +659,14 @@ __device__ void producer_role(const ArgsOf<KIND>& a, uint8_t* smem, const Bars& 
     };
 
     int t = static_cast<int>(blockIdx.x);
-    // Rows: past the parts that a shorter source does not have.
+    // Rows: the task, past the parts that a shorter source does not have.
+    Task ahead = {};
     auto skip_none = [&]() {
-        if constexpr (KIND == kRows)
-            while (t < num_tasks && decode_task<CAUSAL, L::kRot, KIND>(t, a).nbmax == 0) t = fetch();
+        while (KIND == kRows && t < num_tasks) {
+            ahead = decode_task<CAUSAL, L::kRot, KIND>(t, a);
+            if (ahead.nbmax > 0) break;
+            t = fetch();
+        }
     };
     skip_none();
     for (int kt = 0; ok; ++kt) {
@@ -669,7 +675,7 @@ __device__ void producer_role(const ArgsOf<KIND>& a, uint8_t* smem, const Bars& 
             break;
         }
         if (!publish(kt, t)) break;
-        const Task tk = decode_task<CAUSAL, L::kRot, KIND>(t, a);
+        const Task tk = KIND == kRows ? ahead : decode_task<CAUSAL, L::kRot, KIND>(t, a);
         const int kvh = KIND == kRows ? tk.bh % a.Hkv : kv_head_of(tk.bh, a.H, a.Hkv);
         int page = page_of(tk, 0);
         load_q(0, tk);
@@ -695,21 +701,22 @@ __device__ void producer_role(const ArgsOf<KIND>& a, uint8_t* smem, const Bars& 
         t = fetch();
         skip_none();
         if (t < num_tasks && elect_one_sync()) {
-            const Task nx = decode_task<CAUSAL, L::kRot, KIND>(t, a);
             if constexpr (KIND == kRows) {
                 for (int i = 0; i < 2; ++i) {
-                    const QBox q = q_box(a, nx, i);
-                    if (nx.q0 + i < a.tiles)
+                    const QBox q = q_box(a, ahead, i);
+                    if (ahead.q0 + i < a.tiles)
 #pragma unroll
                         for (int at = 0; at < L::kAtoms; ++at) tma_prefetch_4d(&a.tmap_q, at * 64, q.i, q.h, q.b);
                 }
-            } else
+            } else {
+                const Task nx = decode_task<CAUSAL, L::kRot, KIND>(t, a);
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (nx.q0 + i * kTcBM < nx.n)
+                for (int i = 0; i < 2; ++i)
+                    if (nx.q0 + i * kTcBM < nx.n)
 #pragma unroll
-                    for (int at = 0; at < L::kAtoms; ++at)
-                        tma_prefetch_3d(&a.tmap_q, at * 64, nx.start + nx.q0 + i * kTcBM, nx.bh);
+                        for (int at = 0; at < L::kAtoms; ++at)
+                            tma_prefetch_3d(&a.tmap_q, at * 64, nx.start + nx.q0 + i * kTcBM, nx.bh);
+            }
         }
         __syncwarp();
     }
@@ -1429,6 +1436,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_tc_kernel(const __grid
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     if ((smem_u32(smem_raw) & 1023u) != 0u) {
         if (threadIdx.x == 0) atomicOr(&g_error_word, 1u << kDevErrInternal);
+        if constexpr (KIND == kRows) asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
     }
     uint8_t* smem = smem_raw;
@@ -1465,7 +1473,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_tc_kernel(const __grid
     }
     if constexpr (KIND == kRows) {
         if (warp == 9 && lane < 3) tma_prefetch_desc(lane == 0 ? &a.tmap_q : (lane == 1 ? &a.tmap_k : &a.tmap_v));
-        grid_dependency();
+        // A prefix: the kernel before this one, of the own keys, writes nothing that
+        // this one reads or writes, and what came before that is complete once all
+        // its CTAs have let this one start: CTAs start as that one's end, and only
+        // their end waits for it.  (Tables are read through L2.)
+        if (a.own_part)
+            asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        else
+            grid_dependency();
         if (warp == 0) {
             Cut cut;
             if (a.part_o != nullptr) {
@@ -1537,6 +1552,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_tc_kernel(const __grid
             atomicExch(&ctr[0], 0u);
             atomicExch(&ctr[1], 0u);
         }
+    }
+    if constexpr (KIND == kRows) {
+        if (a.own_part) asm volatile("griddepcontrol.wait;" ::: "memory");
     }
 }
 
