@@ -183,6 +183,39 @@ def test_backward(dtype, D, case):
 
 
 @pytest.mark.parametrize("dtype,D", [("bf16", 128), ("fp16", 64)])
+def test_backward_many_blocks(dtype, D):
+    """So many key blocks and query tiles that none is cut into parts; entries without keys, of one key, of a tile."""
+    dt, lens = DT[dtype], [300, 0, 1, 128, 299, 129, 300, 257, 64, 300]
+    q, k, v, do, t = make(10, 8, 8, 260, 300, D, dt, 77, lens)
+    o, lse = fattn.fwd_cross(q, k, v, t)
+    dq, dk, dv = (torch.full(x.shape, math.nan, dtype=dt, device="cuda") for x in (q, k, v))
+    got = fattn.bwd_cross(q, k, v, o, lse, do, t, dq=dq, dk=dk, dv=dv)
+    ok()
+    args, scale = [x.cpu() for x in (q, k, v, do)], fattn._default_scale(D)
+    ref = M.cross_grads(*args, lens, scale)
+    for name, x, r, b in zip(("dq", "dk", "dv"), got, ref, M.cross_grad_bounds(*args, lens, scale, dt, ref)):
+        R.check(x, r, b, name)
+
+
+@pytest.mark.parametrize("case", [(1, 8, 1, 900, 100, [70]), (1, 32, 4, 3, 4000, None), (2, 2, 1, 130, 2000, [2000, 1])])
+def test_backward_cut_into_parts(case):
+    """Few key blocks of many query tiles, few query tiles of many key tiles (more parts than an entry has tiles)."""
+    B, H, Hkv, Nq, Nk, lens = case
+    q, k, v, do, t = make(B, H, Hkv, Nq, Nk, 64, torch.bfloat16, 78, lens)
+    lens = lens or [Nk] * B
+    o, lse = fattn.fwd_cross(q, k, v, t)
+    need = fattn.bwd_cross_workspace_bytes(B, H, Nq, Nk, 64, Hkv)
+    got = fattn.bwd_cross(q, k, v, o, lse, do, t, workspace=torch.full((need,), 255, dtype=torch.uint8, device="cuda"))
+    again = fattn.bwd_cross(q, k, v, o, lse, do, t)
+    ok()
+    assert all(torch.equal(x, y) for x, y in zip(got, again))
+    args = [x.cpu() for x in (q, k, v, do)]
+    ref = M.cross_grads(*args, lens, 0.125)
+    for name, x, r, b in zip(("dq", "dk", "dv"), got, ref, M.cross_grad_bounds(*args, lens, 0.125, torch.bfloat16, ref)):
+        R.check(x, r, b, name)
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("fp16", 64)])
 def test_backward_layouts_and_repeats(dtype, D):
     """Gradients as slices of a projection's gradient, contiguous inputs, a second run: the same bits."""
     dt = DT[dtype]

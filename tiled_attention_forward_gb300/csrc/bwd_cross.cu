@@ -2,83 +2,176 @@
 // length of their own, rows by strides; and the kernel of its row statistics.
 #include "bwd_tc_kernel.cuh"
 
+#include <algorithm>
+
 namespace fattn {
 namespace {
 
 // -LSE_i * log2(e) and -Delta_i, Delta_i = dO_i . O_i, into the padded workspace
 // [B*H][2][Npad]; rows past Nq, and rows that saw no key (LSE = -inf), get -inf
 // and 0.  A row is read as 16-byte pieces by D/8 lanes, kStatLoads such rows of O
-// and of dO in flight a lane.
+// and of dO in flight a lane; rows are taken in the order in which they lie in
+// memory (`heads_inner`: a token's heads one after the other).
 constexpr int kStatLoads = 4;
 template <int D>
 constexpr int kStatRows = (32 / (D / 8)) * kStatLoads;  // of a warp
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(256) cross_stats_kernel(const __grid_constant__ CrossBwdArgs a) {
+__global__ void __launch_bounds__(256) cross_stats_kernel(const __grid_constant__ CrossBwdArgs a, bool heads_inner) {
     constexpr int kLanes = D / 8, kRows = 32 / kLanes;
     const int64_t rows = static_cast<int64_t>(a.BH) * a.Npad;
-    const int64_t warp = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) / 32;
     const int lane = threadIdx.x % 32, piece = lane % kLanes;
-    uint4 o[kStatLoads], g[kStatLoads];
+    struct At {
+        uint32_t b, h, i;
+    };
+    auto at = [&](int64_t warp, int k) {  // (fewer than 2^31 rows of a batch entry: 32-bit divisions)
+        const int64_t row = warp * kStatRows<D> + k * kRows + lane / kLanes;
+        const uint32_t per_b = static_cast<uint32_t>(a.H) * a.Npad;
+        At x;
+        x.b = (row >> 32) == 0 ? static_cast<uint32_t>(row) / per_b : static_cast<uint32_t>(row / per_b);
+        const uint32_t rest = static_cast<uint32_t>(row - static_cast<int64_t>(x.b) * per_b);
+        if (heads_inner) {
+            x.i = rest / a.H;
+            x.h = rest - x.i * a.H;
+        } else {
+            x.h = rest / a.Npad;
+            x.i = rest - x.h * a.Npad;
+        }
+        if (row >= rows) x.b = 0xffffffffu;
+        return x;
+    };
     grid_dependency();
+    const int64_t warps = (rows + kStatRows<D> - 1) / kStatRows<D>, stride = static_cast<int64_t>(gridDim.x) * 8;
+    for (int64_t warp = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / 32; warp < warps; warp += stride) {
+        uint4 o[kStatLoads], g[kStatLoads];
 #pragma unroll
-    for (int k = 0; k < kStatLoads; ++k) {
-        const int64_t row = warp * kStatRows<D> + k * kRows + lane / kLanes;
-        o[k] = g[k] = make_uint4(0u, 0u, 0u, 0u);
-        const int64_t bh = row / a.Npad;
-        const int i = static_cast<int>(row - bh * a.Npad);
-        if (row < rows && i < a.N) {
-            const int64_t b = bh / a.H, h = bh - b * a.H;
-            o[k] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.o) + b * a.o_bs + h * a.o_hs +
-                                                   i * a.o_ns + 8 * piece);
-            g[k] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.dout) + b * a.do_bs + h * a.do_hs +
-                                                   i * a.do_ns + 8 * piece);
-        }
-    }
-#pragma unroll
-    for (int k = 0; k < kStatLoads; ++k) {
-        const uint32_t x[4] = {o[k].x, o[k].y, o[k].z, o[k].w}, y[4] = {g[k].x, g[k].y, g[k].z, g[k].w};
-        float sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            float2 u, v;
-            if (BF16) {
-                u = make_float2(__uint_as_float(x[w] << 16), __uint_as_float(x[w] & 0xffff0000u));
-                v = make_float2(__uint_as_float(y[w] << 16), __uint_as_float(y[w] & 0xffff0000u));
-            } else {
-                u = __half22float2(*reinterpret_cast<const __half2*>(&x[w]));
-                v = __half22float2(*reinterpret_cast<const __half2*>(&y[w]));
+        for (int k = 0; k < kStatLoads; ++k) {
+            const At x = at(warp, k);
+            o[k] = g[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (x.b != 0xffffffffu && x.i < static_cast<uint32_t>(a.N)) {
+                o[k] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.o) + x.b * a.o_bs + x.h * a.o_hs +
+                                                       x.i * a.o_ns + 8 * piece);
+                g[k] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.dout) + x.b * a.do_bs +
+                                                       x.h * a.do_hs + x.i * a.do_ns + 8 * piece);
             }
-            sum = fmaf(u.x, v.x, sum);
-            sum = fmaf(u.y, v.y, sum);
         }
 #pragma unroll
-        for (int d = kLanes / 2; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        const int64_t row = warp * kStatRows<D> + k * kRows + lane / kLanes;
-        if (piece == 0 && row < rows) {
-            const int64_t bh = row / a.Npad;
-            const int i = static_cast<int>(row - bh * a.Npad);
-            float nlse2 = -INFINITY, ndelta = 0.f;
-            if (i < a.N) {
-                const float lse = a.lse[bh * a.N + i];
-                if (lse != -INFINITY) {
-                    nlse2 = -lse * 1.4426950408889634f;
-                    ndelta = -sum;
+        for (int k = 0; k < kStatLoads; ++k) {
+            const uint32_t x[4] = {o[k].x, o[k].y, o[k].z, o[k].w}, y[4] = {g[k].x, g[k].y, g[k].z, g[k].w};
+            float sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                float2 u, v;
+                if (BF16) {
+                    u = make_float2(__uint_as_float(x[w] << 16), __uint_as_float(x[w] & 0xffff0000u));
+                    v = make_float2(__uint_as_float(y[w] << 16), __uint_as_float(y[w] & 0xffff0000u));
+                } else {
+                    u = __half22float2(*reinterpret_cast<const __half2*>(&x[w]));
+                    v = __half22float2(*reinterpret_cast<const __half2*>(&y[w]));
                 }
+                sum = fmaf(u.x, v.x, sum);
+                sum = fmaf(u.y, v.y, sum);
             }
-            a.ws[bh * 2 * a.Npad + i] = nlse2;
-            a.ws[(bh * 2 + 1) * a.Npad + i] = ndelta;
+#pragma unroll
+            for (int d = kLanes / 2; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            const At r = at(warp, k);
+            if (piece == 0 && r.b != 0xffffffffu) {
+                const int64_t bh = static_cast<int64_t>(r.b) * a.H + r.h;
+                float nlse2 = -INFINITY, ndelta = 0.f;
+                if (r.i < static_cast<uint32_t>(a.N)) {
+                    const float lse = a.lse[bh * a.N + r.i];
+                    if (lse != -INFINITY) {
+                        nlse2 = -lse * 1.4426950408889634f;
+                        ndelta = -sum;
+                    }
+                }
+                a.ws[bh * 2 * a.Npad + r.i] = nlse2;
+                a.ws[(bh * 2 + 1) * a.Npad + r.i] = ndelta;
+            }
         }
     }
 }
 
+// Adds the parts, in order: a thread 8 elements of a row, of dk and dv (blocks of
+// row tiles first) and then of dq.  Rows that no part has are zeros.
+constexpr int kAddThreads = 256;
 template <int D, bool BF16>
-cudaError_t launch_all(const CrossBwdArgs& a, cudaStream_t s) {
+__global__ void __launch_bounds__(kAddThreads) cross_add_kernel(const __grid_constant__ CrossBwdArgs a, int64_t kv_rows) {
+    constexpr int kPieces = D / 8;
+    grid_dependency();
+    int64_t row = (static_cast<int64_t>(blockIdx.x) * kAddThreads + threadIdx.x) / kPieces;
+    const int d = 8 * (threadIdx.x % kPieces);
+    const bool kv = row < kv_rows;  // rows of dk and dv: [B * Hkv][Nk][2]
+    if (!kv) row -= kv_rows;
+    const int n = kv ? a.Nk : a.N, heads = kv ? a.Hkv : a.H, accs = kv ? 2 : 1;
+    const int acc = static_cast<int>(row % accs);
+    row /= accs;
+    const int64_t bh = row / n;
+    const int i = static_cast<int>(row - bh * n);
+    const int64_t b = bh / heads, h = bh - b * heads;
+    if (b >= a.BH / a.H || (!kv && a.parts_q == 1)) return;
+    int keys = a.Nk;
+    if (a.lens != nullptr) keys = min(max(a.lens[b], 0), a.Nk);
+    const int parts = kv ? a.parts_k : a.parts_q, padded = kv ? a.tiles_k * kBT : a.Npad, tiles = (keys + kBT - 1) / kBT;
+    const int64_t step = (kv ? static_cast<int64_t>(a.BHkv) : a.BH) * padded * accs * D;
+    const float* src = (kv ? a.part_kv : a.part_q) + ((bh * padded + i) * accs + acc) * D + d;
+    float sum[8] = {};
+    const int upto = kv && i >= keys ? 0 : parts;
+#pragma unroll 4
+    for (int p = 0; p < upto; ++p) {
+        if (!kv && part_begin(tiles, p, parts) == part_begin(tiles, p + 1, parts)) continue;
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(src + p * step));
+        const float4 y = __ldcg(reinterpret_cast<const float4*>(src + p * step + 4));
+        sum[0] += x.x, sum[1] += x.y, sum[2] += x.z, sum[3] += x.w;
+        sum[4] += y.x, sum[5] += y.y, sum[6] += y.z, sum[7] += y.w;
+    }
+    uint16_t* dst;
+    if (!kv)
+        dst = static_cast<uint16_t*>(a.dq) + b * a.dq_bs + h * a.dq_hs + i * a.dq_ns;
+    else if (acc == 0)
+        dst = static_cast<uint16_t*>(a.dv) + b * a.dv_bs + h * a.dv_hs + i * a.dv_ns;
+    else
+        dst = static_cast<uint16_t*>(a.dk) + b * a.dk_bs + h * a.dk_hs + i * a.dk_ns;
+    *reinterpret_cast<uint4*>(dst + d) = make_uint4(pack16(sum[0], sum[1], BF16), pack16(sum[2], sum[3], BF16),
+                                                    pack16(sum[4], sum[5], BF16), pack16(sum[6], sum[7], BF16));
+}
+
+// launch_overlapped with a second argument.
+template <typename X>
+cudaError_t launch_two(void (*fn)(CrossBwdArgs, X), unsigned grid, unsigned threads, cudaStream_t s,
+                       const CrossBwdArgs& a, X x) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, a, x);
+    if (e != cudaSuccess) (void)cudaGetLastError();
+    return e;
+}
+
+template <int D, bool BF16>
+cudaError_t launch_add(const CrossBwdArgs& a, cudaStream_t s) {
+    if (a.parts_k == 1 && a.parts_q == 1) return cudaSuccess;
+    const int64_t kv_rows = a.parts_k > 1 ? static_cast<int64_t>(a.BHkv) * a.Nk * 2 : 0;
+    const int64_t rows = kv_rows + (a.parts_q > 1 ? static_cast<int64_t>(a.BH) * a.N : 0);
+    return launch_two(cross_add_kernel<D, BF16>, static_cast<unsigned>((rows * (D / 8) + kAddThreads - 1) / kAddThreads),
+                      kAddThreads, s, a, kv_rows);
+}
+
+template <int D, bool BF16>
+cudaError_t launch_all(const CrossBwdArgs& a, int sms, cudaStream_t s) {
     // (Without queries the key kernel, without keys the query kernel writes zeros.)
     const int64_t warps = (static_cast<int64_t>(a.BH) * a.Npad + kStatRows<D> - 1) / kStatRows<D>;
     cudaError_t e = cudaSuccess;
     if (a.N > 0 && a.Nk > 0) {
-        e = launch_overlapped(cross_stats_kernel<D, BF16>, static_cast<unsigned>((warps + 7) / 8), 256, 0, s, a);
+        const int64_t blocks = (warps + 7) / 8;
+        e = launch_two(cross_stats_kernel<D, BF16>, static_cast<unsigned>(std::min<int64_t>(blocks, 16 * sms)), 256, s, a,
+                       a.o_hs < a.o_ns);
         if (e != cudaSuccess) return e;
     }
     static std::atomic<bool> kv_done[kMaxDevices] = {};
@@ -86,24 +179,27 @@ cudaError_t launch_all(const CrossBwdArgs& a, cudaStream_t s) {
     auto* kkv = attn_bwd_kernel<D, BF16, true, false, true>;
     if ((e = opt_in_smem_once(kkv, BwdLayout<D, true>::kBytes, kv_done)) != cudaSuccess) return e;
     if (a.tiles_k > 0) {
-        e = launch_overlapped(kkv, static_cast<unsigned>(a.tiles_k * a.BHkv), kBwdThreads, BwdLayout<D, true>::kBytes, s, a);
+        e = launch_overlapped(kkv, static_cast<unsigned>(a.tiles_k * a.BHkv * a.parts_k), kBwdThreads, BwdLayout<D, true>::kBytes, s, a);
         if (e != cudaSuccess) return e;
     }
     if (a.num_tiles == 0) return cudaSuccess;
     auto* kq = attn_bwd_kernel<D, BF16, false, false, true>;
     if ((e = opt_in_smem_once(kq, BwdLayout<D, false>::kBytes, q_done)) != cudaSuccess) return e;
-    const unsigned grid_q = static_cast<unsigned>(a.num_tiles * a.BH);
+    const unsigned grid_q = static_cast<unsigned>(a.num_tiles * a.BH * a.parts_q);
     // (Behind the key kernel only: it reads and writes without waiting first.)
-    if (a.tiles_k > 0) return launch_overlapped(kq, grid_q, kBwdThreads, BwdLayout<D, false>::kBytes, s, a);
+    if (a.tiles_k > 0) {
+        e = launch_overlapped(kq, grid_q, kBwdThreads, BwdLayout<D, false>::kBytes, s, a);
+        return e == cudaSuccess ? launch_add<D, BF16>(a, s) : e;
+    }
     kq<<<grid_q, kBwdThreads, BwdLayout<D, false>::kBytes, s>>>(a);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t bwd_cross_launch(const CrossBwdArgs& a, int D, bool bf16, cudaStream_t s) {
-    if (D == 128) return bf16 ? launch_all<128, true>(a, s) : launch_all<128, false>(a, s);
-    return bf16 ? launch_all<64, true>(a, s) : launch_all<64, false>(a, s);
+cudaError_t bwd_cross_launch(const CrossBwdArgs& a, int D, bool bf16, int sms, cudaStream_t s) {
+    if (D == 128) return bf16 ? launch_all<128, true>(a, sms, s) : launch_all<128, false>(a, sms, s);
+    return bf16 ? launch_all<64, true>(a, sms, s) : launch_all<64, false>(a, sms, s);
 }
 
 cudaError_t bwd_cross_read_and_clear_error_word(uint32_t* out) {

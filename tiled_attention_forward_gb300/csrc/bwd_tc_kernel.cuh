@@ -191,21 +191,32 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32
 // (ascending kb, descending qt); otherwise head-major.
 struct BwdTask {
     int bh, blk, j0, n, per_head;
+    int it0, part;  // cross: the first of the task's inner tiles, and the part of the gradient that they make
 };
 
-// Cross: key blocks behind the batch entry's keys, and all query tiles of an entry
-// without keys, have no inner tiles (n = 0).
+// Cross: the inner tiles of a block are cut into parts (a.parts_k, a.parts_q) where
+// there are few blocks, each a task; key blocks behind the batch entry's keys, all
+// query tiles of an entry without keys, and parts of an entry with fewer key tiles
+// than parts have no inner tiles (n = 0).
+// Cross: the first of n inner tiles that belongs to part p of `parts`.
+__device__ __forceinline__ int part_begin(int n, int p, int parts) {
+    return static_cast<int>(static_cast<int64_t>(n) * p / parts);
+}
+
 template <bool KV, bool CAUSAL, bool CROSS>
 __device__ __forceinline__ BwdTask bwd_task(const BwdArgsOf<CROSS>& a, int keys) {
     BwdTask t;
     const int idx = blockIdx.x;
     if constexpr (CROSS) {
-        const int blocks = KV ? a.tiles_k : a.num_tiles;
-        t.bh = idx / blocks;
-        t.blk = idx % blocks;
+        const int blocks = KV ? a.tiles_k : a.num_tiles, parts = KV ? a.parts_k : a.parts_q;
+        t.part = idx % parts;
+        t.bh = idx / parts / blocks;
+        t.blk = idx / parts % blocks;
         t.j0 = 0;
         t.per_head = KV ? a.num_tiles : (keys + kBT - 1) / kBT;
-        t.n = KV ? (t.blk * kBT < keys ? t.per_head * (a.H / a.Hkv) : 0) : t.per_head;
+        const int all = KV ? (t.blk * kBT < keys ? t.per_head * (a.H / a.Hkv) : 0) : t.per_head;
+        t.it0 = part_begin(all, t.part, parts);
+        t.n = part_begin(all, t.part + 1, parts) - t.it0;
         return t;
     }
     const int heads = KV ? a.BHkv : a.BH;
@@ -237,11 +248,16 @@ __device__ __forceinline__ int bwd_query_head(const BwdArgs& a, const BwdTask& t
     return b * a.H + hk * G + it / tk.per_head;
 }
 
+template <bool KV>
+__device__ __forceinline__ int parts_of(const BwdArgs&) { return 1; }
+template <bool KV>
+__device__ __forceinline__ int parts_of(const CrossBwdArgs& a) { return KV ? a.parts_k : a.parts_q; }
+
 // Cross: keys that the CTA's batch entry sees.
 template <bool KV>
 __device__ __forceinline__ int bwd_visible_keys(const CrossBwdArgs& a) {
     if (a.lens == nullptr) return a.Nk;
-    const int b = KV ? blockIdx.x / a.tiles_k / a.Hkv : blockIdx.x / a.num_tiles / a.H;
+    const int b = KV ? blockIdx.x / a.parts_k / a.tiles_k / a.Hkv : blockIdx.x / a.parts_q / a.num_tiles / a.H;
     const int len = a.lens[b];
     if (len < 0 || len > a.Nk) {
         if (threadIdx.x == 0) atomicOr(&g_error_word, 1u << kDevErrInvalidArg);
@@ -303,9 +319,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_kernel(const __grid_c
     int keys = a.N;  // keys that the task sees
     if constexpr (CROSS) keys = bwd_visible_keys<KV>(a);
     const BwdTask tk = bwd_task<KV, CAUSAL, CROSS>(a, keys);
+    auto at_tile = [&](int it) { return CROSS ? it + tk.it0 : it; };
     if constexpr (CROSS) {
         if (tk.n == 0) {
-            bwd_store_zeros<D, KV>(a, tk);
+            if ((KV ? a.parts_k : a.parts_q) == 1) bwd_store_zeros<D, KV>(a, tk);  // (else: the kernel that adds the parts)
             wait_key_kernel();
             return;
         }
@@ -377,8 +394,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_kernel(const __grid_c
             int issued_a = 0, issued_b = 0;
             bool ok = true;
             for (int it = 0; it < tk.n && ok; ++it) {
-                const int row0 = (tk.j0 + it % tk.per_head) * kBT;
-                const int qh = KV ? bwd_query_head(a, tk, it) : tk.bh;  // head of the Q / dO tiles
+                const int row0 = (tk.j0 + at_tile(it) % tk.per_head) * kBT;
+                const int qh = KV ? bwd_query_head(a, tk, at_tile(it)) : tk.bh;  // head of the Q / dO tiles
                 const int sa = it % L::kSA;
                 if (it >= L::kSA) {
                     ok = mbar_wait_bounded(&bars.empty_a[sa], ((it / L::kSA) - 1) & 1u, bars.abort_flag,
@@ -514,13 +531,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_kernel(const __grid_c
             if (!issuer && ok)
                 ok = warp_wait(&bars.full_a[it % L::kSA], (it / L::kSA) & 1u, bars.abort_flag, a.timeout_ns);
             if (CROSS && !KV && !issuer && ok)
-                bwd_zero_tail<D>(smem + L::kRingA + (it % L::kSA) * L::kSlotA, keys - it * kBT);
+                bwd_zero_tail<D>(smem + L::kRingA + (it % L::kSA) * L::kSlotA, keys - at_tile(it) * kBT);
         };
         auto wait_b = [&](int it) {
             if (!KV && !issuer && ok)
                 ok = warp_wait(&bars.full_b[it % L::kSBm], (it / L::kSBm) & 1u, bars.abort_flag, a.timeout_ns);
             if (CROSS && !KV && !issuer && ok)
-                bwd_zero_tail<D>(smem + L::kRingB + (it % L::kSBm) * L::kSlotB, keys - it * kBT);
+                bwd_zero_tail<D>(smem + L::kRingB + (it % L::kSBm) * L::kSlotB, keys - at_tile(it) * kBT);
         };
         auto sync = [&]() {
             ok = named_barrier_and(kSyncBar, kSyncThreads, ok);
@@ -721,7 +738,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_kernel(const __grid_c
             }
         }
         for (int it = 0; !KV && it < tk.n && ok; ++it) {
-            const int j = tk.j0 + it;
+            const int j = tk.j0 + at_tile(it);
             ok = warp_wait(&bars.s_full[it & 1], (it >> 1) & 1u, bars.abort_flag, a.timeout_ns);
             if (!ok) {
                 failed_at = it;
@@ -798,9 +815,43 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_kernel(const __grid_c
         // Each warp converts half of the D columns of its 32 rows.
         const bool fin = warp_wait(bars.done, 0u, nullptr, a.timeout_ns);
         tc_fence_after();
+        if constexpr (CROSS) {
+            if ((KV ? a.parts_k : a.parts_q) > 1) {
+                // A part, in fp32: 32 rows of 32 elements at a time through 4 KB of the
+                // resident tiles' memory, which no product reads any more, so that a
+                // warp writes whole lines.
+                const int blocks = KV ? a.tiles_k : a.num_tiles, heads = KV ? a.BHkv : a.BH, accs = KV ? 2 : 1;
+                uint8_t* stage = smem + L::kOuter + warp * 4096;
+                const int64_t first = ((static_cast<int64_t>(tk.part) * heads + tk.bh) * blocks + tk.blk) * kBT + quarter * 32;
+#pragma unroll 1
+                for (int x = 0; x < accs * (D / 64); ++x) {
+                    const int acc = x / (D / 64), c = half * (D / 64) + x % (D / 64);
+                    uint32_t v[32];
+                    tmem_ld32((acc == 0 ? t_acc1 : t_acc2) + lane_off + c * 32, v);
+                    tmem_wait_ld();
+                    reg_fence(v);
+                    const float mul = (KV && acc == 0) ? 1.f : a.scale;
+                    __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        *reinterpret_cast<float4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+                            make_float4(__uint_as_float(v[4 * e]) * mul, __uint_as_float(v[4 * e + 1]) * mul,
+                                        __uint_as_float(v[4 * e + 2]) * mul, __uint_as_float(v[4 * e + 3]) * mul);
+                    __syncwarp();
+                    float* dst = (KV ? a.part_kv : a.part_q) + (first * accs + acc) * D + c * 32 + 4 * (lane % 8);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int rr = 4 * e + lane / 8;
+                        const float4 y = *reinterpret_cast<const float4*>(stage + rr * 128 + (((lane % 8) ^ (rr & 7)) << 4));
+                        if (fin) __stcg(reinterpret_cast<float4*>(dst + static_cast<int64_t>(rr) * accs * D), y);
+                    }
+                }
+            }
+        }
+        const bool whole = !CROSS || parts_of<KV>(a) == 1;
         const int64_t out_row = static_cast<int64_t>(tk.bh) * a.N + row;  // (dense)
 #pragma unroll 1
-        for (int acc = 0; acc < (KV ? 2 : 1); ++acc) {
+        for (int acc = 0; whole && acc < (KV ? 2 : 1); ++acc) {
             // KV: acc 0 = dV (no scale), acc 1 = dK (x scale); dQ: acc 0 = dQ (x scale)
             const uint32_t tacc = (acc == 0 ? t_acc1 : t_acc2) + lane_off;
             const float mul = (KV && acc == 0) ? 1.f : a.scale;

@@ -399,6 +399,46 @@ int cross_splits(int64_t B, int64_t Hkv, const RowTiles& t, int64_t Nk) {
     return static_cast<int>(std::min<int64_t>(max_splits(B * Hkv * t.pairs), std::max<int64_t>(ceil_div(Nk, 2 * kTcBN), 1)));
 }
 
+// The gradients of cross attention: parts that the inner tiles of a key block (query
+// tiles of all heads of its group) and of a query tile (key tiles) are cut into, so
+// that few blocks fill the GPU.
+struct CrossParts {
+    int64_t k = 1, q = 1;             // parts
+    int64_t kv_rows = 0, q_rows = 0;  // rows of parts (dk and dv alike; dq)
+};
+CrossParts cross_parts(int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t Nk) {
+    CrossParts p;
+    const int64_t tq = ceil_div(Nq, 128), tk = ceil_div(Nk, 128);
+    if (tq == 0 || tk == 0) return p;
+    const int64_t blocks_k = B * Hkv * tk, blocks_q = B * H * tq, inner_k = H / Hkv * tq, inner_q = tk;
+    // The tasks of both kernels run side by side.  In units of 0.4 us: an inner tile of
+    // a key block takes 4, of a query tile 3; a task's start and end 12, a part 3 more,
+    // and adding the parts 8.  With more tasks than SMs the last ones start late.
+    static constexpr int kTry[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 24, 32, 48, 64};
+    int64_t least = INT64_MAX;
+    for (int64_t sk : kTry) {
+        if (sk > 1 && (sk > inner_k || blocks_k * sk > 2 * kSplitCtas)) break;
+        const int64_t dk = 4 * ceil_div(inner_k, sk) + 12 + (sk > 1 ? 3 : 0);
+        for (int64_t sq : kTry) {
+            if (sq > 1 && (sq > inner_q || blocks_q * sq > 2 * kSplitCtas)) break;
+            const int64_t dq = 3 * ceil_div(inner_q, sq) + 12 + (sq > 1 ? 3 : 0), tasks = blocks_k * sk + blocks_q * sq;
+            const int64_t longest = std::max(dk, dq);
+            int64_t cost = longest;
+            if (tasks > kSplitCtas)
+                cost = std::max(cost, (blocks_k * sk * dk + blocks_q * sq * dq) / kSplitCtas + longest / 2);
+            if (sk > 1 || sq > 1) cost += 8;
+            if (cost < least) {
+                least = cost;
+                p.k = sk;
+                p.q = sq;
+            }
+        }
+    }
+    if (p.k > 1) p.kv_rows = p.k * B * Hkv * tk * 128;
+    if (p.q > 1) p.q_rows = p.q * B * H * tq * 128;
+    return p;
+}
+
 // A shared prefix of up to `keys` tokens: whether every sequence reads it for itself,
 // in one launch of the decode kernel.  Where one does it is read once anyway.
 constexpr int64_t kReadByEach = 64ll << 20;
@@ -1567,7 +1607,9 @@ int fattn_fwd_cross(const void* q, const void* k, const void* v, void* o, float*
 int64_t fattn_bwd_cross_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t Nk, int64_t D) {
     if (B <= 0 || H <= 0 || Nq <= 0 || Nk < 0 || validate_cross(B, H, Hkv, Nq, Nk, D, 1.f, FATTN_BF16) != FATTN_OK)
         return 0;
-    return fattn_bwd_workspace_bytes(B, H, Nq);
+    const int64_t stats = fattn_bwd_workspace_bytes(B, H, Nq);
+    const CrossParts p = cross_parts(B, H, Hkv, Nq, Nk);
+    return stats <= 0 ? 0 : stats + p.kv_rows * 2 * D * 4 + p.q_rows * D * 4;
 }
 
 int fattn_bwd_cross(const void* q, const void* k, const void* v, const void* o, const void* dout, const float* lse,
@@ -1611,6 +1653,7 @@ int fattn_bwd_cross(const void* q, const void* k, const void* v, const void* o, 
         if (ptrs[j] && views_overlap(small[2], range_of(rows[j]))) return FATTN_ERR_INVALID_ARG;
     if (views_overlap(small[2], small[0]) || views_overlap(small[2], small[1])) return FATTN_ERR_INVALID_ARG;
     const int64_t tiles_q = ceil_div(Nq, 128), tiles_k = ceil_div(Nk, 128);
+    // (Blocks are cut into parts only where there are few.)
     if (tiles_q * B * H > 0x7fffffffll || tiles_k * B * Hkv > 0x7fffffffll || tiles_q * (H / Hkv) > 0x7fffffffll)
         return FATTN_ERR_UNSUPPORTED;
     int sms = 0;
@@ -1640,6 +1683,11 @@ int fattn_bwd_cross(const void* q, const void* k, const void* v, const void* o, 
     a.timeout_ns = kDefaultTimeoutNs;
     a.Nk = static_cast<int>(Nk);
     a.tiles_k = static_cast<int>(tiles_k);
+    const CrossParts parts = cross_parts(B, H, Hkv, Nq, Nk);
+    a.parts_k = static_cast<int>(parts.k);
+    a.parts_q = static_cast<int>(parts.q);
+    a.part_kv = a.ws + std::max<int64_t>(fattn_bwd_workspace_bytes(B, H, Nq), 0) / 4;
+    a.part_q = a.part_kv + parts.kv_rows * 2 * D;
     a.lens = kv_lens;
     a.o = o;
     a.dout = dout;
@@ -1649,7 +1697,7 @@ int fattn_bwd_cross(const void* q, const void* k, const void* v, const void* o, 
     a.dq_bs = strides[15], a.dq_hs = strides[16], a.dq_ns = strides[17];
     a.dk_bs = strides[18], a.dk_hs = strides[19], a.dk_ns = strides[20];
     a.dv_bs = strides[21], a.dv_hs = strides[22], a.dv_ns = strides[23];
-    const cudaError_t e = bwd_cross_launch(a, static_cast<int>(D), bf16, reinterpret_cast<cudaStream_t>(stream_h));
+    const cudaError_t e = bwd_cross_launch(a, static_cast<int>(D), bf16, sms, reinterpret_cast<cudaStream_t>(stream_h));
     return e == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
 }
 

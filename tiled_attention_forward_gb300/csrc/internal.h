@@ -224,6 +224,9 @@ cudaError_t bwd_read_and_clear_error_word(uint32_t* out);
 struct CrossBwdArgs : BwdArgs {  // tmaps {D, Nq or Nk, heads, B}; N = Nq, num_tiles = Npad / 128
     int Nk;
     int tiles_k;               // ceil(Nk / 128)
+    int parts_k, parts_q;      // parts that the inner tiles of a key block / a query tile are cut into
+    float* part_kv;            // fp32 [parts_k][B*Hkv][tiles_k * 128][dv, dk][D], where parts_k > 1
+    float* part_q;             // fp32 [parts_q][B*H][Npad][D], where parts_q > 1
     const int32_t* lens;       // visible keys of each batch entry, or nullptr: Nk
     int64_t dq_bs, dq_hs, dq_ns, dk_bs, dk_hs, dk_ns, dv_bs, dv_hs, dv_ns;  // element strides
     const void* o;             // the row statistics' inputs, by strides
@@ -231,7 +234,7 @@ struct CrossBwdArgs : BwdArgs {  // tmaps {D, Nq or Nk, heads, B}; N = Nq, num_t
     const float* lse;
     int64_t o_bs, o_hs, o_ns, do_bs, do_hs, do_ns;
 };
-cudaError_t bwd_cross_launch(const CrossBwdArgs& a, int D, bool bf16, cudaStream_t s);
+cudaError_t bwd_cross_launch(const CrossBwdArgs& a, int D, bool bf16, int sms, cudaStream_t s);
 cudaError_t bwd_cross_read_and_clear_error_word(uint32_t* out);
 
 // ---- rotation by positions with several axes, rotate.cu ----------------------------
