@@ -44,15 +44,21 @@ __global__ void __launch_bounds__(256) cross_stats_kernel(const __grid_constant_
     const int64_t warps = (rows + kStatRows<D> - 1) / kStatRows<D>, stride = static_cast<int64_t>(gridDim.x) * 8;
     for (int64_t warp = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / 32; warp < warps; warp += stride) {
         uint4 o[kStatLoads], g[kStatLoads];
+        float lse[kStatLoads];
+        int64_t dst[kStatLoads];  // of the row's first statistic; < 0: no row
 #pragma unroll
         for (int k = 0; k < kStatLoads; ++k) {
             const At x = at(warp, k);
+            const int64_t bh = static_cast<int64_t>(x.b) * a.H + x.h;
             o[k] = g[k] = make_uint4(0u, 0u, 0u, 0u);
+            lse[k] = -INFINITY;
+            dst[k] = x.b == 0xffffffffu ? -1 : bh * 2 * a.Npad + x.i;
             if (x.b != 0xffffffffu && x.i < static_cast<uint32_t>(a.N)) {
                 o[k] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.o) + x.b * a.o_bs + x.h * a.o_hs +
                                                        x.i * a.o_ns + 8 * piece);
                 g[k] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.dout) + x.b * a.do_bs +
                                                        x.h * a.do_hs + x.i * a.do_ns + 8 * piece);
+                if (piece == 0) lse[k] = a.lse[bh * a.N + x.i];
             }
         }
 #pragma unroll
@@ -74,19 +80,10 @@ __global__ void __launch_bounds__(256) cross_stats_kernel(const __grid_constant_
             }
 #pragma unroll
             for (int d = kLanes / 2; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-            const At r = at(warp, k);
-            if (piece == 0 && r.b != 0xffffffffu) {
-                const int64_t bh = static_cast<int64_t>(r.b) * a.H + r.h;
-                float nlse2 = -INFINITY, ndelta = 0.f;
-                if (r.i < static_cast<uint32_t>(a.N)) {
-                    const float lse = a.lse[bh * a.N + r.i];
-                    if (lse != -INFINITY) {
-                        nlse2 = -lse * 1.4426950408889634f;
-                        ndelta = -sum;
-                    }
-                }
-                a.ws[bh * 2 * a.Npad + r.i] = nlse2;
-                a.ws[(bh * 2 + 1) * a.Npad + r.i] = ndelta;
+            if (piece == 0 && dst[k] >= 0) {
+                const bool none = lse[k] == -INFINITY;
+                a.ws[dst[k]] = none ? -INFINITY : -lse[k] * 1.4426950408889634f;
+                a.ws[dst[k] + a.Npad] = none ? 0.f : -sum;
             }
         }
     }

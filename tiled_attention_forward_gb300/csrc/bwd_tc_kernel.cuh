@@ -248,11 +248,6 @@ __device__ __forceinline__ int bwd_query_head(const BwdArgs& a, const BwdTask& t
     return b * a.H + hk * G + it / tk.per_head;
 }
 
-template <bool KV>
-__device__ __forceinline__ int parts_of(const BwdArgs&) { return 1; }
-template <bool KV>
-__device__ __forceinline__ int parts_of(const CrossBwdArgs& a) { return KV ? a.parts_k : a.parts_q; }
-
 // Cross: keys that the CTA's batch entry sees.
 template <bool KV>
 __device__ __forceinline__ int bwd_visible_keys(const CrossBwdArgs& a) {
@@ -816,69 +811,87 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_kernel(const __grid_c
         const bool fin = warp_wait(bars.done, 0u, nullptr, a.timeout_ns);
         tc_fence_after();
         if constexpr (CROSS) {
-            if ((KV ? a.parts_k : a.parts_q) > 1) {
-                // A part, in fp32: 32 rows of 32 elements at a time through 4 KB of the
-                // resident tiles' memory, which no product reads any more, so that a
-                // warp writes whole lines.
-                const int blocks = KV ? a.tiles_k : a.num_tiles, heads = KV ? a.BHkv : a.BH, accs = KV ? 2 : 1;
-                uint8_t* stage = smem + L::kOuter + warp * 4096;
-                const int64_t first = ((static_cast<int64_t>(tk.part) * heads + tk.bh) * blocks + tk.blk) * kBT + quarter * 32;
+            // Rows leave through 4 KB a warp of the resident tiles' memory, which no
+            // product reads any more, so that a warp writes whole rows: fp32 parts 32
+            // elements at a time, gradients its half of them.
+            const int heads = KV ? a.Hkv : a.H, accs = KV ? 2 : 1;
+            const bool cut = (KV ? a.parts_k : a.parts_q) > 1;
+            uint8_t* stage = smem + L::kOuter + warp * 4096;
+            const int row0 = blk0 + quarter * 32;
 #pragma unroll 1
-                for (int x = 0; x < accs * (D / 64); ++x) {
-                    const int acc = x / (D / 64), c = half * (D / 64) + x % (D / 64);
+            for (int acc = 0; acc < accs; ++acc) {
+                const float mul = (KV && acc == 0) ? 1.f : a.scale;
+                float* part = (KV ? a.part_kv : a.part_q) +
+                              ((((static_cast<int64_t>(tk.part) * (KV ? a.BHkv : a.BH) + tk.bh) * (KV ? a.tiles_k : a.num_tiles)) *
+                                    kBT + row0) * accs + acc) * D;
+#pragma unroll 1
+                for (int c = 0; c < D / 64; ++c) {
                     uint32_t v[32];
-                    tmem_ld32((acc == 0 ? t_acc1 : t_acc2) + lane_off + c * 32, v);
+                    tmem_ld32((acc == 0 ? t_acc1 : t_acc2) + lane_off + (half * (D / 64) + c) * 32, v);
                     tmem_wait_ld();
                     reg_fence(v);
-                    const float mul = (KV && acc == 0) ? 1.f : a.scale;
-                    __syncwarp();
+                    if (cut) {
+                        __syncwarp();
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        *reinterpret_cast<float4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
-                            make_float4(__uint_as_float(v[4 * e]) * mul, __uint_as_float(v[4 * e + 1]) * mul,
-                                        __uint_as_float(v[4 * e + 2]) * mul, __uint_as_float(v[4 * e + 3]) * mul);
-                    __syncwarp();
-                    float* dst = (KV ? a.part_kv : a.part_q) + (first * accs + acc) * D + c * 32 + 4 * (lane % 8);
+                        for (int e = 0; e < 8; ++e)
+                            *reinterpret_cast<float4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+                                make_float4(__uint_as_float(v[4 * e]) * mul, __uint_as_float(v[4 * e + 1]) * mul,
+                                            __uint_as_float(v[4 * e + 2]) * mul, __uint_as_float(v[4 * e + 3]) * mul);
+                        __syncwarp();
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int rr = 4 * e + lane / 8;
-                        const float4 y = *reinterpret_cast<const float4*>(stage + rr * 128 + (((lane % 8) ^ (rr & 7)) << 4));
-                        if (fin) __stcg(reinterpret_cast<float4*>(dst + static_cast<int64_t>(rr) * accs * D), y);
+                        for (int e = 0; e < 8; ++e) {
+                            const int rr = 4 * e + lane / 8;
+                            const float4 y = *reinterpret_cast<const float4*>(stage + rr * 128 + (((lane % 8) ^ (rr & 7)) << 4));
+                            if (fin)
+                                __stcg(reinterpret_cast<float4*>(part + static_cast<int64_t>(rr) * accs * D +
+                                                                 (half * (D / 64) + c) * 32 + 4 * (lane % 8)), y);
+                        }
+                        continue;
                     }
+                    if (c == 0) __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint4 y;
+                        y.x = pack16(__uint_as_float(v[8 * e]) * mul, __uint_as_float(v[8 * e + 1]) * mul, BF16);
+                        y.y = pack16(__uint_as_float(v[8 * e + 2]) * mul, __uint_as_float(v[8 * e + 3]) * mul, BF16);
+                        y.z = pack16(__uint_as_float(v[8 * e + 4]) * mul, __uint_as_float(v[8 * e + 5]) * mul, BF16);
+                        y.w = pack16(__uint_as_float(v[8 * e + 6]) * mul, __uint_as_float(v[8 * e + 7]) * mul, BF16);
+                        *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * c + e) ^ (lane & 7)) << 4)) = y;
+                    }
+                }
+                if (cut) continue;
+                __syncwarp();
+                constexpr int kPieces = D / 16;  // of 16 bytes in a half row
+                const int b = tk.bh / heads, h = tk.bh - b * heads;
+                const int64_t ns = KV ? (acc == 0 ? a.dv_ns : a.dk_ns) : a.dq_ns;
+                uint16_t* base = static_cast<uint16_t*>(KV ? (acc == 0 ? a.dv : a.dk) : a.dq) +
+                                 b * (KV ? (acc == 0 ? a.dv_bs : a.dk_bs) : a.dq_bs) +
+                                 h * (KV ? (acc == 0 ? a.dv_hs : a.dk_hs) : a.dq_hs) + half * (D / 2) + 8 * (lane % kPieces);
+#pragma unroll
+                for (int e = 0; e < kPieces; ++e) {
+                    const int rr = e * (32 / kPieces) + lane / kPieces;
+                    uint4 y = *reinterpret_cast<const uint4*>(stage + rr * 128 + (((lane % kPieces) ^ (rr & 7)) << 4));
+                    // (a key that no row sees: its accumulator may be anything)
+                    if (KV && row0 + rr >= keys) y = make_uint4(0u, 0u, 0u, 0u);
+                    if (fin && row0 + rr < (KV ? a.Nk : a.N)) *reinterpret_cast<uint4*>(base + (row0 + rr) * ns) = y;
                 }
             }
         }
-        const bool whole = !CROSS || parts_of<KV>(a) == 1;
-        const int64_t out_row = static_cast<int64_t>(tk.bh) * a.N + row;  // (dense)
+        const int64_t out_row = static_cast<int64_t>(tk.bh) * a.N + row;
 #pragma unroll 1
-        for (int acc = 0; whole && acc < (KV ? 2 : 1); ++acc) {
+        for (int acc = 0; !CROSS && acc < (KV ? 2 : 1); ++acc) {
             // KV: acc 0 = dV (no scale), acc 1 = dK (x scale); dQ: acc 0 = dQ (x scale)
             const uint32_t tacc = (acc == 0 ? t_acc1 : t_acc2) + lane_off;
             const float mul = (KV && acc == 0) ? 1.f : a.scale;
             void* base = KV ? (acc == 0 ? a.dv : a.dk) : a.dq;
             uint8_t* orow = reinterpret_cast<uint8_t*>(base) + out_row * D * 2;
-            if constexpr (CROSS) {
-                const int heads = KV ? a.Hkv : a.H, b = tk.bh / heads, h = tk.bh % heads;
-                const int64_t bs = KV ? (acc == 0 ? a.dv_bs : a.dk_bs) : a.dq_bs;
-                const int64_t hs = KV ? (acc == 0 ? a.dv_hs : a.dk_hs) : a.dq_hs;
-                const int64_t ns = KV ? (acc == 0 ? a.dv_ns : a.dk_ns) : a.dq_ns;
-                orow = reinterpret_cast<uint8_t*>(base) + 2 * (b * bs + h * hs + row * ns);
-            }
 #pragma unroll 1
             for (int c = half * (D / 64); c < (half + 1) * (D / 64); ++c) {
                 uint32_t v[32];
                 tmem_ld32(tacc + c * 32, v);  // warp-collective: every lane, whatever its row
                 tmem_wait_ld();
                 reg_fence(v);
-                bool stored = row < a.N;
-                if constexpr (CROSS && KV) {
-                    stored = row < a.Nk;
-                    if (row >= keys) {  // a key that no row sees (its accumulator may be anything)
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = 0u;
-                    }
-                }
-                if (fin && stored) {
+                if (fin && row < a.N) {
                     uint32_t pk[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
