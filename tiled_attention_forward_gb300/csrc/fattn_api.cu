@@ -1759,7 +1759,7 @@ int fattn_rotate(const void* q, const void* k, void* q_out, void* k_out, const i
     st = current_sm_count(&sms);
     if (st != FATTN_OK) return st;
     for (int t = 0; t < 2; ++t) {
-        a.x[t] = ptrs[t];
+        a.x[t] = const_cast<void*>(ptrs[t]);
         a.y[t] = const_cast<void*>(ptrs[2 + t]);
         a.x_bs[t] = strides[3 * t], a.x_hs[t] = strides[3 * t + 1], a.x_ns[t] = strides[3 * t + 2];
         a.y_bs[t] = strides[6 + 3 * t], a.y_hs[t] = strides[7 + 3 * t], a.y_ns[t] = strides[8 + 3 * t];

@@ -240,7 +240,7 @@ cudaError_t bwd_cross_read_and_clear_error_word(uint32_t* out);
 // ---- rotation by positions with several axes, rotate.cu ----------------------------
 constexpr int kMaxAxes = 8;
 struct RotateArgs {
-    const void* x[2];      // q and k [B][heads][N][D] by strides (k: or nullptr)
+    void* x[2];            // q and k [B][heads][N][D] by strides (k: or nullptr)
     void* y[2];
     int64_t x_bs[2], x_hs[2], x_ns[2], y_bs[2], y_hs[2], y_ns[2];
     int heads[2];

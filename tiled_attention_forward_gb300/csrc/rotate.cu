@@ -10,7 +10,14 @@
 // Bound by memory (2 x 2 bytes an element, three fp32 operations).  A thread has
 // eight pairs of a token, 16 elements in two 16-byte pieces, for a number of
 // heads: the angles are read once and stay in registers, nothing is exchanged
-// between threads, and the rows of kAtOnce heads are on their way at once.
+// between threads, and the rows of kAtOnce heads are on their way at once.  Which
+// pieces a thread has is chosen such that neighbours have neighbouring ones
+// (interleaved pairs by 32 bytes a thread took 62.5 us where these take 58).
+//
+// Measured (GB300): 2 x 8192 tokens of 32 + 8 heads, D = 128, from a projection into
+// dense tensors (344 MB), 56 us = 6.1 TB/s; 4 x 1000 tokens of 16 + 16 heads, D = 64,
+// 8.0 us, 17 tokens 3.1, which is the launch.  Two heads at once and eight blocks of
+// 128 threads an SM: four heads and three blocks of 256 took 57.6 and 9.3 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -21,8 +28,9 @@ namespace {
 
 __device__ uint32_t g_rotate_error_word;
 
-constexpr int kThreads = 256;
-constexpr int kAtOnce = 4;  // heads whose rows are on their way
+constexpr int kThreads = 128;
+constexpr int kBlocksPerSm = 8;
+constexpr int kAtOnce = 2;  // heads whose rows are on their way
 
 template <bool BF16>
 __device__ __forceinline__ void unpack(const uint4& r, float (&x)[8]) {
@@ -56,98 +64,117 @@ __device__ __forceinline__ uint4 pack(const float (&x)[8]) {
 }
 
 // The two pieces of a row turn: halves, u[e] with v[e] by angle e; interleaved,
-// u[2e] with u[2e+1] by angle e and v's by angle 4 + e.
-template <bool BF16, bool INTERLEAVED>
-__device__ __forceinline__ void turn(uint4& p, uint4& q, const float (&co)[8], const float (&si)[8]) {
+// each piece by itself, u[2e] with u[2e+1] by angle e and v's by angle 4 + e.
+template <bool BF16>
+__device__ __forceinline__ void turn_halves(uint4& p, uint4& q, const float (&co)[8], const float (&si)[8]) {
     float u[8], v[8], x[8], y[8];
     unpack<BF16>(p, u);
     unpack<BF16>(q, v);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        if (INTERLEAVED) {
-            const float sg = (e & 1) ? 1.f : -1.f;
-            x[e] = fmaf(u[e ^ 1], sg * si[e / 2], u[e] * co[e / 2]);
-            y[e] = fmaf(v[e ^ 1], sg * si[4 + e / 2], v[e] * co[4 + e / 2]);
-        } else {
-            x[e] = fmaf(-v[e], si[e], u[e] * co[e]);
-            y[e] = fmaf(u[e], si[e], v[e] * co[e]);
-        }
+        x[e] = fmaf(-v[e], si[e], u[e] * co[e]);
+        y[e] = fmaf(u[e], si[e], v[e] * co[e]);
     }
     p = pack<BF16>(x);
     q = pack<BF16>(y);
 }
+template <bool BF16>
+__device__ __forceinline__ void turn_pairs(uint4& p, const float* co, const float* si) {
+    float u[8], x[8];
+    unpack<BF16>(p, u);
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        x[e] = fmaf(-u[e + 1], si[e / 2], u[e] * co[e / 2]);
+        x[e + 1] = fmaf(u[e], si[e / 2], u[e + 1] * co[e / 2]);
+    }
+    p = pack<BF16>(x);
+}
 
 template <int D, bool BF16, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant__ RotateArgs a) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) rotate_kernel(const __grid_constant__ RotateArgs a) {
     constexpr int kLanes = D / 16;             // threads of a token
     constexpr int kTokens = kThreads / kLanes;  // tokens of a block
     const int p = threadIdx.x % kLanes;
     const int64_t token = static_cast<int64_t>(blockIdx.x) * kTokens + threadIdx.x / kLanes;
     grid_dependency();
     if (token >= a.tokens) return;
-    for (int ax = 0; ax < a.axes; ++ax) {
-        const int at = a.pos[ax * a.tokens + token];
-        if (at < 0 || at >= a.max_pos) {  // the token's rows are left as they were
-            if (p == 0 && blockIdx.y == 0) atomicOr(&g_rotate_error_word, 1u << kDevErrInvalidArg);
-            return;
-        }
-    }
-    const bool turns = p < a.rot / 16;
-    float co[8], si[8];
-    if (turns) {
-        const uint64_t which = *reinterpret_cast<const uint64_t*>(a.axis + 8 * p);
-        if (which == (which & 0xffull) * 0x0101010101010101ull) {  // all on one axis
-            const int64_t at = static_cast<int64_t>(a.pos[(which & 0xffull) * a.tokens + token]) * (a.rot / 2) + 8 * p;
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const float4 c = *reinterpret_cast<const float4*>(a.cos + at + 4 * u);
-                const float4 s = *reinterpret_cast<const float4*>(a.sin + at + 4 * u);
-                co[4 * u] = c.x, co[4 * u + 1] = c.y, co[4 * u + 2] = c.z, co[4 * u + 3] = c.w;
-                si[4 * u] = s.x, si[4 * u + 1] = s.y, si[4 * u + 2] = s.z, si[4 * u + 3] = s.w;
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int64_t row = a.pos[((which >> (8 * e)) & 0xffull) * a.tokens + token];
-                co[e] = a.cos[row * (a.rot / 2) + 8 * p + e];
-                si[e] = a.sin[row * (a.rot / 2) + 8 * p + e];
-            }
-        }
-        if (a.inverse) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) si[e] = -si[e];
-        }
-    }
-    // The two pieces of a row: partners where it turns in halves, else neighbours.
-    const int first = turns && !INTERLEAVED ? 8 * p : 16 * p;
-    const int apart = turns && !INTERLEAVED ? a.rot / 2 : 8;
+    // The two pieces of a row that this thread has, such that a token's threads have
+    // neighbouring ones.  Halves: partners, or two that do not turn.  Interleaved:
+    // any two, each of which turns or not.
+    const int half = a.rot / 16;
+    const bool turns = INTERLEAVED ? p < 2 * half : p < half;  // the first piece
+    const bool second_turns = INTERLEAVED ? p + kLanes < 2 * half : turns;
+    const int first = INTERLEAVED || turns ? 8 * p : 8 * (half + p);
+    const int apart = INTERLEAVED ? 8 * kLanes : (turns ? 8 * half : 8 * (kLanes - half));
     const int64_t b = token / a.N, n = token - b * a.N;
     // This block's heads, numbered over q and k.
     const int all = a.heads[0] + a.heads[1];
-    const int per = (all + gridDim.y - 1) / gridDim.y;
+    const int per = ((all + gridDim.y - 1) / gridDim.y + kAtOnce - 1) / kAtOnce * kAtOnce;
     const int begin = blockIdx.y * per, end = min(all, begin + per);
+    auto row_of = [&](int h, void* const (&p)[2], const int64_t (&bs)[2], const int64_t (&hs)[2], const int64_t (&ns)[2]) {
+        const int k = h >= a.heads[0];
+        return static_cast<uint16_t*>(p[k]) + b * bs[k] + n * ns[k] + (h - (k ? a.heads[0] : 0)) * hs[k] + first;
+    };
+    // Their first rows are on their way before the token's positions and angles,
+    // which depend on one another, have come.
+    uint4 u[kAtOnce], v[kAtOnce];
+    auto load = [&](int h0) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        const int from = max(begin - (t ? a.heads[0] : 0), 0), to = min(end - (t ? a.heads[0] : 0), a.heads[t]);
-        const uint16_t* x = static_cast<const uint16_t*>(a.x[t]) + b * a.x_bs[t] + n * a.x_ns[t] + first;
-        uint16_t* y = static_cast<uint16_t*>(a.y[t]) + b * a.y_bs[t] + n * a.y_ns[t] + first;
-        for (int h0 = from; h0 < to; h0 += kAtOnce) {
-            uint4 u[kAtOnce], v[kAtOnce];
+        for (int i = 0; i < kAtOnce; ++i) {
+            const uint16_t* src = row_of(min(h0 + i, end - 1), a.x, a.x_bs, a.x_hs, a.x_ns);
+            u[i] = __ldcs(reinterpret_cast<const uint4*>(src));
+            v[i] = __ldcs(reinterpret_cast<const uint4*>(src + apart));
+        }
+    };
+    if (begin >= end) return;
+    load(begin);
+    bool outside = false;
+    for (int ax = 0; ax < a.axes; ++ax) {
+        const int at = a.pos[ax * a.tokens + token];
+        outside = outside || at < 0 || at >= a.max_pos;
+    }
+    if (outside) {  // the token's rows are left as they were
+        if (p == 0 && blockIdx.y == 0) atomicOr(&g_rotate_error_word, 1u << kDevErrInvalidArg);
+        return;
+    }
+    // Angles: of pairs 8p .. 8p + 7, or interleaved of each piece's four.
+    float co[8], si[8];
 #pragma unroll
-            for (int i = 0; i < kAtOnce; ++i) {
-                if (h0 + i >= to) break;
-                const uint16_t* src = x + (h0 + i) * a.x_hs[t];
-                u[i] = __ldcs(reinterpret_cast<const uint4*>(src));
-                v[i] = __ldcs(reinterpret_cast<const uint4*>(src + apart));
+    for (int g = 0; g < 2; ++g) {
+        const int i0 = INTERLEAVED ? 4 * p + g * 4 * kLanes : 8 * p + 4 * g;
+        if (!(g == 0 ? turns : second_turns)) continue;
+        const uint32_t which = *reinterpret_cast<const uint32_t*>(a.axis + i0);
+        float4 c, s;
+        if (which == (which & 0xffu) * 0x01010101u) {  // all on one axis
+            const int64_t at = static_cast<int64_t>(a.pos[(which & 0xffu) * a.tokens + token]) * (a.rot / 2) + i0;
+            c = *reinterpret_cast<const float4*>(a.cos + at);
+            s = *reinterpret_cast<const float4*>(a.sin + at);
+        } else {
+            int64_t at[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                at[e] = static_cast<int64_t>(a.pos[((which >> (8 * e)) & 0xffu) * a.tokens + token]) * (a.rot / 2) + i0 + e;
+            c = make_float4(a.cos[at[0]], a.cos[at[1]], a.cos[at[2]], a.cos[at[3]]);
+            s = make_float4(a.sin[at[0]], a.sin[at[1]], a.sin[at[2]], a.sin[at[3]]);
+        }
+        const float sg = a.inverse ? -1.f : 1.f;
+        co[4 * g] = c.x, co[4 * g + 1] = c.y, co[4 * g + 2] = c.z, co[4 * g + 3] = c.w;
+        si[4 * g] = sg * s.x, si[4 * g + 1] = sg * s.y, si[4 * g + 2] = sg * s.z, si[4 * g + 3] = sg * s.w;
+    }
+    for (int h0 = begin; h0 < end; h0 += kAtOnce) {
+        if (h0 > begin) load(h0);
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            if (h0 + i >= end) break;
+            if constexpr (INTERLEAVED) {
+                if (turns) turn_pairs<BF16>(u[i], co, si);
+                if (second_turns) turn_pairs<BF16>(v[i], co + 4, si + 4);
+            } else if (turns) {
+                turn_halves<BF16>(u[i], v[i], co, si);
             }
-#pragma unroll
-            for (int i = 0; i < kAtOnce; ++i) {
-                if (h0 + i >= to) break;
-                if (turns) turn<BF16, INTERLEAVED>(u[i], v[i], co, si);
-                uint16_t* dst = y + (h0 + i) * a.y_hs[t];
-                *reinterpret_cast<uint4*>(dst) = u[i];
-                *reinterpret_cast<uint4*>(dst + apart) = v[i];
-            }
+            uint16_t* dst = row_of(h0 + i, a.y, a.y_bs, a.y_hs, a.y_ns);
+            *reinterpret_cast<uint4*>(dst) = u[i];
+            *reinterpret_cast<uint4*>(dst + apart) = v[i];
         }
     }
 }
@@ -155,12 +182,21 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant_
 template <int D, bool BF16>
 cudaError_t launch_one(const RotateArgs& a, int sms, cudaStream_t s) {
     const int64_t blocks = (a.tokens + kThreads / (D / 16) - 1) / (kThreads / (D / 16));
-    // Heads are dealt to so many blocks that there are four a SM, a turn's rows at least each.
+    // Heads are dealt to so many blocks that the waves of blocks, each as long as its
+    // heads and two turns more (the angles), are shortest; two parts also where they
+    // take an eighth more than one, as their starts spread out (rotation of the 2 x
+    // 8192 tokens above: 56.1 us, one part 58.0).
     const int heads = a.heads[0] + a.heads[1];
-    int64_t parts = (4 * sms + blocks - 1) / blocks;
-    const int64_t most = (heads + kAtOnce - 1) / kAtOnce;
-    if (parts > most) parts = most;
-    if (parts < 1) parts = 1;
+    const int64_t wave = static_cast<int64_t>(kBlocksPerSm) * sms;
+    int64_t parts = 1, least = INT64_MAX;
+    for (int64_t p = 1; p <= (heads + kAtOnce - 1) / kAtOnce && p <= 64; ++p) {
+        const int64_t per = (heads + p - 1) / p, turns = (per + kAtOnce - 1) / kAtOnce + 2;
+        const int64_t cost = (blocks * p + wave - 1) / wave * turns;
+        if (cost < least || (p == 2 && 8 * cost <= 9 * least)) {
+            least = cost;
+            parts = p;
+        }
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(parts));
     cfg.blockDim = dim3(kThreads);
