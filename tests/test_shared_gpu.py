@@ -62,6 +62,11 @@ def check(args, rows, scale, o, lse, what=""):
         R.check(lse[b].cpu()[~none], rl[~none], bl[~none], "%s LSE of %d" % (what, b))
 
 
+def spare_for(B, Hkv, D, page, once):
+    """Unused entries behind the prefix's pages: so many that the prefix could be long enough to be read once for all."""
+    return (170 << 20) // ((B - 1) * Hkv * 4 * D * page) + 1 if once and B > 1 else 2
+
+
 CASES = [
     # B, H, Hkv, page, prefix, own lengths, Nq
     (1, 4, 2, 16, 1, [1], 1), (3, 8, 2, 16, 130, [5, 17, 1], 1), (2, 4, 1, 48, 257, [50, 0], 1), (4, 4, 4, 80, 128, [3, 90, 2, 1], 2),
@@ -71,23 +76,26 @@ CASES = [
 ]
 
 
+@pytest.mark.parametrize("once", [False, True])
 @pytest.mark.parametrize("case", CASES)
 @pytest.mark.parametrize("dtype,D", [("bf16", 128), ("fp16", 64), ("bf16", 64), ("fp16", 128)])
-def test_shared(dtype, D, case):
+def test_shared(dtype, D, case, once):
+    """Read by every sequence for itself, and once for all (which the table's width decides)."""
     B, H, Hkv, page, prefix, lens, Nq = case
-    args, rows = make(B, H, Hkv, D, DT[dtype], page, prefix, lens, Nq, prefix + B, spare=2)
+    args, rows = make(B, H, Hkv, D, DT[dtype], page, prefix, lens, Nq, prefix + B, spare=spare_for(B, Hkv, D, page, once))
     o, lse = fattn.decode_shared(**args)
     ok()
     check(args, rows, fattn._default_scale(D), o, lse, str(case))
 
 
+@pytest.mark.parametrize("once", [False, True])
 @pytest.mark.parametrize("dtype,D", [("bf16", 128), ("fp16", 64)])
-def test_as_decode_over_the_joined_tables(dtype, D):
+def test_as_decode_over_the_joined_tables(dtype, D, once):
     """A prefix of whole pages: decode with the prefix's pages in every table computes the same."""
-    args, rows = make(6, 8, 2, D, DT[dtype], 32, 960, [1, 40, 200, 7, 32, 64], 2, 3)
+    args, rows = make(6, 8, 2, D, DT[dtype], 32, 960, [1, 40, 200, 7, 32, 64], 2, 3, spare=spare_for(6, 2, D, 32, once))
     o, lse = fattn.decode_shared(**args)
     B = 6
-    table = torch.cat([args["prefix_table"][None].expand(B, -1), args["block_table"]], 1).contiguous()
+    table = torch.cat([args["prefix_table"][None, :30].expand(B, -1), args["block_table"]], 1).contiguous()
     o2, lse2 = fattn.decode(args["q"], args["k_pages"], args["v_pages"], table, args["seq_lens"] + 960)
     ok()
     check(args, rows, fattn._default_scale(D), o, lse)
@@ -103,9 +111,11 @@ def test_no_prefix_is_decode():
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
-def test_layouts_workspace_contents_and_repeats():
+@pytest.mark.parametrize("once", [False, True])
+def test_layouts_workspace_contents_and_repeats(once):
     """q and o by strides, K and V pages in one tensor, workspaces of any contents, no lse: the same bits."""
-    args, rows = make(5, 8, 2, 128, torch.bfloat16, 16, 600, [1, 30, 2, 99, 16], 2, 5, fill=0.25)
+    args, rows = make(5, 8, 2, 128, torch.bfloat16, 16, 600, [1, 30, 2, 99, 16], 2, 5, fill=0.25,
+                      spare=spare_for(5, 2, 128, 16, once))
     o, lse = fattn.decode_shared(**args)
     kv = torch.stack([args["k_pages"], args["v_pages"]], 1)
     q = torch.empty(5, 2, 11, 128, dtype=torch.bfloat16, device="cuda")
@@ -136,7 +146,7 @@ def test_lengths_and_pages_out_of_range():
     got = fattn.decode_shared(**dict(args, prefix_len=torch.tensor([-3], dtype=torch.int32).cuda()))
     torch.cuda.synchronize()
     assert fattn.get_device_status() == 1 and torch.equal(got[0], none[0])
-    for bad in (-1, args["k_pages"].shape[0], 2 ** 31 - 1):  # its keys and values are zeros
+    for bad in (-1, -2, -2 ** 31, args["k_pages"].shape[0], 2 ** 31 - 1):  # its keys and values are zeros
         table = args["prefix_table"].clone()
         table[4] = bad
         got = fattn.decode_shared(**dict(args, prefix_table=table))
@@ -148,11 +158,35 @@ def test_lengths_and_pages_out_of_range():
         check(args, zeroed, 0.125, *got, "page %d" % bad)
 
 
-def test_long_pool():
+def test_pages_of_a_long_prefix_out_of_range():
+    """The same where the prefix's keys are read once, a tile and more behind the bad page."""
+    args, rows = make(70, 8, 4, 64, torch.float16, 16, 2600, [3 + i % 7 for i in range(70)], 1, 8, fill=0.0)
+    full = fattn.decode_shared(**args)
+    ok()
+    check(args, rows, 0.125, *full)
+    for at, bad in ((0, -1), (9, -2 ** 31), (100, 10 ** 6), (162, -2)):
+        table = args["prefix_table"].clone()
+        table[at] = bad
+        got = fattn.decode_shared(**dict(args, prefix_table=table))
+        torch.cuda.synchronize()
+        assert fattn.get_device_status() == 1
+        zeroed = [[x.clone() for x in rows[0]]] + rows[1:]
+        for x in zeroed[0]:
+            x[:, 16 * at:16 * at + 16] = 0
+        check(args, zeroed, 0.125, *got, "page %d of %d" % (bad, at))
+    for n, want in ((2601, 2600), (-1, 0)):
+        got = fattn.decode_shared(**dict(args, prefix_len=torch.tensor([n * 16 if n > 0 else n], dtype=torch.int32).cuda()))
+        torch.cuda.synchronize()
+        assert fattn.get_device_status() == 1
+        assert want == 0 or got[0].isfinite().all()
+
+
+@pytest.mark.parametrize("once", [False, True])
+def test_long_pool(once):
     """Pages past 2^32 bytes of the pool."""
     D, Hkv, page = 128, 8, 128
     pages = 9000  # 2.4 GB each of K and V
-    args, rows = make(2, 8, Hkv, D, torch.bfloat16, page, 300, [10, 140], 1, 7)
+    args, rows = make(2, 8, Hkv, D, torch.bfloat16, page, 300, [10, 140], 1, 7, spare=spare_for(2, Hkv, D, page, once))
     kp, vp = (torch.zeros(2 * pages, Hkv, page, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
     n = args["k_pages"].shape[0]
     kp[-n:], vp[-n:] = args["k_pages"], args["v_pages"]
@@ -163,9 +197,11 @@ def test_long_pool():
     check(args, rows, fattn._default_scale(D), o, lse)
 
 
-def test_two_graphs_and_streams():
+@pytest.mark.parametrize("once", [False, True])
+def test_two_graphs_and_streams(once):
     """Two captured steps with workspaces of their own, replayed together with other lengths."""
-    sets = [make(4, 8, 2, 64, torch.float16, 16, 400, [33, 33, 33, 33], 1, 20 + i, fill=0.5) for i in range(2)]
+    sets = [make(4, 8, 2, 64, torch.float16, 16, 400, [33, 33, 33, 33], 1, 20 + i, fill=0.5,
+                 spare=spare_for(4, 2, 64, 16, once)) for i in range(2)]
     streams = [torch.cuda.Stream() for _ in range(2)]
     graphs, outs, spaces = [], [], []
     for (args, _), s in zip(sets, streams):

@@ -391,7 +391,9 @@ int64_t part_bytes(int64_t rows, int64_t pitch, int64_t D) { return rows * pitch
 
 // Cross attention: few rows per K/V head take the kernel of decode steps, which
 // streams the keys once for up to 32 rows; so does a call without keys, which only
-// writes zeros.
+// writes zeros.  (32 heads on 8, D = 128, ragged, 4 / 16 / 32 rows: 24 entries of
+// up to 4096 keys 48.6 / 52.2 / 62.6 us, by the tensor-core forward 72 each; one of
+// 8192 12.8 / 16.7 / 25.3 and 22 each; 4 of up to 300 8.4 / 10.9 / 15.5 and 17 each.)
 bool cross_few_rows(int64_t share, int64_t Nq, int64_t Nk) { return share * Nq <= 32 || Nk == 0; }
 // Parts that the keys may be cut into (the device chooses, by the lengths): two
 // waves of tasks, where that leaves parts of two tiles.  1: they are not.
@@ -440,10 +442,14 @@ CrossParts cross_parts(int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t Nk
 }
 
 // A shared prefix of up to `keys` tokens: whether every sequence reads it for itself,
-// in one launch of the decode kernel.  Where one does it is read once anyway.
-constexpr int64_t kReadByEach = 64ll << 20;
+// in one launch of the decode kernel, where reading it once takes three.  The
+// further reads come from L2, about 10 TB/s; three launches take 18 us more.  (32
+// heads on 8, D = 128: 16 sequences behind 2000 tokens 20.6 us, in three launches
+// 28.3; 2 behind 24000 28.4 and 40.0; 64 behind 500 31.5 and 32.6, behind 700 35.6
+// and 33.1.)
+constexpr int64_t kReadAgain = 160ll << 20;
 bool shared_read_by_each(int64_t B, int64_t share, int64_t Hkv, int64_t Nq, int64_t D, int64_t keys) {
-    return share * Nq <= 32 && (B == 1 || keys <= kReadByEach / (B * Hkv * 4 * D));
+    return share * Nq <= 32 && (B == 1 || keys <= kReadAgain / ((B - 1) * Hkv * 4 * D));
 }
 
 // Sizes of cross attention (dtype, head counts, lengths).
@@ -1654,7 +1660,7 @@ int fattn_bwd_cross(const void* q, const void* k, const void* v, const void* o, 
     if (views_overlap(small[2], small[0]) || views_overlap(small[2], small[1])) return FATTN_ERR_INVALID_ARG;
     const int64_t tiles_q = ceil_div(Nq, 128), tiles_k = ceil_div(Nk, 128);
     // (Blocks are cut into parts only where there are few.)
-    if (tiles_q * B * H > 0x7fffffffll || tiles_k * B * Hkv > 0x7fffffffll || tiles_q * (H / Hkv) > 0x7fffffffll)
+    if (tiles_q * B * H > 0x7fffffffll || tiles_k * B * Hkv > 0x7fffffffll || tiles_q * 128 * H > 0x7fffffffll)
         return FATTN_ERR_UNSUPPORTED;
     int sms = 0;
     st = current_sm_count(&sms);

@@ -152,7 +152,7 @@ __device__ __forceinline__ Cut* cut_of() {
 // Rows: keys of a source that every row sees.
 __device__ __forceinline__ int visible_keys(const RowsArgs& a, int source, bool report) {
     if (a.lens == nullptr) return a.max_keys;
-    const int len = __ldcg(a.lens + source);
+    const int len = a.own_part ? __ldcg(a.lens + source) : a.lens[source];
     if (len < 0 || len > a.max_keys) {
         if (report) atomicOr(&g_error_word, 1u << kDevErrInvalidArg);
         return len < 0 ? 0 : a.max_keys;
@@ -586,18 +586,32 @@ __device__ void producer_role(const ArgsOf<KIND>& a, uint8_t* smem, const Bars& 
         __syncwarp();
         ++qcnt[i];
     };
-    // Rows: this lane's piece of the K/V tiles, and its page of tile j (a page that
-    // is none lies outside the pool, where a copy brings zeros).
+    // Rows: the page of this lane's piece of tile j, asked for two tiles ahead; a page
+    // that is none lies outside the pool, where a copy brings zeros.
+    auto has_key = [&](const Task& tk, int j) -> bool {  // of this lane's piece
+        if constexpr (KIND == kRows) {
+            const int key = j * kTcBN + static_cast<int>(threadIdx.x % 32) * a.piece;
+            return a.table != nullptr && j < tk.nbmax && key < min(tk.n, (j + 1) * kTcBN);
+        } else {
+            return false;
+        }
+    };
     auto page_of = [&](const Task& tk, int j) -> int {
         if constexpr (KIND == kRows) {
             const int key = tk.start + j * kTcBN + static_cast<int>(threadIdx.x % 32) * a.piece;
-            if (a.table == nullptr || j >= tk.nbmax || key >= tk.start + min(tk.n, (j + 1) * kTcBN)) return a.num_pages;
-            const int page = __ldcg(a.table + key / a.page_size);
+            return has_key(tk, j) ? __ldcg(a.table + key / a.page_size) : 0;
+        } else {
+            return 0;
+        }
+    };
+    auto checked = [&](const Task& tk, int j, int page) -> int {
+        if constexpr (KIND == kRows) {
+            if (!has_key(tk, j)) return a.num_pages;
             if (static_cast<uint32_t>(page) < static_cast<uint32_t>(a.num_pages)) return page;
             atomicOr(&g_error_word, 1u << kDevErrInvalidArg);
             return a.num_pages;
         } else {
-            return 0;
+            return page;
         }
     };
     auto load_kv = [&](const CUtensorMap* map, int j, int kvh, const Task& tk, int page) {
@@ -677,9 +691,10 @@ __device__ void producer_role(const ArgsOf<KIND>& a, uint8_t* smem, const Bars& 
         if (!publish(kt, t)) break;
         const Task tk = KIND == kRows ? ahead : decode_task<CAUSAL, L::kRot, KIND>(t, a);
         const int kvh = KIND == kRows ? tk.bh % a.Hkv : kv_head_of(tk.bh, a.H, a.Hkv);
-        int page = page_of(tk, 0);
+        int page = page_of(tk, 0), next_page = page_of(tk, 1);
         load_q(0, tk);
         if (!ok) break;
+        page = checked(tk, 0, page);
         load_kv(&a.tmap_k, 0, kvh, tk, page);
         if (!ok) break;
         if (tk.nb[1] > 0) {
@@ -687,10 +702,11 @@ __device__ void producer_role(const ArgsOf<KIND>& a, uint8_t* smem, const Bars& 
             if (!ok) break;
         }
         for (int j = 0; j < tk.nbmax && ok; ++j) {
-            const int next_page = page_of(tk, j + 1);
+            const int later = page_of(tk, j + 2);
             load_kv(&a.tmap_v, j, kvh, tk, page);
-            if (ok && j + 1 < tk.nbmax) load_kv(&a.tmap_k, j + 1, kvh, tk, next_page);
-            page = next_page;
+            page = checked(tk, j + 1, next_page);
+            if (ok && j + 1 < tk.nbmax) load_kv(&a.tmap_k, j + 1, kvh, tk, page);
+            next_page = later;
         }
         if (!ok) break;
         // The next task is taken only now, a few K/V tiles before this CTA
