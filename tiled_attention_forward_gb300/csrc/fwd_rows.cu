@@ -101,12 +101,11 @@ __global__ void __launch_bounds__(kJoinThreads) rows_join_kernel(const __grid_co
 
 template <int D, bool BF16>
 cudaError_t launch_one(const RowsArgs& a, int grid, cudaStream_t stream) {
-    using L = TcLayout<D>;
     auto* fn = attn_fwd_tc_kernel<D, BF16, false, kRows>;
     static std::atomic<bool> done[kMaxDevices] = {};
-    const cudaError_t e = opt_in_smem_once(fn, L::kAlloc, done);
+    const cudaError_t e = opt_in_smem_once(fn, kRowsAlloc<D>, done);
     if (e != cudaSuccess) return e;
-    return launch_overlapped(fn, grid, kTcThreads, L::kAlloc, stream, a);
+    return launch_overlapped(fn, grid, kTcThreads, kRowsAlloc<D>, stream, a);
 }
 
 }  // namespace

@@ -201,21 +201,6 @@ __device__ __forceinline__ Cut choose_cut(const RowsArgs& a, bool report) {
     return {(most + best - 1) / best, best};
 }
 
-// Rows: which query row thread `trow` of tile u is (false: none).
-struct RowPlace {
-    int b, h, i;  // batch entry, head among those of the K/V head, token
-};
-__device__ __forceinline__ bool row_place(const RowsArgs& a, int source, int u, int trow, RowPlace& r) {
-    const int per_b = a.n_h * a.n_i;
-    const int ub = u / per_b, uh = (u - ub * per_b) / a.n_i, ui = u % a.n_i;
-    const int per_box = a.box_h * a.box_i;
-    const int tb = trow / per_box, th = (trow - tb * per_box) / a.box_i, ti = trow % a.box_i;
-    r.i = ui * a.box_i + ti;
-    r.h = uh * a.box_h + th;
-    r.b = source + ub * a.box_b + tb;
-    return u < a.tiles && tb < a.box_b && r.i < a.Nq && r.h < a.share && r.b < a.B;
-}
-
 struct Task {
     int bh;     // query head (dense: b * H + h; rows: source * Hkv + K/V head)
     int q0;     // first row of the Q block within its sequence (rows: the first tile's index)
@@ -310,6 +295,69 @@ __device__ __forceinline__ Task decode_task(int t, const ArgsOf<KIND>& a) {
         k.nb[1] = k.nbmax;
     }
     return k;
+    }
+}
+
+// Rows: the box of q that tile i of a task is (a tile past the last one lies
+// behind the last batch entry, where a copy brings zeros).
+struct QBox {
+    int i, h, b;
+};
+__device__ __forceinline__ QBox q_box(const RowsArgs& a, const Task& tk, int i) {
+    const int u = tk.q0 + i, per_b = a.n_h * a.n_i;
+    QBox q;
+    q.i = (u % a.n_i) * a.box_i;
+    q.h = (tk.bh % a.Hkv) * a.share + (u % per_b) / a.n_i * a.box_h;
+    q.b = u < a.tiles ? tk.bh / a.Hkv + u / per_b * a.box_b : a.B;
+    return q;
+}
+// A task as the producer hands it to the other roles, beside its word in the task
+// ring: decoding one takes a dozen divisions, which lay on every role's way from one
+// task to the next.
+struct RowsTask {
+    int n, nb0, nb1, bh;
+    int u, part, pad0, pad1;  // first tile; part of the keys
+    QBox q[2];
+    int pad2, pad3;
+};
+static_assert(sizeof(RowsTask) == 64, "slots of the task ring");
+template <int D>
+constexpr int kRowsTaskOff = (TcLayout<D>::kBytes + 15) / 16 * 16;
+template <int D>
+constexpr int kRowsAlloc = kRowsTaskOff<D> + 4 * 64 + 256 * 4;
+static_assert(kRowsAlloc<128> <= 227 * 1024 && kRowsAlloc<64> <= 227 * 1024, "shared memory budget");
+template <int D>
+__device__ __forceinline__ RowsTask* rows_task(int kt) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    return reinterpret_cast<RowsTask*>(smem_raw + kRowsTaskOff<D>) + kt % 4;
+}
+template <int D>
+__device__ __forceinline__ const volatile int* rows_keys(int kt) {
+    return &rows_task<D>(kt)->n;
+}
+// Batch entry, head and token of this softmax thread's row within its box (kept in
+// shared memory: the softmax warps have no register left).
+template <int D>
+__device__ __forceinline__ int* rows_place() {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    return reinterpret_cast<int*>(smem_raw + kRowsTaskOff<D> + 4 * 64) + threadIdx.x;
+}
+
+// The CTA's kt-th task, t, for the roles that do not produce it.
+template <bool CAUSAL, bool EQUAL, Kind KIND>
+__device__ __forceinline__ Task task_of(int kt, int t, const ArgsOf<KIND>& a) {
+    if constexpr (KIND == kRows) {
+        const int4 x = *reinterpret_cast<const int4*>(rows_task<EQUAL ? 64 : 128>(kt));
+        Task k;
+        k.n = x.x;
+        k.nb[0] = x.y;
+        k.nb[1] = x.z;
+        k.nbmax = x.y;
+        k.bh = x.w;
+        k.q0 = k.start = 0;  // (the producer's)
+        return k;
+    } else {
+        return decode_task<CAUSAL, EQUAL, KIND>(t, a);
     }
 }
 
@@ -532,18 +580,21 @@ __device__ __forceinline__ void zero_v_tail(uint8_t* tile, int rows) {
     __syncwarp();
 }
 
-// Rows: the box of q that tile i of a task is (a tile past the last one lies
-// behind the last batch entry, where a copy brings zeros).
-struct QBox {
-    int i, h, b;
-};
-__device__ __forceinline__ QBox q_box(const RowsArgs& a, const Task& tk, int i) {
-    const int u = tk.q0 + i, per_b = a.n_h * a.n_i;
-    QBox q;
-    q.i = (u % a.n_i) * a.box_i;
-    q.h = (tk.bh % a.Hkv) * a.share + (u % per_b) / a.n_i * a.box_h;
-    q.b = u < a.tiles ? tk.bh / a.Hkv + u / per_b * a.box_b : a.B;
-    return q;
+// Rows: what lies in the Q tiles behind the box that copies fill becomes zero (one
+// thread a row of both tiles).  Those rows are never stored, but a warp rescales all
+// its rows where one asks for it, which moves roundings: whatever shared memory held
+// would have a say in that.
+template <int D>
+__device__ __forceinline__ void zero_behind_box(const RowsArgs& a, uint8_t* q_tiles) {
+    const uint32_t row = threadIdx.x % kTcBM;
+    if (threadIdx.x >= 2 * kTcBM || row * 128u < a.box_bytes) return;
+    uint8_t* tile = q_tiles + threadIdx.x / kTcBM * TcLayout<D>::kQTileBytes + row * 128;
+#pragma unroll
+    for (int at = 0; at < D / 64; ++at)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<uint4*>(tile + at * kTcBM * 128 + 16 * e) = make_uint4(0u, 0u, 0u, 0u);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------
@@ -646,6 +697,7 @@ __device__ void producer_role(const ArgsOf<KIND>& a, uint8_t* smem, const Bars& 
     };
 
     uint32_t* ctr = sched_slot();
+    Task ahead = {};  // rows: the task to publish
     // Publish task t as the CTA's kt-th.  False: the wait for a free word
     // gave up, or a reader has already ended the schedule there.
     auto publish = [&](int kt, int t) -> bool {
@@ -657,6 +709,18 @@ __device__ void producer_role(const ArgsOf<KIND>& a, uint8_t* smem, const Bars& 
         if ((threadIdx.x % 32) == 0) {
             const unsigned long long cur = ring_peek(bars.tasks, kt);
             if ((cur >> 32) != static_cast<uint32_t>(kt)) {
+                if constexpr (KIND == kRows) {
+                    RowsTask* out = rows_task<D>(kt);
+                    out->n = ahead.n;
+                    out->nb0 = ahead.nb[0];
+                    out->nb1 = ahead.nb[1];
+                    out->bh = ahead.bh;
+                    out->u = ahead.q0;
+                    out->part = t / a.pairs % cut_of<D>()->parts;
+                    out->q[0] = q_box(a, ahead, 0);
+                    out->q[1] = q_box(a, ahead, 1);
+                    __threadfence_block();
+                }
                 won = atomicCAS(bars.tasks.word(slot), cur, ring_word(kt, static_cast<uint32_t>(t))) == cur;
                 if (won) mbar_arrive(bars.tasks.full(slot));
             }
@@ -674,7 +738,6 @@ __device__ void producer_role(const ArgsOf<KIND>& a, uint8_t* smem, const Bars& 
 
     int t = static_cast<int>(blockIdx.x);
     // Rows: the task, past the parts that a shorter source does not have.
-    Task ahead = {};
     auto skip_none = [&]() {
         while (KIND == kRows && t < num_tasks) {
             ahead = decode_task<CAUSAL, L::kRot, KIND>(t, a);
@@ -822,7 +885,7 @@ __device__ void mma_pair_role(const ArgsOf<KIND>& a, uint8_t* smem, const Bars& 
         sync();
         if (!HELPER) {
             t = static_cast<int>(static_cast<uint32_t>(ring_peek(bars.tasks, kt)));
-            release_task(bars.tasks, kt);
+            if (KIND != kRows) release_task(bars.tasks, kt);  // (rows: once the task is read)
         }
         return t;
     };
@@ -884,7 +947,8 @@ __device__ void mma_pair_role(const ArgsOf<KIND>& a, uint8_t* smem, const Bars& 
     for (int kt = 0;; ++kt) {
         const int t = next_task(kt);
         if (schedule_ended<KIND>(t, a)) break;
-        const Task tk = decode_task<CAUSAL, false, KIND>(t, a);
+        const Task tk = task_of<CAUSAL, false, KIND>(kt, t, a);
+        if (KIND == kRows && !HELPER) release_task(bars.tasks, kt);
         uint32_t kslot, vslot;
         // Prologue: S_0(0), S_1(0).
         wait_q(0);
@@ -1017,7 +1081,7 @@ __device__ void mma_pair_role_rot(const ArgsOf<KIND>& a, uint8_t* smem, const Ba
         sync();
         if (!HELPER) {
             t = static_cast<int>(static_cast<uint32_t>(ring_peek(bars.tasks, kt)));
-            release_task(bars.tasks, kt);
+            if (KIND != kRows) release_task(bars.tasks, kt);  // (rows: once the task is read)
         }
         return t;
     };
@@ -1046,7 +1110,8 @@ __device__ void mma_pair_role_rot(const ArgsOf<KIND>& a, uint8_t* smem, const Ba
     for (int kt = 0;; ++kt) {
         const int t = next_task(kt);
         if (schedule_ended<KIND>(t, a)) break;
-        const Task tk = decode_task<CAUSAL, true, KIND>(t, a);
+        const Task tk = task_of<CAUSAL, true, KIND>(kt, t, a);
+        if (KIND == kRows && !HELPER) release_task(bars.tasks, kt);
         const int nb = tk.nbmax;
         // Prologue: S_0(0), S_1(0), S_0(1).
         wait_q(0);
@@ -1156,10 +1221,10 @@ __device__ void softmax_role(const ArgsOf<KIND>& a, const Bars& bars, uint8_t* q
     const uint32_t lane_field = static_cast<uint32_t>((warp % 4) * 32) << 16;
     const uint32_t tO = tmem_base + lane_field + (kRot ? 3 : 2) * kTcBN + tile * D;
     const float sl2 = a.scale_log2;
-    // Rows: behind a tile's box lies whatever shared memory held; those rows are never
-    // stored, and have no say in when the others are rescaled (which moves roundings).
-    bool in_box = true;
-    if constexpr (KIND == kRows) in_box = static_cast<uint32_t>(trow) * 128u < a.box_bytes;
+    if constexpr (KIND == kRows) {
+        const int per_box = a.box_h * a.box_i, rest = trow % per_box;
+        *rows_place<D>() = trow * 128u < a.box_bytes ? (trow / per_box) << 16 | (rest / a.box_i) << 8 | rest % a.box_i : -1;
+    }
 
     // Barrier phases: D = 128 counts the S products of this tile on
     // s_full[tile]; D = 64 counts them per buffer on s_full[b * 2 + tile].
@@ -1170,10 +1235,11 @@ __device__ void softmax_role(const ArgsOf<KIND>& a, const Bars& bars, uint8_t* q
     for (int kt = 0;; ++kt) {
         const int t = read_task(bars.tasks, kt, abort_flag, a.timeout_ns);
         if (schedule_ended<KIND>(t, a)) break;
-        release_task(bars.tasks, kt);
-        const Task tk = decode_task<CAUSAL, kRot, KIND>(t, a);
+        if (KIND != kRows) release_task(bars.tasks, kt);  // (rows: after the epilogue)
+        const Task tk = task_of<CAUSAL, kRot, KIND>(kt, t, a);
         const int nb = tk.nb[tile];
         if constexpr (!kRot) {
+            if (KIND == kRows && nb == 0) release_task(bars.tasks, kt);
             if (nb == 0) continue;  // tile past N (the three-buffer layout computes it anyway)
         }
         const int row0 = tk.q0 + tile * kTcBM;
@@ -1232,13 +1298,16 @@ __device__ void softmax_role(const ArgsOf<KIND>& a, const Bars& bars, uint8_t* q
             for (int c = 0; c < kTcBN; ++c) s[c] = __uint_as_float(sr[c / 32][c % 32]);
 
             const int kb = j * kTcBN;
+            // (Rows: only the last tile can hold keys past the end, and it alone asks
+            // where that is, which would cost the others a register.)
             const bool need_mask =
-                (!(CAUSAL && KIND == kPacked) && kb + kTcBN > tk.n) || (CAUSAL && kb + kTcBN - 1 > row0);
+                KIND == kRows ? j == nb - 1 && kb + kTcBN > *rows_keys<D>(kt)
+                              : (!(CAUSAL && KIND == kPacked) && kb + kTcBN > tk.n) || (CAUSAL && kb + kTcBN - 1 > row0);
             float mblk = fmaxf(fmaxf(cmx[0], cmx[1]), fmaxf(cmx[2], cmx[3]));
             if (need_mask) {
                 // Keys past N or past the row: masked here, and the row max
                 // taken over the visible scores only.
-                const int vis = lim - kb;
+                const int vis = (KIND == kRows ? *rows_keys<D>(kt) : lim) - kb;
 #pragma unroll
                 for (int c = 0; c < kTcBN; ++c)
                     if (c >= vis) s[c] = -INFINITY;
@@ -1259,7 +1328,7 @@ __device__ void softmax_role(const ArgsOf<KIND>& a, const Bars& bars, uint8_t* q
                 // Rescale O and l only when some row of the warp saw its max
                 // rise by more than the threshold; otherwise keep the stale
                 // max for P and l alike (exact in exact arithmetic, P <= 2^8).
-                const bool grow = in_box && (m_new - m_run) > kRescaleThreshold;
+                const bool grow = (m_new - m_run) > kRescaleThreshold;
                 if (__any_sync(0xffffffffu, grow)) {
                     if (kRot) {
                         // O_i holds P.V_i(j-1) only once that product is done
@@ -1347,19 +1416,21 @@ __device__ void softmax_role(const ArgsOf<KIND>& a, const Bars& bars, uint8_t* q
         uint8_t* orow = reinterpret_cast<uint8_t*>(a.o);
         int64_t lse_at;
         if constexpr (KIND == kRows) {
-            const Task te = decode_task<CAUSAL, kRot, KIND>(t, a);
-            const int u = te.q0 + tile, source = te.bh / a.Hkv, kvh = te.bh % a.Hkv;
+            const RowsTask& te = *rows_task<D>(kt);
             if (!(l_exact > 0.f) && m_run == -INFINITY) inv_l = 0.f;  // no key: O = 0, and its part weighs nothing
-            RowPlace r;
-            valid = row_place(a, source, u, trow, r);
+            const QBox q = te.q[tile];
+            const int bh = te.bh, u = te.u + tile, part = te.part;
+            release_task(bars.tasks, kt);
+            const int place = *rows_place<D>();
+            const int b = q.b + (place >> 16), h = q.h + ((place >> 8) & 255), i = q.i + (place & 255);
+            valid = place >= 0 && i < a.Nq && h < (bh % a.Hkv + 1) * a.share && b < a.B;
             if (a.part_o != nullptr) {
                 // A part: the sum of values not yet divided, by the weights' unrounded sum.
-                const int part = t / a.pairs % cut_of<D>()->parts;
                 // 32 rows of 32 elements at a time go through 4 KB of the task's Q tile,
                 // which no product reads any more, so that a warp writes whole lines (a
                 // row a thread straight to memory took 12 k cycles for a tile of 128
                 // elements).
-                const int64_t at = ((static_cast<int64_t>(te.bh) * a.tiles + u) * kTcBM + trow) * a.part_pitch + part;
+                const int64_t at = ((static_cast<int64_t>(bh) * a.tiles + u) * kTcBM + trow) * a.part_pitch + part;
                 const float f = inv_l * l_exact;
                 const int lane = threadIdx.x % 32;
                 const uint32_t stored = __ballot_sync(0xffffffffu, valid);
@@ -1387,6 +1458,10 @@ __device__ void softmax_role(const ArgsOf<KIND>& a, const Bars& bars, uint8_t* q
                     }
                 }
                 if (valid) __stcg(a.part_ml + at, make_float2(m_run, l_exact));
+                if (trow * 128u >= a.box_bytes)  // (see zero_behind_box)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        *reinterpret_cast<uint4*>(stage + lane * 128 + 16 * e) = make_uint4(0u, 0u, 0u, 0u);
                 // The tile may be loaded again (through the async proxy).
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
@@ -1398,9 +1473,8 @@ __device__ void softmax_role(const ArgsOf<KIND>& a, const Bars& bars, uint8_t* q
                 }
                 continue;
             }
-            const int h = kvh * a.share + r.h;
-            orow += 2 * (r.b * a.o_bs + h * a.o_hs + r.i * a.o_ns);
-            lse_at = (static_cast<int64_t>(r.b) * a.H + h) * a.Nq + r.i;
+            orow += 2 * (b * a.o_bs + h * a.o_hs + i * a.o_ns);
+            lse_at = (static_cast<int64_t>(b) * a.H + h) * a.Nq + i;
         } else
         if constexpr (KIND == kPacked) {
             // Decoded again: its fields would otherwise hold registers through
@@ -1488,6 +1562,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_fwd_tc_kernel(const __grid
         tmem_relinquish();
     }
     if constexpr (KIND == kRows) {
+        zero_behind_box<D>(a, smem + L::kQOff);
         if (warp == 9 && lane < 3) tma_prefetch_desc(lane == 0 ? &a.tmap_q : (lane == 1 ? &a.tmap_k : &a.tmap_v));
         // A prefix: the kernel before this one, of the own keys, writes nothing that
         // this one reads or writes, and what came before that is complete once all
