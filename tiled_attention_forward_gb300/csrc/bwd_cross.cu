@@ -21,24 +21,32 @@ __global__ void __launch_bounds__(256) cross_stats_kernel(const __grid_constant_
     constexpr int kLanes = D / 8, kRows = 32 / kLanes;
     const int64_t rows = static_cast<int64_t>(a.BH) * a.Npad;
     const int lane = threadIdx.x % 32, piece = lane % kLanes;
+    // Row `lane / kLanes` of a warp's rows, and from one of a lane's rows to its next:
+    // inner and outer index, batch entry.  (Fewer than 2^31 rows of an entry: 32-bit
+    // divisions, which were half of all instructions with one a row.)
+    const uint32_t per_b = static_cast<uint32_t>(a.H) * a.Npad, inner = heads_inner ? a.H : a.Npad;
     struct At {
-        uint32_t b, h, i;
+        uint32_t b, outer, in;
     };
-    auto at = [&](int64_t warp, int k) {  // (fewer than 2^31 rows of a batch entry: 32-bit divisions)
-        const int64_t row = warp * kStatRows<D> + k * kRows + lane / kLanes;
-        const uint32_t per_b = static_cast<uint32_t>(a.H) * a.Npad;
+    auto first_of = [&](int64_t warp) {
+        const int64_t row = warp * kStatRows<D> + lane / kLanes;
         At x;
         x.b = (row >> 32) == 0 ? static_cast<uint32_t>(row) / per_b : static_cast<uint32_t>(row / per_b);
         const uint32_t rest = static_cast<uint32_t>(row - static_cast<int64_t>(x.b) * per_b);
-        if (heads_inner) {
-            x.i = rest / a.H;
-            x.h = rest - x.i * a.H;
-        } else {
-            x.h = rest / a.Npad;
-            x.i = rest - x.h * a.Npad;
-        }
-        if (row >= rows) x.b = 0xffffffffu;
+        x.outer = rest / inner;
+        x.in = rest - x.outer * inner;
         return x;
+    };
+    const uint32_t outer_end = per_b / inner, entries = static_cast<uint32_t>(a.BH / a.H);
+    auto step = [&](At& x) {
+        x.in += kRows;
+        while (x.in >= inner) {
+            x.in -= inner;
+            if (++x.outer == outer_end) {
+                x.outer = 0;
+                ++x.b;
+            }
+        }
     };
     grid_dependency();
     const int64_t warps = (rows + kStatRows<D> - 1) / kStatRows<D>, stride = static_cast<int64_t>(gridDim.x) * 8;
@@ -46,19 +54,21 @@ __global__ void __launch_bounds__(256) cross_stats_kernel(const __grid_constant_
         uint4 o[kStatLoads], g[kStatLoads];
         float lse[kStatLoads];
         int64_t dst[kStatLoads];  // of the row's first statistic; < 0: no row
+        At x = first_of(warp);
 #pragma unroll
         for (int k = 0; k < kStatLoads; ++k) {
-            const At x = at(warp, k);
-            const int64_t bh = static_cast<int64_t>(x.b) * a.H + x.h;
+            if (k > 0) step(x);
+            const uint32_t h = heads_inner ? x.in : x.outer, i = heads_inner ? x.outer : x.in;
+            const int64_t bh = static_cast<int64_t>(x.b) * a.H + h;
             o[k] = g[k] = make_uint4(0u, 0u, 0u, 0u);
             lse[k] = -INFINITY;
-            dst[k] = x.b == 0xffffffffu ? -1 : bh * 2 * a.Npad + x.i;
-            if (x.b != 0xffffffffu && x.i < static_cast<uint32_t>(a.N)) {
-                o[k] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.o) + x.b * a.o_bs + x.h * a.o_hs +
-                                                       x.i * a.o_ns + 8 * piece);
+            dst[k] = x.b >= entries ? -1 : bh * 2 * a.Npad + i;
+            if (x.b < entries && i < static_cast<uint32_t>(a.N)) {
+                o[k] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.o) + x.b * a.o_bs + h * a.o_hs +
+                                                       i * a.o_ns + 8 * piece);
                 g[k] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.dout) + x.b * a.do_bs +
-                                                       x.h * a.do_hs + x.i * a.do_ns + 8 * piece);
-                if (piece == 0) lse[k] = a.lse[bh * a.N + x.i];
+                                                       h * a.do_hs + i * a.do_ns + 8 * piece);
+                if (piece == 0) lse[k] = a.lse[bh * a.N + i];
             }
         }
 #pragma unroll

@@ -1433,7 +1433,7 @@ int fattn_decode_shared(const void* q, void* o, float* lse, const int64_t* strid
     if (st != FATTN_OK) return st;
     const RowTiles t = row_tiles_of(H / Hkv, Nq, B, true);
     const int most = max_splits(Hkv * t.pairs), pitch = most + 1;
-    if (Hkv * t.pairs * pitch > (int64_t(1) << 30)) return FATTN_ERR_UNSUPPORTED;
+    if (Hkv * t.pairs * pitch > (int64_t(1) << 30) || B * H * Nq >= (int64_t(1) << 27) - 8) return FATTN_ERR_UNSUPPORTED;
     if (no_device != FATTN_OK) return no_device;
     if (shared_read_by_each(B, H / Hkv, Hkv, Nq, D, prefix_width * page_size)) {
         PrefixDecodeArgs p;
@@ -1545,6 +1545,7 @@ int fattn_fwd_cross(const void* q, const void* k, const void* v, void* o, float*
     const bool few = cross_few_rows(H / Hkv, Nq, Nk);
     const RowTiles t = row_tiles_of(H / Hkv, Nq, B, false);
     const int splits = few ? 1 : cross_splits(B, Hkv, t, Nk);
+    if (splits > 1 && B * H * Nq >= (int64_t(1) << 27) - 8) return FATTN_ERR_UNSUPPORTED;
     if (!few && B * Hkv * t.pairs * splits > (int64_t(1) << 30)) return FATTN_ERR_UNSUPPORTED;
     int sms = 0;
     st = current_sm_count(&sms);

@@ -15,22 +15,24 @@ template <int D, bool BF16>
 __global__ void __launch_bounds__(kJoinThreads) rows_join_kernel(const __grid_constant__ RowsArgs a) {
     constexpr int kPer = D / 32, kAtOnce = 8;
     static_assert(kMaxSplits + 1 <= 5 * 32, "parts of a row in the lanes");
-    const int64_t w = (static_cast<int64_t>(blockIdx.x) * kJoinThreads + threadIdx.x) / 32;
+    // (Fewer than 2^32 rows: rows_join_launch.)
+    const uint32_t w = (blockIdx.x * kJoinThreads + threadIdx.x) / 32;
     const int lane = threadIdx.x % 32;
-    const int i = static_cast<int>(w % a.Nq);
-    const int64_t bh = w / a.Nq;
-    const int b = static_cast<int>(bh / a.H), h = static_cast<int>(bh % a.H);
+    const uint32_t bh = w / static_cast<uint32_t>(a.Nq);
+    const int i = static_cast<int>(w - bh * a.Nq);
+    const int b = static_cast<int>(bh / static_cast<uint32_t>(a.H)), h = static_cast<int>(bh - b * a.H);
     const int kvh = h / a.share, hq = h % a.share;
     const int source = a.sources > 1 ? b : 0, among = b - source;  // (one source: the entry among its rows)
     const int u = (among / a.box_b * a.n_h + hq / a.box_h) * a.n_i + i / a.box_i;
     const int trow = ((among % a.box_b) * a.box_h + hq % a.box_h) * a.box_i + i % a.box_i;
     const int64_t at = (((static_cast<int64_t>(source) * a.Hkv + kvh) * a.tiles + u) * kTcBM + trow) * a.part_pitch;
     grid_dependency();
-    if (w >= static_cast<int64_t>(a.B) * a.H * a.Nq) return;
+    if (b >= a.B) return;
     // What does not depend on the number of parts is on its way with it: the places
     // that may hold one (what lies in those that hold none is not used), the own
     // keys' part as place 0.
-    auto place = [&](int s) { return at + (a.own_part ? (s == 0 ? a.part_pitch - 1 : s - 1) : s); };
+    const float* rows = a.part_o + at * D + lane * kPer;
+    auto place = [&](int s) { return a.own_part ? (s == 0 ? a.part_pitch - 1 : s - 1) : s; };
     const int most = a.max_parts + a.own_part;
     const int per = __ldcg(a.part_count);
     const int tiles = (visible_keys(a, source, false) + kTcBN - 1) / kTcBN;
@@ -38,9 +40,9 @@ __global__ void __launch_bounds__(kJoinThreads) rows_join_kernel(const __grid_co
     float early[kAtOnce][kPer];
 #pragma unroll
     for (int x = 0; x < 5; ++x)
-        if (lane + 32 * x < most) ml[x] = __ldcg(a.part_ml + place(lane + 32 * x));
+        if (lane + 32 * x < most) ml[x] = __ldcg(a.part_ml + at + place(lane + 32 * x));
     auto load = [&](float (&v)[kPer], int s) {
-        const float* src = a.part_o + place(s) * D + lane * kPer;
+        const float* src = rows + place(s) * D;
         if constexpr (kPer == 4) {
             const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
             v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
@@ -73,7 +75,8 @@ __global__ void __launch_bounds__(kJoinThreads) rows_join_kernel(const __grid_co
         const int upto = min(32, all - 32 * x);
         for (int s0 = 0; s0 < upto; s0 += kAtOnce) {
             float v[kAtOnce][kPer];
-            if (s0 + kAtOnce < upto || x < 4)  // the next ones
+            const bool more = 32 * x + s0 + kAtOnce < all;
+            if (more)  // the next ones
 #pragma unroll
                 for (int y = 0; y < kAtOnce; ++y) load(v[y], min(32 * x + s0 + kAtOnce + y, all - 1));
 #pragma unroll
@@ -83,7 +86,8 @@ __global__ void __launch_bounds__(kJoinThreads) rows_join_kernel(const __grid_co
 #pragma unroll
                     for (int e = 0; e < kPer; ++e) acc[e] = fmaf(wt, early[y][e], acc[e]);
 #pragma unroll
-                for (int e = 0; e < kPer; ++e) early[y][e] = v[y][e];
+                for (int e = 0; e < kPer; ++e)
+                    if (more) early[y][e] = v[y][e];
             }
         }
     }
@@ -117,6 +121,7 @@ cudaError_t rows_launch(const RowsArgs& a, int D, bool bf16, int grid, cudaStrea
 
 cudaError_t rows_join_launch(const RowsArgs& a, int D, bool bf16, cudaStream_t s) {
     const int64_t rows = static_cast<int64_t>(a.B) * a.H * a.Nq;
+    if (rows * 32 + kJoinThreads > 0xffffffffll) return cudaErrorInvalidValue;  // (the entry points refuse it)
     const unsigned grid = static_cast<unsigned>((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32));
     auto* fn = D == 128 ? (bf16 ? rows_join_kernel<128, true> : rows_join_kernel<128, false>)
                         : (bf16 ? rows_join_kernel<64, true> : rows_join_kernel<64, false>);
