@@ -156,6 +156,8 @@ BACKWARD = [
     (1, 1, 1, 1, 1, None), (2, 4, 2, 1, 130, [130, 0]), (2, 4, 1, 17, 40, [40, 3]), (1, 2, 2, 128, 128, None),
     (2, 2, 1, 129, 257, [257, 128]), (2, 6, 2, 43, 300, [129, 300]), (1, 2, 2, 300, 127, [126]), (3, 2, 2, 260, 64, [64, 0, 33]),
     (1, 4, 4, 70, 900, [900]), (1, 8, 2, 600, 200, None),
+    (2, 6, 2, 2, 200, [200, 64]), (1, 10, 2, 25, 130, None), (2, 12, 2, 30, 90, [90, 17]), (1, 7, 1, 20, 300, None),  # stacked heads
+    (3, 8, 1, 1, 129, [129, 0, 128]), (1, 24, 1, 11, 70, None),
 ]
 
 
@@ -228,6 +230,23 @@ def test_backward_layouts_and_repeats(dtype, D):
     ok()
     assert all(torch.equal(x, y) for x, y in zip(a, b))
     assert (grad[:, :, 0] == 7).all() and (grad[:, :, 5] == 7).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_backward_other_groups_never_leak(D):
+    """NaN in the queries and gradients of one K/V head's group reaches no other group's gradients."""
+    for Nq, share in ((3, 4), (40, 3), (130, 2)):
+        q, k, v, do, t = make(2, 3 * share, 3, Nq, 200, D, torch.float16, Nq, [200, 150], fill=0.0)
+        o, lse = fattn.fwd_cross(q, k, v, t)
+        want = fattn.bwd_cross(q, k, v, o, lse, do, t)
+        q2, do2 = q.clone(), do.clone()
+        q2[:, share:2 * share] = math.nan
+        do2[:, share:2 * share] = math.inf
+        got = fattn.bwd_cross(q2, k, v, o, lse, do2, t)
+        ok()
+        for x, y, per in zip(want, got, (share, 1, 1)):
+            for g in (0, 2):
+                assert torch.equal(x[:, g * per:(g + 1) * per], y[:, g * per:(g + 1) * per])
 
 
 def test_backward_equals_the_dense_backward():

@@ -7,9 +7,9 @@
 namespace fattn {
 namespace {
 
-// -LSE_i * log2(e) and -Delta_i, Delta_i = dO_i . O_i, into the padded workspace
-// [B*H][2][Npad]; rows past Nq, and rows that saw no key (LSE = -inf), get -inf
-// and 0.  A row is read as 16-byte pieces by D/8 lanes, kStatLoads such rows of O
+// -LSE_i * log2(e) and -Delta_i, Delta_i = dO_i . O_i, into the workspace in the order
+// of the tiles' rows, [B*Hkv][tiles][2][128]; rows past Nq or behind a tile's box, and
+// rows that saw no key (LSE = -inf), get -inf and 0.  A row is read as 16-byte pieces by D/8 lanes, kStatLoads such rows of O
 // and of dO in flight a lane; rows are taken in the order in which they lie in
 // memory (`heads_inner`: a token's heads one after the other).
 constexpr int kStatLoads = 4;
@@ -19,12 +19,13 @@ constexpr int kStatRows = (32 / (D / 8)) * kStatLoads;  // of a warp
 template <int D, bool BF16>
 __global__ void __launch_bounds__(256) cross_stats_kernel(const __grid_constant__ CrossBwdArgs a, bool heads_inner) {
     constexpr int kLanes = D / 8, kRows = 32 / kLanes;
-    const int64_t rows = static_cast<int64_t>(a.BH) * a.Npad;
+    const int padded = a.n_i * a.box_i, share = a.H / a.Hkv;  // tokens, to whole boxes
+    const int64_t rows = static_cast<int64_t>(a.BH) * padded;
     const int lane = threadIdx.x % 32, piece = lane % kLanes;
     // Row `lane / kLanes` of a warp's rows, and from one of a lane's rows to its next:
     // inner and outer index, batch entry.  (Fewer than 2^31 rows of an entry: 32-bit
     // divisions, which were half of all instructions with one a row.)
-    const uint32_t per_b = static_cast<uint32_t>(a.H) * a.Npad, inner = heads_inner ? a.H : a.Npad;
+    const uint32_t per_b = static_cast<uint32_t>(a.H) * padded, inner = heads_inner ? a.H : padded;
     struct At {
         uint32_t b, outer, in;
     };
@@ -62,7 +63,22 @@ __global__ void __launch_bounds__(256) cross_stats_kernel(const __grid_constant_
             const int64_t bh = static_cast<int64_t>(x.b) * a.H + h;
             o[k] = g[k] = make_uint4(0u, 0u, 0u, 0u);
             lse[k] = -INFINITY;
-            dst[k] = x.b >= entries ? -1 : bh * 2 * a.Npad + i;
+            dst[k] = -1;
+            if (x.b < entries) {
+                if (a.box_h == 1 && a.box_i == kBT) {
+                    dst[k] = (bh * a.n_i + i / kBT) * (2 * kBT) + i % kBT;
+                } else {
+                    const uint32_t kvh = h / share, hq = h - kvh * share, uh = hq / a.box_h, ui = i / a.box_i;
+                    const int64_t tile = (static_cast<int64_t>(x.b) * a.Hkv + kvh) * a.tiles + uh * a.n_i + ui;
+                    const uint32_t r = (hq - uh * a.box_h) * a.box_i + (i - ui * a.box_i);
+                    dst[k] = tile * (2 * kBT) + r;
+                    if (r == 0)  // the rows behind the box
+                        for (int y = a.box_h * a.box_i + piece; y < kBT; y += kLanes) {
+                            a.ws[dst[k] + y] = -INFINITY;
+                            a.ws[dst[k] + kBT + y] = 0.f;
+                        }
+                }
+            }
             if (x.b < entries && i < static_cast<uint32_t>(a.N)) {
                 o[k] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.o) + x.b * a.o_bs + h * a.o_hs +
                                                        i * a.o_ns + 8 * piece);
@@ -93,7 +109,7 @@ __global__ void __launch_bounds__(256) cross_stats_kernel(const __grid_constant_
             if (piece == 0 && dst[k] >= 0) {
                 const bool none = lse[k] == -INFINITY;
                 a.ws[dst[k]] = none ? -INFINITY : -lse[k] * 1.4426950408889634f;
-                a.ws[dst[k] + a.Npad] = none ? 0.f : -sum;
+                a.ws[dst[k] + kBT] = none ? 0.f : -sum;
             }
         }
     }
@@ -119,9 +135,14 @@ __global__ void __launch_bounds__(kAddThreads) cross_add_kernel(const __grid_con
     if (b >= a.BH / a.H || (!kv && a.parts_q == 1)) return;
     int keys = a.Nk;
     if (a.lens != nullptr) keys = min(max(a.lens[b], 0), a.Nk);
-    const int parts = kv ? a.parts_k : a.parts_q, padded = kv ? a.tiles_k * kBT : a.Npad, tiles = (keys + kBT - 1) / kBT;
-    const int64_t step = (kv ? static_cast<int64_t>(a.BHkv) : a.BH) * padded * accs * D;
-    const float* src = (kv ? a.part_kv : a.part_q) + ((bh * padded + i) * accs + acc) * D + d;
+    const int parts = kv ? a.parts_k : a.parts_q, tiles = (keys + kBT - 1) / kBT;
+    const int64_t padded = (kv ? a.tiles_k : a.tiles) * kBT, step = static_cast<int64_t>(a.BHkv) * padded * accs * D;
+    int64_t at = bh * padded + i;
+    if (!kv) {
+        const int share = a.H / a.Hkv, hq = static_cast<int>(h) % share, uh = hq / a.box_h, ui = i / a.box_i;
+        at = (bh / share) * padded + (uh * a.n_i + ui) * kBT + (hq - uh * a.box_h) * a.box_i + (i - ui * a.box_i);
+    }
+    const float* src = (kv ? a.part_kv : a.part_q) + (at * accs + acc) * D + d;
     float sum[8] = {};
     const int upto = kv && i >= keys ? 0 : parts;
 #pragma unroll 4
@@ -173,7 +194,7 @@ cudaError_t launch_add(const CrossBwdArgs& a, cudaStream_t s) {
 template <int D, bool BF16>
 cudaError_t launch_all(const CrossBwdArgs& a, int sms, cudaStream_t s) {
     // (Without queries the key kernel, without keys the query kernel writes zeros.)
-    const int64_t warps = (static_cast<int64_t>(a.BH) * a.Npad + kStatRows<D> - 1) / kStatRows<D>;
+    const int64_t warps = (static_cast<int64_t>(a.BH) * a.n_i * a.box_i + kStatRows<D> - 1) / kStatRows<D>;
     cudaError_t e = cudaSuccess;
     if (a.N > 0 && a.Nk > 0) {
         const int64_t blocks = (warps + 7) / 8;
@@ -189,10 +210,10 @@ cudaError_t launch_all(const CrossBwdArgs& a, int sms, cudaStream_t s) {
         e = launch_overlapped(kkv, static_cast<unsigned>(a.tiles_k * a.BHkv * a.parts_k), kBwdThreads, BwdLayout<D, true>::kBytes, s, a);
         if (e != cudaSuccess) return e;
     }
-    if (a.num_tiles == 0) return cudaSuccess;
+    if (a.tiles == 0) return cudaSuccess;
     auto* kq = attn_bwd_kernel<D, BF16, false, false, true>;
     if ((e = opt_in_smem_once(kq, BwdLayout<D, false>::kBytes, q_done)) != cudaSuccess) return e;
-    const unsigned grid_q = static_cast<unsigned>(a.num_tiles * a.BH * a.parts_q);
+    const unsigned grid_q = static_cast<unsigned>(a.tiles * a.BHkv * a.parts_q);
     // (Behind the key kernel only: it reads and writes without waiting first.)
     if (a.tiles_k > 0) {
         e = launch_overlapped(kq, grid_q, kBwdThreads, BwdLayout<D, false>::kBytes, s, a);

@@ -194,7 +194,9 @@ struct BwdTask {
     int it0, part;  // cross: the first of the task's inner tiles, and the part of the gradient that they make
 };
 
-// Cross: the inner tiles of a block are cut into parts (a.parts_k, a.parts_q) where
+// Cross: bh is a K/V head (of all entries) in both kernels, and the query rows of all
+// heads that share it are stacked into tiles (boxes of box_h heads and box_i tokens).
+// The inner tiles of a block are cut into parts (a.parts_k, a.parts_q) where
 // there are few blocks, each a task; key blocks behind the batch entry's keys, all
 // query tiles of an entry without keys, and parts of an entry with fewer key tiles
 // than parts have no inner tiles (n = 0).
@@ -208,13 +210,13 @@ __device__ __forceinline__ BwdTask bwd_task(const BwdArgsOf<CROSS>& a, int keys)
     BwdTask t;
     const int idx = blockIdx.x;
     if constexpr (CROSS) {
-        const int blocks = KV ? a.tiles_k : a.num_tiles, parts = KV ? a.parts_k : a.parts_q;
+        const int blocks = KV ? a.tiles_k : a.tiles, parts = KV ? a.parts_k : a.parts_q;
         t.part = idx % parts;
         t.bh = idx / parts / blocks;
         t.blk = idx / parts % blocks;
         t.j0 = 0;
-        t.per_head = KV ? a.num_tiles : (keys + kBT - 1) / kBT;
-        const int all = KV ? (t.blk * kBT < keys ? t.per_head * (a.H / a.Hkv) : 0) : t.per_head;
+        t.per_head = KV ? a.tiles : (keys + kBT - 1) / kBT;
+        const int all = KV ? (t.blk * kBT < keys ? t.per_head : 0) : t.per_head;
         t.it0 = part_begin(all, t.part, parts);
         t.n = part_begin(all, t.part + 1, parts) - t.it0;
         return t;
@@ -252,7 +254,7 @@ __device__ __forceinline__ int bwd_query_head(const BwdArgs& a, const BwdTask& t
 template <bool KV>
 __device__ __forceinline__ int bwd_visible_keys(const CrossBwdArgs& a) {
     if (a.lens == nullptr) return a.Nk;
-    const int b = KV ? blockIdx.x / a.parts_k / a.tiles_k / a.Hkv : blockIdx.x / a.parts_q / a.num_tiles / a.H;
+    const int b = KV ? blockIdx.x / a.parts_k / a.tiles_k / a.Hkv : blockIdx.x / a.parts_q / a.tiles / a.Hkv;
     const int len = a.lens[b];
     if (len < 0 || len > a.Nk) {
         if (threadIdx.x == 0) atomicOr(&g_error_word, 1u << kDevErrInvalidArg);
@@ -275,20 +277,41 @@ __device__ __forceinline__ void bwd_zero_tail(uint8_t* tile, int rows) {
     __syncwarp();
 }
 
+// Cross: the box of query rows that tile u of K/V head kvh is, and its row r (false:
+// none).
+struct QueryBox {
+    int i, h, b;
+};
+__device__ __forceinline__ QueryBox query_box(const CrossBwdArgs& a, int kvh, int u) {
+    QueryBox x;
+    x.b = kvh / a.Hkv;
+    x.h = (kvh - x.b * a.Hkv) * (a.H / a.Hkv) + u / a.n_i * a.box_h;
+    x.i = u % a.n_i * a.box_i;
+    return x;
+}
+__device__ __forceinline__ bool query_row(const CrossBwdArgs& a, const QueryBox& x, int r, int& h, int& i) {
+    h = x.h + r / a.box_i;
+    i = x.i + r % a.box_i;
+    return r < a.box_h * a.box_i && i < a.N;
+}
+
 // Cross: the gradient rows of a CTA without inner tiles.
 template <int D, bool KV>
 __device__ __forceinline__ void bwd_store_zeros(const CrossBwdArgs& a, const BwdTask& tk) {
-    const int heads = KV ? a.Hkv : a.H, b = tk.bh / heads, h = tk.bh % heads;
-    const int rows = min(kBT, (KV ? a.Nk : a.N) - tk.blk * kBT);
-    for (int x = threadIdx.x; x < rows * (D / 8); x += kBwdThreads) {
-        const int64_t row = tk.blk * kBT + x / (D / 8);
-        const int c = 8 * (x % (D / 8));
+    const QueryBox box = query_box(a, tk.bh, KV ? 0 : tk.blk);
+    const int kv_h = tk.bh - box.b * a.Hkv;
+    for (int x = threadIdx.x; x < kBT * (D / 8); x += kBwdThreads) {
+        const int r = x / (D / 8), c = 8 * (x % (D / 8));
+        const int64_t row = tk.blk * kBT + r;
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
         if (KV) {
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.dk) + b * a.dk_bs + h * a.dk_hs + row * a.dk_ns + c) = zero;
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.dv) + b * a.dv_bs + h * a.dv_hs + row * a.dv_ns + c) = zero;
+            if (row >= a.Nk) break;
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.dk) + box.b * a.dk_bs + kv_h * a.dk_hs + row * a.dk_ns + c) = zero;
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.dv) + box.b * a.dv_bs + kv_h * a.dv_hs + row * a.dv_ns + c) = zero;
         } else {
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.dq) + b * a.dq_bs + h * a.dq_hs + row * a.dq_ns + c) = zero;
+            int h, i;
+            if (query_row(a, box, r, h, i))
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.dq) + box.b * a.dq_bs + h * a.dq_hs + i * a.dq_ns + c) = zero;
         }
     }
 }
@@ -343,6 +366,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_kernel(const __grid_c
         tmem_alloc(bars.tmem_slot, kTmemCols);
         tmem_relinquish();
     }
+    if constexpr (CROSS && KV) {
+        // Rows of the streamed tiles behind the box that copies fill: zeros, which
+        // their weights of 0 meet (a box is whole heads of one group, so that all
+        // others are this group's or, past Nq, zeros too).
+        const int from = a.box_h * a.box_i;
+        if (from < kBT) {
+            for (int x = threadIdx.x; x < L::kSA * 2 * (D / 64) * (kBT - from) * 8; x += kBwdThreads) {
+                const int piece = x % 8, y = x / 8, r = from + y % (kBT - from), z = y / (kBT - from);
+                uint8_t* tile = smem + L::kRingA + z / (2 * (D / 64)) * L::kSlotA + z % (2 * (D / 64)) * L::kAtomIn;
+                *reinterpret_cast<uint4*>(tile + r * 128 + piece * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -363,7 +400,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_kernel(const __grid_c
     const uint32_t t_acc2 = t_acc1 + D;
     const int blk0 = tk.blk * kBT;  // first row of the resident tiles
     // K/V head of the task (dK/dV: the task's own head; dQ: the one its query head reads)
-    const int kvh = KV ? tk.bh : kv_head_of(tk.bh, a.H, a.Hkv);
+    const int kvh = KV || CROSS ? tk.bh : kv_head_of(tk.bh, a.H, a.Hkv);
 
     if (warp == kTmaWarp) {
         // ---------------- TMA producer ----------------
@@ -372,25 +409,39 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_kernel(const __grid_c
             const CUtensorMap* outer2 = KV ? &a.tmap_v : &a.tmap_do;
             const CUtensorMap* inner1 = KV ? &a.tmap_q : &a.tmap_k;
             const CUtensorMap* inner2 = KV ? &a.tmap_do : &a.tmap_v;
-            auto load = [&](void* dst, const CUtensorMap* map, uint64_t* bar, int x, int row, int head, int heads) {
+            // Rows from `row` on of head `head` (cross: of batch entry kv_b).
+            int kv_b = 0, kv_h = 0;
+            uint32_t q_bytes = 2 * L::kTile;  // of a Q and a dO tile
+            QueryBox outer_q = {blk0, tk.bh, 0};
+            if constexpr (CROSS) {
+                kv_b = kvh / a.Hkv;
+                kv_h = kvh - kv_b * a.Hkv;
+                q_bytes = 2 * (D / 64) * a.box_h * a.box_i * 128;
+                outer_q = query_box(a, kvh, tk.blk);
+            }
+            auto load = [&](void* dst, const CUtensorMap* map, uint64_t* bar, int x, int row, int head) {
                 if constexpr (CROSS)
-                    tma_load_4d(dst, map, bar, x, row, head % heads, head / heads);
+                    tma_load_4d(dst, map, bar, x, row, head, kv_b);
                 else
                     tma_load_3d(dst, map, bar, x, row, head);
             };
-            const int outer_heads = KV ? a.Hkv : a.H, inner_heads = KV ? a.H : a.Hkv;  // of a batch entry
-            mbar_arrive_expect_tx(bars.outer_full, 2 * L::kTile);
-            const int oh = KV ? kvh : tk.bh;  // head of the resident tiles
+            mbar_arrive_expect_tx(bars.outer_full, KV ? 2 * L::kTile : q_bytes);
+            const int outer_row = CROSS && !KV ? outer_q.i : blk0;
+            const int oh = CROSS ? (KV ? kv_h : outer_q.h) : (KV ? kvh : tk.bh);  // head of the resident tiles
             for (int at = 0; at < D / 64; ++at) {
-                load(smem + L::kOuter + at * kBT * 128, outer1, bars.outer_full, at * 64, blk0, oh, outer_heads);
-                load(smem + L::kOuter + L::kTile + at * kBT * 128, outer2, bars.outer_full, at * 64, blk0, oh,
-                     outer_heads);
+                load(smem + L::kOuter + at * kBT * 128, outer1, bars.outer_full, at * 64, outer_row, oh);
+                load(smem + L::kOuter + L::kTile + at * kBT * 128, outer2, bars.outer_full, at * 64, outer_row, oh);
             }
             int issued_a = 0, issued_b = 0;
             bool ok = true;
             for (int it = 0; it < tk.n && ok; ++it) {
-                const int row0 = (tk.j0 + at_tile(it) % tk.per_head) * kBT;
-                const int qh = KV ? bwd_query_head(a, tk, at_tile(it)) : tk.bh;  // head of the Q / dO tiles
+                int row0 = (tk.j0 + at_tile(it) % tk.per_head) * kBT;
+                int ih = KV ? bwd_query_head(a, tk, at_tile(it)) : kvh;  // head of the streamed tiles
+                if constexpr (CROSS) {
+                    const QueryBox q = query_box(a, kvh, KV ? at_tile(it) : 0);
+                    if (KV) row0 = q.i;
+                    ih = KV ? q.h : kv_h;
+                }
                 const int sa = it % L::kSA;
                 if (it >= L::kSA) {
                     ok = mbar_wait_bounded(&bars.empty_a[sa], ((it / L::kSA) - 1) & 1u, bars.abort_flag,
@@ -398,17 +449,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_kernel(const __grid_c
                     if (!ok) break;
                 }
                 uint8_t* st = smem + L::kRingA + sa * L::kSlotA;
-                mbar_arrive_expect_tx(&bars.full_a[sa], KV ? 2 * L::kTileIn + L::kStats : L::kTile);
+                mbar_arrive_expect_tx(&bars.full_a[sa], KV ? q_bytes + L::kStats : L::kTile);
                 for (int at = 0; at < D / 64; ++at) {
-                    load(st + at * L::kAtomIn, inner1, &bars.full_a[sa], at * 64, row0, KV ? qh : kvh, inner_heads);
-                    if (KV)
-                        load(st + L::kTileIn + at * L::kAtomIn, inner2, &bars.full_a[sa], at * 64, row0, qh,
-                             inner_heads);
+                    load(st + at * L::kAtomIn, inner1, &bars.full_a[sa], at * 64, row0, ih);
+                    if (KV) load(st + L::kTileIn + at * L::kAtomIn, inner2, &bars.full_a[sa], at * 64, row0, ih);
                 }
                 if (KV) {
-                    const float* stats = a.ws + static_cast<int64_t>(qh) * 2 * a.Npad + row0;
+                    const float* stats = a.ws + static_cast<int64_t>(ih) * 2 * a.Npad + row0;
+                    int apart = a.Npad;
+                    if constexpr (CROSS) {  // [tile][2][128]
+                        stats = a.ws + (static_cast<int64_t>(kvh) * a.tiles + at_tile(it)) * (2 * kBT);
+                        apart = kBT;
+                    }
                     bulk_load(st + 2 * L::kTileIn, stats, kBT * 4, &bars.full_a[sa]);
-                    bulk_load(st + 2 * L::kTileIn + kBT * 4, stats + a.Npad, kBT * 4, &bars.full_a[sa]);
+                    bulk_load(st + 2 * L::kTileIn + kBT * 4, stats + apart, kBT * 4, &bars.full_a[sa]);
                 }
                 ++issued_a;
                 if (!KV) {
@@ -421,7 +475,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_kernel(const __grid_c
                     uint8_t* sv = smem + L::kRingB + sb * L::kSlotB;
                     mbar_arrive_expect_tx(&bars.full_b[sb], L::kTile);
                     for (int at = 0; at < D / 64; ++at)
-                        load(sv + at * kBT * 128, inner2, &bars.full_b[sb], at * 64, row0, kvh, inner_heads);
+                        load(sv + at * kBT * 128, inner2, &bars.full_b[sb], at * 64, row0, ih);
                     ++issued_b;
                 }
             }
@@ -643,8 +697,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_kernel(const __grid_c
         float nlse2_r = 0.f, ndelta_r = 0.f;  // -LSE*log2(e) and -Delta of this row
         if (!KV) {
             const float* stats = a.ws + static_cast<int64_t>(tk.bh) * 2 * a.Npad + row;
+            int apart = a.Npad;
+            if constexpr (CROSS) {
+                stats = a.ws + (static_cast<int64_t>(tk.bh) * a.tiles + tk.blk) * (2 * kBT) + r;
+                apart = kBT;
+            }
             nlse2_r = stats[0];        // -inf past N: the row's P is 0
-            ndelta_r = stats[a.Npad];
+            ndelta_r = stats[apart];
         }
         bool ok = true;
         int failed_at = 0;  // first tile not handed over when a wait gave up
@@ -814,7 +873,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_kernel(const __grid_c
             // Rows leave through 4 KB a warp of the resident tiles' memory, which no
             // product reads any more, so that a warp writes whole rows: fp32 parts 32
             // elements at a time, gradients its half of them.
-            const int heads = KV ? a.Hkv : a.H, accs = KV ? 2 : 1;
+            const int accs = KV ? 2 : 1;
             const bool cut = (KV ? a.parts_k : a.parts_q) > 1;
             uint8_t* stage = smem + L::kOuter + warp * 4096;
             const int row0 = blk0 + quarter * 32;
@@ -822,7 +881,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_kernel(const __grid_c
             for (int acc = 0; acc < accs; ++acc) {
                 const float mul = (KV && acc == 0) ? 1.f : a.scale;
                 float* part = (KV ? a.part_kv : a.part_q) +
-                              ((((static_cast<int64_t>(tk.part) * (KV ? a.BHkv : a.BH) + tk.bh) * (KV ? a.tiles_k : a.num_tiles)) *
+                              ((((static_cast<int64_t>(tk.part) * a.BHkv + tk.bh) * (KV ? a.tiles_k : a.tiles)) *
                                     kBT + row0) * accs + acc) * D;
 #pragma unroll 1
                 for (int c = 0; c < D / 64; ++c) {
@@ -862,18 +921,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_kernel(const __grid_c
                 if (cut) continue;
                 __syncwarp();
                 constexpr int kPieces = D / 16;  // of 16 bytes in a half row
-                const int b = tk.bh / heads, h = tk.bh - b * heads;
+                const QueryBox box = query_box(a, tk.bh, KV ? 0 : tk.blk);
+                const int64_t hs = KV ? (acc == 0 ? a.dv_hs : a.dk_hs) : a.dq_hs;
                 const int64_t ns = KV ? (acc == 0 ? a.dv_ns : a.dk_ns) : a.dq_ns;
                 uint16_t* base = static_cast<uint16_t*>(KV ? (acc == 0 ? a.dv : a.dk) : a.dq) +
-                                 b * (KV ? (acc == 0 ? a.dv_bs : a.dk_bs) : a.dq_bs) +
-                                 h * (KV ? (acc == 0 ? a.dv_hs : a.dk_hs) : a.dq_hs) + half * (D / 2) + 8 * (lane % kPieces);
+                                 box.b * (KV ? (acc == 0 ? a.dv_bs : a.dk_bs) : a.dq_bs) + half * (D / 2) + 8 * (lane % kPieces);
 #pragma unroll
                 for (int e = 0; e < kPieces; ++e) {
                     const int rr = e * (32 / kPieces) + lane / kPieces;
                     uint4 y = *reinterpret_cast<const uint4*>(stage + rr * 128 + (((lane % kPieces) ^ (rr & 7)) << 4));
+                    int h = tk.bh - box.b * a.Hkv, i = row0 + rr;
+                    bool stored = i < a.Nk;
                     // (a key that no row sees: its accumulator may be anything)
-                    if (KV && row0 + rr >= keys) y = make_uint4(0u, 0u, 0u, 0u);
-                    if (fin && row0 + rr < (KV ? a.Nk : a.N)) *reinterpret_cast<uint4*>(base + (row0 + rr) * ns) = y;
+                    if (KV && i >= keys) y = make_uint4(0u, 0u, 0u, 0u);
+                    if (!KV) stored = query_row(a, box, quarter * 32 + rr, h, i);
+                    if (fin && stored) *reinterpret_cast<uint4*>(base + h * hs + i * ns) = y;
                 }
             }
         }

@@ -405,14 +405,27 @@ int cross_splits(int64_t B, int64_t Hkv, const RowTiles& t, int64_t Nk) {
 // tiles of all heads of its group) and of a query tile (key tiles) are cut into, so
 // that few blocks fill the GPU.
 struct CrossParts {
-    int64_t k = 1, q = 1;             // parts
-    int64_t kv_rows = 0, q_rows = 0;  // rows of parts (dk and dv alike; dq)
+    int64_t box_i = 0, box_h = 1, n_i = 0, tiles = 0;  // tiles of a K/V head's query rows
+    int64_t k = 1, q = 1;                              // parts
+    int64_t kv_rows = 0, q_rows = 0;                   // rows of parts (dk and dv alike; dq)
 };
 CrossParts cross_parts(int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t Nk) {
     CrossParts p;
-    const int64_t tq = ceil_div(Nq, 128), tk = ceil_div(Nk, 128);
-    if (tq == 0 || tk == 0) return p;
-    const int64_t blocks_k = B * Hkv * tk, blocks_q = B * H * tq, inner_k = H / Hkv * tq, inner_q = tk;
+    const int64_t tk = ceil_div(Nk, 128), share = H / Hkv;
+    if (Nq == 0) return p;
+    // Whole heads of the group fill a box: no box has rows of another group.
+    for (int64_t bh = 1; bh <= std::min<int64_t>(share, 128); ++bh) {
+        if (share % bh != 0) continue;
+        const int64_t bi = std::min<int64_t>(Nq, 128 / bh), n = ceil_div(Nq, bi) * (share / bh);
+        if (p.tiles == 0 || n < p.tiles) {
+            p.box_i = bi;
+            p.box_h = bh;
+            p.n_i = ceil_div(Nq, bi);
+            p.tiles = n;
+        }
+    }
+    if (tk == 0) return p;
+    const int64_t blocks_k = B * Hkv * tk, blocks_q = B * Hkv * p.tiles, inner_k = p.tiles, inner_q = tk;
     // The tasks of both kernels run side by side.  In units of 0.4 us: an inner tile of
     // a key block takes 4, of a query tile 3; a task's start and end 12, a part 3 more,
     // and adding the parts 8.  With more tasks than SMs the last ones start late.
@@ -437,7 +450,7 @@ CrossParts cross_parts(int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t Nk
         }
     }
     if (p.k > 1) p.kv_rows = p.k * B * Hkv * tk * 128;
-    if (p.q > 1) p.q_rows = p.q * B * H * tq * 128;
+    if (p.q > 1) p.q_rows = p.q * B * Hkv * p.tiles * 128;
     return p;
 }
 
@@ -1614,9 +1627,8 @@ int fattn_fwd_cross(const void* q, const void* k, const void* v, void* o, float*
 int64_t fattn_bwd_cross_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t Nk, int64_t D) {
     if (B <= 0 || H <= 0 || Nq <= 0 || Nk < 0 || validate_cross(B, H, Hkv, Nq, Nk, D, 1.f, FATTN_BF16) != FATTN_OK)
         return 0;
-    const int64_t stats = fattn_bwd_workspace_bytes(B, H, Nq);
     const CrossParts p = cross_parts(B, H, Hkv, Nq, Nk);
-    return stats <= 0 ? 0 : stats + p.kv_rows * 2 * D * 4 + p.q_rows * D * 4;
+    return B * Hkv * p.tiles * 1024 + p.kv_rows * 2 * D * 4 + p.q_rows * D * 4;
 }
 
 int fattn_bwd_cross(const void* q, const void* k, const void* v, const void* o, const void* dout, const float* lse,
@@ -1659,9 +1671,10 @@ int fattn_bwd_cross(const void* q, const void* k, const void* v, const void* o, 
     for (int j = 0; j < 5; ++j)
         if (ptrs[j] && views_overlap(small[2], range_of(rows[j]))) return FATTN_ERR_INVALID_ARG;
     if (views_overlap(small[2], small[0]) || views_overlap(small[2], small[1])) return FATTN_ERR_INVALID_ARG;
-    const int64_t tiles_q = ceil_div(Nq, 128), tiles_k = ceil_div(Nk, 128);
+    const int64_t tiles_k = ceil_div(Nk, 128);
+    const CrossParts parts = cross_parts(B, H, Hkv, Nq, Nk);
     // (Blocks are cut into parts only where there are few.)
-    if (tiles_q * B * H > 0x7fffffffll || tiles_k * B * Hkv > 0x7fffffffll || tiles_q * 128 * H > 0x7fffffffll)
+    if (parts.tiles * B * Hkv > 0x7fffffffll || tiles_k * B * Hkv > 0x7fffffffll || parts.n_i * parts.box_i * H > 0x7fffffffll)
         return FATTN_ERR_UNSUPPORTED;
     int sms = 0;
     st = current_sm_count(&sms);
@@ -1672,28 +1685,30 @@ int fattn_bwd_cross(const void* q, const void* k, const void* v, const void* o, 
     CUtensorMap* maps[5] = {&a.tmap_q, &a.tmap_k, &a.tmap_v, nullptr, &a.tmap_do};
     for (int i = 0; i < 5; ++i)  // (without queries or keys nothing is loaded)
         if (maps[i] && Nq > 0 && Nk > 0 && rows_encode_map(maps[i], {ptrs[i], B, of_keys[i] ? Hkv : H, of_keys[i] ? Nk : Nq, strides + 3 * i,
-                                                 128, 1, 1}, D, bf16) != cudaSuccess)
+                                                 of_keys[i] ? 128 : static_cast<int>(parts.box_i),
+                                                 of_keys[i] ? 1 : static_cast<int>(parts.box_h), 1}, D, bf16) != cudaSuccess)
             return FATTN_ERR_CUDA;
     a.ws = static_cast<float*>(workspace);
     a.dq = dq;
     a.dk = dk;
     a.dv = dv;
     a.N = static_cast<int>(Nq);
-    a.Npad = static_cast<int>(bwd_padded_rows(Nq));
     a.BH = static_cast<int>(B * H);
     a.H = static_cast<int>(H);
     a.Hkv = static_cast<int>(Hkv);
     a.BHkv = static_cast<int>(B * Hkv);
-    a.num_tiles = static_cast<int>(tiles_q);
+    a.box_i = static_cast<int>(parts.box_i);
+    a.box_h = static_cast<int>(parts.box_h);
+    a.n_i = static_cast<int>(parts.n_i);
+    a.tiles = static_cast<int>(parts.tiles);
     a.sl2 = scale * kLog2e;
     a.scale = scale;
     a.timeout_ns = kDefaultTimeoutNs;
     a.Nk = static_cast<int>(Nk);
     a.tiles_k = static_cast<int>(tiles_k);
-    const CrossParts parts = cross_parts(B, H, Hkv, Nq, Nk);
     a.parts_k = static_cast<int>(parts.k);
     a.parts_q = static_cast<int>(parts.q);
-    a.part_kv = a.ws + std::max<int64_t>(fattn_bwd_workspace_bytes(B, H, Nq), 0) / 4;
+    a.part_kv = a.ws + B * Hkv * parts.tiles * 256;
     a.part_q = a.part_kv + parts.kv_rows * 2 * D;
     a.lens = kv_lens;
     a.o = o;

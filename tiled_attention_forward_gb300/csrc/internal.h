@@ -221,12 +221,17 @@ cudaError_t bwd_launch(const BwdArgs& a, const void* o, const void* dout, const 
                        bool bf16, bool causal, cudaStream_t s);
 cudaError_t bwd_read_and_clear_error_word(uint32_t* out);
 
-struct CrossBwdArgs : BwdArgs {  // tmaps {D, Nq or Nk, heads, B}; N = Nq, num_tiles = Npad / 128
+struct CrossBwdArgs : BwdArgs {
+    // tmaps {D, Nq or Nk, heads, B}, boxes {64, box_i, box_h, 1} of q and dO, {64, 128,
+    // 1, 1} of k and v; N = Nq; Npad and num_tiles are unused; ws [B*Hkv][tiles][2][128]
+    int box_i, box_h;          // tokens and heads of a tile of query rows (box_h divides H/Hkv)
+    int n_i;                   // tiles along tokens
+    int tiles;                 // tiles of a K/V head: n_i * (H/Hkv) / box_h
     int Nk;
     int tiles_k;               // ceil(Nk / 128)
     int parts_k, parts_q;      // parts that the inner tiles of a key block / a query tile are cut into
     float* part_kv;            // fp32 [parts_k][B*Hkv][tiles_k * 128][dv, dk][D], where parts_k > 1
-    float* part_q;             // fp32 [parts_q][B*H][Npad][D], where parts_q > 1
+    float* part_q;             // fp32 [parts_q][B*Hkv][tiles * 128][D], where parts_q > 1
     const int32_t* lens;       // visible keys of each batch entry, or nullptr: Nk
     int64_t dq_bs, dq_hs, dq_ns, dk_bs, dk_hs, dk_ns, dv_bs, dv_hs, dv_ns;  // element strides
     const void* o;             // the row statistics' inputs, by strides
