@@ -80,11 +80,11 @@ BWD_FLOP_FACTOR = 2.5
 # once the kernel has changed.
 KERNEL_SOURCES = {"tc": ["fwd_tc.cu", "fwd_tc_kernel.cuh", "sm103_ptx.cuh"], "ffma": ["fwd_ffma.cu"],
                   "unfused": ["fwd_unfused.cu", "sm103_ptx.cuh"],
-                  "bwd": ["bwd_tc.cu", "sm103_ptx.cuh"]}
+                  "bwd": ["bwd_tc.cu", "bwd_tc_kernel.cuh", "sm103_ptx.cuh"]}
 NCU_TRAFFIC = {
-    "bf16_B4_H16_N4096_D128": (202378496 + 37780992, "0629ca7bfe420bee"),
-    "bf16_B2_H32_N8192_D128_causal_qstd4": (409667584 + 107061760, "0629ca7bfe420bee"),
-    "fp16_B1_H16_N16000_D64_causal": (98405376 + 7730688, "0629ca7bfe420bee"),
+    "bf16_B4_H16_N4096_D128": (201958400 + 41573120, "7417b72dad632b2a"),
+    "bf16_B2_H32_N8192_D128_causal_qstd4": (411443456 + 111231488, "7417b72dad632b2a"),
+    "fp16_B1_H16_N16000_D64_causal": (98417152 + 9909504, "7417b72dad632b2a"),
     "fp32_B4_H8_N8192_D64_causal": (201639936 + 51146240, "61c5185890f7842f"),
 }
 
@@ -99,9 +99,9 @@ NCU_TRAFFIC_UNFUSED = {
 
 # The backward: DRAM bytes of one step (statistics, dK/dV and dQ kernels).
 NCU_TRAFFIC_BWD = {
-    "bf16_B4_H16_N4096_D128": (676513536 + 154105856, "77268889cef676d6"),
-    "bf16_B2_H32_N8192_D128_causal_qstd4": (7977567744 + 355400704, "77268889cef676d6"),
-    "fp16_B1_H16_N16000_D64_causal": (463855360 + 51330816, "77268889cef676d6"),
+    "bf16_B4_H16_N4096_D128": (676450560 + 152076288, "5d668d5d83dc1f30"),
+    "bf16_B2_H32_N8192_D128_causal_qstd4": (7985778944 + 355318016, "5d668d5d83dc1f30"),
+    "fp16_B1_H16_N16000_D64_causal": (460237056 + 51237760, "5d668d5d83dc1f30"),
 }
 
 

@@ -498,8 +498,10 @@ FATTN_API int fattn_decode_kv4(const void* q, void* o, float* lse, const int64_t
  *                aligned; contents ignored on entry.  Calls that run at the same
  *                time need workspaces of their own.
  * The stride of a dimension of q of more than one is positive.  With prefix_width
- * = 0 this is fattn_decode.  Everything else as fattn_decode.  Two launches (the
- * prefix, the sequences' own keys and the join).  (B = 1 with many rows serves a
+ * = 0 this is fattn_decode.  Everything else as fattn_decode.  Where the prefix could
+ * be long (prefix_width * page_size tokens) for the batch: three launches (the own
+ * keys, the prefix, the join), and the prefix is read once; else one, in which every
+ * sequence reads it.  B * H * Nq is below 2^27 - 8.  (B = 1 with many rows serves a
  * chunk of new tokens over a long cached prefix.)
  */
 FATTN_API int64_t fattn_decode_shared_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t D);
@@ -614,7 +616,9 @@ FATTN_API int fattn_fwd_cross(const void* q, const void* k, const void* v, void*
  *   workspace : caller-owned, fattn_bwd_cross_workspace_bytes, 16-byte aligned;
  *               contents ignored on entry.
  * dq, dk and dv overlap nothing else (each may be another slice of a tensor that
- * others are slices of).  No atomics: the result is the same for every run.
+ * others are slices of).  No atomics: the result is the same for every run.  Three
+ * launches (row statistics, dK/dV, dQ), or four where there are few rows or keys (the
+ * sum of parts).
  */
 FATTN_API int64_t fattn_bwd_cross_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t Nk,
                                         int64_t D);

@@ -1,5 +1,21 @@
 // bwd_cross.cu -- the backward (bwd_tc_kernel.cuh) of cross attention: keys of a
-// length of their own, rows by strides; and the kernel of its row statistics.
+// length of their own, rows by strides; the kernel of its row statistics, and the one
+// that adds the parts of gradients that were cut.
+//
+// The query rows of all heads that share a K/V head are stacked into tiles, as in the
+// forward, but of whole heads' boxes: a K/V head's dK and dV are sums over them, and
+// no box may bring another group's rows.  The key kernel (dK, dV) and the query
+// kernel (dQ) need nothing of one another, so the second starts as the first one's
+// last CTAs run.  Where there are few blocks their inner tiles are cut into parts.
+//
+// Measured (GB300): 4 entries of 16 heads, 4096 queries over up to 2000 keys, D = 128,
+// bf16 (344 GFLOP, ragged) 481 us = 716 TFLOP/s: statistics 31, dK/dV 254, dQ 226, the
+// last two overlapping by 30.  dK/dV keeps the tensor pipe 53 % busy (three and a half waves of
+// CTAs), dQ 43 % (8 key tiles a CTA, a third of whose time is its start and its end).
+// Dense-shaped, 64 heads of 4096: 1454 us = 945 TFLOP/s (fattn_bwd 910).  2 entries of
+// 8 heads on 2, 257 queries over up to 777 keys, D = 64: 19 us (one kernel after the
+// other, uncut: 37).  32 heads on 4, D = 64, 28 queries over up to 5342 keys, 12
+// entries: 113 us (a tile per head: 230).
 #include "bwd_tc_kernel.cuh"
 
 #include <algorithm>

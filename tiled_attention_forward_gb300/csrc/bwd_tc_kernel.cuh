@@ -42,6 +42,7 @@
 
 #include "internal.h"
 #include "sm103_ptx.cuh"
+#include "tma_4d.cuh"
 
 namespace fattn {
 namespace {

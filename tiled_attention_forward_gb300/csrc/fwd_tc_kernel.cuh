@@ -55,6 +55,7 @@
 
 #include "internal.h"
 #include "sm103_ptx.cuh"
+#include "tma_4d.cuh"
 
 namespace fattn {
 
