@@ -293,3 +293,75 @@ def test_captured_and_on_another_stream():
         want = (o2, l2) + fattn.bwd_cross(q, k, v, o2, l2, do, t, stream=s)
         ok()
         assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, workspaces of their own, give what they give alone."""
+    sets = [make(3, 8, 2, Nq, 1500, 64, torch.float16, 60 + Nq, [1500, 700, 20], fill=0.5) for Nq in (70, 33)]
+    alone = []
+    for q, k, v, do, t in sets:
+        o, lse = fattn.fwd_cross(q, k, v, t)
+        alone.append((o, lse) + fattn.bwd_cross(q, k, v, o, lse, do, t))
+    ok()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(5):
+        got = []
+        for s, (q, k, v, do, t) in zip(streams, sets):
+            s.wait_stream(torch.cuda.current_stream())
+            o, lse = fattn.fwd_cross(q, k, v, t, stream=s)
+            got.append((o, lse) + fattn.bwd_cross(q, k, v, o, lse, do, t, stream=s))
+        ok()
+        for a, b in zip(alone, got):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("Nq", [1, 40])
+def test_tensors_past_32_bits(Nq):
+    """17 million keys (4.4 GB each of K and V): the last one outweighs all others, so
+    that O is its value, its value's gradient the sum of dO, and dQ and dK vanish."""
+    D, Nk = 128, 17_000_001
+    g = torch.Generator().manual_seed(61)
+    k, v = (torch.zeros(1, 1, Nk, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q, do = (torch.randn(1, 1, Nq, D, generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    q[..., 0] = 64.0
+    k[0, 0, -1, 0] = 16.0                     # a score of 1024 / sqrt(128) = 90.5 and more
+    v[0, 0, -1] = torch.randn(D, generator=g).to(torch.bfloat16).cuda()
+    v[0, 0, -2] = 1000.0                      # weighs e^-90
+    o, lse = fattn.fwd_cross(q, k, v)
+    dk, dv = torch.full_like(k, math.nan), torch.full_like(v, math.nan)
+    dq, _, _ = fattn.bwd_cross(q, k, v, o, lse, do, dk=dk, dv=dv)
+    ok()
+    assert torch.equal(o, v[:, :, -1:].expand_as(o))
+    want = do.double().sum(2)[0, 0]
+    assert ((dv[0, 0, -1].double() - want).abs() <= 2.0 ** -8 * (want.abs() + do.double().abs().sum(2)[0, 0])).all()
+    for start in range(0, Nk - 1, 1 << 22):
+        part = slice(start, min(start + (1 << 22), Nk - 1))
+        assert dv[0, 0, part].abs().max() <= 1e-30 and dk[0, 0, part].abs().max() <= 1e-30
+    # dS of the last key is P (dP - Delta), both the sum of dO O: fp32 sums of D exact
+    # products, each off by at most D 2^-23 of the sum of magnitudes
+    small = 2 * D * 2.0 ** -23 * (do.double().abs() * o.double().abs()).sum(-1).max().item() * 16 * D ** -0.5
+    assert dq.double().abs().max().item() <= small and dk[0, 0, -1].isfinite().all()
+
+
+def test_refusals_of_the_binding():
+    q, k, v, do, t = make(2, 4, 2, 5, 30, 64, torch.float16, 62)
+    o, lse = fattn.fwd_cross(q, k, v, t)
+    for bad in (dict(q=q.float()), dict(q=q[0]), dict(k=k[:, :, :-1]), dict(v=v.bfloat16()), dict(kv_lens=t.long()),
+                dict(kv_lens=t[:1]), dict(out=o[..., :32]), dict(lse=lse.double()), dict(k=k.cpu()),
+                dict(q=q.transpose(2, 3)), dict(workspace=torch.empty(8))):
+        args = dict(dict(q=q, k=k, v=v, kv_lens=t), **bad)
+        with pytest.raises(ValueError):
+            fattn.fwd_cross(**args)
+    for bad in (dict(o=o.float()), dict(dout=do[:1]), dict(lse=lse[..., :-1]), dict(dq=torch.empty_like(k)),
+                dict(dk=torch.empty_like(q)), dict(kv_lens=t.cpu())):
+        with pytest.raises(ValueError):
+            fattn.bwd_cross(**dict(dict(q=q, k=k, v=v, o=o, lse=lse, dout=do, kv_lens=t), **bad))
+    for f, args in ((fattn.fwd_cross, dict(q=q, k=k, v=v, out=q)),
+                    (fattn.fwd_cross, dict(q=q, k=k, v=v, scale=-1.0)),
+                    (fattn.fwd_cross, dict(q=q, k=k, v=v, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))),
+                    (fattn.fwd_cross, dict(q=q[:1].expand(2, -1, -1, -1), k=k, v=v)),
+                    (fattn.bwd_cross, dict(q=q, k=k, v=v, o=o, lse=lse, dout=do, dq=do))):
+        with pytest.raises(fattn.FattnError) as e:
+            f(**args)
+        assert e.value.code == 1
+    ok()

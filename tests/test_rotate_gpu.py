@@ -224,3 +224,48 @@ def test_training_step_on_a_graph():
         step(want)
         ok()
         assert torch.equal(grad, want) and torch.isfinite(grad).all() and (grad != 0).any()
+
+
+def test_tensors_past_32_bits():
+    """17 million tokens (4.4 GB of q): the first and the last rows."""
+    N, D = 17_000_001, 128
+    q = torch.zeros(1, 1, N, D, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator().manual_seed(6)
+    rows = [0, 1, 2 ** 24 - 1, 2 ** 24, N - 2, N - 1]
+    q[0, 0, rows] = torch.randn(len(rows), D, generator=g).to(torch.bfloat16).cuda()
+    cos, sin = R.tables(MAX_POS, D)
+    pos = torch.randint(0, MAX_POS, (3, 1, N), generator=g, dtype=torch.int32)
+    axes = axes_of("sections", D, 3)
+    got, _ = fattn.rotate(q, pos.cuda(), cos.cuda(), sin.cuda(), axes=axes)
+    ok()
+    y, mag = M.rotated(q[:, :, rows].cpu(), pos[:, :, rows], axes, cos, sin, False)
+    R.check(got[:, :, rows], y, R.rotated_bound(y, mag, torch.bfloat16), "far rows")
+    assert (got[0, 0, 2:2 ** 24 - 1] == 0).all() and (got[0, 0, 2 ** 24 + 1:N - 2] == 0).all()
+
+
+def test_refusals_of_the_binding():
+    D = 64
+    q, k = (torch.randn(2, h, 9, D, device="cuda").half() for h in (4, 2))
+    cos, sin = (t.cuda() for t in R.tables(MAX_POS, D))
+    pos = torch.zeros(3, 2, 9, dtype=torch.int32, device="cuda")
+    axes = axes_of("in turn", D, 3)
+    good = dict(q=q, pos=pos, cos=cos, sin=sin, axes=axes, k=k)
+    fattn.rotate(**good)
+    for bad in (dict(q=q.float()), dict(pos=pos[0]), dict(pos=pos.long()), dict(axes=axes[:-1]), dict(cos=cos.double()),
+                dict(sin=sin[:, :-1]), dict(k=k[:, :, :-1]), dict(q_out=q[:, :, :-1]), dict(pos=pos[:0]), dict(axes=None)):
+        with pytest.raises((ValueError, fattn.FattnError)):
+            fattn.rotate(**dict(good, **bad))
+    with pytest.raises(fattn.FattnError):      # a pair on an axis that pos does not have
+        fattn.rotate(**dict(good, axes=bytes([3]) * 32))
+    with pytest.raises((ValueError, TypeError)):
+        fattn.rotate(**dict(good, axes="0" * 32))
+    with pytest.raises((ValueError, TypeError)):
+        fattn.rotate(**dict(good, axes=[300] * 32))
+    kp = torch.zeros(2, 2, 16, D, dtype=torch.float16, device="cuda")
+    rows = dict(k=k[0].transpose(0, 1), v=k[1].transpose(0, 1), k_pages=kp, v_pages=kp.clone(), slots=torch.arange(9).cuda(), cos=cos,
+                sin=sin)
+    fattn.cache_append(**rows, pos=pos[:, 0].contiguous(), axes=axes)
+    for bad in (dict(pos=pos[0, 0], axes=axes), dict(pos=pos[:, 0].contiguous()), dict(pos=pos[:, 0].contiguous(), axes=axes[1:])):
+        with pytest.raises(ValueError):
+            fattn.cache_append(**rows, **bad)
+    ok()
