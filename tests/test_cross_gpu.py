@@ -217,6 +217,28 @@ def test_backward_cut_into_parts(case):
         R.check(x, r, b, name)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("case", [(8, 19, 19, 1403, 100, [100, 0, 1, 64, 99, 33, 17, 65]), (4, 76, 38, 700, 128, [128, 127, 0, 2]),
+                                  (3, 60, 20, 450, 5, None), (8, 19, 19, 900, 300, [300, 0, 128, 129, 1, 257, 256, 100]),
+                                  (4, 76, 38, 500, 200, None), (6, 30, 10, 333, 640, [640, 512, 513, 0, 385, 5])])
+def test_backward_of_many_query_tiles(D, case):
+    """A CTA takes a run of query tiles: over keys of one tile and of several, of entries with all, some and no keys."""
+    B, H, Hkv, Nq, Nk, lens = case
+    dt = torch.float16 if D == 64 else torch.bfloat16
+    q, k, v, do, t = make(B, H, Hkv, Nq, Nk, D, dt, Nq + D, lens)
+    lens = lens or [Nk] * B
+    o, lse = fattn.fwd_cross(q, k, v, t)
+    dq, dk, dv = (torch.full(x.shape, math.nan, dtype=dt, device="cuda") for x in (q, k, v))
+    got = fattn.bwd_cross(q, k, v, o, lse, do, t, dq=dq, dk=dk, dv=dv)
+    again = fattn.bwd_cross(q, k, v, o, lse, do, t)
+    ok()
+    assert all(torch.equal(x, y) for x, y in zip(got, again))
+    args, scale = [x.cpu() for x in (q, k, v, do)], fattn._default_scale(D)
+    ref = M.cross_grads(*args, lens, scale)
+    for name, x, r, b in zip(("dq", "dk", "dv"), got, ref, M.cross_grad_bounds(*args, lens, scale, dt, ref)):
+        R.check(x, r, b, name)
+
+
 @pytest.mark.parametrize("dtype,D", [("bf16", 128), ("fp16", 64)])
 def test_backward_layouts_and_repeats(dtype, D):
     """Gradients as slices of a projection's gradient, contiguous inputs, a second run: the same bits."""

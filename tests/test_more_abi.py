@@ -232,3 +232,11 @@ def test_plain_gradients_against_differences():
             up[i], down[i] = x + e, x - e
             diff = (loss(*up) - loss(*down)) / 2e-5
             assert abs(diff - dx[at]) <= 1e-8
+
+
+def test_axes_are_a_list():
+    """A number (of axes, of pairs) is no list of axes."""
+    for bad in (3, 32, 64):
+        with pytest.raises(TypeError):
+            fattn.rotate(torch.zeros(1, 1, 1, 64).half(), None, None, None, axes=bad, q_out=torch.zeros(1, 1, 1, 64).half())
+    assert fattn._axes([0, 1, 2]) == fattn._axes((0, 1, 2)) == fattn._axes(bytearray([0, 1, 2])) == bytes([0, 1, 2])

@@ -477,7 +477,8 @@ def rotary_axes(sections):
 
 
 def _axes(axes):
-    return axes if axes is None or isinstance(axes, bytes) else bytes(axes)
+    # (bytes(n) of a number would be n zeros.)
+    return axes if axes is None or isinstance(axes, bytes) else bytes(list(axes))
 
 
 def cache_append(k, v, k_pages, v_pages, slots, pos=None, cos=None, sin=None, interleaved=False, q=None,

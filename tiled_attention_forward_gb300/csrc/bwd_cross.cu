@@ -16,6 +16,7 @@
 // 8 heads on 2, 257 queries over up to 777 keys, D = 64: 19 us (one kernel after the
 // other, uncut: 37).  32 heads on 4, D = 64, 28 queries over up to 5342 keys, 12
 // entries: 113 us (a tile per head: 230).
+#include "bwd_cross_dq.cuh"
 #include "bwd_tc_kernel.cuh"
 
 #include <algorithm>
@@ -207,6 +208,29 @@ cudaError_t launch_add(const CrossBwdArgs& a, cudaStream_t s) {
                       kAddThreads, s, a, kv_rows);
 }
 
+// The query tiles of a K/V head shared out among chunks_q CTAs.  In half key tiles: a
+// query tile costs one more than its key tiles, a CTA's start and end 8.  With more
+// CTAs than SMs the last ones end late.
+template <int D, bool BF16, bool ONE>
+cudaError_t launch_dq(const CrossBwdArgs& a, int sms, cudaStream_t s) {
+    static std::atomic<bool> opted_in[kMaxDevices] = {};
+    auto* kernel = cross_dq_kernel<D, BF16, ONE>;
+    const cudaError_t e = opt_in_smem_once(kernel, CrossDqLayout<D, ONE>::kBytes, opted_in);
+    if (e != cudaSuccess) return e;
+    CrossBwdArgs x = a;
+    int64_t least = INT64_MAX;
+    for (int64_t m = 1; m <= std::min(a.tiles, 256); ++m) {  // query tiles of a CTA
+        const int64_t c = (a.tiles + m - 1) / m, ctas = c * a.BHkv, longest = m * (2 * a.tiles_k + 1) + 8;
+        const int64_t cost = ctas <= sms ? longest : std::max(longest, ctas * longest / sms + longest / 2);
+        if (cost < least) {
+            least = cost;
+            x.chunks_q = static_cast<int>(c);
+        }
+    }
+    return launch_overlapped(kernel, static_cast<unsigned>(static_cast<int64_t>(x.chunks_q) * a.BHkv), kBwdThreads,
+                             CrossDqLayout<D, ONE>::kBytes, s, x);
+}
+
 template <int D, bool BF16>
 cudaError_t launch_all(const CrossBwdArgs& a, int sms, cudaStream_t s) {
     // (Without queries the key kernel, without keys the query kernel writes zeros.)
@@ -227,6 +251,14 @@ cudaError_t launch_all(const CrossBwdArgs& a, int sms, cudaStream_t s) {
         if (e != cudaSuccess) return e;
     }
     if (a.tiles == 0) return cudaSuccess;
+    // D = 128: the memory holds two (Q, dO) pairs only where K and V stay.
+    if (a.parts_q == 1 && a.tiles_k > 0 && (D == 64 || a.tiles_k == 1)) {
+        if constexpr (D == 64)
+            e = a.tiles_k == 1 ? launch_dq<D, BF16, true>(a, sms, s) : launch_dq<D, BF16, false>(a, sms, s);
+        else
+            e = launch_dq<D, BF16, true>(a, sms, s);
+        return e == cudaSuccess ? launch_add<D, BF16>(a, s) : e;
+    }
     auto* kq = attn_bwd_kernel<D, BF16, false, false, true>;
     if ((e = opt_in_smem_once(kq, BwdLayout<D, false>::kBytes, q_done)) != cudaSuccess) return e;
     const unsigned grid_q = static_cast<unsigned>(a.tiles * a.BHkv * a.parts_q);
