@@ -9,9 +9,9 @@
 // last CTAs run.  Where there are few blocks their inner tiles are cut into parts.
 //
 // Measured (GB300): 4 entries of 16 heads, 4096 queries over up to 2000 keys, D = 128,
-// bf16 (344 GFLOP, ragged) 481 us = 716 TFLOP/s: statistics 31, dK/dV 254, dQ 226, the
-// last two overlapping by 30.  dK/dV keeps the tensor pipe 53 % busy (three and a half waves of
-// CTAs), dQ 43 % (8 key tiles a CTA, a third of whose time is its start and its end).
+// bf16 (344 GFLOP, ragged) 474 us = 726 TFLOP/s: statistics 31, dK/dV 254, dQ 225, the
+// last two overlapping.  dK/dV keeps the tensor pipe 53 % busy (three and a half waves of
+// CTAs), dQ 44 %.
 // Dense-shaped, 64 heads of 4096: 1454 us = 945 TFLOP/s (fattn_bwd 910).  2 entries of
 // 8 heads on 2, 257 queries over up to 777 keys, D = 64: 19 us (one kernel after the
 // other, uncut: 37).  32 heads on 4, D = 64, 28 queries over up to 5342 keys, 12
@@ -208,25 +208,46 @@ cudaError_t launch_add(const CrossBwdArgs& a, cudaStream_t s) {
                       kAddThreads, s, a, kv_rows);
 }
 
-// The query tiles of a K/V head shared out among chunks_q CTAs.  In half key tiles: a
-// query tile costs one more than its key tiles, a CTA's start and end 8.  With more
-// CTAs than SMs the last ones end late.
+// The CTAs that share a K/V head's query tiles: those with which the query kernel, which
+// starts as the key kernel's CTAs leave, ends first.  In units of 0.2 us: a key block's
+// CTA takes 8 a query tile and 24, a run of query tiles 6 a key tile, 3 a query tile and
+// 24; all keys are taken to be seen.  (8 heads of K/V, 4 query heads each, 222 queries
+// over 334 keys, D = 64, 7 entries: 2 CTAs a head 37.3 us, 4 43.6; 4 entries of 16 heads,
+// 4096 queries over up to 900 keys, D = 64: 8 CTAs a head 178, 2 205.)
+int chunks_of(const CrossBwdArgs& a, int sms) {
+    const int64_t blocks = static_cast<int64_t>(a.tiles_k) * a.BHkv * a.parts_k;
+    const int64_t block = 8 * ((a.tiles + a.parts_k - 1) / a.parts_k) + 24;
+    const int64_t early = blocks / sms * block, late = early + block;  // SMs free: at first and at last
+    const int64_t n_late = blocks % sms, n_early = sms - n_late;
+    int64_t least = INT64_MAX, chunks = 1;
+    for (int64_t m = 1; m <= std::min(a.tiles, 128); ++m) {  // query tiles of a CTA
+        const int64_t c = (a.tiles + m - 1) / m, ctas = c * a.BHkv, each = m * (6 * a.tiles_k + 3) + 24;
+        // CTAs that have ended by `t`.
+        auto ended = [&](int64_t t) {
+            return n_early * ((t - early) / each) + (t > late ? n_late * ((t - late) / each) : 0);
+        };
+        int64_t lo = early, hi = late + (ctas / sms + 1) * each;  // (by then all have)
+        while (hi - lo > 1) {
+            const int64_t t = lo + (hi - lo) / 2;
+            (ended(t) >= ctas ? hi : lo) = t;
+        }
+        const int64_t cost = hi + each / 8;  // (lengths differ: rather shorter ones)
+        if (cost < least) {
+            least = cost;
+            chunks = c;
+        }
+    }
+    return static_cast<int>(chunks);
+}
+
 template <int D, bool BF16, bool ONE>
-cudaError_t launch_dq(const CrossBwdArgs& a, int sms, cudaStream_t s) {
+cudaError_t launch_dq(const CrossBwdArgs& a, int chunks, cudaStream_t s) {
     static std::atomic<bool> opted_in[kMaxDevices] = {};
     auto* kernel = cross_dq_kernel<D, BF16, ONE>;
     const cudaError_t e = opt_in_smem_once(kernel, CrossDqLayout<D, ONE>::kBytes, opted_in);
     if (e != cudaSuccess) return e;
     CrossBwdArgs x = a;
-    int64_t least = INT64_MAX;
-    for (int64_t m = 1; m <= std::min(a.tiles, 256); ++m) {  // query tiles of a CTA
-        const int64_t c = (a.tiles + m - 1) / m, ctas = c * a.BHkv, longest = m * (2 * a.tiles_k + 1) + 8;
-        const int64_t cost = ctas <= sms ? longest : std::max(longest, ctas * longest / sms + longest / 2);
-        if (cost < least) {
-            least = cost;
-            x.chunks_q = static_cast<int>(c);
-        }
-    }
+    x.chunks_q = chunks;
     return launch_overlapped(kernel, static_cast<unsigned>(static_cast<int64_t>(x.chunks_q) * a.BHkv), kBwdThreads,
                              CrossDqLayout<D, ONE>::kBytes, s, x);
 }
@@ -251,12 +272,12 @@ cudaError_t launch_all(const CrossBwdArgs& a, int sms, cudaStream_t s) {
         if (e != cudaSuccess) return e;
     }
     if (a.tiles == 0) return cudaSuccess;
-    // D = 128: the memory holds two (Q, dO) pairs only where K and V stay.
-    if (a.parts_q == 1 && a.tiles_k > 0 && (D == 64 || a.tiles_k == 1)) {
-        if constexpr (D == 64)
-            e = a.tiles_k == 1 ? launch_dq<D, BF16, true>(a, sms, s) : launch_dq<D, BF16, false>(a, sms, s);
-        else
-            e = launch_dq<D, BF16, true>(a, sms, s);
+    // A run of query tiles a CTA, where that ends earlier; else, and for parts, one each.
+    // (One each by the run's kernel: 8 heads on 2, 257 queries over up to 777 keys, D =
+    // 128, 2 entries 23.8 us, and not 22.8.)
+    const int chunks = a.parts_q == 1 && a.tiles_k > 0 ? chunks_of(a, sms) : a.tiles;
+    if (chunks < a.tiles) {
+        e = a.tiles_k == 1 ? launch_dq<D, BF16, true>(a, chunks, s) : launch_dq<D, BF16, false>(a, chunks, s);
         return e == cudaSuccess ? launch_add<D, BF16>(a, s) : e;
     }
     auto* kq = attn_bwd_kernel<D, BF16, false, false, true>;

@@ -9,16 +9,16 @@
 // TMEM), and a query tile's dQ is read from TMEM together with the first dS of the
 // next, so that no warp waits for a product.  Rows leave through 4 KB of shared memory
 // a warp, whole halves of rows at a time.  ONE, keys of one tile (Nk <= 128): K and V
-// stay.  Otherwise they stream, in rings of their own (D = 64, whose memory holds two
-// pairs of Q and dO beside them).
+// stay.  Otherwise they stream, in rings of their own.  At D = 128 the memory then holds
+// one pair of Q and dO, which the next one's copy follows, and threads write their own
+// half rows.
 //
-// Measured (GB300; all of the gradients, a CTA a query tile -> this): keys of one tile,
-// 8 heads on 1, 3572 queries over 87 keys, D = 128, 18 entries 303 -> 224 us (the query
-// kernel 177 -> 90); 16 heads, 7594 over 7, D = 64, 14 entries 669 -> 365.  D = 64, 16
-// heads: 2000 queries over 200 keys, 12 entries 209 -> 159; 4 entries of 4096 over 512
-// 206 -> 173, over up to 2000 346 -> 321; 8 heads on 2, 257 over up to 777, 2 entries
-// 19.3 -> 19.7.  Bound by the chain S -> dS -> dQ of a tile, with one key tile by memory
-// too.
+// Measured (GB300; all of the gradients, a CTA a query tile -> this).  Keys of one tile:
+// 8 heads on 1, 3572 queries over 87 keys, D = 128, 18 entries 303 -> 225 us; 16 heads,
+// 7594 over 7, D = 64, 14 entries 669 -> 344.  16 heads, D = 64 / 128: 2000 queries over
+// 200 keys, 12 entries 209 -> 154 / 290 -> 289; 4 entries of 4096 over 512 206 -> 162 /
+// 289 -> 272, over up to 900 210 -> 178 / 293 -> 283, over up to 2000 346 -> 322 / 484 ->
+// 474.  Bound by the chain S -> dS -> dQ of a tile, with one key tile by memory too.
 #pragma once
 
 #include "bwd_tc_kernel.cuh"
@@ -29,14 +29,15 @@ namespace {
 template <int D, bool ONE>
 struct CrossDqLayout {
     static constexpr int kTile = kBT * D * 2;
-    static constexpr int kQs = ONE && D == 64 ? 4 : 2;  // slots of (Q, dO), K and V
-    static constexpr int kKs = ONE ? 1 : 4;
-    static constexpr int kVs = ONE ? 1 : 4;
+    static constexpr int kQs = ONE ? (D == 64 ? 4 : 2) : (D == 64 ? 2 : 1);  // slots of (Q, dO), K and V
+    static constexpr int kKs = ONE ? 1 : (D == 64 ? 4 : 3);
+    static constexpr int kVs = ONE ? 1 : (D == 64 ? 4 : 2);
+    static constexpr bool kStaged = ONE || D == 64;  // rows leave through memory of their own
     static constexpr int kQ = 0;
     static constexpr int kK = kQ + kQs * 2 * kTile;
     static constexpr int kV = kK + kKs * kTile;
     static constexpr int kRows = kV + kVs * kTile;               // 4 KB of each elementwise warp
-    static constexpr int kBar = kRows + 8 * 4096;
+    static constexpr int kBar = kRows + (kStaged ? 8 * 4096 : 0);
     // barriers: full and empty of Q, K and V slots, s_full[2], acc_full, done; abort flag; TMEM slot
     static constexpr int kBytes = kBar + (4 + 2 * (kQs + kKs + kVs)) * 8 + 16;
     static_assert(kBytes <= 227 * 1024, "shared memory");
@@ -138,6 +139,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dq_kernel(const __grid_c
                     tma_load_4d(st + L::kTile + at * kBT * 128, &a.tmap_do, &q_full[s], at * 64, q.i, q.h, b);
                 }
                 ++issued_q;
+                if (L::kQs == 1 && it + 1 < n) {  // the next tile's rows, on their way to L2
+                    const QueryBox x = query_box(a, kvh, u0 + it + 1);
+                    for (int at = 0; at < D / 64; ++at) {
+                        tma_prefetch_4d(&a.tmap_q, at * 64, x.i, x.h, b);
+                        tma_prefetch_4d(&a.tmap_do, at * 64, x.i, x.h, b);
+                    }
+                }
                 for (int j = 1; j < nk && ok; ++j) load_kv(it * nk + j, j);
             }
             if (!ok) {
@@ -220,13 +228,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dq_kernel(const __grid_c
         for (int g = 0, it = 0, j = 0; g < tiles; ++g) {
             const bool more = g + 1 < tiles, last = j + 1 == nk;  // a query tile's last key tile
             const int next_it = last ? it + 1 : it, next_j = last ? 0 : j + 1;
-            if (more) {
+            // With one slot the next query tile's rows are still on their way: this
+            // tile's product first.
+            const bool late = L::kQs == 1 && last;
+            if (more && !late) {
                 wait_qk(g + 1, next_it, next_j);
                 sync();
                 issue([&] { issue_s(g + 1, next_it); });
             }
             take(kDpBar);
-            if (more) {
+            if (more && !late) {
                 if (!ONE) {
                     wait_v(g + 1, next_j);
                     sync();
@@ -242,6 +253,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dq_kernel(const __grid_c
                 if (!ONE) mma_commit(&k_empty[g % L::kKs]);
                 if (last) mma_commit(acc_full);
             });
+            if (more && late) {
+                wait_qk(g + 1, next_it, next_j);
+                wait_v(g + 1, next_j);
+                sync();
+                issue([&] {
+                    issue_s(g + 1, next_it);
+                    issue_dp(g + 1, next_it, next_j);
+                });
+            }
             it = next_it;
             j = next_j;
         }
@@ -265,6 +285,24 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dq_kernel(const __grid_c
             for (int c = 0; c < kChunks; ++c) reg_fence(acc[c]);
         };
         auto store = [&](int it) {
+            const QueryBox box = query_box(a, kvh, u0 + it);
+            if (!L::kStaged) {  // a thread its half row
+                int h, i;
+                if (!query_row(a, box, r, h, i)) return;
+                uint16_t* dst = static_cast<uint16_t*>(a.dq) + b * a.dq_bs + h * a.dq_hs + i * a.dq_ns + half * (D / 2);
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t y[4];
+#pragma unroll
+                        for (int w = 0; w < 4; ++w)
+                            y[w] = pack16(__uint_as_float(acc[c][8 * e + 2 * w]) * a.scale,
+                                          __uint_as_float(acc[c][8 * e + 2 * w + 1]) * a.scale, BF16);
+                        *reinterpret_cast<uint4*>(dst + 32 * c + 8 * e) = make_uint4(y[0], y[1], y[2], y[3]);
+                    }
+                return;
+            }
             __syncwarp();
 #pragma unroll
             for (int c = 0; c < kChunks; ++c)
@@ -280,7 +318,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dq_kernel(const __grid_c
                 }
             __syncwarp();
             constexpr int kPieces = D / 16;  // of 16 bytes in half a row
-            const QueryBox box = query_box(a, kvh, u0 + it);
             uint16_t* base = static_cast<uint16_t*>(a.dq) + b * a.dq_bs + half * (D / 2) + 8 * (lane % kPieces);
 #pragma unroll
             for (int e = 0; e < kPieces; ++e) {
