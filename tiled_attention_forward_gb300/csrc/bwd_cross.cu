@@ -219,9 +219,11 @@ int chunks_of(const CrossBwdArgs& a, int sms) {
     const int64_t block = 8 * ((a.tiles + a.parts_k - 1) / a.parts_k) + 24;
     const int64_t early = blocks / sms * block, late = early + block;  // SMs free: at first and at last
     const int64_t n_late = blocks % sms, n_early = sms - n_late;
-    int64_t least = INT64_MAX, chunks = 1;
+    int64_t least = INT64_MAX, chunks = 1, last_c = 0;
     for (int64_t m = 1; m <= std::min(a.tiles, 128); ++m) {  // query tiles of a CTA
         const int64_t c = (a.tiles + m - 1) / m, ctas = c * a.BHkv, each = m * (6 * a.tiles_k + 3) + 24;
+        if (c == last_c) continue;  // (as many with a shorter run: seen)
+        last_c = c;
         // CTAs that have ended by `t`.
         auto ended = [&](int64_t t) {
             return n_early * ((t - early) / each) + (t > late ? n_late * ((t - late) / each) : 0);
