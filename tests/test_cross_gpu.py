@@ -239,6 +239,58 @@ def test_backward_of_many_query_tiles(D, case):
         R.check(x, r, b, name)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("case", [(8, 16, 16, 85, 1500, [1500, 0, 1, 128, 129, 777, 1499, 640]), (3, 16, 8, 1, 4000, [4000, 3, 2561]),
+                                  (9, 18, 9, 60, 1000, None), (1, 100, 10, 12, 2700, [2690])])
+def test_backward_of_many_key_blocks(D, case):
+    """Queries of one tile, whole or stacked heads: a CTA takes a run of key blocks, some behind an entry's keys."""
+    B, H, Hkv, Nq, Nk, lens = case
+    dt = torch.float16 if D == 64 else torch.bfloat16
+    q, k, v, do, t = make(B, H, Hkv, Nq, Nk, D, dt, Nq + D, lens)
+    lens = lens or [Nk] * B
+    o, lse = fattn.fwd_cross(q, k, v, t)
+    dq, dk, dv = (torch.full(x.shape, math.nan, dtype=dt, device="cuda") for x in (q, k, v))
+    got = fattn.bwd_cross(q, k, v, o, lse, do, t, dq=dq, dk=dk, dv=dv)
+    again = fattn.bwd_cross(q, k, v, o, lse, do, t)
+    ok()
+    assert all(torch.equal(x, y) for x, y in zip(got, again))
+    args, scale = [x.cpu() for x in (q, k, v, do)], fattn._default_scale(D)
+    ref = M.cross_grads(*args, lens, scale)
+    for name, x, r, b in zip(("dq", "dk", "dv"), got, ref, M.cross_grad_bounds(*args, lens, scale, dt, ref)):
+        R.check(x, r, b, name)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("case", [(8, 19, 19, 1000, 100), (8, 19, 19, 1000, 300), (8, 16, 16, 60, 1500)])
+@pytest.mark.parametrize("fill", [math.nan, 0.0])
+def test_captured_gradients(fill, D, case):
+    """Runs of query tiles and of key blocks, captured and replayed over new contents and lengths, gradients of odd
+    strides: the same bits (with `fill` = NaN most entries come to see keys that are NaN)."""
+    B, H, Hkv, Nq, Nk = case
+    q, k, v, do, t = make(B, H, Hkv, Nq, Nk, D, torch.bfloat16, Nq + Nk, [Nk - i for i in range(B)], fill)
+    o, lse = fattn.fwd_cross(q, k, v, t)
+    rows = torch.zeros(B, Nq, H + 1, D, dtype=torch.bfloat16, device="cuda")
+    cols = torch.zeros(2, B, Nk, Hkv + 2, D, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(fattn.bwd_cross_workspace_bytes(B, H, Nq, Nk, D, Hkv), dtype=torch.uint8, device="cuda")
+    out = dict(dq=rows[:, :, 1:].transpose(1, 2), dk=cols[0, :, :, 2:].transpose(1, 2), dv=cols[1, :, :, :Hkv].transpose(1, 2))
+    fattn.bwd_cross(q, k, v, o, lse, do, t, workspace=ws, **out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fattn.fwd_cross(q, k, v, t, out=o, lse=lse)
+        fattn.bwd_cross(q, k, v, o, lse, do, t, workspace=ws, **out)
+    for step in range(3):
+        do.copy_(torch.roll(do, 1, 2))
+        t.copy_(torch.roll(t, 1) if step else torch.tensor([0] + [Nk] * (B - 1), dtype=torch.int32))
+        graph.replay()
+        ws.fill_(255)
+        graph.replay()
+        want_o, want_lse = fattn.fwd_cross(q, k, v, t)
+        want = fattn.bwd_cross(q, k, v, want_o, want_lse, do, t)
+        ok()
+        assert all(torch.equal(x.view(torch.int16), out[name].view(torch.int16)) for x, name in zip(want, ("dq", "dk", "dv")))
+    assert (rows[:, :, 0] == 0).all() and (cols[0, :, :, :2] == 0).all() and (cols[1, :, :, Hkv:] == 0).all()
+
+
 @pytest.mark.parametrize("dtype,D", [("bf16", 128), ("fp16", 64)])
 def test_backward_layouts_and_repeats(dtype, D):
     """Gradients as slices of a projection's gradient, contiguous inputs, a second run: the same bits."""

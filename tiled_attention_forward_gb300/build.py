@@ -28,7 +28,7 @@ SOURCES = ["fattn_api.cu", "fwd_tc.cu", "fwd_ffma.cu", "fwd_unfused.cu", "bwd_tc
            "fwd_packed.cu", "cache_append.cu", "decode.cu", "fwd_rows.cu", "decode_shared.cu",
            "decode_cross.cu", "bwd_cross.cu", "rotate.cu"]
 HEADERS = ["internal.h", "sm103_ptx.cuh", "fwd_tc_kernel.cuh", "bwd_tc_kernel.cuh", "decode_kernel.cuh",
-           "tma_4d.cuh", "bwd_cross_dq.cuh"]
+           "tma_4d.cuh", "bwd_cross_dq.cuh", "bwd_cross_dkv.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",

@@ -12,10 +12,11 @@
 // bf16 (344 GFLOP, ragged) 474 us = 726 TFLOP/s: statistics 31, dK/dV 254, dQ 225, the
 // last two overlapping.  dK/dV keeps the tensor pipe 53 % busy (three and a half waves of
 // CTAs), dQ 44 %.
-// Dense-shaped, 64 heads of 4096: 1454 us = 945 TFLOP/s (fattn_bwd 910).  2 entries of
+// Dense-shaped, 64 heads of 4096: 1471 us = 934 TFLOP/s (fattn_bwd 910).  2 entries of
 // 8 heads on 2, 257 queries over up to 777 keys, D = 64: 19 us (one kernel after the
 // other, uncut: 37).  32 heads on 4, D = 64, 28 queries over up to 5342 keys, 12
 // entries: 113 us (a tile per head: 230).
+#include "bwd_cross_dkv.cuh"
 #include "bwd_cross_dq.cuh"
 #include "bwd_tc_kernel.cuh"
 
@@ -208,6 +209,23 @@ cudaError_t launch_add(const CrossBwdArgs& a, cudaStream_t s) {
                       kAddThreads, s, a, kv_rows);
 }
 
+// The CTAs that share a K/V head's key blocks, of one query tile, that end first: 12 a
+// CTA's start and end, 6 a block.
+int key_chunks_of(const CrossBwdArgs& a, int sms) {
+    int64_t least = INT64_MAX, chunks = a.tiles_k;
+    for (int64_t m = 1, last_c = 0; m <= std::min(a.tiles_k, 128); ++m) {
+        const int64_t c = (a.tiles_k + m - 1) / m;
+        if (c == last_c) continue;
+        last_c = c;
+        const int64_t each = 6 * m + 12, cost = (c * a.BHkv + sms - 1) / sms * each + each / 4;
+        if (cost < least) {
+            least = cost;
+            chunks = c;
+        }
+    }
+    return static_cast<int>(chunks);
+}
+
 // The CTAs that share a K/V head's query tiles: those with which the query kernel, which
 // starts as the key kernel's CTAs leave, ends first.  In units of 0.2 us: a key block's
 // CTA takes 8 a query tile and 24, a run of query tiles 6 a key tile, 3 a query tile and
@@ -265,11 +283,21 @@ cudaError_t launch_all(const CrossBwdArgs& a, int sms, cudaStream_t s) {
                        a.o_hs < a.o_ns);
         if (e != cudaSuccess) return e;
     }
+    static std::atomic<bool> run_done[kMaxDevices] = {};
     static std::atomic<bool> kv_done[kMaxDevices] = {};
     static std::atomic<bool> q_done[kMaxDevices] = {};
-    auto* kkv = attn_bwd_kernel<D, BF16, true, false, true>;
-    if ((e = opt_in_smem_once(kkv, BwdLayout<D, true>::kBytes, kv_done)) != cudaSuccess) return e;
-    if (a.tiles_k > 0) {
+    const int key_chunks = a.tiles == 1 ? key_chunks_of(a, sms) : a.tiles_k;
+    if (key_chunks < a.tiles_k) {  // one query tile: runs of key blocks
+        auto* run = cross_dkv_kernel<D, BF16>;
+        if ((e = opt_in_smem_once(run, CrossDkvLayout<D>::kBytes, run_done)) != cudaSuccess) return e;
+        CrossBwdArgs x = a;
+        x.chunks_k = key_chunks;
+        e = launch_overlapped(run, static_cast<unsigned>(static_cast<int64_t>(key_chunks) * a.BHkv), kBwdThreads,
+                              CrossDkvLayout<D>::kBytes, s, x);
+        if (e != cudaSuccess) return e;
+    } else if (a.tiles_k > 0) {
+        auto* kkv = attn_bwd_kernel<D, BF16, true, false, true>;
+        if ((e = opt_in_smem_once(kkv, BwdLayout<D, true>::kBytes, kv_done)) != cudaSuccess) return e;
         e = launch_overlapped(kkv, static_cast<unsigned>(a.tiles_k * a.BHkv * a.parts_k), kBwdThreads, BwdLayout<D, true>::kBytes, s, a);
         if (e != cudaSuccess) return e;
     }

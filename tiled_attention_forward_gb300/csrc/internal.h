@@ -229,6 +229,7 @@ struct CrossBwdArgs : BwdArgs {
     int tiles;                 // tiles of a K/V head: n_i * (H/Hkv) / box_h
     int Nk;
     int tiles_k;               // ceil(Nk / 128)
+    int chunks_k;              // CTAs that share a K/V head's key blocks, where tiles = 1
     int chunks_q;              // CTAs that share a K/V head's query tiles, where parts_q = 1
     int parts_k, parts_q;      // parts that the inner tiles of a key block / a query tile are cut into
     float* part_kv;            // fp32 [parts_k][B*Hkv][tiles_k * 128][dv, dk][D], where parts_k > 1
