@@ -6,7 +6,9 @@
 // forward, but of whole heads' boxes: a K/V head's dK and dV are sums over them, and
 // no box may bring another group's rows.  The key kernel (dK, dV) and the query
 // kernel (dQ) need nothing of one another, so the second starts as the first one's
-// last CTAs run.  Where there are few blocks their inner tiles are cut into parts.
+// last CTAs run.  Where there are few blocks their inner tiles are cut into parts; where
+// there are many of few inner tiles a CTA takes a run of them (bwd_cross_dq.cuh,
+// bwd_cross_dkv.cuh).
 //
 // Measured (GB300): 4 entries of 16 heads, 4096 queries over up to 2000 keys, D = 128,
 // bf16 (344 GFLOP, ragged) 474 us = 726 TFLOP/s: statistics 31, dK/dV 254, dQ 225, the
