@@ -616,9 +616,12 @@ FATTN_API int fattn_fwd_cross(const void* q, const void* k, const void* v, void*
  *   workspace : caller-owned, fattn_bwd_cross_workspace_bytes, 16-byte aligned;
  *               contents ignored on entry.
  * dq, dk and dv overlap nothing else (each may be another slice of a tensor that
- * others are slices of).  No atomics: the result is the same for every run.  Three
- * launches (row statistics, dK/dV, dQ), or four where there are few rows or keys (the
- * sum of parts).
+ * others are slices of).  The result is the same for every run, and a batch entry's
+ * does not depend on the others.  Three launches (row statistics, dK/dV, dQ), or four
+ * where there are few rows or keys (the sum of parts).  FATTN_F16: dS = P (dP - Delta)
+ * is held in fp16 as in fattn_bwd, and past 65504 it overflows.  Over more than 16384
+ * keys, where it could also be too small, a power of two from the largest rows of dout
+ * and v (two launches more) keeps it in range.
  */
 FATTN_API int64_t fattn_bwd_cross_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64_t Nq, int64_t Nk,
                                         int64_t D);

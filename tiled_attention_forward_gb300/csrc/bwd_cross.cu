@@ -27,9 +27,68 @@
 namespace fattn {
 namespace {
 
+// The largest |dO_i|^2 and |v_j|^2 of each K/V head of a batch entry, over its query rows
+// and seen keys (rows that are not finite, whose gradients are not either, do not count):
+// what grad_scale takes for fp16 over long keys.  `chunks` CTAs a K/V head; D/8 lanes a
+// row, kMostLoads such rows on their way; a.most is zero before.  Maxima: whatever the
+// order, the same.
+constexpr int kMostLoads = 4;
+template <int D>
+__global__ void __launch_bounds__(256) cross_most_kernel(const __grid_constant__ CrossBwdArgs a, int chunks) {
+    constexpr int kLanes = D / 8, kStep = 256 / kLanes;
+    const int kvh = blockIdx.x / chunks, chunk = blockIdx.x % chunks, b = kvh / a.Hkv, kv_h = kvh - b * a.Hkv;
+    const int share = a.H / a.Hkv, piece = threadIdx.x % kLanes;
+    int keys = a.Nk;
+    if (a.lens != nullptr) keys = min(max(a.lens[b], 0), a.Nk);
+    float most[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {  // rows of dO, values
+        const int rows = t == 0 ? share * a.N : keys, end = part_begin(rows, chunk + 1, chunks);
+        const uint16_t* base = t == 0 ? static_cast<const uint16_t*>(a.dout) + b * a.do_bs + kv_h * share * a.do_hs
+                                      : static_cast<const uint16_t*>(a.v) + b * a.v_bs + kv_h * a.v_hs;
+        float mx = 0.f;
+        // (Every lane of a warp takes as many turns.)
+        for (int at = part_begin(rows, chunk, chunks); at < end; at += kMostLoads * kStep) {
+            uint4 x[kMostLoads];
+#pragma unroll
+            for (int k = 0; k < kMostLoads; ++k) {
+                const int r = at + k * kStep + static_cast<int>(threadIdx.x) / kLanes;
+                x[k] = make_uint4(0u, 0u, 0u, 0u);
+                if (r >= end) continue;
+                const int hq = t == 0 ? r / a.N : 0;
+                const int64_t off = t == 0 ? hq * a.do_hs + (r - hq * a.N) * a.do_ns : r * a.v_ns;
+                x[k] = *reinterpret_cast<const uint4*>(base + off + 8 * piece);
+            }
+#pragma unroll
+            for (int k = 0; k < kMostLoads; ++k) {
+                const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+                float sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+                    sum = fmaf(u.x, u.x, sum);
+                    sum = fmaf(u.y, u.y, sum);
+                }
+#pragma unroll
+                for (int d = kLanes / 2; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                if (sum < INFINITY) mx = fmaxf(mx, sum);
+            }
+        }
+        most[t] = mx;
+    }
+    // (Numbers that are not negative compare as their bits.)
+    const uint32_t m0 = __reduce_max_sync(0xffffffffu, __float_as_uint(most[0]));
+    const uint32_t m1 = __reduce_max_sync(0xffffffffu, __float_as_uint(most[1]));
+    if (threadIdx.x % 32 == 0) {
+        atomicMax(reinterpret_cast<uint32_t*>(&a.most[kvh].x), m0);
+        atomicMax(reinterpret_cast<uint32_t*>(&a.most[kvh].y), m1);
+    }
+}
+
 // -LSE_i * log2(e) and -Delta_i, Delta_i = dO_i . O_i, into the workspace in the order
 // of the tiles' rows, [B*Hkv][tiles][2][128]; rows past Nq or behind a tile's box, and
-// rows that saw no key (LSE = -inf), get -inf and 0.  A row is read as 16-byte pieces by D/8 lanes, kStatLoads such rows of O
+// rows that saw no key (LSE = -inf), get -inf and 0.  fp16: of 2^kHeldP P, and f Delta
+// (grad_scale).  A row is read as 16-byte pieces by D/8 lanes, kStatLoads such rows of O
 // and of dO in flight a lane; rows are taken in the order in which they lie in
 // memory (`heads_inner`: a token's heads one after the other).
 constexpr int kStatLoads = 4;
@@ -73,7 +132,7 @@ __global__ void __launch_bounds__(256) cross_stats_kernel(const __grid_constant_
     const int64_t warps = (rows + kStatRows<D> - 1) / kStatRows<D>, stride = static_cast<int64_t>(gridDim.x) * 8;
     for (int64_t warp = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / 32; warp < warps; warp += stride) {
         uint4 o[kStatLoads], g[kStatLoads];
-        float lse[kStatLoads];
+        float lse[kStatLoads], f[kStatLoads];
         int64_t dst[kStatLoads];  // of the row's first statistic; < 0: no row
         At x = first_of(warp);
 #pragma unroll
@@ -83,6 +142,7 @@ __global__ void __launch_bounds__(256) cross_stats_kernel(const __grid_constant_
             const int64_t bh = static_cast<int64_t>(x.b) * a.H + h;
             o[k] = g[k] = make_uint4(0u, 0u, 0u, 0u);
             lse[k] = -INFINITY;
+            f[k] = 1.f;
             dst[k] = -1;
             if (x.b < entries) {
                 if (a.box_h == 1 && a.box_i == kBT) {
@@ -105,6 +165,7 @@ __global__ void __launch_bounds__(256) cross_stats_kernel(const __grid_constant_
                 g[k] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.dout) + x.b * a.do_bs +
                                                        h * a.do_hs + i * a.do_ns + 8 * piece);
                 if (piece == 0) lse[k] = a.lse[bh * a.N + i];
+                if (!BF16) f[k] = grad_scale<BF16>(a, static_cast<int>(x.b * a.Hkv + h / share)).f;
             }
         }
 #pragma unroll
@@ -128,8 +189,8 @@ __global__ void __launch_bounds__(256) cross_stats_kernel(const __grid_constant_
             for (int d = kLanes / 2; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
             if (piece == 0 && dst[k] >= 0) {
                 const bool none = lse[k] == -INFINITY;
-                a.ws[dst[k]] = none ? -INFINITY : -lse[k] * 1.4426950408889634f;
-                a.ws[dst[k] + kBT] = none ? 0.f : -sum;
+                a.ws[dst[k]] = none ? -INFINITY : fmaf(-lse[k], 1.4426950408889634f, BF16 ? 0.f : kHeldP);
+                a.ws[dst[k] + kBT] = none ? 0.f : -sum * f[k];
             }
         }
     }
@@ -280,6 +341,13 @@ cudaError_t launch_all(const CrossBwdArgs& a, int sms, cudaStream_t s) {
     const int64_t warps = (static_cast<int64_t>(a.BH) * a.n_i * a.box_i + kStatRows<D> - 1) / kStatRows<D>;
     cudaError_t e = cudaSuccess;
     if (a.N > 0 && a.Nk > 0) {
+        if (!BF16 && a.most != nullptr) {
+            // (Neither lets the next one start early.)
+            if ((e = cudaMemsetAsync(a.most, 0, static_cast<size_t>(a.BHkv) * sizeof(float2), s)) != cudaSuccess) return e;
+            const int chunks = std::min(std::max(4 * sms / a.BHkv, 1), 64);
+            cross_most_kernel<D><<<static_cast<unsigned>(chunks) * static_cast<unsigned>(a.BHkv), 256, 0, s>>>(a, chunks);
+            if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        }
         const int64_t blocks = (warps + 7) / 8;
         e = launch_two(cross_stats_kernel<D, BF16>, static_cast<unsigned>(std::min<int64_t>(blocks, 16 * sms)), 256, s, a,
                        a.o_hs < a.o_ns);

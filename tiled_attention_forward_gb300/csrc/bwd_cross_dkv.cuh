@@ -212,13 +212,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dkv_kernel(const __grid_
         uint8_t* stage = smem + L::kRows + warp * 4096;
         const float* nlse2s = reinterpret_cast<const float*>(smem + L::kStats);
         const float* ndeltas = nlse2s + kBT;
+        const GradScale held = grad_scale<BF16>(a, kvh);
         // Block g's gradients, through the warp's own memory, whole halves of rows at a
         // time; rows of keys that no query sees are zeros.
         auto store = [&](int g) {
             const int row0 = (j0 + g) * kBT + quarter * 32;
 #pragma unroll 1
             for (int acc = 0; acc < 2; ++acc) {
-                const float mul = acc == 0 ? 1.f : a.scale;
+                const float mul = acc == 0 ? kDvMul<BF16> : held.mul;
                 __syncwarp();
 #pragma unroll 1
                 for (int c = 0; c < D / 64; ++c) {
@@ -292,8 +293,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dkv_kernel(const __grid_
                         fma2(x0, x1, __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]), a.sl2, a.sl2, h2 ? nl.z : nl.x,
                              h2 ? nl.w : nl.y);
                         const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-                        add2(d0, d1, __uint_as_float(dpv[e]), __uint_as_float(dpv[e + 1]), h2 ? nd.z : nd.x,
-                             h2 ? nd.w : nd.y);
+                        minus_delta<!BF16>(d0, d1, dpv[e], dpv[e + 1], held.f, h2 ? nd.z : nd.x, h2 ? nd.w : nd.y);
                         mul2(d0, d1, p0, p1, d0, d1);
                         pk[e / 2] = pack16(p0, p1, BF16);
                         dsk[e / 2] = pack16(d0, d1, BF16);

@@ -275,6 +275,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dq_kernel(const __grid_c
         const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
         uint8_t* stage = smem + L::kRows + warp * 4096;
         const float* stats = a.ws + (static_cast<int64_t>(kvh) * a.tiles + u0) * (2 * kBT) + r;
+        const GradScale held = grad_scale<BF16>(a, kvh);
         constexpr int kChunks = D / 64;  // of 32 columns in half a row
         uint32_t acc[kChunks][32];
         auto load_acc = [&]() {
@@ -297,8 +298,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dq_kernel(const __grid_c
                         uint32_t y[4];
 #pragma unroll
                         for (int w = 0; w < 4; ++w)
-                            y[w] = pack16(__uint_as_float(acc[c][8 * e + 2 * w]) * a.scale,
-                                          __uint_as_float(acc[c][8 * e + 2 * w + 1]) * a.scale, BF16);
+                            y[w] = pack16(__uint_as_float(acc[c][8 * e + 2 * w]) * held.mul,
+                                          __uint_as_float(acc[c][8 * e + 2 * w + 1]) * held.mul, BF16);
                         *reinterpret_cast<uint4*>(dst + 32 * c + 8 * e) = make_uint4(y[0], y[1], y[2], y[3]);
                     }
                 return;
@@ -311,8 +312,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dq_kernel(const __grid_c
                     uint32_t y[4];
 #pragma unroll
                     for (int w = 0; w < 4; ++w)
-                        y[w] = pack16(__uint_as_float(acc[c][8 * e + 2 * w]) * a.scale,
-                                      __uint_as_float(acc[c][8 * e + 2 * w + 1]) * a.scale, BF16);
+                        y[w] = pack16(__uint_as_float(acc[c][8 * e + 2 * w]) * held.mul,
+                                      __uint_as_float(acc[c][8 * e + 2 * w + 1]) * held.mul, BF16);
                     *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * c + e) ^ (lane & 7)) << 4)) =
                         make_uint4(y[0], y[1], y[2], y[3]);
                 }
@@ -373,7 +374,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dq_kernel(const __grid_c
                         if (e >= vis) p0 = 0.f;
                         if (e + 1 >= vis) p1 = 0.f;
                     }
-                    add2(d0, d1, __uint_as_float(dpv[c][e]), __uint_as_float(dpv[c][e + 1]), ndelta, ndelta);
+                    minus_delta<!BF16>(d0, d1, dpv[c][e], dpv[c][e + 1], held.f, ndelta, ndelta);
                     mul2(d0, d1, p0, p1, d0, d1);
                     dsk[e / 2] = pack16(d0, d1, BF16);
                 }

@@ -296,6 +296,46 @@ __device__ __forceinline__ bool query_row(const CrossBwdArgs& a, const QueryBox&
     return r < a.box_h * a.box_i && i < a.N;
 }
 
+// Cross, fp16: how large weights and dS are held.  The weights are at most 1, and about
+// 1 / Nk over many even keys: held as they are, they would be subnormal numbers past
+// 2^14 keys and lose bits (uniform, 100000 keys: dV off by 0.3 %; a million: 3 %).  So
+// the statistics are those of 2^kHeldP P, dV is taken down again in the epilogue, and
+//     dS = (2^kHeldP P) (f dP - f Delta),  f = 2^(E - kHeldP),
+// is held 2^E times its size, `mul` taking dK and dQ down.  E = 0, as fattn_bwd holds
+// it, up to kLongKeys keys.  Past that the weights may be that small, and E is the
+// largest with which nothing can overflow: |dP - Delta| <= B = 2 max|dO_i| max|v_j|
+// (Delta is a mean of dP), over the rows and seen keys of this K/V head of this batch
+// entry alone, so that no entry's gradients depend on another's; 2^14 < 2^E B <= 2^15.
+// bf16 has fp32's range: everything as it is.
+constexpr int kHeldP = 14;
+struct GradScale {
+    float f;    // of dP and Delta
+    float mul;  // of dK and dQ
+};
+template <bool BF16>
+__device__ __forceinline__ GradScale grad_scale(const CrossBwdArgs& a, int kvh) {
+    if (BF16) return {1.f, a.scale};
+    int e = 0;
+    if (a.most != nullptr) {
+        const float2 m = __ldcg(a.most + kvh);
+        const float b2 = 4.f * m.x * m.y;  // (up to 2^81)
+        if (b2 > 0.f) e = 15 - ((static_cast<int>(__float_as_uint(b2) >> 23) - 126 + 1) >> 1);  // B^2 < 2^(..)
+    }
+    return {__uint_as_float(static_cast<uint32_t>(127 + e - kHeldP) << 23),
+            a.scale * __uint_as_float(static_cast<uint32_t>(127 - e) << 23)};
+}
+template <bool BF16>
+constexpr float kDvMul = BF16 ? 1.f : 1.f / (1 << kHeldP);
+
+// dP - Delta, or that times f.
+template <bool SCALED>
+__device__ __forceinline__ void minus_delta(float& d0, float& d1, uint32_t dp0, uint32_t dp1, float f, float nd0, float nd1) {
+    if constexpr (SCALED)
+        fma2(d0, d1, __uint_as_float(dp0), __uint_as_float(dp1), f, f, nd0, nd1);
+    else
+        add2(d0, d1, __uint_as_float(dp0), __uint_as_float(dp1), nd0, nd1);
+}
+
 // Cross: the gradient rows of a CTA without inner tiles.
 template <int D, bool KV>
 __device__ __forceinline__ void bwd_store_zeros(const CrossBwdArgs& a, const BwdTask& tk) {
@@ -695,6 +735,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_kernel(const __grid_c
         const int row = blk0 + r;  // KV: key index; dQ: query index
         const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
         const int c0 = half * 64;  // first column of this warp
+        constexpr bool kScaled = CROSS && !BF16;
+        GradScale held = {1.f, a.scale};
+        if constexpr (CROSS) held = grad_scale<BF16>(a, tk.bh);
         float nlse2_r = 0.f, ndelta_r = 0.f;  // -LSE*log2(e) and -Delta of this row
         if (!KV) {
             const float* stats = a.ws + static_cast<int64_t>(tk.bh) * 2 * a.Npad + row;
@@ -767,7 +810,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_kernel(const __grid_c
                                 if (cq + e < r) p0 = 0.f;
                                 if (cq + e + 1 < r) p1 = 0.f;
                             }
-                            add2(d0, d1, __uint_as_float(dpv[e]), __uint_as_float(dpv[e + 1]), nd0, nd1);
+                            minus_delta<kScaled>(d0, d1, dpv[e], dpv[e + 1], held.f, nd0, nd1);
                             mul2(d0, d1, p0, p1, d0, d1);
                             pk[e / 2] = pack16(p0, p1, BF16);
                             dsk[e / 2] = pack16(d0, d1, BF16);
@@ -837,8 +880,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_kernel(const __grid_c
                         if (e >= vis) p0 = 0.f;
                         if (e + 1 >= vis) p1 = 0.f;
                     }
-                    add2(d0, d1, __uint_as_float(dpv[c][e]), __uint_as_float(dpv[c][e + 1]), ndelta_r,
-                         ndelta_r);
+                    minus_delta<kScaled>(d0, d1, dpv[c][e], dpv[c][e + 1], held.f, ndelta_r, ndelta_r);
                     mul2(d0, d1, p0, p1, d0, d1);
                     dsk[e / 2] = pack16(d0, d1, BF16);
                 }
@@ -880,7 +922,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_kernel(const __grid_c
             const int row0 = blk0 + quarter * 32;
 #pragma unroll 1
             for (int acc = 0; acc < accs; ++acc) {
-                const float mul = (KV && acc == 0) ? 1.f : a.scale;
+                const float mul = (KV && acc == 0) ? kDvMul<BF16> : held.mul;
                 float* part = (KV ? a.part_kv : a.part_q) +
                               ((((static_cast<int64_t>(tk.part) * a.BHkv + tk.bh) * (KV ? a.tiles_k : a.tiles)) *
                                     kBT + row0) * accs + acc) * D;

@@ -1628,7 +1628,7 @@ int64_t fattn_bwd_cross_workspace_bytes(int64_t B, int64_t H, int64_t Hkv, int64
     if (B <= 0 || H <= 0 || Nq <= 0 || Nk < 0 || validate_cross(B, H, Hkv, Nq, Nk, D, 1.f, FATTN_BF16) != FATTN_OK)
         return 0;
     const CrossParts p = cross_parts(B, H, Hkv, Nq, Nk);
-    return B * Hkv * p.tiles * 1024 + p.kv_rows * 2 * D * 4 + p.q_rows * D * 4;
+    return B * Hkv * p.tiles * 1024 + p.kv_rows * 2 * D * 4 + p.q_rows * D * 4 + (Nk > kLongKeys ? B * Hkv * 8 : 0);
 }
 
 int fattn_bwd_cross(const void* q, const void* k, const void* v, const void* o, const void* dout, const float* lse,
@@ -1710,6 +1710,9 @@ int fattn_bwd_cross(const void* q, const void* k, const void* v, const void* o, 
     a.parts_q = static_cast<int>(parts.q);
     a.part_kv = a.ws + B * Hkv * parts.tiles * 256;
     a.part_q = a.part_kv + parts.kv_rows * 2 * D;
+    a.most = !bf16 && Nk > kLongKeys ? reinterpret_cast<float2*>(a.part_q + parts.q_rows * D) : nullptr;
+    a.v = v;
+    a.v_bs = strides[6], a.v_hs = strides[7], a.v_ns = strides[8];
     a.lens = kv_lens;
     a.o = o;
     a.dout = dout;

@@ -221,6 +221,9 @@ cudaError_t bwd_launch(const BwdArgs& a, const void* o, const void* dout, const 
                        bool bf16, bool causal, cudaStream_t s);
 cudaError_t bwd_read_and_clear_error_word(uint32_t* out);
 
+// Keys past which an fp16 dS is held by a power of two of the data (grad_scale,
+// bwd_tc_kernel.cuh): up to there weights of 1 / Nk are normal numbers of the type.
+constexpr int64_t kLongKeys = 1 << 14;
 struct CrossBwdArgs : BwdArgs {
     // tmaps {D, Nq or Nk, heads, B}, boxes {64, box_i, box_h, 1} of q and dO, {64, 128,
     // 1, 1} of k and v; N = Nq; Npad and num_tiles are unused; ws [B*Hkv][tiles][2][128]
@@ -236,6 +239,9 @@ struct CrossBwdArgs : BwdArgs {
     float* part_q;             // fp32 [parts_q][B*Hkv][tiles * 128][D], where parts_q > 1
     const int32_t* lens;       // visible keys of each batch entry, or nullptr: Nk
     int64_t dq_bs, dq_hs, dq_ns, dk_bs, dk_hs, dk_ns, dv_bs, dv_hs, dv_ns;  // element strides
+    float2* most;              // fp16 and long keys: [B*Hkv] largest |dO_i|^2 and |v_j|^2 (seen keys); or nullptr
+    const void* v;             // .. whose values are read for that
+    int64_t v_bs, v_hs, v_ns;
     const void* o;             // the row statistics' inputs, by strides
     const void* dout;
     const float* lse;
