@@ -164,3 +164,57 @@ def test_captured_over_other_contents():
         want = fattn.bwd_cross(q, k, v, o, lse, do, t)
         ok()
         assert all(torch.equal(x, y) for x, y in zip(out, want))
+
+
+def weight_error(s, D, n):
+    """P's one rounding, exponentials, scores (as in serving_ref), and the sum of n values
+    near 1: n / 16 products add to an fp32 accumulator, each with an error of up to 2^-23 of
+    what it holds then (the tensor cores cut), which grows evenly from 0 to the sum."""
+    return U + 2.0 ** -20 + 2 * (D + 1) * 2.0 ** -23 * s + n / 16 * 2.0 ** -23 / 2
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_forward_of_many_keys_beside_one(D):
+    """One key outweighs each of 120000 others 2^14 to 2^18 times, which together weigh about as
+    much: the weights of the others keep their bits (rows enough that keys are not cut)."""
+    H, Nq, Nk = 2, 20000, 120001
+    g = torch.Generator(device="cuda").manual_seed(7)
+    k = torch.zeros(1, H, Nk, D, dtype=torch.float16, device="cuda")
+    v = (1.0 + 0.1 * torch.randn(1, H, Nk, D, generator=g, device="cuda")).half()
+    q = torch.zeros(1, H, Nq, D, dtype=torch.float16, device="cuda")
+    k[:, :, 5, 0] = 1.0
+    v[:, :, 5] = 0.0
+    q[..., 0] = (9.7 + 2.8 * torch.rand(1, H, Nq, generator=g, device="cuda")).half()
+    o, lse = fattn.fwd_cross(q, k, v, scale=1.0)
+    ok()
+    rows = torch.arange(0, Nq, 7, device="cuda")
+    s = q[0, :, rows, 0].double()
+    total = s.exp() + (Nk - 1)
+    ref = v[0].double().sum(1)[:, None] / total[..., None]
+    core = weight_error(s, D, Nk)[..., None] * ref.abs()
+    check(o[0, :, rows], ref, core + U * (ref.abs() + core), "O")
+    # (scores as in serving_ref; Nk / 128 tiles' sums are added one by one, each off by up to 2^-24 of a sum that grows evenly)
+    bound = (D + 1) * 2.0 ** -23 * s + 2.0 ** -20 * (1 + total.log()) + Nk / 128 * 2.0 ** -24 / 2
+    assert ((lse[0, :, rows].double() - total.log()).abs() <= bound).all()
+
+
+def test_decode_behind_a_long_prefix_keeps_small_weights():
+    """The same for a chunk of tokens behind a shared prefix, whose own keys weigh nothing."""
+    H, Nq, D, page, P = 64, 650, 64, 64, 120000
+    g = torch.Generator(device="cuda").manual_seed(8)
+    pages = P // page
+    kp = torch.zeros(pages + 11, 1, page, D, dtype=torch.float16, device="cuda")
+    vp = (1.0 + 0.1 * torch.randn(pages + 11, 1, page, D, generator=g, device="cuda")).half()
+    kp[0, 0, 5, 0], vp[0, 0, 5] = 1.0, 0.0
+    kp[pages:, ..., 0] = -30.0
+    q = torch.zeros(1, H, Nq, D, dtype=torch.float16, device="cuda")
+    q[..., 0] = (9.7 + 2.8 * torch.rand(1, H, Nq, generator=g, device="cuda")).half()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    o, lse = fattn.decode_shared(q, kp, vp, torch.arange(pages, **i32), torch.tensor([P], **i32),
+                                 torch.arange(pages, pages + 11, **i32)[None], torch.tensor([Nq], **i32), scale=1.0)
+    ok()
+    s = q[0, :, :, 0].double()
+    total = s.exp() + (P - 1)  # (an own key weighs e^-291 at most)
+    ref = vp[:pages, 0].double().sum((0, 1)) / total[..., None]
+    core = weight_error(s, D, P)[..., None] * ref.abs()
+    check(o[0], ref, core + U * (ref.abs() + core), "O")

@@ -1257,6 +1257,12 @@ __device__ void softmax_role(const ArgsOf<KIND>& a, const Bars& bars, uint8_t* q
         // unrounded values) serves both and the sum of the rounded ones is
         // not formed.
         constexpr bool kRoundedSum = BF16;
+        // Rows, fp16: weights are held 2^7 times their size (at most 2^15, with the stale
+        // max), as in decode_kernel.cuh.  Many keys may each be 2^-18 of a row's largest
+        // and together as much: as subnormal numbers of the type they would lose bits
+        // (120000 of them beside one key: O off by up to 0.76 %, so 0.13 %).  The sums are of the same
+        // weights, and the max that goes with them is 7 less.
+        constexpr float kHeld = KIND == kRows && !BF16 ? 7.f : 0.f;
         float l_run = 0.f;
         float l_exact = 0.f;
 
@@ -1359,7 +1365,7 @@ __device__ void softmax_role(const ArgsOf<KIND>& a, const Bars& bars, uint8_t* q
                     }
                 }
             }
-            const float neg_m = (m_run == -INFINITY) ? 0.f : -m_run;
+            const float neg_m = (m_run == -INFINITY) ? 0.f : kHeld - m_run;
 
             // P = exp2(s*scale*log2e - m) rounded to the operand type, written
             // over the first half of S.  l_run sums exactly the rounded values
@@ -1405,6 +1411,7 @@ __device__ void softmax_role(const ArgsOf<KIND>& a, const Bars& bars, uint8_t* q
         }
 
         // Epilogue: O = O~ / l, LSE = (m + log2 l) ln 2, rows < N only.
+        m_run -= kHeld;
         const bool ok = warp_wait(&bars.o_full[tile], ocnt & 1u, abort_flag, a.timeout_ns);
         ++ocnt;
         if (!ok) {
