@@ -71,7 +71,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dq_kernel(const __grid_c
     const int b = kvh / a.Hkv, kv_h = kvh - b * a.Hkv;
     const int u0 = part_begin(a.tiles, chunk, a.chunks_q), n = part_begin(a.tiles, chunk + 1, a.chunks_q) - u0;
     int keys = a.Nk;
-    if (a.lens != nullptr) keys = min(max(a.lens[b], 0), a.Nk);  // (the key kernel reports one out of range)
+    // (Read through L2, like the statistics: launch_overlapped.  The key kernel reports one out of range.)
+    if (a.lens != nullptr) keys = min(max(__ldcg(a.lens + b), 0), a.Nk);
     // Key tiles of a query tile, and of the CTA: tile g is key tile g % nk of query
     // tile u0 + g / nk.
     const int nk = ONE ? 1 : (keys + kBT - 1) / kBT, tiles = n * nk;
@@ -331,12 +332,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dq_kernel(const __grid_c
         };
         bool ok = true;
         int failed_at = 0;  // first tile not handed over when a wait gave up
-        float nlse2 = stats[0], ndelta = stats[kBT];  // -LSE*log2(e) (past Nq: -inf) and -Delta of this row
+        float nlse2 = __ldcg(stats), ndelta = __ldcg(stats + kBT);  // -LSE*log2(e) (past Nq: -inf) and -Delta of this row
         float nlse2_next = 0.f, ndelta_next = 0.f;
         for (int g = 0, it = 0, j = 0; g < tiles && ok; ++g) {
             if (j == 0 && it + 1 < n) {
-                nlse2_next = stats[(it + 1) * (2 * kBT)];
-                ndelta_next = stats[(it + 1) * (2 * kBT) + kBT];
+                nlse2_next = __ldcg(stats + (it + 1) * (2 * kBT));
+                ndelta_next = __ldcg(stats + (it + 1) * (2 * kBT) + kBT);
             }
             ok = warp_wait(&s_full[g & 1], (g >> 1) & 1u, abort_flag, a.timeout_ns);
             if (!ok) {

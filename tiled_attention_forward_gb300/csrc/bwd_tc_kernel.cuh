@@ -256,7 +256,7 @@ template <bool KV>
 __device__ __forceinline__ int bwd_visible_keys(const CrossBwdArgs& a) {
     if (a.lens == nullptr) return a.Nk;
     const int b = KV ? blockIdx.x / a.parts_k / a.tiles_k / a.Hkv : blockIdx.x / a.parts_q / a.tiles / a.Hkv;
-    const int len = a.lens[b];
+    const int len = KV ? a.lens[b] : __ldcg(a.lens + b);  // (the query kernel has not waited: launch_overlapped)
     if (len < 0 || len > a.Nk) {
         if (threadIdx.x == 0) atomicOr(&g_error_word, 1u << kDevErrInvalidArg);
         return len < 0 ? 0 : a.Nk;
@@ -746,8 +746,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_kernel(const __grid_c
                 stats = a.ws + (static_cast<int64_t>(tk.bh) * a.tiles + tk.blk) * (2 * kBT) + r;
                 apart = kBT;
             }
-            nlse2_r = stats[0];        // -inf past N: the row's P is 0
-            ndelta_r = stats[apart];
+            // -inf past N: the row's P is 0.  (Cross: the query kernel has not waited.)
+            nlse2_r = CROSS ? __ldcg(stats) : stats[0];
+            ndelta_r = CROSS ? __ldcg(stats + apart) : stats[apart];
         }
         bool ok = true;
         int failed_at = 0;  // first tile not handed over when a wait gave up

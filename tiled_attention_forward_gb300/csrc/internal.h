@@ -32,6 +32,15 @@ inline cudaError_t opt_in_smem_once(K* fn, int bytes, std::atomic<bool> (&done)[
 // Launches a kernel whose start may overlap the end of the kernel before it on
 // the stream (programmatic stream serialization): it calls grid_dependency()
 // before it touches memory, which waits for that kernel to complete.
+//
+// Three kernels wait only at their end: the prefix's rows (fwd_rows.cu, own_part) and
+// the dQ kernels of cross attention (attn_bwd_kernel and cross_dq_kernel), which run
+// beside the kernel before them, K.  They read nothing that K writes and write nothing
+// that K touches.  What they read, kernels before K wrote: every CTA of K passes its
+// grid_dependency(), behind the end of those, before the first CTA here starts, so
+// their writes have reached L2 by then.  But no wait of this grid's own has dropped
+// what an SM's L1 may hold: all such reads, plain loads of tables, lengths and
+// statistics, go to L2 (__ldcg), as TMA copies do.
 template <typename A>
 inline cudaError_t launch_overlapped(void (*fn)(A), unsigned grid, unsigned threads, size_t smem, cudaStream_t s,
                                      const A& a) {
