@@ -339,7 +339,8 @@ __device__ __forceinline__ void minus_delta(float& d0, float& d1, uint32_t dp0, 
 // Cross: the gradient rows of a CTA without inner tiles.
 template <int D, bool KV>
 __device__ __forceinline__ void bwd_store_zeros(const CrossBwdArgs& a, const BwdTask& tk) {
-    const QueryBox box = query_box(a, tk.bh, KV ? 0 : tk.blk);
+    // (Key blocks are written without queries too, where there are no boxes of them.)
+    const QueryBox box = KV ? QueryBox{0, 0, tk.bh / a.Hkv} : query_box(a, tk.bh, tk.blk);
     const int kv_h = tk.bh - box.b * a.Hkv;
     for (int x = threadIdx.x; x < kBT * (D / 8); x += kBwdThreads) {
         const int r = x / (D / 8), c = 8 * (x % (D / 8));
@@ -458,7 +459,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_kernel(const __grid_c
                 kv_b = kvh / a.Hkv;
                 kv_h = kvh - kv_b * a.Hkv;
                 q_bytes = 2 * (D / 64) * a.box_h * a.box_i * 128;
-                outer_q = query_box(a, kvh, tk.blk);
+                if (!KV) outer_q = query_box(a, kvh, tk.blk);
             }
             auto load = [&](void* dst, const CUtensorMap* map, uint64_t* bar, int x, int row, int head) {
                 if constexpr (CROSS)
@@ -965,7 +966,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_kernel(const __grid_c
                 if (cut) continue;
                 __syncwarp();
                 constexpr int kPieces = D / 16;  // of 16 bytes in a half row
-                const QueryBox box = query_box(a, tk.bh, KV ? 0 : tk.blk);
+                const QueryBox box = KV ? QueryBox{0, 0, tk.bh / a.Hkv} : query_box(a, tk.bh, tk.blk);
                 const int64_t hs = KV ? (acc == 0 ? a.dv_hs : a.dk_hs) : a.dq_hs;
                 const int64_t ns = KV ? (acc == 0 ? a.dv_ns : a.dk_ns) : a.dq_ns;
                 uint16_t* base = static_cast<uint16_t*>(KV ? (acc == 0 ? a.dv : a.dk) : a.dq) +
