@@ -562,6 +562,7 @@ FATTN_API int fattn_cache_append_kv4_axes(const void* q, const void* k, const vo
  *              it gives the gradients of the rows before they turned.
  *   cos, sin, max_pos, rot, interleaved : as fattn_cache_append; rows' elements
  *              past rot are copied.  One launch; fp32 products, one rounding.
+ *              With B, H or N = 0 nothing is written.
  */
 FATTN_API int fattn_rotate(const void* q, const void* k, void* q_out, void* k_out, const int64_t* strides,
                  const int32_t* pos, const uint8_t* axis_of_pair, int64_t axes, const float* cos,
@@ -608,7 +609,8 @@ FATTN_API int fattn_fwd_cross(const void* q, const void* k, const void* v, void*
  * fattn_bwd_cross -- its gradients: dq [B, H, Nq, D] and dk, dv [B, Hkv, Nk, D] of
  * L = sum(dout * O), from the forward's o and lse, by the formulas of
  * fattn_bwd_gqa.  dk and dv are sums over the query heads that share a K/V head;
- * rows of keys behind kv_lens[b] are zeros, and so is dq where there are no keys.
+ * rows of keys behind kv_lens[b] are zeros, and so is dq where there are no keys, and
+ * dk and dv where Nq = 0.  With B or H = 0 nothing is written.
  *
  *   strides   : host array of 24: batch, head and token stride of q, k, v, o,
  *               dout, dq, dk, dv.

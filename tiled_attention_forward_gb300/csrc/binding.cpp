@@ -464,6 +464,14 @@ PyObject* py_rotate(PyObject*, PyObject* const* args, Py_ssize_t n) {
         }
         const float* cos = static_cast<float*>(p.dense("cos", cos_t, at::kFloat, {max_pos, rot / 2}));
         const float* sin = static_cast<float*>(p.dense("sin", sin_t, at::kFloat, {max_pos, rot / 2}));
+        // Queries of no heads: the keys alone (the C call has nothing to do where H = 0).
+        if (H == 0 && Hkv > 0) {
+            for (int i = 0; i < 3; ++i) st[i] = st[3 + i], st[6 + i] = st[9 + i];
+            return run(p, stream, [&](fattn_stream_t s) {
+                return fattn_rotate(ptr(k), nullptr, ptr(k_out), nullptr, st, pos, of_pair, axes, cos, sin, max_pos, rot,
+                                    interleaved, inverse, B, Hkv, 0, N, D, p.dtype, s);
+            });
+        }
         return run(p, stream, [&](fattn_stream_t s) {
             return fattn_rotate(q.data_ptr(), ptr(k), q_out.data_ptr(), ptr(k_out), st, pos, of_pair, axes, cos, sin, max_pos,
                                 rot, interleaved, inverse, B, H, Hkv, N, D, p.dtype, s);
@@ -534,6 +542,8 @@ PyObject* py_bwd_cross(PyObject*, PyObject* const* args, Py_ssize_t n) {
         x.take_lens(p, lens);
         const float* l = static_cast<float*>(p.dense("lse", lse, at::kFloat, {x.B, x.H, x.Nq}));
         void* w = p.workspace(ws, &ws_bytes);
+        // Queries of no heads: as none at all, dk and dv are zeros (the C call has nothing to do where H = 0).
+        if (x.H == 0) x.H = x.Hkv, x.Nq = 0;
         return run(p, stream, [&](fattn_stream_t s) {
             return fattn_bwd_cross(t[0]->data_ptr(), t[1]->data_ptr(), t[2]->data_ptr(), t[3]->data_ptr(), t[4]->data_ptr(), l,
                                    t[5]->data_ptr(), t[6]->data_ptr(), t[7]->data_ptr(), st, x.lens, w, ws_bytes, x.B, x.H,
