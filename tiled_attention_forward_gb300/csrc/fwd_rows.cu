@@ -77,7 +77,8 @@ __global__ void __launch_bounds__(kJoinThreads) rows_join_kernel(const __grid_co
     };
 #pragma unroll
     for (int y = 0; y < kAtOnce; ++y) load(early[y], min(y, most - 1));
-    const int all = max((tiles + per - 1) / per, 1) + a.own_part;
+    // (No more than the workspace has room for, whatever a forward that gave up left as `per`.)
+    const int all = min(max((tiles + per - 1) / max(per, 1), 1), a.max_parts) + a.own_part;
     float m = -INFINITY;
 #pragma unroll
     for (int x = 0; x < 5; ++x) {
