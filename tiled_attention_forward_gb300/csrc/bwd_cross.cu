@@ -17,7 +17,11 @@
 // Dense-shaped, 64 heads of 4096: 1471 us = 934 TFLOP/s (fattn_bwd 910).  2 entries of
 // 8 heads on 2, 257 queries over up to 777 keys, D = 64: 19 us (one kernel after the
 // other, uncut: 37).  32 heads on 4, D = 64, 28 queries over up to 5342 keys, 12
-// entries: 113 us (a tile per head: 230).
+// entries: 113 us (a tile per head: 230).  fp16 over more than kLongKeys keys (what
+// cross_most_kernel costs, two launches and a third read of the values): one query of 8
+// heads over a million keys, D = 64, 1403 -> 1564 us; 300 over 100000, D = 128, 605 -> 649;
+// 4 entries of 16 heads, 4096 over 17000 6040 -> 6120; 20 of 8 heads on 2 over 20000, D =
+// 64, 39 -> 49.
 #include "bwd_cross_dkv.cuh"
 #include "bwd_cross_dq.cuh"
 #include "bwd_tc_kernel.cuh"

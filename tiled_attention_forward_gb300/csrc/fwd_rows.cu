@@ -17,9 +17,10 @@
 // shared memory as whole lines, and read from L2.
 //
 // Measured (GB300).  Enough tiles: 2 entries of 32 heads on 8, 8192 tokens over 4096
-// keys, D = 128, bf16, 678 us = 1620 TFLOP/s (0.84 of the measured peak; tensor pipe
-// 72 %), the dense forward's chain; 64 heads of 4096 tokens and keys 353 us where the
-// dense forward takes 336, the difference being what a task costs: with every role
+// keys, D = 128, bf16, 674 us in a burst of 20 calls = 1630 TFLOP/s (0.85 of the measured
+// peak; tensor pipe 72 %), 719 to 724 among other calls or for seconds, at the power limit
+// (0.80), the dense forward's chain; 64 heads of 4096 tokens and keys 346 to 355 us where
+// the dense forward takes 336, the difference being what a task costs: with every role
 // decoding tasks for itself 370.  Few: 3 entries of 16 heads on 4, 130 tokens over up
 // to 8192 keys, D = 64, 29 us, of which 17 the forward (2 its setup, 3 its first
 // loads, 10 tiles of 0.85, 2.5 the parts) and 7 the join.  A prefix of 16000 tokens, 256
