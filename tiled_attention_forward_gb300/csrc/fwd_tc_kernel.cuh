@@ -1365,7 +1365,7 @@ __device__ void softmax_role(const ArgsOf<KIND>& a, const Bars& bars, uint8_t* q
                     }
                 }
             }
-            const float neg_m = (m_run == -INFINITY) ? 0.f : kHeld - m_run;
+            const float neg_m = (m_run == -INFINITY) ? 0.f : (kHeld > 0.f ? kHeld - m_run : -m_run);
 
             // P = exp2(s*scale*log2e - m) rounded to the operand type, written
             // over the first half of S.  l_run sums exactly the rounded values
@@ -1411,7 +1411,7 @@ __device__ void softmax_role(const ArgsOf<KIND>& a, const Bars& bars, uint8_t* q
         }
 
         // Epilogue: O = O~ / l, LSE = (m + log2 l) ln 2, rows < N only.
-        m_run -= kHeld;
+        if (kHeld > 0.f) m_run -= kHeld;
         const bool ok = warp_wait(&bars.o_full[tile], ocnt & 1u, abort_flag, a.timeout_ns);
         ++ocnt;
         if (!ok) {
