@@ -82,9 +82,9 @@ KERNEL_SOURCES = {"tc": ["fwd_tc.cu", "fwd_tc_kernel.cuh", "sm103_ptx.cuh"], "ff
                   "unfused": ["fwd_unfused.cu", "sm103_ptx.cuh"],
                   "bwd": ["bwd_tc.cu", "bwd_tc_kernel.cuh", "sm103_ptx.cuh"]}
 NCU_TRAFFIC = {
-    "bf16_B4_H16_N4096_D128": (201958400 + 41573120, "7417b72dad632b2a"),
-    "bf16_B2_H32_N8192_D128_causal_qstd4": (411443456 + 111231488, "7417b72dad632b2a"),
-    "fp16_B1_H16_N16000_D64_causal": (98417152 + 9909504, "7417b72dad632b2a"),
+    "bf16_B4_H16_N4096_D128": (201901312 + 38220288, "6476c99a0001741a"),
+    "bf16_B2_H32_N8192_D128_causal_qstd4": (411496192 + 111004672, "6476c99a0001741a"),
+    "fp16_B1_H16_N16000_D64_causal": (98445568 + 9487104, "6476c99a0001741a"),
     "fp32_B4_H8_N8192_D64_causal": (201639936 + 51146240, "61c5185890f7842f"),
 }
 
@@ -99,9 +99,9 @@ NCU_TRAFFIC_UNFUSED = {
 
 # The backward: DRAM bytes of one step (statistics, dK/dV and dQ kernels).
 NCU_TRAFFIC_BWD = {
-    "bf16_B4_H16_N4096_D128": (676450560 + 152076288, "5d668d5d83dc1f30"),
-    "bf16_B2_H32_N8192_D128_causal_qstd4": (7985778944 + 355318016, "5d668d5d83dc1f30"),
-    "fp16_B1_H16_N16000_D64_causal": (460237056 + 51237760, "5d668d5d83dc1f30"),
+    "bf16_B4_H16_N4096_D128": (676449024 + 152473600, "99ed17208ca64d05"),
+    "bf16_B2_H32_N8192_D128_causal_qstd4": (7978893312 + 354733568, "99ed17208ca64d05"),
+    "fp16_B1_H16_N16000_D64_causal": (456454656 + 50708736, "99ed17208ca64d05"),
 }
 
 
